@@ -30,6 +30,7 @@ FA_ERR_TIMEOUT = -4
 FA_ERR_WORKSPACE = -5
 FA_ERR_DEVICE = -6
 FA_ERR_BOUNDS = -7
+FA_ERR_INDEX = -8
 FA_F32, FA_F16, FA_BF16 = 0, 1, 2
 
 
@@ -103,6 +104,8 @@ def load() -> ctypes.CDLL:
         "fa_fp8_quantize": (I, [PP, P, P, P, P, P, P, P, P, P, P, P]),
         "fa_fwd_fp8": (I, [PP, P, P, P, P, P, P, P, P, P]),
     }
+    from . import ops
+    sigs.update(ops.signatures())
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
@@ -373,3 +376,18 @@ def selftest_timeout(stream=None) -> None:
 
 def check_params(p: FaParams, for_backward: bool = False) -> int:
     return int(load().fa_check(ctypes.byref(p), int(bool(for_backward))))
+
+
+# the operators around the attention (norms and rotation, 4-bit cache, block tables)
+def __getattr__(name):
+    # on first use: the module needs torch, this one only where a call does
+    if name in _OPS:
+        from . import ops
+        globals().update((n, getattr(ops, n)) for n in _OPS)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+_OPS = ("rope_freqs", "qk_norm_rope", "qk_norm_rope_bwd", "kv4_block_bytes", "kv4_cache", "kv4_append", "kv4_gather",
+        "kv4_attention", "paged_plan", "FaQkParams", "FaKv4Cache", "FaKv4Rows", "FaKv4AttnParams", "FaPlanParams",
+        "KV4_GROUP", "KV4_BLOCK", "KV4_SATURATE", "PLAN_MAX_REQUESTS")

@@ -21,8 +21,10 @@ LIB = os.path.join(HERE, "libfa.so")
 # the debug build: kernels with index checks (FA_DEBUG), objects and library of its own
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libfa_debug.so")
-SOURCES = ["fa_api.cu", "fwd_tc.cu", "fwd_f32.cu", "bwd_tc.cu", "bwd_aux.cu", "fa_noalloc.cu", "fwd_fp8.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "bwd_sched.cuh", "fp8.h", "tiles.cuh", "fwd_common.cuh"]
+SOURCES = ["fa_api.cu", "fwd_tc.cu", "fwd_f32.cu", "bwd_tc.cu", "bwd_aux.cu", "fa_noalloc.cu", "fwd_fp8.cu",
+           "ops_api.cu", "qk_norm_rope.cu", "kv4.cu", "kv4_attn.cu", "plan.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "bwd_sched.cuh", "fp8.h", "tiles.cuh", "fwd_common.cuh",
+           "ops.h", "kv4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

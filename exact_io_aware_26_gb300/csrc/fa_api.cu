@@ -357,13 +357,16 @@ fa_status need16(const void* ptr, const char* name) {
   return FA_OK;
 }
 
-#define FA_TRY(x)                    \
-  do {                               \
-    fa_status _s = (x);              \
-    if (_s != FA_OK) return _s;      \
-  } while (0)
-
 }  // namespace
+
+fa_status fa::api_device(Report* rep, int* sms) {
+  DevStatus* st = nullptr;
+  FA_TRY(device_ready(&st));
+  *rep = make_report(st);
+  if (sms) *sms = device_sms();
+  return FA_OK;
+}
+fa_status fa::api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
 extern "C" {
 
@@ -497,6 +500,7 @@ const char* fa_status_string(int s) {
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
     case FA_ERR_DEVICE: return "device is not sm_103";
     case FA_ERR_BOUNDS: return "index check failed in a kernel (debug build)";
+    case FA_ERR_INDEX: return "page, slot or length outside the cache";
     default: return "unknown status";
   }
 }

@@ -135,4 +135,16 @@ cudaError_t launch_wait_selftest(const Report& rep, cudaStream_t s);
 // Records the text fa_last_error() returns on this thread.
 void set_error_text(const char* text);
 
+// For the entry points outside fa_api.cu: the current device must be sm_103 (else
+// FA_ERR_DEVICE), a launch's report and, where wanted, the SM count; and a failed
+// CUDA call as FA_ERR_CUDA with its text.
+fa_status api_device(Report* rep, int* sms);
+fa_status api_cuda_fail(cudaError_t e, const char* what);
+
+#define FA_TRY(x)                    \
+  do {                               \
+    fa_status _s = (x);              \
+    if (_s != FA_OK) return _s;      \
+  } while (0)
+
 }  // namespace fa

@@ -1,0 +1,88 @@
+// ops.h -- declarations shared by the entry points of the operators around the
+// attention (ops_api.cu) and their kernels.  Not part of the public interface.
+#pragma once
+#include "internal.h"
+
+namespace fa {
+
+// Norm and rotation of query and key heads (qk_norm_rope.cu).
+struct QkArgs {
+  int B, N, Hq, Hk;
+  int rot, interleaved;
+  float eps;
+  const void* x[2];   // q, k
+  const void* w[2];   // wq, wk
+  void* y[2];         // forward: results; backward: gradients of q, k
+  const void* dy[2];  // backward: gradients at the results
+  long long xs[2][3], ys[2][3], ds[2][3];  // element strides {batch, token, head} of x, y, dy
+  const unsigned long long* freqs;
+  const int* pos;  // or nullptr
+  long long pos_stride;
+  int tok_tile;   // tokens of a tile (a power of two)
+  int tiles;      // token tiles of a batch entry
+  int ctas;       // backward: CTAs of the launch
+  float* part;    // backward: [ctas][2][d] partial weight gradients
+  float* dw[2];
+};
+int qk_rows_per_pass(int d);
+cudaError_t launch_qk_norm_rope(const QkArgs& a, int d, int dtype, bool w_f32, cudaStream_t s);
+cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, int d, int dtype, bool w_f32, cudaStream_t s);
+
+// The 4-bit cache (kv4.cuh has its block layout).
+struct Kv4Cache {
+  const uint8_t* data;
+  long long page_stride;  // bytes
+  int num_pages, page_log, Hk;  // tokens of a page: 1 << page_log
+};
+struct Kv4RowArgs {
+  Kv4Cache c;
+  int T;
+  const int* slots;
+  void* x[2];              // keys, values
+  long long xs[2][2];      // element strides {token, head}
+  DevStatus* st;
+};
+cudaError_t launch_kv4_append(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
+cudaError_t launch_kv4_gather(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
+
+struct Kv4AttnArgs {
+  Kv4Cache c;
+  int R, T, Hq, G;
+  int window;
+  int table_width;
+  long long table_stride;
+  const int* table;
+  const int* kv_lens;
+  const int* cu_q;  // or nullptr
+  float scale_log2;
+  const void* q;
+  long long qs[2];  // element strides {token, head}
+  void* o;
+  long long os[2];
+  float* lse;       // or nullptr
+  float* part;      // 2 slots per CTA: rows x (d + 2) fp32 each
+  int4* meta;       // per CTA: the tile whose share starts in it and goes on
+  Report rep;
+};
+// Rows of a query tile: 8, 16 or 32 (see kv4_attn.cu), and the most CTAs a launch has.
+int kv4_tile_rows(int G, int max_q_len);
+int kv4_max_ctas(int d, int rows, int sms);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int d, bool f16, int rows, int ctas, cudaStream_t s);
+
+struct PlanArgs {
+  int R, T, page, pages, width;
+  long long stride;
+  const int* seq;
+  const int* fresh;
+  int* table;
+  int* stack;
+  const int* count;
+  int* kv;
+  int* cu;
+  int* pos;
+  int* slots;
+  int* counts;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
+
+}  // namespace fa

@@ -1,0 +1,420 @@
+// ops_api.cu -- the C ABI of the operators around the attention (include/fa.h): norm
+// and rotation of queries and keys, the 4-bit paged cache and its attention, block
+// tables and slot maps.  Host code: argument checks, before any CUDA call, and the
+// launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "kv4.cuh"
+#include "ops.h"
+
+#include <nvtx3/nvToolsExt.h>
+
+using namespace fa;
+
+namespace {
+
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+fa_status fail(fa_status s, const char* fmt, ...) {
+  char text[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(text, sizeof(text), fmt, ap);
+  va_end(ap);
+  set_error_text(text);
+  return s;
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+long long elem_bytes(int dtype) { return dtype == FA_F32 ? 4 : 2; }
+
+fa_status need(const void* p, size_t align, const char* name) {
+  if (!p) return fail(FA_ERR_INVALID, "%s is NULL", name);
+  if (!aligned(p, align)) return fail(FA_ERR_INVALID, "%s is not %zu-byte aligned", name, align);
+  return FA_OK;
+}
+
+// Strides (elements) of a tensor [size[0]][size[1]]...[inner]: whole 16-byte vectors,
+// not negative; for a tensor that is written, no two elements in one place.
+fa_status check_strides(const long long* stride, const long long* size, int n, long long inner, int dtype, bool written,
+                        const char* name) {
+  const long long vec = 16 / elem_bytes(dtype);
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < n; ++i)
+    if (stride[i] < 0 || stride[i] % vec != 0)
+      return fail(FA_ERR_INVALID, "%s: stride %lld is negative or no multiple of 16 bytes", name, stride[i]);
+  if (!written) return FA_OK;
+  std::sort(order, order + n, [&](int x, int y) { return stride[x] < stride[y]; });
+  long long extent = inner;
+  for (int i = 0; i < n; ++i) {
+    const int k = order[i];
+    if (size[k] <= 1) continue;
+    if (stride[k] < extent) return fail(FA_ERR_INVALID, "%s overlaps itself (stride %lld)", name, stride[k]);
+    extent = stride[k] * (size[k] - 1) + extent;
+  }
+  return FA_OK;
+}
+
+// ------------------------------------------------------- norm and rotation
+
+fa_status qk_check(const fa_qk_params* p, bool bwd) {
+  if (!p) return fail(FA_ERR_INVALID, "params is NULL");
+  if (p->B < 1 || p->N < 0 || p->Hq < 1 || p->Hk < 1)
+    return fail(FA_ERR_INVALID, "B, Hq, Hk must be >= 1 and N >= 0 (got %d, %d, %d, %d)", p->B, p->Hq, p->Hk, p->N);
+  if (p->d != 64 && p->d != 128) return fail(FA_ERR_UNSUPPORTED, "head size %d is not supported (64 or 128)", p->d);
+  if (p->dtype != FA_F32 && p->dtype != FA_F16 && p->dtype != FA_BF16)
+    return fail(FA_ERR_INVALID, "dtype %d is not an fa_dtype", p->dtype);
+  if (p->weight_dtype != p->dtype && p->weight_dtype != FA_F32)
+    return fail(FA_ERR_INVALID, "weight_dtype must be dtype or FA_F32");
+  if (p->rot_dim < 0 || p->rot_dim > p->d || p->rot_dim % 2 != 0)
+    return fail(FA_ERR_INVALID, "rot_dim %d must be even, from 0 to d", p->rot_dim);
+  if (!(std::isfinite(p->eps) && p->eps > 0.f)) return fail(FA_ERR_INVALID, "eps must be positive and finite");
+  if (p->pos_stride < 0) return fail(FA_ERR_INVALID, "pos_stride is negative");
+  // a launch has a CTA per tile of at least one token
+  if ((long long)p->B * p->N >= (1ll << 31)) return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^31 - 1");
+  const long long sq[3] = {p->B, p->N, p->Hq}, sk[3] = {p->B, p->N, p->Hk};
+  FA_TRY(check_strides(p->q_stride, sq, 3, p->d, p->dtype, false, "q"));
+  FA_TRY(check_strides(p->k_stride, sk, 3, p->d, p->dtype, false, "k"));
+  FA_TRY(check_strides(p->yq_stride, sq, 3, p->d, p->dtype, !bwd, bwd ? "dyq" : "yq"));
+  FA_TRY(check_strides(p->yk_stride, sk, 3, p->d, p->dtype, !bwd, bwd ? "dyk" : "yk"));
+  if (bwd) {
+    FA_TRY(check_strides(p->dq_stride, sq, 3, p->d, p->dtype, true, "dq"));
+    FA_TRY(check_strides(p->dk_stride, sk, 3, p->d, p->dtype, true, "dk"));
+  }
+  return FA_OK;
+}
+
+constexpr int kQkBwdCtasPerSm = 2;
+constexpr int kQkBwdMaxCtas = 160 * kQkBwdCtasPerSm;
+
+// Tokens of a tile: as many as the row slots of a CTA (each lane then forms its angles
+// once for all heads), fewer -- the slots share a token's heads -- while the launch
+// would have under four CTAs per SM.
+int qk_tok_tile(const fa_qk_params* p, int sms) {
+  int tile = qk_rows_per_pass(p->d);
+  while (tile > 1 && (long long)p->B * ((p->N + tile - 1) / tile) < 4LL * sms) tile /= 2;
+  return tile;
+}
+
+QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* wq, const void* wk,
+               const uint64_t* freqs, const int* positions, int sms) {
+  QkArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.B = p->B;
+  a.N = p->N;
+  a.Hq = p->Hq;
+  a.Hk = p->Hk;
+  a.rot = p->rot_dim;
+  a.interleaved = p->interleaved != 0;
+  a.eps = p->eps;
+  a.x[0] = q;
+  a.x[1] = k;
+  a.w[0] = wq;
+  a.w[1] = wk;
+  a.freqs = reinterpret_cast<const unsigned long long*>(freqs);
+  a.pos = positions;
+  a.pos_stride = p->pos_stride;
+  std::memcpy(a.xs[0], p->q_stride, sizeof(a.xs[0]));
+  std::memcpy(a.xs[1], p->k_stride, sizeof(a.xs[1]));
+  a.tok_tile = qk_tok_tile(p, sms);
+  a.tiles = (p->N + a.tok_tile - 1) / a.tok_tile;
+  return a;
+}
+
+fa_status qk_pointers(const fa_qk_params* p, const void* q, const void* k, const void* wq, const void* wk,
+                      const uint64_t* freqs, const int* positions) {
+  FA_TRY(need(q, 16, "q"));
+  FA_TRY(need(k, 16, "k"));
+  FA_TRY(need(wq, 16, "wq"));
+  FA_TRY(need(wk, 16, "wk"));
+  if (p->rot_dim > 0) FA_TRY(need(freqs, 8, "freqs"));
+  if (positions && !aligned(positions, 4)) return fail(FA_ERR_INVALID, "positions is not 4-byte aligned");
+  return FA_OK;
+}
+
+// ------------------------------------------------------- 4-bit cache
+
+fa_status cache_check(const fa_kv4_cache* c) {
+  if (!c) return fail(FA_ERR_INVALID, "cache description is NULL");
+  if (c->d != 64 && c->d != 128) return fail(FA_ERR_UNSUPPORTED, "head size %d is not supported (64 or 128)", c->d);
+  if (c->num_pages < 1 || c->Hk < 1) return fail(FA_ERR_INVALID, "num_pages and Hk must be >= 1");
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0)
+    return fail(FA_ERR_UNSUPPORTED, "page_size %d must be a power of two from 16 to 4096", c->page_size);
+  if ((long long)c->num_pages * c->page_size > 0x7FFFFFFFll)
+    return fail(FA_ERR_UNSUPPORTED, "num_pages * page_size exceeds 2^31 - 1 slots");
+  const long long page = (long long)c->Hk * (c->page_size / 16) * fa_kv4_block_bytes(c->d);
+  if (c->page_stride < page || c->page_stride % 16 != 0)
+    return fail(FA_ERR_INVALID, "page_stride %lld must be a multiple of 16, at least %lld", c->page_stride, page);
+  return FA_OK;
+}
+
+Kv4Cache cache_args(const fa_kv4_cache* c, const void* data) {
+  Kv4Cache k;
+  k.data = static_cast<const uint8_t*>(data);
+  k.page_stride = c->page_stride;
+  k.num_pages = c->num_pages;
+  k.page_log = 0;
+  while ((1 << k.page_log) < c->page_size) ++k.page_log;
+  k.Hk = c->Hk;
+  return k;
+}
+
+fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* k, const void* v, const int* slots,
+                        const void* cache, bool gather, void* stream) {
+  FA_TRY(cache_check(c));
+  if (!rows) return fail(FA_ERR_INVALID, "rows is NULL");
+  if (rows->T < 0) return fail(FA_ERR_INVALID, "T is negative");
+  if (rows->dtype != FA_F32 && rows->dtype != FA_F16 && rows->dtype != FA_BF16)
+    return fail(FA_ERR_INVALID, "dtype %d is not an fa_dtype", rows->dtype);
+  const long long size[2] = {rows->T, c->Hk};
+  FA_TRY(check_strides(rows->k_stride, size, 2, c->d, rows->dtype, gather, "k"));
+  FA_TRY(check_strides(rows->v_stride, size, 2, c->d, rows->dtype, gather, "v"));
+  if (rows->T > 0) {
+    FA_TRY(need(k, 16, "k"));
+    FA_TRY(need(v, 16, "v"));
+    FA_TRY(need(slots, 4, "slots"));
+  }
+  FA_TRY(need(cache, 16, "cache"));
+  Report rep;
+  FA_TRY(api_device(&rep, nullptr));
+  if (rows->T == 0) return FA_OK;
+  Kv4RowArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.c = cache_args(c, cache);
+  a.T = rows->T;
+  a.slots = slots;
+  a.x[0] = const_cast<void*>(k);
+  a.x[1] = const_cast<void*>(v);
+  std::memcpy(a.xs[0], rows->k_stride, sizeof(a.xs[0]));
+  std::memcpy(a.xs[1], rows->v_stride, sizeof(a.xs[1]));
+  a.st = rep.st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = gather ? launch_kv4_gather(a, c->d, rows->dtype, s) : launch_kv4_append(a, c->d, rows->dtype, s);
+  if (e != cudaSuccess) return api_cuda_fail(e, gather ? "cache gather launch" : "cache append launch");
+  return FA_OK;
+}
+
+fa_status attn_check(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
+  FA_TRY(cache_check(c));
+  if (!p) return fail(FA_ERR_INVALID, "params is NULL");
+  if (p->dtype != FA_F16 && p->dtype != FA_BF16)
+    return fail(p->dtype == FA_F32 ? FA_ERR_UNSUPPORTED : FA_ERR_INVALID, "the cache's attention takes fp16 or bf16 queries");
+  if (p->R < 1 || p->T < 0) return fail(FA_ERR_INVALID, "R must be >= 1 and T >= 0 (got %d, %d)", p->R, p->T);
+  if (p->Hq < 1 || p->Hq % c->Hk != 0)
+    return fail(FA_ERR_INVALID, "Hq = %d is no multiple of the cache's %d heads", p->Hq, c->Hk);
+  if ((long long)p->T * p->Hq >= (1ll << 31)) return fail(FA_ERR_UNSUPPORTED, "T*Hq exceeds 2^31 - 1");
+  if (p->max_q_len < 1) return fail(FA_ERR_INVALID, "max_q_len must be >= 1");
+  if (p->window < 0) return fail(FA_ERR_INVALID, "window is negative");
+  if (p->table_width < 1 || p->table_stride < p->table_width)
+    return fail(FA_ERR_INVALID, "block_table needs at least one column and a row stride of at least its width");
+  if ((long long)p->table_width * c->page_size > 0x7FFFFFFFll)
+    return fail(FA_ERR_UNSUPPORTED, "table_width * page_size exceeds 2^31 - 1 tokens");
+  if (!(std::isfinite(p->scale) && p->scale > 0.f)) return fail(FA_ERR_INVALID, "scale must be positive and finite");
+  const long long size[2] = {p->T, p->Hq};
+  FA_TRY(check_strides(p->q_stride, size, 2, c->d, p->dtype, false, "q"));
+  FA_TRY(check_strides(p->o_stride, size, 2, c->d, p->dtype, true, "o"));
+  return FA_OK;
+}
+
+constexpr int kMaxSms = 160;
+
+size_t attn_part_bytes(int ctas, int rows, int d) { return align256((size_t)2 * ctas * rows * (d + 4) * 4); }
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, const void* wq, const void* wk,
+                          const uint64_t* freqs, const int* positions, void* yq, void* yk, void* stream) {
+  NvtxRange nvtx_range("fa_qk_norm_rope");
+  FA_TRY(qk_check(p, false));
+  if (p->N > 0) {
+    FA_TRY(qk_pointers(p, q, k, wq, wk, freqs, positions));
+    FA_TRY(need(yq, 16, "yq"));
+    FA_TRY(need(yk, 16, "yk"));
+  }
+  Report rep;
+  int sms = 0;
+  FA_TRY(api_device(&rep, &sms));
+  if (p->N == 0) return FA_OK;
+  QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms);
+  a.y[0] = yq;
+  a.y[1] = yk;
+  std::memcpy(a.ys[0], p->yq_stride, sizeof(a.ys[0]));
+  std::memcpy(a.ys[1], p->yk_stride, sizeof(a.ys[1]));
+  const cudaError_t e =
+      launch_qk_norm_rope(a, p->d, p->dtype, p->weight_dtype == FA_F32, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return api_cuda_fail(e, "norm and rotation launch");
+  return FA_OK;
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(const fa_qk_params* p) {
+  if (qk_check(p, true) != FA_OK) return 0;
+  return (size_t)kQkBwdMaxCtas * 2 * p->d * 4;
+}
+
+fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* k, const void* dyq, const void* dyk,
+                              const void* wq, const void* wk, const uint64_t* freqs, const int* positions, void* dq,
+                              void* dk, float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("fa_qk_norm_rope_bwd");
+  FA_TRY(qk_check(p, true));
+  if (p->N > 0) {
+    FA_TRY(qk_pointers(p, q, k, wq, wk, freqs, positions));
+    FA_TRY(need(dyq, 16, "dyq"));
+    FA_TRY(need(dyk, 16, "dyk"));
+    FA_TRY(need(dq, 16, "dq"));
+    FA_TRY(need(dk, 16, "dk"));
+  }
+  FA_TRY(need(dwq, 4, "dwq"));
+  FA_TRY(need(dwk, 4, "dwk"));
+  const size_t want = fa_qk_norm_rope_bwd_workspace_size(p);
+  if (!workspace || workspace_bytes < want || !aligned(workspace, 256))
+    return fail(FA_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", workspace,
+                workspace_bytes, want);
+  Report rep;
+  int sms = 0;
+  FA_TRY(api_device(&rep, &sms));
+  QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms);
+  a.y[0] = dq;
+  a.y[1] = dk;
+  a.dy[0] = dyq;
+  a.dy[1] = dyk;
+  std::memcpy(a.ys[0], p->dq_stride, sizeof(a.ys[0]));
+  std::memcpy(a.ys[1], p->dk_stride, sizeof(a.ys[1]));
+  std::memcpy(a.ds[0], p->yq_stride, sizeof(a.ds[0]));
+  std::memcpy(a.ds[1], p->yk_stride, sizeof(a.ds[1]));
+  a.ctas = (int)std::min<long long>((long long)a.B * a.tiles, std::min(kQkBwdMaxCtas, sms * kQkBwdCtasPerSm));
+  a.part = static_cast<float*>(workspace);
+  a.dw[0] = dwq;
+  a.dw[1] = dwk;
+  const cudaError_t e =
+      launch_qk_norm_rope_bwd(a, p->d, p->dtype, p->weight_dtype == FA_F32, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return api_cuda_fail(e, "norm and rotation backward launch");
+  return FA_OK;
+}
+
+int fa_kv4_block_bytes(int d) { return d == 128 ? KvBlock<128>::bytes : d == 64 ? KvBlock<64>::bytes : 0; }
+
+fa_status fa_kv4_append(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* k, const void* v, const int* slots,
+                        void* cache, void* stream) {
+  NvtxRange nvtx_range("fa_kv4_append");
+  return kv4_rows_call(c, rows, k, v, slots, cache, false, stream);
+}
+
+fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* cache, const int* slots, void* k,
+                        void* v, void* stream) {
+  NvtxRange nvtx_range("fa_kv4_gather");
+  return kv4_rows_call(c, rows, k, v, slots, cache, true, stream);
+}
+
+size_t fa_kv4_attention_workspace_size(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
+  if (attn_check(c, p) != FA_OK) return 0;
+  const int rows = kv4_tile_rows(p->Hq / c->Hk, p->max_q_len);
+  const int ctas = kv4_max_ctas(c->d, rows, kMaxSms);
+  return attn_part_bytes(ctas, rows, c->d) + align256((size_t)ctas * 16);
+}
+
+fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, const void* q, const void* cache,
+                           const int* block_table, const int* kv_lens, const int* cu_q, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("fa_kv4_attention");
+  FA_TRY(attn_check(c, p));
+  if (p->T > 0) {
+    FA_TRY(need(q, 16, "q"));
+    FA_TRY(need(o, 16, "o"));
+  }
+  FA_TRY(need(cache, 16, "cache"));
+  FA_TRY(need(block_table, 4, "block_table"));
+  FA_TRY(need(kv_lens, 4, "kv_lens"));
+  if (cu_q && !aligned(cu_q, 4)) return fail(FA_ERR_INVALID, "cu_q is not 4-byte aligned");
+  if (lse && !aligned(lse, 4)) return fail(FA_ERR_INVALID, "lse is not 4-byte aligned");
+  const size_t want = fa_kv4_attention_workspace_size(c, p);
+  if (!workspace || workspace_bytes < want || !aligned(workspace, 256))
+    return fail(FA_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", workspace,
+                workspace_bytes, want);
+  Report rep;
+  int sms = 0;
+  FA_TRY(api_device(&rep, &sms));
+  if (p->T == 0) return FA_OK;
+  Kv4AttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.c = cache_args(c, cache);
+  a.R = p->R;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.G = p->Hq / c->Hk;
+  a.window = p->window;
+  a.table_width = p->table_width;
+  a.table_stride = p->table_stride;
+  a.table = block_table;
+  a.kv_lens = kv_lens;
+  a.cu_q = cu_q;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.q = q;
+  a.o = o;
+  std::memcpy(a.qs, p->q_stride, sizeof(a.qs));
+  std::memcpy(a.os, p->o_stride, sizeof(a.os));
+  a.lse = lse;
+  const int rows = kv4_tile_rows(a.G, p->max_q_len);
+  const int ctas = kv4_max_ctas(c->d, rows, std::min(sms, kMaxSms));
+  a.part = static_cast<float*>(workspace);
+  a.meta = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attn_part_bytes(ctas, rows, c->d));
+  a.rep = rep;
+  const cudaError_t e =
+      launch_kv4_attention(a, c->d, p->dtype == FA_F16, rows, ctas, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return api_cuda_fail(e, "cache attention launch");
+  return FA_OK;
+}
+
+fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int* new_lens, int* block_table,
+                        int* free_pages, const int* free_count, int* kv_lens, int* cu_q, int* positions, int* slots,
+                        int* counts, void* stream) {
+  NvtxRange nvtx_range("fa_paged_plan");
+  if (!p) return fail(FA_ERR_INVALID, "params is NULL");
+  if (p->R < 1 || p->T < 0 || p->page_size < 1 || p->num_pages < 1)
+    return fail(FA_ERR_INVALID, "R, page_size and num_pages must be >= 1 and T >= 0");
+  if (p->R > FA_PLAN_MAX_REQUESTS) return fail(FA_ERR_UNSUPPORTED, "R = %d exceeds %d", p->R, FA_PLAN_MAX_REQUESTS);
+  if (p->table_width < 1 || p->table_stride < p->table_width)
+    return fail(FA_ERR_INVALID, "block_table needs at least one column and a row stride of at least its width");
+  const void* all[] = {seq_lens, new_lens, block_table, free_pages, free_count, kv_lens, cu_q, counts};
+  const char* names[] = {"seq_lens", "new_lens", "block_table", "free_pages", "free_count", "kv_lens", "cu_q", "counts"};
+  for (int i = 0; i < 8; ++i) FA_TRY(need(all[i], 4, names[i]));
+  if (p->T > 0) {
+    FA_TRY(need(positions, 4, "positions"));
+    FA_TRY(need(slots, 4, "slots"));
+  }
+  Report rep;
+  FA_TRY(api_device(&rep, nullptr));
+  PlanArgs a;
+  a.R = p->R;
+  a.T = p->T;
+  a.page = p->page_size;
+  a.pages = p->num_pages;
+  a.width = p->table_width;
+  a.stride = p->table_stride;
+  a.seq = seq_lens;
+  a.fresh = new_lens;
+  a.table = block_table;
+  a.stack = free_pages;
+  a.count = free_count;
+  a.kv = kv_lens;
+  a.cu = cu_q;
+  a.pos = positions;
+  a.slots = slots;
+  a.counts = counts;
+  const cudaError_t e = launch_paged_plan(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return api_cuda_fail(e, "plan launch");
+  return FA_OK;
+}
+
+}  // extern "C"

@@ -50,7 +50,8 @@ typedef enum {
   FA_ERR_TIMEOUT = -4,     /* a kernel gave up waiting on a barrier (via fa_get_status) */
   FA_ERR_WORKSPACE = -5,   /* workspace missing or smaller than required */
   FA_ERR_DEVICE = -6,      /* the current device is not compute capability 10.3 */
-  FA_ERR_BOUNDS = -7       /* debug build only: a kernel's index check failed (via fa_get_status) */
+  FA_ERR_BOUNDS = -7,      /* debug build only: a kernel's index check failed (via fa_get_status) */
+  FA_ERR_INDEX = -8        /* a page, slot or length outside the cache it was used with (via fa_get_status) */
 } fa_status;
 
 typedef enum { FA_F32 = 0, FA_F16 = 1, FA_BF16 = 2 } fa_dtype;
@@ -330,6 +331,172 @@ fa_status fa_fp8_quantize(const fa_params* p, const void* Q, const void* K, cons
 fa_status fa_fwd_fp8(const fa_params* p, const void* q8, const void* k8, const void* vt8,
                      const float* sq, const float* sk, const float* sv, void* O, float* LSE,
                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norms of the query and key heads and the rotation by position, in one pass
+ * from the projection to the layout the attention reads, and its gradient.
+ *
+ *   n_c = x_c * r * w_c,  r = 1 / sqrt(mean_c x_c^2 + eps)     for every head row
+ *   (y_a, y_b) = (n_a cos t - n_b sin t, n_a sin t + n_b cos t)  for every pair i
+ *
+ * with t = position * angle per step of pair i.  Pair i is (i, i + rot_dim / 2),
+ * or (2 i, 2 i + 1) with `interleaved`, for i < rot_dim / 2; channels from
+ * rot_dim on are normed only.  freqs[i] is the pair's angle per step in units of
+ * 2^-64 turns: position * freqs[i] mod 2^64 is then the exact phase at any
+ * position, and its leading 32 bits give the angle to 2^-32 turns.
+ *
+ *   B, N, Hq, Hk, d  batch, tokens per batch entry (>= 0), query and key heads,
+ *               head size (64 or 128).
+ *   dtype       fa_dtype of q, k, yq, yk and their gradients (fp32 arithmetic
+ *               inside); weight_dtype that of wq, wk: `dtype` or FA_F32.
+ *   eps         positive and finite.
+ *   *_stride    element strides {batch, token, head}; channels are contiguous.
+ *               Bases 16-byte aligned, strides multiples of 16 bytes; written
+ *               tensors must not overlap themselves.  q and k may be views of one
+ *               packed projection, and yq (yk) may be q (k) itself, with the same
+ *               strides.
+ *   pos_stride  batch stride of `positions` in elements (0: one row for all).
+ * positions: device int32 [B][N], or NULL for positions 0 .. N - 1.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int B, N, Hq, Hk, d;
+  int dtype, weight_dtype;
+  int rot_dim, interleaved;
+  float eps;
+  long long pos_stride;
+  long long q_stride[3], k_stride[3];   /* the projection */
+  long long yq_stride[3], yk_stride[3]; /* the result; its gradient in the backward */
+  long long dq_stride[3], dk_stride[3]; /* backward: the projection's gradient */
+} fa_qk_params;
+
+fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, const void* wq,
+                          const void* wk, const uint64_t* freqs, const int* positions, void* yq,
+                          void* yk, void* stream);
+
+/* Bytes of workspace of the backward (fp32 partial sums of the weights'
+ * gradients); 0 on invalid p. */
+size_t fa_qk_norm_rope_bwd_workspace_size(const fa_qk_params* p);
+
+/* Gradients of fa_qk_norm_rope for the gradients dyq, dyk at its results: with
+ * dz the back-rotated dy and h = x r, dx = r (w dz - h mean(w dz h)) and
+ * dw = sum over rows of dz h (fp32 [d] each, summed in a fixed order).  q and k
+ * are the forward's inputs; r is formed again.  The workspace is 256-byte
+ * aligned and owned by the caller; its contents do not matter. */
+fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* k, const void* dyq,
+                              const void* dyk, const void* wq, const void* wk,
+                              const uint64_t* freqs, const int* positions, void* dq, void* dk,
+                              float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged key/value cache in 4 bits, and the attention that reads it.
+ *
+ * The cache is num_pages pages of page_size tokens (a power of two, 16 to 4096) of Hk
+ * heads, page_stride bytes apart; a page holds, head by head, page_size / 16 blocks of 16
+ * tokens.  A block (fa_kv4_block_bytes(d) bytes) is
+ *     uint8  key codes   [16][d / 2]    channel 2 b in the low, 2 b + 1 in the high half of byte b
+ *     half2  key pairs   [16][d / 32]   (scale, base) of each 32 channels
+ *     the same for the values.
+ * Code c of a pair (scale, base) stands for the fp16 number nearest to
+ * base + scale * (1 + c / 16): c is the top of the mantissa of an fp16 number in
+ * [1, 2), which one fused multiply-add turns into the value.  Token j of page p is
+ * slot p * page_size + j.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int num_pages, page_size, Hk, d;
+  long long page_stride; /* bytes; a multiple of 16, at least one page's blocks */
+} fa_kv4_cache;
+
+/* Bytes of a 16-token block of one head: 2560 for d = 128, 1280 for d = 64, else 0. */
+int fa_kv4_block_bytes(int d);
+
+/* T tokens' keys and values ([T][Hk][d], element strides {token, head}, of `dtype`). */
+typedef struct {
+  int T, dtype;
+  long long k_stride[2], v_stride[2];
+} fa_kv4_rows;
+
+/* Quantise T tokens' keys and values into their slots (device int32 [T]; a
+ * negative slot's token is left out).  For each token, head and 32 channels, of
+ * x saturated at +-16384 and widened to fp32 (lo, hi its least and largest):
+ *     scale = fp16((hi - lo) * 16 / 15),  base = fp16(lo - scale),
+ *     c = min(15, max(0, rint((x - base) * 16 / scale - 16))), 0 where scale = 0.
+ * A NaN makes its 32 values NaN.  A slot past the cache is left out and recorded
+ * as FA_ERR_INDEX.  The slots >= 0 of one call must be distinct: of two tokens
+ * with one slot the result is a mixture. */
+fa_status fa_kv4_append(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* k,
+                        const void* v, const int* slots, void* cache, void* stream);
+
+/* The values that T slots hold, rounded to `dtype` (zeros for a negative slot). */
+fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* cache,
+                        const int* slots, void* k, void* v, void* stream);
+
+/*
+ * Attention of R requests' newest tokens over their cached keys and values:
+ * O = softmax(scale * q K^T) V and LSE (natural log) for query heads Hq, a multiple
+ * G of the cache's Hk: query head h reads key head h / G.  Request r has
+ * kv_lens[r] cached tokens, token j in page block_table[r][j / page_size]; its
+ * queries are rows cu_q[r] .. cu_q[r + 1] of q (row r alone where cu_q is NULL) and
+ * stand for its last tokens, so that the i-th of n sees the tokens up to
+ * p = kv_lens[r] - n + i, and with window > 0 only those after p - window.  A row
+ * that sees no token gets O = 0 and LSE = -inf; rows of q outside every request
+ * are not written.
+ *   T           rows of q and o ([T][Hq][d], element strides {token, head}, FA_F16 or
+ *               FA_BF16); lse: fp32 [T][Hq] or NULL.
+ *   max_q_len   the largest number of rows of a request: a hint for the tile height
+ *               (a larger one is still computed).
+ *   table_width, table_stride  columns of block_table and its row stride.
+ * Lengths are device memory: the tokens of all requests are cut into equal shares
+ * on the GPU.  A page outside the cache contributes nothing and is recorded as
+ * FA_ERR_INDEX, as is a length beyond table_width * page_size, which is cut to that.
+ */
+typedef struct {
+  int R, T, Hq, dtype;
+  int max_q_len, window;
+  int table_width;
+  float scale;
+  long long table_stride;
+  long long q_stride[2], o_stride[2];
+} fa_kv4_attn_params;
+
+/* Bytes of workspace (shares that end inside a request's tokens, in fp32), 256-byte
+ * aligned, contents on entry do not matter; 0 on invalid arguments. */
+size_t fa_kv4_attention_workspace_size(const fa_kv4_cache* c, const fa_kv4_attn_params* p);
+fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, const void* q,
+                           const void* cache, const int* block_table, const int* kv_lens,
+                           const int* cu_q, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Block tables and slot maps of one step, from R request lengths, on the GPU.
+ * Request r holds seq_lens[r] tokens in the first ceil(seq_lens[r] / page_size)
+ * pages of its row of block_table; new_lens[r] tokens are added, or, where it is
+ * negative, the request has ended and its pages go back.  free_pages[0 ..
+ * free_count) is a stack: the ended requests' pages are put on top of it in order,
+ * then each request in turn takes the pages its new tokens need off the top, all
+ * or none.  A request is not served (no page, its tokens' slots -1, its length
+ * unchanged) when its tokens end past T, its pages past table_width, or, where it
+ * needs pages, when the pages wanted up to and including its own exceed the stack.
+ * Written:
+ *   block_table, free_pages   the entries that changed
+ *   kv_lens[R]                tokens held after the step (0 where ended)
+ *   cu_q[R + 1]               first of each request's new tokens, cut to T
+ *   positions[T], slots[T]    of each new token; 0 and -1 after the last one
+ *   counts[3]                 pages left on the stack, new tokens, pages missing
+ * kv_lens may be seq_lens and counts may be free_count (three ints): everything is
+ * read before anything is written.  Lengths below 0 count as 0 tokens; all arrays
+ * are device int32.  R in [1, FA_PLAN_MAX_REQUESTS].
+ */
+#define FA_PLAN_MAX_REQUESTS 8192
+typedef struct {
+  int R, T, page_size, num_pages; /* num_pages: entries of free_pages */
+  int table_width;
+  long long table_stride;
+} fa_plan_params;
+
+fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int* new_lens,
+                        int* block_table, int* free_pages, const int* free_count, int* kv_lens,
+                        int* cu_q, int* positions, int* slots, int* counts, void* stream);
 
 #ifdef __cplusplus
 }
