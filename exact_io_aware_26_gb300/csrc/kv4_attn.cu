@@ -26,12 +26,13 @@
 // score of the block is above it by more than 2^8 (one vote); then it is reduced by
 // shuffles and O and l are rescaled.  l is kept per lane and reduced at the end.
 //
-// Work.  All tiles (request, 8 NT query rows, key head) lie one after the other as
-// 16-token blocks; each CTA takes an equal share of all blocks, wherever it begins and
-// ends, so that ragged lengths leave no SM idle.  A tile inside one share is finished
-// there; one that is cut leaves fp32 (O, m, l) per share, which the second kernel adds.
-// Within a CTA the warps take the blocks of a tile in turn, each with its own ring of
-// bulk copies and its own m, l, O, joined in shared memory at the tile's end.
+// Work.  All tiles (request, 8 NT query rows, key head) lie one after the other as units
+// of 32 tokens; each CTA takes an equal share of all units, wherever it begins and ends,
+// so that ragged lengths leave no SM idle.  A tile inside one share is finished there;
+// one that is cut leaves fp32 (O, m, l) per share, which the second kernel adds (launched
+// with the first, it waits for it on the GPU).  Within a CTA the warps take the units of a
+// tile in turn, each with its own ring of bulk copies and its own m, l, O, joined in
+// shared memory at the tile's end.
 #include "kv4.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -42,18 +43,22 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;     // running maximum before any token is seen
-constexpr int kMinShare = 32;        // blocks: shares are not cut finer (8 per warp)
+constexpr int kUnit = 2 * kKvBlock;  // tokens a warp takes at a time
+constexpr int kMinShare = 16;        // units: shares are not cut finer (4 per warp)
 constexpr int kReqCache = 128;       // requests whose lengths a CTA keeps at hand
 
 template <int D, int NT>
 struct Cfg {
   using Blk = KvBlock<D>;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr int CTAS_PER_SM = NT == 1 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int LDO = D + 4;  // row pitch of the joined O, in floats
-  static constexpr int ring = kWarps * STAGES * Blk::bytes;
-  static constexpr int joined = kWarps * ROWS * LDO * 4;
+  static constexpr int stage = 2 * Blk::bytes;
+  static constexpr int ring = kWarps * STAGES * stage;
+  // a warp's O for the join goes where its last unit was, if that is large enough
+  static constexpr bool in_ring = ROWS * LDO * 4 <= stage;
+  static constexpr int joined = in_ring ? 0 : kWarps * ROWS * LDO * 4;
   static constexpr int qfrag = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int smem = ring + joined + qfrag;
 };
@@ -126,25 +131,26 @@ __device__ __forceinline__ Req load_req(const Kv4AttnArgs& a, int r) {
 }
 
 // Tile `t` of a request: rows [row0, row0 + ROWS) of its n * G, tokens [k0, k1) that some
-// row of it sees, blocks [b0, b0 + nb) (one, of hidden tokens, where no row sees any).
+// row of it sees, units from token u0 on, n_u of them (one, of hidden tokens, where no
+// row sees any).
 struct Tile {
-  int row0, rows, k0, k1, b0, nb;
+  int row0, rows, k0, k1, u0, n_u;
 };
 template <int ROWS>
 __device__ __forceinline__ int tiles_of(const Kv4AttnArgs& a, const Req& x) {
-  return (int)(((long long)x.n * a.G + ROWS - 1) / ROWS);
+  return (int)(((long long)x.n * a.G.d + ROWS - 1) / ROWS);
 }
 template <int ROWS>
 __device__ __forceinline__ Tile tile_of(const Kv4AttnArgs& a, const Req& x, int t) {
   Tile y;
   y.row0 = t * ROWS;
-  y.rows = min(ROWS, x.n * a.G - y.row0);
-  const int i0 = y.row0 / a.G, i1 = (y.row0 + y.rows - 1) / a.G;
+  y.rows = min(ROWS, x.n * (int)a.G.d - y.row0);
+  const int i0 = a.G.div(y.row0), i1 = a.G.div(y.row0 + y.rows - 1);
   y.k1 = max(0, x.kv - x.n + i1 + 1);
   y.k0 = a.window > 0 ? max(0, x.kv - x.n + i0 - a.window + 1) : 0;
   y.k0 = min(y.k0, y.k1);
-  y.b0 = y.k0 / kKvBlock;
-  y.nb = max(1, (y.k1 + kKvBlock - 1) / kKvBlock - y.b0);
+  y.u0 = y.k0 & ~(kUnit - 1);
+  y.n_u = max(1, (y.k1 - y.u0 + kUnit - 1) / kUnit);
   return y;
 }
 
@@ -181,6 +187,73 @@ struct Walk {
   }
 };
 
+// Where a warp's coming units lie, in shared memory: its copies' addresses are formed 32
+// units at a time, one by each lane, off the path of the unit loop.
+template <int ROWS>
+struct Feed {
+  Walk<ROWS> w;           // tile of the coming units
+  long long tile0;        // its first unit
+  int u, end;             // the warp's next unit of it, and the end of the share's part of it
+  int ids_r, ids_tok;     // request and first token that `id` was read for
+  int id[2][32];          // pages of the two blocks of each of the 32 units
+  ulonglong2 src[32];     // addresses of the two blocks; 1 for one that is not to be read
+  uint32_t hidden[8];     // per ring stage: bit h for block h not read
+};
+
+// Fills src with the warp's next units of the share, at most 32, all of one tile; returns
+// how many (0: none left).
+template <int D, int ROWS>
+__device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, const Req* reqs, int reqs_r0, int warp,
+                                        long long u1) {
+  using Blk = KvBlock<D>;
+  const int lane = threadIdx.x & 31, page_log = a.c.page_log;
+  __syncwarp();
+  Walk<ROWS> w = f.w;
+  long long tile0 = f.tile0;
+  int u = f.u, end = f.end;
+  const bool moved = u >= end;
+  while (u >= end) {
+    if (tile0 + w.y.n_u >= u1) return 0;
+    tile0 += w.y.n_u;
+    w.next(a, reqs, reqs_r0);
+    u = warp;
+    end = (int)min((long long)w.y.n_u, u1 - tile0);
+  }
+  const int first = w.y.u0 + u * kUnit, tok = first + lane * kWarps * kUnit;
+  int id0 = f.id[0][lane], id1 = f.id[1][lane];
+  if (f.ids_r != w.r || f.ids_tok != first) {  // not another head of the same tokens
+    const int pg0 = tok >> page_log, pg1 = (tok + kKvBlock) >> page_log;
+    const int* row = a.table + w.r * a.table_stride;
+    id0 = pg0 < a.table_width ? __ldg(row + pg0) : -1;
+    id1 = pg1 == pg0 ? id0 : pg1 < a.table_width ? __ldg(row + pg1) : -1;
+    f.id[0][lane] = id0;
+    f.id[1][lane] = id1;
+  }
+  const bool in0 = u + lane * kWarps < end && tok < w.y.k1, in1 = in0 && tok + kKvBlock < w.y.k1;
+  const bool ok0 = in0 && (unsigned)id0 < (unsigned)a.c.num_pages, ok1 = in1 && (unsigned)id1 < (unsigned)a.c.num_pages;
+  if ((in0 && !ok0) || (in1 && !ok1)) atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
+  auto place = [&](int id, int t) {
+    const int blk = (t & ((1 << page_log) - 1)) / kKvBlock;
+    return reinterpret_cast<unsigned long long>(a.c.data) + id * a.c.page_stride +
+           (((long long)w.h << (page_log - 4)) + blk) * Blk::bytes;
+  };
+  f.src[lane] = make_ulonglong2(ok0 ? place(id0, tok) : 1ull, ok1 ? place(id1, tok + kKvBlock) : 1ull);
+  __syncwarp();  // every lane has read the old state
+  const int n = min(32, (end - u + kWarps - 1) / kWarps);
+  if (lane == 0) {
+    f.ids_r = w.r;
+    f.ids_tok = first;
+    f.u = u + n * kWarps;
+    if (moved) {
+      f.w = w;
+      f.tile0 = tile0;
+      f.end = end;
+    }
+  }
+  __syncwarp();
+  return n;
+}
+
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_kernel(const Kv4AttnArgs a) {
   using C = Cfg<D, NT>;
@@ -188,31 +261,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
   constexpr int ROWS = C::ROWS, S = C::STAGES, KS = D / 16, MT = D / 16, WPT = D / 32 /* words per lane of K */;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][S];
-  __shared__ long long thread_end[kThreads];
+  __shared__ long long warp_units[kWarps];
   __shared__ Req reqs[kReqCache];
-  __shared__ long long start_s[2];
+  __shared__ long long start_u;
   __shared__ int start_r, start_t, start_h;
   __shared__ float m_s[kWarps][ROWS], l_s[kWarps][ROWS];
+  __shared__ int held_s[kWarps];
   __shared__ volatile int abort_s;
+  __shared__ Feed<ROWS> feed_s[kWarps];
+  __shared__ Walk<ROWS> tile_s[2];  // the current tile; the next one
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const uint32_t ring = smem_addr(smem) + warp * (S * Blk::bytes);
-  float* joined = reinterpret_cast<float*>(smem + C::ring);
+  const uint32_t ring = smem_addr(smem) + warp * (S * C::stage);
+  const uint32_t bar0 = smem_addr(&bars[warp][0]);
   uint2* qfrag = reinterpret_cast<uint2*>(smem + C::ring + C::joined);
   (void)qfrag;
 
-  // ---- shares: prefix sums of the blocks of all requests
+  // ---- shares: prefix sums of the units of all requests
   if (tid == 0) abort_s = 0;
   if (lane == 0)
-    for (int s = 0; s < S; ++s) mbar_init(smem_addr(&bars[warp][s]), 1);
+    for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
   fence_barrier_init();
   const int per = (a.R + kThreads - 1) / kThreads;
   const int my0 = min(a.R, tid * per), my1 = min(a.R, my0 + per);
+  auto units_of = [&](const Req& x) {
+    const int nt = tiles_of<ROWS>(a, x);
+    long long n = 0;
+    for (int t = 0; t < nt; ++t) n += tile_of<ROWS>(a, x, t).n_u;
+    return n * a.c.Hk;
+  };
   long long units = 0;
   for (int r = my0; r < my1; ++r) {
     const Req x = load_req(a, r);
-    const int nt = tiles_of<ROWS>(a, x);
-    for (int t = 0; t < nt; ++t) units += (long long)tile_of<ROWS>(a, x, t).nb * a.c.Hk;
+    if (per == 1) reqs[tid] = x;
+    units += units_of(x);
   }
   long long end = units;
 #pragma unroll
@@ -220,15 +303,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     const long long up = __shfl_up_sync(0xffffffffu, end, off);
     if (lane >= off) end += up;
   }
-  thread_end[tid] = end;
+  if (lane == 31) warp_units[warp] = end;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long total = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const long long x = thread_end[32 * w + 31];
-    if (w < warp) before += x;
-    total += x;
+    if (w < warp) end += warp_units[w];
+    total += warp_units[w];
   }
-  end += before;
   long long share = (total + gridDim.x - 1) / gridDim.x;
   share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
   const long long u0 = (long long)blockIdx.x * share, u1 = min(total, u0 + share);
@@ -236,101 +318,91 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  // the thread whose requests hold block u0 finds its tile
+  // the thread whose requests hold unit u0 finds its tile
   if (u0 < end && u0 >= end - units) {
     long long u = end - units;
     bool found = false;
     for (int r = my0; r < my1 && !found; ++r) {
-      const Req x = load_req(a, r);
+      const Req x = per == 1 ? reqs[tid] : load_req(a, r);
       const int nt = tiles_of<ROWS>(a, x);
       for (int t = 0; t < nt && !found; ++t) {
-        const long long nb = tile_of<ROWS>(a, x, t).nb;
-        if (u0 < u + nb * a.c.Hk) {
-          const long long h = (u0 - u) / nb;
+        const long long n = tile_of<ROWS>(a, x, t).n_u;
+        if (u0 < u + n * a.c.Hk) {
+          const int h = (int)((u0 - u) / n);
           start_r = r;
           start_t = t;
-          start_h = (int)h;
-          start_s[0] = u + h * nb;  // first block of the tile
+          start_h = h;
+          start_u = u + h * n;  // first unit of the tile
           found = true;
         } else {
-          u += nb * a.c.Hk;
+          u += n * a.c.Hk;
         }
       }
     }
   }
   __syncthreads();
-  const int cache_r0 = start_r;
-  for (int i = tid; i < kReqCache; i += kThreads)
-    if (cache_r0 + i < a.R) reqs[i] = load_req(a, cache_r0 + i);
-  __syncthreads();
+  const int cache_r0 = per == 1 ? 0 : start_r;
+  if (per > 1) {
+    for (int i = tid; i < kReqCache; i += kThreads)
+      if (cache_r0 + i < a.R) reqs[i] = load_req(a, cache_r0 + i);
+    __syncthreads();
+  }
 
   const WaitCtx wc{&abort_s, a.rep.st, a.rep.epoch, a.rep.wait_ns};
-  const int page_log = a.c.page_log - 4;  // blocks of a page, log2
 
-  // ---- producer state of this warp: the tile its next copy belongs to, the block of
-  // it, and the pages of its next 32 blocks (one per lane)
-  Walk<ROWS> pw;
-  pw.at(a, reqs, cache_r0, start_r, start_t, start_h);
-  Walk<ROWS> cw = pw;
-  long long p_tile0 = start_s[0];  // first block of the producer's tile, as a unit
-  int p_b = (int)(u0 - p_tile0) + warp;
-  int ids = -1, ids_r = -1, ids_b = 0;  // ... of request ids_r, from block ids_b on
-  uint32_t bad = 0;  // stages whose page is outside the cache
-  bool p_done = false;
-  auto refill = [&]() {  // pages of blocks p_b + 4 i (i < 32) of the producer's tile
-    const int b = p_b + lane * kWarps;
-    const int pg = (pw.y.b0 + b) >> page_log;
-    ids = pg < a.table_width ? __ldg(a.table + pw.r * a.table_stride + pg) : -1;
-    ids_r = pw.r;
-    ids_b = pw.y.b0 + p_b;
-  };
-  auto produce = [&](int stage) {  // the copy of this warp's next block, if any is left
-    while (!p_done && (p_b >= pw.y.nb || p_tile0 + p_b >= u1)) {
-      if (p_tile0 + pw.y.nb >= u1) {
-        p_done = true;
-        break;
-      }
-      p_tile0 += pw.y.nb;
-      pw.next(a, reqs, cache_r0);
-      p_b = warp;
+  Feed<ROWS>& feed = feed_s[warp];
+  if (lane == 0) {
+    feed.w.at(a, reqs, cache_r0, start_r, start_t, start_h);
+    feed.tile0 = start_u;
+    feed.u = (int)(u0 - start_u) + warp;
+    feed.end = (int)min((long long)feed.w.y.n_u, u1 - start_u);
+    feed.ids_r = -1;
+    if (warp == 0) tile_s[0] = feed.w;
+  }
+  int turn = 0, ready = 0;  // of feed.src
+  auto produce = [&](int stage) {  // the copies of this warp's next unit, if any is left
+    if (turn == ready) {
+      ready = feed_refill<D, ROWS>(a, feed, reqs, cache_r0, warp, u1);
+      turn = 0;
+      if (ready == 0) return;
     }
-    if (p_done) return;
-    const int ab = pw.y.b0 + p_b, i = (ab - ids_b) / kWarps;
-    if (ids_r != pw.r || ab < ids_b || i >= 32 || (ab - ids_b) % kWarps != 0) refill();
-    const int id = __shfl_sync(0xffffffffu, ids, (ab - ids_b) / kWarps);
-    const bool ok = (unsigned)id < (unsigned)a.c.num_pages && pw.y.k1 > pw.y.k0;
-    bad = (bad & ~(1u << stage)) | ((ok ? 0u : 1u) << stage);
     if (lane == 0) {
-      const uint32_t bar = smem_addr(&bars[warp][stage]);
-      if (ok) {
-        const uint8_t* src = a.c.data + id * a.c.page_stride +
-                             (((long long)pw.h << page_log) + (ab & ((1 << page_log) - 1))) * Blk::bytes;
-        mbar_arrive_expect_tx(bar, Blk::bytes);
-        bulk_load(ring + stage * Blk::bytes, src, Blk::bytes, bar);
+      const ulonglong2 src = feed.src[turn];
+      const uint32_t bar = bar0 + 8 * stage, dst = ring + stage * C::stage;
+      if (src.y == src.x + Blk::bytes) {
+        mbar_arrive_expect_tx(bar, C::stage);
+        bulk_load(dst, reinterpret_cast<const void*>(src.x), C::stage, bar);
+        feed.hidden[stage] = 0;
       } else {
-        if (pw.y.k1 > pw.y.k0) atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
-        mbar_arrive(bar);
+        const bool b0 = src.x == 1, b1 = src.y == 1;
+        mbar_arrive_expect_tx(bar, (uint32_t)(2 - b0 - b1) * Blk::bytes);
+        if (!b0) bulk_load(dst, reinterpret_cast<const void*>(src.x), Blk::bytes, bar);
+        if (!b1) bulk_load(dst + Blk::bytes, reinterpret_cast<const void*>(src.y), Blk::bytes, bar);
+        feed.hidden[stage] = (uint32_t)b0 | ((uint32_t)b1 << 1);
       }
     }
-    p_b += kWarps;
+    ++turn;
   };
 #pragma unroll 1
   for (int s = 0; s < S; ++s) produce(s);
+  __syncthreads();  // tile_s
 
   // ---- the share's tiles
-  int it = 0;  // blocks this warp has taken
+  int stage = 0;
+  uint32_t parity = 0;
   int4 meta = make_int4(-1, 0, 0, 0);
-  long long tile0 = start_s[0];
-  while (tile0 < u1) {
+  long long tile0 = start_u;
+#pragma unroll 1
+  for (int which = 0; tile0 < u1; which ^= 1) {
+    const Walk<ROWS>& cw = tile_s[which];
     const Tile y = cw.y;
     const Req x = cw.x;
-    const int first = (int)max(0ll, u0 - tile0), last = (int)min((long long)y.nb, u1 - tile0);
+    const int first = (int)max(0ll, u0 - tile0), last = (int)min((long long)y.n_u, u1 - tile0);
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
     // which its score factor takes back: no 16-bit query leaves fp16's range.
     uint32_t qf[NT == 4 ? 1 : NT][KS][2];
     float factor[NT][2];
-    int lim[NT][2], low[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int n = g + 8 * j;
@@ -338,10 +410,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
       if (n < y.rows) {
-        const int row = y.row0 + n, qi = row / a.G;
+        const int row = y.row0 + n, qi = a.G.div(row);
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q) + (x.q0 + qi) * a.qs[0] +
-            ((long long)cw.h * a.G + row % a.G) * a.qs[1] + t4 * (D / 4));
+            ((long long)cw.h * a.G.d + (row - qi * (int)a.G.d)) * a.qs[1] + t4 * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(src + i);
       }
@@ -382,18 +454,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         }
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float u = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + c));
-        factor[j][c] = u * a.scale_log2;
-        const int row = y.row0 + 8 * j + 2 * t4 + c;
-        const int pos = x.kv - x.n + row / a.G;  // rows behind the last: of no consequence
-        lim[j][c] = min(pos + 1, x.kv);
-        low[j][c] = a.window > 0 ? pos - a.window + 1 : 0;
-      }
+      for (int c = 0; c < 2; ++c) factor[j][c] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + c)) * a.scale_log2;
     }
     if constexpr (NT == 4) __syncthreads();
-    // tokens that every row sees: no comparisons in their blocks
-    const int i0 = y.row0 / a.G, i1 = (y.row0 + y.rows - 1) / a.G;
+    // tokens that every row sees: no comparisons in their units
+    const int i0 = a.G.div(y.row0), i1 = a.G.div(y.row0 + y.rows - 1);
     const int all_hi = x.kv - x.n + i0 + 1;
     const int all_lo = a.window > 0 ? x.kv - x.n + i1 - a.window + 1 : 0;
 
@@ -407,26 +472,107 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
     }
+    const int kr = g ^ ((g >> 1) & 1);  // token of fragment row g of a block (and kr + 8 of row g + 8)
+    // S^T of a block: raw products
+    auto scores = [&](uint32_t kb, float (&s)[NT][4]) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[j][c] = 0.f;
+      uint32_t wa[WPT], wb[WPT];
+      const uint32_t ra = kb + kr * Blk::row + t4 * (D / 8), rb = ra + 8 * Blk::row;
+      if constexpr (D == 128) {
+        const uint4 u = ld_shared_v4(ra), v = ld_shared_v4(rb);
+        wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
+        wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
+      } else {
+        const uint2 u = lds64(ra), v = lds64(rb);
+        wa[0] = u.x; wa[1] = u.y;
+        wb[0] = v.x; wb[1] = v.y;
+      }
+      const uint32_t pa = kb + Blk::codes + (kr * Blk::groups + (D == 128 ? t4 : t4 >> 1)) * 4;
+      const uint32_t xa = lds32(pa), xb = lds32(pa + 8 * Blk::groups * 4);
+      const uint32_t sa = __byte_perm(xa, xa, 0x1010), ca = __byte_perm(xa, xa, 0x3232);
+      const uint32_t sb = __byte_perm(xb, xb, 0x1010), cb = __byte_perm(xb, xb, 0x3232);
+#pragma unroll
+      for (int i = 0; i < WPT; ++i) {
+        const uint32_t a0 = hfma2(code_pair<0>(wa[i]), sa, ca), a1 = hfma2(code_pair<0>(wb[i]), sb, cb);
+        const uint32_t a2 = hfma2(code_pair<1>(wa[i]), sa, ca), a3 = hfma2(code_pair<1>(wb[i]), sb, cb);
+        const uint32_t c0 = hfma2(code_pair<2>(wa[i]), sa, ca), c1 = hfma2(code_pair<2>(wb[i]), sb, cb);
+        const uint32_t c2 = hfma2(code_pair<3>(wa[i]), sa, ca), c3 = hfma2(code_pair<3>(wb[i]), sb, cb);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint2 q0, q1;
+          if constexpr (NT == 4) {
+            q0 = qfrag[(j * KS + 2 * i) * 32 + lane];
+            q1 = qfrag[(j * KS + 2 * i + 1) * 32 + lane];
+          } else {
+            q0 = make_uint2(qf[j][2 * i][0], qf[j][2 * i][1]);
+            q1 = make_uint2(qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+          }
+          mma16816(s[j], a0, a1, a2, a3, q0.x, q0.y);
+          mma16816(s[j], c0, c1, c2, c3, q1.x, q1.y);
+        }
+      }
+    };
+    // O^T += V^T P^T of a block: this lane's tokens are those of fragment rows 2 t, 2 t + 1 and 8 more
+    auto values = [&](uint32_t vb, const uint32_t (&p0)[NT], const uint32_t (&p1)[NT]) {
+      constexpr int WV = D / 64;  // words of codes of a token per lane (8 channels each)
+      const int e0 = 2 * t4, e1 = 2 * t4 + 1;
+      const int ke = e0 ^ ((e0 >> 1) & 1), kf = e1 ^ ((e1 >> 1) & 1);
+      uint32_t w[4][WV], pr[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int key = (q & 1 ? kf : ke) + (q >> 1) * 8;
+        const uint32_t at = vb + key * Blk::row + g * (D / 16);
+        if constexpr (D == 128) {
+          const uint2 u = lds64(at);
+          w[q][0] = u.x;
+          w[q][1] = u.y;
+        } else {
+          w[q][0] = lds32(at);
+        }
+        pr[q] = lds32(vb + Blk::codes + (key * Blk::groups + (D == 128 ? g >> 1 : g >> 2)) * 4);
+      }
+      const uint32_t sx = __byte_perm(pr[0], pr[1], 0x5410), cx = __byte_perm(pr[0], pr[1], 0x7632);
+      const uint32_t sy = __byte_perm(pr[2], pr[3], 0x5410), cy = __byte_perm(pr[2], pr[3], 0x7632);
+#pragma unroll
+      for (int i = 0; i < WV; ++i) {
+        const uint32_t xl = __byte_perm(w[0][i], w[1][i], 0x5410), xh = __byte_perm(w[0][i], w[1][i], 0x7632);
+        const uint32_t yl = __byte_perm(w[2][i], w[3][i], 0x5410), yh = __byte_perm(w[2][i], w[3][i], 0x7632);
+        auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          a0 = hfma2(a0, sx, cx);
+          a1 = hfma2(a1, sx, cx);
+          a2 = hfma2(a2, sy, cy);
+          a3 = hfma2(a3, sy, cy);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma16816(o[mt][j], a0, a1, a2, a3, p0[j], p1[j]);
+        };
+        product(4 * i + 0, code_pair<0>(xl), code_pair<0>(xh), code_pair<0>(yl), code_pair<0>(yh));
+        product(4 * i + 1, code_pair<1>(xl), code_pair<1>(xh), code_pair<1>(yl), code_pair<1>(yh));
+        product(4 * i + 2, code_pair<2>(xl), code_pair<2>(xh), code_pair<2>(yl), code_pair<2>(yh));
+        product(4 * i + 3, code_pair<3>(xl), code_pair<3>(xh), code_pair<3>(yl), code_pair<3>(yh));
+      }
+    };
 
+    int held = -1;  // stage of the tile's last unit, kept for the join (C::in_ring)
 #pragma unroll 1
-    for (int b = first + warp; b < last; b += kWarps) {
-      const int stage = it % S;
-      const uint32_t parity = (uint32_t)(it / S) & 1u;
+    for (int u = first + warp; u < last; u += kWarps) {
       // a wait that gave up has recorded it; the copy must still land before the stage is left
-      if (!warp_wait(wc, smem_addr(&bars[warp][stage]), parity)) mbar_drain(wc, smem_addr(&bars[warp][stage]), parity);
-      const uint32_t kb = ring + stage * Blk::bytes, vb = kb + Blk::half;
-      const int key0 = (y.b0 + b) * kKvBlock;
-      const int kr = g ^ ((g >> 1) & 1);  // token of fragment row g (and kr + 8 of row g + 8)
-      const bool hidden = (bad >> stage) & 1u;
-      const bool masked = hidden || key0 + kKvBlock > all_hi || key0 < all_lo;
+      if (!warp_wait(wc, bar0 + 8 * stage, parity)) mbar_drain(wc, bar0 + 8 * stage, parity);
+      const uint32_t kb = ring + stage * C::stage;
+      const int key0 = y.u0 + u * kUnit;
+      const uint32_t hidden = feed.hidden[stage];
+      const bool masked = hidden || key0 + kUnit > all_hi || key0 < all_lo;
       uint32_t nan_keys = 0;
       if (masked) {
         // values that no row sees must not reach the product (0 x NaN), nor a NaN that only
         // some rows see: their pairs become 0, and a NaN one marks its token's scores
-        for (int e = lane; e < kKvBlock * Blk::groups; e += 32) {
+        for (int e = lane; e < kUnit * Blk::groups; e += 32) {
           const int key = e / Blk::groups;
-          const uint32_t at = vb + Blk::codes + e * 4, pair = lds32(at);
-          const bool seen = !hidden && key0 + key >= y.k0 && key0 + key < y.k1;
+          const uint32_t at = kb + (key / kKvBlock) * Blk::bytes + Blk::half + Blk::codes + (e % (kKvBlock * Blk::groups)) * 4;
+          const uint32_t pair = lds32(at);
+          const bool seen = !((hidden >> (key / kKvBlock)) & 1u) && key0 + key >= y.k0 && key0 + key < y.k1;
           const __half2 h = *reinterpret_cast<const __half2*>(&pair);
           const bool nan = __hisnan(__low2half(h)) || __hisnan(__high2half(h));
           if (!seen || nan) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
@@ -436,81 +582,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         __syncwarp();
         fence_async_smem();  // these stores before the copy that reuses the stage
       }
-
-      // S^T
-      float s[NT][4];
+      float s[2][NT][4];
+      scores(kb, s[0]);
+      scores(kb + Blk::bytes, s[1]);
+      // in log2 units; hidden tokens
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[j][c] = 0.f;
-      {
-        uint32_t wa[WPT], wb[WPT];
-        const uint32_t ra = kb + kr * Blk::row + t4 * (D / 8), rb = ra + 8 * Blk::row;
-        if constexpr (D == 128) {
-          const uint4 u = ld_shared_v4(ra), v = ld_shared_v4(rb);
-          wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
-          wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
-        } else {
-          const uint2 u = lds64(ra), v = lds64(rb);
-          wa[0] = u.x; wa[1] = u.y;
-          wb[0] = v.x; wb[1] = v.y;
-        }
-        const uint32_t pa = kb + Blk::codes + (kr * Blk::groups + (D == 128 ? t4 : t4 >> 1)) * 4;
-        const uint32_t xa = lds32(pa), xb = lds32(pa + 8 * Blk::groups * 4);
-        const uint32_t sa = __byte_perm(xa, xa, 0x1010), ca = __byte_perm(xa, xa, 0x3232);
-        const uint32_t sb = __byte_perm(xb, xb, 0x1010), cb = __byte_perm(xb, xb, 0x3232);
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < WPT; ++i) {
-          const uint32_t a0 = hfma2(code_pair<0>(wa[i]), sa, ca), a1 = hfma2(code_pair<0>(wb[i]), sb, cb);
-          const uint32_t a2 = hfma2(code_pair<1>(wa[i]), sa, ca), a3 = hfma2(code_pair<1>(wb[i]), sb, cb);
-          const uint32_t c0 = hfma2(code_pair<2>(wa[i]), sa, ca), c1 = hfma2(code_pair<2>(wb[i]), sb, cb);
-          const uint32_t c2 = hfma2(code_pair<3>(wa[i]), sa, ca), c3 = hfma2(code_pair<3>(wb[i]), sb, cb);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint2 q0, q1;
-            if constexpr (NT == 4) {
-              q0 = qfrag[(j * KS + 2 * i) * 32 + lane];
-              q1 = qfrag[(j * KS + 2 * i + 1) * 32 + lane];
-            } else {
-              q0 = make_uint2(qf[j][2 * i][0], qf[j][2 * i][1]);
-              q1 = make_uint2(qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
-            }
-            mma16816(s[j], a0, a1, a2, a3, q0.x, q0.y);
-            mma16816(s[j], c0, c1, c2, c3, q1.x, q1.y);
-          }
-        }
-      }
-      // scores in log2 units; hidden tokens
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s[j][c] *= factor[j][c & 1];
+          for (int c = 0; c < 4; ++c) s[h][j][c] *= factor[j][c & 1];
       if (masked) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = kr + (c >= 2 ? 8 : 0);
-            const bool seen = !hidden && key0 + key < lim[j][c & 1] && key0 + key >= low[j][c & 1];
-            s[j][c] = !seen ? -INFINITY : (nan_keys >> key) & 1u ? NAN : s[j][c];
+          for (int c = 0; c < 2; ++c) {
+            const int pos = x.kv - x.n + a.G.div(y.row0 + 8 * j + 2 * t4 + c);  // rows behind the last: of no consequence
+            const int lim = min(pos + 1, x.kv) - key0, low = (a.window > 0 ? pos - a.window + 1 : 0) - key0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int key = 16 * h + 8 * q + kr;
+                const bool seen = !((hidden >> h) & 1u) && key < lim && key >= low;
+                float& v = s[h][j][2 * q + c];
+                v = !seen ? -INFINITY : (nan_keys >> key) & 1u ? NAN : v;
+              }
           }
       }
-      // the running maximum, moved when a score is above it by more than 2^8
+      // the running maximum, moved when a score is above it by more than 8
+      float most[NT][2];
       bool grow = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) grow |= s[j][c] > m[j][c & 1] + 8.f;
+        for (int c = 0; c < 2; ++c) {
+          most[j][c] = fmax3(fmaxf(s[0][j][c], s[0][j][c + 2]), s[1][j][c], s[1][j][c + 2]);
+          grow |= most[j][c] > m[j][c] + 8.f;
+        }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(s[j][c], s[j][c + 2]);
+            float top = fmaxf(most[j][c], m[j][c]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, m[j][c]);
             const float back = ex2(m[j][c] - top);
             m[j][c] = top;
             l[j][c] *= back;
@@ -522,63 +640,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
           }
       }
       // weights, and their transpose as the B operand
-      uint32_t p0[NT], p1[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p0[NT], p1[NT];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[j][c] = ex2(s[j][c] - m[j][c & 1]);
-        l[j][0] += s[j][0] + s[j][2];
-        l[j][1] += s[j][1] + s[j][3];
-        p0[j] = transpose8x8(pack2<true>(s[j][0], s[j][1]));
-        p1[j] = transpose8x8(pack2<true>(s[j][2], s[j][3]));
-      }
-      // O^T += V^T P^T: this lane's tokens are those of fragment rows 2 t, 2 t + 1 and 8 more
-      {
-        constexpr int WV = D / 64;  // words of codes of a token per lane (8 channels each)
-        const int e0 = 2 * t4, e1 = 2 * t4 + 1;
-        const int ke = e0 ^ ((e0 >> 1) & 1), kf = e1 ^ ((e1 >> 1) & 1);
-        uint32_t w[4][WV], pr[4];
+        for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int key = (q & 1 ? kf : ke) + (q >> 1) * 8;
-          const uint32_t at = vb + key * Blk::row + g * (D / 16);
-          if constexpr (D == 128) {
-            const uint2 u = lds64(at);
-            w[q][0] = u.x;
-            w[q][1] = u.y;
-          } else {
-            w[q][0] = lds32(at);
-          }
-          pr[q] = lds32(vb + Blk::codes + (key * Blk::groups + (D == 128 ? g >> 1 : g >> 2)) * 4);
+          for (int c = 0; c < 4; ++c) s[h][j][c] = ex2(s[h][j][c] - m[j][c & 1]);
+          l[j][0] += s[h][j][0] + s[h][j][2];
+          l[j][1] += s[h][j][1] + s[h][j][3];
+          p0[j] = transpose8x8(pack2<true>(s[h][j][0], s[h][j][1]));
+          p1[j] = transpose8x8(pack2<true>(s[h][j][2], s[h][j][3]));
         }
-        const uint32_t sx = __byte_perm(pr[0], pr[1], 0x5410), cx = __byte_perm(pr[0], pr[1], 0x7632);
-        const uint32_t sy = __byte_perm(pr[2], pr[3], 0x5410), cy = __byte_perm(pr[2], pr[3], 0x7632);
-#pragma unroll
-        for (int i = 0; i < WV; ++i) {
-          const uint32_t xl = __byte_perm(w[0][i], w[1][i], 0x5410), xh = __byte_perm(w[0][i], w[1][i], 0x7632);
-          const uint32_t yl = __byte_perm(w[2][i], w[3][i], 0x5410), yh = __byte_perm(w[2][i], w[3][i], 0x7632);
-          auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-            a0 = hfma2(a0, sx, cx);
-            a1 = hfma2(a1, sx, cx);
-            a2 = hfma2(a2, sy, cy);
-            a3 = hfma2(a3, sy, cy);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(o[mt][j], a0, a1, a2, a3, p0[j], p1[j]);
-          };
-          product(4 * i + 0, code_pair<0>(xl), code_pair<0>(xh), code_pair<0>(yl), code_pair<0>(yh));
-          product(4 * i + 1, code_pair<1>(xl), code_pair<1>(xh), code_pair<1>(yl), code_pair<1>(yh));
-          product(4 * i + 2, code_pair<2>(xl), code_pair<2>(xh), code_pair<2>(yl), code_pair<2>(yh));
-          product(4 * i + 3, code_pair<3>(xl), code_pair<3>(xh), code_pair<3>(yl), code_pair<3>(yh));
-        }
+        values(kb + h * Blk::bytes + Blk::half, p0, p1);
       }
       __syncwarp();  // every lane has read the stage
-      produce(stage);
-      ++it;
+      if (C::in_ring && u + kWarps >= last)
+        held = stage;
+      else
+        produce(stage);
+      if (++stage == S) {
+        stage = 0;
+        parity ^= 1u;
+      }
     }
 
-    // ---- join the warps that took blocks of the tile
+    // ---- join the warps that took units of the tile
     const int active = min(kWarps, last - first);
+    auto joined = [&](int w) {  // warp w's O, [ROWS][LDO]
+      return C::in_ring ? reinterpret_cast<float*>(smem + w * (S * C::stage)) : reinterpret_cast<float*>(smem + C::ring + w * ROWS * C::LDO * 4);
+    };
     if (warp < active) {
+      float* mine = joined(warp) + (C::in_ring ? held * (C::stage / 4) : 0);
+      if (lane == 0) held_s[warp] = held;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -592,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
             m_s[warp][row] = m[j][c];
             l_s[warp][row] = v;
           }
-          float* to = joined + (warp * ROWS + row) * C::LDO + g * (D / 8);
+          float* to = mine + row * C::LDO + g * (D / 8);
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
             *reinterpret_cast<float4*>(to + 8 * i) =
@@ -604,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
       }
     }
     __syncthreads();
-    const bool from_before = first > 0, goes_on = tile0 + y.nb > u1;
+    const bool from_before = first > 0, goes_on = tile0 + y.n_u > u1;
     constexpr int TPR = D / 8;  // threads per row, 8 channels each
     for (int e = tid; e < ROWS * TPR; e += kThreads) {
       const int row = e / TPR, ch = (e % TPR) * 8;
@@ -615,7 +709,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
       for (int w = 0; w < active; ++w) {
         const float f = ex2(m_s[w][row] - top);
         sum = fmaf(f, l_s[w][row], sum);
-        const float4* src = reinterpret_cast<const float4*>(joined + (w * ROWS + row) * C::LDO + ch);
+        const float4* src = reinterpret_cast<const float4*>(
+            joined(w) + (C::in_ring ? held_s[w] * (C::stage / 4) : 0) + row * C::LDO + ch);
         const float4 u = src[0], v = src[1];
         acc[0] = fmaf(f, u.x, acc[0]); acc[1] = fmaf(f, u.y, acc[1]);
         acc[2] = fmaf(f, u.z, acc[2]); acc[3] = fmaf(f, u.w, acc[3]);
@@ -632,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         }
       } else {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int gr = y.row0 + row, qi = gr / a.G;
-        const long long head = (long long)cw.h * a.G + gr % a.G;
+        const int gr = y.row0 + row, qi = a.G.div(gr);
+        const long long head = (long long)cw.h * a.G.d + (gr - qi * (int)a.G.d);
         uint16_t* to = static_cast<uint16_t*>(a.o) + (x.q0 + qi) * a.os[0] + head * a.os[1] + ch;
         if (fa_bounds(a.rep.st, x.q0 + qi < a.T && head < a.Hq)) {
           *reinterpret_cast<uint4*>(to) =
@@ -645,56 +740,100 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         }
       }
     }
-    if (goes_on && !from_before) {
-      const long long tile_end = tile0 + y.nb;
-      meta = make_int4(cw.r, cw.t, cw.h, (int)((tile_end - 1) / share));
+    if (tid == 0) {
+      const long long tile_end = tile0 + y.n_u;
+      if (goes_on && !from_before) meta = make_int4(cw.r, cw.t, cw.h, (int)((tile_end - 1) / share));
+      if (tile_end < u1) {
+        Walk<ROWS> w = cw;
+        w.next(a, reqs, cache_r0);
+        tile_s[which ^ 1] = w;
+      }
     }
-    __syncthreads();  // joined, m_s, l_s read
-    tile0 += y.nb;
-    if (tile0 < u1) cw.next(a, reqs, cache_r0);
+    __syncthreads();  // joined, m_s, l_s read; the next tile known
+    if (C::in_ring && held >= 0) {
+      fence_async_smem();  // the join's stores before the copy that reuses the stage
+      produce(held);
+    }
+    tile0 += y.n_u;
   }
   if (tid == 0) a.meta[blockIdx.x] = meta;
 }
 
-// Adds the shares of the tile that starts in share blockIdx.x and goes on, if any.
-// One warp per row: the row's slots are read with 4 (d = 128) or 2 channels per lane.
+// Adds the shares of the tile that starts in share blockIdx.x and goes on, if any; rows
+// 8 blockIdx.y .. + 7 of it.  The warps divide the shares, each lane D / 32 channels.
+constexpr int kMergeWarps = 8;
 template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4AttnArgs a) {
   constexpr int ROWS = 8 * NT, CPL = D / 32;
+  __shared__ float top_s[kMergeWarps][8], sum_s[kMergeWarps][8];
+  __shared__ float acc_s[kMergeWarps][8][D + 4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = a.meta[blockIdx.x];
   if (meta.x < 0) return;
   const Req x = load_req(a, meta.x);
   const Tile y = tile_of<ROWS>(a, x, meta.y);
-  const int lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x;
-  for (int row = threadIdx.x >> 5; row < y.rows; row += 8) {
-    auto slot = [&](int c) {  // the first share's slot is its second one
-      return a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * ROWS + row) * (D + 4);
-    };
+  const int r0 = 8 * blockIdx.y, rows = min(8, y.rows - r0);
+  if (rows <= 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
+  auto slot = [&](int c, int row) {  // the first share's slot is its second one
+    return a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * ROWS + r0 + row) * (D + 4);
+  };
+  // the rows' largest maxima
+  {
     float top = kNoMax;
-    for (int c = c0 + lane; c <= meta.w; c += 32) top = fmaxf(top, slot(c)[0]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float sum = 0.f, acc[CPL] = {};
-#pragma unroll 4
-    for (int c = c0; c <= meta.w; ++c) {
-      const float* s = slot(c);
-      const float f = ex2(s[0] - top);
-      sum = fmaf(f, s[1], sum);
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) acc[i] = fmaf(f, s[4 + lane * CPL + i], acc[i]);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int gr = y.row0 + row, qi = gr / a.G;
-    const long long head = (long long)meta.z * a.G + gr % a.G;
-    if (!fa_bounds(a.rep.st, x.q0 + qi < a.T && head < a.Hq)) continue;
-    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + (x.q0 + qi) * a.os[0] +
-                                               head * a.os[1] + lane * CPL);
-#pragma unroll
-    for (int i = 0; i < CPL / 2; ++i) to[i] = pack2<F16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (lane == 0 && a.lse)
-      a.lse[(long long)(x.q0 + qi) * a.Hq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    const int row = lane & 7;
+    if (row < rows)
+      for (int c = c0 + (threadIdx.x >> 3); c <= meta.w; c += 4 * kMergeWarps) top = fmaxf(top, slot(c, row)[0]);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    if (lane < 8) top_s[warp][row] = top;
   }
+  __syncthreads();
+  float top[8], sum[8] = {}, acc[8][CPL] = {};
+#pragma unroll
+  for (int row = 0; row < 8; ++row) {
+    top[row] = top_s[0][row];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) top[row] = fmaxf(top[row], top_s[w][row]);
+  }
+  for (int c = c0 + warp; c <= meta.w; c += kMergeWarps) {
+#pragma unroll
+    for (int row = 0; row < 8; ++row) {
+      if (row < rows) {
+        const float* s = slot(c, row);
+        const float f = ex2(s[0] - top[row]);
+        sum[row] = fmaf(f, s[1], sum[row]);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) acc[row][i] = fmaf(f, s[4 + lane * CPL + i], acc[row][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int row = 0; row < 8; ++row) {
+    if (lane == 0) sum_s[warp][row] = sum[row];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) acc_s[warp][row][lane * CPL + i] = acc[row][i];
+  }
+  __syncthreads();
+  const int row = warp;
+  if (row >= rows) return;
+  float total = 0.f, best = kNoMax, v[CPL] = {};
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    best = fmaxf(best, top_s[w][row]);
+    total += sum_s[w][row];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) v[i] += acc_s[w][row][lane * CPL + i];
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const int gr = y.row0 + r0 + row, qi = a.G.div(gr);
+  const long long head = (long long)meta.z * a.G.d + (gr - qi * (int)a.G.d);
+  if (!fa_bounds(a.rep.st, x.q0 + qi < a.T && head < a.Hq)) return;
+  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + (x.q0 + qi) * a.os[0] + head * a.os[1] + lane * CPL);
+#pragma unroll
+  for (int i = 0; i < CPL / 2; ++i) to[i] = pack2<F16>(v[2 * i] * inv, v[2 * i + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[(long long)(x.q0 + qi) * a.Hq + head] = total == 0.f ? -INFINITY : (best + log2f(total)) * 0.6931471805599453f;
 }
 
 template <int D, int NT, bool F16>
@@ -704,8 +843,16 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   kv4_attn_kernel<D, NT, F16><<<ctas, kThreads, C::smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kv4_merge_kernel<D, NT, F16><<<ctas, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, NT);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16>, a);
 }
 
 template <int D, bool F16>

@@ -45,9 +45,25 @@ struct Kv4RowArgs {
 cudaError_t launch_kv4_append(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
 
+// Quotients by a fixed divisor of numbers below 2^31: a multiplication, an addition and a
+// shift (with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1).
+struct FastDiv {
+  uint32_t d, m, s;
+  static FastDiv of(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
+    return f;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+#endif
+};
+
 struct Kv4AttnArgs {
   Kv4Cache c;
-  int R, T, Hq, G;
+  int R, T, Hq;
+  FastDiv G;  // query heads of a key head
   int window;
   int table_width;
   long long table_stride;

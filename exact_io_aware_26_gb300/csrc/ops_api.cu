@@ -54,6 +54,8 @@ fa_status check_strides(const long long* stride, const long long* size, int n, l
     if (stride[i] < 0 || stride[i] % vec != 0)
       return fail(FA_ERR_INVALID, "%s: stride %lld is negative or no multiple of 16 bytes", name, stride[i]);
   if (!written) return FA_OK;
+  for (int i = 0; i < n; ++i)
+    if (size[i] == 0) return FA_OK;  // no element
   std::sort(order, order + n, [&](int x, int y) { return stride[x] < stride[y]; });
   long long extent = inner;
   for (int i = 0; i < n; ++i) {
@@ -352,7 +354,7 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   a.R = p->R;
   a.T = p->T;
   a.Hq = p->Hq;
-  a.G = p->Hq / c->Hk;
+  a.G = FastDiv::of((uint32_t)(p->Hq / c->Hk));
   a.window = p->window;
   a.table_width = p->table_width;
   a.table_stride = p->table_stride;
@@ -365,7 +367,7 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   std::memcpy(a.qs, p->q_stride, sizeof(a.qs));
   std::memcpy(a.os, p->o_stride, sizeof(a.os));
   a.lse = lse;
-  const int rows = kv4_tile_rows(a.G, p->max_q_len);
+  const int rows = kv4_tile_rows((int)a.G.d, p->max_q_len);
   const int ctas = kv4_max_ctas(c->d, rows, std::min(sms, kMaxSms));
   a.part = static_cast<float*>(workspace);
   a.meta = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attn_part_bytes(ctas, rows, c->d));

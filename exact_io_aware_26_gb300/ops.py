@@ -26,7 +26,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import math
 from typing import Optional
 
@@ -95,9 +94,27 @@ def signatures() -> dict:
 
 
 # ---------------------------------------------------------------- checks
+# A call's checks and its C parameters depend on its arguments' sizes, strides, types and
+# devices alone.  They are done once for each such signature; later calls with the same
+# one look it up (a call on sixteen tokens takes the GPU a few microseconds: the checks
+# would take longer).
+
+_seen: dict = {}
+
+
+def _remember(key, plan):
+    if len(_seen) >= 4096:
+        _seen.clear()
+    _seen[key] = plan
+    return plan
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
 
 def _need(t, name: str, dtype, shape=None):
-    """t is a cuda tensor on the current device of the dtype and, with None for any, the shape."""
+    """t is a cuda tensor of the dtype and, with None for any, the shape."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a cuda tensor")
     if t.dtype != dtype:
@@ -106,11 +123,12 @@ def _need(t, name: str, dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
 
 
-def _same_device(*tensors):
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor on {t.device}: every tensor must be on the current device, cuda:{here}")
+def _one_device(*tensors) -> torch.device:
+    """The device of the tensors, which must be one."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"every tensor must be on one device, not on {sorted(map(str, devices))}")
+    return devices.pop()
 
 
 def _contiguous(t, name: str):
@@ -126,24 +144,31 @@ def _strides(t, name: str, dims) -> tuple:
     return tuple(stride[i] if shape[i] > 1 else 0 for i in dims)
 
 
-def _enter(stream, *inputs):
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_HERE = contextlib.nullcontext()
+
+
+def _enter(device, stream, *inputs):
     """(stream handle, context to allocate in): results and workspaces belong to the stream
     that the kernels run on, and inputs made on another one are marked as used there."""
-    current = torch.cuda.current_stream()
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    current = _raw_stream(device.index)
     if stream is None:
-        return current.cuda_stream, contextlib.nullcontext()
+        return current, _HERE
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    if stream.cuda_stream == current.cuda_stream:
-        return stream.cuda_stream, contextlib.nullcontext()
+    if stream.cuda_stream == current:
+        return current, _HERE
     for t in inputs:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream, torch.cuda.stream(stream)
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 # ---------------------------------------------------------------- norms and rotation
@@ -164,45 +189,54 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, inv_freq=None, device="cuda"
     return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
-@functools.lru_cache(maxsize=256)
-def _qk_params(B, N, Hq, Hk, d, dtype, w_dtype, rot, interleaved, eps, pos_stride, q, k, yq, yk, dq, dk):
-    p = FaQkParams(B, N, Hq, Hk, d, dtype, w_dtype, rot, interleaved, eps, pos_stride, _I64x3(*q), _I64x3(*k),
-                   _I64x3(*yq), _I64x3(*yk), _I64x3(*dq), _I64x3(*dk))
-    return p, ctypes.byref(p)
-
-
 _BNH, _BHN = (0, 1, 2), (0, 2, 1)  # where batch, token and head stand in the two layouts
 
 
-def _qk_shapes(q, k, wq, wk, freqs, positions):
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q and k must be [B, N, H, d]")
-    B, N, Hq, d = q.shape
+def _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, y, dx):
+    """(C parameters, their address, device, shapes of q and k in the result's layout)."""
     dt = q.dtype
     if dt not in _CODES:
         raise TypeError(f"unsupported dtype {dt}")
-    _need(q, "q", dt)
+    _need(q, "q", dt, (None, None, None, None))
+    B, N, Hq, d = q.shape
     _need(k, "k", dt, (B, N, None, d))
-    wt = wq.dtype
+    Hk, wt = k.shape[2], wq.dtype
     if wt != dt and wt != torch.float32:
         raise TypeError(f"the weights must be {dt} or torch.float32, not {wt}")
-    _need(wq, "wq", wt, (d,))
-    _need(wk, "wk", wt, (d,))
-    _contiguous(wq, "wq")
-    _contiguous(wk, "wk")
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        _need(w, name, wt, (d,))
+        _contiguous(w, name)
     _need(freqs, "freqs", torch.int64, (None,))
     _contiguous(freqs, "freqs")
     pos_stride = 0
     if positions is not None:
-        if positions.dim() == 1:
-            _need(positions, "positions", torch.int32, (N,))
-        else:
-            _need(positions, "positions", torch.int32, (B, N))
-            pos_stride = positions.stride(0) if B > 1 else 0
+        _need(positions, "positions", torch.int32, (N,) if positions.dim() == 1 else (B, N))
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
         if N > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous in its last dimension")
-    _same_device(q, k, wq, wk, freqs, positions)
-    return B, N, Hq, k.shape[2], d, _CODES[dt], _CODES[wt], 2 * freqs.shape[0], pos_stride
+    device = _one_device(q, k, wq, wk, freqs, positions, *y, *dx)
+    names = ("dyq", "dyk") if dx else ("out[0]", "out[1]")
+    ys, ds, shapes = [], [], []
+    for i, h in enumerate((Hq, Hk)):
+        shape = (B, h, N, d) if heads_first else (B, N, h, d)
+        shapes.append(shape)
+        if y[i] is None:  # a new tensor, contiguous
+            st = (h * N * d, d if heads_first else h * d, N * d if heads_first else d)
+            ys.append(tuple(s if size > 1 else 0 for s, size in zip(st, (B, N, h))))
+        else:
+            _need(y[i], names[i], dt, shape)
+            ys.append(_strides(y[i], names[i], _BHN if heads_first else _BNH))
+        if dx and dx[i] is not None:
+            _need(dx[i], "dq" if i == 0 else "dk", dt, (B, N, h, d))
+            ds.append(_strides(dx[i], "dq" if i == 0 else "dk", _BNH))
+        else:
+            ds.append(tuple(s if size > 1 else 0 for s, size in zip((N * h * d, h * d, d), (B, N, h))))
+    p = FaQkParams(B, N, Hq, Hk, d, _CODES[dt], _CODES[wt], 2 * freqs.shape[0], int(bool(interleaved)), float(eps),
+                   pos_stride, _I64x3(*_strides(q, "q", _BNH)), _I64x3(*_strides(k, "k", _BNH)), _I64x3(*ys[0]),
+                   _I64x3(*ys[1]), _I64x3(*ds[0]), _I64x3(*ds[1]))
+    ref = ctypes.byref(p)
+    nbytes = int(load().fa_qk_norm_rope_bwd_workspace_size(ref)) if dx else 0
+    return ref, device, shapes, nbytes
 
 
 def qk_norm_rope(q, k, wq, wk, freqs, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -212,21 +246,16 @@ def qk_norm_rope(q, k, wq, wk, freqs, positions=None, eps: float = 1e-6, interle
     the rotation of the first 2 * len(freqs) channels by the positions (int32 [N] or
     [B, N]; None: 0 .. N - 1).  Results are [B, H, N, d] as ``attention_fwd`` takes them,
     or, with ``heads_first`` false, [B, N, H, d]; ``out`` (yq, yk) may be (q, k) there."""
-    B, N, Hq, Hk, d, dt, wt, rot, ps = _qk_shapes(q, k, wq, wk, freqs, positions)
-    handle, alloc = _enter(stream, q, k, wq, wk, freqs, positions)
-    shape = (lambda h: (B, h, N, d)) if heads_first else (lambda h: (B, N, h, d))
+    yq, yk = (None, None) if out is None else out
+    key = ("qk", _sig(q), _sig(k), _sig(wq), _sig(wk), _sig(freqs), _sig(positions), _sig(yq), _sig(yk), eps,
+           interleaved, heads_first)
+    ref, device, shapes, _ = _seen.get(key) or _remember(
+        key, _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, (yq, yk), ()))
+    handle, alloc = _enter(device, stream, q, k, wq, wk, freqs, positions, yq, yk)
     if out is None:
         with alloc:
-            yq, yk = q.new_empty(shape(Hq)), q.new_empty(shape(Hk))
-    else:
-        yq, yk = out
-        _need(yq, "out[0]", q.dtype, shape(Hq))
-        _need(yk, "out[1]", q.dtype, shape(Hk))
-        _same_device(yq, yk)
-    dims = _BHN if heads_first else _BNH
-    _, ref = _qk_params(B, N, Hq, Hk, d, dt, wt, rot, int(bool(interleaved)), float(eps), ps, _strides(q, "q", _BNH),
-                        _strides(k, "k", _BNH), _strides(yq, "out[0]", dims), _strides(yk, "out[1]", dims),
-                        (0, 0, 0), (0, 0, 0))
+            yq = torch.empty(shapes[0], dtype=q.dtype, device=device)
+            yk = torch.empty(shapes[1], dtype=q.dtype, device=device)
     _check(load().fa_qk_norm_rope(ref, q.data_ptr(), k.data_ptr(), wq.data_ptr(), wk.data_ptr(), freqs.data_ptr(),
                                   _ptr(positions), yq.data_ptr(), yk.data_ptr(), handle), "fa_qk_norm_rope")
     return yq, yk
@@ -237,34 +266,33 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float =
     """(dq, dk, dwq, dwk): gradients of ``qk_norm_rope`` for dyq, dyk at its results (in its
     layout); q and k are its inputs.  dq, dk are [B, N, H, d] in q's dtype (views of a
     packed gradient may be given), dwq, dwk fp32 [d]."""
-    B, N, Hq, Hk, d, dt, wt, rot, ps = _qk_shapes(q, k, wq, wk, freqs, positions)
-    shape = (lambda h: (B, h, N, d)) if heads_first else (lambda h: (B, N, h, d))
-    _need(dyq, "dyq", q.dtype, shape(Hq))
-    _need(dyk, "dyk", q.dtype, shape(Hk))
-    _same_device(dyq, dyk, dq, dk, workspace)
-    handle, alloc = _enter(stream, q, k, dyq, dyk, wq, wk, freqs, positions, workspace)
-    lib = load()
+    key = ("qk_bwd", _sig(q), _sig(k), _sig(dyq), _sig(dyk), _sig(wq), _sig(wk), _sig(freqs), _sig(positions),
+           _sig(dq), _sig(dk), _sig(workspace), eps, interleaved, heads_first)
+    plan = _seen.get(key)
+    if plan is None:
+        if workspace is not None:
+            _need(workspace, "workspace", workspace.dtype)
+            _contiguous(workspace, "workspace")
+            _one_device(q, workspace)
+        plan = _remember(key, _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, (dyq, dyk), (dq, dk)))
+    ref, device, _, nbytes = plan
+    handle, alloc = _enter(device, stream, q, k, dyq, dyk, wq, wk, freqs, positions, dq, dk, workspace)
+    d = q.shape[3]
     with alloc:
         if dq is None:
-            dq = q.new_empty((B, N, Hq, d))
-        else:
-            _need(dq, "dq", q.dtype, (B, N, Hq, d))
+            dq = torch.empty(q.shape, dtype=q.dtype, device=device)
         if dk is None:
-            dk = q.new_empty((B, N, Hk, d))
-        else:
-            _need(dk, "dk", q.dtype, (B, N, Hk, d))
-        dims = _BHN if heads_first else _BNH
-        _, ref = _qk_params(B, N, Hq, Hk, d, dt, wt, rot, int(bool(interleaved)), float(eps), ps,
-                            _strides(q, "q", _BNH), _strides(k, "k", _BNH), _strides(dyq, "dyq", dims),
-                            _strides(dyk, "dyk", dims), _strides(dq, "dq", _BNH), _strides(dk, "dk", _BNH))
-        dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
+            dk = torch.empty(k.shape, dtype=q.dtype, device=device)
+        dw = torch.empty((2, d), dtype=torch.float32, device=device)
         if workspace is None:
-            workspace = torch.empty(lib.fa_qk_norm_rope_bwd_workspace_size(ref), dtype=torch.uint8, device=q.device)
-    _check(lib.fa_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(), dyq.data_ptr(), dyk.data_ptr(), wq.data_ptr(),
-                                   wk.data_ptr(), freqs.data_ptr(), _ptr(positions), dq.data_ptr(), dk.data_ptr(),
-                                   dw.data_ptr(), dw.data_ptr() + 4 * d, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), handle), "fa_qk_norm_rope_bwd")
-    return dq, dk, dw[0], dw[1]
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    at = dw.data_ptr()
+    _check(load().fa_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(), dyq.data_ptr(), dyk.data_ptr(), wq.data_ptr(),
+                                      wk.data_ptr(), freqs.data_ptr(), _ptr(positions), dq.data_ptr(), dk.data_ptr(),
+                                      at, at + 4 * d, workspace.data_ptr(), workspace.nbytes, handle),
+           "fa_qk_norm_rope_bwd")
+    dwq, dwk = dw.unbind()
+    return dq, dk, dwq, dwk
 
 
 # ---------------------------------------------------------------- the 4-bit cache
@@ -283,45 +311,48 @@ def kv4_cache(num_pages: int, heads: int, d: int, page_size: int = 64, device="c
     return torch.zeros((num_pages, heads, page_size // KV4_BLOCK, kv4_block_bytes(d)), dtype=torch.uint8, device=device)
 
 
-@functools.lru_cache(maxsize=256)
-def _cache_params(pages, heads, blocks, nbytes, d, page_stride):
-    p = FaKv4Cache(pages, KV4_BLOCK * blocks, heads, d, page_stride)
-    return p, ctypes.byref(p)
-
-
-def _cache_key(cache, d: int) -> tuple:
-    """The sizes of a cache, as _cache_params takes them."""
+def _cache_params(cache, d: int) -> FaKv4Cache:
     _need(cache, "cache", torch.uint8, (None, None, None, {64: 1280, 128: 2560}.get(d, -1)))
     P, H, n, b = cache.shape
     s = cache.stride()
-    if s[3] != 1 or s[2] != b or (H > 1 and s[1] != n * b):
+    if s[3] != 1 or (n > 1 and s[2] != b) or (H > 1 and s[1] != n * b):
         raise ValueError("cache must be contiguous within a page")
-    return P, H, n, b, d, s[0] if P > 1 else H * n * b
+    return FaKv4Cache(P, KV4_BLOCK * n, H, d, s[0] if P > 1 else H * n * b)
 
 
-@functools.lru_cache(maxsize=256)
-def _rows_params(T, dtype, k, v):
-    p = FaKv4Rows(T, dtype, _I64x2(*k), _I64x2(*v))
-    return p, ctypes.byref(p)
+def _plan_rows(cache, slots, k, v, T, H, d, dtype, dims, names):
+    """(cache parameters, row parameters, device)."""
+    c = _cache_params(cache, d)
+    if cache.shape[1] != H:
+        raise ValueError(f"{names[0]} has {H} heads, the cache {cache.shape[1]}")
+    _need(slots, "slots", torch.int32, (T,))
+    _contiguous(slots, "slots")
+    strides = []
+    for x, name in zip((k, v), names):
+        if x is None:  # new and contiguous
+            strides.append(tuple(st if size > 1 else 0 for st, size in zip((H * d, d) if dims == (0, 1) else (d, T * d), (T, H))))
+        else:
+            _need(x, name, dtype, (T, H, d) if dims == (0, 1) else (H, T, d))
+            strides.append(_strides(x, name, dims))
+    device = _one_device(cache, slots, k, v)
+    rows = FaKv4Rows(T, _CODES[dtype], _I64x2(*strides[0]), _I64x2(*strides[1]))
+    return ctypes.byref(c), ctypes.byref(rows), device
 
 
 def kv4_append(k, v, slots, cache, stream=None) -> None:
     """Quantise the keys and values [T, Hk, d] of T tokens into their slots (int32 [T];
     negative: left out; distinct otherwise) of the cache.  Values saturate at +-16384."""
-    if k.dtype not in _CODES:
-        raise TypeError(f"unsupported dtype {k.dtype}")
-    T, H, d = k.shape
-    _need(k, "k", k.dtype, (T, H, d))
-    _need(v, "v", k.dtype, (T, H, d))
-    _need(slots, "slots", torch.int32, (T,))
-    _contiguous(slots, "slots")
-    key = _cache_key(cache, d)
-    if cache.shape[1] != H:
-        raise ValueError(f"k has {H} heads, the cache {cache.shape[1]}")
-    _same_device(k, v, slots, cache)
-    handle, _ = _enter(stream, k, v, slots, cache)
-    _, rows = _rows_params(T, _CODES[k.dtype], _strides(k, "k", (0, 1)), _strides(v, "v", (0, 1)))
-    _check(load().fa_kv4_append(_cache_params(*key)[1], rows, k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr(), handle),
+    key = ("append", _sig(k), _sig(v), _sig(slots), _sig(cache))
+    plan = _seen.get(key)
+    if plan is None:
+        if k.dtype not in _CODES:
+            raise TypeError(f"unsupported dtype {k.dtype}")
+        _need(k, "k", k.dtype, (None, None, None))
+        T, H, d = k.shape
+        plan = _remember(key, _plan_rows(cache, slots, k, v, T, H, d, k.dtype, (0, 1), ("k", "v")))
+    c, rows, device = plan
+    handle, _ = _enter(device, stream, k, v, slots, cache)
+    _check(load().fa_kv4_append(c, rows, k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr(), handle),
            "fa_kv4_append")
 
 
@@ -329,52 +360,34 @@ def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = F
     """(k, v): the cached keys and values of T slots (zeros for a negative one), rounded to
     ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d] (with a leading batch of one,
     as ``attention_fwd`` takes them)."""
-    if dtype not in _CODES:
-        raise TypeError(f"unsupported dtype {dtype}")
-    _need(slots, "slots", torch.int32, (None,))
-    _contiguous(slots, "slots")
-    key = _cache_key(cache, d)
-    T, H = slots.shape[0], cache.shape[1]
-    _same_device(slots, cache)
-    handle, alloc = _enter(stream, slots, cache)
-    shape = (H, T, d) if heads_first else (T, H, d)
+    k, v = (None, None) if out is None else out
+    key = ("gather", _sig(cache), _sig(slots), d, dtype, heads_first, _sig(k), _sig(v))
+    plan = _seen.get(key)
+    if plan is None:
+        if dtype not in _CODES:
+            raise TypeError(f"unsupported dtype {dtype}")
+        _need(cache, "cache", torch.uint8, (None, None, None, None))
+        _need(slots, "slots", torch.int32, (None,))
+        plan = _remember(key, _plan_rows(cache, slots, k, v, slots.shape[0], cache.shape[1], d, dtype,
+                                         (1, 0) if heads_first else (0, 1), ("out[0]", "out[1]")))
+    c, rows, device = plan
+    handle, alloc = _enter(device, stream, slots, cache, k, v)
     if out is None:
+        T, H = slots.shape[0], cache.shape[1]
         with alloc:
-            kv = torch.empty((2,) + shape, dtype=dtype, device=cache.device)
-        k, v = kv[0], kv[1]
-    else:
-        k, v = out
-        _need(k, "out[0]", dtype, shape)
-        _need(v, "out[1]", dtype, shape)
-        _same_device(k, v)
-    dims = (1, 0) if heads_first else (0, 1)
-    _, rows = _rows_params(T, _CODES[dtype], _strides(k, "out[0]", dims), _strides(v, "out[1]", dims))
-    _check(load().fa_kv4_gather(_cache_params(*key)[1], rows, cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), handle),
+            k, v = torch.empty((2, H, T, d) if heads_first else (2, T, H, d), dtype=dtype, device=device).unbind()
+    _check(load().fa_kv4_gather(c, rows, cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), handle),
            "fa_kv4_gather")
     return k, v
 
 
-@functools.lru_cache(maxsize=1024)
-def _attn_params(key, R, T, Hq, dtype, max_q_len, window, width, scale, table_stride, q, o):
-    p = FaKv4AttnParams(R, T, Hq, dtype, max_q_len, window, width, scale, table_stride, _I64x2(*q), _I64x2(*o))
-    ref, cref = ctypes.byref(p), _cache_params(*key)[1]
-    return cref, ref, int(load().fa_kv4_attention_workspace_size(cref, ref)), p
-
-
-def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1, scale: Optional[float] = None,
-                  window: int = 0, out=None, lse=None, workspace=None, stream=None):
-    """(o, lse): attention of each request's newest tokens, q [T, Hq, d], over its cached
-    tokens.  Request r has kv_lens[r] tokens (these queries' own among them) in the pages
-    block_table[r]; its queries are rows cu_q[r] : cu_q[r + 1] (None: row r), the last of
-    them at its last token; each sees the tokens up to its own, and with ``window`` > 0
-    only the last ``window`` of those.  Rows without a token to see: o = 0, lse = -inf;
-    rows outside every request are not written.  ``max_q_len``: the most rows of a request,
-    a hint.  Lengths stay on the GPU: the call does not synchronise."""
+def _plan_attention(q, cache, block_table, kv_lens, cu_q, max_q_len, scale, window, out, lse, workspace):
+    """(cache parameters, parameters, workspace bytes, device)."""
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be fp16 or bf16, not {q.dtype}")
+    _need(q, "q", q.dtype, (None, None, None))
     T, Hq, d = q.shape
-    _need(q, "q", q.dtype)
-    key = _cache_key(cache, d)
+    c = _cache_params(cache, d)
     _need(block_table, "block_table", torch.int32, (None, None))
     R, width = block_table.shape
     if width > 1 and block_table.stride(1) != 1:
@@ -386,40 +399,77 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1,
         _contiguous(cu_q, "cu_q")
     elif T < R:
         raise ValueError(f"q has {T} rows for {R} requests")
-    _same_device(q, cache, block_table, kv_lens, cu_q, out, lse, workspace)
-    handle, alloc = _enter(stream, q, cache, block_table, kv_lens, cu_q, workspace)
+    o_stride = tuple(st if size > 1 else 0 for st, size in zip((Hq * d, d), (T, Hq)))
+    if out is not None:
+        _need(out, "out", q.dtype, (T, Hq, d))
+        o_stride = _strides(out, "out", (0, 1))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, Hq))
+        _contiguous(lse, "lse")
+    if workspace is not None:
+        _need(workspace, "workspace", workspace.dtype)
+        _contiguous(workspace, "workspace")
+    device = _one_device(q, cache, block_table, kv_lens, cu_q, out, lse, workspace)
+    p = FaKv4AttnParams(R, T, Hq, _CODES[q.dtype], int(max_q_len), int(window), width,
+                        1.0 / math.sqrt(d) if scale is None else float(scale),
+                        block_table.stride(0) if R > 1 else width, _I64x2(*_strides(q, "q", (0, 1))), _I64x2(*o_stride))
+    cref, ref = ctypes.byref(c), ctypes.byref(p)
+    return cref, ref, int(load().fa_kv4_attention_workspace_size(cref, ref)), device
+
+
+def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1, scale: Optional[float] = None,
+                  window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """(o, lse): attention of each request's newest tokens, q [T, Hq, d], over its cached
+    tokens.  Request r has kv_lens[r] tokens (these queries' own among them) in the pages
+    block_table[r]; its queries are rows cu_q[r] : cu_q[r + 1] (None: row r), the last of
+    them at its last token; each sees the tokens up to its own, and with ``window`` > 0
+    only the last ``window`` of those.  Rows without a token to see: o = 0, lse = -inf;
+    rows outside every request are not written.  ``max_q_len``: the most rows of a request,
+    a hint.  Lengths stay on the GPU: the call does not synchronise."""
+    key = ("attention", _sig(q), _sig(cache), _sig(block_table), _sig(kv_lens), _sig(cu_q), max_q_len, scale, window,
+           _sig(out), _sig(lse), _sig(workspace))
+    c, p, nbytes, device = _seen.get(key) or _remember(
+        key, _plan_attention(q, cache, block_table, kv_lens, cu_q, max_q_len, scale, window, out, lse, workspace))
+    handle, alloc = _enter(device, stream, q, cache, block_table, kv_lens, cu_q, out, lse, workspace)
     with alloc:
         if out is None:
-            out = q.new_empty((T, Hq, d))
-        else:
-            _need(out, "out", q.dtype, (T, Hq, d))
+            out = torch.empty(q.shape, dtype=q.dtype, device=device)
         if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-        else:
-            _need(lse, "lse", torch.float32, (T, Hq))
-            _contiguous(lse, "lse")
-        ref, par, nbytes, _ = _attn_params(key, R, T, Hq, _CODES[q.dtype], int(max_q_len), int(window), width,
-                                      1.0 / math.sqrt(d) if scale is None else float(scale),
-                                      block_table.stride(0) if R > 1 else width, _strides(q, "q", (0, 1)),
-                                      _strides(out, "out", (0, 1)))
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device)
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _check(load().fa_kv4_attention(ref, par, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
-                                   kv_lens.data_ptr(), _ptr(cu_q), out.data_ptr(), lse.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle),
-           "fa_kv4_attention")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _check(load().fa_kv4_attention(c, p, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+                                   _ptr(cu_q), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                   handle), "fa_kv4_attention")
     return out, lse
 
 
 # ---------------------------------------------------------------- block tables and slot maps
 
-@functools.lru_cache(maxsize=256)
-def _plan_params(R, T, page, pages, width, stride):
-    p = FaPlanParams(R, T, page, pages, width, stride)
-    return p, ctypes.byref(p)
-
-
 _PLAN_OUT = ("kv_lens", "cu_q", "positions", "slots", "counts")
+
+
+def _plan_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size, T, out):
+    """(parameters, sizes of the results, device)."""
+    i32 = torch.int32
+    _need(block_table, "block_table", i32, (None, None))
+    R, width = block_table.shape
+    if width > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table must be contiguous in its last dimension")
+    for t, name, n in ((seq_lens, "seq_lens", R), (new_lens, "new_lens", R), (free_pages, "free_pages", None),
+                       (free_count, "free_count", None)):
+        _need(t, name, i32, (n,))
+        _contiguous(t, name)
+    if free_count.shape[0] < 1:
+        raise ValueError("free_count is empty")
+    sizes = [R, R + 1, int(T), int(T), 3]
+    if out is not None:
+        for name, n in zip(_PLAN_OUT, sizes):
+            _need(out[name], f"out[{name!r}]", i32, (n,))
+            _contiguous(out[name], f"out[{name!r}]")
+    device = _one_device(seq_lens, new_lens, block_table, free_pages, free_count, *(out[n] for n in _PLAN_OUT if out))
+    p = FaPlanParams(R, int(T), int(page_size), free_pages.shape[0], width, block_table.stride(0) if R > 1 else width)
+    return ctypes.byref(p), sizes, device
 
 
 def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size: int, T: int, out=None, stream=None):
@@ -431,36 +481,18 @@ def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_siz
     tokens, pages missing).  A request whose pages are not there keeps its length and gets
     slots of -1.  out["kv_lens"] may be seq_lens, and out["counts"] the tensor whose first
     element is free_count."""
-    R, width = block_table.shape
-    _need(block_table, "block_table", torch.int32, (None, None))
-    if width > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table must be contiguous in its last dimension")
-    i32 = torch.int32
-    for t, name, n in ((seq_lens, "seq_lens", R), (new_lens, "new_lens", R), (free_pages, "free_pages", None)):
-        _need(t, name, i32, (n,))
-        _contiguous(t, name)
-    _need(free_count, "free_count", i32, (None,))
-    if free_count.shape[0] < 1:
-        raise ValueError("free_count is empty")
-    sizes = (R, R + 1, T, T, 3)
-    _same_device(seq_lens, new_lens, block_table, free_pages, free_count)
-    handle, alloc = _enter(stream, seq_lens, new_lens, block_table, free_pages, free_count)
+    given = () if out is None else tuple(out[name] for name in _PLAN_OUT)
+    key = ("plan", _sig(seq_lens), _sig(new_lens), _sig(block_table), _sig(free_pages), _sig(free_count), page_size, T,
+           *map(_sig, given))
+    p, sizes, device = _seen.get(key) or _remember(
+        key, _plan_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size, T, out))
+    handle, alloc = _enter(device, stream, seq_lens, new_lens, block_table, free_pages, free_count, *given)
     if out is None:
-        with alloc:  # one allocation, each part 16-byte aligned
-            ends, at = [], 0
-            for n in sizes:
-                ends.append(at)
-                at += (n + 3) // 4 * 4
-            flat = torch.empty(at, dtype=i32, device=seq_lens.device)
-        out = {name: flat[a:a + n] for name, a, n in zip(_PLAN_OUT, ends, sizes)}
-    else:
-        for name, n in zip(_PLAN_OUT, sizes):
-            _need(out[name], f"out[{name!r}]", i32, (n,))
-            _contiguous(out[name], f"out[{name!r}]")
-        _same_device(*(out[name] for name in _PLAN_OUT))
-    _, ref = _plan_params(R, int(T), int(page_size), free_pages.shape[0], width, block_table.stride(0) if R > 1 else width)
-    _check(load().fa_paged_plan(ref, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                                free_pages.data_ptr(), free_count.data_ptr(), out["kv_lens"].data_ptr(),
-                                out["cu_q"].data_ptr(), out["positions"].data_ptr(), out["slots"].data_ptr(),
-                                out["counts"].data_ptr(), handle), "fa_paged_plan")
+        with alloc:
+            given = torch.empty(sum(sizes), dtype=torch.int32, device=device).split(sizes)
+        out = dict(zip(_PLAN_OUT, given))
+    kv, cu, pos, slots, counts = given
+    _check(load().fa_paged_plan(p, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                                free_pages.data_ptr(), free_count.data_ptr(), kv.data_ptr(), cu.data_ptr(),
+                                pos.data_ptr(), slots.data_ptr(), counts.data_ptr(), handle), "fa_paged_plan")
     return out
