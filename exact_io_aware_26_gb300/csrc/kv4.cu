@@ -33,6 +33,7 @@ __device__ __forceinline__ void load8(const void* base, long long at, float (&v)
 // Byte address of a slot's block, and its row there; nullptr for a slot that is left
 // out (negative) or outside the cache (recorded).
 __device__ __forceinline__ uint8_t* slot_block(const Kv4RowArgs& a, int slot, int head, int block_bytes, int& row) {
+  row = 0;
   if (slot < 0) return nullptr;
   const int page = slot >> a.c.page_log, in = slot & ((1 << a.c.page_log) - 1);
   if (page >= a.c.num_pages) {
@@ -44,59 +45,92 @@ __device__ __forceinline__ uint8_t* slot_block(const Kv4RowArgs& a, int slot, in
          (((long long)head << (a.c.page_log - 4)) + in / kKvBlock) * block_bytes;
 }
 
+// Codes of a lane's eight values and the pair of its group of four lanes.
+__device__ __forceinline__ void quantise8(float (&v)[8], uint32_t& word, uint32_t& pair) {
+  float lo = kKvSaturate, hi = -kKvSaturate;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    nan |= v[i] != v[i];
+    v[i] = fminf(fmaxf(v[i], -kKvSaturate), kKvSaturate);
+    lo = fminf(lo, v[i]);
+    hi = fmaxf(hi, v[i]);
+  }
+#pragma unroll
+  for (int off = 1; off < 4; off <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    nan |= __shfl_xor_sync(0xffffffffu, (int)nan, off) != 0;
+  }
+  // the documented steps, each rounded once: plain fp32, no contraction
+  const __half s = __float2half_rn(__fdiv_rn(__fmul_rn(__fsub_rn(hi, lo), 16.f), 15.f));
+  const __half c = __float2half_rn(__fsub_rn(lo, __half2float(s)));
+  const float sf = __half2float(s), cf = __half2float(c);
+  word = 0;
+  if (sf > 0.f && !nan) {
+    // The quotient only decides between neighbouring codes: a product with the rounded
+    // reciprocal is off by less than 2^-22 of it, at most 31 + a clamped rest, so that
+    // its rounding is the quotient's unless it lies within 2^-16 of a half, where the
+    // division itself is done (a fifth of the time of eight divisions).
+    const float inv = 1.f / sf;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = __fmul_rn(__fsub_rn(v[i], cf), 16.f);
+      float t = fminf(__fmul_rn(d, inv), 64.f) - 16.f;
+      if (fabsf(fabsf(t - rintf(t)) - 0.5f) < 0x1p-16f) t = __fsub_rn(__fdiv_rn(d, sf), 16.f);
+      word |= (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f) << (4 * i);
+    }
+  }
+  pair = nan ? 0x7E007E00u : (uint32_t)__half_as_ushort(s) | ((uint32_t)__half_as_ushort(c) << 16);
+}
+
+// A row is one head of one token: D / 8 lanes, which take its key and its value.
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowArgs a) {
   using Blk = KvBlock<D>;
-  constexpr int LPR = D / 8;  // lanes per row
-  const int j = threadIdx.x % LPR;
-  const long long rows = (long long)a.T * a.c.Hk * 2;
-  const long long step = (long long)gridDim.x * (kThreads / LPR);
-  for (long long r0 = (long long)blockIdx.x * (kThreads / LPR); r0 < rows; r0 += step) {
-    const long long r = r0 + threadIdx.x / LPR;
-    const bool live = r < rows;
-    const int side = (int)(r & 1);
-    const long long th = r >> 1;
-    const int tok = (int)(th / a.c.Hk), head = (int)(th % a.c.Hk);
-    int row = 0;
-    uint8_t* blk = live ? slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row) : nullptr;
-    float v[8] = {};
-    if (blk) load8<DT>(side ? a.x[1] : a.x[0], tok * (side ? a.xs[1][0] : a.xs[0][0]) + head * (side ? a.xs[1][1] : a.xs[0][1]) + 8 * j, v);
-    float lo = kKvSaturate, hi = -kKvSaturate;
-    bool nan = false;
+  constexpr int LPR = D / 8;
+  const int j = threadIdx.x % LPR, r = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+  const bool live = r < a.rows;
+  const int tok = a.heads.div(r), head = r - tok * (int)a.heads.d;
+  float k[8] = {}, v[8] = {};
+  int row = 0;
+  uint8_t* blk = nullptr;
+  if (live) {
+    load8<DT>(a.x[0], tok * a.xs[0][0] + head * a.xs[0][1] + 8 * j, k);
+    load8<DT>(a.x[1], tok * a.xs[1][0] + head * a.xs[1][1] + 8 * j, v);
+    blk = slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row);
+  }
+  uint32_t wk, pk, wv, pv;
+  quantise8(k, wk, pk);
+  quantise8(v, wv, pv);
+  if (!blk) return;
+  uint8_t* at = blk + row * Blk::row + 4 * j;
+  *reinterpret_cast<uint32_t*>(at) = wk;
+  *reinterpret_cast<uint32_t*>(at + Blk::half) = wv;
+  if ((j & 3) == 0) {
+    at = blk + Blk::codes + (row * Blk::groups + (j >> 2)) * 4;
+    *reinterpret_cast<uint32_t*>(at) = pk;
+    *reinterpret_cast<uint32_t*>(at + Blk::half) = pv;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_values(void* x, long long to, uint32_t word, uint32_t pair) {
+  const __half2 p = *reinterpret_cast<const __half2*>(&pair);
+  float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      nan |= v[i] != v[i];
-      v[i] = fminf(fmaxf(v[i], -kKvSaturate), kKvSaturate);
-      lo = fminf(lo, v[i]);
-      hi = fmaxf(hi, v[i]);
-    }
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-      nan |= __shfl_xor_sync(0xffffffffu, (int)nan, off) != 0;
-    }
-    // the documented steps, each rounded once: plain fp32, no contraction
-    const __half s = __float2half_rn(__fdiv_rn(__fmul_rn(__fsub_rn(hi, lo), 16.f), 15.f));
-    const __half c = __float2half_rn(__fsub_rn(lo, __half2float(s)));
-    const float sf = __half2float(s), cf = __half2float(c);
-    uint32_t word = 0;
-    if (sf > 0.f && !nan) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = __fsub_rn(__fdiv_rn(__fmul_rn(__fsub_rn(v[i], cf), 16.f), sf), 16.f);
-        word |= (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f) << (4 * i);
-      }
-    }
-    if (blk) {
-      uint8_t* at = blk + side * Blk::half;
-      *reinterpret_cast<uint32_t*>(at + row * Blk::row + 4 * j) = word;
-      if ((j & 3) == 0) {
-        const uint32_t pair = nan ? 0x7E007E00u
-                                  : (uint32_t)__half_as_ushort(s) | ((uint32_t)__half_as_ushort(c) << 16);
-        *reinterpret_cast<uint32_t*>(at + Blk::codes + (row * Blk::groups + (j >> 2)) * 4) = pair;
-      }
-    }
+  for (int i = 0; i < 8; ++i) {
+    const __half m = __ushort_as_half((unsigned short)(0x3C00u | (((word >> (4 * i)) & 15u) << 6)));
+    v[i] = __half2float(__hfma(m, __low2half(p), __high2half(p)));
+  }
+  if constexpr (DT == FA_F32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + to);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    constexpr bool F16 = DT == FA_F16;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + to) =
+        make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
   }
 }
 
@@ -104,46 +138,27 @@ template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4RowArgs a) {
   using Blk = KvBlock<D>;
   constexpr int LPR = D / 8;
-  const int j = threadIdx.x % LPR;
-  const long long rows = (long long)a.T * a.c.Hk * 2;
-  const long long step = (long long)gridDim.x * (kThreads / LPR);
-  for (long long r = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; r < rows; r += step) {
-    const int side = (int)(r & 1);
-    const long long th = r >> 1;
-    const int tok = (int)(th / a.c.Hk), head = (int)(th % a.c.Hk);
-    int row = 0;
-    const uint8_t* blk = slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row);
-    float v[8] = {};
-    if (blk) {
-      const uint8_t* at = blk + side * Blk::half;
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(at + row * Blk::row + 4 * j);
-      const uint32_t pair = *reinterpret_cast<const uint32_t*>(at + Blk::codes + (row * Blk::groups + (j >> 2)) * 4);
-      const __half s = __ushort_as_half((unsigned short)(pair & 0xFFFFu));
-      const __half c = __ushort_as_half((unsigned short)(pair >> 16));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __half m = __ushort_as_half((unsigned short)(0x3C00u | (((word >> (4 * i)) & 15u) << 6)));
-        v[i] = __half2float(__hfma(m, s, c));
-      }
-    }
-    const long long to = tok * (side ? a.xs[1][0] : a.xs[0][0]) + head * (side ? a.xs[1][1] : a.xs[0][1]) + 8 * j;
-    if constexpr (DT == FA_F32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(side ? a.x[1] : a.x[0]) + to);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      constexpr bool F16 = DT == FA_F16;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(side ? a.x[1] : a.x[0]) + to) =
-          make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
-    }
+  const int j = threadIdx.x % LPR, r = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+  if (r >= a.rows) return;
+  const int tok = a.heads.div(r), head = r - tok * (int)a.heads.d;
+  int row;
+  const uint8_t* blk = slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row);
+  uint32_t wk = 0, pk = 0, wv = 0, pv = 0;
+  if (blk) {
+    const uint8_t* at = blk + row * Blk::row + 4 * j;
+    wk = *reinterpret_cast<const uint32_t*>(at);
+    wv = *reinterpret_cast<const uint32_t*>(at + Blk::half);
+    at = blk + Blk::codes + (row * Blk::groups + (j >> 2)) * 4;
+    pk = *reinterpret_cast<const uint32_t*>(at);
+    pv = *reinterpret_cast<const uint32_t*>(at + Blk::half);
   }
+  store_values<DT>(a.x[0], tok * a.xs[0][0] + head * a.xs[0][1] + 8 * j, wk, pk);
+  store_values<DT>(a.x[1], tok * a.xs[1][0] + head * a.xs[1][1] + 8 * j, wv, pv);
 }
 
 template <int D, int DT>
 cudaError_t launch(const Kv4RowArgs& a, bool gather, cudaStream_t s) {
-  const long long per = kThreads / (D / 8);
-  const long long want = ((long long)a.T * a.c.Hk * 2 + per - 1) / per;
-  const int grid = (int)(want < (1 << 20) ? want : (1 << 20));
+  const int per = kThreads / (D / 8), grid = (a.rows + per - 1) / per;
   if (gather)
     kv4_gather_kernel<D, DT><<<grid, kThreads, 0, s>>>(a);
   else

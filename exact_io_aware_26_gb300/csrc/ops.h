@@ -5,6 +5,21 @@
 
 namespace fa {
 
+// Quotients by a fixed divisor of numbers below 2^31: a multiplication, an addition and a
+// shift (with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1).
+struct FastDiv {
+  uint32_t d, m, s;
+  static FastDiv of(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
+    return f;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+#endif
+};
+
 // Norm and rotation of query and key heads (qk_norm_rope.cu).
 struct QkArgs {
   int B, N, Hq, Hk;
@@ -20,8 +35,8 @@ struct QkArgs {
   long long pos_stride;
   int tok_tile;   // tokens of a tile (a power of two)
   int tiles;      // token tiles of a batch entry
-  int ctas;       // backward: CTAs of the launch
-  float* part;    // backward: [ctas][2][d] partial weight gradients
+  int ctas[2];    // CTAs of the launch for each tensor
+  float* part;    // backward: [CTA][d] partial weight gradients
   float* dw[2];
 };
 int qk_rows_per_pass(int d);
@@ -36,7 +51,8 @@ struct Kv4Cache {
 };
 struct Kv4RowArgs {
   Kv4Cache c;
-  int T;
+  int rows;       // tokens x heads
+  FastDiv heads;
   const int* slots;
   void* x[2];              // keys, values
   long long xs[2][2];      // element strides {token, head}
@@ -44,21 +60,6 @@ struct Kv4RowArgs {
 };
 cudaError_t launch_kv4_append(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
-
-// Quotients by a fixed divisor of numbers below 2^31: a multiplication, an addition and a
-// shift (with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1).
-struct FastDiv {
-  uint32_t d, m, s;
-  static FastDiv of(uint32_t d) {
-    FastDiv f{d, 0, 0};
-    while ((1ull << f.s) < d) ++f.s;
-    f.m = (uint32_t)(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
-    return f;
-  }
-#ifdef __CUDACC__
-  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
-#endif
-};
 
 struct Kv4AttnArgs {
   Kv4Cache c;

@@ -82,8 +82,8 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
     return fail(FA_ERR_INVALID, "rot_dim %d must be even, from 0 to d", p->rot_dim);
   if (!(std::isfinite(p->eps) && p->eps > 0.f)) return fail(FA_ERR_INVALID, "eps must be positive and finite");
   if (p->pos_stride < 0) return fail(FA_ERR_INVALID, "pos_stride is negative");
-  // a launch has a CTA per tile of at least one token
-  if ((long long)p->B * p->N >= (1ll << 31)) return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^31 - 1");
+  // a launch has a CTA for each tensor and tile of at least one token
+  if ((long long)p->B * p->N >= (1ll << 30)) return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^30 - 1");
   const long long sq[3] = {p->B, p->N, p->Hq}, sk[3] = {p->B, p->N, p->Hk};
   FA_TRY(check_strides(p->q_stride, sq, 3, p->d, p->dtype, false, "q"));
   FA_TRY(check_strides(p->k_stride, sk, 3, p->d, p->dtype, false, "k"));
@@ -96,12 +96,11 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
   return FA_OK;
 }
 
-constexpr int kQkBwdCtasPerSm = 2;
-constexpr int kQkBwdMaxCtas = 160 * kQkBwdCtasPerSm;
+constexpr int kQkMaxCtas = 2048;  // of a tensor, in the backward (each leaves a partial sum)
 
 // Tokens of a tile: as many as the row slots of a CTA (each lane then forms its angles
-// once for all heads), fewer -- the slots share a token's heads -- while the launch
-// would have under four CTAs per SM.
+// once for all heads), fewer -- the slots share a token's heads -- while there would be
+// fewer than four tiles for each SM.
 int qk_tok_tile(const fa_qk_params* p, int sms) {
   int tile = qk_rows_per_pass(p->d);
   while (tile > 1 && (long long)p->B * ((p->N + tile - 1) / tile) < 4LL * sms) tile /= 2;
@@ -109,7 +108,7 @@ int qk_tok_tile(const fa_qk_params* p, int sms) {
 }
 
 QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* wq, const void* wk,
-               const uint64_t* freqs, const int* positions, int sms) {
+               const uint64_t* freqs, const int* positions, int sms, bool bwd) {
   QkArgs a;
   std::memset(&a, 0, sizeof(a));
   a.B = p->B;
@@ -130,6 +129,12 @@ QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* 
   std::memcpy(a.xs[1], p->k_stride, sizeof(a.xs[1]));
   a.tok_tile = qk_tok_tile(p, sms);
   a.tiles = (p->N + a.tok_tile - 1) / a.tok_tile;
+  const long long tiles = (long long)a.B * a.tiles;
+  a.ctas[0] = a.ctas[1] = (int)tiles;
+  if (bwd && tiles > kQkMaxCtas) {  // the same number of tiles for each
+    const long long each = (tiles + kQkMaxCtas - 1) / kQkMaxCtas;
+    a.ctas[0] = a.ctas[1] = (int)((tiles + each - 1) / each);
+  }
   return a;
 }
 
@@ -176,6 +181,7 @@ fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
   FA_TRY(cache_check(c));
   if (!rows) return fail(FA_ERR_INVALID, "rows is NULL");
   if (rows->T < 0) return fail(FA_ERR_INVALID, "T is negative");
+  if ((long long)rows->T * c->Hk >= (1ll << 30)) return fail(FA_ERR_UNSUPPORTED, "T*Hk exceeds 2^30 - 1");
   if (rows->dtype != FA_F32 && rows->dtype != FA_F16 && rows->dtype != FA_BF16)
     return fail(FA_ERR_INVALID, "dtype %d is not an fa_dtype", rows->dtype);
   const long long size[2] = {rows->T, c->Hk};
@@ -193,7 +199,8 @@ fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
   Kv4RowArgs a;
   std::memset(&a, 0, sizeof(a));
   a.c = cache_args(c, cache);
-  a.T = rows->T;
+  a.rows = rows->T * c->Hk;
+  a.heads = FastDiv::of((uint32_t)c->Hk);
   a.slots = slots;
   a.x[0] = const_cast<void*>(k);
   a.x[1] = const_cast<void*>(v);
@@ -249,7 +256,7 @@ fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, c
   int sms = 0;
   FA_TRY(api_device(&rep, &sms));
   if (p->N == 0) return FA_OK;
-  QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms);
+  QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms, false);
   a.y[0] = yq;
   a.y[1] = yk;
   std::memcpy(a.ys[0], p->yq_stride, sizeof(a.ys[0]));
@@ -262,7 +269,7 @@ fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, c
 
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_qk_params* p) {
   if (qk_check(p, true) != FA_OK) return 0;
-  return (size_t)kQkBwdMaxCtas * 2 * p->d * 4;
+  return (size_t)2 * kQkMaxCtas * p->d * 4;
 }
 
 fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* k, const void* dyq, const void* dyk,
@@ -286,7 +293,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* 
   Report rep;
   int sms = 0;
   FA_TRY(api_device(&rep, &sms));
-  QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms);
+  QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms, true);
   a.y[0] = dq;
   a.y[1] = dk;
   a.dy[0] = dyq;
@@ -295,7 +302,6 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* 
   std::memcpy(a.ys[1], p->dk_stride, sizeof(a.ys[1]));
   std::memcpy(a.ds[0], p->yq_stride, sizeof(a.ds[0]));
   std::memcpy(a.ds[1], p->yk_stride, sizeof(a.ds[1]));
-  a.ctas = (int)std::min<long long>((long long)a.B * a.tiles, std::min(kQkBwdMaxCtas, sms * kQkBwdCtasPerSm));
   a.part = static_cast<float*>(workspace);
   a.dw[0] = dwq;
   a.dw[1] = dwk;

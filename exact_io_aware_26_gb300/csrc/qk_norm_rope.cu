@@ -22,44 +22,37 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// eight consecutive elements <-> fp32
+// Eight consecutive elements, as loaded and as fp32.  (Plain loads: the result may be the
+// input itself.)
 template <int DT>
-__device__ __forceinline__ void load8(const void* base, long long at, float (&v)[8]) {
-  if constexpr (DT == FA_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+  uint4 u[DT == FA_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (DT == FA_F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<DT == FA_F16>(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
+    for (int i = 0; i < (DT == FA_F32 ? 2 : 1); ++i) u[i] = p[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (DT == FA_F32 ? 2 : 1); ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (DT == FA_F32) {
+      v[0] = __uint_as_float(u[0].x); v[1] = __uint_as_float(u[0].y);
+      v[2] = __uint_as_float(u[0].z); v[3] = __uint_as_float(u[0].w);
+      v[4] = __uint_as_float(u[1].x); v[5] = __uint_as_float(u[1].y);
+      v[6] = __uint_as_float(u[1].z); v[7] = __uint_as_float(u[1].w);
+    } else {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<DT == FA_F16>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
     }
   }
-}
-// as load8, but not through the read-only path: the result may be the input itself
-template <int DT>
-__device__ __forceinline__ void load8_rw(const void* base, long long at, float (&v)[8]) {
-  if constexpr (DT == FA_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<DT == FA_F16>(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
+};
 template <int DT>
 __device__ __forceinline__ void store8(void* base, long long at, const float (&v)[8]) {
   if constexpr (DT == FA_F32) {
@@ -75,10 +68,15 @@ __device__ __forceinline__ void store8(void* base, long long at, const float (&v
 }
 template <int DT>
 __device__ __forceinline__ void load_w8(const void* w, bool w_f32, int at, float (&v)[8]) {
-  if (w_f32)
-    load8<FA_F32>(w, at, v);
-  else
-    load8<DT>(w, at, v);
+  if (w_f32) {
+    Raw8<FA_F32> r;
+    r.load(w, at);
+    r.get(v);
+  } else {
+    Raw8<DT> r;
+    r.load(w, at);
+    r.get(v);
+  }
 }
 
 __device__ __forceinline__ void angle(const QkArgs& a, int pair, int pos, float& c, float& s) {
@@ -202,42 +200,62 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// One CTA per (batch entry, tile of tok_tile tokens); the kThreads / (D / 16) row
-// slots of the CTA hold tok_tile tokens, each by as many slots as are left, which
-// share its heads.
+// What a CTA does: its tensor (0: queries, 1: keys) and its place among that tensor's CTAs.
+struct Part {
+  int t, first, step;
+};
+__device__ __forceinline__ Part part_of(const QkArgs& a) {
+  const int b = blockIdx.x;
+  return b < a.ctas[0] ? Part{0, b, a.ctas[0]} : Part{1, b - a.ctas[0], a.ctas[1]};
+}
+
+// The kThreads / (D / 16) row slots of a CTA hold tok_tile tokens, each by as many slots as
+// are left, which share its heads; the CTA walks the tiles (batch entry, tok_tile tokens)
+// of its tensor.  The next row is loaded before this one is worked on.
 template <int D, int DT, bool ANY>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR;
   __shared__ float rows_s[ANY ? ROWS * D : 1];
+  const Part part = part_of(a);
+  const int t = part.t, H = t ? a.Hk : a.Hq;
   const int j = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-  const int tok = slot % a.tok_tile, share = slot / a.tok_tile, shares = ROWS / a.tok_tile;
-  const int b = blockIdx.x / a.tiles, n = (blockIdx.x % a.tiles) * a.tok_tile + tok;
-  const bool in = n < a.N;
-  const int pos = !in ? 0 : a.pos ? __ldg(a.pos + b * a.pos_stride + n) : n;
+  const int tok = slot & (a.tok_tile - 1), share = slot / a.tok_tile, shares = ROWS / a.tok_tile;
   Lane L;
   if constexpr (ANY) {
     L.lo = 8 * j;
     L.hi = D / 2 + 8 * j;
   } else {
     lane_channels<D>(a, j, L);
-    lane_angles(a, pos, L);
   }
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int H = t ? a.Hk : a.Hq;
-    float wl[8], wh[8];
-    load_w8<DT>(a.w[t], w_f32, L.lo, wl);
-    load_w8<DT>(a.w[t], w_f32, L.hi, wh);
-    const long long xb = b * a.xs[t][0] + (long long)n * a.xs[t][1];
-    const long long yb = b * a.ys[t][0] + (long long)n * a.ys[t][1];
+  const long long xh = t ? a.xs[1][2] : a.xs[0][2], yh = t ? a.ys[1][2] : a.ys[0][2];
+  const void* x = t ? a.x[1] : a.x[0];
+  void* y = t ? a.y[1] : a.y[0];
+  float wl[8], wh[8];
+  load_w8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, wl);
+  load_w8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, wh);
+  for (int tile = part.first; tile < a.B * a.tiles; tile += part.step) {
+    const int b = tile / a.tiles, n = (tile - b * a.tiles) * a.tok_tile + tok;
+    const bool in = n < a.N;
+    const long long xb = b * (t ? a.xs[1][0] : a.xs[0][0]) + (long long)n * (t ? a.xs[1][1] : a.xs[0][1]);
+    const long long yb = b * (t ? a.ys[1][0] : a.ys[0][0]) + (long long)n * (t ? a.ys[1][1] : a.ys[0][1]);
+    Raw8<DT> rl, rh;
+    rl.zero();
+    rh.zero();
+    if (in && share < H) {
+      rl.load(x, xb + share * xh + L.lo);
+      rh.load(x, xb + share * xh + L.hi);
+    }
+    const int pos = !in ? 0 : a.pos ? __ldg(a.pos + b * a.pos_stride + n) : n;
+    if constexpr (!ANY) lane_angles(a, pos, L);
     // every lane of a warp takes the same number of turns: the row sums are shuffles
     for (int h0 = 0; h0 < H; h0 += shares) {
       const int h = h0 + share;
-      const bool live = in && h < H;
-      float lo[8] = {}, hi[8] = {};
-      if (live) {
-        load8_rw<DT>(a.x[t], xb + h * a.xs[t][2] + L.lo, lo);
-        load8_rw<DT>(a.x[t], xb + h * a.xs[t][2] + L.hi, hi);
+      float lo[8], hi[8];
+      rl.get(lo);
+      rh.get(hi);
+      if (in && h + shares < H) {
+        rl.load(x, xb + (h + shares) * xh + L.lo);
+        rh.load(x, xb + (h + shares) * xh + L.hi);
       }
       float ss = 0.f;
 #pragma unroll
@@ -252,23 +270,25 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkArgs a, 
         rotate_any<D>(a, rows_s + slot * D, pos, 1.f, L, lo, hi);
       else
         rotate(a, L, 1.f, lo, hi);
-      if (live) {
-        store8<DT>(a.y[t], yb + h * a.ys[t][2] + L.lo, lo);
-        store8<DT>(a.y[t], yb + h * a.ys[t][2] + L.hi, hi);
+      if (in && h < H) {
+        store8<DT>(y, yb + h * yh + L.lo, lo);
+        store8<DT>(y, yb + h * yh + L.hi, hi);
       }
     }
   }
 }
 
-// The gradient: CTAs walk the token tiles (grid-stride) and add up the weights'
-// gradients of the channels their lanes hold; each CTA leaves one partial sum.
+// The gradient, in the same way; a lane adds up the weights' gradients of its channels, and
+// each CTA leaves one partial sum.
 template <int D, int DT, bool ANY>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const QkArgs a, const bool w_f32) {
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, WARPS = kThreads / 32;
   __shared__ float rows_s[ANY ? ROWS * D : 1];
   __shared__ float red[WARPS][D];
+  const Part part = part_of(a);
+  const int t = part.t, H = t ? a.Hk : a.Hq;
   const int j = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-  const int tok = slot % a.tok_tile, share = slot / a.tok_tile, shares = ROWS / a.tok_tile;
+  const int tok = slot & (a.tok_tile - 1), share = slot / a.tok_tile, shares = ROWS / a.tok_tile;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Lane L;
   if constexpr (ANY) {
@@ -277,101 +297,112 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const QkArgs
   } else {
     lane_channels<D>(a, j, L);
   }
-  float acc[2][16] = {};
-  for (int tile = blockIdx.x; tile < a.B * a.tiles; tile += gridDim.x) {
-    const int b = tile / a.tiles, n = (tile % a.tiles) * a.tok_tile + tok;
+  const long long xh = t ? a.xs[1][2] : a.xs[0][2], yh = t ? a.ys[1][2] : a.ys[0][2], dh = t ? a.ds[1][2] : a.ds[0][2];
+  const void *x = t ? a.x[1] : a.x[0], *dy = t ? a.dy[1] : a.dy[0];
+  void* y = t ? a.y[1] : a.y[0];
+  float wl[8], wh[8];
+  load_w8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, wl);
+  load_w8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, wh);
+  float acc[16] = {};
+  for (int tile = part.first; tile < a.B * a.tiles; tile += part.step) {
+    const int b = tile / a.tiles, n = (tile - b * a.tiles) * a.tok_tile + tok;
     const bool in = n < a.N;
+    const long long xb = b * (t ? a.xs[1][0] : a.xs[0][0]) + (long long)n * (t ? a.xs[1][1] : a.xs[0][1]);
+    const long long yb = b * (t ? a.ys[1][0] : a.ys[0][0]) + (long long)n * (t ? a.ys[1][1] : a.ys[0][1]);
+    const long long db = b * (t ? a.ds[1][0] : a.ds[0][0]) + (long long)n * (t ? a.ds[1][1] : a.ds[0][1]);
+    Raw8<DT> rl, rh, sl, sh;
+    rl.zero();
+    rh.zero();
+    sl.zero();
+    sh.zero();
+    if (in && share < H) {
+      rl.load(x, xb + share * xh + L.lo);
+      rh.load(x, xb + share * xh + L.hi);
+      sl.load(dy, db + share * dh + L.lo);
+      sh.load(dy, db + share * dh + L.hi);
+    }
     const int pos = !in ? 0 : a.pos ? __ldg(a.pos + b * a.pos_stride + n) : n;
     if constexpr (!ANY) lane_angles(a, pos, L);
+    for (int h0 = 0; h0 < H; h0 += shares) {
+      const int h = h0 + share;
+      const bool live = in && h < H;
+      float lo[8], hi[8], gl[8], gh[8];
+      rl.get(lo);
+      rh.get(hi);
+      sl.get(gl);
+      sh.get(gh);
+      if (in && h + shares < H) {
+        rl.load(x, xb + (h + shares) * xh + L.lo);
+        rh.load(x, xb + (h + shares) * xh + L.hi);
+        sl.load(dy, db + (h + shares) * dh + L.lo);
+        sh.load(dy, db + (h + shares) * dh + L.hi);
+      }
+      if constexpr (ANY)
+        rotate_any<D>(a, rows_s + slot * D, pos, -1.f, L, gl, gh);
+      else
+        rotate(a, L, -1.f, gl, gh);
+      float ss = 0.f, sd = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int H = t ? a.Hk : a.Hq;
-      float wl[8], wh[8];
-      load_w8<DT>(a.w[t], w_f32, L.lo, wl);
-      load_w8<DT>(a.w[t], w_f32, L.hi, wh);
-      const long long xb = b * a.xs[t][0] + (long long)n * a.xs[t][1];
-      const long long yb = b * a.ys[t][0] + (long long)n * a.ys[t][1];
-      const long long db = b * a.ds[t][0] + (long long)n * a.ds[t][1];
-      for (int h0 = 0; h0 < H; h0 += shares) {
-        const int h = h0 + share;
-        const bool live = in && h < H;
-        float lo[8] = {}, hi[8] = {}, gl[8] = {}, gh[8] = {};
-        if (live) {
-          load8_rw<DT>(a.x[t], xb + h * a.xs[t][2] + L.lo, lo);
-          load8_rw<DT>(a.x[t], xb + h * a.xs[t][2] + L.hi, hi);
-          load8_rw<DT>(a.dy[t], db + h * a.ds[t][2] + L.lo, gl);
-          load8_rw<DT>(a.dy[t], db + h * a.ds[t][2] + L.hi, gh);
-        }
-        if constexpr (ANY)
-          rotate_any<D>(a, rows_s + slot * D, pos, -1.f, L, gl, gh);
-        else
-          rotate(a, L, -1.f, gl, gh);
-        float ss = 0.f, sd = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
+        sd = fmaf(gl[i] * wl[i], lo[i], fmaf(gh[i] * wh[i], hi[i], sd));
+      }
+      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
+      const float m = row_sum<D>(sd) * (1.f / D) * r * r;  // mean(dn h) r: what x takes off dn
+      const float in_sum = live ? r : 0.f;                 // rows of other lanes' turns add nothing
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
-          sd = fmaf(gl[i] * wl[i], lo[i], fmaf(gh[i] * wh[i], hi[i], sd));
-        }
-        const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-        const float m = row_sum<D>(sd) * (1.f / D) * r * r;  // mean(dn h) / |x| units of x
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[t][i] = fmaf(gl[i], lo[i] * r, acc[t][i]);
-          acc[t][8 + i] = fmaf(gh[i], hi[i] * r, acc[t][8 + i]);
-          lo[i] = r * (gl[i] * wl[i] - lo[i] * m);
-          hi[i] = r * (gh[i] * wh[i] - hi[i] * m);
-        }
-        if (live) {
-          store8<DT>(a.y[t], yb + h * a.ys[t][2] + L.lo, lo);
-          store8<DT>(a.y[t], yb + h * a.ys[t][2] + L.hi, hi);
-        }
+      for (int i = 0; i < 8; ++i) {
+        acc[i] = fmaf(gl[i], lo[i] * in_sum, acc[i]);
+        acc[8 + i] = fmaf(gh[i], hi[i] * in_sum, acc[8 + i]);
+        lo[i] = r * (gl[i] * wl[i] - lo[i] * m);
+        hi[i] = r * (gh[i] * wh[i] - hi[i] * m);
+      }
+      if (live) {
+        store8<DT>(y, yb + h * yh + L.lo, lo);
+        store8<DT>(y, yb + h * yh + L.hi, hi);
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int i = 0; i < 16; ++i) {
+    float v = acc[i];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = acc[t][i];
+    for (int off = LPR; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane < LPR) red[warp][(i < 8 ? L.lo : L.hi) + (i & 7)] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.f;
 #pragma unroll
-      for (int off = LPR; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (lane < LPR) red[warp][(i < 8 ? L.lo : L.hi) + (i & 7)] = v;
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) v += red[w][threadIdx.x];
-      a.part[((size_t)blockIdx.x * 2 + t) * D + threadIdx.x] = v;
-    }
-    __syncthreads();
+    for (int w = 0; w < WARPS; ++w) v += red[w][threadIdx.x];
+    a.part[(size_t)blockIdx.x * D + threadIdx.x] = v;
   }
 }
 
-// dw: the partial sums of all CTAs, in a fixed order.  One CTA per 32 channels.
-__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* __restrict__ part, int ctas, int D, float* dwq,
-                                                     float* dwk) {
+// dw: the partial sums of a tensor's CTAs, in a fixed order.  One CTA per 32 channels.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const QkArgs a, const int D) {
   __shared__ float red[32][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = blockIdx.x * 32 >= D, lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int ch = blockIdx.x * 32 - t * D + lane;
+  const int c0 = t ? a.ctas[0] : 0, c1 = c0 + a.ctas[t];
   float v = 0.f;
-  for (int c = row; c < ctas; c += 32) v += part[(size_t)c * 2 * D + col];
-  red[row][threadIdx.x & 31] = v;
+#pragma unroll 8
+  for (int c = c0 + row; c < c1; c += 32) v += a.part[(size_t)c * D + ch];
+  red[row][lane] = v;
   __syncthreads();
   if (row == 0) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-    if (col < D)
-      dwq[col] = s;
-    else
-      dwk[col - D] = s;
+    for (int i = 0; i < 32; ++i) s += red[i][lane];
+    (t ? a.dw[1] : a.dw[0])[ch] = s;
   }
 }
 
 template <int D, int DT>
 cudaError_t launch_d(const QkArgs& a, bool w_f32, bool bwd, cudaStream_t s) {
   const bool any = !a.interleaved && a.rot % 16 != 0;
-  const int grid = bwd ? a.ctas : a.B * a.tiles;
+  const int grid = a.ctas[0] + a.ctas[1];
   if (grid > 0) {
     if (bwd) {
       if (any)
@@ -388,8 +419,17 @@ cudaError_t launch_d(const QkArgs& a, bool w_f32, bool bwd, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (bwd) {
-    qk_dw_kernel<<<2 * D / 32, 1024, 0, s>>>(a.part, grid, D, a.dw[0], a.dw[1]);
-    return cudaGetLastError();
+    // launched with the first kernel, whose end it waits for on the GPU
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * D / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = grid > 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, qk_dw_kernel, a, D);
   }
   return cudaSuccess;
 }
