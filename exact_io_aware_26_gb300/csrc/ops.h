@@ -33,10 +33,9 @@ struct QkArgs {
   const unsigned long long* freqs;
   const int* pos;  // or nullptr
   long long pos_stride;
-  int tok_tile;   // tokens of a tile (a power of two)
-  int tiles;      // token tiles of a batch entry
-  int ctas[2];    // CTAs of the launch for each tensor
-  float* part;    // backward: [CTA][d] partial weight gradients
+  FastDiv divN, divH[2];
+  int ctas;       // each takes an equal run of the B * N tokens
+  float* part;    // backward: [CTA][2][d] partial weight gradients
   float* dw[2];
 };
 int qk_rows_per_pass(int d);

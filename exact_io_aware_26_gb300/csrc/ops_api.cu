@@ -82,8 +82,9 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
     return fail(FA_ERR_INVALID, "rot_dim %d must be even, from 0 to d", p->rot_dim);
   if (!(std::isfinite(p->eps) && p->eps > 0.f)) return fail(FA_ERR_INVALID, "eps must be positive and finite");
   if (p->pos_stride < 0) return fail(FA_ERR_INVALID, "pos_stride is negative");
-  // a launch has a CTA for each tensor and tile of at least one token
-  if ((long long)p->B * p->N >= (1ll << 30)) return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^30 - 1");
+  // tokens and rows of a chunk are counted in 32 bits
+  if ((long long)p->B * p->N >= (1ll << 30) || p->Hq >= (1 << 24) || p->Hk >= (1 << 24))
+    return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^30 - 1 or the heads 2^24 - 1");
   const long long sq[3] = {p->B, p->N, p->Hq}, sk[3] = {p->B, p->N, p->Hk};
   FA_TRY(check_strides(p->q_stride, sq, 3, p->d, p->dtype, false, "q"));
   FA_TRY(check_strides(p->k_stride, sk, 3, p->d, p->dtype, false, "k"));
@@ -96,16 +97,7 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
   return FA_OK;
 }
 
-constexpr int kQkMaxCtas = 2048;  // of a tensor, in the backward (each leaves a partial sum)
-
-// Tokens of a tile: as many as the row slots of a CTA (each lane then forms its angles
-// once for all heads), fewer -- the slots share a token's heads -- while there would be
-// fewer than four tiles for each SM.
-int qk_tok_tile(const fa_qk_params* p, int sms) {
-  int tile = qk_rows_per_pass(p->d);
-  while (tile > 1 && (long long)p->B * ((p->N + tile - 1) / tile) < 4LL * sms) tile /= 2;
-  return tile;
-}
+constexpr int kQkCtasPerSm = 3, kQkBwdCtasPerSm = 2, kQkMaxSms = 160;
 
 QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* wq, const void* wk,
                const uint64_t* freqs, const int* positions, int sms, bool bwd) {
@@ -127,14 +119,14 @@ QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* 
   a.pos_stride = p->pos_stride;
   std::memcpy(a.xs[0], p->q_stride, sizeof(a.xs[0]));
   std::memcpy(a.xs[1], p->k_stride, sizeof(a.xs[1]));
-  a.tok_tile = qk_tok_tile(p, sms);
-  a.tiles = (p->N + a.tok_tile - 1) / a.tok_tile;
-  const long long tiles = (long long)a.B * a.tiles;
-  a.ctas[0] = a.ctas[1] = (int)tiles;
-  if (bwd && tiles > kQkMaxCtas) {  // the same number of tiles for each
-    const long long each = (tiles + kQkMaxCtas - 1) / kQkMaxCtas;
-    a.ctas[0] = a.ctas[1] = (int)((tiles + each - 1) / each);
-  }
+  a.divN = FastDiv::of((uint32_t)std::max(p->N, 1));
+  a.divH[0] = FastDiv::of((uint32_t)p->Hq);
+  a.divH[1] = FastDiv::of((uint32_t)p->Hk);
+  // one wave of CTAs, but no more than have a row for each of their row slots
+  const long long T = (long long)p->B * p->N, slots = qk_rows_per_pass(p->d);
+  const long long least = std::max(1ll, slots / (p->Hq + p->Hk));
+  const long long wave = (long long)std::min(sms, kQkMaxSms) * (bwd ? kQkBwdCtasPerSm : kQkCtasPerSm);
+  a.ctas = (int)std::min(wave, (T + least - 1) / least);
   return a;
 }
 
@@ -269,7 +261,7 @@ fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, c
 
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_qk_params* p) {
   if (qk_check(p, true) != FA_OK) return 0;
-  return (size_t)2 * kQkMaxCtas * p->d * 4;
+  return (size_t)kQkMaxSms * kQkBwdCtasPerSm * 2 * p->d * 4;
 }
 
 fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* k, const void* dyq, const void* dyk,
