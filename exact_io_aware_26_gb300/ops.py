@@ -283,15 +283,14 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float =
             dq = torch.empty(q.shape, dtype=q.dtype, device=device)
         if dk is None:
             dk = torch.empty(k.shape, dtype=q.dtype, device=device)
-        dw = torch.empty((2, d), dtype=torch.float32, device=device)
+        dwq = torch.empty(d, dtype=torch.float32, device=device)
+        dwk = torch.empty(d, dtype=torch.float32, device=device)
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    at = dw.data_ptr()
     _check(load().fa_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(), dyq.data_ptr(), dyk.data_ptr(), wq.data_ptr(),
                                       wk.data_ptr(), freqs.data_ptr(), _ptr(positions), dq.data_ptr(), dk.data_ptr(),
-                                      at, at + 4 * d, workspace.data_ptr(), workspace.nbytes, handle),
+                                      dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle),
            "fa_qk_norm_rope_bwd")
-    dwq, dwk = dw.unbind()
     return dq, dk, dwq, dwk
 
 
@@ -374,8 +373,10 @@ def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = F
     handle, alloc = _enter(device, stream, slots, cache, k, v)
     if out is None:
         T, H = slots.shape[0], cache.shape[1]
+        shape = (H, T, d) if heads_first else (T, H, d)
         with alloc:
-            k, v = torch.empty((2, H, T, d) if heads_first else (2, T, H, d), dtype=dtype, device=device).unbind()
+            k = torch.empty(shape, dtype=dtype, device=device)
+            v = torch.empty(shape, dtype=dtype, device=device)
     _check(load().fa_kv4_gather(c, rows, cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), handle),
            "fa_kv4_gather")
     return k, v
@@ -489,7 +490,7 @@ def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_siz
     handle, alloc = _enter(device, stream, seq_lens, new_lens, block_table, free_pages, free_count, *given)
     if out is None:
         with alloc:
-            given = torch.empty(sum(sizes), dtype=torch.int32, device=device).split(sizes)
+            given = [torch.empty(n, dtype=torch.int32, device=device) for n in sizes]
         out = dict(zip(_PLAN_OUT, given))
     kv, cu, pos, slots, counts = given
     _check(load().fa_paged_plan(p, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
