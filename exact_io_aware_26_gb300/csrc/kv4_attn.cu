@@ -44,23 +44,25 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;     // running maximum before any token is seen
 constexpr int kUnit = 2 * kKvBlock;  // tokens a warp takes at a time
-constexpr int kMinShare = 16;        // units: shares are not cut finer (4 per warp)
+constexpr int kMinShare = kWarps;    // units: shares are not cut finer (one per warp)
 constexpr int kReqCache = 128;       // requests whose lengths a CTA keeps at hand
 
 template <int D, int NT>
 struct Cfg {
   using Blk = KvBlock<D>;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr int CTAS_PER_SM = NT == 1 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int LDO = D + 4;  // row pitch of the joined O, in floats
   static constexpr int stage = 2 * Blk::bytes;
+  // For the join each warp's O goes into its ring.  Eight rows take the stage of the tile's
+  // last unit, and the copies of the next tile go on in the others; more rows take the whole
+  // ring, which then holds one tile at a time.
+  static constexpr bool across = NT == 1;
+  static constexpr int STAGES = D == 64 || NT == 4 ? 4 : 2;
   static constexpr int ring = kWarps * STAGES * stage;
-  // a warp's O for the join goes where its last unit was, if that is large enough
-  static constexpr bool in_ring = ROWS * LDO * 4 <= stage;
-  static constexpr int joined = in_ring ? 0 : kWarps * ROWS * LDO * 4;
+  static_assert(ROWS * LDO * 4 <= (across ? stage : STAGES * stage), "a warp's O fits");
   static constexpr int qfrag = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;
-  static constexpr int smem = ring + joined + qfrag;
+  static constexpr int smem = ring + qfrag;
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -84,11 +86,23 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// 1 + c / 16 of codes P and P + 4 (bits 4 P and 16 + 4 P) of a word, as half2.
+// 1 + c / 16 of codes P and P + 4 (bits 4 P and 16 + 4 P) of a word, as half2: a shift, and
+// one (x & mask) | one -- written out, with both constants in registers, because as two
+// operations with constants it would cost a third more of the integer pipe, which is
+// what bounds the unit loop.
+struct Magic {
+  uint32_t mask, one;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.u32 %0, 0x03C003C0;" : "=r"(mask));
+    asm volatile("mov.u32 %0, 0x3C003C00;" : "=r"(one));
+  }
+};
 template <int P>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+__device__ __forceinline__ uint32_t code_pair(const Magic& k, uint32_t w) {
   const uint32_t x = P == 0 ? w << 6 : P == 1 ? w << 2 : P == 2 ? w >> 2 : w >> 6;
-  return (x & 0x03C003C0u) | 0x3C003C00u;
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(k.mask), "r"(k.one));
+  return y;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * (S * C::stage);
   const uint32_t bar0 = smem_addr(&bars[warp][0]);
-  uint2* qfrag = reinterpret_cast<uint2*>(smem + C::ring + C::joined);
+  uint2* qfrag = reinterpret_cast<uint2*>(smem + C::ring);
   (void)qfrag;
 
   // ---- shares: prefix sums of the units of all requests
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
   share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
   const long long u0 = (long long)blockIdx.x * share, u1 = min(total, u0 + share);
   if (u0 >= total) {  // no share (the CTA's threads all leave)
-    if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
   // the thread whose requests hold unit u0 finds its tile
@@ -348,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     __syncthreads();
   }
 
+  const Magic magic;
   const WaitCtx wc{&abort_s, a.rep.st, a.rep.epoch, a.rep.wait_ns};
 
   Feed<ROWS>& feed = feed_s[warp];
@@ -383,14 +398,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     }
     ++turn;
   };
+  if constexpr (C::across)
 #pragma unroll 1
-  for (int s = 0; s < S; ++s) produce(s);
+    for (int s = 0; s < S; ++s) produce(s);
   __syncthreads();  // tile_s
 
   // ---- the share's tiles
   int stage = 0;
   uint32_t parity = 0;
   int4 meta = make_int4(-1, 0, 0, 0);
+  int meta_q0 = 0;
   long long tile0 = start_u;
 #pragma unroll 1
   for (int which = 0; tile0 < u1; which ^= 1) {
@@ -398,6 +415,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     const Tile y = cw.y;
     const Req x = cw.x;
     const int first = (int)max(0ll, u0 - tile0), last = (int)min((long long)y.n_u, u1 - tile0);
+    if constexpr (!C::across) {
+      fence_async_smem();  // the join's stores before the copies that reuse the ring
+      for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((stage + s) % S);
+    }
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
     // which its score factor takes back: no 16-bit query leaves fp16's range.
@@ -496,10 +517,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
       const uint32_t sb = __byte_perm(xb, xb, 0x1010), cb = __byte_perm(xb, xb, 0x3232);
 #pragma unroll
       for (int i = 0; i < WPT; ++i) {
-        const uint32_t a0 = hfma2(code_pair<0>(wa[i]), sa, ca), a1 = hfma2(code_pair<0>(wb[i]), sb, cb);
-        const uint32_t a2 = hfma2(code_pair<1>(wa[i]), sa, ca), a3 = hfma2(code_pair<1>(wb[i]), sb, cb);
-        const uint32_t c0 = hfma2(code_pair<2>(wa[i]), sa, ca), c1 = hfma2(code_pair<2>(wb[i]), sb, cb);
-        const uint32_t c2 = hfma2(code_pair<3>(wa[i]), sa, ca), c3 = hfma2(code_pair<3>(wb[i]), sb, cb);
+        const uint32_t a0 = hfma2(code_pair<0>(magic, wa[i]), sa, ca), a1 = hfma2(code_pair<0>(magic, wb[i]), sb, cb);
+        const uint32_t a2 = hfma2(code_pair<1>(magic, wa[i]), sa, ca), a3 = hfma2(code_pair<1>(magic, wb[i]), sb, cb);
+        const uint32_t c0 = hfma2(code_pair<2>(magic, wa[i]), sa, ca), c1 = hfma2(code_pair<2>(magic, wb[i]), sb, cb);
+        const uint32_t c2 = hfma2(code_pair<3>(magic, wa[i]), sa, ca), c3 = hfma2(code_pair<3>(magic, wb[i]), sb, cb);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint2 q0, q1;
@@ -548,14 +569,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma16816(o[mt][j], a0, a1, a2, a3, p0[j], p1[j]);
         };
-        product(4 * i + 0, code_pair<0>(xl), code_pair<0>(xh), code_pair<0>(yl), code_pair<0>(yh));
-        product(4 * i + 1, code_pair<1>(xl), code_pair<1>(xh), code_pair<1>(yl), code_pair<1>(yh));
-        product(4 * i + 2, code_pair<2>(xl), code_pair<2>(xh), code_pair<2>(yl), code_pair<2>(yh));
-        product(4 * i + 3, code_pair<3>(xl), code_pair<3>(xh), code_pair<3>(yl), code_pair<3>(yh));
+        product(4 * i + 0, code_pair<0>(magic, xl), code_pair<0>(magic, xh), code_pair<0>(magic, yl), code_pair<0>(magic, yh));
+        product(4 * i + 1, code_pair<1>(magic, xl), code_pair<1>(magic, xh), code_pair<1>(magic, yl), code_pair<1>(magic, yh));
+        product(4 * i + 2, code_pair<2>(magic, xl), code_pair<2>(magic, xh), code_pair<2>(magic, yl), code_pair<2>(magic, yh));
+        product(4 * i + 3, code_pair<3>(magic, xl), code_pair<3>(magic, xh), code_pair<3>(magic, yl), code_pair<3>(magic, yh));
       }
     };
 
-    int held = -1;  // stage of the tile's last unit, kept for the join (C::in_ring)
+    int held = -1;  // stage of the tile's last unit, kept for the join (across)
 #pragma unroll 1
     for (int u = first + warp; u < last; u += kWarps) {
       // a wait that gave up has recorded it; the copy must still land before the stage is left
@@ -655,10 +676,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         values(kb + h * Blk::bytes + Blk::half, p0, p1);
       }
       __syncwarp();  // every lane has read the stage
-      if (C::in_ring && u + kWarps >= last)
-        held = stage;
-      else
+      if (C::across ? u + kWarps < last : u + S * kWarps < last)
         produce(stage);
+      else
+        held = stage;
       if (++stage == S) {
         stage = 0;
         parity ^= 1u;
@@ -668,11 +689,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     // ---- join the warps that took units of the tile
     const int active = min(kWarps, last - first);
     auto joined = [&](int w) {  // warp w's O, [ROWS][LDO]
-      return C::in_ring ? reinterpret_cast<float*>(smem + w * (S * C::stage)) : reinterpret_cast<float*>(smem + C::ring + w * ROWS * C::LDO * 4);
+      return reinterpret_cast<float*>(smem + w * (S * C::stage) + (C::across ? held_s[w] * C::stage : 0));
     };
     if (warp < active) {
-      float* mine = joined(warp) + (C::in_ring ? held * (C::stage / 4) : 0);
       if (lane == 0) held_s[warp] = held;
+      __syncwarp();
+      float* mine = joined(warp);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -710,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         const float f = ex2(m_s[w][row] - top);
         sum = fmaf(f, l_s[w][row], sum);
         const float4* src = reinterpret_cast<const float4*>(
-            joined(w) + (C::in_ring ? held_s[w] * (C::stage / 4) : 0) + row * C::LDO + ch);
+            joined(w) + row * C::LDO + ch);
         const float4 u = src[0], v = src[1];
         acc[0] = fmaf(f, u.x, acc[0]); acc[1] = fmaf(f, u.y, acc[1]);
         acc[2] = fmaf(f, u.z, acc[2]); acc[3] = fmaf(f, u.w, acc[3]);
@@ -742,7 +764,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     }
     if (tid == 0) {
       const long long tile_end = tile0 + y.n_u;
-      if (goes_on && !from_before) meta = make_int4(cw.r, cw.t, cw.h, (int)((tile_end - 1) / share));
+      if (goes_on && !from_before) {
+        meta = make_int4(y.row0, y.rows, cw.h, (int)((tile_end - 1) / share));
+        meta_q0 = x.q0;
+      }
       if (tile_end < u1) {
         Walk<ROWS> w = cw;
         w.next(a, reqs, cache_r0);
@@ -750,13 +775,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
       }
     }
     __syncthreads();  // joined, m_s, l_s read; the next tile known
-    if (C::in_ring && held >= 0) {
+    if (C::across && held >= 0) {
       fence_async_smem();  // the join's stores before the copy that reuses the stage
       produce(held);
     }
     tile0 += y.n_u;
   }
-  if (tid == 0) a.meta[blockIdx.x] = meta;
+  if (tid == 0) {
+    a.meta[2 * blockIdx.x] = meta;
+    a.meta[2 * blockIdx.x + 1] = make_int4(meta_q0, 0, 0, 0);
+  }
 }
 
 // Adds the shares of the tile that starts in share blockIdx.x and goes on, if any; rows
@@ -768,11 +796,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
   __shared__ float top_s[kMergeWarps][8], sum_s[kMergeWarps][8];
   __shared__ float acc_s[kMergeWarps][8][D + 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 meta = a.meta[blockIdx.x];
+  const int4 meta = a.meta[2 * blockIdx.x];  // first row, rows, key head, last share
+  const int q0 = a.meta[2 * blockIdx.x + 1].x;
   if (meta.x < 0) return;
-  const Req x = load_req(a, meta.x);
-  const Tile y = tile_of<ROWS>(a, x, meta.y);
-  const int r0 = 8 * blockIdx.y, rows = min(8, y.rows - r0);
+  const int r0 = 8 * blockIdx.y, rows = min(8, meta.y - r0);
   if (rows <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
   auto slot = [&](int c, int row) {  // the first share's slot is its second one
@@ -826,14 +853,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
     for (int i = 0; i < CPL; ++i) v[i] += acc_s[w][row][lane * CPL + i];
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  const int gr = y.row0 + r0 + row, qi = a.G.div(gr);
+  const int gr = meta.x + r0 + row, qi = a.G.div(gr);
   const long long head = (long long)meta.z * a.G.d + (gr - qi * (int)a.G.d);
-  if (!fa_bounds(a.rep.st, x.q0 + qi < a.T && head < a.Hq)) return;
-  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + (x.q0 + qi) * a.os[0] + head * a.os[1] + lane * CPL);
+  if (!fa_bounds(a.rep.st, q0 + qi < a.T && head < a.Hq)) return;
+  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + (q0 + qi) * a.os[0] + head * a.os[1] + lane * CPL);
 #pragma unroll
   for (int i = 0; i < CPL / 2; ++i) to[i] = pack2<F16>(v[2 * i] * inv, v[2 * i + 1] * inv);
   if (lane == 0 && a.lse)
-    a.lse[(long long)(x.q0 + qi) * a.Hq + head] = total == 0.f ? -INFINITY : (best + log2f(total)) * 0.6931471805599453f;
+    a.lse[(long long)(q0 + qi) * a.Hq + head] = total == 0.f ? -INFINITY : (best + log2f(total)) * 0.6931471805599453f;
 }
 
 template <int D, int NT, bool F16>

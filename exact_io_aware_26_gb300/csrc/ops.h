@@ -77,7 +77,7 @@ struct Kv4AttnArgs {
   long long os[2];
   float* lse;       // or nullptr
   float* part;      // 2 slots per CTA: rows x (d + 2) fp32 each
-  int4* meta;       // per CTA: the tile whose share starts in it and goes on
+  int4* meta;       // two per CTA: the tile that starts in its share and goes on
   Report rep;
 };
 // Rows of a query tile: 8, 16 or 32 (see kv4_attn.cu), and the most CTAs a launch has.

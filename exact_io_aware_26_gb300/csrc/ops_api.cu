@@ -321,7 +321,7 @@ size_t fa_kv4_attention_workspace_size(const fa_kv4_cache* c, const fa_kv4_attn_
   if (attn_check(c, p) != FA_OK) return 0;
   const int rows = kv4_tile_rows(p->Hq / c->Hk, p->max_q_len);
   const int ctas = kv4_max_ctas(c->d, rows, kMaxSms);
-  return attn_part_bytes(ctas, rows, c->d) + align256((size_t)ctas * 16);
+  return attn_part_bytes(ctas, rows, c->d) + align256((size_t)ctas * 32);
 }
 
 fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, const void* q, const void* cache,
