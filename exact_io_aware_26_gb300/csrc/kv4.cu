@@ -1,7 +1,7 @@
 // kv4.cu -- writing tokens' keys and values into the 4-bit cache, and reading them
 // back.  Both are streams: bound by HBM for prompts, by latency for single tokens.
-// Eight channels per lane (a 16-byte load of a 16-bit type, one 4-byte word of
-// codes), four lanes per pair, whose least and largest are two shuffles each.
+// Eight channels per lane (a 16-byte load of a 16-bit type, one 4-byte word of codes),
+// four lanes per pair, whose least and largest are two shuffles each.
 #include "kv4.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -42,46 +42,89 @@ __device__ __forceinline__ uint8_t* slot_block(const Kv4RowArgs& a, int slot, in
   }
   row = in % kKvBlock;
   return const_cast<uint8_t*>(a.c.data) + page * a.c.page_stride +
-         (((long long)head << (a.c.page_log - 4)) + in / kKvBlock) * block_bytes;
+         (long long)((head << (a.c.page_log - 4)) + in / kKvBlock) * block_bytes;
 }
 
-// Codes of a lane's eight values and the pair of its group of four lanes.
+__device__ __forceinline__ long long row_at(const Kv4RowArgs& a, int side, int tok, int head) {
+  return (long long)tok * a.xs[side][0] + (long long)head * a.xs[side][1];
+}
+
+// Least and largest of three, NaN if one is.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Codes of a lane's eight values and the pair of its group of four lanes.  Writing prompts
+// is bound by these instructions before HBM; hence packed fp32 arithmetic, three-input
+// minima, and no division or clamping per value where neither can matter.
 __device__ __forceinline__ void quantise8(float (&v)[8], uint32_t& word, uint32_t& pair) {
-  float lo = kKvSaturate, hi = -kKvSaturate;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    nan |= v[i] != v[i];
-    v[i] = fminf(fmaxf(v[i], -kKvSaturate), kKvSaturate);
-    lo = fminf(lo, v[i]);
-    hi = fmaxf(hi, v[i]);
-  }
+  float lo = min3_nan(min3_nan(v[0], v[1], v[2]), min3_nan(v[3], v[4], v[5]), min3_nan(v[6], v[7], v[7]));
+  float hi = max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], v[7]));
 #pragma unroll
   for (int off = 1; off < 4; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-    nan |= __shfl_xor_sync(0xffffffffu, (int)nan, off) != 0;
+    const float l = __shfl_xor_sync(0xffffffffu, lo, off), h = __shfl_xor_sync(0xffffffffu, hi, off);
+    lo = min3_nan(lo, l, l);
+    hi = max3_nan(hi, h, h);
+  }
+  const bool nan = lo != lo;
+  if (lo < -kKvSaturate || hi > kKvSaturate) {  // (rare)
+    lo = fminf(fmaxf(lo, -kKvSaturate), kKvSaturate);
+    hi = fminf(fmaxf(hi, -kKvSaturate), kKvSaturate);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -kKvSaturate), kKvSaturate);
   }
   // the documented steps, each rounded once: plain fp32, no contraction
   const __half s = __float2half_rn(__fdiv_rn(__fmul_rn(__fsub_rn(hi, lo), 16.f), 15.f));
   const __half c = __float2half_rn(__fsub_rn(lo, __half2float(s)));
   const float sf = __half2float(s), cf = __half2float(c);
-  word = 0;
-  if (sf > 0.f && !nan) {
-    // The quotient only decides between neighbouring codes: a product with the rounded
-    // reciprocal is off by less than 2^-22 of it, at most 31 + a clamped rest, so that
-    // its rounding is the quotient's unless it lies within 2^-16 of a half, where the
-    // division itself is done (a fifth of the time of eight divisions).
-    const float inv = 1.f / sf;
+  pair = nan ? 0x7E007E00u : (uint32_t)__half_as_ushort(s) | ((uint32_t)__half_as_ushort(c) << 16);
+  // The quotient (x - base) * 16 / scale only decides between neighbouring codes.  A product
+  // with the reciprocal is off by less than 2^-22 of it, below 2^-17 where no code is
+  // clamped, so its rounding is the quotient's unless it lies within 2^-16 of a half.  Then,
+  // and where the group's least or largest value has a code out of range (fp16's rounding
+  // of a base far from 0), the documented steps themselves are done.
+  const float inv = __fdividef(16.f, sf);
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+  const uint64_t inv2 = f2pack(inv, inv), base2 = f2pack(-cf, -cf), off2 = f2pack(-16.f, -16.f);
+  const uint64_t up2 = f2pack(kRound, kRound), down2 = f2pack(-kRound, -kRound), neg2 = f2pack(-1.f, -1.f);
+  uint64_t code[4];
+  float border = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = __fmul_rn(__fsub_rn(v[i], cf), 16.f);
-      float t = fminf(__fmul_rn(d, inv), 64.f) - 16.f;
-      if (fabsf(fabsf(t - rintf(t)) - 0.5f) < 0x1p-16f) t = __fsub_rn(__fdiv_rn(d, sf), 16.f);
-      word |= (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = ffma2(fadd2(f2pack(v[2 * i], v[2 * i + 1]), base2), inv2, off2);
+    code[i] = fadd2(fadd2(t, up2), down2);
+    float x, y;
+    f2unpack(ffma2(code[i], neg2, t), x, y);
+    border = fmax3(border, fabsf(x), fabsf(y));
+  }
+  const float first = fmaf(lo - cf, inv, -16.f), last = fmaf(hi - cf, inv, -16.f);
+  const bool plain = border < 0.5f - 0x1p-16f && first > -0.5f && last < 15.5f;
+  if (plain) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // four codes: a whole number below 2^16, in the low bits of 2^23 more
+      float even, odd;
+      f2unpack(ffma2(code[2 * k + 1], f2pack(256.f, 256.f), code[2 * k]), even, odd);
+      w[k] = __float_as_uint(fmaf(odd, 16.f, even) + 8388608.f);
+    }
+    word = __byte_perm(w[0], w[1], 0x5410);
+  } else {  // also a scale of 0 or NaN, whose codes are 0
+    word = 0;
+    if (sf > 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = __fsub_rn(__fdiv_rn(__fmul_rn(__fsub_rn(v[i], cf), 16.f), sf), 16.f);
+        word |= (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f) << (4 * i);
+      }
     }
   }
-  pair = nan ? 0x7E007E00u : (uint32_t)__half_as_ushort(s) | ((uint32_t)__half_as_ushort(c) << 16);
 }
 
 // A row is one head of one token: D / 8 lanes, which take its key and its value.
@@ -96,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowArgs a
   int row = 0;
   uint8_t* blk = nullptr;
   if (live) {
-    load8<DT>(a.x[0], tok * a.xs[0][0] + head * a.xs[0][1] + 8 * j, k);
-    load8<DT>(a.x[1], tok * a.xs[1][0] + head * a.xs[1][1] + 8 * j, v);
+    load8<DT>(a.x[0], row_at(a, 0, tok, head) + 8 * j, k);
+    load8<DT>(a.x[1], row_at(a, 1, tok, head) + 8 * j, v);
     blk = slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row);
   }
   uint32_t wk, pk, wv, pv;
@@ -107,58 +150,79 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowArgs a
   uint8_t* at = blk + row * Blk::row + 4 * j;
   *reinterpret_cast<uint32_t*>(at) = wk;
   *reinterpret_cast<uint32_t*>(at + Blk::half) = wv;
-  if ((j & 3) == 0) {
+  // the pairs of a group: its first lane stores the key's, its second the value's
+  if ((j & 2) == 0) {
     at = blk + Blk::codes + (row * Blk::groups + (j >> 2)) * 4;
-    *reinterpret_cast<uint32_t*>(at) = pk;
-    *reinterpret_cast<uint32_t*>(at + Blk::half) = pv;
+    *reinterpret_cast<uint32_t*>(at + (j & 1) * Blk::half) = j & 1 ? pv : pk;
   }
 }
 
 template <int DT>
 __device__ __forceinline__ void store_values(void* x, long long to, uint32_t word, uint32_t pair) {
+  // codes p and p + 4 of the word as half2, then neighbours side by side
   const __half2 p = *reinterpret_cast<const __half2*>(&pair);
-  float v[8];
+  uint32_t q[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half m = __ushort_as_half((unsigned short)(0x3C00u | (((word >> (4 * i)) & 15u) << 6)));
-    v[i] = __half2float(__hfma(m, __low2half(p), __high2half(p)));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = ((i < 2 ? word << (6 - 4 * i) : word >> (4 * i - 6)) & 0x03C003C0u) | 0x3C003C00u;
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&m), __low2half2(p), __high2half2(p));
+    q[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  if constexpr (DT == FA_F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + to);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  const uint32_t n[4] = {__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                         __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632)};
+  if constexpr (DT == FA_F16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + to) = make_uint4(n[0], n[1], n[2], n[3]);
   } else {
-    constexpr bool F16 = DT == FA_F16;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + to) =
-        make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = unpack2<true>(n[i]);
+    if constexpr (DT == FA_F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + to);
+      o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + to) =
+          make_uint4(pack2<false>(f[0].x, f[0].y), pack2<false>(f[1].x, f[1].y), pack2<false>(f[2].x, f[2].y),
+                     pack2<false>(f[3].x, f[3].y));
+    }
   }
 }
 
+// Two rows per lane, so that two chains of loads (slot, then codes) are in flight.
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4RowArgs a) {
   using Blk = KvBlock<D>;
-  constexpr int LPR = D / 8;
-  const int j = threadIdx.x % LPR, r = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-  if (r >= a.rows) return;
-  const int tok = a.heads.div(r), head = r - tok * (int)a.heads.d;
-  int row;
-  const uint8_t* blk = slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row);
-  uint32_t wk = 0, pk = 0, wv = 0, pv = 0;
-  if (blk) {
-    const uint8_t* at = blk + row * Blk::row + 4 * j;
-    wk = *reinterpret_cast<const uint32_t*>(at);
-    wv = *reinterpret_cast<const uint32_t*>(at + Blk::half);
-    at = blk + Blk::codes + (row * Blk::groups + (j >> 2)) * 4;
-    pk = *reinterpret_cast<const uint32_t*>(at);
-    pv = *reinterpret_cast<const uint32_t*>(at + Blk::half);
+  constexpr int LPR = D / 8, ROWS = kThreads / LPR;
+  const int j = threadIdx.x % LPR, r0 = blockIdx.x * (2 * ROWS) + threadIdx.x / LPR;
+  int tok[2], head[2];
+  uint32_t wk[2] = {}, pk[2] = {}, wv[2] = {}, pv[2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = min(r0 + i * ROWS, a.rows - 1);
+    tok[i] = a.heads.div(r);
+    head[i] = r - tok[i] * (int)a.heads.d;
+    int row;
+    const uint8_t* blk = slot_block(a, __ldg(a.slots + tok[i]), head[i], Blk::bytes, row);
+    if (blk) {
+      const uint8_t* at = blk + row * Blk::row + 4 * j;
+      wk[i] = *reinterpret_cast<const uint32_t*>(at);
+      wv[i] = *reinterpret_cast<const uint32_t*>(at + Blk::half);
+      at = blk + Blk::codes + (row * Blk::groups + (j >> 2)) * 4;
+      pk[i] = *reinterpret_cast<const uint32_t*>(at);
+      pv[i] = *reinterpret_cast<const uint32_t*>(at + Blk::half);
+    }
   }
-  store_values<DT>(a.x[0], tok * a.xs[0][0] + head * a.xs[0][1] + 8 * j, wk, pk);
-  store_values<DT>(a.x[1], tok * a.xs[1][0] + head * a.xs[1][1] + 8 * j, wv, pv);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (r0 + i * ROWS >= a.rows) return;
+    store_values<DT>(a.x[0], row_at(a, 0, tok[i], head[i]) + 8 * j, wk[i], pk[i]);
+    store_values<DT>(a.x[1], row_at(a, 1, tok[i], head[i]) + 8 * j, wv[i], pv[i]);
+  }
 }
 
 template <int D, int DT>
 cudaError_t launch(const Kv4RowArgs& a, bool gather, cudaStream_t s) {
-  const int per = kThreads / (D / 8), grid = (a.rows + per - 1) / per;
+  const int per = kThreads / (D / 8) * (gather ? 2 : 1), grid = (a.rows + per - 1) / per;
   if (gather)
     kv4_gather_kernel<D, DT><<<grid, kThreads, 0, s>>>(a);
   else

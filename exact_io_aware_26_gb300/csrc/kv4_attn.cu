@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
   __shared__ int start_r, start_t, start_h;
   __shared__ float m_s[kWarps][ROWS], l_s[kWarps][ROWS];
   __shared__ int held_s[kWarps];
+  __shared__ float up_s[NT == 4 ? ROWS : 1];
+  static_assert(NT != 4 || kWarps == 4, "a warp for every eight rows");
   __shared__ volatile int abort_s;
   __shared__ Feed<ROWS> feed_s[kWarps];
   __shared__ Walk<ROWS> tile_s[2];  // the current tile; the next one
@@ -422,10 +424,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
     // which its score factor takes back: no 16-bit query leaves fp16's range.
+    // (32 rows: each warp prepares eight of them for all, in shared memory.)
     uint32_t qf[NT == 4 ? 1 : NT][KS][2];
     float factor[NT][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int jj = 0; jj < (NT == 4 ? 1 : NT); ++jj) {
+      const int j = NT == 4 ? warp : jj;
       const int n = g + 8 * j;
       uint4 raw[D / 32];
 #pragma unroll
@@ -468,16 +472,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
         for (int p = 0; p < 4; ++p) {
           const uint32_t v = pack2<true>(f[p], f[p + 4]);
           if constexpr (NT == 4) {
-            if (warp == j) reinterpret_cast<uint32_t*>(qfrag)[((j * KS + 2 * i + (p >> 1)) * 32 + lane) * 2 + (p & 1)] = v;
+            reinterpret_cast<uint32_t*>(qfrag)[((j * KS + 2 * i + (p >> 1)) * 32 + lane) * 2 + (p & 1)] = v;
           } else {
-            qf[j][2 * i + (p >> 1)][p & 1] = v;
+            qf[jj][2 * i + (p >> 1)][p & 1] = v;
           }
         }
       }
+      if constexpr (NT == 4) {
+        if (t4 == 0) up_s[n] = up;
+      } else {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) factor[j][c] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + c)) * a.scale_log2;
+        for (int c = 0; c < 2; ++c) factor[jj][c] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + c)) * a.scale_log2;
+      }
     }
-    if constexpr (NT == 4) __syncthreads();
+    if constexpr (NT == 4) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) factor[j][c] = up_s[8 * j + 2 * t4 + c] * a.scale_log2;
+    }
     // tokens that every row sees: no comparisons in their units
     const int i0 = a.G.div(y.row0), i1 = a.G.div(y.row0 + y.rows - 1);
     const int all_hi = x.kv - x.n + i0 + 1;

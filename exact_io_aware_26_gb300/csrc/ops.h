@@ -54,7 +54,7 @@ struct Kv4RowArgs {
   FastDiv heads;
   const int* slots;
   void* x[2];              // keys, values
-  long long xs[2][2];      // element strides {token, head}
+  int xs[2][2];            // element strides {token, head}
   DevStatus* st;
 };
 cudaError_t launch_kv4_append(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);

@@ -152,6 +152,7 @@ fa_status cache_check(const fa_kv4_cache* c) {
   if ((long long)c->num_pages * c->page_size > 0x7FFFFFFFll)
     return fail(FA_ERR_UNSUPPORTED, "num_pages * page_size exceeds 2^31 - 1 slots");
   const long long page = (long long)c->Hk * (c->page_size / 16) * fa_kv4_block_bytes(c->d);
+  if (page > 0x7FFFFFFFll) return fail(FA_ERR_UNSUPPORTED, "a page of %lld bytes exceeds 2^31 - 1", page);
   if (c->page_stride < page || c->page_stride % 16 != 0)
     return fail(FA_ERR_INVALID, "page_stride %lld must be a multiple of 16, at least %lld", c->page_stride, page);
   return FA_OK;
@@ -177,6 +178,9 @@ fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
   if (rows->dtype != FA_F32 && rows->dtype != FA_F16 && rows->dtype != FA_BF16)
     return fail(FA_ERR_INVALID, "dtype %d is not an fa_dtype", rows->dtype);
   const long long size[2] = {rows->T, c->Hk};
+  for (int i = 0; i < 2; ++i)
+    if (rows->k_stride[i] > 0x7FFFFFFFll || rows->v_stride[i] > 0x7FFFFFFFll)
+      return fail(FA_ERR_UNSUPPORTED, "a stride of k or v exceeds 2^31 - 1 elements");
   FA_TRY(check_strides(rows->k_stride, size, 2, c->d, rows->dtype, gather, "k"));
   FA_TRY(check_strides(rows->v_stride, size, 2, c->d, rows->dtype, gather, "v"));
   if (rows->T > 0) {
@@ -196,8 +200,10 @@ fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
   a.slots = slots;
   a.x[0] = const_cast<void*>(k);
   a.x[1] = const_cast<void*>(v);
-  std::memcpy(a.xs[0], rows->k_stride, sizeof(a.xs[0]));
-  std::memcpy(a.xs[1], rows->v_stride, sizeof(a.xs[1]));
+  for (int i = 0; i < 2; ++i) {
+    a.xs[0][i] = (int)rows->k_stride[i];
+    a.xs[1][i] = (int)rows->v_stride[i];
+  }
   a.st = rep.st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = gather ? launch_kv4_gather(a, c->d, rows->dtype, s) : launch_kv4_append(a, c->d, rows->dtype, s);
