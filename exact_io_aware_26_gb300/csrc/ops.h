@@ -25,15 +25,17 @@ struct QkArgs {
   int B, N, Hq, Hk;
   int rot, interleaved;
   float eps;
-  const void* x[2];   // q, k
+  const char* x[2];   // q, k
   const void* w[2];   // wq, wk
-  void* y[2];         // forward: results; backward: gradients of q, k
-  const void* dy[2];  // backward: gradients at the results
-  long long xs[2][3], ys[2][3], ds[2][3];  // element strides {batch, token, head} of x, y, dy
+  char* y[2];         // forward: results; backward: gradients of q, k
+  const char* dy[2];  // backward: gradients at the results
+  // byte strides between batch entries, tokens and heads of x, y, dy
+  long long xb[2], yb[2], db[2];
+  int xn[2], xh[2], yn[2], yh[2], dn[2], dh[2];
   const unsigned long long* freqs;
   const int* pos;  // or nullptr
   long long pos_stride;
-  FastDiv divN, divH[2];
+  FastDiv divN, divH[2], divAll;  // by N, Hq and Hk, their sum
   int ctas;       // each takes an equal run of the B * N tokens
   float* part;    // backward: [CTA][2][d] partial weight gradients
   float* dw[2];

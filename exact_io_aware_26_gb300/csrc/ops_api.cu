@@ -85,6 +85,11 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
   // tokens and rows of a chunk are counted in 32 bits
   if ((long long)p->B * p->N >= (1ll << 30) || p->Hq >= (1 << 24) || p->Hk >= (1 << 24))
     return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^30 - 1 or the heads 2^24 - 1");
+  for (int i = 1; i < 3; ++i)
+    for (const long long* st : {p->q_stride, p->k_stride, p->yq_stride, p->yk_stride, bwd ? p->dq_stride : p->q_stride,
+                                bwd ? p->dk_stride : p->k_stride})
+      if (st[i] * elem_bytes(p->dtype) > 0x7FFFFFFFll)
+        return fail(FA_ERR_UNSUPPORTED, "a token or head stride exceeds 2^31 - 1 bytes");
   const long long sq[3] = {p->B, p->N, p->Hq}, sk[3] = {p->B, p->N, p->Hk};
   FA_TRY(check_strides(p->q_stride, sq, 3, p->d, p->dtype, false, "q"));
   FA_TRY(check_strides(p->k_stride, sk, 3, p->d, p->dtype, false, "k"));
@@ -97,7 +102,18 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
   return FA_OK;
 }
 
-constexpr int kQkCtasPerSm = 3, kQkBwdCtasPerSm = 2, kQkMaxSms = 160;
+constexpr int kQkCtasPerSm = 4, kQkBwdCtasPerSm = 2, kQkMaxSms = 160;
+
+// Byte strides of a pair of tensors.
+void qk_strides(const fa_qk_params* p, const long long* q, const long long* k, long long (&b)[2], int (&n)[2], int (&h)[2]) {
+  const long long e = elem_bytes(p->dtype);
+  for (int t = 0; t < 2; ++t) {
+    const long long* s = t ? k : q;
+    b[t] = s[0] * e;
+    n[t] = (int)(s[1] * e);
+    h[t] = (int)(s[2] * e);
+  }
+}
 
 QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* wq, const void* wk,
                const uint64_t* freqs, const int* positions, int sms, bool bwd) {
@@ -110,18 +126,18 @@ QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* 
   a.rot = p->rot_dim;
   a.interleaved = p->interleaved != 0;
   a.eps = p->eps;
-  a.x[0] = q;
-  a.x[1] = k;
+  a.x[0] = static_cast<const char*>(q);
+  a.x[1] = static_cast<const char*>(k);
   a.w[0] = wq;
   a.w[1] = wk;
   a.freqs = reinterpret_cast<const unsigned long long*>(freqs);
   a.pos = positions;
   a.pos_stride = p->pos_stride;
-  std::memcpy(a.xs[0], p->q_stride, sizeof(a.xs[0]));
-  std::memcpy(a.xs[1], p->k_stride, sizeof(a.xs[1]));
+  qk_strides(p, p->q_stride, p->k_stride, a.xb, a.xn, a.xh);
   a.divN = FastDiv::of((uint32_t)std::max(p->N, 1));
   a.divH[0] = FastDiv::of((uint32_t)p->Hq);
   a.divH[1] = FastDiv::of((uint32_t)p->Hk);
+  a.divAll = FastDiv::of((uint32_t)(p->Hq + p->Hk));
   // one wave of CTAs, but no more than have a row for each of their row slots
   const long long T = (long long)p->B * p->N, slots = qk_rows_per_pass(p->d);
   const long long least = std::max(1ll, slots / (p->Hq + p->Hk));
@@ -255,10 +271,9 @@ fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, c
   FA_TRY(api_device(&rep, &sms));
   if (p->N == 0) return FA_OK;
   QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms, false);
-  a.y[0] = yq;
-  a.y[1] = yk;
-  std::memcpy(a.ys[0], p->yq_stride, sizeof(a.ys[0]));
-  std::memcpy(a.ys[1], p->yk_stride, sizeof(a.ys[1]));
+  a.y[0] = static_cast<char*>(yq);
+  a.y[1] = static_cast<char*>(yk);
+  qk_strides(p, p->yq_stride, p->yk_stride, a.yb, a.yn, a.yh);
   const cudaError_t e =
       launch_qk_norm_rope(a, p->d, p->dtype, p->weight_dtype == FA_F32, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return api_cuda_fail(e, "norm and rotation launch");
@@ -292,14 +307,12 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* 
   int sms = 0;
   FA_TRY(api_device(&rep, &sms));
   QkArgs a = qk_args(p, q, k, wq, wk, freqs, positions, sms, true);
-  a.y[0] = dq;
-  a.y[1] = dk;
-  a.dy[0] = dyq;
-  a.dy[1] = dyk;
-  std::memcpy(a.ys[0], p->dq_stride, sizeof(a.ys[0]));
-  std::memcpy(a.ys[1], p->dk_stride, sizeof(a.ys[1]));
-  std::memcpy(a.ds[0], p->yq_stride, sizeof(a.ds[0]));
-  std::memcpy(a.ds[1], p->yk_stride, sizeof(a.ds[1]));
+  a.y[0] = static_cast<char*>(dq);
+  a.y[1] = static_cast<char*>(dk);
+  a.dy[0] = static_cast<const char*>(dyq);
+  a.dy[1] = static_cast<const char*>(dyk);
+  qk_strides(p, p->dq_stride, p->dk_stride, a.yb, a.yn, a.yh);
+  qk_strides(p, p->yq_stride, p->yk_stride, a.db, a.dn, a.dh);
   a.part = static_cast<float*>(workspace);
   a.dw[0] = dwq;
   a.dw[1] = dwk;
