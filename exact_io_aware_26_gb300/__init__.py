@@ -16,6 +16,7 @@ import ctypes
 import math
 import os
 import re
+import sys
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +70,9 @@ def use_library(path: str) -> str:
     old = LIB_PATH
     LIB_PATH = path
     _lib = None
+    launch = sys.modules.get(__name__ + "._launch")
+    if launch is not None:  # its plans hold the addresses of the library's functions
+        launch.clear()
     return old
 
 

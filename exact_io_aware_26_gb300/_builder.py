@@ -12,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -25,6 +26,9 @@ SOURCES = ["fa_api.cu", "fwd_tc.cu", "fwd_f32.cu", "bwd_tc.cu", "bwd_aux.cu", "f
            "ops_api.cu", "qk_norm_rope.cu", "kv4.cu", "kv4_attn.cu", "plan.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "bwd_sched.cuh", "fp8.h", "tiles.cuh", "fwd_common.cuh",
            "ops.h", "kv4.cuh"]
+# the short way from Python to the C entry points (a CPython extension; gcc, torch's headers)
+LAUNCH_SOURCE = os.path.join(CSRC, "launch.cpp")
+LAUNCH = os.path.join(HERE, "_launch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -59,12 +63,34 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     return obj
 
 
+def build_launch(force: bool = False) -> str:
+    """Build _launch.so if its source is newer (or if forced); returns its path."""
+    if not force and os.path.exists(LAUNCH) and all(
+            os.path.getmtime(p) <= os.path.getmtime(LAUNCH) for p in (LAUNCH_SOURCE, os.path.abspath(__file__))):
+        return LAUNCH
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = LAUNCH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", cuda, "-o", tmp, LAUNCH_SOURCE, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on launch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LAUNCH)
+    return LAUNCH
+
+
 def build(force: bool = False, extra_flags: list[str] | None = None, verbose: bool = False,
           debug: bool = False) -> str:
     """Build libfa.so (debug: libfa_debug.so, with the kernels' index checks) if any
-    source is newer than it (or if forced); returns its path."""
+    source is newer than it (or if forced), and _launch.so; returns its path."""
     lib, build_dir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
     if not force and up_to_date(lib):
+        build_launch()
         return lib
     os.makedirs(build_dir, exist_ok=True)
     extra = list(extra_flags or [])
@@ -72,8 +98,10 @@ def build(force: bool = False, extra_flags: list[str] | None = None, verbose: bo
         extra += ["-DFA_DEBUG"]
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        launch = ex.submit(build_launch, force)
         objs = list(ex.map(lambda s: _compile(s, extra, build_dir), SOURCES))
+        launch.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

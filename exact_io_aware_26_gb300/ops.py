@@ -24,7 +24,6 @@ as used there.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional
@@ -32,6 +31,11 @@ from typing import Optional
 import torch
 
 from . import FA_BF16, FA_F16, FA_F32, _check, load
+
+try:
+    from . import _launch
+except ImportError as e:
+    raise ImportError("_launch.so is missing or does not load: run exact_io_aware_26_gb300.build() first") from e
 
 KV4_GROUP = 32    # channels that share a (scale, base) pair
 KV4_BLOCK = 16    # tokens of a cache block
@@ -93,24 +97,61 @@ def signatures() -> dict:
     }
 
 
-# ---------------------------------------------------------------- checks
+# ---------------------------------------------------------------- checks and calls
 # A call's checks and its C parameters depend on its arguments' sizes, strides, types and
-# devices alone.  They are done once for each such signature; later calls with the same
-# one look it up (a call on sixteen tokens takes the GPU a few microseconds: the checks
-# would take longer).
+# device alone.  They are done once for each such combination, which is then registered
+# with the extension (csrc/launch.cpp) that repeats the call: a call on sixteen tokens
+# takes the GPU a few microseconds, the checks would take several times that.
 
-_seen: dict = {}
-
-
-def _remember(key, plan):
-    if len(_seen) >= 4096:
-        _seen.clear()
-    _seen[key] = plan
-    return plan
+_QK, _QK_BWD, _APPEND, _GATHER, _ATTENTION, _PLAN = range(6)
+_ENTRY = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attention", "fa_paged_plan")
+_STREAM = (3, 0)
 
 
-def _sig(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+def _in(i: int) -> tuple:
+    return 0, i
+
+
+def _const(value) -> tuple:
+    """A number, or the address of a C struct."""
+    return 2, ctypes.addressof(value) if isinstance(value, ctypes.Structure) else int(value)
+
+
+class _Outputs(list):
+    """The (sizes, dtype) of the tensors that a call allocates."""
+
+    def new(self, sizes, dtype) -> tuple:
+        self.append((tuple(int(n) for n in sizes), dtype))
+        return 1, len(self) - 1
+
+    def given(self, i: int, t, sizes, dtype) -> tuple:
+        """Argument i where it is given, else a new tensor."""
+        return self.new(sizes, dtype) if t is None else _in(i)
+
+
+def _call(op: int, tensors: tuple, scalars: tuple, stream, plan):
+    """Run an entry point: ``plan(*tensors, *scalars)``, once for each combination of sizes,
+    strides, types and scalars, checks them and gives (device, arguments, outputs, results,
+    what to keep alive).  Results and workspaces are allocated on the stream that the
+    kernels run on, and inputs made on another one are marked as used there."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+            for t in tensors:
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+            with torch.cuda.stream(stream):
+                return _call(op, tensors, scalars, None, plan)
+    got = _launch.run(op, tensors, scalars)
+    if got is None:
+        device, args, outputs, results, keep = plan(*tensors, *scalars)
+        entry = ctypes.cast(getattr(load(), _ENTRY[op]), ctypes.c_void_p).value
+        _launch.register(op, tensors, scalars, entry, device.index, args, outputs, results, keep)
+        got = _launch.run(op, tensors, scalars)
+    if type(got) is int:
+        _check(got, _ENTRY[op])
+    return got
 
 
 def _need(t, name: str, dtype, shape=None):
@@ -144,31 +185,20 @@ def _strides(t, name: str, dims) -> tuple:
     return tuple(stride[i] if shape[i] > 1 else 0 for i in dims)
 
 
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _dense(sizes, strides) -> tuple:
+    """Strides of a new tensor, 0 for a dimension of at most one element."""
+    return tuple(st if n > 1 else 0 for st, n in zip(strides, sizes))
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
-_HERE = contextlib.nullcontext()
-
-
-def _enter(device, stream, *inputs):
-    """(stream handle, context to allocate in): results and workspaces belong to the stream
-    that the kernels run on, and inputs made on another one are marked as used there."""
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    current = _raw_stream(device.index)
-    if stream is None:
-        return current, _HERE
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    if stream.cuda_stream == current:
-        return current, _HERE
-    for t in inputs:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+def _workspace(new: _Outputs, i: int, given, nbytes: int, device) -> tuple:
+    """(where the workspace comes from, its bytes); 0 bytes wanted is a refusal of the
+    parameters, which the call itself will put in words."""
+    if given is None:
+        return new.new((max(int(nbytes), 1),), torch.uint8), int(nbytes)
+    _need(given, "workspace", given.dtype)
+    _contiguous(given, "workspace")
+    _one_device(given, torch.empty(0, device=device))
+    return _in(i), given.numel() * given.element_size()
 
 
 # ---------------------------------------------------------------- norms and rotation
@@ -192,8 +222,9 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, inv_freq=None, device="cuda"
 _BNH, _BHN = (0, 1, 2), (0, 2, 1)  # where batch, token and head stand in the two layouts
 
 
-def _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, y, dx):
-    """(C parameters, their address, device, shapes of q and k in the result's layout)."""
+def _qk_checked(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, y, dx, names):
+    """(C parameters, device, shapes in the result's layout) of a call; y: the results or
+    their gradients, dx: the gradients to write, None for one that is still to be made."""
     dt = q.dtype
     if dt not in _CODES:
         raise TypeError(f"unsupported dtype {dt}")
@@ -215,28 +246,41 @@ def _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, y, d
         if N > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous in its last dimension")
     device = _one_device(q, k, wq, wk, freqs, positions, *y, *dx)
-    names = ("dyq", "dyk") if dx else ("out[0]", "out[1]")
     ys, ds, shapes = [], [], []
     for i, h in enumerate((Hq, Hk)):
-        shape = (B, h, N, d) if heads_first else (B, N, h, d)
-        shapes.append(shape)
+        shapes.append((B, h, N, d) if heads_first else (B, N, h, d))
         if y[i] is None:  # a new tensor, contiguous
-            st = (h * N * d, d if heads_first else h * d, N * d if heads_first else d)
-            ys.append(tuple(s if size > 1 else 0 for s, size in zip(st, (B, N, h))))
+            ys.append(_dense((B, N, h), (h * N * d, d, N * d) if heads_first else (h * N * d, h * d, d)))
         else:
-            _need(y[i], names[i], dt, shape)
+            _need(y[i], names[i], dt, shapes[i])
             ys.append(_strides(y[i], names[i], _BHN if heads_first else _BNH))
         if dx and dx[i] is not None:
-            _need(dx[i], "dq" if i == 0 else "dk", dt, (B, N, h, d))
-            ds.append(_strides(dx[i], "dq" if i == 0 else "dk", _BNH))
+            _need(dx[i], names[2 + i], dt, (B, N, h, d))
+            ds.append(_strides(dx[i], names[2 + i], _BNH))
         else:
-            ds.append(tuple(s if size > 1 else 0 for s, size in zip((N * h * d, h * d, d), (B, N, h))))
+            ds.append(_dense((B, N, h), (N * h * d, h * d, d)))
     p = FaQkParams(B, N, Hq, Hk, d, _CODES[dt], _CODES[wt], 2 * freqs.shape[0], int(bool(interleaved)), float(eps),
                    pos_stride, _I64x3(*_strides(q, "q", _BNH)), _I64x3(*_strides(k, "k", _BNH)), _I64x3(*ys[0]),
                    _I64x3(*ys[1]), _I64x3(*ds[0]), _I64x3(*ds[1]))
-    ref = ctypes.byref(p)
-    nbytes = int(load().fa_qk_norm_rope_bwd_workspace_size(ref)) if dx else 0
-    return ref, device, shapes, nbytes
+    return p, device, shapes
+
+
+def _plan_qk(q, k, wq, wk, freqs, positions, yq, yk, eps, interleaved, heads_first):
+    p, device, shapes = _qk_checked(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, (yq, yk), (),
+                                    ("out[0]", "out[1]"))
+    new = _Outputs()
+    res = [new.given(6, yq, shapes[0], q.dtype), new.given(7, yk, shapes[1], q.dtype)]
+    return device, [_const(p), *map(_in, range(6)), *res, _STREAM], new, res, p
+
+
+def _plan_qk_bwd(q, k, dyq, dyk, wq, wk, freqs, positions, dq, dk, workspace, eps, interleaved, heads_first):
+    p, device, shapes = _qk_checked(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, (dyq, dyk), (dq, dk),
+                                    ("dyq", "dyk", "dq", "dk"))
+    new = _Outputs()
+    res = [new.given(8, dq, q.shape, q.dtype), new.given(9, dk, k.shape, q.dtype),
+           new.new((q.shape[3],), torch.float32), new.new((q.shape[3],), torch.float32)]
+    ws, nbytes = _workspace(new, 10, workspace, load().fa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)), device)
+    return device, [_const(p), *map(_in, range(8)), *res, ws, _const(nbytes), _STREAM], new, res, p
 
 
 def qk_norm_rope(q, k, wq, wk, freqs, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -247,18 +291,7 @@ def qk_norm_rope(q, k, wq, wk, freqs, positions=None, eps: float = 1e-6, interle
     [B, N]; None: 0 .. N - 1).  Results are [B, H, N, d] as ``attention_fwd`` takes them,
     or, with ``heads_first`` false, [B, N, H, d]; ``out`` (yq, yk) may be (q, k) there."""
     yq, yk = (None, None) if out is None else out
-    key = ("qk", _sig(q), _sig(k), _sig(wq), _sig(wk), _sig(freqs), _sig(positions), _sig(yq), _sig(yk), eps,
-           interleaved, heads_first)
-    ref, device, shapes, _ = _seen.get(key) or _remember(
-        key, _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, (yq, yk), ()))
-    handle, alloc = _enter(device, stream, q, k, wq, wk, freqs, positions, yq, yk)
-    if out is None:
-        with alloc:
-            yq = torch.empty(shapes[0], dtype=q.dtype, device=device)
-            yk = torch.empty(shapes[1], dtype=q.dtype, device=device)
-    _check(load().fa_qk_norm_rope(ref, q.data_ptr(), k.data_ptr(), wq.data_ptr(), wk.data_ptr(), freqs.data_ptr(),
-                                  _ptr(positions), yq.data_ptr(), yk.data_ptr(), handle), "fa_qk_norm_rope")
-    return yq, yk
+    return _call(_QK, (q, k, wq, wk, freqs, positions, yq, yk), (eps, interleaved, heads_first), stream, _plan_qk)
 
 
 def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -266,32 +299,8 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float =
     """(dq, dk, dwq, dwk): gradients of ``qk_norm_rope`` for dyq, dyk at its results (in its
     layout); q and k are its inputs.  dq, dk are [B, N, H, d] in q's dtype (views of a
     packed gradient may be given), dwq, dwk fp32 [d]."""
-    key = ("qk_bwd", _sig(q), _sig(k), _sig(dyq), _sig(dyk), _sig(wq), _sig(wk), _sig(freqs), _sig(positions),
-           _sig(dq), _sig(dk), _sig(workspace), eps, interleaved, heads_first)
-    plan = _seen.get(key)
-    if plan is None:
-        if workspace is not None:
-            _need(workspace, "workspace", workspace.dtype)
-            _contiguous(workspace, "workspace")
-            _one_device(q, workspace)
-        plan = _remember(key, _plan_qk(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, (dyq, dyk), (dq, dk)))
-    ref, device, _, nbytes = plan
-    handle, alloc = _enter(device, stream, q, k, dyq, dyk, wq, wk, freqs, positions, dq, dk, workspace)
-    d = q.shape[3]
-    with alloc:
-        if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=device)
-        dwq = torch.empty(d, dtype=torch.float32, device=device)
-        dwk = torch.empty(d, dtype=torch.float32, device=device)
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _check(load().fa_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(), dyq.data_ptr(), dyk.data_ptr(), wq.data_ptr(),
-                                      wk.data_ptr(), freqs.data_ptr(), _ptr(positions), dq.data_ptr(), dk.data_ptr(),
-                                      dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle),
-           "fa_qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
+    return _call(_QK_BWD, (q, k, dyq, dyk, wq, wk, freqs, positions, dq, dk, workspace), (eps, interleaved, heads_first),
+                 stream, _plan_qk_bwd)
 
 
 # ---------------------------------------------------------------- the 4-bit cache
@@ -319,7 +328,7 @@ def _cache_params(cache, d: int) -> FaKv4Cache:
     return FaKv4Cache(P, KV4_BLOCK * n, H, d, s[0] if P > 1 else H * n * b)
 
 
-def _plan_rows(cache, slots, k, v, T, H, d, dtype, dims, names):
+def _rows_checked(cache, slots, k, v, T, H, d, dtype, heads_first, names):
     """(cache parameters, row parameters, device)."""
     c = _cache_params(cache, d)
     if cache.shape[1] != H:
@@ -329,30 +338,39 @@ def _plan_rows(cache, slots, k, v, T, H, d, dtype, dims, names):
     strides = []
     for x, name in zip((k, v), names):
         if x is None:  # new and contiguous
-            strides.append(tuple(st if size > 1 else 0 for st, size in zip((H * d, d) if dims == (0, 1) else (d, T * d), (T, H))))
+            strides.append(_dense((T, H), (d, T * d) if heads_first else (H * d, d)))
         else:
-            _need(x, name, dtype, (T, H, d) if dims == (0, 1) else (H, T, d))
-            strides.append(_strides(x, name, dims))
-    device = _one_device(cache, slots, k, v)
+            _need(x, name, dtype, (H, T, d) if heads_first else (T, H, d))
+            strides.append(_strides(x, name, (1, 0) if heads_first else (0, 1)))
     rows = FaKv4Rows(T, _CODES[dtype], _I64x2(*strides[0]), _I64x2(*strides[1]))
-    return ctypes.byref(c), ctypes.byref(rows), device
+    return c, rows, _one_device(cache, slots, k, v)
+
+
+def _plan_append(k, v, slots, cache):
+    if k.dtype not in _CODES:
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    _need(k, "k", k.dtype, (None, None, None))
+    T, H, d = k.shape
+    c, rows, device = _rows_checked(cache, slots, k, v, T, H, d, k.dtype, False, ("k", "v"))
+    return device, [_const(c), _const(rows), *map(_in, range(4)), _STREAM], (), (), (c, rows)
+
+
+def _plan_gather(cache, slots, k, v, d, dtype, heads_first):
+    if dtype not in _CODES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    _need(cache, "cache", torch.uint8, (None, None, None, None))
+    _need(slots, "slots", torch.int32, (None,))
+    T, H = slots.shape[0], cache.shape[1]
+    c, rows, device = _rows_checked(cache, slots, k, v, T, H, d, dtype, heads_first, ("out[0]", "out[1]"))
+    new, shape = _Outputs(), (H, T, d) if heads_first else (T, H, d)
+    res = [new.given(2, k, shape, dtype), new.given(3, v, shape, dtype)]
+    return device, [_const(c), _const(rows), _in(0), _in(1), *res, _STREAM], new, res, (c, rows)
 
 
 def kv4_append(k, v, slots, cache, stream=None) -> None:
     """Quantise the keys and values [T, Hk, d] of T tokens into their slots (int32 [T];
     negative: left out; distinct otherwise) of the cache.  Values saturate at +-16384."""
-    key = ("append", _sig(k), _sig(v), _sig(slots), _sig(cache))
-    plan = _seen.get(key)
-    if plan is None:
-        if k.dtype not in _CODES:
-            raise TypeError(f"unsupported dtype {k.dtype}")
-        _need(k, "k", k.dtype, (None, None, None))
-        T, H, d = k.shape
-        plan = _remember(key, _plan_rows(cache, slots, k, v, T, H, d, k.dtype, (0, 1), ("k", "v")))
-    c, rows, device = plan
-    handle, _ = _enter(device, stream, k, v, slots, cache)
-    _check(load().fa_kv4_append(c, rows, k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr(), handle),
-           "fa_kv4_append")
+    _call(_APPEND, (k, v, slots, cache), (), stream, _plan_append)
 
 
 def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = False, out=None, stream=None):
@@ -360,30 +378,10 @@ def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = F
     ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d] (with a leading batch of one,
     as ``attention_fwd`` takes them)."""
     k, v = (None, None) if out is None else out
-    key = ("gather", _sig(cache), _sig(slots), d, dtype, heads_first, _sig(k), _sig(v))
-    plan = _seen.get(key)
-    if plan is None:
-        if dtype not in _CODES:
-            raise TypeError(f"unsupported dtype {dtype}")
-        _need(cache, "cache", torch.uint8, (None, None, None, None))
-        _need(slots, "slots", torch.int32, (None,))
-        plan = _remember(key, _plan_rows(cache, slots, k, v, slots.shape[0], cache.shape[1], d, dtype,
-                                         (1, 0) if heads_first else (0, 1), ("out[0]", "out[1]")))
-    c, rows, device = plan
-    handle, alloc = _enter(device, stream, slots, cache, k, v)
-    if out is None:
-        T, H = slots.shape[0], cache.shape[1]
-        shape = (H, T, d) if heads_first else (T, H, d)
-        with alloc:
-            k = torch.empty(shape, dtype=dtype, device=device)
-            v = torch.empty(shape, dtype=dtype, device=device)
-    _check(load().fa_kv4_gather(c, rows, cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), handle),
-           "fa_kv4_gather")
-    return k, v
+    return _call(_GATHER, (cache, slots, k, v), (d, dtype, heads_first), stream, _plan_gather)
 
 
-def _plan_attention(q, cache, block_table, kv_lens, cu_q, max_q_len, scale, window, out, lse, workspace):
-    """(cache parameters, parameters, workspace bytes, device)."""
+def _plan_attention(q, cache, block_table, kv_lens, cu_q, out, lse, workspace, max_q_len, scale, window):
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be fp16 or bf16, not {q.dtype}")
     _need(q, "q", q.dtype, (None, None, None))
@@ -400,22 +398,21 @@ def _plan_attention(q, cache, block_table, kv_lens, cu_q, max_q_len, scale, wind
         _contiguous(cu_q, "cu_q")
     elif T < R:
         raise ValueError(f"q has {T} rows for {R} requests")
-    o_stride = tuple(st if size > 1 else 0 for st, size in zip((Hq * d, d), (T, Hq)))
+    o_stride = _dense((T, Hq), (Hq * d, d))
     if out is not None:
         _need(out, "out", q.dtype, (T, Hq, d))
         o_stride = _strides(out, "out", (0, 1))
     if lse is not None:
         _need(lse, "lse", torch.float32, (T, Hq))
         _contiguous(lse, "lse")
-    if workspace is not None:
-        _need(workspace, "workspace", workspace.dtype)
-        _contiguous(workspace, "workspace")
-    device = _one_device(q, cache, block_table, kv_lens, cu_q, out, lse, workspace)
+    device = _one_device(q, cache, block_table, kv_lens, cu_q, out, lse)
     p = FaKv4AttnParams(R, T, Hq, _CODES[q.dtype], int(max_q_len), int(window), width,
                         1.0 / math.sqrt(d) if scale is None else float(scale),
                         block_table.stride(0) if R > 1 else width, _I64x2(*_strides(q, "q", (0, 1))), _I64x2(*o_stride))
-    cref, ref = ctypes.byref(c), ctypes.byref(p)
-    return cref, ref, int(load().fa_kv4_attention_workspace_size(cref, ref)), device
+    new = _Outputs()
+    res = [new.given(5, out, (T, Hq, d), q.dtype), new.given(6, lse, (T, Hq), torch.float32)]
+    ws, nbytes = _workspace(new, 7, workspace, load().fa_kv4_attention_workspace_size(ctypes.byref(c), ctypes.byref(p)), device)
+    return device, [_const(c), _const(p), *map(_in, range(5)), *res, ws, _const(nbytes), _STREAM], new, res, (c, p)
 
 
 def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1, scale: Optional[float] = None,
@@ -427,22 +424,8 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1,
     only the last ``window`` of those.  Rows without a token to see: o = 0, lse = -inf;
     rows outside every request are not written.  ``max_q_len``: the most rows of a request,
     a hint.  Lengths stay on the GPU: the call does not synchronise."""
-    key = ("attention", _sig(q), _sig(cache), _sig(block_table), _sig(kv_lens), _sig(cu_q), max_q_len, scale, window,
-           _sig(out), _sig(lse), _sig(workspace))
-    c, p, nbytes, device = _seen.get(key) or _remember(
-        key, _plan_attention(q, cache, block_table, kv_lens, cu_q, max_q_len, scale, window, out, lse, workspace))
-    handle, alloc = _enter(device, stream, q, cache, block_table, kv_lens, cu_q, out, lse, workspace)
-    with alloc:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device)
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _check(load().fa_kv4_attention(c, p, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-                                   _ptr(cu_q), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                   handle), "fa_kv4_attention")
-    return out, lse
+    return _call(_ATTENTION, (q, cache, block_table, kv_lens, cu_q, out, lse, workspace), (max_q_len, scale, window),
+                 stream, _plan_attention)
 
 
 # ---------------------------------------------------------------- block tables and slot maps
@@ -450,8 +433,8 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1,
 _PLAN_OUT = ("kv_lens", "cu_q", "positions", "slots", "counts")
 
 
-def _plan_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size, T, out):
-    """(parameters, sizes of the results, device)."""
+def _plan_plan(seq_lens, new_lens, block_table, free_pages, free_count, kv_lens, cu_q, positions, slots, counts,
+               page_size, T):
     i32 = torch.int32
     _need(block_table, "block_table", i32, (None, None))
     R, width = block_table.shape
@@ -463,14 +446,17 @@ def _plan_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_siz
         _contiguous(t, name)
     if free_count.shape[0] < 1:
         raise ValueError("free_count is empty")
-    sizes = [R, R + 1, int(T), int(T), 3]
-    if out is not None:
-        for name, n in zip(_PLAN_OUT, sizes):
-            _need(out[name], f"out[{name!r}]", i32, (n,))
-            _contiguous(out[name], f"out[{name!r}]")
-    device = _one_device(seq_lens, new_lens, block_table, free_pages, free_count, *(out[n] for n in _PLAN_OUT if out))
+    if T < 0:
+        raise ValueError("T is negative")
+    given, new, res = (kv_lens, cu_q, positions, slots, counts), _Outputs(), []
+    for i, (t, name, n) in enumerate(zip(given, _PLAN_OUT, (R, R + 1, int(T), int(T), 3))):
+        if t is not None:
+            _need(t, f"out[{name!r}]", i32, (n,))
+            _contiguous(t, f"out[{name!r}]")
+        res.append(new.given(5 + i, t, (n,), i32))
+    device = _one_device(seq_lens, new_lens, block_table, free_pages, free_count, *given)
     p = FaPlanParams(R, int(T), int(page_size), free_pages.shape[0], width, block_table.stride(0) if R > 1 else width)
-    return ctypes.byref(p), sizes, device
+    return device, [_const(p), *map(_in, range(5)), *res, _STREAM], new, res, p
 
 
 def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size: int, T: int, out=None, stream=None):
@@ -482,18 +468,6 @@ def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_siz
     tokens, pages missing).  A request whose pages are not there keeps its length and gets
     slots of -1.  out["kv_lens"] may be seq_lens, and out["counts"] the tensor whose first
     element is free_count."""
-    given = () if out is None else tuple(out[name] for name in _PLAN_OUT)
-    key = ("plan", _sig(seq_lens), _sig(new_lens), _sig(block_table), _sig(free_pages), _sig(free_count), page_size, T,
-           *map(_sig, given))
-    p, sizes, device = _seen.get(key) or _remember(
-        key, _plan_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size, T, out))
-    handle, alloc = _enter(device, stream, seq_lens, new_lens, block_table, free_pages, free_count, *given)
-    if out is None:
-        with alloc:
-            given = [torch.empty(n, dtype=torch.int32, device=device) for n in sizes]
-        out = dict(zip(_PLAN_OUT, given))
-    kv, cu, pos, slots, counts = given
-    _check(load().fa_paged_plan(p, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                                free_pages.data_ptr(), free_count.data_ptr(), kv.data_ptr(), cu.data_ptr(),
-                                pos.data_ptr(), slots.data_ptr(), counts.data_ptr(), handle), "fa_paged_plan")
-    return out
+    given = (None,) * 5 if out is None else tuple(out[name] for name in _PLAN_OUT)
+    got = _call(_PLAN, (seq_lens, new_lens, block_table, free_pages, free_count, *given), (page_size, T), stream, _plan_plan)
+    return dict(zip(_PLAN_OUT, got))
