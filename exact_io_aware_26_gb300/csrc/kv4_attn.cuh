@@ -1,4 +1,4 @@
-// kv4_attn.cu -- attention of each request's newest tokens over its 4-bit cache.
+// kv4_attn.cuh -- attention of each request's newest tokens over its 4-bit cache.
 //
 // Bound: HBM.  A token of one head is 160 bytes (d = 128) for both its key and its
 // value, and 8 query rows need 4 * 8 * d FLOPs of it: 26 FLOPs a byte, far below
@@ -26,13 +26,18 @@
 // score of the block is above it by more than 2^8 (one vote); then it is reduced by
 // shuffles and O and l are rescaled.  l is kept per lane and reduced at the end.
 //
-// Work.  All tiles (request, 8 NT query rows, key head) lie one after the other as units
-// of 32 tokens; each CTA takes an equal share of all units, wherever it begins and ends,
-// so that ragged lengths leave no SM idle.  A tile inside one share is finished there;
-// one that is cut leaves fp32 (O, m, l) per share, which the second kernel adds (launched
-// with the first, it waits for it on the GPU).  Within a CTA the warps take the units of a
-// tile in turn, each with its own ring of bulk copies and its own m, l, O, joined in
-// shared memory at the tile's end.
+// Work.  A tile is a request's 8 NT query rows of one key head; its tokens are taken in
+// units of 32.  Within a CTA the warps take the units in turn, each with its own ring of
+// bulk copies and its own m, l, O, joined in shared memory at the end.  Across CTAs there
+// are two ways:
+//   - shares: all tiles lie one after the other, and each CTA takes an equal share of all
+//     units, wherever it begins and ends, so that ragged lengths leave no SM idle.  A tile
+//     that is cut leaves fp32 (O, m, l) per share, which a second kernel adds (launched with
+//     the first, it waits for it on the GPU).
+//   - clusters, for few tiles of few units: the CTAs of a cluster divide a tile evenly and
+//     join through distributed shared memory; one launch, nothing in device memory.
+// kv4_way chooses, by the number of tiles and the units a warp would take.
+#pragma once
 #include "kv4.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -40,26 +45,25 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;     // running maximum before any token is seen
 constexpr int kUnit = 2 * kKvBlock;  // tokens a warp takes at a time
-constexpr int kMinShare = kWarps;    // units: shares are not cut finer (one per warp)
 constexpr int kReqCache = 128;       // requests whose lengths a CTA keeps at hand
 
-template <int D, int NT>
+// CL: the CTAs are a cluster's.
+template <int D, int NT, bool CL>
 struct Cfg {
   using Blk = KvBlock<D>;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int CTAS_PER_SM = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int WARPS = CL ? 8 : 4, THREADS = 32 * WARPS;
+  static constexpr int CTAS_PER_SM = CL ? (NT == 1 ? 2 : 1) : NT == 1 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int LDO = D + 4;  // row pitch of the joined O, in floats
   static constexpr int stage = 2 * Blk::bytes;
-  // For the join each warp's O goes into its ring.  Eight rows take the stage of the tile's
-  // last unit, and the copies of the next tile go on in the others; more rows take the whole
-  // ring, which then holds one tile at a time.
-  static constexpr bool across = NT == 1;
+  // For the join each warp's O goes into its ring.  Eight rows of a share take the stage of the
+  // tile's last unit, and the copies of the next tile go on in the others; otherwise it is
+  // the whole ring, which then holds one tile at a time.
+  static constexpr bool across = NT == 1 && !CL;
   static constexpr int STAGES = D == 64 || NT == 4 ? 4 : 2;
-  static constexpr int ring = kWarps * STAGES * stage;
+  static constexpr int ring = WARPS * STAGES * stage;
   static_assert(ROWS * LDO * 4 <= (across ? stage : STAGES * stage), "a warp's O fits");
   static constexpr int qfrag = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int smem = ring + qfrag;
@@ -216,7 +220,7 @@ struct Feed {
 
 // Fills src with the warp's next units of the share, at most 32, all of one tile; returns
 // how many (0: none left).
-template <int D, int ROWS>
+template <int D, int ROWS, int kWarps>
 __device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, const Req* reqs, int reqs_r0, int warp,
                                         long long u1) {
   using Blk = KvBlock<D>;
@@ -268,97 +272,108 @@ __device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, con
   return n;
 }
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_kernel(const Kv4AttnArgs a) {
-  using C = Cfg<D, NT>;
+template <int D, int NT, bool F16, bool CL>
+__global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_PER_SM) kv4_attn_kernel(const Kv4AttnArgs a) {
+  using C = Cfg<D, NT, CL>;
   using Blk = KvBlock<D>;
+  constexpr int kWarps = C::WARPS, kThreads = C::THREADS;
   constexpr int ROWS = C::ROWS, S = C::STAGES, KS = D / 16, MT = D / 16, WPT = D / 32 /* words per lane of K */;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][S];
-  __shared__ long long warp_units[kWarps];
+  __shared__ long long warp_sums[kWarps];
   __shared__ Req reqs[kReqCache];
   __shared__ long long start_u;
   __shared__ int start_r, start_t, start_h;
   __shared__ float m_s[kWarps][ROWS], l_s[kWarps][ROWS];
+  __shared__ __align__(16) float2 ml_s[CL ? ROWS : 1];  // of the CTA, for the cluster
   __shared__ int held_s[kWarps];
   __shared__ float up_s[NT == 4 ? ROWS : 1];
-  static_assert(NT != 4 || kWarps == 4, "a warp for every eight rows");
+  static_assert(NT != 4 || kWarps >= 4, "a warp for every eight rows");
   __shared__ volatile int abort_s;
   __shared__ Feed<ROWS> feed_s[kWarps];
   __shared__ Walk<ROWS> tile_s[2];  // the current tile; the next one
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
+  if constexpr (!CL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * (S * C::stage);
   const uint32_t bar0 = smem_addr(&bars[warp][0]);
   uint2* qfrag = reinterpret_cast<uint2*>(smem + C::ring);
   (void)qfrag;
 
-  // ---- shares: prefix sums of the units of all requests
+  // ---- prefix sums over all requests, of their units or (CL) their tiles
   if (tid == 0) abort_s = 0;
   if (lane == 0)
     for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
   fence_barrier_init();
   const int per = (a.R + kThreads - 1) / kThreads;
   const int my0 = min(a.R, tid * per), my1 = min(a.R, my0 + per);
-  auto units_of = [&](const Req& x) {
+  auto count_of = [&](const Req& x) {
     const int nt = tiles_of<ROWS>(a, x);
-    long long n = 0;
-    for (int t = 0; t < nt; ++t) n += tile_of<ROWS>(a, x, t).n_u;
+    long long n = nt;
+    if constexpr (!CL) {
+      n = 0;
+      for (int t = 0; t < nt; ++t) n += tile_of<ROWS>(a, x, t).n_u;
+    }
     return n * a.c.Hk;
   };
-  long long units = 0;
+  const bool cached = a.R <= min(kThreads, kReqCache);  // every request's lengths are at hand
+  long long mine = 0;
   for (int r = my0; r < my1; ++r) {
     const Req x = load_req(a, r);
-    if (per == 1) reqs[tid] = x;
-    units += units_of(x);
+    if (cached) reqs[r] = x;
+    mine += count_of(x);
   }
-  long long end = units;
+  long long end = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const long long up = __shfl_up_sync(0xffffffffu, end, off);
     if (lane >= off) end += up;
   }
-  if (lane == 31) warp_units[warp] = end;
+  if (lane == 31) warp_sums[warp] = end;
   __syncthreads();
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) end += warp_units[w];
-    total += warp_units[w];
+    if (w < warp) end += warp_sums[w];
+    total += warp_sums[w];
   }
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
-  const long long u0 = (long long)blockIdx.x * share, u1 = min(total, u0 + share);
-  if (u0 >= total) {  // no share (the CTA's threads all leave)
-    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  // the thread whose requests hold unit u0 finds its tile
-  if (u0 < end && u0 >= end - units) {
-    long long u = end - units;
-    bool found = false;
-    for (int r = my0; r < my1 && !found; ++r) {
-      const Req x = per == 1 ? reqs[tid] : load_req(a, r);
-      const int nt = tiles_of<ROWS>(a, x);
-      for (int t = 0; t < nt && !found; ++t) {
-        const long long n = tile_of<ROWS>(a, x, t).n_u;
-        if (u0 < u + n * a.c.Hk) {
-          const int h = (int)((u0 - u) / n);
-          start_r = r;
-          start_t = t;
-          start_h = h;
-          start_u = u + h * n;  // first unit of the tile
-          found = true;
-        } else {
-          u += n * a.c.Hk;
+  // shares: this CTA's units [u0, u1)
+  long long share = 0, u0 = 0, u1 = 0;
+  if constexpr (!CL) {
+    share = (total + gridDim.x - 1) / gridDim.x;
+    share = (share + kWarps - 1) / kWarps * kWarps;  // at least a unit for each warp
+    u0 = (long long)blockIdx.x * share;
+    u1 = min(total, u0 + share);
+    if (u0 >= total) {  // no share (the CTA's threads all leave)
+      if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    // the thread whose requests hold unit u0 finds its tile
+    if (u0 < end && u0 >= end - mine) {
+      long long u = end - mine;
+      bool found = false;
+      for (int r = my0; r < my1 && !found; ++r) {
+        const Req x = cached ? reqs[r] : load_req(a, r);
+        const int nt = tiles_of<ROWS>(a, x);
+        for (int t = 0; t < nt && !found; ++t) {
+          const long long n = tile_of<ROWS>(a, x, t).n_u;
+          if (u0 < u + n * a.c.Hk) {
+            const int h = (int)((u0 - u) / n);
+            start_r = r;
+            start_t = t;
+            start_h = h;
+            start_u = u + h * n;  // first unit of the tile
+            found = true;
+          } else {
+            u += n * a.c.Hk;
+          }
         }
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
-  const int cache_r0 = per == 1 ? 0 : start_r;
-  if (per > 1) {
+  const int cache_r0 = CL || cached ? 0 : start_r;
+  if (!CL && !cached) {
     for (int i = tid; i < kReqCache; i += kThreads)
       if (cache_r0 + i < a.R) reqs[i] = load_req(a, cache_r0 + i);
     __syncthreads();
@@ -368,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
   const WaitCtx wc{&abort_s, a.rep.st, a.rep.epoch, a.rep.wait_ns};
 
   Feed<ROWS>& feed = feed_s[warp];
-  if (lane == 0) {
+  if (!CL && lane == 0) {
     feed.w.at(a, reqs, cache_r0, start_r, start_t, start_h);
     feed.tile0 = start_u;
     feed.u = (int)(u0 - start_u) + warp;
@@ -379,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
   int turn = 0, ready = 0;  // of feed.src
   auto produce = [&](int stage) {  // the copies of this warp's next unit, if any is left
     if (turn == ready) {
-      ready = feed_refill<D, ROWS>(a, feed, reqs, cache_r0, warp, u1);
+      ready = feed_refill<D, ROWS, kWarps>(a, feed, reqs, cache_r0, warp, u1);
       turn = 0;
       if (ready == 0) return;
     }
@@ -405,22 +420,68 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
     for (int s = 0; s < S; ++s) produce(s);
   __syncthreads();  // tile_s
 
-  // ---- the share's tiles
+  // ---- the tiles of the share, or of the cluster
   int stage = 0;
   uint32_t parity = 0;
   int4 meta = make_int4(-1, 0, 0, 0);
   int meta_q0 = 0;
-  long long tile0 = start_u;
+  long long tile0 = CL ? 0 : start_u;
+  uint32_t rank = 0, ctas = 1;
+  long long index = 0;
+  if constexpr (CL) {
+    rank = cluster_rank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    index = blockIdx.x / ctas;
+  }
 #pragma unroll 1
-  for (int which = 0; tile0 < u1; which ^= 1) {
+  for (int which = 0; CL ? index < total : tile0 < u1; which ^= (CL ? 0 : 1)) {
+    if constexpr (CL) {
+      if (index < end && index >= end - mine) {
+        long long u = end - mine;
+        bool found = false;
+        for (int r = my0; r < my1 && !found; ++r) {
+          const Req x = cached ? reqs[r] : load_req(a, r);
+          const long long n = count_of(x);
+          if (index < u + n) {
+            Walk<ROWS> w;
+            w.r = r;
+            w.t = (int)((uint32_t)(index - u) / (uint32_t)a.c.Hk);
+            w.h = (int)((uint32_t)(index - u) - (uint32_t)w.t * (uint32_t)a.c.Hk);
+            w.x = x;
+            w.y = tile_of<ROWS>(a, x, w.t);
+            tile_s[0] = w;
+            found = true;
+          }
+          u += n;
+        }
+      }
+      __syncthreads();
+    }
     const Walk<ROWS>& cw = tile_s[which];
     const Tile y = cw.y;
     const Req x = cw.x;
-    const int first = (int)max(0ll, u0 - tile0), last = (int)min((long long)y.n_u, u1 - tile0);
-    if constexpr (!C::across) {
-      fence_async_smem();  // the join's stores before the copies that reuse the ring
-      for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((stage + s) % S);
+    int first, last;
+    bool alone = true;  // CL: the whole tile is this CTA's
+    if constexpr (CL) {
+      int part = (y.n_u + (int)ctas - 1) / (int)ctas;
+      part = (part + kWarps - 1) / kWarps * kWarps;
+      first = min(y.n_u, (int)rank * part);
+      last = min(y.n_u, first + part);
+      alone = part >= y.n_u;
+      if (lane == 0) {
+        feed.w = cw;
+        feed.tile0 = 0;
+        feed.u = first + warp;
+        feed.end = last;
+        feed.ids_r = -1;
+      }
+      turn = ready = 0;
+    } else {
+      first = (int)max(0ll, u0 - tile0);
+      last = (int)min((long long)y.n_u, u1 - tile0);
     }
+    if constexpr (!C::across)
+      for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((stage + s) % S);
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
     // which its score factor takes back: no 16-bit query leaves fp16's range.
@@ -430,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
 #pragma unroll
     for (int jj = 0; jj < (NT == 4 ? 1 : NT); ++jj) {
       const int j = NT == 4 ? warp : jj;
+      if (NT == 4 && warp >= 4) break;
       const int n = g + 8 * j;
       uint4 raw[D / 32];
 #pragma unroll
@@ -732,70 +794,126 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS_PER_SM) kv4_attn_ke
           }
         }
       }
+      fence_async_smem();  // these stores before the copies that reuse the ring
     }
     __syncthreads();
-    const bool from_before = first > 0, goes_on = tile0 + y.n_u > u1;
     constexpr int TPR = D / 8;  // threads per row, 8 channels each
-    for (int e = tid; e < ROWS * TPR; e += kThreads) {
-      const int row = e / TPR, ch = (e % TPR) * 8;
-      if (row >= y.rows) continue;
-      float top = m_s[0][row];
-      for (int w = 1; w < active; ++w) top = fmaxf(top, m_s[w][row]);
-      float sum = 0.f, acc[8] = {};
+    // adds weight f's (l, O[8 channels])
+    auto add8 = [](float f, float l, const float4& u, const float4& v, float& sum, float (&acc)[8]) {
+      sum = fmaf(f, l, sum);
+      acc[0] = fmaf(f, u.x, acc[0]); acc[1] = fmaf(f, u.y, acc[1]);
+      acc[2] = fmaf(f, u.z, acc[2]); acc[3] = fmaf(f, u.w, acc[3]);
+      acc[4] = fmaf(f, v.x, acc[4]); acc[5] = fmaf(f, v.y, acc[5]);
+      acc[6] = fmaf(f, v.z, acc[6]); acc[7] = fmaf(f, v.w, acc[7]);
+    };
+    // the warps' sum at (row, channels ch .. ch + 7)
+    auto join = [&](int row, int ch, float& top, float& sum, float (&acc)[8]) {
+      top = kNoMax;
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+      for (int w = 0; w < active; ++w) top = fmaxf(top, m_s[w][row]);
       for (int w = 0; w < active; ++w) {
-        const float f = ex2(m_s[w][row] - top);
-        sum = fmaf(f, l_s[w][row], sum);
-        const float4* src = reinterpret_cast<const float4*>(
-            joined(w) + row * C::LDO + ch);
-        const float4 u = src[0], v = src[1];
-        acc[0] = fmaf(f, u.x, acc[0]); acc[1] = fmaf(f, u.y, acc[1]);
-        acc[2] = fmaf(f, u.z, acc[2]); acc[3] = fmaf(f, u.w, acc[3]);
-        acc[4] = fmaf(f, v.x, acc[4]); acc[5] = fmaf(f, v.y, acc[5]);
-        acc[6] = fmaf(f, v.z, acc[6]); acc[7] = fmaf(f, v.w, acc[7]);
+        const float4* src = reinterpret_cast<const float4*>(joined(w) + row * C::LDO + ch);
+        add8(ex2(m_s[w][row] - top), l_s[w][row], src[0], src[1], sum, acc);
       }
-      if (from_before || goes_on) {
-        float* to = a.part + ((size_t)(2 * blockIdx.x + (from_before ? 0 : 1)) * ROWS + row) * (D + 4);
-        *reinterpret_cast<float4*>(to + 4 + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        *reinterpret_cast<float4*>(to + 8 + ch) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        if (ch == 0) {
-          to[0] = top;
-          to[1] = sum;
-        }
+    };
+    auto write = [&](int row, int ch, float top, float sum, const float (&acc)[8]) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int gr = y.row0 + row, qi = a.G.div(gr);
+      const long long head = (long long)cw.h * a.G.d + (gr - qi * (int)a.G.d);
+      uint16_t* to = static_cast<uint16_t*>(a.o) + (x.q0 + qi) * a.os[0] + head * a.os[1] + ch;
+      if (fa_bounds(a.rep.st, x.q0 + qi < a.T && head < a.Hq)) {
+        *reinterpret_cast<uint4*>(to) =
+            make_uint4(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv),
+                       pack2<F16>(acc[4] * inv, acc[5] * inv), pack2<F16>(acc[6] * inv, acc[7] * inv));
+        if (ch == 0 && a.lse)
+          a.lse[(long long)(x.q0 + qi) * a.Hq + head] =
+              sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      }
+    };
+    if constexpr (CL) {
+      constexpr int ITEMS = (ROWS * TPR + kThreads - 1) / kThreads;
+      if (alone) {  // the first CTA's
+        if (rank == 0)
+          for (int e = tid; e < y.rows * TPR; e += kThreads) {
+            float top, sum, acc[8];
+            join(e / TPR, e % TPR * 8, top, sum, acc);
+            write(e / TPR, e % TPR * 8, top, sum, acc);
+          }
+        __syncthreads();  // joined, m_s, l_s, tile_s read
       } else {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int gr = y.row0 + row, qi = a.G.div(gr);
-        const long long head = (long long)cw.h * a.G.d + (gr - qi * (int)a.G.d);
-        uint16_t* to = static_cast<uint16_t*>(a.o) + (x.q0 + qi) * a.os[0] + head * a.os[1] + ch;
-        if (fa_bounds(a.rep.st, x.q0 + qi < a.T && head < a.Hq)) {
-          *reinterpret_cast<uint4*>(to) =
-              make_uint4(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv),
-                         pack2<F16>(acc[4] * inv, acc[5] * inv), pack2<F16>(acc[6] * inv, acc[7] * inv));
-          if (ch == 0 && a.lse)
-            a.lse[(long long)(x.q0 + qi) * a.Hq + head] =
-                sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        float top[ITEMS], sum[ITEMS], acc[ITEMS][8];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int e = tid + i * kThreads;
+          if (e < y.rows * TPR) join(e / TPR, e % TPR * 8, top[i], sum[i], acc[i]);
+        }
+        __syncthreads();  // joined read: the CTA's sum takes its place
+        float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int e = tid + i * kThreads, row = e / TPR, ch = e % TPR * 8;
+          if (e < y.rows * TPR) {
+            *reinterpret_cast<float4*>(red + row * C::LDO + ch) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            *reinterpret_cast<float4*>(red + row * C::LDO + ch + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+            if (ch == 0) ml_s[row] = make_float2(top[i], sum[i]);
+          }
+        }
+        fence_async_smem();
+        cluster_sync();
+        // the cluster's sum, its items spread over the CTAs
+        for (int e = (int)rank * kThreads + tid; e < y.rows * TPR; e += (int)ctas * kThreads) {
+          const int row = e / TPR, ch = e % TPR * 8;
+          float t = kNoMax, l = 0.f, v[8] = {};
+          const uint32_t ml = smem_addr(&ml_s[row]), at = smem_addr(red + row * C::LDO + ch);
+          for (uint32_t c = 0; c < ctas; ++c) t = fmaxf(t, ld_cluster_f32x2(cluster_map(ml, c)).x);
+          for (uint32_t c = 0; c < ctas; ++c) {
+            const float2 p = ld_cluster_f32x2(cluster_map(ml, c));
+            const uint32_t from = cluster_map(at, c);
+            add8(ex2(p.x - t), p.y, ld_cluster_f32x4(from), ld_cluster_f32x4(from + 16), l, v);
+          }
+          write(row, ch, t, l, v);
+        }
+        cluster_sync();  // the CTAs' sums read
+      }
+      index += gridDim.x / ctas;
+    } else {
+      const bool from_before = first > 0, goes_on = tile0 + y.n_u > u1;
+      for (int e = tid; e < y.rows * TPR; e += kThreads) {
+        const int row = e / TPR, ch = (e % TPR) * 8;
+        float top, sum, acc[8];
+        join(row, ch, top, sum, acc);
+        if (from_before || goes_on) {
+          float* to = a.part + ((size_t)(2 * blockIdx.x + (from_before ? 0 : 1)) * ROWS + row) * (D + 4);
+          *reinterpret_cast<float4*>(to + 4 + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          *reinterpret_cast<float4*>(to + 8 + ch) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+          if (ch == 0) {
+            to[0] = top;
+            to[1] = sum;
+          }
+        } else {
+          write(row, ch, top, sum, acc);
         }
       }
-    }
-    if (tid == 0) {
-      const long long tile_end = tile0 + y.n_u;
-      if (goes_on && !from_before) {
-        meta = make_int4(y.row0, y.rows, cw.h, (int)((tile_end - 1) / share));
-        meta_q0 = x.q0;
+      if (tid == 0) {
+        const long long tile_end = tile0 + y.n_u;
+        if (goes_on && !from_before) {
+          meta = make_int4(y.row0, y.rows, cw.h, (int)((tile_end - 1) / share));
+          meta_q0 = x.q0;
+        }
+        if (tile_end < u1) {
+          Walk<ROWS> w = cw;
+          w.next(a, reqs, cache_r0);
+          tile_s[which ^ 1] = w;
+        }
       }
-      if (tile_end < u1) {
-        Walk<ROWS> w = cw;
-        w.next(a, reqs, cache_r0);
-        tile_s[which ^ 1] = w;
-      }
+      __syncthreads();  // joined, m_s, l_s read; the next tile known
     }
-    __syncthreads();  // joined, m_s, l_s read; the next tile known
-    if (C::across && held >= 0) {
-      fence_async_smem();  // the join's stores before the copy that reuses the stage
-      produce(held);
-    }
+    if (C::across && held >= 0) produce(held);
     tile0 += y.n_u;
   }
-  if (tid == 0) {
+  if (!CL && tid == 0) {
     a.meta[2 * blockIdx.x] = meta;
     a.meta[2 * blockIdx.x + 1] = make_int4(meta_q0, 0, 0, 0);
   }
@@ -877,45 +995,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
     a.lse[(long long)(q0 + qi) * a.Hq + head] = total == 0.f ? -INFINITY : (best + log2f(total)) * 0.6931471805599453f;
 }
 
+// ctas: of the launch; cluster: CTAs of a cluster, or 0 for shares.
 template <int D, int NT, bool F16>
-cudaError_t launch(const Kv4AttnArgs& a, int ctas, cudaStream_t s) {
-  using C = Cfg<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-  if (e != cudaSuccess) return e;
-  kv4_attn_kernel<D, NT, F16><<<ctas, kThreads, C::smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) {
+  using C = Cfg<D, NT, false>;
+  using CC = Cfg<D, NT, true>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, NT);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  cfg.stream = s;
+  cudaError_t e;
+  if (cluster > 0) {
+    const auto k = kv4_attn_kernel<D, NT, F16, true>;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CC::smem)) != cudaSuccess) return e;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(CC::THREADS);
+    cfg.dynamicSmemBytes = CC::smem;
+    return cudaLaunchKernelEx(&cfg, k, a);
+  }
+  const auto k = kv4_attn_kernel<D, NT, F16, false>;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem)) != cudaSuccess) return e;
+  k<<<ctas, C::THREADS, C::smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(ctas, NT);
+  cfg.blockDim = dim3(32 * kMergeWarps);
   return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16>, a);
-}
-
-template <int D, bool F16>
-cudaError_t launch_rows(const Kv4AttnArgs& a, int rows, int ctas, cudaStream_t s) {
-  return rows == 8 ? launch<D, 1, F16>(a, ctas, s) : rows == 16 ? launch<D, 2, F16>(a, ctas, s) : launch<D, 4, F16>(a, ctas, s);
 }
 
 }  // namespace
 
-int kv4_tile_rows(int G, int max_q_len) {
-  const long long rows = (long long)G * max_q_len;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-}
-
-int kv4_max_ctas(int d, int rows, int sms) {
-  (void)d;
-  return sms * (rows == 8 ? Cfg<128, 1>::CTAS_PER_SM : rows == 16 ? Cfg<128, 2>::CTAS_PER_SM : Cfg<128, 4>::CTAS_PER_SM);
-}
-
-cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int d, bool f16, int rows, int ctas, cudaStream_t s) {
-  if (d == 64) return f16 ? launch_rows<64, true>(a, rows, ctas, s) : launch_rows<64, false>(a, rows, ctas, s);
-  return f16 ? launch_rows<128, true>(a, rows, ctas, s) : launch_rows<128, false>(a, rows, ctas, s);
+template <int D>
+cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s) {
+  if (f16)
+    return rows == 8    ? launch<D, 1, true>(a, ctas, cluster, s)
+           : rows == 16 ? launch<D, 2, true>(a, ctas, cluster, s)
+                        : launch<D, 4, true>(a, ctas, cluster, s);
+  return rows == 8    ? launch<D, 1, false>(a, ctas, cluster, s)
+         : rows == 16 ? launch<D, 2, false>(a, ctas, cluster, s)
+                      : launch<D, 4, false>(a, ctas, cluster, s);
 }
 
 }  // namespace fa

@@ -82,10 +82,15 @@ struct Kv4AttnArgs {
   int4* meta;       // two per CTA: the tile that starts in its share and goes on
   Report rep;
 };
-// Rows of a query tile: 8, 16 or 32 (see kv4_attn.cu), and the most CTAs a launch has.
-int kv4_tile_rows(int G, int max_q_len);
-int kv4_max_ctas(int d, int rows, int sms);
-cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int d, bool f16, int rows, int ctas, cudaStream_t s);
+// Rows of a query tile: 8, 16 or 32 (kv4_attn.cuh).
+inline int kv4_tile_rows(int G, int max_q_len) {
+  const long long rows = (long long)G * max_q_len;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+// The CTAs of a launch in shares: one wave.
+inline int kv4_share_ctas(int rows, int sms) { return sms * (rows == 8 ? 4 : rows == 16 ? 3 : 2); }
+template <int D>
+cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s);
 
 struct PlanArgs {
   int R, T, page, pages, width;

@@ -251,6 +251,26 @@ fa_status attn_check(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
 
 constexpr int kMaxSms = 160;
 
+// Tiles of a launch whose requests all have max_q_len rows.
+long long kv4_tiles(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows) {
+  const long long q_rows = (long long)std::min(p->max_q_len, std::max(p->T, 1)) * (p->Hq / c->Hk);
+  return (long long)p->R * c->Hk * ((q_rows + rows - 1) / rows);
+}
+
+// CTAs of a cluster (8 warps each) for a tile, as many as one wave has room for; 0 for the
+// way in shares: with more tiles than a wave has CTAs, or where the longest request the
+// block table has room for would give a warp more than 16 units of 32 tokens, the even
+// shares make up for the second launch.
+int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int sms) {
+  const long long tiles = kv4_tiles(c, p, rows), slots = (long long)sms * (rows == 8 ? 2 : 1);
+  long long tokens = (long long)p->table_width * c->page_size;
+  if (p->window > 0) tokens = std::min(tokens, (long long)p->window + p->max_q_len + 31);
+  int cluster = 8;
+  while (cluster > 1 && tiles * cluster > slots) cluster /= 2;
+  if (tiles > slots || (tokens + 31) / 32 > 16ll * 8 * cluster) return 0;
+  return cluster;
+}
+
 size_t attn_part_bytes(int ctas, int rows, int d) { return align256((size_t)2 * ctas * rows * (d + 4) * 4); }
 
 }  // namespace
@@ -339,7 +359,7 @@ fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
 size_t fa_kv4_attention_workspace_size(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
   if (attn_check(c, p) != FA_OK) return 0;
   const int rows = kv4_tile_rows(p->Hq / c->Hk, p->max_q_len);
-  const int ctas = kv4_max_ctas(c->d, rows, kMaxSms);
+  const int ctas = kv4_share_ctas(rows, kMaxSms);
   return attn_part_bytes(ctas, rows, c->d) + align256((size_t)ctas * 32);
 }
 
@@ -385,12 +405,16 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   std::memcpy(a.os, p->o_stride, sizeof(a.os));
   a.lse = lse;
   const int rows = kv4_tile_rows((int)a.G.d, p->max_q_len);
-  const int ctas = kv4_max_ctas(c->d, rows, std::min(sms, kMaxSms));
+  int ctas = kv4_share_ctas(rows, std::min(sms, kMaxSms));
   a.part = static_cast<float*>(workspace);
   a.meta = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attn_part_bytes(ctas, rows, c->d));
+  int cluster = kv4_cluster(c, p, rows, sms);
+  if (cluster > 0) ctas = (int)std::min<long long>(kv4_tiles(c, p, rows), (1 << 20)) * cluster;
   a.rep = rep;
-  const cudaError_t e =
-      launch_kv4_attention(a, c->d, p->dtype == FA_F16, rows, ctas, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f16 = p->dtype == FA_F16;
+  const cudaError_t e = c->d == 64 ? launch_kv4_attention_d<64>(a, f16, rows, ctas, cluster, st)
+                                   : launch_kv4_attention_d<128>(a, f16, rows, ctas, cluster, st);
   if (e != cudaSuccess) return api_cuda_fail(e, "cache attention launch");
   return FA_OK;
 }
