@@ -1009,6 +1009,8 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) 
   if (cluster > 0) {
     const auto k = kv4_attn_kernel<D, NT, F16, true>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CC::smem)) != cudaSuccess) return e;
+    if (cluster > 8 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = 1;

@@ -105,6 +105,7 @@ struct PlanArgs {
   int* pos;
   int* slots;
   int* counts;
+  bool aliased;  // kv or counts lie over the inputs (set by the launch)
 };
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
 

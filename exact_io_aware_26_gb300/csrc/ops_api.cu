@@ -265,7 +265,7 @@ int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, in
   const long long tiles = kv4_tiles(c, p, rows), slots = (long long)sms * (rows == 8 ? 2 : 1);
   long long tokens = (long long)p->table_width * c->page_size;
   if (p->window > 0) tokens = std::min(tokens, (long long)p->window + p->max_q_len + 31);
-  int cluster = 8;
+  int cluster = 16;
   while (cluster > 1 && tiles * cluster > slots) cluster /= 2;
   if (tiles > slots || (tokens + 31) / 32 > 16ll * 8 * cluster) return 0;
   return cluster;
@@ -455,6 +455,7 @@ fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int*
   a.pos = positions;
   a.slots = slots;
   a.counts = counts;
+  a.aliased = false;
   const cudaError_t e = launch_paged_plan(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return api_cuda_fail(e, "plan launch");
   return FA_OK;

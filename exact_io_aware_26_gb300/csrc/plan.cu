@@ -1,10 +1,11 @@
 // plan.cu -- block tables and slot maps of a serving step from request lengths.
 //
-// One cluster of CTAs; every CTA forms the prefix sums over all requests (new
-// tokens, pages given back, pages needed) in its shared memory, the cluster meets
-// once -- every input that an output may alias has been read by then -- and the CTAs
-// write the step's tokens and table entries side by side.  Integers in a fixed
-// order, no atomics.  Bound by latency: a step writes 8 bytes per token.
+// Every CTA forms the prefix sums over all requests (new tokens, pages given back, pages
+// needed) in its shared memory, and the CTAs write the step's tokens and table entries side
+// by side: what one writes no other reads, except where kv_lens or counts lie over the
+// inputs.  Then the CTAs are one cluster, which meets once all inputs have been read.
+// Integers in a fixed order, no atomics.  Bound by latency (a step writes 8 bytes per
+// token): the time goes into chains of searches and loads, so few tokens per thread.
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -128,10 +129,8 @@ __global__ void __launch_bounds__(kMaxThreads) paged_plan_kernel(const PlanArgs 
   taken = __reduce_max_sync(0xffffffffu, taken);
   __shared__ int taken_s[32];
   if ((threadIdx.x & 31) == 0) taken_s[threadIdx.x >> 5] = taken;
-  int n_ctas;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_ctas));
-  // inputs read everywhere, shared arrays complete here
-  if (n_ctas > 1)
+  // shared arrays complete; with outputs over inputs, also the inputs read by every CTA
+  if (a.aliased)
     cluster_sync();
   else
     __syncthreads();
@@ -146,26 +145,62 @@ __global__ void __launch_bounds__(kMaxThreads) paged_plan_kernel(const PlanArgs 
     if (r >= R) return -1;
     return a.table[r * a.stride + f - (r ? freed_end[r - 1] : 0)];
   };
-  const int t0 = cluster_rank() * n_threads + threadIdx.x, step = n_ctas * n_threads;
+  const int t0 = blockIdx.x * n_threads + threadIdx.x, step = gridDim.x * n_threads;
   const uint32_t page = (uint32_t)a.page;
   auto held = [&](int seq) { return (int)(((uint32_t)seq + page - 1) / page); };
 
-  for (int t = t0; t < a.T; t += step) {
-    const int r = upper_bound(tok_end, R, t);
-    int pos = 0, slot = -1;
-    if (r < R) {
-      const int seq = seq_s[r];
-      const long long p = (long long)seq + t - (r ? tok_end[r - 1] : 0);
-      pos = clamp_int(p);
-      if (served[r]) {
-        const int i = (int)((uint32_t)pos / page), have = held(seq);
-        const int id = i < have ? a.table[r * a.stride + i] : pool(there - 1 - ((r ? need_end[r - 1] : 0) + i - have));
-        const long long sl = (long long)id * a.page + ((uint32_t)pos - (uint32_t)i * page);
-        slot = id < 0 || sl > 0x7FFFFFFFll ? -1 : (int)sl;
+  // page i of a served request, after the step
+  auto page_of = [&](int r, int i) {
+    const int have = held(seq_s[r]);
+    return i < have ? a.table[r * a.stride + i] : pool(there - 1 - ((r ? need_end[r - 1] : 0) + i - have));
+  };
+  // more tokens than threads: four neighbours a thread, one search and the next from there
+  const int each = a.T > step ? 4 : 1;
+  const bool wide = each == 4 && ((reinterpret_cast<uintptr_t>(a.pos) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
+  for (int first = each * t0; first < a.T; first += each * step) {
+    int r = upper_bound(tok_end, R, first);
+    int pos[4], slot[4];
+    // the token's place in its request, its page there and its place in it, the page's number
+    long long p = 0;
+    int i = 0, in = -1, id = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= each) break;
+      const int t = first + k;
+      pos[k] = 0;
+      slot[k] = -1;
+      while (r < R && tok_end[r] <= t) {
+        ++r;
+        in = -1;
+      }
+      if (r >= R) continue;
+      if (in < 0) {
+        p = (long long)seq_s[r] + t - (r ? tok_end[r - 1] : 0);
+        i = (int)((uint32_t)clamp_int(p) / page);
+        in = (int)((uint32_t)clamp_int(p) - (uint32_t)i * page);
+        id = served[r] ? page_of(r, i) : -1;
+      }
+      pos[k] = clamp_int(p);
+      const long long sl = (long long)id * a.page + in;
+      slot[k] = id < 0 || sl > 0x7FFFFFFFll ? -1 : (int)sl;
+      ++p;
+      if (++in == a.page) {
+        in = 0;
+        ++i;
+        id = served[r] && t + 1 < tok_end[r] ? page_of(r, i) : -1;
       }
     }
-    a.pos[t] = pos;
-    a.slots[t] = slot;
+    if (wide && first + 4 <= a.T) {
+      *reinterpret_cast<int4*>(a.pos + first) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.slots + first) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < each && first + k < a.T) {
+          a.pos[first + k] = pos[k];
+          a.slots[first + k] = slot[k];
+        }
+    }
   }
   for (int r = t0; r < R; r += step) {
     const int fresh = tok_end[r] - (r ? tok_end[r - 1] : 0);
@@ -188,6 +223,8 @@ __global__ void __launch_bounds__(kMaxThreads) paged_plan_kernel(const PlanArgs 
   }
 }
 
+bool overlap(const int* a, int na, const int* b, int nb) { return a < b + nb && b < a + na; }
+
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
@@ -197,11 +234,19 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  // A CTA of as many threads as there are tokens and requests to spread over it; a cluster
-  // of eight where one CTA would write more than a few tokens a thread.
-  const int most = a.T > a.R ? a.T : a.R;
-  const int threads = most >= kMaxThreads ? kMaxThreads : (most + 127) / 128 * 128;
-  const int ctas = a.T <= 4 * kMaxThreads ? 1 : 8;
+  // A token for each thread, and threads for the pages of ended requests besides (the step of
+  // 256 single tokens: 8.4 us with as many threads as tokens).
+  const bool few = a.T <= 256 && a.R <= 32;
+  const int threads = few ? 256 : kMaxThreads;
+  const long long want = ((long long)a.T + threads - 1) / threads;
+  PlanArgs b = a;
+  b.aliased = overlap(a.kv, a.R, a.seq, a.R) || overlap(a.kv, a.R, a.fresh, a.R) || overlap(a.kv, a.R, a.count, 1) ||
+              overlap(a.counts, 3, a.count, 1) || overlap(a.counts, 3, a.seq, a.R) || overlap(a.counts, 3, a.fresh, a.R);
+  const int ctas = (int)(want < 1 ? 1 : b.aliased ? (want < 8 ? want : 8) : (want < 128 ? want : 128));
+  if (!b.aliased) {
+    paged_plan_kernel<<<ctas, threads, smem, s>>>(b);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(threads);
@@ -214,7 +259,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, b);
 }
 
 }  // namespace fa

@@ -383,14 +383,15 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const QkArgs 
   }
 }
 
-// The gradient, in the same way, one tensor after the other (their rows in one loop, with the
-// sums of both, measured 10% slower): a lane adds up the weights' gradients of its channels,
-// and each CTA leaves one partial sum for each tensor.
+// The gradient, in the same way; of a chunk first the queries' rows, then the keys' (both
+// token by token in one loop, with the sums of both, measured 10% slower): a lane adds up the
+// weights' gradients of its channels, its warp's sums are kept in shared memory from one
+// change of tensor to the next, and each CTA leaves one partial sum for each tensor.
 template <int D, int DT, bool ANY>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, WARPS = kThreads / 32, E = DT == FA_F32 ? 4 : 2;
   extern __shared__ __align__(16) char smem[];
-  __shared__ float red[WARPS][D];
+  __shared__ float red[2][WARPS][D];
   Angles<D>& ang = *reinterpret_cast<Angles<D>*>(smem);
   float* rows_s = reinterpret_cast<float*>(smem + sizeof(Angles<D>)) + 2 * D;
   const Feed<DT, 4> feed(smem + sizeof(Angles<D>) + 2 * D * 4 + (ANY ? kThreads * 16 * 4 : 0));
@@ -398,90 +399,99 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkA
   const int slot = threadIdx.x / LPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Lane L = lane_channels<D, ANY>(a, threadIdx.x % LPR);
   const Run run = run_of(a);
+  for (int e = lane; e < 2 * D; e += 32) red[e / D][warp][e % D] = 0.f;
+  __syncwarp();
+  for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
+    const int nt = min(run.chunk, run.last - t0);
+    const int turns_q = (nt * a.Hq + ROWS - 1) / ROWS, turns = turns_q + (nt * a.Hk + ROWS - 1) / ROWS;
+    // row of this slot in a turn; `live`: there is one
+    auto row_in = [&](int i, bool& live) {
+      const int t = i >= turns_q, rows = nt * (t ? a.Hk : a.Hq), k = (i - (t ? turns_q : 0)) * ROWS + slot;
+      live = i < turns && k < rows;
+      return row_of(a, t, t0, min(k, rows - 1));
+    };
+    auto load = [&](int place, int i) {
+      bool live;
+      const Row r = row_in(i, live);
+      if (live) {
+        const char *p = row_at(r, a.x, a.xb, a.xn, a.xh), *q = row_at(r, a.dy, a.db, a.dn, a.dh);
+        feed.load(place, 0, p + L.lo * E);
+        feed.load(place, 1, p + L.hi * E);
+        feed.load(place, 2, q + L.lo * E);
+        feed.load(place, 3, q + L.hi * E);
+      }
+      feed.commit();
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD - 1; ++k) load(k, k);
+    __syncthreads();  // the angles before have been used
+    form_angles<D>(a, t0, nt, ang);
+    __syncthreads();
+    int place = 0;
+    for (int t = 0, i = 0; t < 2; ++t) {
+      uint64_t wl[4], wh[4], acc[8];
+      weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, wl);
+      weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, wh);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = 0;
 #pragma unroll 1
-  for (int t = 0; t < 2; ++t) {
-    uint64_t wl[4], wh[4], acc[8];
-    weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, wl);
-    weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, wh);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0;
-    for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
-      const int nt = min(run.chunk, run.last - t0), rows = nt * (t ? a.Hk : a.Hq);
-      auto load = [&](int turn, int i) {
-        if (i < rows) {
-          const Row r = row_of(a, t, t0, i);
-          const char *p = row_at(r, a.x, a.xb, a.xn, a.xh), *q = row_at(r, a.dy, a.db, a.dn, a.dh);
-          feed.load(turn, 0, p + L.lo * E);
-          feed.load(turn, 1, p + L.hi * E);
-          feed.load(turn, 2, q + L.lo * E);
-          feed.load(turn, 3, q + L.hi * E);
-        }
-        feed.commit();
-      };
-#pragma unroll
-      for (int k = 0; k < AHEAD - 1; ++k) load(k, slot + k * ROWS);
-      __syncthreads();  // the angles before have been used
-      form_angles<D>(a, t0, nt, ang);
-      __syncthreads();
-      int turn = 0;
-      for (int i0 = 0; i0 < rows; i0 += ROWS) {
-        const bool live = i0 + slot < rows;
-        const Row r = row_of(a, t, t0, min(i0 + slot, rows - 1));
-        load(turn == 0 ? AHEAD - 1 : turn - 1, i0 + (AHEAD - 1) * ROWS + slot);
+      for (; i < (t ? turns : turns_q); ++i) {
+        bool live;
+        const Row r = row_in(i, live);
+        load(place == 0 ? AHEAD - 1 : place - 1, i + AHEAD - 1);
         feed.wait();
         uint64_t lo[4], hi[4], gl[4], gh[4];
-        feed.get(turn, 0, lo);
-        feed.get(turn, 1, hi);
-        feed.get(turn, 2, gl);
-        feed.get(turn, 3, gh);
-        turn = turn + 1 == AHEAD ? 0 : turn + 1;
+        feed.get(place, 0, lo);
+        feed.get(place, 1, hi);
+        feed.get(place, 2, gl);
+        feed.get(place, 3, gh);
+        place = place + 1 == AHEAD ? 0 : place + 1;
         if constexpr (ANY)
           rotate_any<D, true>(a, rows_s + slot * D, L, ang.c[r.tok], ang.s[r.tok], gl, gh);
         else
           rotate<D, true>(a, L, ang.c[r.tok], ang.s[r.tok], gl, gh);
         uint64_t ss = 0, sd = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ss = ffma2(lo[i], lo[i], ffma2(hi[i], hi[i], ss));
-          sd = ffma2(fmul2(gl[i], wl[i]), lo[i], ffma2(fmul2(gh[i], wh[i]), hi[i], sd));
+        for (int k = 0; k < 4; ++k) {
+          ss = ffma2(lo[k], lo[k], ffma2(hi[k], hi[k], ss));
+          sd = ffma2(fmul2(gl[k], wl[k]), lo[k], ffma2(fmul2(gh[k], wh[k]), hi[k], sd));
         }
         const float rn = rsqrtf(row_sum<D>(fsum2(ss)) * (1.f / D) + a.eps);
         const float m = row_sum<D>(fsum2(sd)) * (1.f / D) * rn * rn;  // mean(dn h) r: what x takes off dn
-        // a slot without a row holds an earlier one's values: they add nothing
-        const uint64_t in_sum = fdup(live ? rn : 0.f), rn2 = fdup(rn), m2 = fdup(-m);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i] = ffma2(gl[i], fmul2(lo[i], in_sum), acc[i]);
-          acc[4 + i] = ffma2(gh[i], fmul2(hi[i], in_sum), acc[4 + i]);
-          lo[i] = fmul2(rn2, ffma2(lo[i], m2, fmul2(gl[i], wl[i])));
-          hi[i] = fmul2(rn2, ffma2(hi[i], m2, fmul2(gh[i], wh[i])));
-        }
+        const uint64_t rn2 = fdup(rn), m2 = fdup(-m);
         if (live) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[k] = ffma2(gl[k], fmul2(lo[k], rn2), acc[k]);
+            acc[4 + k] = ffma2(gh[k], fmul2(hi[k], rn2), acc[4 + k]);
+            lo[k] = fmul2(rn2, ffma2(lo[k], m2, fmul2(gl[k], wl[k])));
+            hi[k] = fmul2(rn2, ffma2(hi[k], m2, fmul2(gh[k], wh[k])));
+          }
           char* p = row_at(r, a.y, a.yb, a.yn, a.yh);
           store8<DT>(p + L.lo * E, lo);
           store8<DT>(p + L.hi * E, hi);
         }
       }
-    }
-    __syncthreads();  // red of the tensor before has been read
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[2];
-      f2unpack(acc[i], v[0], v[1]);
+      for (int k = 0; k < 8; ++k) {
+        float v[2];
+        f2unpack(acc[k], v[0], v[1]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int off = LPR; off < 32; off <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-        if (lane < LPR) red[warp][(i < 4 ? L.lo : L.hi) + 2 * (i & 3) + k] = v[k];
+          for (int off = LPR; off < 32; off <<= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], off);
+          if (lane < LPR) red[t][warp][(k < 4 ? L.lo : L.hi) + 2 * (k & 3) + c] += v[c];
+        }
       }
     }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float v = 0.f;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 * D) {
+    const int t = threadIdx.x / D, ch = threadIdx.x % D;
+    float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) v += red[w][threadIdx.x];
-      a.part[((size_t)blockIdx.x * 2 + t) * D + threadIdx.x] = v;
-    }
+    for (int w = 0; w < WARPS; ++w) v += red[t][w][ch];
+    a.part[((size_t)blockIdx.x * 2 + t) * D + ch] = v;
   }
 }
 
