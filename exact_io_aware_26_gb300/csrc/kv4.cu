@@ -61,36 +61,44 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return r;
 }
 
-// Codes of a lane's eight values and the pair of its group of four lanes.  Writing prompts
-// is bound by these instructions before HBM; hence packed fp32 arithmetic, three-input
-// minima, and no division or clamping per value where neither can matter.
-__device__ __forceinline__ void quantise8(float (&v)[8], uint32_t& word, uint32_t& pair) {
-  float lo = min3_nan(min3_nan(v[0], v[1], v[2]), min3_nan(v[3], v[4], v[5]), min3_nan(v[6], v[7], v[7]));
-  float hi = max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], v[7]));
+// Writing prompts is bound by its instructions before HBM; hence packed fp32 arithmetic,
+// three-input minima, one pair per lane (the key's or the value's), and no division or
+// clamping per value where neither can matter.
+
+// Least and largest of a lane's eight values and those of its group of four lanes.
+__device__ __forceinline__ void range8(const float (&v)[8], float& lo, float& hi) {
+  lo = min3_nan(min3_nan(v[0], v[1], v[2]), min3_nan(v[3], v[4], v[5]), min3_nan(v[6], v[7], v[7]));
+  hi = max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], v[7]));
 #pragma unroll
   for (int off = 1; off < 4; off <<= 1) {
     const float l = __shfl_xor_sync(0xffffffffu, lo, off), h = __shfl_xor_sync(0xffffffffu, hi, off);
     lo = min3_nan(lo, l, l);
     hi = max3_nan(hi, h, h);
   }
+}
+
+// The pair of a group, and 16 / scale: negative where its codes need the documented steps
+// one by one (codes8).
+__device__ __forceinline__ void pair_of(float lo, float hi, uint32_t& pair, float& inv) {
   const bool nan = lo != lo;
-  if (lo < -kKvSaturate || hi > kKvSaturate) {  // (rare)
-    lo = fminf(fmaxf(lo, -kKvSaturate), kKvSaturate);
-    hi = fminf(fmaxf(hi, -kKvSaturate), kKvSaturate);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -kKvSaturate), kKvSaturate);
-  }
+  const float sat_lo = fminf(fmaxf(lo, -kKvSaturate), kKvSaturate), sat_hi = fminf(fmaxf(hi, -kKvSaturate), kKvSaturate);
   // the documented steps, each rounded once: plain fp32, no contraction
-  const __half s = __float2half_rn(__fdiv_rn(__fmul_rn(__fsub_rn(hi, lo), 16.f), 15.f));
-  const __half c = __float2half_rn(__fsub_rn(lo, __half2float(s)));
+  const __half s = __float2half_rn(__fdiv_rn(__fmul_rn(__fsub_rn(sat_hi, sat_lo), 16.f), 15.f));
+  const __half c = __float2half_rn(__fsub_rn(sat_lo, __half2float(s)));
   const float sf = __half2float(s), cf = __half2float(c);
   pair = nan ? 0x7E007E00u : (uint32_t)__half_as_ushort(s) | ((uint32_t)__half_as_ushort(c) << 16);
-  // The quotient (x - base) * 16 / scale only decides between neighbouring codes.  A product
-  // with the reciprocal is off by less than 2^-22 of it, below 2^-17 where no code is
-  // clamped, so its rounding is the quotient's unless it lies within 2^-16 of a half.  Then,
-  // and where the group's least or largest value has a code out of range (fp16's rounding
-  // of a base far from 0), the documented steps themselves are done.
-  const float inv = __fdividef(16.f, sf);
+  inv = __fdividef(16.f, sf);
+  // a scale of 0 or NaN, saturated values, or a least or largest value whose code is out of
+  // range (fp16's rounding of a base far from 0)
+  const float first = fmaf(lo - cf, inv, -16.f), last = fmaf(hi - cf, inv, -16.f);
+  if (!(first > -0.5f && last < 15.5f && sat_lo == lo && sat_hi == hi && sf > 0.f)) inv = -1.f;
+}
+
+// Codes of a lane's eight values.  The quotient (x - base) * 16 / scale only decides between
+// neighbouring codes: a product with the reciprocal is off by less than 2^-22 of it, below
+// 2^-17, so its rounding is the quotient's unless it lies within 2^-16 of a half.
+__device__ __forceinline__ uint32_t codes8(float (&v)[8], uint32_t pair, float inv) {
+  const float cf = __half2float(__ushort_as_half((unsigned short)(pair >> 16)));
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
   const uint64_t inv2 = f2pack(inv, inv), base2 = f2pack(-cf, -cf), off2 = f2pack(-16.f, -16.f);
   const uint64_t up2 = f2pack(kRound, kRound), down2 = f2pack(-kRound, -kRound), neg2 = f2pack(-1.f, -1.f);
@@ -104,9 +112,8 @@ __device__ __forceinline__ void quantise8(float (&v)[8], uint32_t& word, uint32_
     f2unpack(ffma2(code[i], neg2, t), x, y);
     border = fmax3(border, fabsf(x), fabsf(y));
   }
-  const float first = fmaf(lo - cf, inv, -16.f), last = fmaf(hi - cf, inv, -16.f);
-  const bool plain = border < 0.5f - 0x1p-16f && first > -0.5f && last < 15.5f;
-  if (plain) {
+  uint32_t word;
+  if (border < 0.5f - 0x1p-16f && inv > 0.f) {
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // four codes: a whole number below 2^16, in the low bits of 2^23 more
@@ -115,16 +122,19 @@ __device__ __forceinline__ void quantise8(float (&v)[8], uint32_t& word, uint32_
       w[k] = __float_as_uint(fmaf(odd, 16.f, even) + 8388608.f);
     }
     word = __byte_perm(w[0], w[1], 0x5410);
-  } else {  // also a scale of 0 or NaN, whose codes are 0
+  } else {
+    const float sf = __half2float(__ushort_as_half((unsigned short)(pair & 0xFFFFu)));
     word = 0;
     if (sf > 0.f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = __fsub_rn(__fdiv_rn(__fmul_rn(__fsub_rn(v[i], cf), 16.f), sf), 16.f);
+        const float x = fminf(fmaxf(v[i], -kKvSaturate), kKvSaturate);
+        const float t = __fsub_rn(__fdiv_rn(__fmul_rn(__fsub_rn(x, cf), 16.f), sf), 16.f);
         word |= (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f) << (4 * i);
       }
     }
   }
+  return word;
 }
 
 // A row is one head of one token: D / 8 lanes, which take its key and its value.
@@ -143,9 +153,16 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowArgs a
     load8<DT>(a.x[1], row_at(a, 1, tok, head) + 8 * j, v);
     blk = slot_block(a, __ldg(a.slots + tok), head, Blk::bytes, row);
   }
-  uint32_t wk, pk, wv, pv;
-  quantise8(k, wk, pk);
-  quantise8(v, wv, pv);
+  float lo[2], hi[2];
+  range8(k, lo[0], hi[0]);
+  range8(v, lo[1], hi[1]);
+  uint32_t pair;  // even lanes the key's, odd lanes the value's
+  float inv;
+  pair_of(j & 1 ? lo[1] : lo[0], j & 1 ? hi[1] : hi[0], pair, inv);
+  const int lane = threadIdx.x & 31;
+  const uint32_t pk = __shfl_sync(0xffffffffu, pair, lane & ~1), pv = __shfl_sync(0xffffffffu, pair, lane | 1);
+  const float ik = __shfl_sync(0xffffffffu, inv, lane & ~1), iv = __shfl_sync(0xffffffffu, inv, lane | 1);
+  const uint32_t wk = codes8(k, pk, ik), wv = codes8(v, pv, iv);
   if (!blk) return;
   uint8_t* at = blk + row * Blk::row + 4 * j;
   *reinterpret_cast<uint32_t*>(at) = wk;

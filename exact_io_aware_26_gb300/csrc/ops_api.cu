@@ -83,7 +83,7 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
   if (!(std::isfinite(p->eps) && p->eps > 0.f)) return fail(FA_ERR_INVALID, "eps must be positive and finite");
   if (p->pos_stride < 0) return fail(FA_ERR_INVALID, "pos_stride is negative");
   // tokens and rows of a chunk are counted in 32 bits
-  if ((long long)p->B * p->N >= (1ll << 30) || p->Hq >= (1 << 24) || p->Hk >= (1 << 24))
+  if ((long long)p->B * p->N >= (1ll << 30) || (long long)p->Hq + p->Hk >= (1 << 24))
     return fail(FA_ERR_UNSUPPORTED, "B*N exceeds 2^30 - 1 or the heads 2^24 - 1");
   for (int i = 1; i < 3; ++i)
     for (const long long* st : {p->q_stride, p->k_stride, p->yq_stride, p->yk_stride, bwd ? p->dq_stride : p->q_stride,
@@ -154,6 +154,13 @@ fa_status qk_pointers(const fa_qk_params* p, const void* q, const void* k, const
   FA_TRY(need(wk, 16, "wk"));
   if (p->rot_dim > 0) FA_TRY(need(freqs, 8, "freqs"));
   if (positions && !aligned(positions, 4)) return fail(FA_ERR_INVALID, "positions is not 4-byte aligned");
+  return FA_OK;
+}
+
+// A result over its own input: rows are read ahead, so every row must stay in its place.
+fa_status qk_in_place(const void* x, const void* y, const long long* sx, const long long* sy, const char* name) {
+  if (x == y && std::memcmp(sx, sy, 3 * sizeof(long long)) != 0)
+    return fail(FA_ERR_INVALID, "%s lies over its input with other strides", name);
   return FA_OK;
 }
 
@@ -240,8 +247,8 @@ fa_status attn_check(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
   if (p->window < 0) return fail(FA_ERR_INVALID, "window is negative");
   if (p->table_width < 1 || p->table_stride < p->table_width)
     return fail(FA_ERR_INVALID, "block_table needs at least one column and a row stride of at least its width");
-  if ((long long)p->table_width * c->page_size > 0x7FFFFFFFll)
-    return fail(FA_ERR_UNSUPPORTED, "table_width * page_size exceeds 2^31 - 1 tokens");
+  if ((long long)p->table_width * c->page_size > (1ll << 30))
+    return fail(FA_ERR_UNSUPPORTED, "table_width * page_size exceeds 2^30 tokens");
   if (!(std::isfinite(p->scale) && p->scale > 0.f)) return fail(FA_ERR_INVALID, "scale must be positive and finite");
   const long long size[2] = {p->T, p->Hq};
   FA_TRY(check_strides(p->q_stride, size, 2, c->d, p->dtype, false, "q"));
@@ -285,6 +292,8 @@ fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, c
     FA_TRY(qk_pointers(p, q, k, wq, wk, freqs, positions));
     FA_TRY(need(yq, 16, "yq"));
     FA_TRY(need(yk, 16, "yk"));
+    FA_TRY(qk_in_place(q, yq, p->q_stride, p->yq_stride, "yq"));
+    FA_TRY(qk_in_place(k, yk, p->k_stride, p->yk_stride, "yk"));
   }
   Report rep;
   int sms = 0;
@@ -316,6 +325,10 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* 
     FA_TRY(need(dyk, 16, "dyk"));
     FA_TRY(need(dq, 16, "dq"));
     FA_TRY(need(dk, 16, "dk"));
+    FA_TRY(qk_in_place(q, dq, p->q_stride, p->dq_stride, "dq"));
+    FA_TRY(qk_in_place(k, dk, p->k_stride, p->dk_stride, "dk"));
+    FA_TRY(qk_in_place(dyq, dq, p->yq_stride, p->dq_stride, "dq"));
+    FA_TRY(qk_in_place(dyk, dk, p->yk_stride, p->dk_stride, "dk"));
   }
   FA_TRY(need(dwq, 4, "dwq"));
   FA_TRY(need(dwk, 4, "dwk"));
@@ -426,6 +439,7 @@ fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int*
   if (!p) return fail(FA_ERR_INVALID, "params is NULL");
   if (p->R < 1 || p->T < 0 || p->page_size < 1 || p->num_pages < 1)
     return fail(FA_ERR_INVALID, "R, page_size and num_pages must be >= 1 and T >= 0");
+  if (p->T > (1 << 30) || p->num_pages > (1 << 30)) return fail(FA_ERR_UNSUPPORTED, "T or num_pages exceeds 2^30");
   if (p->R > FA_PLAN_MAX_REQUESTS) return fail(FA_ERR_UNSUPPORTED, "R = %d exceeds %d", p->R, FA_PLAN_MAX_REQUESTS);
   if (p->table_width < 1 || p->table_stride < p->table_width)
     return fail(FA_ERR_INVALID, "block_table needs at least one column and a row stride of at least its width");

@@ -291,7 +291,8 @@ def qk_norm_rope(q, k, wq, wk, freqs, positions=None, eps: float = 1e-6, interle
     [B, N]; None: 0 .. N - 1).  Results are [B, H, N, d] as ``attention_fwd`` takes them,
     or, with ``heads_first`` false, [B, N, H, d]; ``out`` (yq, yk) may be (q, k) there."""
     yq, yk = (None, None) if out is None else out
-    return _call(_QK, (q, k, wq, wk, freqs, positions, yq, yk), (eps, interleaved, heads_first), stream, _plan_qk)
+    return _call(_QK, (q, k, wq, wk, freqs, positions, yq, yk), (float(eps), bool(interleaved), bool(heads_first)),
+                 stream, _plan_qk)
 
 
 def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -299,8 +300,8 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float =
     """(dq, dk, dwq, dwk): gradients of ``qk_norm_rope`` for dyq, dyk at its results (in its
     layout); q and k are its inputs.  dq, dk are [B, N, H, d] in q's dtype (views of a
     packed gradient may be given), dwq, dwk fp32 [d]."""
-    return _call(_QK_BWD, (q, k, dyq, dyk, wq, wk, freqs, positions, dq, dk, workspace), (eps, interleaved, heads_first),
-                 stream, _plan_qk_bwd)
+    return _call(_QK_BWD, (q, k, dyq, dyk, wq, wk, freqs, positions, dq, dk, workspace),
+                 (float(eps), bool(interleaved), bool(heads_first)), stream, _plan_qk_bwd)
 
 
 # ---------------------------------------------------------------- the 4-bit cache
@@ -378,7 +379,7 @@ def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = F
     ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d] (with a leading batch of one,
     as ``attention_fwd`` takes them)."""
     k, v = (None, None) if out is None else out
-    return _call(_GATHER, (cache, slots, k, v), (d, dtype, heads_first), stream, _plan_gather)
+    return _call(_GATHER, (cache, slots, k, v), (int(d), dtype, bool(heads_first)), stream, _plan_gather)
 
 
 def _plan_attention(q, cache, block_table, kv_lens, cu_q, out, lse, workspace, max_q_len, scale, window):
@@ -424,8 +425,8 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1,
     only the last ``window`` of those.  Rows without a token to see: o = 0, lse = -inf;
     rows outside every request are not written.  ``max_q_len``: the most rows of a request,
     a hint.  Lengths stay on the GPU: the call does not synchronise."""
-    return _call(_ATTENTION, (q, cache, block_table, kv_lens, cu_q, out, lse, workspace), (max_q_len, scale, window),
-                 stream, _plan_attention)
+    return _call(_ATTENTION, (q, cache, block_table, kv_lens, cu_q, out, lse, workspace),
+                 (int(max_q_len), None if scale is None else float(scale), int(window)), stream, _plan_attention)
 
 
 # ---------------------------------------------------------------- block tables and slot maps
@@ -469,5 +470,6 @@ def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_siz
     slots of -1.  out["kv_lens"] may be seq_lens, and out["counts"] the tensor whose first
     element is free_count."""
     given = (None,) * 5 if out is None else tuple(out[name] for name in _PLAN_OUT)
-    got = _call(_PLAN, (seq_lens, new_lens, block_table, free_pages, free_count, *given), (page_size, T), stream, _plan_plan)
+    got = _call(_PLAN, (seq_lens, new_lens, block_table, free_pages, free_count, *given), (int(page_size), int(T)),
+                stream, _plan_plan)
     return dict(zip(_PLAN_OUT, got))

@@ -346,15 +346,16 @@ fa_status fa_fwd_fp8(const fa_params* p, const void* q8, const void* k8, const v
  * position, and its leading 32 bits give the angle to 2^-32 turns.
  *
  *   B, N, Hq, Hk, d  batch, tokens per batch entry (>= 0), query and key heads,
- *               head size (64 or 128).
+ *               head size (64 or 128); B*N < 2^30.
  *   dtype       fa_dtype of q, k, yq, yk and their gradients (fp32 arithmetic
  *               inside); weight_dtype that of wq, wk: `dtype` or FA_F32.
  *   eps         positive and finite.
  *   *_stride    element strides {batch, token, head}; channels are contiguous.
  *               Bases 16-byte aligned, strides multiples of 16 bytes; written
  *               tensors must not overlap themselves.  q and k may be views of one
- *               packed projection, and yq (yk) may be q (k) itself, with the same
- *               strides.
+ *               packed projection.  yq (yk) may be q (k), and dq (dk) may be q or dyq
+ *               (k or dyk), with the same strides; other overlaps are not allowed.
+ *               Token and head strides below 2^31 bytes.
  *   pos_stride  batch stride of `positions` in elements (0: one row for all).
  * positions: device int32 [B][N], or NULL for positions 0 .. N - 1.
  * ------------------------------------------------------------------------ */

@@ -146,12 +146,14 @@ def attention(q, cache, table, kv_lens, cu_q, scale, window, d):
     G = Hq // Hk
     o, lse = np.zeros((T, Hq, d)), np.full((T, Hq), -np.inf)
     size, slack = np.zeros((T, Hq, d)), np.zeros((T, Hq))
+    half = cache.shape[3] // 2
+    every = [unpack(cache[..., a:a + half], d) for a in (0, half)]
     for r, n in enumerate(kv_lens):
         q0, q1 = cu_q[r], cu_q[r + 1]
         if n <= 0 or q1 <= q0:
             continue
         j = np.arange(n)
-        k, v = slot_values(cache, table[r][j // page_size].astype(np.int64) * page_size + j % page_size, d)
+        k, v = (x[table[r][j // page_size], :, j % page_size // BLOCK, j % BLOCK] for x in every)
         for i in range(q1 - q0):
             p = n - (q1 - q0) + i
             first = max(0, p - window + 1) if window else 0

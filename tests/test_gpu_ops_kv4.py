@@ -182,7 +182,17 @@ ATTN = [  # kv, new, Hq, Hk, d, dtype, page, window
     ([900], [4], 16, 2, 128, "bf16", 32, 1),                      # each sees itself only
     ([4000], [1], 24, 1, 64, "f16", 4096, 0),                     # 24 rows of one token
     (list(range(0, 150)), [1] * 150, 3, 1, 64, "bf16", 16, 0),    # more requests than a CTA keeps
+    ([i % 41 for i in range(350)], [1] * 350, 2, 2, 64, "f16", 16, 0),  # more tiles than CTAs
+    ([600] * 40, [2] * 40, 12, 4, 128, "bf16", 64, 100),
 ]
+
+
+def widened(table):
+    """The table with room for 100,000 tokens of 16-token pages: what a call has to reckon
+    with, which makes it take the way in shares instead of clusters."""
+    out = np.full((table.shape[0], 6250), -1, np.int32)
+    out[:, :table.shape[1]] = table
+    return out
 
 
 @pytest.mark.parametrize("kv,new,Hq,Hk,d,dtype,page,window", ATTN)
@@ -193,7 +203,6 @@ def test_attention(cuda_lib, kv, new, Hq, Hk, d, dtype, page, window):
     raw_l, lse = guarded((q.shape[0], Hq), torch.float32)
     dev = lambda a: torch.from_numpy(a).cuda()
     single = all(n == 1 for n in new)
-    raw_w, ws = None, None
     for cu_q in ([None] if single else []) + [dev(cu)]:
         o.fill_(float("nan"))
         fa.kv4_attention(q.cuda(), dev(cache), dev(table), dev(lens), cu_q=cu_q, max_q_len=max(new), scale=0.3,
@@ -201,6 +210,15 @@ def test_attention(cuda_lib, kv, new, Hq, Hk, d, dtype, page, window):
         assert fa.get_status() == fa.FA_OK
         check(o, lse, want, dtype)
         assert guards_intact(raw_o) and guards_intact(raw_l)
+    o.fill_(float("nan"))
+    ws_bytes = 16 << 20
+    raw_w, ws = guarded((ws_bytes,), torch.uint8, fill=0xFF)
+    aligned = ws[-ws.data_ptr() % 256:]
+    fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table)), dev(lens), cu_q=dev(cu), max_q_len=max(new), scale=0.3,
+                     window=window, out=o, lse=lse, workspace=aligned)
+    assert fa.get_status() == fa.FA_OK
+    check(o, lse, want, dtype)
+    assert guards_intact(raw_o) and guards_intact(raw_l) and guards_intact(raw_w, fill=0xFF)
     # the hint alone changes the tile height, not the result
     for hint in (1, 2, 100):
         o2, l2 = fa.kv4_attention(q.cuda(), dev(cache), dev(table), dev(lens), cu_q=dev(cu), max_q_len=hint, scale=0.3,
@@ -208,12 +226,13 @@ def test_attention(cuda_lib, kv, new, Hq, Hk, d, dtype, page, window):
         check(o2, l2, want, dtype)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("spread,scale", [(30.0, 0.5), (1e-3, 1.0), (100.0, 1e-4)])
-def test_attention_of_large_and_small_scores(cuda_lib, spread, scale):
+def test_attention_of_large_and_small_scores(cuda_lib, spread, scale, wide):
     q, cache, table, lens, cu = build([333, 70], [1, 1], 8, 2, 128, "bf16", 16, 5, spread)
     want = ref.attention(to_np64(q), cache, table, lens, cu, scale, 0, 128)
     dev = lambda a: torch.from_numpy(a).cuda()
-    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(table), dev(lens), scale=scale)
+    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens), scale=scale)
     check(o, lse, want, "bf16")
 
 
@@ -226,7 +245,8 @@ def test_queries_outside_fp16s_range(cuda_lib):
         check(o, lse, want, "bf16")
 
 
-def test_rising_scores_move_the_maximum(cuda_lib):
+@pytest.mark.parametrize("wide", [False, True])
+def test_rising_scores_move_the_maximum(cuda_lib, wide):
     """Keys that grow with the position: every block raises the running maximum."""
     n, d = 1000, 64
     rng = np.random.default_rng(8)
@@ -238,11 +258,12 @@ def test_rising_scores_move_the_maximum(cuda_lib):
     lens, cu = np.array([n], np.int32), np.array([0, 1], np.int32)
     want = ref.attention(to_np64(q), cache, table, lens, cu, 0.5, 0, d)
     dev = lambda a: torch.from_numpy(a).cuda()
-    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(table), dev(lens), scale=0.5)
+    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens), scale=0.5)
     check(o, lse, want, "f16")
 
 
-def test_nan_keys_and_values_reach_only_the_rows_that_see_them(cuda_lib):
+@pytest.mark.parametrize("wide", [False, True])
+def test_nan_keys_and_values_reach_only_the_rows_that_see_them(cuda_lib, wide):
     kv, new, d = [40, 60], [4, 4], 64
     q, cache, table, lens, cu = build(kv, new, 2, 1, d, "bf16", 16, 9)
     clean = ref.attention(to_np64(q), cache, table, lens, cu, 0.3, 0, d)
@@ -251,7 +272,8 @@ def test_nan_keys_and_values_reach_only_the_rows_that_see_them(cuda_lib):
         p, row = table[r, tok // 16], tok % 16
         cache[p, 0, 0, side * half + 8 * d + row * 8:side * half + 8 * d + row * 8 + 4] = 0x7E
     dev = lambda a: torch.from_numpy(a).cuda()
-    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(table), dev(lens), cu_q=dev(cu), max_q_len=4, scale=0.3)
+    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens), cu_q=dev(cu),
+                              max_q_len=4, scale=0.3)
     o, lse = to_np64(o), to_np64(lse)
     for r in range(2):
         for i in range(4):
@@ -344,14 +366,15 @@ def test_a_cache_beyond_32_bit_offsets(cuda_lib):
     check(o, lse, want, "bf16")
 
 
-def test_streams_graphs_and_shared_workspaces(cuda_lib):
+@pytest.mark.parametrize("wide", [False, True])
+def test_streams_graphs_and_shared_workspaces(cuda_lib, wide):
     """Two attentions at once on two streams, each with its own workspace; two captured
     graphs that share one workspace, replayed in turn; results equal to plain calls'."""
     dev = lambda a: torch.from_numpy(a).cuda()
     sets = []
     for seed, kv in ((20, [3000, 40]), (21, [5, 1800])):
         q, cache, table, lens, cu = build(kv, [1, 1], 8, 2, 128, "bf16", 64, seed)
-        args = (q.cuda(), dev(cache), dev(table), dev(lens))
+        args = (q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens))
         sets.append((args, fa.kv4_attention(*args)))
     torch.cuda.synchronize()
     side = [torch.cuda.Stream() for _ in sets]
@@ -362,7 +385,7 @@ def test_streams_graphs_and_shared_workspaces(cuda_lib):
     torch.cuda.synchronize()
     for g, (_, w) in zip(got, sets):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
-    ws = torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((16 << 20,), 255, dtype=torch.uint8, device="cuda")
     graphs = []
     for args, _ in sets:
         graph = torch.cuda.CUDAGraph()
@@ -387,6 +410,7 @@ def test_streams_graphs_and_shared_workspaces(cuda_lib):
     (20, 300, 16, 10, 150, 100, 0.2, 6),                                         # tables that are full
     (8, 20000, 7, 3000, 100, 9000, 0.0, 7), (1500, 3000, 16, 8, 100, 1500, 0.5, 8), (8192, 9000, 16, 3, 30, 9000, 0.3, 9),
     (3, 0, 16, 4, 40, 10, 0.7, 10), (10, 50, 16, 12, 100, 0, 1.0, 11),
+    (1, 300000, 16, 20000, 100, 20000, 0.0, 12), (300, 300000, 64, 40, 1500, 9000, 0.4, 13),  # many CTAs
 ])
 def test_plan(cuda_lib, R, T, page, width, most, spare, ended, seed):
     rng = np.random.default_rng(seed)
@@ -514,3 +538,16 @@ def test_serving_steps_with_a_graph(cuda_lib):
         verify(*held, int(cu[-1]))
     assert seq.tolist() == [40, 0, 57]
     assert int(counts[0]) == pages - 3 - 4
+
+
+def test_plan_of_lengths_that_are_out_of_range(cuda_lib):
+    """Negative lengths count as none; a length beyond the table is not served, and where it
+    has ended only the table's pages go back."""
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    table = i32([[5, 6], [7, 8], [1, 2], [3, 4]])
+    seq, new, stack, count = [-3, 33, 500, 2 ** 31 - 1], [2, 3, -1, 2 ** 31 - 1], [0, 9, 0, 0, 0, 0, 0, 0], 2
+    want = ref.plan([0, 33, 500, 2 ** 31 - 1], new, table.tolist(), stack, count, 16, 8)
+    t, s = table.clone(), i32(stack)
+    got = fa.paged_plan(i32(seq), i32(new), t, s, i32([count]), 16, 8)
+    assert got["kv_lens"].tolist() == want[0] and got["slots"].tolist() == want[3] and t.tolist() == want[5]
+    assert s.tolist() == want[6] and got["counts"].tolist()[0] == want[4][0]

@@ -12,6 +12,11 @@ import exact_io_aware_26_gb300 as fa
 OK = 1 << 20  # an aligned address that is never dereferenced
 
 
+def apart(n):
+    """n such addresses, none over another."""
+    return [OK + (i << 20) for i in range(n)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     fa.build()
@@ -104,14 +109,14 @@ def test_qk_pointers(lib):
     p = ctypes.byref(qk())
     for i in range(8):  # q k wq wk freqs positions yq yk
         for bad in ((None, OK + 2) if i != 5 else (OK + 2,)):
-            a = [OK] * 8
+            a = apart(8)
             a[i] = bad
             assert lib.fa_qk_norm_rope(p, *a, None) == fa.FA_ERR_INVALID
     assert lib.fa_qk_norm_rope(None, *[OK] * 8, None) == fa.FA_ERR_INVALID
     need = lib.fa_qk_norm_rope_bwd_workspace_size(p)
     assert need > 0
     for ws, n in ((None, need), (OK, need - 1), (OK + 16, need)):
-        assert lib.fa_qk_norm_rope_bwd(p, *[OK] * 12, ws, n, None) == fa.FA_ERR_WORKSPACE
+        assert lib.fa_qk_norm_rope_bwd(p, *apart(12), ws, n, None) == fa.FA_ERR_WORKSPACE
     assert b"workspace" in lib.fa_last_error()
 
 
@@ -189,6 +194,47 @@ def test_plan_refusals(lib, kw, code):
             a = [OK] * 10
             a[i] = bad
             assert lib.fa_paged_plan(ctypes.byref(good), *a, None) == fa.FA_ERR_INVALID
+
+
+def test_sizes_that_would_overflow_are_refused(lib):
+    good = dict(R=4, T=4, page_size=16, num_pages=10, table_width=4, table_stride=4)
+    for kw in ({"T": (1 << 30) + 1}, {"num_pages": (1 << 30) + 1}):
+        assert lib.fa_paged_plan(ctypes.byref(fa.FaPlanParams(**{**good, **kw})), *[OK] * 10, None) == fa.FA_ERR_UNSUPPORTED
+    assert lib.fa_qk_norm_rope(ctypes.byref(qk(Hq=1 << 23, Hk=1 << 23)), *[OK] * 8, None) == fa.FA_ERR_UNSUPPORTED
+    far = L3(1 << 40, 1 << 31, 64)
+    assert lib.fa_qk_norm_rope(ctypes.byref(qk(q_stride=far)), *[OK] * 8, None) == fa.FA_ERR_UNSUPPORTED
+    rows = fa.FaKv4Rows(4, fa.FA_BF16, L2(1 << 31, 64), L2(128, 64))
+    assert lib.fa_kv4_append(ctypes.byref(cache()), ctypes.byref(rows), *[OK] * 4, None) == fa.FA_ERR_UNSUPPORTED
+
+
+def test_results_over_their_inputs_need_the_same_strides(lib):
+    """In place with another layout would overwrite rows before they are read."""
+    a = apart(8)
+    a[7] = a[1]  # yk over k, whose strides are others
+    assert lib.fa_qk_norm_rope(ctypes.byref(qk()), *a, None) == fa.FA_ERR_INVALID
+    assert b"strides" in lib.fa_last_error()
+
+
+def test_launch_registers_and_forgets():
+    """The extension knows a combination only once it is registered, tells sizes, strides,
+    types and scalars apart, and forgets when the library changes."""
+    from exact_io_aware_26_gb300 import _launch
+    _launch.clear()
+    t = torch.zeros(4, 6)
+    assert _launch.run(99, (t, None), (1, 2.0)) is None
+    _launch.register(99, (t, None), (1, 2.0), 0, 0, [(2, 0)] * 7, [], [], None)
+    for tensors, scalars in (((t.t(), None), (1, 2.0)), ((t.double(), None), (1, 2.0)), ((t, t), (1, 2.0)),
+                             ((t[:, :5], None), (1, 2.0)), ((t, None), (1, 3.0))):
+        assert _launch.run(99, tensors, scalars) is None
+    with pytest.raises(TypeError):
+        _launch.run(99, ([1], None), (1, 2.0))
+    with pytest.raises(ValueError):
+        _launch.register(99, (t,), (), 0, 0, [(2, 0)] * 3, [], [], None)
+    with pytest.raises(ValueError):
+        _launch.register(99, (t,), (), 0, 0, [(0, 5)] * 7, [], [], None)
+    fa.use_library(fa.use_library(fa.LIB_PATH))
+    assert _launch.run(99, (t, None), (1, 2.0)) is None
+    fa.load()
 
 
 def test_block_bytes(lib):
