@@ -919,19 +919,21 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   }
 }
 
-// Adds the shares of the tile that starts in share blockIdx.x and goes on, if any; rows
-// 8 blockIdx.y .. + 7 of it.  The warps divide the shares, each lane D / 32 channels.
+// Adds the shares of the tile that starts in share blockIdx.x and goes on, if any; RPB rows of
+// it from RPB blockIdx.y on.  The warps divide the shares, each lane D / 32 channels.
+// RPB: 8, or 1 with few tiles, each of which may be cut into hundreds of shares (one tile of
+// 65,536 tokens: 88 us with eight rows to a block).
 constexpr int kMergeWarps = 8;
-template <int D, int NT, bool F16>
+template <int D, int NT, bool F16, int RPB>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4AttnArgs a) {
-  constexpr int ROWS = 8 * NT, CPL = D / 32;
-  __shared__ float top_s[kMergeWarps][8], sum_s[kMergeWarps][8];
-  __shared__ float acc_s[kMergeWarps][8][D + 4];
+  constexpr int ROWS = 8 * NT, CPL = D / 32, LANES = 32 * kMergeWarps / RPB;  // threads that look for a row's maximum
+  __shared__ float top_s[kMergeWarps][RPB], sum_s[kMergeWarps][RPB];
+  __shared__ float acc_s[kMergeWarps][RPB][D + 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = a.meta[2 * blockIdx.x];  // first row, rows, key head, last share
   const int q0 = a.meta[2 * blockIdx.x + 1].x;
   if (meta.x < 0) return;
-  const int r0 = 8 * blockIdx.y, rows = min(8, meta.y - r0);
+  const int r0 = RPB * blockIdx.y, rows = min(RPB, meta.y - r0);
   if (rows <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
   auto slot = [&](int c, int row) {  // the first share's slot is its second one
@@ -940,24 +942,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
   // the rows' largest maxima
   {
     float top = kNoMax;
-    const int row = lane & 7;
+    const int row = threadIdx.x % RPB;
     if (row < rows)
-      for (int c = c0 + (threadIdx.x >> 3); c <= meta.w; c += 4 * kMergeWarps) top = fmaxf(top, slot(c, row)[0]);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    if (lane < 8) top_s[warp][row] = top;
+      for (int c = c0 + threadIdx.x / RPB; c <= meta.w; c += LANES) top = fmaxf(top, slot(c, row)[0]);
+#pragma unroll
+    for (int off = RPB; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane < RPB) top_s[warp][row] = top;
   }
   __syncthreads();
-  float top[8], sum[8] = {}, acc[8][CPL] = {};
+  float top[RPB], sum[RPB] = {}, acc[RPB][CPL] = {};
 #pragma unroll
-  for (int row = 0; row < 8; ++row) {
+  for (int row = 0; row < RPB; ++row) {
     top[row] = top_s[0][row];
 #pragma unroll
     for (int w = 1; w < kMergeWarps; ++w) top[row] = fmaxf(top[row], top_s[w][row]);
   }
+#pragma unroll RPB == 1 ? 8 : 1
   for (int c = c0 + warp; c <= meta.w; c += kMergeWarps) {
 #pragma unroll
-    for (int row = 0; row < 8; ++row) {
+    for (int row = 0; row < RPB; ++row) {
       if (row < rows) {
         const float* s = slot(c, row);
         const float f = ex2(s[0] - top[row]);
@@ -968,7 +971,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
     }
   }
 #pragma unroll
-  for (int row = 0; row < 8; ++row) {
+  for (int row = 0; row < RPB; ++row) {
     if (lane == 0) sum_s[warp][row] = sum[row];
 #pragma unroll
     for (int i = 0; i < CPL; ++i) acc_s[warp][row][lane * CPL + i] = acc[row][i];
@@ -995,9 +998,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
     a.lse[(long long)(q0 + qi) * a.Hq + head] = total == 0.f ? -INFINITY : (best + log2f(total)) * 0.6931471805599453f;
 }
 
-// ctas: of the launch; cluster: CTAs of a cluster, or 0 for shares.
+// ctas: of the launch; cluster: CTAs of a cluster, or 0 for shares; few_tiles: see the merge.
 template <int D, int NT, bool F16>
-cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) {
+cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, bool few_tiles, cudaStream_t s) {
   using C = Cfg<D, NT, false>;
   using CC = Cfg<D, NT, true>;
   cudaLaunchConfig_t cfg = {};
@@ -1026,22 +1029,24 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) 
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(ctas, NT);
   cfg.blockDim = dim3(32 * kMergeWarps);
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16>, a);
+  cfg.gridDim = dim3(ctas, few_tiles ? 8 * NT : NT);
+  return few_tiles ? cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16, 1>, a)
+                   : cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16, 8>, a);
 }
 
 }  // namespace
 
 template <int D>
-cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s) {
+cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, bool few_tiles,
+                                   cudaStream_t s) {
   if (f16)
-    return rows == 8    ? launch<D, 1, true>(a, ctas, cluster, s)
-           : rows == 16 ? launch<D, 2, true>(a, ctas, cluster, s)
-                        : launch<D, 4, true>(a, ctas, cluster, s);
-  return rows == 8    ? launch<D, 1, false>(a, ctas, cluster, s)
-         : rows == 16 ? launch<D, 2, false>(a, ctas, cluster, s)
-                      : launch<D, 4, false>(a, ctas, cluster, s);
+    return rows == 8    ? launch<D, 1, true>(a, ctas, cluster, few_tiles, s)
+           : rows == 16 ? launch<D, 2, true>(a, ctas, cluster, few_tiles, s)
+                        : launch<D, 4, true>(a, ctas, cluster, few_tiles, s);
+  return rows == 8    ? launch<D, 1, false>(a, ctas, cluster, few_tiles, s)
+         : rows == 16 ? launch<D, 2, false>(a, ctas, cluster, few_tiles, s)
+                      : launch<D, 4, false>(a, ctas, cluster, few_tiles, s);
 }
 
 }  // namespace fa

@@ -266,15 +266,17 @@ long long kv4_tiles(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows
 
 // CTAs of a cluster (8 warps each) for a tile, as many as one wave has room for; 0 for the
 // way in shares: with more tiles than a wave has CTAs, or where the longest request the
-// block table has room for would give a warp more than 16 units of 32 tokens, the even
-// shares make up for the second launch.
+// block table has room for would give a warp more than 12 units of 32 tokens, the even
+// shares make up for the second launch (d = 128, in clusters and in shares: one tile of
+// 65,536 tokens, 16 units a warp, 30.2 and 24.5 us; d = 64: 12 tiles of 23,400 tokens,
+// 6 units, 14.4 and 18.8 us; 48 ragged tiles of up to 2048 tokens, 2 units, 8.9 and 12.5).
 int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int sms) {
   const long long tiles = kv4_tiles(c, p, rows), slots = (long long)sms * (rows == 8 ? 2 : 1);
   long long tokens = (long long)p->table_width * c->page_size;
   if (p->window > 0) tokens = std::min(tokens, (long long)p->window + p->max_q_len + 31);
   int cluster = 16;
   while (cluster > 1 && tiles * cluster > slots) cluster /= 2;
-  if (tiles > slots || (tokens + 31) / 32 > 16ll * 8 * cluster) return 0;
+  if (tiles > slots || (tokens + 31) / 32 > 12ll * 8 * cluster) return 0;
   return cluster;
 }
 
@@ -425,9 +427,9 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   if (cluster > 0) ctas = (int)std::min<long long>(kv4_tiles(c, p, rows), (1 << 20)) * cluster;
   a.rep = rep;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool f16 = p->dtype == FA_F16;
-  const cudaError_t e = c->d == 64 ? launch_kv4_attention_d<64>(a, f16, rows, ctas, cluster, st)
-                                   : launch_kv4_attention_d<128>(a, f16, rows, ctas, cluster, st);
+  const bool f16 = p->dtype == FA_F16, few = kv4_tiles(c, p, rows) < 32;
+  const cudaError_t e = c->d == 64 ? launch_kv4_attention_d<64>(a, f16, rows, ctas, cluster, few, st)
+                                   : launch_kv4_attention_d<128>(a, f16, rows, ctas, cluster, few, st);
   if (e != cudaSuccess) return api_cuda_fail(e, "cache attention launch");
   return FA_OK;
 }

@@ -184,6 +184,8 @@ ATTN = [  # kv, new, Hq, Hk, d, dtype, page, window
     (list(range(0, 150)), [1] * 150, 3, 1, 64, "bf16", 16, 0),    # more requests than a CTA keeps
     ([i % 41 for i in range(350)], [1] * 350, 2, 2, 64, "f16", 16, 0),  # more tiles than CTAs
     ([600] * 40, [2] * 40, 12, 4, 128, "bf16", 64, 100),
+    ([70000], [1], 3, 1, 64, "f16", 64, 0),                       # one tile in hundreds of shares
+    ([9000, 50000], [2, 3], 20, 2, 128, "bf16", 128, 0),
 ]
 
 
@@ -545,7 +547,7 @@ def test_plan_of_lengths_that_are_out_of_range(cuda_lib):
     has ended only the table's pages go back."""
     i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
     table = i32([[5, 6], [7, 8], [1, 2], [3, 4]])
-    seq, new, stack, count = [-3, 33, 500, 2 ** 31 - 1], [2, 3, -1, 2 ** 31 - 1], [0, 9, 0, 0, 0, 0, 0, 0], 2
+    seq, new, stack, count = [-3, 33, 500, 2 ** 31 - 1], [2, 3, -1, 1000], [0, 9, 0, 0, 0, 0, 0, 0], 2
     want = ref.plan([0, 33, 500, 2 ** 31 - 1], new, table.tolist(), stack, count, 16, 8)
     t, s = table.clone(), i32(stack)
     got = fa.paged_plan(i32(seq), i32(new), t, s, i32([count]), 16, 8)
