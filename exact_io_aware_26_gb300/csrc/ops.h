@@ -24,6 +24,7 @@ struct FastDiv {
 struct QkArgs {
   int B, N, Hq, Hk;
   int rot, interleaved;
+  int any;  // rotate through shared memory
   float eps;
   const char* x[2];   // q, k
   const void* w[2];   // wq, wk
@@ -40,6 +41,8 @@ struct QkArgs {
   float* part;    // backward: [CTA][2][d] partial weight gradients
   float* dw[2];
 };
+// CTAs on an SM, rows of a CTA's turn.
+int qk_ctas_per_sm(bool any, bool bwd);
 int qk_rows_per_pass(int d);
 cudaError_t launch_qk_norm_rope(const QkArgs& a, int d, int dtype, bool w_f32, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, int d, int dtype, bool w_f32, cudaStream_t s);

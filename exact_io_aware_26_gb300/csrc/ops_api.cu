@@ -102,7 +102,7 @@ fa_status qk_check(const fa_qk_params* p, bool bwd) {
   return FA_OK;
 }
 
-constexpr int kQkCtasPerSm = 4, kQkBwdCtasPerSm = 2, kQkMaxSms = 160;
+constexpr int kQkMaxSms = 160;
 
 // Byte strides of a pair of tensors.
 void qk_strides(const fa_qk_params* p, const long long* q, const long long* k, long long (&b)[2], int (&n)[2], int (&h)[2]) {
@@ -125,6 +125,14 @@ QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* 
   a.Hk = p->Hk;
   a.rot = p->rot_dim;
   a.interleaved = p->interleaved != 0;
+  // Through shared memory where the rotated halves are no whole chunks; and a rotated part of a
+  // 64-channel head where a row is read twice or is of 256 bytes, because the halves of the part
+  // are read in pieces of 32 bytes then (80 heads, N = 19735, 32 of 64 channels, in registers
+  // and through shared memory: bf16 forward 79 and 93 us, backward 122 and 104; fp32 forward
+  // 150 and 137, backward 221 and 202.  128 channels, 24 heads, N = 26016: bf16 backward 84 and
+  // 104, fp32 alike).
+  a.any = !a.interleaved && (p->rot_dim % 16 != 0 || (p->d == 64 && p->rot_dim > 0 && p->rot_dim < 64 &&
+                                                      (bwd || p->dtype == FA_F32)));
   a.eps = p->eps;
   a.x[0] = static_cast<const char*>(q);
   a.x[1] = static_cast<const char*>(k);
@@ -141,7 +149,7 @@ QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* 
   // one wave of CTAs, but no more than have a row for each of their row slots
   const long long T = (long long)p->B * p->N, slots = qk_rows_per_pass(p->d);
   const long long least = std::max(1ll, slots / (p->Hq + p->Hk));
-  const long long wave = (long long)std::min(sms, kQkMaxSms) * (bwd ? kQkBwdCtasPerSm : kQkCtasPerSm);
+  const long long wave = (long long)std::min(sms, kQkMaxSms) * qk_ctas_per_sm(a.any, bwd);
   a.ctas = (int)std::min(wave, (T + least - 1) / least);
   return a;
 }
@@ -313,7 +321,7 @@ fa_status fa_qk_norm_rope(const fa_qk_params* p, const void* q, const void* k, c
 
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_qk_params* p) {
   if (qk_check(p, true) != FA_OK) return 0;
-  return (size_t)kQkMaxSms * kQkBwdCtasPerSm * 2 * p->d * 4;
+  return (size_t)kQkMaxSms * qk_ctas_per_sm(false, true) * 2 * p->d * 4;
 }
 
 fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* k, const void* dyq, const void* dyk,

@@ -23,16 +23,15 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int align16(int n) { return (n + 15) / 16 * 16; }
 
-// Eight consecutive elements, as loaded and as fp32.  (Plain loads: the result may be the
-// input itself.)
+// Eight elements, as loaded and as fp32; in fp32 two words `step` elements apart.
 template <int DT>
 struct Raw8 {
   uint4 u[DT == FA_F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const char* at) {
-    const uint4* p = reinterpret_cast<const uint4*>(at);
+  __device__ __forceinline__ void load(const char* at, int step) {
 #pragma unroll
-    for (int i = 0; i < (DT == FA_F32 ? 2 : 1); ++i) u[i] = p[i];
+    for (int i = 0; i < (DT == FA_F32 ? 2 : 1); ++i) u[i] = *reinterpret_cast<const uint4*>(at + 4 * i * step);
   }
   // as four pairs for packed fp32 arithmetic
   __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
@@ -52,13 +51,13 @@ struct Raw8 {
   }
 };
 template <int DT>
-__device__ __forceinline__ void store8(char* p, const uint64_t (&v)[4]) {
+__device__ __forceinline__ void store8(char* p, int step, const uint64_t (&v)[4]) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f2unpack(v[i], f[2 * i], f[2 * i + 1]);
   if constexpr (DT == FA_F32) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + 4 * step) = make_float4(f[4], f[5], f[6], f[7]);
   } else {
     constexpr bool F16 = DT == FA_F16;
     *reinterpret_cast<uint4*>(p) =
@@ -77,83 +76,91 @@ __device__ __forceinline__ float fsum2(uint64_t v) {
   return x + y;
 }
 
-constexpr int kChunk = 64;  // tokens whose angles a CTA holds at a time
-
-// cos and sin of a chunk's tokens, [token][pair], in shared memory.
-template <int D>
+// cos and sin of a chunk's tokens, [token][pair], in shared memory; with ANY by channel,
+// the sine with its sign, and (1, 0) behind the rotated channels.
+template <int D, bool ANY>
 struct Angles {
-  float c[kChunk][D / 2], s[kChunk][D / 2];
+  static constexpr int W = ANY ? D : D / 2;
+  float *c, *s;
+  __device__ __forceinline__ Angles(char* smem, int chunk)
+      : c(reinterpret_cast<float*>(smem)), s(reinterpret_cast<float*>(smem) + chunk * W) {}
+  __device__ __forceinline__ const float* cos_of(int tok) const { return c + tok * W; }
+  __device__ __forceinline__ const float* sin_of(int tok) const { return s + tok * W; }
 };
-template <int D>
-__device__ __forceinline__ void form_angles(const QkArgs& a, int token0, int n, Angles<D>& out) {
+template <int D, bool ANY>
+__device__ __forceinline__ void form_angles(const QkArgs& a, int token0, int n, const Angles<D, ANY>& out) {
   const int pairs = a.rot / 2;
   for (int e = threadIdx.x; e < n * (D / 2); e += kThreads) {
     const int tok = e / (D / 2), pair = e % (D / 2);
-    if (pair >= pairs) continue;
+    float *c = out.c + tok * out.W, *s = out.s + tok * out.W;
+    if (pair >= pairs) {
+      if constexpr (ANY) {
+        c[2 * pair] = c[2 * pair + 1] = 1.f;
+        s[2 * pair] = s[2 * pair + 1] = 0.f;
+      }
+      continue;
+    }
     const int t = token0 + tok, b = a.divN.div(t), i = t - b * a.N;
     const int pos = a.pos ? __ldg(a.pos + b * a.pos_stride + i) : i;
     const unsigned long long ph = (unsigned long long)(long long)pos * __ldg(a.freqs + pair);
     // signed leading 32 bits: the phase in 2^-32 turns; in half turns for sincospi
-    sincospif((float)(int)(ph >> 32) * 4.656612873077393e-10f, &out.s[tok][pair], &out.c[tok][pair]);
+    float sn, cs;
+    sincospif((float)(int)(ph >> 32) * 4.656612873077393e-10f, &sn, &cs);
+    c[pair] = cs;
+    s[pair] = ANY ? -sn : sn;
+    if constexpr (ANY) {
+      c[pair + pairs] = cs;
+      s[pair + pairs] = sn;
+    }
   }
 }
 
-// Which channels and pairs a lane holds.  With rot % 16 == 0 (or interleaved pairs) the
-// lane's chunks lo, hi hold both elements of its pairs -- element e of lo with element e of
-// hi, or, interleaved, neighbours within each chunk -- and `on` has a bit for each of its
-// eight pairs that is rotated; pl, ph are the first pairs of its chunks.
+// Which channels a lane holds: eight from lo and eight from hi on (in fp32 two words of four
+// each, `step` apart), so that every access of a row's lanes is to neighbouring words.  With
+// rot % 16 == 0 the rotated channels and those behind them have lanes of their own, and
+// element e of lo is paired with element e of hi; interleaved pairs are neighbours anyway,
+// and `on` has a bit for each of the lane's eight pairs that is rotated.
 struct Lane {
-  int lo, hi;  // first channel of each chunk
-  int pl, ph;
+  int lo, hi, step;
   uint32_t on;
 };
 
-template <int D, bool ANY>
+template <int D, int DT, bool ANY>
 __device__ __forceinline__ Lane lane_channels(const QkArgs& a, int j) {
+  constexpr int LPR = D / 16, WORD = DT == FA_F32 ? 4 : 8;
+  const bool split = !ANY && !a.interleaved;
+  const int q = split ? a.rot / 16 : LPR;  // lanes of the rotated channels
+  const bool behind = j >= q;
+  const int n = behind ? LPR - q : q;
   Lane L;
-  const int q = a.rot / 16;  // chunks in the first elements of the rotated pairs
-  L.lo = 8 * j;
-  L.hi = D / 2 + 8 * j;
-  L.on = 0;
-  if (ANY) {
-    L.pl = L.ph = 0;
-  } else if (a.interleaved) {
-    L.pl = L.lo / 2;
-    L.ph = L.hi / 2;
+  L.lo = (behind ? 16 * q : 0) + WORD * (behind ? j - q : j);
+  L.hi = L.lo + 8 * n;
+  L.step = DT == FA_F32 ? 4 * n : 4;
+  L.on = split && !behind ? 0xFFu : 0u;
+  if (a.interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      L.on |= (uint32_t)(L.lo + 2 * i < a.rot) << i;
-      L.on |= (uint32_t)(L.hi + 2 * i < a.rot) << (4 + i);
+      const int ch = (i & 1) * 2 + (i >> 1) * L.step;
+      L.on |= (uint32_t)(L.lo + ch < a.rot) << i;
+      L.on |= (uint32_t)(L.hi + ch < a.rot) << (4 + i);
     }
-  } else if (j < q) {
-    L.hi = 8 * (j + q);
-    L.pl = L.lo;
-    L.ph = L.lo + 4;
-    L.on = 0xFFu;
-  } else {  // behind the rotated channels: two neighbouring chunks
-    L.lo = 8 * (2 * j);
-    L.hi = 8 * (2 * j + 1);
-    L.pl = L.ph = 0;
   }
   return L;
 }
 
 // Rotates the lane's pairs (back with BACK).
-template <int D, bool BACK>
+template <bool BACK>
 __device__ __forceinline__ void rotate(const QkArgs& a, const Lane& L, const float* c_row, const float* s_row,
                                        uint64_t (&lo)[4], uint64_t (&hi)[4]) {
   if (L.on == 0) return;
   uint64_t c[4], s[4];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(c_row + (k ? L.ph : L.pl));
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s_row + (k ? L.ph : L.pl));
-    c[2 * k] = u.x;
-    c[2 * k + 1] = u.y;
-    s[2 * k] = v.x;
-    s[2 * k + 1] = v.y;
-  }
   if (a.interleaved) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int pair = ((k < 2 ? L.lo : L.hi) + (k & 1) * L.step) / 2;
+      c[k] = *reinterpret_cast<const uint64_t*>(c_row + pair);
+      s[k] = *reinterpret_cast<const uint64_t*>(s_row + pair);
+    }
     float cf[8], sf[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -173,6 +180,15 @@ __device__ __forceinline__ void rotate(const QkArgs& a, const Lane& L, const flo
     }
   } else {
 #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(c_row + L.lo + k * L.step);
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s_row + L.lo + k * L.step);
+      c[2 * k] = u.x;
+      c[2 * k + 1] = u.y;
+      s[2 * k] = v.x;
+      s[2 * k + 1] = v.y;
+    }
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint64_t uc = fmul2(lo[i], c[i]), us = fmul2(lo[i], s[i]);
       lo[i] = BACK ? ffma2(hi[i], s[i], uc) : fsub2(uc, fmul2(hi[i], s[i]));
@@ -183,29 +199,45 @@ __device__ __forceinline__ void rotate(const QkArgs& a, const Lane& L, const flo
 
 // A rotated range whose halves are no whole chunks (rot % 16 != 0, pairs i and
 // i + rot / 2): the row goes through shared memory and every element finds its
-// partner there.  All lanes of the row's group call it.
+// partner there.  Four words are left free after each 32 and one after each row, so that
+// the lanes of a warp, 8 channels apart, meet different banks (with the rows packed the
+// forward pass of 64 + 16 heads, N = 19735, d = 64 took 276 us, and 121 so).  All lanes of
+// the row's group call it.
+template <int D>
+struct AnyRow {
+  static constexpr int stride = D + D / 32 * 4 + 1;  // floats
+  static __device__ __forceinline__ int at(int ch) { return ch + (ch >> 5) * 4; }
+};
 template <int D, bool BACK>
 __device__ __forceinline__ void rotate_any(const QkArgs& a, float* row, const Lane& L, const float* c_row,
                                            const float* s_row, uint64_t (&lo)[4], uint64_t (&hi)[4]) {
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    *reinterpret_cast<uint64_t*>(row + L.lo + 2 * i) = lo[i];
-    *reinterpret_cast<uint64_t*>(row + L.hi + 2 * i) = hi[i];
-  }
+  using R = AnyRow<D>;
   __syncwarp();
   const int half = a.rot / 2;
-  auto turned = [&](int ch) {
-    if (ch >= a.rot) return row[ch];
-    const int pair = ch < half ? ch : ch - half;
-    const float c = c_row[pair], s = BACK ? -s_row[pair] : s_row[pair];
-    const float u = row[pair], v = row[pair + half];
-    return ch < half ? u * c - v * s : u * s + v * c;
-  };
+  auto channel = [&](int i) { return (i < 4 ? L.lo : L.hi) + (i & 1) * 2 + ((i >> 1) & 1) * L.step; };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = f2pack(turned(L.lo + 2 * i), turned(L.lo + 2 * i + 1));
-    hi[i] = f2pack(turned(L.hi + 2 * i), turned(L.hi + 2 * i + 1));
+  for (int i = 0; i < 8; ++i) {
+    float* p = row + R::at(channel(i));
+    f2unpack(i < 4 ? lo[i & 3] : hi[i & 3], p[0], p[1]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int ch = channel(2 * k);
+    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(c_row + ch);
+    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(s_row + ch);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int x = ch + e, partner = x < half ? x + half : x - half;
+      v[e] = x < a.rot ? row[R::at(partner)] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint64_t& x = (k < 2 ? lo : hi)[2 * (k & 1) + e];
+      const uint64_t y = fmul2(f2pack(v[2 * e], v[2 * e + 1]), e ? s.y : s.x), z = fmul2(x, e ? c.y : c.x);
+      x = BACK ? fsub2(z, y) : fadd2(z, y);
+    }
   }
 }
 
@@ -248,14 +280,14 @@ __device__ __forceinline__ P row_at(const Row& r, P const (&base)[2], const long
 
 // A lane's eight weights from channel c on, as pairs.
 template <int DT>
-__device__ __forceinline__ void weights8(const void* w, bool w_f32, int c, uint64_t (&v)[4]) {
+__device__ __forceinline__ void weights8(const void* w, bool w_f32, int c, int step, uint64_t (&v)[4]) {
   if (w_f32) {
     Raw8<FA_F32> r;
-    r.load(static_cast<const char*>(w) + 4 * c);
+    r.load(static_cast<const char*>(w) + 4 * c, step);
     r.get(v);
   } else {
     Raw8<DT> r;
-    r.load(static_cast<const char*>(w) + (DT == FA_F32 ? 4 : 2) * c);
+    r.load(static_cast<const char*>(w) + (DT == FA_F32 ? 4 : 2) * c, step);
     r.get(v);
   }
 }
@@ -264,12 +296,12 @@ __device__ __forceinline__ void weights8(const void* w, bool w_f32, int c, uint6
 struct Run {
   int first, last, chunk;
 };
-__device__ __forceinline__ Run run_of(const QkArgs& a) {
+__device__ __forceinline__ Run run_of(const QkArgs& a, int most) {
   Run r;
   const long long T = (long long)a.B * a.N;
   r.first = (int)(T * blockIdx.x / gridDim.x);
   r.last = (int)(T * (blockIdx.x + 1) / gridDim.x);
-  const int n = r.last - r.first, chunks = (n + kChunk - 1) / kChunk;
+  const int n = r.last - r.first, chunks = (n + most - 1) / most;
   r.chunk = chunks ? (n + chunks - 1) / chunks : 1;
   return r;
 }
@@ -286,11 +318,11 @@ struct Feed {
     // a slot without a row works on zeros or an earlier row's values: never on garbage
     for (int i = 0; i < kAhead * N * V; ++i) st_shared_v4(base + i * kThreads * 16, 0, 0, 0, 0);
   }
-  __device__ __forceinline__ void load(int turn, int chunk, const char* src) const {
+  __device__ __forceinline__ void load(int turn, int chunk, const char* src, int step) const {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + ((turn * N + chunk) * V + v) * kThreads * 16),
-                   "l"(src + 16 * v)
+                   "l"(src + 4 * v * step)
                    : "memory");
   }
   static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -304,44 +336,59 @@ struct Feed {
   }
 };
 
-// Shared memory: the angles, the weights in fp32 (forward), rows for rotate_any, the feed.
+template <bool ANY, bool BWD>
+constexpr int kCtasPerSm = BWD ? 2 : ANY ? 3 : 4;
+
+// Shared memory: the weights in fp32 (forward), rows for rotate_any, the feed, and the angles
+// of as many tokens as the rest of a CTA's part of the SM holds, 64 at most (128 at d = 64).
 template <int D, int DT, bool ANY, bool BWD>
-constexpr int smem_bytes() {
-  return (int)sizeof(Angles<D>) + 2 * D * 4 + (ANY ? kThreads * 16 * 4 : 0) + Feed<DT, BWD ? 4 : 2>::bytes;
-}
+struct Smem {
+  static constexpr int ctas = kCtasPerSm<ANY, BWD>;
+  static constexpr int rows = BWD ? 0 : 2 * D * 4;  // behind the weights
+  static constexpr int feed = align16(rows + (ANY ? kThreads / (D / 16) * AnyRow<D>::stride * 4 : 0));
+  static constexpr int angles = feed + Feed<DT, BWD ? 4 : 2>::bytes;
+  static constexpr int token = 2 * Angles<D, ANY>::W * 4;
+  static constexpr int room = (228 * 1024 / ctas - 1024 - (BWD ? 2 * (kThreads / 32) * D * 4 : 0) - angles) / token;
+  static constexpr int most = 64 * 128 / D;
+  static constexpr int chunk = room < most ? room : most;
+  static constexpr int bytes = angles + chunk * token;
+  static_assert(chunk >= 16, "angles of a chunk");
+};
 
 template <int D, int DT, bool ANY>
-__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
+__global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, E = DT == FA_F32 ? 4 : 2;
+  using S = Smem<D, DT, ANY, false>;
   extern __shared__ __align__(16) char smem[];
-  Angles<D>& ang = *reinterpret_cast<Angles<D>*>(smem);
-  float* w_s = reinterpret_cast<float*>(smem + sizeof(Angles<D>));
-  float* rows_s = w_s + 2 * D;
-  const Feed<DT, 2> feed(smem + sizeof(Angles<D>) + 2 * D * 4 + (ANY ? kThreads * 16 * 4 : 0));
+  const Angles<D, ANY> ang(smem + S::angles, S::chunk);
+  float* w_s = reinterpret_cast<float*>(smem);
+  const Feed<DT, 2> feed(smem + S::feed);
   constexpr int AHEAD = Feed<DT, 2>::kAhead;
   const int slot = threadIdx.x / LPR;
-  const Lane L = lane_channels<D, ANY>(a, threadIdx.x % LPR);
+  float* row_s = reinterpret_cast<float*>(smem + S::rows) + slot * AnyRow<D>::stride;
+  Lane L = lane_channels<D, DT, ANY>(a, threadIdx.x % LPR);
+  if (DT != FA_F32) L.step = 4;
   for (int e = threadIdx.x; e < 2 * D / 8; e += kThreads) {
     uint64_t v[4];
-    weights8<DT>(e < D / 8 ? a.w[0] : a.w[1], w_f32, 8 * (e % (D / 8)), v);
+    weights8<DT>(e < D / 8 ? a.w[0] : a.w[1], w_f32, 8 * (e % (D / 8)), 4, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) reinterpret_cast<uint64_t*>(w_s)[4 * e + i] = v[i];
   }
-  const Run run = run_of(a);
+  const Run run = run_of(a, S::chunk);
   for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
     const int nt = min(run.chunk, run.last - t0), rows = nt * (a.Hq + a.Hk);
     auto load = [&](int turn, int i) {
       if (i < rows) {
         const char* p = row_at(row_of(a, -1, t0, i), a.x, a.xb, a.xn, a.xh);
-        feed.load(turn, 0, p + L.lo * E);
-        feed.load(turn, 1, p + L.hi * E);
+        feed.load(turn, 0, p + L.lo * E, L.step);
+        feed.load(turn, 1, p + L.hi * E, L.step);
       }
       feed.commit();
     };
 #pragma unroll
     for (int k = 0; k < AHEAD - 1; ++k) load(k, slot + k * ROWS);
     __syncthreads();  // the angles before have been used
-    form_angles<D>(a, t0, nt, ang);
+    form_angles(a, t0, nt, ang);
     __syncthreads();
     // every lane of a warp takes the same number of turns: the row sums are shuffles
     int turn = 0;
@@ -360,24 +407,24 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const QkArgs 
 #pragma unroll
       for (int i = 0; i < 4; ++i) ss = ffma2(hi[i], hi[i], ss);
       const uint64_t rn = fdup(rsqrtf(row_sum<D>(fsum2(ss)) * (1.f / D) + a.eps));
-      const ulonglong2 *wl = reinterpret_cast<const ulonglong2*>(w_s + r.t * D + L.lo),
-                       *wh = reinterpret_cast<const ulonglong2*>(w_s + r.t * D + L.hi);
+      const float *wl = w_s + r.t * D + L.lo, *wh = w_s + r.t * D + L.hi;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const ulonglong2 u = wl[i], v = wh[i];
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(wl + i * L.step),
+                         v = *reinterpret_cast<const ulonglong2*>(wh + i * L.step);
         lo[2 * i] = fmul2(fmul2(lo[2 * i], rn), u.x);
         lo[2 * i + 1] = fmul2(fmul2(lo[2 * i + 1], rn), u.y);
         hi[2 * i] = fmul2(fmul2(hi[2 * i], rn), v.x);
         hi[2 * i + 1] = fmul2(fmul2(hi[2 * i + 1], rn), v.y);
       }
       if constexpr (ANY)
-        rotate_any<D, false>(a, rows_s + slot * D, L, ang.c[r.tok], ang.s[r.tok], lo, hi);
+        rotate_any<D, false>(a, row_s, L, ang.cos_of(r.tok), ang.sin_of(r.tok), lo, hi);
       else
-        rotate<D, false>(a, L, ang.c[r.tok], ang.s[r.tok], lo, hi);
+        rotate<false>(a, L, ang.cos_of(r.tok), ang.sin_of(r.tok), lo, hi);
       if (live) {
         char* p = row_at(r, a.y, a.yb, a.yn, a.yh);
-        store8<DT>(p + L.lo * E, lo);
-        store8<DT>(p + L.hi * E, hi);
+        store8<DT>(p + L.lo * E, L.step, lo);
+        store8<DT>(p + L.hi * E, L.step, hi);
       }
     }
   }
@@ -388,17 +435,19 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const QkArgs 
 // weights' gradients of its channels, its warp's sums are kept in shared memory from one
 // change of tensor to the next, and each CTA leaves one partial sum for each tensor.
 template <int D, int DT, bool ANY>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkArgs a, const bool w_f32) {
+__global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, true>::ctas) qk_norm_rope_bwd_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, WARPS = kThreads / 32, E = DT == FA_F32 ? 4 : 2;
+  using S = Smem<D, DT, ANY, true>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2][WARPS][D];
-  Angles<D>& ang = *reinterpret_cast<Angles<D>*>(smem);
-  float* rows_s = reinterpret_cast<float*>(smem + sizeof(Angles<D>)) + 2 * D;
-  const Feed<DT, 4> feed(smem + sizeof(Angles<D>) + 2 * D * 4 + (ANY ? kThreads * 16 * 4 : 0));
+  const Angles<D, ANY> ang(smem + S::angles, S::chunk);
+  const Feed<DT, 4> feed(smem + S::feed);
   constexpr int AHEAD = Feed<DT, 4>::kAhead;
   const int slot = threadIdx.x / LPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Lane L = lane_channels<D, ANY>(a, threadIdx.x % LPR);
-  const Run run = run_of(a);
+  float* row_s = reinterpret_cast<float*>(smem + S::rows) + slot * AnyRow<D>::stride;
+  Lane L = lane_channels<D, DT, ANY>(a, threadIdx.x % LPR);
+  if (DT != FA_F32) L.step = 4;
+  const Run run = run_of(a, S::chunk);
   for (int e = lane; e < 2 * D; e += 32) red[e / D][warp][e % D] = 0.f;
   __syncwarp();
   for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
@@ -415,23 +464,23 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkA
       const Row r = row_in(i, live);
       if (live) {
         const char *p = row_at(r, a.x, a.xb, a.xn, a.xh), *q = row_at(r, a.dy, a.db, a.dn, a.dh);
-        feed.load(place, 0, p + L.lo * E);
-        feed.load(place, 1, p + L.hi * E);
-        feed.load(place, 2, q + L.lo * E);
-        feed.load(place, 3, q + L.hi * E);
+        feed.load(place, 0, p + L.lo * E, L.step);
+        feed.load(place, 1, p + L.hi * E, L.step);
+        feed.load(place, 2, q + L.lo * E, L.step);
+        feed.load(place, 3, q + L.hi * E, L.step);
       }
       feed.commit();
     };
 #pragma unroll
     for (int k = 0; k < AHEAD - 1; ++k) load(k, k);
     __syncthreads();  // the angles before have been used
-    form_angles<D>(a, t0, nt, ang);
+    form_angles(a, t0, nt, ang);
     __syncthreads();
     int place = 0;
     for (int t = 0, i = 0; t < 2; ++t) {
       uint64_t wl[4], wh[4], acc[8];
-      weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, wl);
-      weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, wh);
+      weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, L.step, wl);
+      weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, L.step, wh);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = 0;
 #pragma unroll 1
@@ -447,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkA
         feed.get(place, 3, gh);
         place = place + 1 == AHEAD ? 0 : place + 1;
         if constexpr (ANY)
-          rotate_any<D, true>(a, rows_s + slot * D, L, ang.c[r.tok], ang.s[r.tok], gl, gh);
+          rotate_any<D, true>(a, row_s, L, ang.cos_of(r.tok), ang.sin_of(r.tok), gl, gh);
         else
-          rotate<D, true>(a, L, ang.c[r.tok], ang.s[r.tok], gl, gh);
+          rotate<true>(a, L, ang.cos_of(r.tok), ang.sin_of(r.tok), gl, gh);
         uint64_t ss = 0, sd = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -468,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkA
             hi[k] = fmul2(rn2, ffma2(hi[k], m2, fmul2(gh[k], wh[k])));
           }
           char* p = row_at(r, a.y, a.yb, a.yn, a.yh);
-          store8<DT>(p + L.lo * E, lo);
-          store8<DT>(p + L.hi * E, hi);
+          store8<DT>(p + L.lo * E, L.step, lo);
+          store8<DT>(p + L.hi * E, L.step, hi);
         }
       }
 #pragma unroll
@@ -480,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const QkA
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int off = LPR; off < 32; off <<= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], off);
-          if (lane < LPR) red[t][warp][(k < 4 ? L.lo : L.hi) + 2 * (k & 3) + c] += v[c];
+          if (lane < LPR) red[t][warp][(k < 4 ? L.lo : L.hi) + ((k >> 1) & 1) * L.step + 2 * (k & 1) + c] += v[c];
         }
       }
     }
@@ -525,13 +574,13 @@ cudaError_t launch_one(K kernel, int smem, const QkArgs& a, bool w_f32, cudaStre
 
 template <int D, int DT>
 cudaError_t launch_d(const QkArgs& a, bool w_f32, bool bwd, cudaStream_t s) {
-  const bool any = !a.interleaved && a.rot % 16 != 0;
+  const bool any = a.any;
   if (a.ctas > 0) {
     const cudaError_t e =
-        bwd ? (any ? launch_one(qk_norm_rope_bwd_kernel<D, DT, true>, smem_bytes<D, DT, true, true>(), a, w_f32, s)
-                   : launch_one(qk_norm_rope_bwd_kernel<D, DT, false>, smem_bytes<D, DT, false, true>(), a, w_f32, s))
-            : (any ? launch_one(qk_norm_rope_kernel<D, DT, true>, smem_bytes<D, DT, true, false>(), a, w_f32, s)
-                   : launch_one(qk_norm_rope_kernel<D, DT, false>, smem_bytes<D, DT, false, false>(), a, w_f32, s));
+        bwd ? (any ? launch_one(qk_norm_rope_bwd_kernel<D, DT, true>, Smem<D, DT, true, true>::bytes, a, w_f32, s)
+                   : launch_one(qk_norm_rope_bwd_kernel<D, DT, false>, Smem<D, DT, false, true>::bytes, a, w_f32, s))
+            : (any ? launch_one(qk_norm_rope_kernel<D, DT, true>, Smem<D, DT, true, false>::bytes, a, w_f32, s)
+                   : launch_one(qk_norm_rope_kernel<D, DT, false>, Smem<D, DT, false, false>::bytes, a, w_f32, s));
     if (e != cudaSuccess) return e;
   }
   if (!bwd) return cudaSuccess;
@@ -560,6 +609,9 @@ cudaError_t launch(const QkArgs& a, int d, int dtype, bool w_f32, bool bwd, cuda
 
 }  // namespace
 
+int qk_ctas_per_sm(bool any, bool bwd) {
+  return bwd ? kCtasPerSm<false, true> : any ? kCtasPerSm<true, false> : kCtasPerSm<false, false>;
+}
 int qk_rows_per_pass(int d) { return kThreads / (d / 16); }
 
 cudaError_t launch_qk_norm_rope(const QkArgs& a, int d, int dtype, bool w_f32, cudaStream_t s) {

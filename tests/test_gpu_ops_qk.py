@@ -74,6 +74,11 @@ CASES = [  # B, N, Hq, Hk, d, dtype, rot, interleaved, heads_first, positions
     (1, 8, 2, 1, 64, "f32", 2, False, False, "negative"),
     (1, 700, 12, 4, 64, "bf16", 64, False, True, None),  # several tiles and turns
     (2, 300, 40, 8, 128, "bf16", 128, False, True, "far"),
+    (2, 40, 3, 1, 64, "bf16", 48, False, False, "row"),  # a rotated part of a 64-channel head
+    (1, 1500, 20, 4, 64, "f32", 32, False, True, None),
+    (1, 900, 12, 12, 128, "f32", 90, False, False, "far"),
+    (2, 33, 3, 2, 64, "f32", 24, True, False, None),
+    (2, 50, 2, 1, 128, "f32", 96, False, True, None),
 ]
 
 
