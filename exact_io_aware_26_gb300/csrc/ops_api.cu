@@ -404,6 +404,8 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   if (!workspace || workspace_bytes < want || !aligned(workspace, 256))
     return fail(FA_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", workspace,
                 workspace_bytes, want);
+  // shares read a request's queries when another has already written its rows
+  if (p->T > 0 && o == q) return fail(FA_ERR_INVALID, "o lies over q");
   Report rep;
   int sms = 0;
   FA_TRY(api_device(&rep, &sms));

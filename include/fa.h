@@ -346,7 +346,7 @@ fa_status fa_fwd_fp8(const fa_params* p, const void* q8, const void* k8, const v
  * position, and its leading 32 bits give the angle to 2^-32 turns.
  *
  *   B, N, Hq, Hk, d  batch, tokens per batch entry (>= 0), query and key heads,
- *               head size (64 or 128); B*N < 2^30.
+ *               head size (64 or 128); B*N < 2^30, Hq + Hk < 2^24.
  *   dtype       fa_dtype of q, k, yq, yk and their gradients (fp32 arithmetic
  *               inside); weight_dtype that of wq, wk: `dtype` or FA_F32.
  *   eps         positive and finite.
@@ -382,7 +382,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(const fa_qk_params* p);
  * dz the back-rotated dy and h = x r, dx = r (w dz - h mean(w dz h)) and
  * dw = sum over rows of dz h (fp32 [d] each, summed in a fixed order).  q and k
  * are the forward's inputs; r is formed again.  The workspace is 256-byte
- * aligned and owned by the caller; its contents do not matter. */
+ * aligned and owned by the caller; its contents do not matter, and calls that may
+ * run at the same time need workspaces of their own. */
 fa_status fa_qk_norm_rope_bwd(const fa_qk_params* p, const void* q, const void* k, const void* dyq,
                               const void* dyk, const void* wq, const void* wk,
                               const uint64_t* freqs, const int* positions, void* dq, void* dk,
@@ -411,7 +412,8 @@ typedef struct {
 /* Bytes of a 16-token block of one head: 2560 for d = 128, 1280 for d = 64, else 0. */
 int fa_kv4_block_bytes(int d);
 
-/* T tokens' keys and values ([T][Hk][d], element strides {token, head}, of `dtype`). */
+/* T tokens' keys and values ([T][Hk][d], element strides {token, head}, of `dtype`);
+ * T*Hk < 2^30, strides below 2^31 elements. */
 typedef struct {
   int T, dtype;
   long long k_stride[2], v_stride[2];
@@ -450,6 +452,9 @@ fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
  * Lengths are device memory: the tokens of all requests are cut into equal shares
  * on the GPU.  A page outside the cache contributes nothing and is recorded as
  * FA_ERR_INDEX, as is a length beyond table_width * page_size, which is cut to that.
+ * o must not lie over q.  Calls that may run at the same time need workspaces of their
+ * own.  Limits: T*Hq < 2^31, table_width * page_size <= 2^30, num_pages * page_size < 2^31,
+ * a page below 2^31 bytes.
  */
 typedef struct {
   int R, T, Hq, dtype;
@@ -486,7 +491,7 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
  *   counts[3]                 pages left on the stack, new tokens, pages missing
  * kv_lens may be seq_lens and counts may be free_count (three ints): everything is
  * read before anything is written.  Lengths below 0 count as 0 tokens; all arrays
- * are device int32.  R in [1, FA_PLAN_MAX_REQUESTS].
+ * are device int32.  R in [1, FA_PLAN_MAX_REQUESTS], T and num_pages at most 2^30.
  */
 #define FA_PLAN_MAX_REQUESTS 8192
 typedef struct {

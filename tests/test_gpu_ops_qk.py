@@ -170,6 +170,40 @@ def test_in_place_and_zero_tokens(cuda_lib):
     assert float(dwq.abs().sum()) == 0 and float(dwk.abs().sum()) == 0
 
 
+@pytest.mark.parametrize("dtype,d,rot", [("bf16", 128, 128), ("f32", 64, 32), ("f16", 64, 18)])
+def test_gradients_over_their_inputs(cuda_lib, dtype, d, rot):
+    """dq, dk written over q, k and over dyq, dyk: the same bits as elsewhere."""
+    q, k, wq, wk, g = make(2, 300, 5, 2, d, dtype, 17, packed=False)
+    freqs = fa.rope_freqs(rot)
+    dyq, dyk = (torch.randn(x.shape, generator=g).to(x.dtype).cuda() for x in (q, k))
+    want = fa.qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, heads_first=False)
+    over_dy = [x.clone() for x in (dyq, dyk)]
+    got = fa.qk_norm_rope_bwd(q, k, *over_dy, wq, wk, freqs, heads_first=False, dq=over_dy[0], dk=over_dy[1])
+    assert got[0].data_ptr() == over_dy[0].data_ptr() and all(torch.equal(a, b) for a, b in zip(got, want))
+    got = fa.qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, heads_first=False, dq=q, dk=k)
+    assert got[0].data_ptr() == q.data_ptr() and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_calls_at_once(cuda_lib):
+    """Forward and backward passes of two inputs on two streams; results equal to plain calls'."""
+    sets = []
+    for seed, (N, rot) in enumerate(((2000, 64), (700, 30))):
+        q, k, wq, wk, g = make(1, N, 8, 8, 64, "bf16", 40 + seed)
+        dyq, dyk = (torch.randn(1, 8, N, 64, generator=g).bfloat16().cuda() for _ in range(2))
+        sets.append((q, k, dyq, dyk, wq, wk, fa.rope_freqs(rot)))
+    run = lambda q, k, dyq, dyk, wq, wk, f, stream=None: (fa.qk_norm_rope(q, k, wq, wk, f, stream=stream)
+                                                         + fa.qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, f, stream=stream))
+    want = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(10):
+        got += [[run(*s, stream=t), w] for s, t, w in zip(sets, side, want)]
+    torch.cuda.synchronize()
+    for g, w in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
 def test_rows_of_zeros_infinities_and_nans_stay_in_their_rows(cuda_lib):
     q, k, wq, wk, _ = make(1, 16, 2, 1, 64, "f32", 21, packed=False)
     freqs = fa.rope_freqs(64)

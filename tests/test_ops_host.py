@@ -181,6 +181,9 @@ def test_attention_pointers(lib):
             assert lib.fa_kv4_attention(c, p, *a, OK, need, None) == fa.FA_ERR_INVALID
     for ws, n in ((None, need), (OK, need - 1), (OK + 16, need)):
         assert lib.fa_kv4_attention(c, p, *[OK] * 7, ws, n, None) == fa.FA_ERR_WORKSPACE
+    a = [OK] * 7  # a result over its queries, which other CTAs still read
+    assert lib.fa_kv4_attention(c, p, *a, OK, need, None) == fa.FA_ERR_INVALID
+    assert b"over q" in lib.fa_last_error()
 
 
 @pytest.mark.parametrize("kw,code", [({"R": 0}, -1), ({"T": -1}, -1), ({"page_size": 0}, -1), ({"num_pages": 0}, -1),
