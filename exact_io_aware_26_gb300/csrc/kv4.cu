@@ -1,5 +1,5 @@
 // kv4.cu -- writing tokens' keys and values into the 4-bit cache, and reading them
-// back.  Both are streams: bound by HBM for prompts, by latency for single tokens.
+// back.  Both are streams, of long prompts against HBM, of single tokens against latency.
 // Eight channels per lane (a 16-byte load of a 16-bit type, one 4-byte word of codes),
 // four lanes per pair, whose least and largest are two shuffles each.
 #include "kv4.cuh"
@@ -9,7 +9,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kAppendThreads = 128;
 
 template <int DT>
 __device__ __forceinline__ void load8(const void* base, long long at, float (&v)[8]) {
@@ -61,9 +61,12 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return r;
 }
 
-// Writing prompts is bound by its instructions before HBM; hence packed fp32 arithmetic,
-// three-input minima, one pair per lane (the key's or the value's), and no division or
-// clamping per value where neither can matter.
+// Writing prompts of 16-bit types is bound by its instructions (326 a warp for 512 values,
+// 0.72 issued a cycle) before HBM; hence packed fp32 arithmetic, three-input minima, one pair
+// per lane (the key's or the value's), and no division or clamping per value where neither
+// can matter.  23,400 tokens of 12 heads, d = 64: bf16 27.2 us (94 MB, 3.5 TB/s; 25.3 with
+// sixteen values of each tensor to a lane, where single tokens of 256 requests cost 3.3 us
+// instead of 2.8), fp32 30.0 us (166 MB, 5.5 TB/s).
 
 // Least and largest of a lane's eight values and those of its group of four lanes.
 __device__ __forceinline__ void range8(const float (&v)[8], float& lo, float& hi) {
@@ -139,10 +142,10 @@ __device__ __forceinline__ uint32_t codes8(float (&v)[8], uint32_t pair, float i
 
 // A row is one head of one token: D / 8 lanes, which take its key and its value.
 template <int D, int DT>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4RowArgs a) {
   using Blk = KvBlock<D>;
   constexpr int LPR = D / 8;
-  const int j = threadIdx.x % LPR, r = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+  const int j = threadIdx.x % LPR, r = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
   const bool live = r < a.rows;
   const int tok = a.heads.div(r), head = r - tok * (int)a.heads.d;
   float k[8] = {}, v[8] = {};
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowArgs a
 }
 
 template <int DT>
-__device__ __forceinline__ void store_values(void* x, long long to, uint32_t word, uint32_t pair) {
+__device__ __forceinline__ void store_values(void* x, long long to, bool live, uint32_t word, uint32_t pair) {
   // codes p and p + 4 of the word as half2, then neighbours side by side
   const __half2 p = *reinterpret_cast<const __half2*>(&pair);
   uint32_t q[4];
@@ -185,8 +188,19 @@ __device__ __forceinline__ void store_values(void* x, long long to, uint32_t wor
     const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&m), __low2half2(p), __high2half2(p));
     q[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  const uint32_t n[4] = {__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
-                         __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632)};
+  uint32_t n[4] = {__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                   __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632)};
+  // fp32: two lanes swap halves, so that their stores lie side by side (whole sectors)
+  const int odd = threadIdx.x & 1;
+  if constexpr (DT == FA_F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? n[i] : n[2 + i], 1);
+      n[i] = odd ? got : n[i];
+      n[2 + i] = odd ? n[2 + i] : got;
+    }
+  }
+  if (!live) return;
   if constexpr (DT == FA_F16) {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + to) = make_uint4(n[0], n[1], n[2], n[3]);
   } else {
@@ -194,9 +208,9 @@ __device__ __forceinline__ void store_values(void* x, long long to, uint32_t wor
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = unpack2<true>(n[i]);
     if constexpr (DT == FA_F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + to);
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + to - 4 * odd);
       o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-      o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+      o[2] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     } else {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + to) =
           make_uint4(pack2<false>(f[0].x, f[0].y), pack2<false>(f[1].x, f[1].y), pack2<false>(f[2].x, f[2].y),
@@ -205,7 +219,9 @@ __device__ __forceinline__ void store_values(void* x, long long to, uint32_t wor
   }
 }
 
-// Two rows per lane, so that two chains of loads (slot, then codes) are in flight.
+// Two rows per lane, so that two chains of loads (slot, then codes) are in flight: what
+// there is of latency bounds it.  23,400 tokens of 12 heads, d = 64: bf16 20.6 us (94 MB, 4.6
+// TB/s), fp32 33.0 us (166 MB, 5.0 TB/s; 42.6 with each lane's 32 bytes in two stores).
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4RowArgs a) {
   using Blk = KvBlock<D>;
@@ -231,19 +247,20 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4RowArgs a
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if (r0 + i * ROWS >= a.rows) return;
-    store_values<DT>(a.x[0], row_at(a, 0, tok[i], head[i]) + 8 * j, wk[i], pk[i]);
-    store_values<DT>(a.x[1], row_at(a, 1, tok[i], head[i]) + 8 * j, wv[i], pv[i]);
+    const bool live = r0 + i * ROWS < a.rows;
+    store_values<DT>(a.x[0], row_at(a, 0, tok[i], head[i]) + 8 * j, live, wk[i], pk[i]);
+    store_values<DT>(a.x[1], row_at(a, 1, tok[i], head[i]) + 8 * j, live, wv[i], pv[i]);
   }
 }
 
 template <int D, int DT>
 cudaError_t launch(const Kv4RowArgs& a, bool gather, cudaStream_t s) {
-  const int per = kThreads / (D / 8) * (gather ? 2 : 1), grid = (a.rows + per - 1) / per;
-  if (gather)
-    kv4_gather_kernel<D, DT><<<grid, kThreads, 0, s>>>(a);
-  else
-    kv4_append_kernel<D, DT><<<grid, kThreads, 0, s>>>(a);
+  auto grid = [&](int rows) { return (a.rows + rows - 1) / rows; };
+  if (gather) {
+    kv4_gather_kernel<D, DT><<<grid(2 * kThreads / (D / 8)), kThreads, 0, s>>>(a);
+  } else {
+    kv4_append_kernel<D, DT><<<grid(kAppendThreads / (D / 8)), kAppendThreads, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 
