@@ -1,8 +1,8 @@
 // kv4.cuh -- the 4-bit cache's block: 16 tokens of one head,
 //   key codes [16][D / 2] bytes | key pairs [16][D / 32] half2 (scale, base) |
 //   value codes | value pairs.
-// One block is what a warp of the attention kernel takes at a time: contiguous, so
-// that a single bulk copy brings it, whatever the page size.  Code c stands for
+// A block is contiguous, so that a single bulk copy brings it, whatever the page size (two
+// blocks side by side, a unit of the attention kernel, in one).  Code c stands for
 // fp16(base + scale * (1 + c / 16)): 1 + c / 16 is the fp16 number with bits
 // 0x3C00 | c << 6, so that a mask and one half2 fused multiply-add give two values.
 #pragma once

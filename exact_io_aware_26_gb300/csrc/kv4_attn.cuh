@@ -36,7 +36,12 @@
 //     the first, it waits for it on the GPU).
 //   - clusters, for few tiles of few units: the CTAs of a cluster divide a tile evenly and
 //     join through distributed shared memory; one launch, nothing in device memory.
-// kv4_way chooses, by the number of tiles and the units a warp would take.
+// kv4_cluster (ops_api.cu) chooses, by the number of tiles and the units a warp would take.
+//
+// Measured (shares): 64 requests of up to 16384 tokens, 32 query and 8 key heads, d = 128:
+// 149 us for 748 MB, 5.0 TB/s; the unit loop alone goes at 5.9 TB/s, with the integer pipe at
+// 54% (codes to fp16) and four warps a scheduler, and about 16 us are start-up, uneven ends
+// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.4 us.
 #pragma once
 #include "kv4.cuh"
 #include "ops.h"

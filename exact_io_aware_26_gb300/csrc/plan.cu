@@ -6,6 +6,8 @@
 // inputs.  Then the CTAs are one cluster, which meets once all inputs have been read.
 // Integers in a fixed order, no atomics.  Bound by latency (a step writes 8 bytes per
 // token): the time goes into chains of searches and loads, so few tokens per thread.
+// Measured: 256 requests of a token each 7.0 us, 96 requests with 65,536 tokens 7.2 us (as
+// one cluster of 8 CTAs 15.3 us).
 #include "ops.h"
 #include "ptx.cuh"
 

@@ -355,6 +355,9 @@ struct Smem {
   static_assert(chunk >= 16, "angles of a chunk");
 };
 
+// The forward pass.  Measured: 23,400 tokens of 12 + 12 heads, d = 64, bf16 26.5 us (144 MB,
+// 5.4 TB/s; three CTAs an SM 27.3 us), bound by issue slots (0.67 a cycle) and HBM together;
+// 19,735 tokens of 64 + 16 heads, d = 64, fp32 142 us (808 MB, 5.7 TB/s).
 template <int D, int DT, bool ANY>
 __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, E = DT == FA_F32 ? 4 : 2;
@@ -434,6 +437,9 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_no
 // token by token in one loop, with the sums of both, measured 10% slower): a lane adds up the
 // weights' gradients of its channels, its warp's sums are kept in shared memory from one
 // change of tensor to the next, and each CTA leaves one partial sum for each tensor.
+// Measured: 2 x 16384 tokens of 16 + 16 heads, d = 128, bf16 127 us (805 MB, 6.3 TB/s, 94% of a
+// copy); 4 x 2048 of 12 + 12, d = 64, 20 us (75 MB), of which start-up, angles and the
+// weights' sums are 8.
 template <int D, int DT, bool ANY>
 __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, true>::ctas) qk_norm_rope_bwd_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, WARPS = kThreads / 32, E = DT == FA_F32 ? 4 : 2;
@@ -544,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, true>::ctas) qk_nor
   }
 }
 
-// dw: the partial sums of all CTAs, in a fixed order.  One CTA per 32 channels.
+// dw: the partial sums of all CTAs, in a fixed order.  One CTA per 32 channels; it is
+// launched with the kernel before and waits for its end on the GPU (5.8 us by itself).
 __global__ void __launch_bounds__(1024) qk_dw_kernel(const QkArgs a, const int ctas, const int D) {
   __shared__ float red[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
