@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   int stage = 0;
   uint32_t parity = 0;
   int4 meta = make_int4(-1, 0, 0, 0);
-  int meta_q0 = 0;
+  int meta_q0 = 0, meta_c0 = 0;
   long long tile0 = CL ? 0 : start_u;
   uint32_t rank = 0, ctas = 1;
   long long index = 0;
@@ -916,9 +916,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       }
       if (tid == 0) {
         const long long tile_end = tile0 + y.n_u;
-        if (goes_on && !from_before) {
+        if (goes_on) {  // this share's last tile
           meta = make_int4(y.row0, y.rows, cw.h, (int)((tile_end - 1) / share));
           meta_q0 = x.q0;
+          meta_c0 = from_before ? (int)(tile0 / share) : (int)blockIdx.x;
         }
         if (tile_end < u1) {
           Walk<ROWS> w = cw;
@@ -933,92 +934,132 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   }
   if (!CL && tid == 0) {
     a.meta[2 * blockIdx.x] = meta;
-    a.meta[2 * blockIdx.x + 1] = make_int4(meta_q0, 0, 0, 0);
+    a.meta[2 * blockIdx.x + 1] = make_int4(meta_q0, meta_c0, 0, 0);
   }
 }
 
-// Adds the shares of the tile that starts in share blockIdx.x and goes on, if any; RPB rows of
-// it from RPB blockIdx.y on.  The warps divide the shares, each lane D / 32 channels.
-// RPB: 8, or 1 with few tiles, each of which may be cut into hundreds of shares (one tile of
-// 65,536 tokens: 88 us with eight rows to a block).
+// Adds the shares of the tiles that were cut.  A tile cut into k shares has k - 1 blocks here,
+// those of its shares but the last, and as many of them as it has rows divide the rows: a
+// pair of shares is one block's, a tile of hundreds of shares (a long context among short
+// ones) a block's for every row.  Few shares: a warp for each row; many: the block's warps
+// divide a row's shares.  A lane has D / 32 channels.  Bound by the chain: the end of the
+// first kernel, the tile's place, its sums.
 constexpr int kMergeWarps = 8;
-template <int D, int NT, bool F16, int RPB>
-__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4AttnArgs a) {
-  constexpr int ROWS = 8 * NT, CPL = D / 32, LANES = 32 * kMergeWarps / RPB;  // threads that look for a row's maximum
-  __shared__ float top_s[kMergeWarps][RPB], sum_s[kMergeWarps][RPB];
-  __shared__ float acc_s[kMergeWarps][RPB][D + 4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 meta = a.meta[2 * blockIdx.x];  // first row, rows, key head, last share
-  const int q0 = a.meta[2 * blockIdx.x + 1].x;
-  if (meta.x < 0) return;
-  const int r0 = RPB * blockIdx.y, rows = min(RPB, meta.y - r0);
-  if (rows <= 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
-  auto slot = [&](int c, int row) {  // the first share's slot is its second one
-    return a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * ROWS + r0 + row) * (D + 4);
-  };
-  // the rows' largest maxima
-  {
-    float top = kNoMax;
-    const int row = threadIdx.x % RPB;
-    if (row < rows)
-      for (int c = c0 + threadIdx.x / RPB; c <= meta.w; c += LANES) top = fmaxf(top, slot(c, row)[0]);
+// Of shares c, c + step, ... to `last` of a row: the largest maximum, and l and O by it.
+// AT_ONCE of them are on their way together.  (The first share's slot is its second one.)
+template <int D, int ROWS, int AT_ONCE>
+__device__ __forceinline__ void add_shares(const float* part, int row, int c0, int last, int c, int step, float& top,
+                                           float& sum, float (&acc)[D / 32]) {
+  constexpr int CPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  top = kNoMax;
+  sum = 0.f;
 #pragma unroll
-    for (int off = RPB; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane < RPB) top_s[warp][row] = top;
-  }
-  __syncthreads();
-  float top[RPB], sum[RPB] = {}, acc[RPB][CPL] = {};
+  for (int i = 0; i < CPL; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (; c <= last; c += AT_ONCE * step) {
+    float2 ml[AT_ONCE];
+    float v[AT_ONCE][CPL];
 #pragma unroll
-  for (int row = 0; row < RPB; ++row) {
-    top[row] = top_s[0][row];
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int e = c + k * step;
+      ml[k] = make_float2(kNoMax, 0.f);
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) top[row] = fmaxf(top[row], top_s[w][row]);
-  }
-#pragma unroll RPB == 1 ? 8 : 1
-  for (int c = c0 + warp; c <= meta.w; c += kMergeWarps) {
-#pragma unroll
-    for (int row = 0; row < RPB; ++row) {
-      if (row < rows) {
-        const float* s = slot(c, row);
-        const float f = ex2(s[0] - top[row]);
-        sum[row] = fmaf(f, s[1], sum[row]);
-#pragma unroll
-        for (int i = 0; i < CPL; ++i) acc[row][i] = fmaf(f, s[4 + lane * CPL + i], acc[row][i]);
+      for (int i = 0; i < CPL; ++i) v[k][i] = 0.f;
+      if (e <= last) {
+        const float* s = part + ((size_t)(2 * e + (e == c0 ? 1 : 0)) * ROWS + row) * (D + 4);
+        ml[k] = *reinterpret_cast<const float2*>(s);
+        if constexpr (CPL == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(s + 4 + 4 * lane);
+          v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
+        } else {
+          const float2 u = *reinterpret_cast<const float2*>(s + 4 + 2 * lane);
+          v[k][0] = u.x; v[k][1] = u.y;
+        }
       }
     }
+    float t = top;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) t = fmaxf(t, ml[k].x);
+    const float f = ex2(top - t);
+    top = t;
+    sum *= f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) acc[i] *= f;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const float g = ex2(ml[k].x - t);
+      sum = fmaf(g, ml[k].y, sum);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) acc[i] = fmaf(g, v[k][i], acc[i]);
+    }
   }
-#pragma unroll
-  for (int row = 0; row < RPB; ++row) {
-    if (lane == 0) sum_s[warp][row] = sum[row];
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) acc_s[warp][row][lane * CPL + i] = acc[row][i];
-  }
-  __syncthreads();
-  const int row = warp;
-  if (row >= rows) return;
-  float total = 0.f, best = kNoMax, v[CPL] = {};
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    best = fmaxf(best, top_s[w][row]);
-    total += sum_s[w][row];
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) v[i] += acc_s[w][row][lane * CPL + i];
-  }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  const int gr = meta.x + r0 + row, qi = a.G.div(gr);
-  const long long head = (long long)meta.z * a.G.d + (gr - qi * (int)a.G.d);
-  if (!fa_bounds(a.rep.st, q0 + qi < a.T && head < a.Hq)) return;
-  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + (q0 + qi) * a.os[0] + head * a.os[1] + lane * CPL);
-#pragma unroll
-  for (int i = 0; i < CPL / 2; ++i) to[i] = pack2<F16>(v[2 * i] * inv, v[2 * i + 1] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[(long long)(q0 + qi) * a.Hq + head] = total == 0.f ? -INFINITY : (best + log2f(total)) * 0.6931471805599453f;
 }
 
-// ctas: of the launch; cluster: CTAs of a cluster, or 0 for shares; few_tiles: see the merge.
 template <int D, int NT, bool F16>
-cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, bool few_tiles, cudaStream_t s) {
+__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4AttnArgs a) {
+  constexpr int ROWS = 8 * NT, CPL = D / 32, FEW = 16;
+  __shared__ float top_s[kMergeWarps], sum_s[kMergeWarps];
+  __shared__ __align__(16) float acc_s[kMergeWarps][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 meta = a.meta[2 * blockIdx.x];  // first row, rows, key head, last share
+  const int4 more = a.meta[2 * blockIdx.x + 1];
+  const int q0 = more.x, c0 = more.y;  // the request's first query row, the tile's first share
+  if (meta.x < 0) return;
+  const int rows = meta.y, shares = meta.w - c0 + 1, blocks = min(rows, shares - 1), mine = (int)blockIdx.x - c0;
+  if (mine >= blocks) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto write = [&](int row, float top, float sum, const float (&acc)[CPL]) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int gr = meta.x + row, qi = a.G.div(gr);
+    const long long head = (long long)meta.z * a.G.d + (gr - qi * (int)a.G.d);
+    if (!fa_bounds(a.rep.st, q0 + qi < a.T && head < a.Hq)) return;
+    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + (q0 + qi) * a.os[0] + head * a.os[1] + lane * CPL);
+#pragma unroll
+    for (int i = 0; i < CPL / 2; ++i) to[i] = pack2<F16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (lane == 0 && a.lse)
+      a.lse[(long long)(q0 + qi) * a.Hq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  };
+  float top, sum, acc[CPL];
+  if (shares <= FEW) {
+    for (int row = mine + blocks * warp; row < rows; row += blocks * kMergeWarps) {
+      add_shares<D, ROWS, 4>(a.part, row, c0, meta.w, c0, 1, top, sum, acc);
+      write(row, top, sum, acc);
+    }
+    return;
+  }
+  for (int row = mine; row < rows; row += blocks) {
+    add_shares<D, ROWS, 8>(a.part, row, c0, meta.w, c0 + warp, kMergeWarps, top, sum, acc);
+    __syncthreads();  // the row before has been written
+    if (lane == 0) {
+      top_s[warp] = top;
+      sum_s[warp] = sum;
+    }
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) acc_s[warp][lane * CPL + i] = acc[i];
+    __syncthreads();
+    if (warp == 0) {
+      top = top_s[0];
+#pragma unroll
+      for (int w = 1; w < kMergeWarps; ++w) top = fmaxf(top, top_s[w]);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float f = ex2(top_s[w] - top);
+        sum = fmaf(f, sum_s[w], sum);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) acc[i] = fmaf(f, acc_s[w][lane * CPL + i], acc[i]);
+      }
+      write(row, top, sum, acc);
+    }
+  }
+}
+
+// ctas: of the launch; cluster: CTAs of a cluster, or 0 for shares.
+template <int D, int NT, bool F16>
+cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) {
   using C = Cfg<D, NT, false>;
   using CC = Cfg<D, NT, true>;
   cudaLaunchConfig_t cfg = {};
@@ -1048,23 +1089,21 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, bool few_tiles, 
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.gridDim = dim3(ctas, few_tiles ? 8 * NT : NT);
-  return few_tiles ? cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16, 1>, a)
-                   : cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16, 8>, a);
+  cfg.gridDim = dim3(ctas);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16>, a);
 }
 
 }  // namespace
 
 template <int D>
-cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, bool few_tiles,
-                                   cudaStream_t s) {
+cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s) {
   if (f16)
-    return rows == 8    ? launch<D, 1, true>(a, ctas, cluster, few_tiles, s)
-           : rows == 16 ? launch<D, 2, true>(a, ctas, cluster, few_tiles, s)
-                        : launch<D, 4, true>(a, ctas, cluster, few_tiles, s);
-  return rows == 8    ? launch<D, 1, false>(a, ctas, cluster, few_tiles, s)
-         : rows == 16 ? launch<D, 2, false>(a, ctas, cluster, few_tiles, s)
-                      : launch<D, 4, false>(a, ctas, cluster, few_tiles, s);
+    return rows == 8    ? launch<D, 1, true>(a, ctas, cluster, s)
+           : rows == 16 ? launch<D, 2, true>(a, ctas, cluster, s)
+                        : launch<D, 4, true>(a, ctas, cluster, s);
+  return rows == 8    ? launch<D, 1, false>(a, ctas, cluster, s)
+         : rows == 16 ? launch<D, 2, false>(a, ctas, cluster, s)
+                      : launch<D, 4, false>(a, ctas, cluster, s);
 }
 
 }  // namespace fa

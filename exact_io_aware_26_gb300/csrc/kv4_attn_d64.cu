@@ -2,5 +2,5 @@
 #include "kv4_attn.cuh"
 
 namespace fa {
-template cudaError_t launch_kv4_attention_d<64>(const Kv4AttnArgs&, bool, int, int, int, bool, cudaStream_t);
+template cudaError_t launch_kv4_attention_d<64>(const Kv4AttnArgs&, bool, int, int, int, cudaStream_t);
 }

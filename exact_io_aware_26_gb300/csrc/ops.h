@@ -93,8 +93,7 @@ inline int kv4_tile_rows(int G, int max_q_len) {
 // The CTAs of a launch in shares: one wave.
 inline int kv4_share_ctas(int rows, int sms) { return sms * (rows == 8 ? 4 : rows == 16 ? 3 : 2); }
 template <int D>
-cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, bool few_tiles,
-                                   cudaStream_t s);
+cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s);
 
 struct PlanArgs {
   int R, T, page, pages, width;

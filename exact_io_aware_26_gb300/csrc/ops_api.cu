@@ -437,9 +437,9 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   if (cluster > 0) ctas = (int)std::min<long long>(kv4_tiles(c, p, rows), (1 << 20)) * cluster;
   a.rep = rep;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool f16 = p->dtype == FA_F16, few = kv4_tiles(c, p, rows) < 32;
-  const cudaError_t e = c->d == 64 ? launch_kv4_attention_d<64>(a, f16, rows, ctas, cluster, few, st)
-                                   : launch_kv4_attention_d<128>(a, f16, rows, ctas, cluster, few, st);
+  const bool f16 = p->dtype == FA_F16;
+  const cudaError_t e = c->d == 64 ? launch_kv4_attention_d<64>(a, f16, rows, ctas, cluster, st)
+                                   : launch_kv4_attention_d<128>(a, f16, rows, ctas, cluster, st);
   if (e != cudaSuccess) return api_cuda_fail(e, "cache attention launch");
   return FA_OK;
 }
