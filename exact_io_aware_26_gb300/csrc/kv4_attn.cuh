@@ -1095,6 +1095,36 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) 
 
 }  // namespace
 
+// Clusters of a size that the GPU holds at once: what its groups of SMs have room for, fewer
+// than the CTAs alone would allow (of 16 CTAs, two to an SM: 14, not 19).
+template <int D>
+int kv4_clusters_at_once(int rows, int cluster) {
+  auto ask = [&](auto k, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    int n = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    return n;
+  };
+  return rows == 8    ? ask(kv4_attn_kernel<D, 1, false, true>, Cfg<D, 1, true>::THREADS, Cfg<D, 1, true>::smem)
+         : rows == 16 ? ask(kv4_attn_kernel<D, 2, false, true>, Cfg<D, 2, true>::THREADS, Cfg<D, 2, true>::smem)
+                      : ask(kv4_attn_kernel<D, 4, false, true>, Cfg<D, 4, true>::THREADS, Cfg<D, 4, true>::smem);
+}
+
 template <int D>
 cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s) {
   if (f16)

@@ -3,4 +3,5 @@
 
 namespace fa {
 template cudaError_t launch_kv4_attention_d<128>(const Kv4AttnArgs&, bool, int, int, int, cudaStream_t);
+template int kv4_clusters_at_once<128>(int, int);
 }

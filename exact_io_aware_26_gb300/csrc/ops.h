@@ -94,6 +94,8 @@ inline int kv4_tile_rows(int G, int max_q_len) {
 inline int kv4_share_ctas(int rows, int sms) { return sms * (rows == 8 ? 4 : rows == 16 ? 3 : 2); }
 template <int D>
 cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s);
+template <int D>
+int kv4_clusters_at_once(int rows, int cluster);
 
 struct PlanArgs {
   int R, T, page, pages, width;

@@ -3,6 +3,7 @@
 // tables and slot maps.  Host code: argument checks, before any CUDA call, and the
 // launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -272,20 +273,41 @@ long long kv4_tiles(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows
   return (long long)p->R * c->Hk * ((q_rows + rows - 1) / rows);
 }
 
-// CTAs of a cluster (8 warps each) for a tile, as many as one wave has room for; 0 for the
-// way in shares: with more tiles than a wave has CTAs, or where the longest request the
-// block table has room for would give a warp more than 12 units of 32 tokens, the even
-// shares make up for the second launch (d = 128, in clusters and in shares: one tile of
-// 65,536 tokens, 16 units a warp, 30.2 and 24.5 us; d = 64: 12 tiles of 23,400 tokens,
-// 6 units, 14.4 and 18.8 us; 48 ragged tiles of up to 2048 tokens, 2 units, 8.9 and 12.5).
-int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int sms) {
-  const long long tiles = kv4_tiles(c, p, rows), slots = (long long)sms * (rows == 8 ? 2 : 1);
+// How many clusters of 1 << log CTAs the current device `dev` holds at once, asked for once.
+long long kv4_clusters(int dev, int d, int rows, int log) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][2][3][5];  // number + 1
+  if (dev < 0 || dev >= kDevices) return 0;
+  std::atomic<int>& k = known[dev][d == 128][rows == 8 ? 0 : rows == 16 ? 1 : 2][log];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = 1 + (d == 64 ? kv4_clusters_at_once<64>(rows, 1 << log) : kv4_clusters_at_once<128>(rows, 1 << log));
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+// CTAs of a cluster (8 warps each) for a tile, as many as lets one wave hold all tiles; 0 for
+// the way in shares: with more tiles than that, or where even shares would save a warp more
+// units of 32 tokens (for requests as long as the block table has room for) than the second
+// launch costs, two of them at d = 64 and one at d = 128.  Measured, in clusters and in
+// shares: d = 64, 12 tiles of 16384 tokens 12.7 and 15.0 us (4 units a warp and 3), of 24576
+// 14.9 and 14.7 (6 and 4), of 49152 22.4 and 19.4 (12 and 8); d = 128, 8 tiles of 4096
+// tokens 10.5 and 11.1 us (1 and 1), of 8192 12.5 and 12.2 (2 and 1), of 16384 16.6 and 14.4
+// (4 and 2).
+int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int share_ctas) {
+  const long long tiles = kv4_tiles(c, p, rows);
   long long tokens = (long long)p->table_width * c->page_size;
   if (p->window > 0) tokens = std::min(tokens, (long long)p->window + p->max_q_len + 31);
-  int cluster = 16;
-  while (cluster > 1 && tiles * cluster > slots) cluster /= 2;
-  if (tiles > slots || (tokens + 31) / 32 > 12ll * 8 * cluster) return 0;
-  return cluster;
+  const long long units = (tokens + 31) / 32;
+  int dev = 0, log = 4;
+  if (tiles > 2 * kMaxSms || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  while (tiles > kv4_clusters(dev, c->d, rows, log))
+    if (--log < 0) return 0;
+  const int cluster = 1 << log;
+  const long long mine = (units + 8 * cluster - 1) / (8 * cluster);
+  const long long share = (tiles * units + 4 * share_ctas - 1) / (4 * share_ctas);
+  return (mine - share) * c->d > 128 ? 0 : cluster;
 }
 
 size_t attn_part_bytes(int ctas, int rows, int d) { return align256((size_t)2 * ctas * rows * (d + 4) * 4); }
@@ -433,7 +455,7 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
   int ctas = kv4_share_ctas(rows, std::min(sms, kMaxSms));
   a.part = static_cast<float*>(workspace);
   a.meta = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attn_part_bytes(ctas, rows, c->d));
-  int cluster = kv4_cluster(c, p, rows, sms);
+  const int cluster = kv4_cluster(c, p, rows, ctas);
   if (cluster > 0) ctas = (int)std::min<long long>(kv4_tiles(c, p, rows), (1 << 20)) * cluster;
   a.rep = rep;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
