@@ -292,17 +292,19 @@ __device__ __forceinline__ void weights8(const void* w, bool w_f32, int c, int s
   }
 }
 
-// Tokens [first, last) of the CTA, and chunks of equal size over them.
+// Tokens [first, last) of the CTA, and chunks over them: of equal size, whole turns of rows
+// where a chunk may have as many tokens (which fills the turns of a single head, too).
 struct Run {
   int first, last, chunk;
 };
-__device__ __forceinline__ Run run_of(const QkArgs& a, int most) {
+__device__ __forceinline__ Run run_of(const QkArgs& a, int most, int turn) {
   Run r;
   const long long T = (long long)a.B * a.N;
   r.first = (int)(T * blockIdx.x / gridDim.x);
   r.last = (int)(T * (blockIdx.x + 1) / gridDim.x);
   const int n = r.last - r.first, chunks = (n + most - 1) / most;
   r.chunk = chunks ? (n + chunks - 1) / chunks : 1;
+  if (chunks > 1 && most >= turn) r.chunk = min(most / turn, (r.chunk + turn - 1) / turn) * turn;
   return r;
 }
 
@@ -377,28 +379,38 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_no
 #pragma unroll
     for (int i = 0; i < 4; ++i) reinterpret_cast<uint64_t*>(w_s)[4 * e + i] = v[i];
   }
-  const Run run = run_of(a, S::chunk);
-  for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
-    const int nt = min(run.chunk, run.last - t0), rows = nt * (a.Hq + a.Hk);
-    auto load = [&](int turn, int i) {
-      if (i < rows) {
-        const char* p = row_at(row_of(a, -1, t0, i), a.x, a.xb, a.xn, a.xh);
-        feed.load(turn, 0, p + L.lo * E, L.step);
-        feed.load(turn, 1, p + L.hi * E, L.step);
-      }
-      feed.commit();
-    };
+  const Run run = run_of(a, S::chunk, ROWS);
+  // the rows to load next, of the chunk that starts at token lt: they run ahead of the
+  // chunk whose rows are worked on
+  const int H = a.Hq + a.Hk;
+  int lt = run.first, li = 0;
+  auto load = [&](int place) {
+    const int rows = min(run.chunk, run.last - lt) * H, i = li + slot;
+    if (i < rows) {
+      const char* p = row_at(row_of(a, -1, lt, i), a.x, a.xb, a.xn, a.xh);
+      feed.load(place, 0, p + L.lo * E, L.step);
+      feed.load(place, 1, p + L.hi * E, L.step);
+    }
+    feed.commit();
+    li += ROWS;
+    if (li >= rows) {
+      li = 0;
+      lt = min(lt + run.chunk, run.last);
+    }
+  };
 #pragma unroll
-    for (int k = 0; k < AHEAD - 1; ++k) load(k, slot + k * ROWS);
+  for (int k = 0; k < AHEAD - 1; ++k) load(k);
+  int turn = 0;
+  for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
+    const int nt = min(run.chunk, run.last - t0), rows = nt * H;
     __syncthreads();  // the angles before have been used
     form_angles(a, t0, nt, ang);
     __syncthreads();
     // every lane of a warp takes the same number of turns: the row sums are shuffles
-    int turn = 0;
     for (int i0 = 0; i0 < rows; i0 += ROWS) {
       const bool live = i0 + slot < rows;
       const Row r = row_of(a, -1, t0, min(i0 + slot, rows - 1));
-      load(turn == 0 ? AHEAD - 1 : turn - 1, i0 + (AHEAD - 1) * ROWS + slot);
+      load(turn == 0 ? AHEAD - 1 : turn - 1);
       feed.wait();
       uint64_t lo[4], hi[4];
       feed.get(turn, 0, lo);
@@ -453,47 +465,49 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, true>::ctas) qk_nor
   float* row_s = reinterpret_cast<float*>(smem + S::rows) + slot * AnyRow<D>::stride;
   Lane L = lane_channels<D, DT, ANY>(a, threadIdx.x % LPR);
   if (DT != FA_F32) L.step = 4;
-  const Run run = run_of(a, S::chunk);
+  const Run run = run_of(a, S::chunk, ROWS);
   for (int e = lane; e < 2 * D; e += 32) red[e / D][warp][e % D] = 0.f;
   __syncwarp();
+  // the rows to load next: of tensor ltn in the chunk that starts at token lt
+  int lt = run.first, ltn = 0, li = 0;
+  auto load = [&](int place) {
+    const int rows = min(run.chunk, run.last - lt) * (ltn ? a.Hk : a.Hq), i = li + slot;
+    if (i < rows) {
+      const Row r = row_of(a, ltn, lt, i);
+      const char *p = row_at(r, a.x, a.xb, a.xn, a.xh), *q = row_at(r, a.dy, a.db, a.dn, a.dh);
+      feed.load(place, 0, p + L.lo * E, L.step);
+      feed.load(place, 1, p + L.hi * E, L.step);
+      feed.load(place, 2, q + L.lo * E, L.step);
+      feed.load(place, 3, q + L.hi * E, L.step);
+    }
+    feed.commit();
+    li += ROWS;
+    if (li >= rows) {
+      li = 0;
+      if (ltn) lt = min(lt + run.chunk, run.last);
+      ltn ^= 1;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD - 1; ++k) load(k);
+  int place = 0;
   for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
     const int nt = min(run.chunk, run.last - t0);
-    const int turns_q = (nt * a.Hq + ROWS - 1) / ROWS, turns = turns_q + (nt * a.Hk + ROWS - 1) / ROWS;
-    // row of this slot in a turn; `live`: there is one
-    auto row_in = [&](int i, bool& live) {
-      const int t = i >= turns_q, rows = nt * (t ? a.Hk : a.Hq), k = (i - (t ? turns_q : 0)) * ROWS + slot;
-      live = i < turns && k < rows;
-      return row_of(a, t, t0, min(k, rows - 1));
-    };
-    auto load = [&](int place, int i) {
-      bool live;
-      const Row r = row_in(i, live);
-      if (live) {
-        const char *p = row_at(r, a.x, a.xb, a.xn, a.xh), *q = row_at(r, a.dy, a.db, a.dn, a.dh);
-        feed.load(place, 0, p + L.lo * E, L.step);
-        feed.load(place, 1, p + L.hi * E, L.step);
-        feed.load(place, 2, q + L.lo * E, L.step);
-        feed.load(place, 3, q + L.hi * E, L.step);
-      }
-      feed.commit();
-    };
-#pragma unroll
-    for (int k = 0; k < AHEAD - 1; ++k) load(k, k);
     __syncthreads();  // the angles before have been used
     form_angles(a, t0, nt, ang);
     __syncthreads();
-    int place = 0;
-    for (int t = 0, i = 0; t < 2; ++t) {
+    for (int t = 0; t < 2; ++t) {
+      const int rows = nt * (t ? a.Hk : a.Hq);
       uint64_t wl[4], wh[4], acc[8];
       weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.lo, L.step, wl);
       weights8<DT>(t ? a.w[1] : a.w[0], w_f32, L.hi, L.step, wh);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = 0;
 #pragma unroll 1
-      for (; i < (t ? turns : turns_q); ++i) {
-        bool live;
-        const Row r = row_in(i, live);
-        load(place == 0 ? AHEAD - 1 : place - 1, i + AHEAD - 1);
+      for (int i0 = 0; i0 < rows; i0 += ROWS) {
+        const bool live = i0 + slot < rows;
+        const Row r = row_of(a, t, t0, min(i0 + slot, rows - 1));
+        load(place == 0 ? AHEAD - 1 : place - 1);
         feed.wait();
         uint64_t lo[4], hi[4], gl[4], gh[4];
         feed.get(place, 0, lo);
