@@ -37,7 +37,9 @@ struct QkArgs {
   const int* pos;  // or nullptr
   long long pos_stride;
   FastDiv divN, divH[2], divAll;  // by N, Hq and Hk, their sum
-  int ctas;       // each takes an equal run of the B * N tokens
+  int ctas;
+  long long share;  // forward: rows of a CTA; the first `spare` CTAs have one more
+  int spare;
   float* part;    // backward: [CTA][2][d] partial weight gradients
   float* dw[2];
 };

@@ -149,9 +149,13 @@ QkArgs qk_args(const fa_qk_params* p, const void* q, const void* k, const void* 
   a.divAll = FastDiv::of((uint32_t)(p->Hq + p->Hk));
   // one wave of CTAs, but no more than have a row for each of their row slots
   const long long T = (long long)p->B * p->N, slots = qk_rows_per_pass(p->d);
-  const long long least = std::max(1ll, slots / (p->Hq + p->Hk));
+  const long long rows = T * (p->Hq + p->Hk), least = std::max(1ll, slots / (p->Hq + p->Hk));
   const long long wave = (long long)std::min(sms, kQkMaxSms) * qk_ctas_per_sm(a.any, bwd);
-  a.ctas = (int)std::min(wave, (T + least - 1) / least);
+  a.ctas = (int)std::min(wave, bwd ? (T + least - 1) / least : (rows + slots - 1) / slots);
+  if (a.ctas > 0) {
+    a.share = rows / a.ctas;
+    a.spare = (int)(rows % a.ctas);
+  }
   return a;
 }
 

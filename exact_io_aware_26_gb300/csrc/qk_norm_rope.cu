@@ -8,7 +8,7 @@
 // HBM.  A row (one head of one token) belongs to D / 16 lanes of 16 channels, two
 // chunks of eight (16-byte loads for 16-bit types) chosen so that a lane holds both
 // elements of its pairs: sums over the row are a few shuffles and the rotation none.
-// Each CTA takes an equal run of tokens, a few per SM in flight, and walks their rows
+// Each CTA takes an equal run of rows (backward: of tokens), a few CTAs per SM, and walks them
 // token by token (a token's heads lie side by side in the projection); the coming rows are
 // on their way into shared memory, each lane's own chunks at its own place, so that no
 // barrier is needed; the angles of a run's tokens are formed once for all their heads.
@@ -297,13 +297,10 @@ __device__ __forceinline__ void weights8(const void* w, bool w_f32, int c, int s
 struct Run {
   int first, last, chunk;
 };
-__device__ __forceinline__ Run run_of(const QkArgs& a, int most, int turn) {
-  Run r;
-  const long long T = (long long)a.B * a.N;
-  r.first = (int)(T * blockIdx.x / gridDim.x);
-  r.last = (int)(T * (blockIdx.x + 1) / gridDim.x);
+__device__ __forceinline__ Run run_of(int first, int last, int most, int turn) {
+  Run r{first, last, 1};
   const int n = r.last - r.first, chunks = (n + most - 1) / most;
-  r.chunk = chunks ? (n + chunks - 1) / chunks : 1;
+  if (chunks) r.chunk = (n + chunks - 1) / chunks;
   if (chunks > 1 && most >= turn) r.chunk = min(most / turn, (r.chunk + turn - 1) / turn) * turn;
   return r;
 }
@@ -379,13 +376,19 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_no
 #pragma unroll
     for (int i = 0; i < 4; ++i) reinterpret_cast<uint64_t*>(w_s)[4 * e + i] = v[i];
   }
-  const Run run = run_of(a, S::chunk, ROWS);
+  // an equal share of all rows, which may begin and end inside a token: rows [skip, stop) from
+  // its first token on
+  const int H = a.Hq + a.Hk;
+  const long long row0 = a.share * blockIdx.x + min((int)blockIdx.x, a.spare);
+  const long long row1 = row0 + a.share + ((int)blockIdx.x < a.spare);
+  auto token_of = [&](long long row) { return row < (1ll << 31) ? a.divAll.div((int)row) : (int)(row / H); };
+  const Run run = run_of(token_of(row0), token_of(row1 - 1) + 1, S::chunk, ROWS);
+  const int skip = (int)(row0 - (long long)run.first * H), stop = (int)(row1 - (long long)run.first * H);
   // the rows to load next, of the chunk that starts at token lt: they run ahead of the
   // chunk whose rows are worked on
-  const int H = a.Hq + a.Hk;
-  int lt = run.first, li = 0;
+  int lt = run.first, li = skip;
   auto load = [&](int place) {
-    const int rows = min(run.chunk, run.last - lt) * H, i = li + slot;
+    const int rows = min(run.chunk * H, stop - (lt - run.first) * H), i = li + slot;
     if (i < rows) {
       const char* p = row_at(row_of(a, -1, lt, i), a.x, a.xb, a.xn, a.xh);
       feed.load(place, 0, p + L.lo * E, L.step);
@@ -402,12 +405,12 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_no
   for (int k = 0; k < AHEAD - 1; ++k) load(k);
   int turn = 0;
   for (int t0 = run.first; t0 < run.last; t0 += run.chunk) {
-    const int nt = min(run.chunk, run.last - t0), rows = nt * H;
+    const int nt = min(run.chunk, run.last - t0), before = (t0 - run.first) * H, rows = min(nt * H, stop - before);
     __syncthreads();  // the angles before have been used
     form_angles(a, t0, nt, ang);
     __syncthreads();
     // every lane of a warp takes the same number of turns: the row sums are shuffles
-    for (int i0 = 0; i0 < rows; i0 += ROWS) {
+    for (int i0 = max(skip - before, 0); i0 < rows; i0 += ROWS) {
       const bool live = i0 + slot < rows;
       const Row r = row_of(a, -1, t0, min(i0 + slot, rows - 1));
       load(turn == 0 ? AHEAD - 1 : turn - 1);
@@ -465,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, true>::ctas) qk_nor
   float* row_s = reinterpret_cast<float*>(smem + S::rows) + slot * AnyRow<D>::stride;
   Lane L = lane_channels<D, DT, ANY>(a, threadIdx.x % LPR);
   if (DT != FA_F32) L.step = 4;
-  const Run run = run_of(a, S::chunk, ROWS);
+  const long long T = (long long)a.B * a.N;
+  const Run run = run_of((int)(T * blockIdx.x / gridDim.x), (int)(T * (blockIdx.x + 1) / gridDim.x), S::chunk, ROWS);
   for (int e = lane; e < 2 * D; e += 32) red[e / D][warp][e % D] = 0.f;
   __syncwarp();
   // the rows to load next: of tensor ltn in the chunk that starts at token lt
