@@ -51,6 +51,7 @@ namespace fa {
 namespace {
 
 constexpr float kNoMax = -1e30f;     // running maximum before any token is seen
+constexpr float kLeast = 1e-37f;     // of a score's factor: a hidden token's -inf times it stays -inf
 constexpr int kUnit = 2 * kKvBlock;  // tokens a warp takes at a time
 constexpr int kReqCache = 128;       // requests whose lengths a CTA keeps at hand
 
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
         if (t4 == 0) up_s[n] = up;
       } else {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) factor[jj][c] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + c)) * a.scale_log2;
+        for (int c = 0; c < 2; ++c) factor[jj][c] = fmaxf(__shfl_sync(0xffffffffu, up, 4 * (2 * t4 + c)) * a.scale_log2, kLeast);
       }
     }
     if constexpr (NT == 4) {
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) factor[j][c] = up_s[8 * j + 2 * t4 + c] * a.scale_log2;
+        for (int c = 0; c < 2; ++c) factor[j][c] = fmaxf(up_s[8 * j + 2 * t4 + c] * a.scale_log2, kLeast);
     }
     // tokens that every row sees: no comparisons in their units
     const int i0 = a.G.div(y.row0), i1 = a.G.div(y.row0 + y.rows - 1);
@@ -700,14 +701,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       float s[2][NT][4];
       scores(kb, s[0]);
       scores(kb + Blk::bytes, s[1]);
-      // in log2 units; hidden tokens
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][j][c] *= factor[j][c & 1];
-      if (masked) {
+      if (masked) {  // hidden tokens
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -725,14 +719,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
               }
           }
       }
-      // the running maximum, moved when a score is above it by more than 8
+      // the running maximum, in log2 units, moved when a score is above it by more than 8
       float most[NT][2];
       bool grow = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          most[j][c] = fmax3(fmaxf(s[0][j][c], s[0][j][c + 2]), s[1][j][c], s[1][j][c + 2]);
+          most[j][c] = fmax3(fmaxf(s[0][j][c], s[0][j][c + 2]), s[1][j][c], s[1][j][c + 2]) * factor[j][c];
           grow |= most[j][c] > m[j][c] + 8.f;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -761,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][j][c] = ex2(s[h][j][c] - m[j][c & 1]);
+          for (int c = 0; c < 4; ++c) s[h][j][c] = ex2(fmaf(s[h][j][c], factor[j][c & 1], -m[j][c & 1]));
           l[j][0] += s[h][j][0] + s[h][j][2];
           l[j][1] += s[h][j][1] + s[h][j][3];
           p0[j] = transpose8x8(pack2<true>(s[h][j][0], s[h][j][1]));

@@ -186,6 +186,8 @@ ATTN = [  # kv, new, Hq, Hk, d, dtype, page, window
     ([600] * 40, [2] * 40, 12, 4, 128, "bf16", 64, 100),
     ([70000], [1], 3, 1, 64, "f16", 64, 0),                       # one tile in hundreds of shares
     ([9000, 50000], [2, 3], 20, 2, 128, "bf16", 128, 0),
+    ([20000, 40], [4, 1], 4, 1, 64, "bf16", 32, 0),               # the same with 16 rows
+    ([12000] + [20 + i for i in range(330)], [1] * 331, 2, 1, 128, "f16", 16, 0),  # and among many of one unit
 ]
 
 
