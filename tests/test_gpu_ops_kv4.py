@@ -555,3 +555,24 @@ def test_plan_of_lengths_that_are_out_of_range(cuda_lib):
     got = fa.paged_plan(i32(seq), i32(new), t, s, i32([count]), 16, 8)
     assert got["kv_lens"].tolist() == want[0] and got["slots"].tolist() == want[3] and t.tolist() == want[5]
     assert s.tolist() == want[6] and got["counts"].tolist()[0] == want[4][0]
+
+
+def test_results_lie_apart(cuda_lib):
+    """New results never overlap, start at whole 16-byte vectors and keep their values when the
+    others are written; a result above 1 MB has a block of its own."""
+    R, T = 5, 300000
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = fa.paged_plan(torch.zeros(R, **i32), torch.full((R,), 7, **i32), torch.full((R, 4), -1, **i32),
+                         torch.arange(40, **i32), torch.full((1,), 40, **i32), 16, T)
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in plan.values())
+    assert all(a % 16 == 0 for a, _ in spans) and all(e <= b for (_, e), (b, _) in zip(spans, spans[1:]))
+    blocks = {name: t.untyped_storage().data_ptr() for name, t in plan.items()}
+    assert blocks["positions"] != blocks["slots"] != blocks["kv_lens"] == blocks["counts"]
+    want = {name: t.clone() for name, t in plan.items()}
+    for name in plan:
+        plan[name].fill_(-9)
+        for other in plan:
+            if other != name:
+                assert torch.equal(plan[other], want[other])
+        plan[name].copy_(want[name])
+    assert plan["kv_lens"].tolist() == [7] * R and plan["counts"].tolist() == [35, 35, 0]
