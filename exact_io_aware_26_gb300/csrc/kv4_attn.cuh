@@ -39,9 +39,9 @@
 // kv4_cluster (ops_api.cu) chooses, by the number of tiles and the units a warp would take.
 //
 // Measured (shares): 64 requests of up to 16384 tokens, 32 query and 8 key heads, d = 128:
-// 149 us for 748 MB, 5.0 TB/s; the unit loop alone goes at 5.9 TB/s, with the integer pipe at
-// 54% (codes to fp16) and four warps a scheduler, and about 16 us are start-up, uneven ends
-// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.4 us.
+// 145 us for 748 MB, 5.2 TB/s; the unit loop alone goes at 5.9 TB/s, with the integer pipe at
+// 54% (codes to fp16) and four warps a scheduler, and about 13 us are start-up, uneven ends
+// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.5 us.
 #pragma once
 #include "kv4.cuh"
 #include "ops.h"
@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 // pair of shares is one block's, a tile of hundreds of shares (a long context among short
 // ones) a block's for every row.  Few shares: a warp for each row; many: the block's warps
 // divide a row's shares.  A lane has D / 32 channels.  Bound by the chain: the end of the
-// first kernel, the tile's place, its sums.
+// first kernel, the tile's place, its sums (64 requests up to 16384 tokens: about 3 us after the
+// last share; with eight rows to a block and two passes 6).
 constexpr int kMergeWarps = 8;
 // Of shares c, c + step, ... to `last` of a row: the largest maximum, and l and O by it.
 // AT_ONCE of them are on their way together.  (The first share's slot is its second one.)

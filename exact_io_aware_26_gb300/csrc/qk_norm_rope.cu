@@ -355,8 +355,8 @@ struct Smem {
 };
 
 // The forward pass.  Measured: 23,400 tokens of 12 + 12 heads, d = 64, bf16 26.5 us (144 MB,
-// 5.4 TB/s; three CTAs an SM 27.3 us), bound by issue slots (0.67 a cycle) and HBM together;
-// 19,735 tokens of 64 + 16 heads, d = 64, fp32 142 us (808 MB, 5.7 TB/s).
+// 5.4 TB/s; three CTAs an SM 27.3 us), of which about 3 are the launch, the angles and the
+// first rows; 19,735 tokens of 64 + 16 heads, d = 64, fp32 142 us (808 MB, 5.7 TB/s).
 template <int D, int DT, bool ANY>
 __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, E = DT == FA_F32 ? 4 : 2;
