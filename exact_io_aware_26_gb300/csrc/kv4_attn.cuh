@@ -937,8 +937,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 // pair of shares is one block's, a tile of hundreds of shares (a long context among short
 // ones) a block's for every row.  Few shares: a warp for each row; many: the block's warps
 // divide a row's shares.  A lane has D / 32 channels.  Bound by the chain: the end of the
-// first kernel, the tile's place, its sums (64 requests up to 16384 tokens: about 3 us after the
-// last share; with eight rows to a block and two passes 6).
+// first kernel, the tile's place, its sums (64 requests up to 16384 tokens: 146 us with the first
+// kernel; with eight rows to a block and two passes 149).
 constexpr int kMergeWarps = 8;
 // Of shares c, c + step, ... to `last` of a row: the largest maximum, and l and O by it.
 // AT_ONCE of them are on their way together.  (The first share's slot is its second one.)

@@ -20,6 +20,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -162,71 +163,68 @@ PyObject* run(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     PyErr_SetString(PyExc_TypeError, "run(op, tensors, scalars)");
     return nullptr;
   }
-  try {
-    static thread_local std::vector<int64_t> sig;
-    if (!sign(PyLong_AsLong(args[0]), args[1], sig)) return nullptr;
-    bool ok;
-    const uint64_t h = hash_of(sig, args[2], ok);
-    if (!ok) return nullptr;
-    const std::shared_ptr<Plan> p = find(sig, args[2], h);
-    if (!p) {
-      if (PyErr_Occurred()) return nullptr;
-      Py_RETURN_NONE;
-    }
-    const int here = c10::cuda::current_device();
-    if (here != p->device) {
-      PyErr_Format(PyExc_ValueError, "the tensors are on cuda:%d, the current device is cuda:%d", p->device, here);
-      return nullptr;
-    }
-    at::Tensor out[kMaxOutputs];
-    c10::DataPtr scratch[kMaxOutputs];
-    c10::Storage shared;
-    if (p->shared > 0) shared = block(p->shared);
-    for (size_t i = 0; i < p->outputs.size(); ++i) {
-      const Output& o = p->outputs[i];
-      if (o.result)
-        out[i] = tensor_in(o.shared ? shared : block(o.bytes), o);
-      else
-        scratch[i] = c10::cuda::CUDACachingAllocator::get()->allocate(o.bytes);
-    }
-    uintptr_t a[kMaxArgs];
-    for (size_t i = 0; i < p->args.size(); ++i) {
-      const Source& s = p->args[i];
-      if (s.kind == kInput) {
-        PyObject* o = PyTuple_GET_ITEM(args[1], s.value);
-        a[i] = o == Py_None ? 0 : reinterpret_cast<uintptr_t>(THPVariable_Unpack(o).data_ptr());
-      } else if (s.kind == kOutput) {
-        a[i] = reinterpret_cast<uintptr_t>(p->outputs[s.value].result ? out[s.value].data_ptr() : scratch[s.value].get());
-      } else if (s.kind == kStream) {
-        a[i] = reinterpret_cast<uintptr_t>(c10::cuda::getCurrentCUDAStream(p->device).stream());
-      } else {
-        a[i] = static_cast<uintptr_t>(s.value);
-      }
-    }
-    const int status = call(p->entry, a, p->args.size());
-    if (status != 0) return PyLong_FromLong(status);
-    PyObject* results = PyTuple_New(static_cast<Py_ssize_t>(p->results.size()));
-    if (!results) return nullptr;
-    for (size_t i = 0; i < p->results.size(); ++i) {
-      const Source& s = p->results[i];
-      PyObject* o;
-      if (s.kind == kInput) {
-        o = PyTuple_GET_ITEM(args[1], s.value);
-        Py_INCREF(o);
-      } else {
-        o = THPVariable_Wrap(out[s.value]);
-      }
-      if (!o) {
-        Py_DECREF(results);
-        return nullptr;
-      }
-      PyTuple_SET_ITEM(results, static_cast<Py_ssize_t>(i), o);
-    }
-    return results;
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  HANDLE_TH_ERRORS
+  static thread_local std::vector<int64_t> sig;
+  if (!sign(PyLong_AsLong(args[0]), args[1], sig)) return nullptr;
+  bool ok;
+  const uint64_t h = hash_of(sig, args[2], ok);
+  if (!ok) return nullptr;
+  const std::shared_ptr<Plan> p = find(sig, args[2], h);
+  if (!p) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  const int here = c10::cuda::current_device();
+  if (here != p->device) {
+    PyErr_Format(PyExc_ValueError, "the tensors are on cuda:%d, the current device is cuda:%d", p->device, here);
     return nullptr;
   }
+  at::Tensor out[kMaxOutputs];
+  c10::DataPtr scratch[kMaxOutputs];
+  c10::Storage shared;
+  if (p->shared > 0) shared = block(p->shared);
+  for (size_t i = 0; i < p->outputs.size(); ++i) {
+    const Output& o = p->outputs[i];
+    if (o.result)
+      out[i] = tensor_in(o.shared ? shared : block(o.bytes), o);
+    else
+      scratch[i] = c10::cuda::CUDACachingAllocator::get()->allocate(o.bytes);
+  }
+  uintptr_t a[kMaxArgs];
+  for (size_t i = 0; i < p->args.size(); ++i) {
+    const Source& s = p->args[i];
+    if (s.kind == kInput) {
+      PyObject* o = PyTuple_GET_ITEM(args[1], s.value);
+      a[i] = o == Py_None ? 0 : reinterpret_cast<uintptr_t>(THPVariable_Unpack(o).data_ptr());
+    } else if (s.kind == kOutput) {
+      a[i] = reinterpret_cast<uintptr_t>(p->outputs[s.value].result ? out[s.value].data_ptr() : scratch[s.value].get());
+    } else if (s.kind == kStream) {
+      a[i] = reinterpret_cast<uintptr_t>(c10::cuda::getCurrentCUDAStream(p->device).stream());
+    } else {
+      a[i] = static_cast<uintptr_t>(s.value);
+    }
+  }
+  const int status = call(p->entry, a, p->args.size());
+  if (status != 0) return PyLong_FromLong(status);
+  PyObject* results = PyTuple_New(static_cast<Py_ssize_t>(p->results.size()));
+  if (!results) return nullptr;
+  for (size_t i = 0; i < p->results.size(); ++i) {
+    const Source& s = p->results[i];
+    PyObject* o;
+    if (s.kind == kInput) {
+      o = PyTuple_GET_ITEM(args[1], s.value);
+      Py_INCREF(o);
+    } else {
+      o = THPVariable_Wrap(out[s.value]);
+    }
+    if (!o) {
+      Py_DECREF(results);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(results, static_cast<Py_ssize_t>(i), o);
+  }
+  return results;
+  END_HANDLE_TH_ERRORS  // out of memory is torch.OutOfMemoryError
 }
 
 bool sources(PyObject* list, std::vector<Source>& out, Py_ssize_t tensors, size_t outputs) {

@@ -576,3 +576,18 @@ def test_results_lie_apart(cuda_lib):
                 assert torch.equal(plan[other], want[other])
         plan[name].copy_(want[name])
     assert plan["kv_lens"].tolist() == [7] * R and plan["counts"].tolist() == [35, 35, 0]
+
+
+def test_results_that_do_not_fit_the_memory(cuda_lib):
+    """The allocator's own error, before anything is launched; the next call runs."""
+    cache = fa.kv4_cache(4, 8, 64, 16)
+    slots = torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.empty_cache()
+    try:
+        torch.cuda.set_per_process_memory_fraction(0.001)  # less than the 4 GB of results
+        with pytest.raises(torch.OutOfMemoryError):
+            fa.kv4_gather(cache, slots, 64, dtype=torch.float32)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    k, v = fa.kv4_gather(cache, slots[:5], 64)
+    assert k.shape == (5, 8, 64) and float(k.abs().sum() + v.abs().sum()) == 0
