@@ -20,7 +20,7 @@ Serving, one step of R requests:
 
 Every tensor lies on the current device.  Results and workspaces are allocated on
 ``stream`` (default: the current one); inputs that another stream may free are marked
-as used there.
+as used there.  New results of up to 1 MB share a block of memory.
 """
 from __future__ import annotations
 
