@@ -41,7 +41,7 @@
 // Measured (shares): 64 requests of up to 16384 tokens, 32 query and 8 key heads, d = 128:
 // 145 us for 748 MB, 5.2 TB/s; the unit loop alone goes at 5.9 TB/s, with the integer pipe at
 // 54% (codes to fp16) and four warps a scheduler, and about 13 us are start-up, uneven ends
-// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.5 us.
+// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.1 us.
 #pragma once
 #include "kv4.cuh"
 #include "ops.h"
@@ -499,8 +499,29 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       first = (int)max(0ll, u0 - tile0);
       last = (int)min((long long)y.n_u, u1 - tile0);
     }
+    // the lane's channels of the query rows that its warp prepares (32 rows: eight for each warp)
+    constexpr int NQ = NT == 4 ? 1 : NT;
+    uint4 raw[NQ][D / 32];
+    auto load_q = [&] {
+#pragma unroll
+      for (int jj = 0; jj < NQ; ++jj) {
+        const int n = g + 8 * (NT == 4 ? warp : jj);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw[jj][i] = make_uint4(0, 0, 0, 0);
+        if (n < y.rows) {
+          const int row = y.row0 + n, qi = a.G.div(row);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(a.q) + (x.q0 + qi) * a.qs[0] +
+              ((long long)cw.h * a.G.d + (row - qi * (int)a.G.d)) * a.qs[1] + t4 * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) raw[jj][i] = __ldg(src + i);
+        }
+      }
+    };
+    if constexpr (CL) load_q();  // on their way beside the first units (shares: no gain, more registers)
     if constexpr (!C::across)
       for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((stage + s) % S);
+    if constexpr (!CL) load_q();
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
     // which its score factor takes back: no 16-bit query leaves fp16's range.
@@ -508,25 +529,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     uint32_t qf[NT == 4 ? 1 : NT][KS][2];
     float factor[NT][2];
 #pragma unroll
-    for (int jj = 0; jj < (NT == 4 ? 1 : NT); ++jj) {
+    for (int jj = 0; jj < NQ; ++jj) {
       const int j = NT == 4 ? warp : jj;
       if (NT == 4 && warp >= 4) break;
       const int n = g + 8 * j;
-      uint4 raw[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      if (n < y.rows) {
-        const int row = y.row0 + n, qi = a.G.div(row);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) + (x.q0 + qi) * a.qs[0] +
-            ((long long)cw.h * a.G.d + (row - qi * (int)a.G.d)) * a.qs[1] + t4 * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(src + i);
-      }
       float big = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const uint32_t w[4] = {raw[jj][i].x, raw[jj][i].y, raw[jj][i].z, raw[jj][i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = unpack2<F16>(w[k]);
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const uint32_t w[4] = {raw[jj][i].x, raw[jj][i].y, raw[jj][i].z, raw[jj][i].w};
         float f[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
