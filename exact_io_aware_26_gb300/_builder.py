@@ -25,7 +25,7 @@ LIB_DEBUG = os.path.join(HERE, "libfa_debug.so")
 SOURCES = ["fa_api.cu", "fwd_tc.cu", "fwd_f32.cu", "bwd_tc.cu", "bwd_aux.cu", "fa_noalloc.cu", "fwd_fp8.cu",
            "ops_api.cu", "qk_norm_rope.cu", "kv4.cu", "kv4_attn_d64.cu", "kv4_attn_d128.cu", "plan.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "bwd_sched.cuh", "fp8.h", "tiles.cuh", "fwd_common.cuh",
-           "ops.h", "kv4.cuh", "kv4_attn.cuh"]
+           "ops.h", "kv4.cuh", "kv4_ring.cuh", "kv4_attn.cuh"]
 # the short way from Python to the C entry points (a CPython extension; gcc, torch's headers)
 LAUNCH_SOURCE = os.path.join(CSRC, "launch.cpp")
 LAUNCH = os.path.join(HERE, "_launch.so")

@@ -44,6 +44,7 @@
 // and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.1 us.
 #pragma once
 #include "kv4.cuh"
+#include "kv4_ring.cuh"
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -221,7 +222,7 @@ struct Feed {
   int ids_r, ids_tok;     // request and first token that `id` was read for
   int id[2][32];          // pages of the two blocks of each of the 32 units
   ulonglong2 src[32];     // addresses of the two blocks; 1 for one that is not to be read
-  uint32_t hidden[8];     // per ring stage: bit h for block h not read
+  uint32_t hidden[8];     // per ring stage: bit h for block h not read, or kStageIdle
 };
 
 // Fills src with the warp's next units of the share, at most 32, all of one tile; returns
@@ -276,6 +277,21 @@ __device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, con
   }
   __syncwarp();
   return n;
+}
+
+// A wait gave up (which is recorded, and void what this launch writes): the warp's copies
+// under way must land, within one limit for all of them, before anything else is written over
+// the ring or the CTA ends.  No more are issued and no unit is consumed from then on, but the
+// CTA goes through its barriers to the end.
+template <int S>
+__device__ __noinline__ void drain_ring(WaitCtx wc, uint32_t bar0, uint32_t* words, Ring<S> at) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  const uint64_t since = globaltimer_ns();
+  at.each_armed(words, [&](int s, uint32_t p) { mbar_drain_since(wc, bar0 + 8 * s, p, since); });
+  __syncwarp();
+  if (lane < S) words[lane] = kStageIdle;
+  __syncwarp();
 }
 
 template <int D, int NT, bool F16, bool CL>
@@ -402,6 +418,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   const WaitCtx wc{&abort_s, a.rep.st, a.rep.epoch, a.rep.wait_ns};
 
   Feed<ROWS>& feed = feed_s[warp];
+  if (lane < S) feed.hidden[lane] = kStageIdle;
+  __syncwarp();
   if (!CL && lane == 0) {
     feed.w.at(a, reqs, cache_r0, start_r, start_t, start_h);
     feed.tile0 = start_u;
@@ -415,7 +433,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     if (turn == ready) {
       ready = feed_refill<D, ROWS, kWarps>(a, feed, reqs, cache_r0, warp, u1);
       turn = 0;
-      if (ready == 0) return;
+      if (ready == 0) {
+        if (lane == 0) feed.hidden[stage] = kStageIdle;
+        return;
+      }
     }
     if (lane == 0) {
       const ulonglong2 src = feed.src[turn];
@@ -440,8 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   __syncthreads();  // tile_s
 
   // ---- the tiles of the share, or of the cluster
-  int stage = 0;
-  uint32_t parity = 0;
+  Ring<S> ring_at;
   int4 meta = make_int4(-1, 0, 0, 0);
   int meta_q0 = 0, meta_c0 = 0;
   long long tile0 = CL ? 0 : start_u;
@@ -454,7 +474,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   }
 #pragma unroll 1
   for (int which = 0; CL ? index < total : tile0 < u1; which ^= (CL ? 0 : 1)) {
+    [[maybe_unused]] bool given_up = false;
     if constexpr (CL) {
+      given_up = tile0 > 0 && abort_s != 0;  // in a tile before; no thread waits for a copy until the barrier below
       if (index < end && index >= end - mine) {
         long long u = end - mine;
         bool found = false;
@@ -487,6 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       first = min(y.n_u, (int)rank * part);
       last = min(y.n_u, first + part);
       alone = part >= y.n_u;
+      if (given_up) first = last = y.n_u;
       if (lane == 0) {
         feed.w = cw;
         feed.tile0 = 0;
@@ -520,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     };
     if constexpr (CL) load_q();  // on their way beside the first units (shares: no gain, more registers)
     if constexpr (!C::across)
-      for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((stage + s) % S);
+      for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((ring_at.stage + s) % S);
     if constexpr (!CL) load_q();
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
@@ -681,11 +704,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       }
     };
 
-    int held = -1;  // stage of the tile's last unit, kept for the join (across)
+    constexpr int kGaveUp = S;
+    int held = -1;  // stage of the tile's last unit, kept for the join (across); kGaveUp
 #pragma unroll 1
     for (int u = first + warp; u < last; u += kWarps) {
-      // a wait that gave up has recorded it; the copy must still land before the stage is left
-      if (!warp_wait(wc, bar0 + 8 * stage, parity)) mbar_drain(wc, bar0 + 8 * stage, parity);
+      const int stage = ring_at.stage;
+      if (!warp_wait(wc, bar0 + 8 * stage, ring_at.parity)) {
+        held = kGaveUp;
+        break;
+      }
       const uint32_t kb = ring + stage * C::stage;
       const int key0 = y.u0 + u * kUnit;
       const uint32_t hidden = feed.hidden[stage];
@@ -776,12 +803,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       __syncwarp();  // every lane has read the stage
       if (C::across ? u + kWarps < last : u + S * kWarps < last)
         produce(stage);
-      else
+      else {
         held = stage;
-      if (++stage == S) {
-        stage = 0;
-        parity ^= 1u;
+        if (!C::across && lane == 0) feed.hidden[stage] = kStageIdle;
       }
+      ring_at.next();
+    }
+    if (held == kGaveUp) {
+      drain_ring<S>(wc, bar0, feed.hidden, ring_at);
+      held = ring_at.stage;
     }
 
     // ---- join the warps that took units of the tile
@@ -902,6 +932,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       index += gridDim.x / ctas;
     } else {
       const bool from_before = first > 0, goes_on = tile0 + y.n_u > u1;
+      given_up = abort_s != 0;  // no thread waits for a copy until the barrier below
       for (int e = tid; e < y.rows * TPR; e += kThreads) {
         const int row = e / TPR, ch = (e % TPR) * 8;
         float top, sum, acc[8];
@@ -932,6 +963,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
         }
       }
       __syncthreads();  // joined, m_s, l_s read; the next tile known
+    }
+    if constexpr (!CL) {
+      if (given_up) {
+        if (held >= 0 && lane == 0) feed.hidden[held] = kStageIdle;  // consumed
+        drain_ring<S>(wc, bar0, feed.hidden, ring_at);
+        break;
+      }
     }
     if (C::across && held >= 0) produce(held);
     tile0 += y.n_u;

@@ -168,8 +168,7 @@ __device__ __forceinline__ bool mbar_wait(const WaitCtx& w, uint32_t bar, uint32
 // Drain wait used on the way out: ignores the abort word (copies or MMAs that
 // are in flight must land before shared memory or TMEM is released) but still
 // ends after the time limit.
-static __device__ __noinline__ bool mbar_drain(const WaitCtx& w, uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
+__device__ __forceinline__ bool drain_until(const WaitCtx& w, uint32_t bar, uint32_t parity, uint64_t t0) {
   for (uint32_t n = 0;; ++n) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((n & 63u) == 63u && globaltimer_ns() - t0 > w.limit_ns) {
@@ -177,6 +176,13 @@ static __device__ __noinline__ bool mbar_drain(const WaitCtx& w, uint32_t bar, u
       return false;
     }
   }
+}
+static __device__ __noinline__ bool mbar_drain(const WaitCtx& w, uint32_t bar, uint32_t parity) {
+  return drain_until(w, bar, parity, globaltimer_ns());
+}
+// The same with the limit counted from t0 on: one for several barriers.
+static __device__ __noinline__ bool mbar_drain_since(const WaitCtx& w, uint32_t bar, uint32_t parity, uint64_t t0) {
+  return drain_until(w, bar, parity, t0);
 }
 
 // Warp-uniform wait: every lane polls, and the warp proceeds only if all lanes
