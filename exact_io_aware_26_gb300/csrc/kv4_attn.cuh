@@ -155,6 +155,12 @@ __device__ __forceinline__ Req load_req(const Kv4AttnArgs& a, int r) {
   return x;
 }
 
+// The first token that the row at position pos sees (pos may be negative, and the window any:
+// pos - window is formed only where it is not negative).
+__device__ __forceinline__ int first_seen(const Kv4AttnArgs& a, int pos) {
+  return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
 // Tile `t` of a request: rows [row0, row0 + ROWS) of its n * G, tokens [k0, k1) that some
 // row of it sees, units from token u0 on, n_u of them (one, of hidden tokens, where no
 // row sees any).
@@ -172,8 +178,7 @@ __device__ __forceinline__ Tile tile_of(const Kv4AttnArgs& a, const Req& x, int 
   y.rows = min(ROWS, x.n * (int)a.G.d - y.row0);
   const int i0 = a.G.div(y.row0), i1 = a.G.div(y.row0 + y.rows - 1);
   y.k1 = max(0, x.kv - x.n + i1 + 1);
-  y.k0 = a.window > 0 ? max(0, x.kv - x.n + i0 - a.window + 1) : 0;
-  y.k0 = min(y.k0, y.k1);
+  y.k0 = min(first_seen(a, x.kv - x.n + i0), y.k1);
   y.u0 = y.k0 & ~(kUnit - 1);
   y.n_u = max(1, (y.k1 - y.u0 + kUnit - 1) / kUnit);
   return y;
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     // tokens that every row sees: no comparisons in their units
     const int i0 = a.G.div(y.row0), i1 = a.G.div(y.row0 + y.rows - 1);
     const int all_hi = x.kv - x.n + i0 + 1;
-    const int all_lo = a.window > 0 ? x.kv - x.n + i1 - a.window + 1 : 0;
+    const int all_lo = first_seen(a, x.kv - x.n + i1);
 
     float m[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
@@ -744,7 +749,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int pos = x.kv - x.n + a.G.div(y.row0 + 8 * j + 2 * t4 + c);  // rows behind the last: of no consequence
-            const int lim = min(pos + 1, x.kv) - key0, low = (a.window > 0 ? pos - a.window + 1 : 0) - key0;
+            const int lim = min(pos + 1, x.kv) - key0, low = first_seen(a, pos) - key0;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
