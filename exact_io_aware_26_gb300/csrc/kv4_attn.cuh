@@ -161,6 +161,9 @@ __device__ __forceinline__ int first_seen(const Kv4AttnArgs& a, int pos) {
   return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
 }
 
+// Bits 0 .. n - 1, for any n.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // Tile `t` of a request: rows [row0, row0 + ROWS) of its n * G, tokens [k0, k1) that some
 // row of it sees, units from token u0 on, n_u of them (one, of hidden tokens, where no
 // row sees any).
@@ -722,10 +725,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       const int key0 = y.u0 + u * kUnit;
       const uint32_t hidden = feed.hidden[stage];
       const bool masked = hidden || key0 + kUnit > all_hi || key0 < all_lo;
-      uint32_t nan_keys = 0;
       if (masked) {
         // values that no row sees must not reach the product (0 x NaN), nor a NaN that only
-        // some rows see: their pairs become 0, and a NaN one marks its token's scores
+        // some rows see: their pairs become 0, and a NaN one makes the sums NaN of the rows
+        // that see its token, in its group's channels
+        uint32_t nan_keys = 0;  // of group lane % groups
         for (int e = lane; e < kUnit * Blk::groups; e += 32) {
           const int key = e / Blk::groups;
           const uint32_t at = kb + (key / kKvBlock) * Blk::bytes + Blk::half + Blk::codes + (e % (kKvBlock * Blk::groups)) * 4;
@@ -736,7 +740,24 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
           if (!seen || nan) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
           if (seen && nan) nan_keys |= 1u << key;
         }
-        nan_keys = __reduce_or_sync(0xffffffffu, nan_keys);
+        if (__any_sync(0xffffffffu, nan_keys)) {
+#pragma unroll
+          for (int off = Blk::groups; off < 32; off <<= 1) nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, off);
+          nan_keys = __shfl_sync(0xffffffffu, nan_keys, D == 128 ? g >> 1 : g >> 2);  // of this lane's channels
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int pos = x.kv - x.n + a.G.div(y.row0 + 8 * j + 2 * t4 + c);
+              const uint32_t behind = below(min(pos + 1, x.kv) - key0), before = below(first_seen(a, pos) - key0);
+              const float add = nan_keys & behind & ~before ? NAN : 0.f;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[i][j][c] += add;
+                o[i][j][c + 2] += add;
+              }
+            }
+        }
         __syncwarp();
         fence_async_smem();  // these stores before the copy that reuses the stage
       }
@@ -757,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
                 const int key = 16 * h + 8 * q + kr;
                 const bool seen = !((hidden >> h) & 1u) && key < lim && key >= low;
                 float& v = s[h][j][2 * q + c];
-                v = !seen ? -INFINITY : (nan_keys >> key) & 1u ? NAN : v;
+                v = seen ? v : -INFINITY;
               }
           }
       }

@@ -443,7 +443,8 @@ fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
  * stand for its last tokens, so that the i-th of n sees the tokens up to
  * p = kv_lens[r] - n + i, and with window > 0 only those after p - window.  A row
  * that sees no token gets O = 0 and LSE = -inf; rows of q outside every request
- * are not written.
+ * are not written.  A NaN in a cached key (a pair of NaN) makes O and LSE of the rows that
+ * see its token NaN; one in a cached value O's 32 channels of that pair, and nothing else.
  *   T           rows of q and o ([T][Hq][d], element strides {token, head}, FA_F16 or
  *               FA_BF16); lse: fp32 [T][Hq] or NULL.
  *   max_q_len   the largest number of rows of a request: a hint for the tile height

@@ -27,3 +27,34 @@ def test_a_window_beyond_every_length_hides_nothing(cuda_lib, kv, new, wide):
                                   max_q_len=max(new), scale=0.3, window=window)
         check(o, lse, want, "bf16")
     assert fa.get_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d,dtype", [(2, 1, 64, "bf16"), (8, 2, 128, "f16"), (7, 1, 128, "bf16")])
+@pytest.mark.parametrize("side,tok,group,window", [
+    (1, 5, 0, 0), (1, 5, 1, 0),       # a value in a unit that every row sees
+    (1, 197, 0, 0), (1, 198, 1, 0),   # in one that some rows see a part of
+    (1, 160, 1, 0), (1, 199, 0, 0),
+    (1, 134, 1, 64), (1, 140, 0, 64), (1, 100, 0, 64),  # the window's end; behind it
+    (0, 5, 0, 0), (0, 198, 1, 0), (0, 134, 0, 64),      # a key
+])
+def test_a_nan_reaches_what_the_formula_says(cuda_lib, side, tok, group, window, Hq, Hk, d, dtype, wide):
+    """A NaN value makes its 32 channels NaN for the rows that see it, and nothing else; a NaN
+    key the rows' every channel and LSE: whatever the tile's height, the other rows in it and
+    the place of the token in its unit."""
+    kv, new = [200, 50], [4, 2]
+    q, cache, table, lens, cu = build(kv, new, Hq, Hk, d, dtype, 16, 32)
+    clean = ref.attention(to_np64(q), cache, table, lens, cu, 0.3, window, d)
+    at = side * cache.shape[3] // 2 + 8 * d + tok % 16 * (d // 8) + 4 * group
+    cache[table[0, tok // 16], Hk - 1, 0, at:at + 4] = 0x7E  # pages of one block
+    with np.errstate(invalid="ignore"):
+        dirty = ref.attention(to_np64(q), cache, table, lens, cu, 0.3, window, d)
+    for hint in (1, 4, 40):
+        o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens), cu_q=dev(cu),
+                                  max_q_len=hint, scale=0.3, window=window)
+        assert np.array_equal(np.isnan(to_np64(o)), np.isnan(dirty[0]))
+        assert np.array_equal(np.isnan(to_np64(lse)), np.isnan(dirty[1]))
+        zero = lambda x, like: np.where(np.isnan(like), 0, x)
+        want = (zero(clean[0], dirty[0]), zero(clean[1], dirty[1]), zero(clean[2], dirty[0]), zero(clean[3], dirty[1]))
+        check(torch.where(o.isnan(), 0, o), torch.where(lse.isnan(), 0, lse), want, dtype)
+    assert fa.get_status() == fa.FA_OK
