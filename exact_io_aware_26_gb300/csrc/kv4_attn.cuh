@@ -550,8 +550,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       }
     };
     if constexpr (CL) load_q();  // on their way beside the first units (shares: no gain, more registers)
-    if constexpr (!C::across)
+    if constexpr (!C::across) {
       for (int s = 0, u = first + warp; s < S && u < last; ++s, u += kWarps) produce((ring_at.stage + s) % S);
+      __syncwarp();  // the stages' words, which lane 0 writes (of later copies: the unit loop's)
+    }
     if constexpr (!CL) load_q();
     // query rows: column n = g + 8 j of the tile's rows, this lane's channels, as B fragments.
     // Each row is brought to a largest magnitude in [1, 2) by a power of two (exact),
