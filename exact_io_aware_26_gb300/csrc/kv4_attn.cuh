@@ -43,6 +43,8 @@
 // 54% (codes to fp16) and four warps a scheduler, and about 13 us are start-up, uneven ends
 // and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.1 us.
 #pragma once
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "kv4_ring.cuh"
 #include "ops.h"
@@ -230,7 +232,7 @@ struct Feed {
   int ids_r, ids_tok;     // request and first token that `id` was read for
   int id[2][32];          // pages of the two blocks of each of the 32 units
   ulonglong2 src[32];     // addresses of the two blocks; 1 for one that is not to be read
-  uint32_t hidden[8];     // per ring stage: bit h for block h not read, or kStageIdle
+  uint32_t hidden[8];     // per ring stage: bit h for block h not read, or kStageIdle (across)
 };
 
 // Fills src with the warp's next units of the share, at most 32, all of one tile; returns
@@ -287,18 +289,16 @@ __device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, con
   return n;
 }
 
-// A wait gave up (which is recorded, and void what this launch writes): the warp's copies
+// A wait gave up (which is recorded, and void what this launch writes): the warp's n copies
 // under way must land, within one limit for all of them, before anything else is written over
 // the ring or the CTA ends.  No more are issued and no unit is consumed from then on, but the
-// CTA goes through its barriers to the end.
-template <int S>
-__device__ __noinline__ void drain_ring(WaitCtx wc, uint32_t bar0, uint32_t* words, Ring<S> at) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
+// CTA goes through its barriers to the end.  W: the context, by reference in shares and by value in
+// clusters, which is what costs the unit loop least (decode_n16384 145.0 and 146.7 us, shares;
+// decode_n2048 9.08 and 8.90, clusters).
+template <int S, typename W>
+__device__ __noinline__ void drain_ring(W wc, uint32_t bar0, Ring<S> at, int n) {
   const uint64_t since = globaltimer_ns();
-  at.each_armed(words, [&](int s, uint32_t p) { mbar_drain_since(wc, bar0 + 8 * s, p, since); });
-  __syncwarp();
-  if (lane < S) words[lane] = kStageIdle;
+  at.each(n, [&](int s, uint32_t p) { mbar_drain_since(wc, bar0 + 8 * s, p, since); });
   __syncwarp();
 }
 
@@ -423,11 +423,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   }
 
   const Magic magic;
+  using Context = std::conditional_t<CL, WaitCtx, const WaitCtx&>;
   const WaitCtx wc{&abort_s, a.rep.st, a.rep.epoch, a.rep.wait_ns};
 
   Feed<ROWS>& feed = feed_s[warp];
-  if (lane < S) feed.hidden[lane] = kStageIdle;
-  __syncwarp();
   if (!CL && lane == 0) {
     feed.w.at(a, reqs, cache_r0, start_r, start_t, start_h);
     feed.tile0 = start_u;
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       ready = feed_refill<D, ROWS, kWarps>(a, feed, reqs, cache_r0, warp, u1);
       turn = 0;
       if (ready == 0) {
-        if (lane == 0) feed.hidden[stage] = kStageIdle;
+        if (C::across && lane == 0) feed.hidden[stage] = kStageIdle;
         return;
       }
     }
@@ -715,9 +714,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     };
 
     constexpr int kGaveUp = S;
+    int u;
     int held = -1;  // stage of the tile's last unit, kept for the join (across); kGaveUp
 #pragma unroll 1
-    for (int u = first + warp; u < last; u += kWarps) {
+    for (u = first + warp; u < last; u += kWarps) {
       const int stage = ring_at.stage;
       if (!warp_wait(wc, bar0 + 8 * stage, ring_at.parity)) {
         held = kGaveUp;
@@ -831,14 +831,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       __syncwarp();  // every lane has read the stage
       if (C::across ? u + kWarps < last : u + S * kWarps < last)
         produce(stage);
-      else {
+      else
         held = stage;
-        if (!C::across && lane == 0) feed.hidden[stage] = kStageIdle;
-      }
       ring_at.next();
     }
     if (held == kGaveUp) {
-      drain_ring<S>(wc, bar0, feed.hidden, ring_at);
+      __syncwarp();
+      drain_ring<S, Context>(wc, bar0, ring_at, C::across ? ring_at.armed(feed.hidden) : min(S, (last - u + kWarps - 1) / kWarps));
       held = ring_at.stage;
     }
 
@@ -994,8 +993,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     }
     if constexpr (!CL) {
       if (given_up) {
-        if (held >= 0 && lane == 0) feed.hidden[held] = kStageIdle;  // consumed
-        drain_ring<S>(wc, bar0, feed.hidden, ring_at);
+        if constexpr (C::across) {  // what was fetched of the coming tiles
+          if (held >= 0 && lane == 0) feed.hidden[held] = kStageIdle;  // consumed
+          __syncwarp();
+          drain_ring<S, Context>(wc, bar0, ring_at, ring_at.armed(feed.hidden));
+        }
         break;
       }
     }

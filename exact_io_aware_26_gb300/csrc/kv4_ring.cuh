@@ -12,8 +12,8 @@
 
 namespace fa {
 
-// A stage's word: bit h for a block h of its unit that is not read, or kStageIdle alone where
-// no copy is under way and none has landed that is still to be consumed.
+// A stage's word: bit h for a block h of its unit that is not read, or kStageIdle where there was
+// no unit left to copy.
 constexpr uint32_t kStageIdle = 4;
 
 template <int S>
@@ -27,13 +27,18 @@ struct Ring {
       parity ^= 1u;
     }
   }
-  // Calls f(stage, parity) for each stage with a copy under way, in the order of their arming.
+  // Units that have a copy, of those that the stages were last filled for.
+  __host__ __device__ inline int armed(const uint32_t* words) const {
+    int n = 0;
+    while (n < S && !(words[(stage + n) % S] & kStageIdle)) ++n;
+    return n;
+  }
+  // Calls f(stage, parity) for the coming n units, n <= S.
   template <class F>
-  __host__ __device__ inline void each_armed(const volatile uint32_t* words, F f) const {
-    for (int k = 0; k < S; ++k) {
+  __host__ __device__ inline void each(int n, F f) const {
+    for (int k = 0; k < n; ++k) {
       const bool around = stage + k >= S;
-      const int s = around ? stage + k - S : stage + k;
-      if (!(words[s] & kStageIdle)) f(s, around ? parity ^ 1u : parity);
+      f(around ? stage + k - S : stage + k, around ? parity ^ 1u : parity);
     }
   }
 };

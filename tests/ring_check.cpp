@@ -46,7 +46,7 @@ struct Barrier {
 template <int S>
 int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails, std::mt19937& rng) {
   uint32_t words[S];
-  for (auto& w : words) w = kStageIdle;
+  for (auto& w : words) w = (uint32_t)(rng() % 8);  // whatever shared memory holds
   Barrier bars[S];
   std::vector<int> in(S, -1);  // unit of a stage: armed or landed, -1 when consumed
   Ring<S> at;
@@ -61,7 +61,7 @@ int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails
   auto produce = [&](int s) {
     CHECK(!stopped);
     if (across ? left == 0 : left_of_tile == 0) {
-      words[s] = kStageIdle;
+      if (across) words[s] = kStageIdle;
       return;
     }
     CHECK(in[s] == -1);
@@ -71,11 +71,12 @@ int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails
     --left;
     --left_of_tile;
   };
-  auto drain = [&] {
+  auto drain = [&](int n) {
     stopped = true;
+    CHECK(n <= S);
     std::vector<int> named(S, 0);
     int before = -1;
-    at.each_armed(words, [&](int s, uint32_t p) {
+    at.each(n, [&](int s, uint32_t p) {
       CHECK(!named[s]++);
       CHECK(in[s] != -1 && in[s] > before);  // in the order of their arming
       before = in[s];
@@ -86,7 +87,6 @@ int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails
     for (int s = 0; s < S; ++s) {
       CHECK(!bars[s].armed);
       CHECK(named[s] == (in[s] != -1));
-      words[s] = kStageIdle;
       in[s] = -1;  // given up
     }
   };
@@ -107,12 +107,12 @@ int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails
       if (consumed == give_up) {
         given_up = true;
         if (warp_fails) {
-          drain();
+          drain(across ? at.armed(words) : n - u < S ? n - u : S);
           held = s;
           break;
         }
       }
-      CHECK(in[s] == consumed && !(words[s] & kStageIdle));
+      CHECK(in[s] == consumed && (!across || !(words[s] & kStageIdle)));
       if (bars[s].armed) {
         CHECK(!bars[s].done(at.parity));
         bars[s].land();
@@ -124,7 +124,6 @@ int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails
         produce(s);
       } else {
         held = s;
-        if (!across) words[s] = kStageIdle;
       }
       at.next();
     }
@@ -135,13 +134,15 @@ int run(const std::vector<int>& tiles, bool across, int give_up, bool warp_fails
       for (auto& b : bars) CHECK(!b.armed);
     }
     if (given_up) {
-      if (across && held >= 0) words[held] = kStageIdle;
-      drain();
+      if (across) {
+        if (held >= 0) words[held] = kStageIdle;
+        drain(at.armed(words));
+      }
       return 1;
     }
     if (across && held >= 0) produce(held);
   }
-  at.each_armed(words, [&](int, uint32_t) { CHECK(false); });
+  if (across) CHECK(at.armed(words) == 0);
   for (auto& b : bars) CHECK(!b.armed);
   return 0;
 }
