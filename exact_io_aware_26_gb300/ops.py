@@ -144,7 +144,7 @@ def _call(op: int, tensors: tuple, scalars: tuple, stream, plan):
             with torch.cuda.stream(stream):
                 return _call(op, tensors, scalars, None, plan)
     got = _launch.run(op, tensors, scalars)
-    if got is None:
+    while got is None:  # again where another thread empties the table before this one's plan has run
         device, args, outputs, results, keep = plan(*tensors, *scalars)
         entry = ctypes.cast(getattr(load(), _ENTRY[op]), ctypes.c_void_p).value
         _launch.register(op, tensors, scalars, entry, device.index, args, outputs, results, keep)
