@@ -231,9 +231,10 @@ bool overlap(const int* a, int na, const int* b, int nb) { return a < b + nb && 
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
   const size_t smem = (size_t)a.R * 17;
-  static_assert(FA_PLAN_MAX_REQUESTS * 17 + 4096 <= 227 * 1024, "a CTA's shared memory holds every request");
-  if (smem > 40 * 1024) {  // beyond what every kernel may have
-    const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int kMost = FA_PLAN_MAX_REQUESTS * 17;
+  static_assert(kMost + 4096 <= 227 * 1024, "a CTA's shared memory holds every request");
+  if (smem > 40 * 1024) {  // beyond what every kernel may have: one limit for all calls, which may run at once
+    const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   // A token for each thread, and threads for the pages of ended requests besides (the step of

@@ -1,4 +1,7 @@
 """Edges of the operators around the attention."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -57,4 +60,34 @@ def test_a_nan_reaches_what_the_formula_says(cuda_lib, side, tok, group, window,
         zero = lambda x, like: np.where(np.isnan(like), 0, x)
         want = (zero(clean[0], dirty[0]), zero(clean[1], dirty[1]), zero(clean[2], dirty[0]), zero(clean[3], dirty[1]))
         check(torch.where(o.isnan(), 0, o), torch.where(lse.isnan(), 0, lse), want, dtype)
+    assert fa.get_status() == fa.FA_OK
+
+
+def test_plans_of_different_sizes_from_several_host_threads(cuda_lib):
+    """The C entry from threads that do not hold a common lock, with requests for more than
+    the shared memory that every kernel may have, and for all of it."""
+    lib, failed = fa.load(), []
+
+    def work(R, turns):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        seq, new, table = torch.zeros(R, **i32), torch.ones(R, **i32), torch.full((R, 2), -1, **i32)
+        free, count = torch.arange(R, **i32), torch.full((3,), R, **i32)
+        outs = [torch.empty(n, **i32) for n in (R, R + 1, R, R, 3)]
+        p = fa.FaPlanParams(R, R, 16, R, 2, 2)
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        ptrs = [t.data_ptr() for t in (seq, new, table, free, count, *outs)]
+        for _ in range(turns):
+            status = lib.fa_paged_plan(ctypes.byref(p), *ptrs, stream.cuda_stream)
+            if status != fa.FA_OK:
+                failed.append((R, status, lib.fa_last_error()))
+                break
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=a) for a in ((8192, 3000), (2500, 3000), (4000, 3000))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
     assert fa.get_status() == fa.FA_OK
