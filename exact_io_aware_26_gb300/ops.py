@@ -46,7 +46,19 @@ _CODES = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}
 _I64x2, _I64x3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
 
 
-class FaQkParams(ctypes.Structure):
+class _Params(ctypes.Structure):
+    """A struct that refuses numbers its C ints do not hold (ctypes would keep their low bits,
+    and the call be made with another size)."""
+
+    def __init__(self, *args, **kw):
+        given = {**dict(zip((name for name, _ in self._fields_), args)), **kw}
+        for name, kind in self._fields_:
+            if kind is ctypes.c_int and not -2 ** 31 <= given.get(name, 0) < 2 ** 31:
+                raise ValueError(f"{name} = {given[name]} is beyond 32 bits")
+        super().__init__(*args, **kw)
+
+
+class FaQkParams(_Params):
     """Mirror of ``fa_qk_params``."""
     _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
                 ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
@@ -55,18 +67,18 @@ class FaQkParams(ctypes.Structure):
                 ("yq_stride", _I64x3), ("yk_stride", _I64x3), ("dq_stride", _I64x3), ("dk_stride", _I64x3)]
 
 
-class FaKv4Cache(ctypes.Structure):
+class FaKv4Cache(_Params):
     """Mirror of ``fa_kv4_cache``."""
     _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hk", ctypes.c_int), ("d", ctypes.c_int),
                 ("page_stride", ctypes.c_longlong)]
 
 
-class FaKv4Rows(ctypes.Structure):
+class FaKv4Rows(_Params):
     """Mirror of ``fa_kv4_rows``."""
     _fields_ = [("T", ctypes.c_int), ("dtype", ctypes.c_int), ("k_stride", _I64x2), ("v_stride", _I64x2)]
 
 
-class FaKv4AttnParams(ctypes.Structure):
+class FaKv4AttnParams(_Params):
     """Mirror of ``fa_kv4_attn_params``."""
     _fields_ = [("R", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("max_q_len", ctypes.c_int), ("window", ctypes.c_int), ("table_width", ctypes.c_int),
@@ -74,7 +86,7 @@ class FaKv4AttnParams(ctypes.Structure):
                 ("o_stride", _I64x2)]
 
 
-class FaPlanParams(ctypes.Structure):
+class FaPlanParams(_Params):
     """Mirror of ``fa_plan_params``."""
     _fields_ = [("R", ctypes.c_int), ("T", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("table_width", ctypes.c_int), ("table_stride", ctypes.c_longlong)]

@@ -91,3 +91,19 @@ def test_plans_of_different_sizes_from_several_host_threads(cuda_lib):
         t.join()
     assert not failed
     assert fa.get_status() == fa.FA_OK
+
+
+def test_numbers_beyond_32_bits_are_refused(cuda_lib):
+    q, cache, table, lens, cu = build([40], [1], 2, 1, 64, "bf16", 16, 33)
+    args = (q.cuda(), dev(cache), dev(table), dev(lens))
+    with pytest.raises(ValueError):
+        fa.kv4_attention(*args, window=2 ** 32 + 1)
+    with pytest.raises(ValueError):
+        fa.kv4_attention(*args, max_q_len=2 ** 32 + 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = (torch.zeros(1, **i32), torch.ones(1, **i32), torch.full((1, 4), -1, **i32), torch.arange(4, **i32), torch.full((1,), 4, **i32))
+    with pytest.raises(ValueError):
+        fa.paged_plan(*plan, page_size=2 ** 32 + 16, T=4)
+    with pytest.raises(ValueError):
+        fa.paged_plan(*plan, page_size=16, T=2 ** 32 + 4)
+    assert fa.paged_plan(*plan, page_size=16, T=4)["counts"].tolist() == [3, 1, 0]

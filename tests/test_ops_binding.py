@@ -1,6 +1,9 @@
 """The binding of the operators around the attention, without a GPU."""
 import types
 
+import pytest
+
+import exact_io_aware_26_gb300 as fa
 from exact_io_aware_26_gb300 import ops
 
 
@@ -23,3 +26,18 @@ def test_a_call_whose_plan_was_dropped_is_made_all_the_same(monkeypatch):
     monkeypatch.setattr(ops, "load", lambda: types.SimpleNamespace(fa_kv4_append=ops.ctypes.CFUNCTYPE(None)(lambda: None)))
     got = ops._call(ops._APPEND, (None,), (), None, lambda *a: (device, [], [], [], None))
     assert got == ("done",) and len(made) == 3
+
+
+@pytest.mark.parametrize("make", [
+    lambda n: fa.FaPlanParams(4, n, 16, 10, 4, 4), lambda n: fa.FaPlanParams(4, 4, n, 10, 4, 4),
+    lambda n: fa.FaPlanParams(R=4, T=4, page_size=16, num_pages=n, table_width=4, table_stride=4),
+    lambda n: fa.FaKv4AttnParams(R=2, T=2, Hq=4, dtype=fa.FA_BF16, max_q_len=1, window=n, table_width=5, scale=0.1, table_stride=5),
+    lambda n: fa.FaKv4AttnParams(2, 2, 4, fa.FA_BF16, n), lambda n: fa.FaKv4Cache(n, 64, 2, 64, 10240),
+    lambda n: fa.FaKv4Rows(n, fa.FA_BF16), lambda n: fa.FaQkParams(B=1, N=n, Hq=1, Hk=1, d=64),
+])
+def test_numbers_that_a_c_int_does_not_hold_are_refused(make):
+    """They would be cut to their low 32 bits, and the call made with another number."""
+    make(2 ** 31 - 1)
+    for n in (2 ** 31, 2 ** 32 + 1, 2 ** 32 + 16, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match=str(n)):
+            make(n)
