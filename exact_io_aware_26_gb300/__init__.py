@@ -108,8 +108,8 @@ def load() -> ctypes.CDLL:
         "fa_fp8_quantize": (I, [PP, P, P, P, P, P, P, P, P, P, P, P]),
         "fa_fwd_fp8": (I, [PP, P, P, P, P, P, P, P, P, P]),
     }
-    from . import ops
-    sigs.update(ops.signatures())
+    from . import _abi
+    sigs.update(_abi.signatures())
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args

@@ -25,17 +25,14 @@ as used there.  New results of up to 1 MB share a block of memory.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 from typing import Optional
 
 import torch
 
 from . import FA_BF16, FA_F16, FA_F32, _check, load
-
-try:
-    from . import _launch
-except ImportError as e:
-    raise ImportError("_launch.so is missing or does not load: run exact_io_aware_26_gb300.build() first") from e
+from ._abi import I64x2, I64x3, FaKv4AttnParams, FaKv4Cache, FaKv4Rows, FaPlanParams, FaQkParams
 
 KV4_GROUP = 32    # channels that share a (scale, base) pair
 KV4_BLOCK = 16    # tokens of a cache block
@@ -43,70 +40,6 @@ KV4_SATURATE = 16384.0
 PLAN_MAX_REQUESTS = 8192
 
 _CODES = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}
-_I64x2, _I64x3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
-
-
-class _Params(ctypes.Structure):
-    """A struct that refuses numbers its C ints do not hold (ctypes would keep their low bits,
-    and the call be made with another size)."""
-
-    def __init__(self, *args, **kw):
-        given = {**dict(zip((name for name, _ in self._fields_), args)), **kw}
-        for name, kind in self._fields_:
-            if kind is ctypes.c_int and not -2 ** 31 <= given.get(name, 0) < 2 ** 31:
-                raise ValueError(f"{name} = {given[name]} is beyond 32 bits")
-        super().__init__(*args, **kw)
-
-
-class FaQkParams(_Params):
-    """Mirror of ``fa_qk_params``."""
-    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
-                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
-                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("eps", ctypes.c_float),
-                ("pos_stride", ctypes.c_longlong), ("q_stride", _I64x3), ("k_stride", _I64x3),
-                ("yq_stride", _I64x3), ("yk_stride", _I64x3), ("dq_stride", _I64x3), ("dk_stride", _I64x3)]
-
-
-class FaKv4Cache(_Params):
-    """Mirror of ``fa_kv4_cache``."""
-    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hk", ctypes.c_int), ("d", ctypes.c_int),
-                ("page_stride", ctypes.c_longlong)]
-
-
-class FaKv4Rows(_Params):
-    """Mirror of ``fa_kv4_rows``."""
-    _fields_ = [("T", ctypes.c_int), ("dtype", ctypes.c_int), ("k_stride", _I64x2), ("v_stride", _I64x2)]
-
-
-class FaKv4AttnParams(_Params):
-    """Mirror of ``fa_kv4_attn_params``."""
-    _fields_ = [("R", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("dtype", ctypes.c_int),
-                ("max_q_len", ctypes.c_int), ("window", ctypes.c_int), ("table_width", ctypes.c_int),
-                ("scale", ctypes.c_float), ("table_stride", ctypes.c_longlong), ("q_stride", _I64x2),
-                ("o_stride", _I64x2)]
-
-
-class FaPlanParams(_Params):
-    """Mirror of ``fa_plan_params``."""
-    _fields_ = [("R", ctypes.c_int), ("T", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int),
-                ("table_width", ctypes.c_int), ("table_stride", ctypes.c_longlong)]
-
-
-def signatures() -> dict:
-    """(result, arguments) of the C functions that this module calls."""
-    P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-    QP, CP, RP, AP, PP = (ctypes.POINTER(t) for t in (FaQkParams, FaKv4Cache, FaKv4Rows, FaKv4AttnParams, FaPlanParams))
-    return {
-        "fa_qk_norm_rope": (I, [QP] + [P] * 9),
-        "fa_qk_norm_rope_bwd_workspace_size": (S, [QP]),
-        "fa_qk_norm_rope_bwd": (I, [QP] + [P] * 13 + [S, P]),
-        "fa_kv4_block_bytes": (I, [I]),
-        "fa_kv4_append": (I, [CP, RP] + [P] * 5),
-        "fa_kv4_gather": (I, [CP, RP] + [P] * 5),
-        "fa_kv4_attention_workspace_size": (S, [CP, AP]),
-        "fa_kv4_attention": (I, [CP, AP] + [P] * 8 + [S, P]),
-        "fa_paged_plan": (I, [PP] + [P] * 11),
-    }
 
 
 # ---------------------------------------------------------------- checks and calls
@@ -118,6 +51,16 @@ def signatures() -> dict:
 _QK, _QK_BWD, _APPEND, _GATHER, _ATTENTION, _PLAN = range(6)
 _ENTRY = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attention", "fa_paged_plan")
 _STREAM = (3, 0)
+_launch = None  # the extension, from the first call on
+
+
+def _extension():
+    global _launch
+    try:
+        _launch = importlib.import_module("._launch", __package__)
+    except ImportError as e:
+        raise ImportError(f"_launch.so is missing or does not load ({e}): run exact_io_aware_26_gb300.build() first") from e
+    return _launch
 
 
 def _in(i: int) -> tuple:
@@ -155,12 +98,13 @@ def _call(op: int, tensors: tuple, scalars: tuple, stream, plan):
                     t.record_stream(stream)
             with torch.cuda.stream(stream):
                 return _call(op, tensors, scalars, None, plan)
-    got = _launch.run(op, tensors, scalars)
+    launch = _launch or _extension()
+    got = launch.run(op, tensors, scalars)
     while got is None:  # again where another thread empties the table before this one's plan has run
         device, args, outputs, results, keep = plan(*tensors, *scalars)
         entry = ctypes.cast(getattr(load(), _ENTRY[op]), ctypes.c_void_p).value
-        _launch.register(op, tensors, scalars, entry, device.index, args, outputs, results, keep)
-        got = _launch.run(op, tensors, scalars)
+        launch.register(op, tensors, scalars, entry, device.index, args, outputs, results, keep)
+        got = launch.run(op, tensors, scalars)
     if type(got) is int:
         _check(got, _ENTRY[op])
     return got
@@ -272,8 +216,8 @@ def _qk_checked(q, k, wq, wk, freqs, positions, eps, interleaved, heads_first, y
         else:
             ds.append(_dense((B, N, h), (N * h * d, h * d, d)))
     p = FaQkParams(B, N, Hq, Hk, d, _CODES[dt], _CODES[wt], 2 * freqs.shape[0], int(bool(interleaved)), float(eps),
-                   pos_stride, _I64x3(*_strides(q, "q", _BNH)), _I64x3(*_strides(k, "k", _BNH)), _I64x3(*ys[0]),
-                   _I64x3(*ys[1]), _I64x3(*ds[0]), _I64x3(*ds[1]))
+                   pos_stride, I64x3(*_strides(q, "q", _BNH)), I64x3(*_strides(k, "k", _BNH)), I64x3(*ys[0]),
+                   I64x3(*ys[1]), I64x3(*ds[0]), I64x3(*ds[1]))
     return p, device, shapes
 
 
@@ -355,7 +299,7 @@ def _rows_checked(cache, slots, k, v, T, H, d, dtype, heads_first, names):
         else:
             _need(x, name, dtype, (H, T, d) if heads_first else (T, H, d))
             strides.append(_strides(x, name, (1, 0) if heads_first else (0, 1)))
-    rows = FaKv4Rows(T, _CODES[dtype], _I64x2(*strides[0]), _I64x2(*strides[1]))
+    rows = FaKv4Rows(T, _CODES[dtype], I64x2(*strides[0]), I64x2(*strides[1]))
     return c, rows, _one_device(cache, slots, k, v)
 
 
@@ -421,7 +365,7 @@ def _plan_attention(q, cache, block_table, kv_lens, cu_q, out, lse, workspace, m
     device = _one_device(q, cache, block_table, kv_lens, cu_q, out, lse)
     p = FaKv4AttnParams(R, T, Hq, _CODES[q.dtype], int(max_q_len), int(window), width,
                         1.0 / math.sqrt(d) if scale is None else float(scale),
-                        block_table.stride(0) if R > 1 else width, _I64x2(*_strides(q, "q", (0, 1))), _I64x2(*o_stride))
+                        block_table.stride(0) if R > 1 else width, I64x2(*_strides(q, "q", (0, 1))), I64x2(*o_stride))
     new = _Outputs()
     res = [new.given(5, out, (T, Hq, d), q.dtype), new.given(6, lse, (T, Hq), torch.float32)]
     ws, nbytes = _workspace(new, 7, workspace, load().fa_kv4_attention_workspace_size(ctypes.byref(c), ctypes.byref(p)), device)

@@ -1,10 +1,15 @@
 """The binding of the operators around the attention, without a GPU."""
+import os
+import subprocess
+import sys
 import types
 
 import pytest
 
 import exact_io_aware_26_gb300 as fa
 from exact_io_aware_26_gb300 import ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def test_a_call_whose_plan_was_dropped_is_made_all_the_same(monkeypatch):
@@ -41,3 +46,40 @@ def test_numbers_that_a_c_int_does_not_hold_are_refused(make):
     for n in (2 ** 31, 2 ** 32 + 1, 2 ** 32 + 16, -2 ** 31 - 1):
         with pytest.raises(ValueError, match=str(n)):
             make(n)
+
+
+@pytest.mark.parametrize("absent", [["exact_io_aware_26_gb300._launch"], ["exact_io_aware_26_gb300._launch", "torch"]])
+def test_the_attention_needs_the_library_alone(absent):
+    """Neither the extension of the operators nor torch is needed to load libfa.so and to call
+    a function that takes no tensor."""
+    fa.build()
+    code = f"""
+import sys
+sys.modules.update(dict.fromkeys({absent!r}))  # importing one of them raises ImportError
+import exact_io_aware_26_gb300 as fa
+fa.load()
+p = fa.FaParams(B=1, H=1, N=128, d=64, dtype=fa.FA_BF16, scale=0.125)
+assert fa.check_params(p) == fa.FA_OK
+fa.use_library(fa.use_library(fa.LIB_PATH))
+assert fa.load().fa_kv4_block_bytes(64) == 1280
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_an_operator_without_the_extension_says_what_to_do():
+    code = """
+import sys
+sys.modules["exact_io_aware_26_gb300._launch"] = None
+import torch
+import exact_io_aware_26_gb300 as fa
+i = torch.zeros(2, dtype=torch.int32)
+try:
+    fa.paged_plan(i, i, i[None], i, i, 16, 2)
+except ImportError as e:
+    assert "build()" in str(e)
+else:
+    raise SystemExit("no error")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
