@@ -9,6 +9,7 @@ symbol-export tests) and runs on any sm_103 device.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -63,11 +64,28 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     return obj
 
 
+def linked_against() -> str | None:
+    """The Python and the torch that _launch.so is built for, as text; None without torch.
+    (Read from torch's files: importing it takes seconds.)"""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    where = list(spec.submodule_search_locations)[0]
+    with open(os.path.join(where, "version.py")) as f:
+        return "\n".join([str(sysconfig.get_config_var("SOABI")), where, f.read()])
+
+
 def build_launch(force: bool = False) -> str:
-    """Build _launch.so if its source is newer (or if forced); returns its path."""
-    if not force and os.path.exists(LAUNCH) and all(
+    """Build _launch.so if its source is newer or it was built for another Python or torch
+    (or if forced); returns its path."""
+    made_for, note = linked_against(), os.path.join(BUILD, "launch_made_for.txt")
+    if made_for is None:
+        raise RuntimeError("torch is not installed: the operators around the attention need it")
+    if not force and os.path.exists(LAUNCH) and os.path.exists(note) and all(
             os.path.getmtime(p) <= os.path.getmtime(LAUNCH) for p in (LAUNCH_SOURCE, os.path.abspath(__file__))):
-        return LAUNCH
+        with open(note) as f:
+            if f.read() == made_for:
+                return LAUNCH
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -81,16 +99,22 @@ def build_launch(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on launch.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LAUNCH)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(note, "w") as f:
+        f.write(made_for)
     return LAUNCH
 
 
 def build(force: bool = False, extra_flags: list[str] | None = None, verbose: bool = False,
           debug: bool = False) -> str:
     """Build libfa.so (debug: libfa_debug.so, with the kernels' index checks) if any
-    source is newer than it (or if forced), and _launch.so; returns its path."""
+    source is newer than it (or if forced), and, with torch installed, _launch.so; returns
+    the library's path.  The library is in place also where _launch.so fails to build."""
     lib, build_dir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
+    with_torch = linked_against() is not None
     if not force and up_to_date(lib):
-        build_launch()
+        if with_torch:
+            build_launch()
         return lib
     os.makedirs(build_dir, exist_ok=True)
     extra = list(extra_flags or [])
@@ -99,15 +123,16 @@ def build(force: bool = False, extra_flags: list[str] | None = None, verbose: bo
     if verbose:
         extra += ["-Xptxas", "-v"]
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        launch = ex.submit(build_launch, force)
+        launch = ex.submit(build_launch, force) if with_torch else None
         objs = list(ex.map(lambda s: _compile(s, extra, build_dir), SOURCES))
-        launch.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if launch is not None:
+        launch.result()
     return lib
 
 

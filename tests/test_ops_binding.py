@@ -1,13 +1,15 @@
 """The binding of the operators around the attention, without a GPU."""
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 import types
 
 import pytest
 
 import exact_io_aware_26_gb300 as fa
-from exact_io_aware_26_gb300 import ops
+from exact_io_aware_26_gb300 import _builder, ops
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -83,3 +85,56 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_the_extension_is_built_again_for_another_python_or_torch(tmp_path, monkeypatch):
+    """Its file is newer than its source, but it was linked against other libraries."""
+    import torch
+    torch_spec = importlib.util.find_spec("torch")
+    monkeypatch.setattr(_builder, "LAUNCH", str(tmp_path / "_launch.so"))
+    monkeypatch.setattr(_builder, "BUILD", str(tmp_path))
+    built = []
+
+    def run(cmd, **kw):
+        built.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(_builder.subprocess, "run", run)
+    _builder.build_launch()
+    _builder.build_launch()
+    assert len(built) == 1
+    config_var = sysconfig.get_config_var
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda n: "cpython-399-none" if n == "SOABI" else config_var(n))
+        _builder.build_launch()
+        _builder.build_launch()
+    assert len(built) == 2
+    _builder.build_launch()
+    assert len(built) == 3
+    # a torch package with the files of this one, of another version
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '99.0'\n")
+    spec = types.SimpleNamespace(submodule_search_locations=[str(other)], origin=str(other / "__init__.py"))
+    with monkeypatch.context() as m:
+        m.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else torch_spec)
+        _builder.build_launch()
+    assert len(built) == 4
+
+
+def test_the_library_is_in_place_when_the_extension_fails(tmp_path, monkeypatch):
+    """A compiler or a torch that the extension cannot be built with costs its operators only."""
+    monkeypatch.setattr(_builder, "LIB", str(tmp_path / "libfa.so"))
+    monkeypatch.setattr(_builder, "BUILD", str(tmp_path))
+    monkeypatch.setattr(_builder, "_compile", lambda src, extra, build_dir: src)
+    monkeypatch.setattr(_builder.subprocess, "run",
+                        lambda cmd, **kw: (open(cmd[cmd.index("-o") + 1], "w").close(), subprocess.CompletedProcess(cmd, 0, "", ""))[1])
+
+    def fails(force=False):
+        raise RuntimeError("g++ failed")
+
+    monkeypatch.setattr(_builder, "build_launch", fails)
+    with pytest.raises(RuntimeError, match=r"g\+\+ failed"):
+        _builder.build(force=True)
+    assert os.path.exists(tmp_path / "libfa.so")
