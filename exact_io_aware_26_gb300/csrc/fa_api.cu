@@ -828,7 +828,9 @@ fa_status fa_get_status(void* stream) {
   if ((e = cudaMemcpy(&code, &st->code, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return cuda_fail(e, "reading the status word");
   if (code != 0) {
-    if ((e = cudaMemset(&st->code, 0, sizeof(int))) != cudaSuccess)
+    // the code, and the epoch that lets a failed launch's other CTAs give up: a graph of an
+    // earlier launch would otherwise give up at its next replay, without a word
+    if ((e = cudaMemset(st, 0, sizeof(*st))) != cudaSuccess)
       return cuda_fail(e, "clearing the status word");
     set_err("device reported: %s", fa_status_string(code));
   }

@@ -11,8 +11,8 @@ namespace fa {
 
 // Library status word in device memory (one per device).  `code` is the first
 // device-side error since the last fa_get_status(); `abort_epoch` is the
-// highest launch epoch in which some CTA gave up, so that the other CTAs of
-// the same launch stop waiting too.
+// highest launch epoch in which some CTA gave up since then, so that the other
+// CTAs of the same launch stop waiting too.
 struct DevStatus {
   int code;
   unsigned int abort_epoch;

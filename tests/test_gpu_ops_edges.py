@@ -1,4 +1,4 @@
-"""Edges of the operators around the attention."""
+"""Edges of the operators around the attention, and of what the status word says."""
 import ctypes
 import threading
 
@@ -107,3 +107,25 @@ def test_numbers_beyond_32_bits_are_refused(cuda_lib):
     with pytest.raises(ValueError):
         fa.paged_plan(*plan, page_size=16, T=2 ** 32 + 4)
     assert fa.paged_plan(*plan, page_size=16, T=4)["counts"].tolist() == [3, 1, 0]
+
+
+def test_a_graph_waits_and_reports_after_another_launch_gave_up(cuda_lib):
+    """A launch that is replayed after the status of a later launch's failure was read neither
+    gives up at once nor does it keep silent about a wait that runs out."""
+    assert fa.get_status() == fa.FA_OK
+    old = fa.set_wait_limit_ns(20_000_000)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fa.selftest_timeout()  # an earlier launch than the next one
+        fa.selftest_timeout()
+        assert fa.get_status() == fa.FA_ERR_TIMEOUT
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        graph.replay()
+        end.record()
+        assert fa.get_status() == fa.FA_ERR_TIMEOUT
+        assert start.elapsed_time(end) > 15  # its own limit of 20 ms
+        assert fa.get_status() == fa.FA_OK
+    finally:
+        fa.set_wait_limit_ns(old)
