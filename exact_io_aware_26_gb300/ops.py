@@ -244,8 +244,8 @@ def qk_norm_rope(q, k, wq, wk, freqs, positions=None, eps: float = 1e-6, interle
     """(yq, yk): RMS norm of each head of q [B, N, Hq, d] and k [B, N, Hk, d] (any strides of
     whole 16-byte vectors, such as views of one packed projection), times wq, wk [d], then
     the rotation of the first 2 * len(freqs) channels by the positions (int32 [N] or
-    [B, N]; None: 0 .. N - 1).  Results are [B, H, N, d] as ``attention_fwd`` takes them,
-    or, with ``heads_first`` false, [B, N, H, d]; ``out`` (yq, yk) may be (q, k) there."""
+    [B, N]; None: 0 .. N - 1).  Results are [B, H, N, d] as ``attention_fwd`` takes them
+    (where Hq = Hk), or, with ``heads_first`` false, [B, N, H, d]; ``out`` (yq, yk) may be (q, k) there."""
     yq, yk = (None, None) if out is None else out
     return _call(_QK, (q, k, wq, wk, freqs, positions, yq, yk), (float(eps), bool(interleaved), bool(heads_first)),
                  stream, _plan_qk)
@@ -332,8 +332,8 @@ def kv4_append(k, v, slots, cache, stream=None) -> None:
 
 def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = False, out=None, stream=None):
     """(k, v): the cached keys and values of T slots (zeros for a negative one), rounded to
-    ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d] (with a leading batch of one,
-    as ``attention_fwd`` takes them)."""
+    ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d]; with a leading batch of one
+    ``attention_fwd`` takes these for the T queries of the same tokens and Hq = Hk."""
     k, v = (None, None) if out is None else out
     return _call(_GATHER, (cache, slots, k, v), (int(d), dtype, bool(heads_first)), stream, _plan_gather)
 

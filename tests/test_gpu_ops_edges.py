@@ -8,7 +8,7 @@ import torch
 
 import _ops_ref as ref
 import exact_io_aware_26_gb300 as fa
-from _parity import to_np64
+from _parity import check_fwd, to_np64
 from test_gpu_ops_kv4 import build, check, widened
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +129,26 @@ def test_a_graph_waits_and_reports_after_another_launch_gave_up(cuda_lib):
         assert fa.get_status() == fa.FA_OK
     finally:
         fa.set_wait_limit_ns(old)
+
+
+@pytest.mark.parametrize("N,H,d,page", [(150, 3, 64, 16), (77, 2, 128, 32)])
+def test_cached_tokens_read_back_for_the_dense_attention(cuda_lib, N, H, d, page):
+    """Append -> gather -> attention_fwd over a request's cached tokens: the result of
+    kv4_attention on the same cache for all of its rows, both against 64 bits."""
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn(N, 3 * H, d, generator=g).to(torch.float16).cuda()
+    w = torch.ones(d, dtype=torch.float16, device="cuda")
+    q, k = fa.qk_norm_rope(x[None, :, :H], x[None, :, H:2 * H], w, w, fa.rope_freqs(d), heads_first=False)
+    pages = -(-N // page)
+    cache = fa.kv4_cache(pages + 2, H, d, page)
+    table = torch.randperm(pages + 2, generator=g)[:pages].to(torch.int32)
+    slots = (table.long()[torch.arange(N) // page] * page + torch.arange(N) % page).to(torch.int32).cuda()
+    fa.kv4_append(k[0], x[:, 2 * H:], slots, cache)
+    k16, v16 = fa.kv4_gather(cache, slots, d, dtype=torch.float16, heads_first=True)
+    dense, dense_lse = fa.attention_fwd(q.transpose(1, 2).contiguous(), k16[None], v16[None], causal=True)
+    o, lse = fa.kv4_attention(q[0], cache, table[None].cuda(), torch.tensor([N], dtype=torch.int32, device="cuda"),
+                              cu_q=torch.tensor([0, N], dtype=torch.int32, device="cuda"), max_q_len=N)
+    want = ref.attention(to_np64(q[0]), cache.cpu().numpy(), table[None].numpy(), np.array([N]), np.array([0, N]), d ** -0.5, 0, d)
+    check(o, lse, want, "f16")
+    check_fwd(dense[0].transpose(0, 1), dense_lse[0].T, want[0], want[1], "f16")
+    assert fa.get_status() == fa.FA_OK
