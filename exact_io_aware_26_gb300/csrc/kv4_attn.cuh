@@ -53,7 +53,7 @@
 namespace fa {
 namespace {
 
-constexpr float kNoMax = -1e30f;     // running maximum before any token is seen
+constexpr float kNoMax = -3e38f;     // running maximum before any token is seen
 constexpr float kLeast = 1e-37f;     // of a score's factor: a hidden token's -inf times it stays -inf
 constexpr int kUnit = 2 * kKvBlock;  // tokens a warp takes at a time
 constexpr int kReqCache = 128;       // requests whose lengths a CTA keeps at hand
@@ -620,10 +620,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
     const int all_hi = x.kv - x.n + i0 + 1;
     const int all_lo = first_seen(a, x.kv - x.n + i1);
 
+    // m: less the running maximum of the raw products; a score is (product + m) * factor, the
+    // difference first: it is exact near the maximum, so that the weight there is 1 however large
+    // the products (a product with the factor is off by whole powers of two from 2^24 on)
     float m[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      m[j][0] = m[j][1] = kNoMax;
+      m[j][0] = m[j][1] = -kNoMax;
       l[j][0] = l[j][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -784,27 +787,27 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
               }
           }
       }
-      // the running maximum, in log2 units, moved when a score is above it by more than 8
+      // the running maximum, moved when a score is above it by more than 8 in log2 units
       float most[NT][2];
       bool grow = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          most[j][c] = fmax3(fmaxf(s[0][j][c], s[0][j][c + 2]), s[1][j][c], s[1][j][c + 2]) * factor[j][c];
-          grow |= most[j][c] > m[j][c] + 8.f;
+          most[j][c] = fmax3(fmaxf(s[0][j][c], s[0][j][c + 2]), s[1][j][c], s[1][j][c + 2]);
+          grow |= (most[j][c] + m[j][c]) * factor[j][c] > 8.f;
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(most[j][c], m[j][c]);
+            float top = fmaxf(most[j][c], -m[j][c]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float back = ex2(m[j][c] - top);
-            m[j][c] = top;
+            const float back = ex2((-m[j][c] - top) * factor[j][c]);
+            m[j][c] = -top;
             l[j][c] *= back;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -820,7 +823,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][j][c] = ex2(fmaf(s[h][j][c], factor[j][c & 1], -m[j][c & 1]));
+          for (int c = 0; c < 4; c += 2) {
+            float x, y;
+            f2unpack(fmul2(fadd2(f2pack(s[h][j][c], s[h][j][c + 1]), f2pack(m[j][0], m[j][1])), f2pack(factor[j][0], factor[j][1])), x, y);
+            s[h][j][c] = ex2(x);
+            s[h][j][c + 1] = ex2(y);
+          }
           l[j][0] += s[h][j][0] + s[h][j][2];
           l[j][1] += s[h][j][1] + s[h][j][3];
           p0[j] = transpose8x8(pack2<true>(s[h][j][0], s[h][j][1]));
@@ -860,7 +868,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
           v += __shfl_xor_sync(0xffffffffu, v, 16);
           const int row = 8 * j + 2 * t4 + c;
           if (g == 0) {
-            m_s[warp][row] = m[j][c];
+            m_s[warp][row] = m[j][c] == -kNoMax ? kNoMax : -m[j][c] * factor[j][c];
             l_s[warp][row] = v;
           }
           float* to = mine + row * C::LDO + g * (D / 8);

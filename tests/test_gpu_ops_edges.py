@@ -152,3 +152,37 @@ def test_cached_tokens_read_back_for_the_dense_attention(cuda_lib, N, H, d, page
     check(o, lse, want, "f16")
     check_fwd(dense[0].transpose(0, 1), dense_lse[0].T, want[0], want[1], "f16")
     assert fa.get_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d,dtype", [(2, 1, 64, "bf16"), (8, 2, 128, "f16"), (24, 1, 128, "bf16")])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 8, 2.0 ** 12, 2.0 ** 15, 2.0 ** 40, 2.0 ** 95])
+def test_scores_whose_rounding_is_larger_than_one(cuda_lib, size, Hq, Hk, d, dtype, wide):
+    """Scores from 2^4 to 2^123: fp32 keeps them to 2^-24 of themselves, whole powers of the
+    weights.  Where one token leads by more than what d fp32 roundings of the scores' terms
+    make of two scores, its value is the result: within half a step of the type and the leader's
+    weight, in fp16 and at most 2^8 of another, and LSE its score to the same accuracy."""
+    if dtype == "f16" and size > 2.0 ** 8:
+        pytest.skip("16 * 2^12 is beyond fp16's 65504")
+    kv = [1, 2, 300, 900]
+    q, cache, table, lens, cu = build(kv, [1] * 4, Hq, Hk, d, dtype, 16, 34, 16.0)
+    q = (q.double() * size).to(q.dtype)
+    scale = d ** -0.5 * 16
+    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens), scale=scale)
+    o, lse = to_np64(o), to_np64(lse)
+    e, leads = torch.finfo(q.dtype).eps / 2, 0
+    for r, n in enumerate(kv):
+        j = np.arange(n)
+        k, v = ref.slot_values(cache, table[r].astype(np.int64)[j // 16] * 16 + j % 16, d)
+        for h in range(Hq):
+            s = k[:, h // (Hq // Hk)] @ to_np64(q)[r, h] * scale
+            off = 2.0 ** -23 * d * (np.abs(k[:, h // (Hq // Hk)]) @ np.abs(to_np64(q)[r, h])).max() * scale
+            best = int(s.argmax())
+            assert np.isfinite(lse[r, h]) and np.isfinite(o[r, h]).all()
+            assert abs(lse[r, h] - s.max()) <= off + np.log(n) + 2.0 ** -20 * abs(s.max()) + 2.0 ** -20
+            if n == 1 or s[best] - np.delete(s, best).max() > 2 * off + 40:  # e^-40: below a bf16 step of any value here
+                want = v[best, h // (Hq // Hk)]
+                leads += 1
+                assert np.all(np.abs(o[r, h] - want) <= (e + 2.0 ** -11 + 2.0 ** -20) * np.abs(want) + 2.0 ** -20)
+    assert leads >= 2 * Hq
+    assert fa.get_status() == fa.FA_OK
