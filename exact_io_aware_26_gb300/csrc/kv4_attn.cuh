@@ -264,7 +264,11 @@ __device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, con
     f.id[0][lane] = id0;
     f.id[1][lane] = id1;
   }
-  const bool in0 = u + lane * kWarps < end && tok < w.y.k1, in1 = in0 && tok + kKvBlock < w.y.k1;
+  // blocks that some row sees a token of (the first one of a window may lie behind it, in a page
+  // that is no longer the request's)
+  const bool mine = u + lane * kWarps < end;
+  const bool in0 = mine && tok < w.y.k1 && tok + kKvBlock > w.y.k0;
+  const bool in1 = mine && tok + kKvBlock < w.y.k1 && tok + 2 * kKvBlock > w.y.k0;
   const bool ok0 = in0 && (unsigned)id0 < (unsigned)a.c.num_pages, ok1 = in1 && (unsigned)id1 < (unsigned)a.c.num_pages;
   if ((in0 && !ok0) || (in1 && !ok1)) atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
   auto place = [&](int id, int t) {

@@ -186,3 +186,24 @@ def test_scores_whose_rounding_is_larger_than_one(cuda_lib, size, Hq, Hk, d, dty
                 assert np.all(np.abs(o[r, h] - want) <= (e + 2.0 ** -11 + 2.0 ** -20) * np.abs(want) + 2.0 ** -20)
     assert leads >= 2 * Hq
     assert fa.get_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("kv,new,Hq,Hk,d,page,window", [
+    ([300, 77, 32], [1, 1, 1], 4, 2, 64, 16, 40), ([500], [3], 8, 2, 128, 16, 1), ([4000, 130], [2, 5], 12, 2, 64, 32, 100),
+    ([257], [1], 1, 1, 128, 16, 16),
+])
+def test_pages_behind_every_window_are_not_looked_at(cuda_lib, kv, new, Hq, Hk, d, page, window, wide):
+    """A request whose pages behind the window have gone back to the pool, its table's entries
+    with them: the rows' results are those of the whole table, and no bad page is recorded."""
+    q, cache, table, lens, cu = build(kv, new, Hq, Hk, d, "bf16", page, 35)
+    want = ref.attention(to_np64(q), cache, table, lens, cu, 0.3, window, d)
+    for bad in (-1, cache.shape[0] + 5):
+        t = table.copy()
+        for r, (n, m) in enumerate(zip(kv, new)):
+            t[r, :max(0, n - m - window + 1) // page] = bad
+        assert (t != table).any()
+        o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(t) if wide else t), dev(lens), cu_q=dev(cu), max_q_len=max(new),
+                                  scale=0.3, window=window)
+        assert fa.get_status() == fa.FA_OK
+        check(o, lse, want, "bf16")
