@@ -720,14 +720,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       }
     };
 
-    constexpr int kGaveUp = S;
-    int u;
-    int held = -1;  // stage of the tile's last unit, kept for the join (across); kGaveUp
+    constexpr int kGaveUp = S;  // of `held`: and the copies under way
+    int held = -1;  // stage of the tile's last unit, kept for the join (across)
 #pragma unroll 1
-    for (u = first + warp; u < last; u += kWarps) {
+    for (int u = first + warp; u < last; u += kWarps) {
       const int stage = ring_at.stage;
       if (!warp_wait(wc, bar0 + 8 * stage, ring_at.parity)) {
-        held = kGaveUp;
+        held = kGaveUp + (C::across ? 0 : min(S, (last - u + kWarps - 1) / kWarps));
         break;
       }
       const uint32_t kb = ring + stage * C::stage;
@@ -847,9 +846,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
         held = stage;
       ring_at.next();
     }
-    if (held == kGaveUp) {
+    if (held >= kGaveUp) {
       __syncwarp();
-      drain_ring<S, Context>(wc, bar0, ring_at, C::across ? ring_at.armed(feed.hidden) : min(S, (last - u + kWarps - 1) / kWarps));
+      drain_ring<S, Context>(wc, bar0, ring_at, C::across ? ring_at.armed(feed.hidden) : held - kGaveUp);
       held = ring_at.stage;
     }
 
