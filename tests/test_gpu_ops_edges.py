@@ -207,3 +207,24 @@ def test_pages_behind_every_window_are_not_looked_at(cuda_lib, kv, new, Hq, Hk, 
                                   scale=0.3, window=window)
         assert fa.get_status() == fa.FA_OK
         check(o, lse, want, "bf16")
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("pair", [0x7C007C00, 0xFC007C00, 0x7BFF7BFF])
+def test_tokens_that_no_row_sees_may_hold_anything(cuda_lib, pair, wide):
+    """Infinite pairs, of both signs, and pairs whose values overflow, behind the last token,
+    behind the window and in the other pages."""
+    q, cache, table, lens, cu = build([70, 300, 1, 47], [1, 3, 1, 2], 6, 2, 128, "bf16", 16, 36)
+    want = ref.attention(to_np64(q), cache, table, lens, cu, 0.3, 33, 128)
+    pairs = cache.reshape(-1, 2, cache.shape[3] // 2)[..., 8 * 128:].copy().view(np.uint32)
+    pairs[pairs == 0x7E7E7E7E] = pair  # what build() leaves in tokens that are no request's
+    cache.reshape(-1, 2, cache.shape[3] // 2)[..., 8 * 128:] = pairs.view(np.uint8)
+    for r, (n, m) in enumerate(zip([70, 300, 1, 47], [1, 3, 1, 2])):
+        for tok in range(max(0, n - m - 33 + 1)):  # behind the window of every row
+            at = 8 * 128 + tok % 16 * 16
+            for half in (0, cache.shape[3] // 2):
+                cache[table[r, tok // 16], :, 0, half + at:half + at + 16] = np.full(4, pair, np.uint32).view(np.uint8)
+    o, lse = fa.kv4_attention(q.cuda(), dev(cache), dev(widened(table) if wide else table), dev(lens), cu_q=dev(cu), max_q_len=3,
+                              scale=0.3, window=33)
+    check(o, lse, want, "bf16")
+    assert fa.get_status() == fa.FA_OK
