@@ -64,9 +64,9 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // Writing prompts of 16-bit types is bound by its instructions (326 a warp for 512 values,
 // 0.72 issued a cycle) before HBM; hence packed fp32 arithmetic, three-input minima, one pair
 // per lane (the key's or the value's), and no division or clamping per value where neither
-// can matter.  23,400 tokens of 12 heads, d = 64: bf16 27.2 us (94 MB, 3.5 TB/s; 25.3 with
+// can matter.  23,400 tokens of 12 heads, d = 64: bf16 27.3 us (94 MB, 3.4 TB/s; 25.3 with
 // sixteen values of each tensor to a lane, where single tokens of 256 requests cost 3.3 us
-// instead of 2.8), fp32 30.0 us (166 MB, 5.5 TB/s).
+// instead of 2.8), fp32 27.8 us (166 MB, 6.0 TB/s).
 
 // Least and largest of a lane's eight values and those of its group of four lanes.
 __device__ __forceinline__ void range8(const float (&v)[8], float& lo, float& hi) {
@@ -220,8 +220,8 @@ __device__ __forceinline__ void store_values(void* x, long long to, bool live, u
 }
 
 // Two rows per lane, so that two chains of loads (slot, then codes) are in flight: what
-// there is of latency bounds it.  23,400 tokens of 12 heads, d = 64: bf16 20.6 us (94 MB, 4.6
-// TB/s), fp32 33.0 us (166 MB, 5.0 TB/s; 42.6 with each lane's 32 bytes in two stores).
+// there is of latency bounds it.  23,400 tokens of 12 heads, d = 64: bf16 18.7 us (94 MB, 5.0
+// TB/s), fp32 30.8 us (166 MB, 5.4 TB/s; 42.6 with each lane's 32 bytes in two stores).
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4RowArgs a) {
   using Blk = KvBlock<D>;

@@ -41,7 +41,7 @@
 // Measured (shares): 64 requests of up to 16384 tokens, 32 query and 8 key heads, d = 128:
 // 145 us for 748 MB, 5.2 TB/s; the unit loop alone goes at 5.9 TB/s, with the integer pipe at
 // 54% (codes to fp16) and four warps a scheduler, and about 13 us are start-up, uneven ends
-// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.1 us.
+// and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.5 us.
 #pragma once
 #include <type_traits>
 
@@ -819,7 +819,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
             }
           }
       }
-      // weights, and their transpose as the B operand
+      // weights, and their transpose as the B operand: in fp16 (2^-11 of each, 2^-25 where
+      // subnormal), the type of the values they are multiplied with; l adds them in fp32
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p0[NT], p1[NT];

@@ -356,7 +356,8 @@ struct Smem {
 
 // The forward pass.  Measured: 23,400 tokens of 12 + 12 heads, d = 64, bf16 26.5 us (144 MB,
 // 5.4 TB/s; three CTAs an SM 27.3 us), of which about 3 are the launch, the angles and the
-// first rows; 19,735 tokens of 64 + 16 heads, d = 64, fp32 142 us (808 MB, 5.7 TB/s).
+// first rows; 19,735 tokens of 64 + 16 heads, d = 64, fp32 142 us (808 MB, 5.7
+// TB/s; 137 with 34 of the channels rotated, which go through shared memory).
 template <int D, int DT, bool ANY>
 __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, false>::ctas) qk_norm_rope_kernel(const QkArgs a, const bool w_f32) {
   constexpr int LPR = D / 16, ROWS = kThreads / LPR, E = DT == FA_F32 ? 4 : 2;
@@ -568,8 +569,9 @@ __global__ void __launch_bounds__(kThreads, Smem<D, DT, ANY, true>::ctas) qk_nor
   }
 }
 
-// dw: the partial sums of all CTAs, in a fixed order.  One CTA per 32 channels; it is
-// launched with the kernel before and waits for its end on the GPU (5.8 us by itself).
+// dw: the partial sums of all CTAs, in a fixed order.  One CTA per 32 channels.  It is a
+// dependent launch of the kernel before, but that one does not let it start early
+// (griddepcontrol.launch_dependents): it starts at its end (5.8 us by itself).
 __global__ void __launch_bounds__(1024) qk_dw_kernel(const QkArgs a, const int ctas, const int D) {
   __shared__ float red[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -609,7 +611,7 @@ cudaError_t launch_d(const QkArgs& a, bool w_f32, bool bwd, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (!bwd) return cudaSuccess;
-  // launched with the first kernel, whose end it waits for on the GPU
+  // a dependent launch: it starts at the first kernel's end, and waits for it besides
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * D / 32);
   cfg.blockDim = dim3(1024);

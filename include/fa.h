@@ -259,12 +259,15 @@ fa_status fa_bwd_noalloc(const fa_params* p, const void* Q, const void* K, const
                          void* dV, void* stream);
 
 /* Synchronises `stream`, returns the device-side status recorded since the
- * previous call (FA_OK or FA_ERR_TIMEOUT) and clears it; FA_ERR_CUDA if the
- * synchronisation itself fails.  The pages have no counterpart: it reports the
- * library's own failure detection (every on-chip barrier wait of every kernel is
- * bounded in time, so a kernel that cannot proceed gives up and records the
- * error instead of hanging), which guards the custom low-level CUDA that
- * "Limitações e questões em aberto" (reading guide) names as the method's cost. */
+ * previous call (FA_OK, FA_ERR_TIMEOUT, FA_ERR_INDEX, or FA_ERR_BOUNDS in the
+ * debug build; the first one counts) and clears it, so that calls and graphs that
+ * run afterwards are not affected; FA_ERR_CUDA if the synchronisation itself
+ * fails.  What a launch that recorded FA_ERR_TIMEOUT wrote is void.  The pages
+ * have no counterpart: it reports the library's own failure detection (every
+ * on-chip barrier wait of every kernel is bounded in time, so a kernel that cannot
+ * proceed gives up and records the error instead of hanging), which guards the
+ * custom low-level CUDA that "Limitações e questões em aberto" (reading guide)
+ * names as the method's cost. */
 fa_status fa_get_status(void* stream);
 
 /* Upper bound, in nanoseconds, on any single barrier wait inside the kernels
@@ -445,6 +448,8 @@ fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
  * that sees no token gets O = 0 and LSE = -inf; rows of q outside every request
  * are not written.  A NaN in a cached key (a pair of NaN) makes O and LSE of the rows that
  * see its token NaN; one in a cached value O's 32 channels of that pair, and nothing else.
+ * Tokens that no row sees may hold anything; pairs of seen ones are as fa_kv4_append writes
+ * them (finite values, or NaN).
  *   T           rows of q and o ([T][Hq][d], element strides {token, head}, FA_F16 or
  *               FA_BF16); lse: fp32 [T][Hq] or NULL.
  *   max_q_len   the largest number of rows of a request: a hint for the tile height
