@@ -54,10 +54,19 @@ class FaPlanParams(_Params):
                 ("table_width", ctypes.c_int), ("table_stride", ctypes.c_longlong)]
 
 
+class FaPackedParams(_Params):
+    """Mirror of ``fa_packed_params``."""
+    _fields_ = [("R", ctypes.c_int), ("Tq", ctypes.c_int), ("Tk", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("causal", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_stride", I64x2), ("k_stride", I64x2), ("v_stride", I64x2), ("o_stride", I64x2), ("do_stride", I64x2),
+                ("dq_stride", I64x2), ("dk_stride", I64x2), ("dv_stride", I64x2)]
+
+
 def signatures() -> dict:
     """(result, arguments) of the C functions of the operators."""
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-    QP, CP, RP, AP, PP = (ctypes.POINTER(t) for t in (FaQkParams, FaKv4Cache, FaKv4Rows, FaKv4AttnParams, FaPlanParams))
+    QP, CP, RP, AP, PP, SP = (ctypes.POINTER(t) for t in (FaQkParams, FaKv4Cache, FaKv4Rows, FaKv4AttnParams, FaPlanParams,
+                                                          FaPackedParams))
     return {
         "fa_qk_norm_rope": (I, [QP] + [P] * 9),
         "fa_qk_norm_rope_bwd_workspace_size": (S, [QP]),
@@ -68,4 +77,8 @@ def signatures() -> dict:
         "fa_kv4_attention_workspace_size": (S, [CP, AP]),
         "fa_kv4_attention": (I, [CP, AP] + [P] * 8 + [S, P]),
         "fa_paged_plan": (I, [PP] + [P] * 11),
+        "fa_fwd_packed_workspace_size": (S, [SP]),
+        "fa_fwd_packed": (I, [SP] + [P] * 8 + [S, P]),
+        "fa_bwd_packed_workspace_size": (S, [SP]),
+        "fa_bwd_packed": (I, [SP] + [P] * 12 + [S, P]),
     }

@@ -261,6 +261,28 @@ fa_status encode_u8(CUtensorMap* m, const void* ptr, uint64_t x, uint64_t y, uin
   return FA_OK;
 }
 
+}  // namespace
+
+fa_status fa::api_encode_3d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t (&dims)[3],
+                            const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) {
+    set_err("cuTensorMapEncodeTiled is not available from the driver");
+    return FA_ERR_CUDA;
+  }
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
+  const cuuint32_t b[3] = {box[0], box[1], box[2]}, estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, type, 3, const_cast<void*>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_err("cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+namespace {
+
 MaskArgs mask_args(const fa_params* p) {
   MaskArgs m;
   m.causal = p->causal ? 1 : 0;

@@ -140,6 +140,10 @@ void set_error_text(const char* text);
 // CUDA call as FA_ERR_CUDA with its text.
 fa_status api_device(Report* rep, int* sms);
 fa_status api_cuda_fail(cudaError_t e, const char* what);
+// A tensor map of three dimensions (the first contiguous; byte strides of the others); reads past
+// the extents give zero.
+fa_status api_encode_3d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t (&dims)[3],
+                        const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 
 #define FA_TRY(x)                    \
   do {                               \

@@ -146,9 +146,15 @@ int call(uintptr_t f, const uintptr_t* a, size_t n) {
     case 10:
       return reinterpret_cast<int (*)(P, P, P, P, P, P, P, P, P, P)>(f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7],
                                                                        a[8], a[9]);
+    case 11:
+      return reinterpret_cast<int (*)(P, P, P, P, P, P, P, P, P, P, P)>(f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7],
+                                                                          a[8], a[9], a[10]);
     case 12:
       return reinterpret_cast<int (*)(P, P, P, P, P, P, P, P, P, P, P, P)>(f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6],
                                                                              a[7], a[8], a[9], a[10], a[11]);
+    case 15:
+      return reinterpret_cast<int (*)(P, P, P, P, P, P, P, P, P, P, P, P, P, P, P)>(f)(
+          a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13], a[14]);
     case 16:
       return reinterpret_cast<int (*)(P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P)>(f)(
           a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13], a[14], a[15]);
@@ -294,7 +300,7 @@ PyObject* register_plan(PyObject*, PyObject* args) {
       p->shared += (o.bytes + kAlign - 1) / kAlign * kAlign;
     }
     const size_t n = p->args.size();
-    if (!(n == 7 || n == 10 || n == 12 || n == 16) || p->outputs.size() > kMaxOutputs) {
+    if (!(n == 7 || (n >= 10 && n <= 12) || n == 15 || n == 16) || p->outputs.size() > kMaxOutputs) {
       PyErr_SetString(PyExc_ValueError, "no such count of arguments or outputs");
       return nullptr;
     }

@@ -5,68 +5,15 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 
+#include "api_checks.h"
 #include "kv4.cuh"
 #include "ops.h"
-
-#include <nvtx3/nvToolsExt.h>
 
 using namespace fa;
 
 namespace {
-
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-fa_status fail(fa_status s, const char* fmt, ...) {
-  char text[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(text, sizeof(text), fmt, ap);
-  va_end(ap);
-  set_error_text(text);
-  return s;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-long long elem_bytes(int dtype) { return dtype == FA_F32 ? 4 : 2; }
-
-fa_status need(const void* p, size_t align, const char* name) {
-  if (!p) return fail(FA_ERR_INVALID, "%s is NULL", name);
-  if (!aligned(p, align)) return fail(FA_ERR_INVALID, "%s is not %zu-byte aligned", name, align);
-  return FA_OK;
-}
-
-// Strides (elements) of a tensor [size[0]][size[1]]...[inner]: whole 16-byte vectors,
-// not negative; for a tensor that is written, no two elements in one place.
-fa_status check_strides(const long long* stride, const long long* size, int n, long long inner, int dtype, bool written,
-                        const char* name) {
-  const long long vec = 16 / elem_bytes(dtype);
-  int order[3] = {0, 1, 2};
-  for (int i = 0; i < n; ++i)
-    if (stride[i] < 0 || stride[i] % vec != 0)
-      return fail(FA_ERR_INVALID, "%s: stride %lld is negative or no multiple of 16 bytes", name, stride[i]);
-  if (!written) return FA_OK;
-  for (int i = 0; i < n; ++i)
-    if (size[i] == 0) return FA_OK;  // no element
-  std::sort(order, order + n, [&](int x, int y) { return stride[x] < stride[y]; });
-  long long extent = inner;
-  for (int i = 0; i < n; ++i) {
-    const int k = order[i];
-    if (size[k] <= 1) continue;
-    if (stride[k] < extent) return fail(FA_ERR_INVALID, "%s overlaps itself (stride %lld)", name, stride[k]);
-    extent = stride[k] * (size[k] - 1) + extent;
-  }
-  return FA_OK;
-}
 
 // ------------------------------------------------------- norm and rotation
 

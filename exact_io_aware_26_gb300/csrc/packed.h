@@ -1,0 +1,60 @@
+// packed.h -- declarations shared by the entry points of packed attention (packed_api.cu) and
+// its kernels.  Not part of the public interface.
+#pragma once
+#include "ops.h"
+#include "packed_sched.cuh"
+
+namespace fa {
+
+// The list of a call's work, made on the GPU (packed_plan.cu), in the workspace.
+struct PackedList {
+  int* head;           // [0] items, [1] cut units
+  PackedItem* items;
+  PackedItem* cuts;
+  int* starts;         // scratch: first query, first key and first unit of each sequence and behind the last
+};
+
+struct PackedPlanArgs {
+  int R, Tq, Tk, Hk;
+  int tpt, causal, bwd;
+  int target;          // CTAs to share the steps among
+  long long least;     // steps that a slice has at least
+  const int* cu_q;
+  const int* cu_k;
+  PackedList list;
+  DevStatus* st;
+};
+
+struct PackedArgs {
+  int R, Tq, Tk, Hq, Hk, G;
+  FastDiv divG, divHk;
+  int tpt, causal;
+  int head_major;      // CTAs in the order of key heads first
+  float scale, scale_log2;
+  PackedList list;
+  const void* v;       // for values that are not finite
+  long long vs[2];     // element strides {token, head}
+  void* o;             // forward: result; backward: its values
+  const void* dout;
+  float* lse;
+  void *dq, *dk, *dv;
+  long long os[2], dos[2], dqs[2], dks[2], dvs[2];
+  float* slots;        // partial results of cut units
+  float *stat_lse, *stat_d;  // backward: [Hk][Tq * G] LSE log2 e (+inf: no key seen) and rowsum(dO O)
+  float* dq_acc;       // backward: [Hk][Tq * G][d]
+  int first_q, most_cuts;
+  Report rep;
+};
+
+// fp32 words of a slot: forward (m, l) and O of 128 rows; backward dV and dK of 128 keys.
+inline size_t packed_slot_words(int d, bool bwd) { return bwd ? (size_t)2 * 128 * d : (size_t)128 * (d + 2); }
+
+cudaError_t launch_packed_plan(const PackedPlanArgs& a, cudaStream_t s);
+// `items`: at most that many; `cuts`: at most that many cut units, 0 where none can be.
+cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, int cuts,
+                              cudaStream_t s);
+cudaError_t launch_packed_bwd_preprocess(const PackedArgs& a, int d, bool f16, cudaStream_t s);
+cudaError_t launch_packed_bwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s);
+cudaError_t launch_packed_bwd_finalize(const PackedArgs& a, int d, bool f16, int cuts, cudaStream_t s);
+
+}  // namespace fa

@@ -1,0 +1,758 @@
+// packed_bwd.cu -- attention backward of packed sequences with grouped heads: the main kernel.
+//
+// The tiled recomputation of bwd_tc.cu ("Passe arrière : recalculer au lieu de stocker",
+// marketmaker.cc): one CTA holds a 128-key tile (K_j, V_j) of a sequence and key head, accumulates
+// dK_j and dV_j in TMEM and walks the query tiles that see it,
+//   S^T = K_j Q_i^T, P^T = exp(scale S^T - LSE_i), dP^T = V_j dO_i^T, dV += P^T dO_i,
+//   dS^T = P^T (dP^T - D_i), dK += dS^T Q_i, dQ_i = dS K_j (added to an fp32 accumulator by TMA).
+// A query tile is tpt tokens times the G query heads of the key head (row = token * G + head), so
+// that the sum over a group's heads is part of the products' sums: dK and dV of shared heads
+// need no pass of their own, and their order is fixed.  The CTAs take the list that
+// packed_plan.cu makes: key tiles by the query tiles they visit, the longest first, cut where
+// one is longer than an even share; parts of a cut tile are fp32 sums that the last kernel adds.
+//
+// What lies behind a sequence's end in its last tiles is another sequence's or nobody's: rows of
+// Q, dO and K there are zeroed in shared memory before the products read them, dS of hidden pairs
+// is 0, and rows of dQ there are added as 0.
+//
+// Bound: the tensor core (five products, 10 d FLOPs a seen pair and query head) beside the
+// exponentials and the elementwise steps; one CTA an SM.
+//
+// Warp roles as in bwd_tc.cu: 4 NG compute warps in NG groups that split the 128 query
+// columns of a tile (TMEM lane = key row); a producer warp; a warp that owns TMEM and issues the
+// products; at d = 64 four warps that read dQ_i out of TMEM.
+#include "packed.h"
+#include "ptx.cuh"
+#include "tiles.cuh"
+
+namespace fa {
+namespace {
+
+template <int D>
+struct Layout {
+  static constexpr int NG = D == 64 ? 4 : 2;  // compute warpgroups (d = 128: a warp's dQ box is its own dS^T rows)
+  static constexpr int CW = kTile / NG;       // query columns of a warpgroup
+  static constexpr int KPG = CW / 16;
+  static constexpr int NCW = 4 * NG;
+  static constexpr bool QW = D == 64;         // warps of their own for dQ
+  static constexpr int NQW = QW ? 4 : 0;
+  static constexpr int NT = 32 * (NCW + 2 + NQW);
+  static constexpr int DQG = D / NG;
+  static constexpr int DQC = 32;              // columns of a dQ box of 32 rows
+  static constexpr uint32_t BOXB = 32u * DQC * 4u;
+  static constexpr int DQ_READERS = QW ? NQW : NCW;
+  static constexpr uint32_t TILE = kTile * D * 2;
+  static constexpr int NS = D == 64 ? 3 : 2;  // Q/dO ring depth
+  static constexpr uint32_t K = 0;
+  static constexpr uint32_t V = TILE;
+  static constexpr uint32_t QS = 2 * TILE;    // stage s: Q at QS + 2 s TILE, dO behind it
+  static constexpr int NDS = D == 64 ? 2 : 1;
+  static constexpr uint32_t DSB = kTile * kTile * 2;
+  static constexpr uint32_t DST = QS + NS * 2 * TILE;
+  static constexpr uint32_t STAT = DST + NDS * DSB;  // per stage -LSE log2 e [128], -D [128]
+  static constexpr bool STG_SEP = D == 64;           // dQ boxes: of their own, or over dS^T
+  static constexpr uint32_t STG_BYTES = (QW ? NQW : NCW) * BOXB;
+  static constexpr uint32_t STG = STG_SEP ? STAT + NS * 256 * 4 : DST;
+  static_assert(STG_SEP || STG_BYTES == DSB, "staging size");
+  static constexpr uint32_t BAR = STAT + NS * 256 * 4 + (STG_SEP ? STG_BYTES : 0);
+  // 0 kv, 1 s_full, 2 dp_full, 3 dp_free, 4 p_full, 5 ds_full, 6 dq_full, 7 dq_free, 8 done,
+  // 9 pt_free, 10 tail (copies of tiles whose rows are to be zeroed), 11.. q_full, q_empty, ds_free
+  static constexpr uint32_t NBAR = 11 + 2 * NS + NDS;
+  static constexpr uint32_t TSLOT = BAR + NBAR * 8;
+  static constexpr uint32_t ABORT = TSLOT + 4;
+  static constexpr uint32_t BYTES = ABORT + 4;
+  static_assert(BYTES <= 232448, "shared memory per CTA");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
+  static constexpr bool ALIAS = D == 128;  // dQ over dP^T, P^T over S^T
+  static constexpr uint32_t T_DQ = ALIAS ? T_DP : 384;
+  static constexpr uint32_t T_PT = ALIAS ? T_S : 448;
+  __device__ static constexpr uint32_t pt_col(int kk) {
+    return ALIAS ? (uint32_t)CW * (uint32_t)(kk / KPG) + 8u * (uint32_t)(kk % KPG) : T_PT + 8u * (uint32_t)kk;
+  }
+  __device__ static constexpr uint32_t pt_write_col(int g) {
+    return ALIAS ? (uint32_t)CW * (uint32_t)g : T_PT + (uint32_t)(CW / 2) * (uint32_t)g;
+  }
+};
+
+// Rows [from, 128) of a tile in shared memory become 0 (a warp's lanes, or `n` threads).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int t, int n) {
+  const int chunks = (kTile - from) * 8;  // 16-byte chunks of the rows of an atom of 64 channels
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    for (int i = t; i < chunks; i += n) st_shared_v4(tile + (uint32_t)(c * kTile * 128 + from * 128 + 16 * i), 0u, 0u, 0u, 0u);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(Layout<D>::NT, 1)
+    packed_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                      const __grid_constant__ CUtensorMap tmdQ, const PackedArgs a) {
+  using L = Layout<D>;
+  constexpr int NS = L::NS;
+  constexpr int kProd = L::NCW, kMma = L::NCW + 1;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list, the rows' statistics, the zeroed accumulator
+  const int index = a.divHk.div((int)blockIdx.x), hk = (int)blockIdx.x - index * a.Hk;
+  if (index >= a.list.head[0]) return;
+  const PackedItem x = a.list.items[index];
+  const int kt = x.tile, q_end = x.s1, tpt = a.tpt, G = a.G;
+  const int keys = min(kTile, x.seq.m - kt * kTile);  // of the tile that are the sequence's
+  const int ahead = x.seq.m - x.seq.n;
+  auto rows_of = [&](int qt) { return min(tpt, x.seq.n - qt * tpt) * G; };  // rows of a query tile
+  const int full = tpt * G;
+  // some row of query tile qt does not see some key of this tile
+  auto diagonal = [&](int qt) { return a.causal && kt * kTile + keys - 1 > qt * tpt + ahead; };
+
+  auto bar = [&](int i) { return sb + L::BAR + 8u * (uint32_t)i; };
+  const uint32_t bar_kv = bar(0), bar_s_full = bar(1), bar_dp_full = bar(2), bar_dp_free = bar(3), bar_p_full = bar(4),
+                 bar_ds_full = bar(5), bar_dq_full = bar(6), bar_dq_free = bar(7), bar_done = bar(8),
+                 bar_pt_free = bar(9), bar_tail = bar(10);
+  auto bar_qf = [&](int s) { return bar(11 + s); };
+  auto bar_qe = [&](int s) { return bar(11 + NS + s); };
+  auto bar_ds_free = [&](int b) { return bar(11 + 2 * NS + b); };
+
+  volatile int* abort_cta = reinterpret_cast<volatile int*>(smem + L::ABORT);
+  const WaitCtx w{abort_cta, a.rep.st, a.rep.epoch, a.rep.wait_ns};
+  if ((sb & 1023u) != 0) {
+    if (threadIdx.x == 0) raise_error(w, FA_ERR_CUDA);
+    return;
+  }
+  // debug build: the tile lies in its sequence, and that in the tensors
+  if (!dbg_check(w, keys > 0 && x.s0 >= 0 && x.s0 <= x.s1 && x.s1 <= packed_units(x.seq, tpt, false) && x.seq.q0 >= 0 &&
+                        x.seq.q0 + x.seq.n <= a.Tq && x.seq.k0 >= 0 && x.seq.k0 + x.seq.m <= a.Tk && hk < a.Hk))
+    return;
+  const uint32_t q_bytes = (uint32_t)full * D * 2u;
+  auto load_q = [&](int s, int qt, uint32_t at) {  // Q_i and dO_i into stage s
+    const uint32_t dst = sb + L::QS + (uint32_t)s * 2u * L::TILE;
+    const int token = x.seq.q0 + qt * tpt;
+    for (int c = 0; c < D / 64; ++c) {
+      tma_load_3d(dst + c * (kTile * 128), &tmQ, at, c * 64, hk * G, token);
+      tma_load_3d(dst + L::TILE + c * (kTile * 128), &tmdO, at, c * 64, hk * G, token);
+    }
+  };
+  // The producer lane sets up the barriers and issues the copies that need no wait: K_j, V_j and
+  // the first query tiles, up to one with rows to be zeroed.
+  const bool producer = warp == kProd && lane == 0;
+  int pre = 0;
+  if (producer) {
+    mbar_init(bar_kv, 2);
+    mbar_init(bar_s_full, 1);
+    mbar_init(bar_dp_full, 1);
+    mbar_init(bar_dp_free, L::NCW);
+    mbar_init(bar_p_full, L::NCW);
+    mbar_init(bar_ds_full, L::NCW);
+    for (int b = 0; b < L::NDS; ++b) mbar_init(bar_ds_free(b), 1);
+    mbar_init(bar_dq_full, 1);
+    mbar_init(bar_dq_free, L::DQ_READERS);
+    mbar_init(bar_done, 1);
+    mbar_init(bar_pt_free, 1);
+    mbar_init(bar_tail, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar_qf(s), 1 + 32);  // the copies' arrival and every producer lane
+      mbar_init(bar_qe(s), 1);
+    }
+    *abort_cta = 0;
+    fence_barrier_init();
+    const uint32_t at_k = keys < kTile ? bar_tail : bar_kv;
+    mbar_arrive_expect_tx(bar_kv, (keys < kTile ? 1u : 2u) * L::TILE);
+    if (keys < kTile) mbar_arrive_expect_tx(bar_tail, L::TILE);
+    for (int c = 0; c < D / 64; ++c) {
+      tma_load_3d(sb + L::K + c * (kTile * 128), &tmK, at_k, c * 64, hk, x.seq.k0 + kt * kTile);
+      tma_load_3d(sb + L::V + c * (kTile * 128), &tmV, bar_kv, c * 64, hk, x.seq.k0 + kt * kTile);
+    }
+    for (int qt = x.s0; qt < q_end && pre < NS && rows_of(qt) == full; ++qt, ++pre) {
+      mbar_arrive_expect_tx(bar_qf(pre), 2 * q_bytes);
+      load_q(pre, qt, bar_qf(pre));
+    }
+  }
+  if (full < kTile) {  // rows that no copy writes
+    for (int s = 0; s < 2 * NS; ++s) zero_rows<D>(sb + L::QS + (uint32_t)s * L::TILE, full, (int)threadIdx.x, L::NT);
+    fence_async_smem();
+  }
+  if (warp == kMma) {
+    tmem_alloc(sb + L::TSLOT, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::TSLOT);
+
+  if (warp == kProd) {
+    // ------------------------------------------------------------ producer
+    pre = __shfl_sync(0xffffffffu, pre, 0);
+    int it = 0;
+    uint32_t tails = 0;  // copies issued on bar_tail
+    bool go = true;
+    if (keys < kTile) {  // the keys behind the sequence's end
+      tails = 1;
+      go = warp_wait(w, bar_tail, 0);
+      if (go) {
+        zero_rows<D>(sb + L::K, keys, lane, 32);
+        fence_async_smem();
+        __syncwarp();
+      }
+    }
+    if (go && lane == 0) mbar_arrive(bar_kv);
+    const float* lse = a.stat_lse + (long long)hk * a.Tq * G;
+    const float* dsum = a.stat_d + (long long)hk * a.Tq * G;
+    for (int qt = x.s0; go && qt < q_end; ++qt) {
+      const int s = it % NS, rows = rows_of(qt);
+      // statistics, negated as the compute warps use them, loaded before the wait for the stage
+      const long long row0 = (long long)(x.seq.q0 + qt * tpt) * G;
+      float l4[4], d4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 4 * lane + k;
+        l4[k] = r < rows ? -__ldg(lse + row0 + r) : -INFINITY;
+        d4[k] = r < rows ? -__ldg(dsum + row0 + r) : 0.f;
+      }
+      if (it >= NS && !warp_wait(w, bar_qe(s), ((it / NS) - 1) & 1)) break;
+      const bool tail = rows < full;  // the sequence's last query tile
+      if (lane == 0 && it >= pre) {
+        mbar_arrive_expect_tx(tail ? bar_tail : bar_qf(s), 2 * q_bytes);
+        load_q(s, qt, tail ? bar_tail : bar_qf(s));
+      }
+      float* st = reinterpret_cast<float*>(smem + L::STAT) + s * 256;
+      reinterpret_cast<float4*>(st)[lane] = make_float4(l4[0], l4[1], l4[2], l4[3]);
+      reinterpret_cast<float4*>(st + 128)[lane] = make_float4(d4[0], d4[1], d4[2], d4[3]);
+      if (tail) {
+        const uint32_t parity = tails++ & 1u;
+        if (!warp_wait(w, bar_tail, parity)) break;
+        const uint32_t dst = sb + L::QS + (uint32_t)s * 2u * L::TILE;
+        zero_rows<D>(dst, rows, lane, 32);
+        zero_rows<D>(dst + L::TILE, rows, lane, 32);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_qf(s));
+      }
+      mbar_arrive(bar_qf(s));
+      ++it;
+    }
+    if (lane == 0) {  // every copy has landed before the CTA ends
+      if (tails > 0) mbar_drain(w, bar_tail, (tails - 1) & 1u);
+      mbar_drain(w, bar_kv, 0);
+      const int issued = it > pre ? it : pre;
+      for (int s = 0; s < NS; ++s) {
+        const int n = (issued - s + NS - 1) / NS;
+        if (n > 0) mbar_drain(w, bar_qf(s), (n - 1) & 1);
+      }
+    }
+  } else if (warp == kMma) {
+    // ------------------------------------------------------------ MMA issuer
+    // Per query tile i, in the order of bwd_tc.cu:
+    //   d = 64:  S^T_{i+1}, dV_i, dP^T_{i+1}, then dQ_i, dK_i
+    //   d = 128: dV_i, S^T_{i+1} (over P^T), then dQ_i, dK_i, dP^T_{i+1} (over dQ_i)
+    constexpr uint32_t idS = idesc_f16(F16, kTile, kTile, false, false);
+    constexpr uint32_t idKV = idesc_f16(F16, kTile, D, false, true);
+    constexpr uint32_t idQ = idesc_f16(F16, kTile, D, true, true);
+    constexpr int KS = D / 16;
+    const uint32_t tS = tmem + L::T_S, tDP = tmem + L::T_DP, tDV = tmem + L::T_DV, tDK = tmem + L::T_DK,
+                   tDQ = tmem + L::T_DQ;
+    const uint64_t dK_k = desc_kmajor_base(sb + L::K), dV_k = desc_kmajor_base(sb + L::V);
+    const uint64_t dK_mn = desc_mnmajor_base(sb + L::K, kTile);
+    const uint64_t dS_k = desc_kmajor_base(sb + L::DST);
+    const uint64_t dS_mn = desc_mnmajor_base(sb + L::DST, kTile);
+    auto ds_off = [&](int it) { return (uint32_t)(it % L::NDS) * L::DSB; };
+    const uint64_t dQ_k0 = desc_kmajor_base(sb + L::QS), dQ_mn0 = desc_mnmajor_base(sb + L::QS, kTile);
+    auto stage_off = [&](int it) { return (uint32_t)(it % NS) * 2u * L::TILE; };
+    auto mma_s = [&](int it, int kk) {
+      tc_mma_ss_elect(tS, dK_k + kmajor_step(kk, kTile), desc_add(dQ_k0, stage_off(it)) + kmajor_step(kk, kTile), idS,
+                      kk > 0 ? 1u : 0u);
+    };
+    auto mma_dp = [&](int it, int kk) {
+      tc_mma_ss_elect(tDP, dV_k + kmajor_step(kk, kTile),
+                      desc_add(dQ_k0, stage_off(it) + L::TILE) + kmajor_step(kk, kTile), idS, kk > 0 ? 1u : 0u);
+    };
+    auto mma_dv = [&](int it, int kk) {
+      tc_mma_ts_elect(tDV, tmem + L::pt_col(kk), desc_add(dQ_mn0, stage_off(it) + L::TILE) + mnmajor_step(kk), idKV,
+                      (it > 0 || kk > 0) ? 1u : 0u);
+    };
+    auto mma_dk = [&](int it, int kk) {
+      tc_mma_ss_elect(tDK, desc_add(dS_k, ds_off(it)) + kmajor_step(kk, kTile),
+                      desc_add(dQ_mn0, stage_off(it)) + mnmajor_step(kk), idKV, (it > 0 || kk > 0) ? 1u : 0u);
+    };
+    auto mma_dq = [&](int it, int kk) {
+      tc_mma_ss_elect(tDQ, desc_add(dS_mn, ds_off(it)) + mnmajor_step(kk), dK_mn + mnmajor_step(kk), idQ,
+                      kk > 0 ? 1u : 0u);
+    };
+    bool ok = warp_wait(w, bar_kv, 0);
+    int qt = x.s0;
+    if (ok && qt < q_end && (ok = warp_wait(w, bar_qf(0), 0))) {
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        mma_s(0, kk);
+        mma_dp(0, kk);
+      }
+      tc_commit_elect(bar_s_full);
+      tc_commit_elect(bar_dp_full);
+    }
+    for (int it = 0; ok && qt < q_end; ++it, ++qt) {
+      const bool next = qt + 1 < q_end;
+      if (!(ok = warp_wait(w, bar_p_full, it & 1))) break;
+      if (next && !(ok = warp_wait(w, bar_qf((it + 1) % NS), ((it + 1) / NS) & 1))) break;
+      tc_fence_after();
+      if (!L::ALIAS) {
+        if (next) {
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) mma_s(it + 1, kk);
+          tc_commit_elect(bar_s_full);
+        }
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) mma_dv(it, kk);
+        tc_commit_elect(bar_pt_free);
+        if (next) {
+          if (!(ok = warp_wait(w, bar_dp_free, it & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) mma_dp(it + 1, kk);
+          tc_commit_elect(bar_dp_full);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) mma_dv(it, kk);
+        if (next) {
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) mma_s(it + 1, kk);
+          tc_commit_elect(bar_s_full);
+        }
+      }
+      if (!(ok = warp_wait(w, bar_ds_full, it & 1))) break;
+      if (!L::ALIAS && it > 0 && !(ok = warp_wait(w, bar_dq_free, (it - 1) & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk) mma_dq(it, kk);
+      if (L::STG_SEP) tc_commit_elect(bar_dq_full);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk) mma_dk(it, kk);
+      if (!L::STG_SEP) tc_commit_elect(bar_dq_full);  // the boxes lie over the dS^T that dK_i reads
+      tc_commit_elect(bar_ds_free(it % L::NDS));
+      tc_commit_elect(bar_qe(it % NS));
+      if (L::ALIAS && next) {  // dP^T_{i+1} goes over dQ_i
+        if (!(ok = warp_wait(w, bar_dp_free, it & 1))) break;
+        if (!(ok = warp_wait(w, bar_dq_free, it & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) mma_dp(it + 1, kk);
+        tc_commit_elect(bar_dp_full);
+      }
+    }
+    tc_commit_elect(bar_done);
+    if (lane == 0) mbar_drain(w, bar_done, 0);
+    __syncwarp();
+  } else if (warp > kMma) {
+    if constexpr (L::QW) {
+      // ------------------------------------------------------------ dQ warps (d = 64)
+      const int qd = warp & 3;
+      const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+      const uint32_t stg = sb + L::STG + (uint32_t)qd * L::BOXB;
+      bool pend = false;  // a reduce may still be reading the box
+      int it = 0;
+      for (int qt = x.s0; qt < q_end; ++qt, ++it) {
+        if (!warp_wait(w, bar_dq_full, it & 1)) break;
+        tc_fence_after();
+        const int rows = rows_of(qt);
+        const bool dead = 32 * qd + lane >= rows;  // a row of 0: of no query, or another sequence's
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += L::DQC) {
+          uint32_t dq[L::DQC];
+          tmem_ld_n<L::DQC>(tmem + L::T_DQ + lane_off + (uint32_t)c0, dq);
+          if (c0 + L::DQC == D) {  // dQ_i is in registers: the next one may be computed
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_dq_free);
+          }
+          if (32 * qd >= rows) continue;
+          if (pend) {
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+          }
+          if (dead) {
+#pragma unroll
+            for (int k = 0; k < L::DQC; ++k) dq[k] = 0u;
+          }
+#pragma unroll
+          for (int v = 0; v < L::DQC / 4; ++v)
+            st_shared_v4(stg + (uint32_t)lane * 128u + (uint32_t)((v ^ (lane & 7)) * 16), dq[4 * v], dq[4 * v + 1],
+                         dq[4 * v + 2], dq[4 * v + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_reduce_add_3d(&tmdQ, stg, c0, (x.seq.q0 + qt * tpt) * G + qd * 32, hk);
+            bulk_commit_group();
+          }
+          pend = true;
+        }
+      }
+      if (lane == 0) bulk_wait_group0();
+    }
+  } else {
+    // ------------------------------------------------------------ compute warpgroups
+    constexpr int CW = L::CW;
+    const int g = warp >> 2;               // query columns [CW g, CW g + CW)
+    const int r = (warp & 3) * 32 + lane;  // key row of the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint64_t c2p = f2pack(a.scale_log2, a.scale_log2);
+    const bool tail = keys < kTile;
+    // the first of the warpgroup's columns whose query sees this key
+    auto first_col = [&](int qt) {
+      if (r >= keys) return kTile;
+      const int i = a.causal ? kt * kTile + r - ahead - qt * tpt : 0;  // first such token of the tile
+      return (i <= 0 ? 0 : i >= tpt ? kTile : i * G) - CW * g;
+    };
+    const uint32_t stg = sb + L::STG + (uint32_t)warp * L::BOXB;
+    bool pend = false;
+    auto stg_acquire = [&]() {
+      if (pend) {
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+        pend = false;
+      }
+    };
+    auto stat = [&](int it) { return reinterpret_cast<const float*>(smem + L::STAT) + (it % NS) * 256; };
+    float p[CW];
+    // S^T -> P^T: fp32 in p[] for dS, 16-bit into TMEM for dV
+    auto p_phase = [&](int it, int qt) -> bool {
+      if (!warp_wait(w, bar_qf(it % NS), (it / NS) & 1)) return false;
+      if (!warp_wait(w, bar_s_full, it & 1)) return false;
+      tc_fence_after();
+      {
+        uint32_t u[CW];
+        tmem_ld_n<CW>(tmem + L::T_S + lane_off + CW * g, u);
+#pragma unroll
+        for (int c = 0; c < CW; ++c) p[c] = __uint_as_float(u[c]);
+      }
+      const float4* nl4 = reinterpret_cast<const float4*>(stat(it) + CW * g);  // -LSE log2 e
+      uint32_t pk[CW / 2];
+#pragma unroll
+      for (int c = 0; c < CW; c += 4) {
+        const float4 nl = nl4[c / 4];
+        float x0, x1, x2, x3;
+        f2unpack(ffma2(f2pack(p[c], p[c + 1]), c2p, f2pack(nl.x, nl.y)), x0, x1);
+        f2unpack(ffma2(f2pack(p[c + 2], p[c + 3]), c2p, f2pack(nl.z, nl.w)), x2, x3);
+        p[c] = ex2(x0);
+        p[c + 1] = ex2(x1);
+        p[c + 2] = ex2(x2);
+        p[c + 3] = ex2(x3);
+      }
+      if (tail || diagonal(qt)) {
+        const int first = first_col(qt);
+#pragma unroll
+        for (int c = 0; c < CW; ++c)
+          if (c < first) p[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < CW; c += 2) pk[c / 2] = pack2<F16>(p[c], p[c + 1]);
+      if constexpr (!L::ALIAS) {
+        if (it > 0) {  // dV of the tile before has read its P^T
+          if (!warp_wait(w, bar_pt_free, (it - 1) & 1)) return false;
+          tc_fence_after();
+        }
+      }
+      tmem_st_n<CW / 2>(tmem + L::pt_write_col(g) + lane_off, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p_full);
+      return true;
+    };
+    bool ok = true;
+    int it = 0;
+    int qt = x.s0;
+    if (qt < q_end) ok = p_phase(0, qt);
+    for (; ok && qt < q_end; ++it, ++qt) {
+      // ---- dS_i = P_i (dP_i - D)
+      if (!(ok = warp_wait(w, bar_dp_full, it & 1))) break;
+      tc_fence_after();
+      uint32_t pk[CW / 2];
+      const float4* nd4 = reinterpret_cast<const float4*>(stat(it) + 128 + CW * g);  // -D
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        constexpr int HW = CW / 2;
+        uint32_t u[HW];
+        tmem_ld_n<HW>(tmem + L::T_DP + lane_off + CW * g + HW * hf, u);
+        if (hf == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_dp_free);
+        }
+#pragma unroll
+        for (int c = 0; c < HW; c += 4) {
+          const int cc = HW * hf + c;
+          const float4 nd = nd4[cc / 4];
+          float y0, y1, y2, y3;
+          f2unpack(fmul2(f2pack(p[cc], p[cc + 1]),
+                         fadd2(f2pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), f2pack(nd.x, nd.y))),
+                   y0, y1);
+          f2unpack(fmul2(f2pack(p[cc + 2], p[cc + 3]),
+                         fadd2(f2pack(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), f2pack(nd.z, nd.w))),
+                   y2, y3);
+          pk[cc / 2] = pack2<F16>(y0, y1);
+          pk[cc / 2 + 1] = pack2<F16>(y2, y3);
+        }
+      }
+      if (tail || diagonal(qt)) {  // 0, whatever dP is there
+        const int first = first_col(qt);
+#pragma unroll
+        for (int c = 0; c < CW; c += 2) {
+          if (c < first) pk[c / 2] &= 0xFFFF0000u;
+          if (c + 1 < first) pk[c / 2] &= 0x0000FFFFu;
+        }
+      }
+      if (it >= L::NDS && !(ok = warp_wait(w, bar_ds_free(it % L::NDS), ((it / L::NDS) - 1) & 1))) break;
+      if (!L::STG_SEP) stg_acquire();
+#pragma unroll
+      for (int ch = 0; ch < CW / 8; ++ch)
+        st_shared_v4(sb + L::DST + (uint32_t)(it % L::NDS) * L::DSB + sw128_chunk_offset(r, (CW / 8) * g + ch, kTile),
+                     pk[ch * 4 + 0], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ds_full);
+
+      // ---- P of the next query tile, while dK_i, dQ_i, dP^T_{i+1} run
+      if (qt + 1 < q_end && !(ok = p_phase(it + 1, qt + 1))) break;
+
+      // ---- dQ_i -> the fp32 accumulator (d = 128; at d = 64 the dQ warps' job)
+      if constexpr (!L::QW) {
+        if (!(ok = warp_wait(w, bar_dq_full, it & 1))) break;
+        tc_fence_after();
+        const int rows = rows_of(qt);
+        uint32_t dq[L::DQG];
+        tmem_ld_n<L::DQG>(tmem + L::T_DQ + lane_off + g * L::DQG, dq);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_dq_free);
+        if (32 * (warp & 3) < rows) {
+          if (r >= rows) {  // a row of 0: of no query, or another sequence's
+#pragma unroll
+            for (int k = 0; k < L::DQG; ++k) dq[k] = 0u;
+          }
+#pragma unroll
+          for (int c0 = 0; c0 < L::DQG; c0 += L::DQC) {
+            stg_acquire();
+#pragma unroll
+            for (int v = 0; v < L::DQC / 4; ++v)
+              st_shared_v4(stg + (uint32_t)lane * 128u + (uint32_t)((v ^ (lane & 7)) * 16), dq[c0 + 4 * v],
+                           dq[c0 + 4 * v + 1], dq[c0 + 4 * v + 2], dq[c0 + 4 * v + 3]);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_reduce_add_3d(&tmdQ, stg, g * L::DQG + c0, (x.seq.q0 + qt * tpt) * G + (warp & 3) * 32, hk);
+              bulk_commit_group();
+            }
+            pend = true;
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+    // ------------------------------------------------------------ dK, dV
+    bool have = false;
+    if (ok) {
+      ok = warp_wait(w, bar_done, 0);
+      tc_fence_after();
+      have = ok && it > 0;
+    }
+    if (ok) {
+      const int token = x.seq.k0 + kt * kTile + r;
+      const bool store = r < keys && dbg_check(w, token < a.Tk);
+      float* part = x.slot < 0 ? nullptr
+                               : a.slots + ((long long)x.slot * a.Hk + hk) * (2 * kTile * D) + (long long)r * D + g * L::DQG;
+      constexpr int EC = L::DQG < 32 ? L::DQG : 32;
+      for (int which = 0; which < 2; ++which) {
+        const uint32_t col = (which == 0 ? L::T_DV : L::T_DK) + g * L::DQG;
+        const float mul = which == 0 ? 1.f : a.scale;
+        const long long* st = which == 0 ? a.dvs : a.dks;
+        uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) + (long long)token * st[0] + hk * st[1] + g * L::DQG;
+#pragma unroll
+        for (int c0 = 0; c0 < L::DQG; c0 += EC) {
+          uint32_t u[EC];
+          if (have) {
+            tmem_ld_n<EC>(tmem + col + lane_off + c0, u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < EC; ++k) u[k] = 0u;
+          }
+          if (part) {
+#pragma unroll
+            for (int v = 0; v < EC / 4; ++v)
+              *reinterpret_cast<uint4*>(part + (long long)which * (kTile * D) + c0 + 4 * v) =
+                  make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
+          } else if (store) {
+#pragma unroll
+            for (int v = 0; v < EC / 8; ++v) {
+              uint4 q;
+              q.x = pack2<F16>(__uint_as_float(u[v * 8 + 0]) * mul, __uint_as_float(u[v * 8 + 1]) * mul);
+              q.y = pack2<F16>(__uint_as_float(u[v * 8 + 2]) * mul, __uint_as_float(u[v * 8 + 3]) * mul);
+              q.z = pack2<F16>(__uint_as_float(u[v * 8 + 4]) * mul, __uint_as_float(u[v * 8 + 5]) * mul);
+              q.w = pack2<F16>(__uint_as_float(u[v * 8 + 6]) * mul, __uint_as_float(u[v * 8 + 7]) * mul);
+              *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+// Before the main kernel: the rows' statistics in the order of the query tiles' rows, and the
+// accumulator of dQ zeroed.  Streams O, dO and the accumulator; runs beside the list's making.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) packed_rows_kernel(const PackedArgs a) {
+  constexpr int TPR = D / 8;
+  const long long total = (long long)a.Tq * a.Hq * TPR, n = (long long)gridDim.x * blockDim.x;
+  for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t - (threadIdx.x & 31) < total; t += n) {
+    const bool in = t < total;
+    const long long row = (in ? t : 0) / TPR;
+    const int c = (int)(t % TPR), token = (int)(row / a.Hq), head = (int)(row - (long long)token * a.Hq);
+    const int hk = a.divG.div(head);
+    const long long at = ((long long)hk * a.Tq + token) * a.G + (head - hk * a.G);  // [Hk][Tq][G]
+    float acc = 0.f;
+    if (in) {
+      const uint4 o = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + token * a.os[0] + head * a.os[1] + 8 * c);
+      const uint4 g = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + token * a.dos[0] + head * a.dos[1] + 8 * c);
+      const uint32_t ov[4] = {o.x, o.y, o.z, o.w}, gv[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = unpack2<F16>(ov[i]), v = unpack2<F16>(gv[i]);
+        acc = fmaf(u.x, v.x, acc);
+        acc = fmaf(u.y, v.y, acc);
+      }
+      float4* z = reinterpret_cast<float4*>(a.dq_acc + at * D + 8 * c);
+      z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (in && c == 0) {
+      const float lse = a.lse[row];
+      a.stat_d[at] = acc;
+      a.stat_lse[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // so that what waits for this grid finds the list too
+}
+
+// After it: dQ = scale * accumulator, for rows that are a sequence's; and dK, dV of the cut key
+// tiles from their parts, in order.
+constexpr int kSumParts = 8;
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, int dq_blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < dq_blocks) {
+    constexpr int TPR = D / 8;
+    const int first = a.list.head[2], end = a.list.head[3];
+    const long long total = (long long)(end - first) * a.Hq * TPR, n = (long long)dq_blocks * blockDim.x;
+    for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += n) {
+      const long long row = t / TPR;
+      const int c = (int)(t % TPR), rel = (int)(row / a.Hq), head = (int)(row - (long long)rel * a.Hq), token = first + rel;
+      const int hk = a.divG.div(head);
+      const long long at = ((long long)hk * a.Tq + token) * a.G + (head - hk * a.G);
+      const float4* src = reinterpret_cast<const float4*>(a.dq_acc + at * D + 8 * c);
+      const float4 x = src[0], y = src[1];
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dq) + token * a.dqs[0] + head * a.dqs[1] + 8 * c) =
+          make_uint4(pack2<F16>(x.x * a.scale, x.y * a.scale), pack2<F16>(x.z * a.scale, x.w * a.scale),
+                     pack2<F16>(y.x * a.scale, y.y * a.scale), pack2<F16>(y.z * a.scale, y.w * a.scale));
+    }
+    return;
+  }
+  const int k = (int)blockIdx.x - dq_blocks, unit = k / kSumParts, part = k % kSumParts;
+  const int cut = a.divHk.div(unit), hk = unit - cut * a.Hk;
+  if (cut >= a.list.head[1]) return;
+  const PackedItem x = a.list.cuts[cut];
+  constexpr int PER = 2 * kTile * D / 4, PART = PER / kSumParts;  // float4 of a slot, of a block
+  const float4* base = reinterpret_cast<const float4*>(a.slots) + ((size_t)x.s0 * a.Hk + hk) * PER;
+  const int keys = min(kTile, x.seq.m - x.tile * kTile);
+  for (int e = part * PART + (int)threadIdx.x; e < (part + 1) * PART; e += blockDim.x) {
+    const int f = e * 4, which = f / (kTile * D), row = f / D % kTile, col = f % D;
+    if (row >= keys) continue;
+    float4 acc = base[e];
+    for (int s = 1; s < x.s1; ++s) {
+      const float4 v = base[(size_t)s * a.Hk * PER + e];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const float mul = which == 0 ? 1.f : a.scale;
+    const long long* st = which == 0 ? a.dvs : a.dks;
+    uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) +
+                    (long long)(x.seq.k0 + x.tile * kTile + row) * st[0] + hk * st[1] + col;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(acc.x * mul, acc.y * mul), pack2<F16>(acc.z * mul, acc.w * mul));
+  }
+}
+
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  Launch(long long grid, int threads, size_t smem, cudaStream_t s) {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+  }
+};
+
+int stream_blocks(long long threads) {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const long long blocks = (threads + 255) / 256, most = (long long)sms * 8;
+  return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+}
+
+template <int D, bool F16>
+cudaError_t main_t(const PackedArgs& a, const CUtensorMap* tm, int items, cudaStream_t s) {
+  using L = Layout<D>;
+  const auto kern = packed_bwd_kernel<D, F16>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
+  if (e != cudaSuccess) return e;
+  Launch l((long long)items * a.Hk, L::NT, L::BYTES, s);
+  return cudaLaunchKernelEx(&l.cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], a);
+}
+template <int D, bool F16>
+cudaError_t rows_t(const PackedArgs& a, cudaStream_t s) {
+  Launch l(stream_blocks((long long)a.Tq * a.Hq * (D / 8)), 256, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, packed_rows_kernel<D, F16>, a);
+}
+template <int D, bool F16>
+cudaError_t finish_t(const PackedArgs& a, int cuts, cudaStream_t s) {
+  const int dq_blocks = stream_blocks((long long)a.Tq * a.Hq * (D / 8));
+  Launch l(dq_blocks + (long long)cuts * a.Hk * kSumParts, 256, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, packed_finish_kernel<D, F16>, a, dq_blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_bwd_preprocess(const PackedArgs& a, int d, bool f16, cudaStream_t s) {
+  if (d == 64) return f16 ? rows_t<64, true>(a, s) : rows_t<64, false>(a, s);
+  return f16 ? rows_t<128, true>(a, s) : rows_t<128, false>(a, s);
+}
+cudaError_t launch_packed_bwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s) {
+  if (d == 64) return f16 ? main_t<64, true>(a, tm, items, s) : main_t<64, false>(a, tm, items, s);
+  return f16 ? main_t<128, true>(a, tm, items, s) : main_t<128, false>(a, tm, items, s);
+}
+cudaError_t launch_packed_bwd_finalize(const PackedArgs& a, int d, bool f16, int cuts, cudaStream_t s) {
+  if (d == 64) return f16 ? finish_t<64, true>(a, cuts, s) : finish_t<64, false>(a, cuts, s);
+  return f16 ? finish_t<128, true>(a, cuts, s) : finish_t<128, false>(a, cuts, s);
+}
+
+}  // namespace fa

@@ -1,0 +1,452 @@
+// packed_fwd.cu -- attention forward of packed sequences with grouped heads (sm_103a).
+//
+// O = softmax(scale Q K^T) V and LSE for each sequence's queries over its own keys: the tiled
+// recurrence of fwd_tc.cu ("L'algorithme Flash Attention", marketmaker.cc), with
+//   - a query tile of tpt tokens times the G query heads of one key head, row = token * G + head,
+//     which one TMA box {64 channels, G heads, tpt tokens} brings: a short prompt fills a tile's
+//     128 rows with its heads, and K and V are read once for all of them;
+//   - tiles taken from the list that packed_plan.cu makes of the offsets, longest first; units
+//     longer than an even share of the steps are cut along the keys, their parts (m, l, O in
+//     fp32) joined by a second kernel, so that few rows over many keys fill the GPU;
+//   - keys and values behind a sequence's end, which belong to the next sequence or to none, and
+//     those that only some rows of a tile see: scores are replaced by -inf, and values that are
+//     not finite, which a weight of 0 would make NaN, are zeroed in shared memory and added
+//     to the rows that see them at the end.
+//
+// Bound: the tensor core (4 d FLOPs a seen pair and query head) beside one exponential for each
+// 4 d FLOPs; two CTAs an SM, so that one's exponentials run beside the other's products.
+//
+// Warp roles (192 threads) as in fwd_tc.cu: warps 0-3 softmax (thread = row = TMEM lane), warp
+// 4 TMA producer, warp 5 TMEM owner and MMA issuer.
+#include "fwd_common.cuh"
+#include "packed.h"
+
+namespace fa {
+namespace {
+
+constexpr float kRescaleThr = 8.f;  // the running maximum moves past 2^8 only
+constexpr float kLargeScore = 65536.f;  // log2 units, from which on the maximum is taken off first
+constexpr int kNone = 0x7FFFFFFF;
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t TILE = kTile * D * 2;
+  static constexpr int NS = D == 64 ? 2 : 1;  // K/V ring depth: two CTAs on an SM
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t K0 = Q + TILE;
+  static constexpr uint32_t V0 = K0 + NS * TILE;
+  static constexpr uint32_t BAR = V0 + NS * TILE;
+  static constexpr uint32_t TSLOT = BAR + FwdBars<NS>::kCount * 8;
+  static constexpr uint32_t ABORT = TSLOT + 4;
+  static constexpr uint32_t SCRUB = ABORT + 4;  // first key tile some of whose values were zeroed
+  static constexpr uint32_t BYTES = SCRUB + 4;
+  // TMEM: S at [0, 128), O behind it; at d = 64 P~ has columns of its own, at d = 128 S's
+  static constexpr uint32_t TMEM_COLS = 256;
+  static constexpr bool PSEP = D == 64;
+  static constexpr uint32_t T_S = 0, T_O = 128, T_P = PSEP ? 192 : 0;
+};
+
+template <bool F16>
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc) {  // NaN where a value is not finite
+  uint32_t y;
+  if constexpr (F16)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0), "r"(acc));
+  else
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0), "r"(acc));
+  return y;
+}
+// The halves of a word that are infinite or NaN, as all ones.
+template <bool F16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  return ((x & e) == e ? 0xFFFFu : 0u) | ((x >> 16 & e) == e ? 0xFFFF0000u : 0u);
+}
+
+// Whether the 128 values rows of the tile at `tile` are all finite; those that are not become 0.
+// 1: some were of its first `inside` rows.  A warp calls it.
+template <int D, bool F16>
+__device__ __forceinline__ bool scrub_tile(uint32_t tile, int inside) {
+  const int lane = threadIdx.x & 31;
+  constexpr int CHUNKS = kTile * D * 2 / 16;
+  uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 8
+  for (int i = lane; i < CHUNKS; i += 32) {
+    const uint4 v = ld_shared_v4(tile + 16u * (uint32_t)i);
+    acc[0] = times_zero<F16>(v.x, acc[0]);
+    acc[1] = times_zero<F16>(v.y, acc[1]);
+    acc[2] = times_zero<F16>(v.z, acc[2]);
+    acc[3] = times_zero<F16>(v.w, acc[3]);
+  }
+  const bool bad = (not_finite<F16>(acc[0]) | not_finite<F16>(acc[1]) | not_finite<F16>(acc[2]) | not_finite<F16>(acc[3])) != 0u;
+  if (!__any_sync(0xffffffffu, bad)) return false;
+  bool in = false;
+#pragma unroll 1
+  for (int i = lane; i < CHUNKS; i += 32) {
+    const uint4 v = ld_shared_v4(tile + 16u * (uint32_t)i);
+    const uint32_t m[4] = {not_finite<F16>(v.x), not_finite<F16>(v.y), not_finite<F16>(v.z), not_finite<F16>(v.w)};
+    if ((m[0] | m[1] | m[2] | m[3]) != 0u) {
+      st_shared_v4(tile + 16u * (uint32_t)i, v.x & ~m[0], v.y & ~m[1], v.z & ~m[2], v.w & ~m[3]);
+      in |= i % (kTile * 8) / 8 < inside;  // 8 chunks a row of 64 channels
+    }
+  }
+  fence_async_smem();
+  return __any_sync(0xffffffffu, in);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(192, 2)
+    packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const PackedArgs a) {
+  using L = Layout<D>;
+  constexpr int NS = L::NS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
+  const int count = a.list.head[0];
+  int index, hk;
+  if (a.head_major) {
+    if (count == 0) return;
+    hk = (int)blockIdx.x / count;
+    index = (int)blockIdx.x - hk * count;
+    if (hk >= a.Hk) return;
+  } else {
+    index = a.divHk.div((int)blockIdx.x);
+    hk = (int)blockIdx.x - index * a.Hk;
+    if (index >= count) return;
+  }
+  const PackedItem x = a.list.items[index];
+  const int t0 = x.tile * a.tpt;                       // the tile's first token in its sequence
+  const int rows = min(a.tpt, x.seq.n - t0) * a.G;     // rows that are the sequence's
+  const int pos0 = x.seq.m - x.seq.n + t0;             // its place among the keys
+  const int seen_by_all = a.causal ? min(x.seq.m, pos0 + 1) : x.seq.m;
+
+  const FwdBars<NS> bars{sb + L::BAR};
+  volatile int* abort_cta = reinterpret_cast<volatile int*>(smem + L::ABORT);
+  volatile int* scrubbed = reinterpret_cast<volatile int*>(smem + L::SCRUB);
+  const WaitCtx w{abort_cta, a.rep.st, a.rep.epoch, a.rep.wait_ns};
+  if ((sb & 1023u) != 0) {  // the swizzled layouts need a 1024-byte aligned base
+    if (threadIdx.x == 0) raise_error(w, FA_ERR_CUDA);
+    return;
+  }
+  // debug build: the tile lies in its sequence, and that in the tensors
+  if (!dbg_check(w, rows > 0 && x.s0 >= 0 && x.s0 <= x.s1 && x.s1 <= packed_units(x.seq, a.tpt, true) && x.seq.q0 >= 0 &&
+                        x.seq.q0 + x.seq.n <= a.Tq && x.seq.k0 >= 0 && x.seq.k0 + x.seq.m <= a.Tk && hk < a.Hk))
+    return;
+
+  const bool producer = warp == 4 && lane == 0;
+  int nk = 0, nv = 0;  // producer lane: K and V copies issued
+  int kt_next = x.s1;
+  auto load_k = [&](int st, int kt) {
+    mbar_arrive_expect_tx(bars.kf(st), L::TILE);
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(sb + L::K0 + st * L::TILE + c * (kTile * 128), &tmK, bars.kf(st), c * 64, hk, x.seq.k0 + kt * kTile);
+  };
+  auto load_v = [&](int st, int kt) {
+    mbar_arrive_expect_tx(bars.vf(st), L::TILE);
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(sb + L::V0 + st * L::TILE + c * (kTile * 128), &tmV, bars.vf(st), c * 64, hk, x.seq.k0 + kt * kTile);
+  };
+  auto next = [](int kt) { return kt; };
+  if (producer) {
+    bars.init();
+    *abort_cta = 0;
+    *scrubbed = kNone;
+    fence_barrier_init();
+    mbar_arrive_expect_tx(bars.q(), (uint32_t)(a.tpt * a.G) * D * 2u);
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(sb + L::Q + c * (kTile * 128), &tmQ, bars.q(), c * 64, hk * a.G, x.seq.q0 + t0);
+    kt_next = fwd_produce(w, bars, x.s0, x.s1, x.seq.m, NS, nk, nv, next, load_k, load_v);
+  }
+  if (warp == 5) {
+    tmem_alloc(sb + L::TSLOT, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::TSLOT);
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      if (kt_next >= 0) fwd_produce(w, bars, kt_next, x.s1, x.seq.m, 1 << 30, nk, nv, next, load_k, load_v);
+      fwd_drain_copies(w, bars, nk, nv);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idS = idesc_f16(F16, kTile, kTile, false, false);
+    constexpr uint32_t idO = idesc_f16(F16, kTile, D, false, true);
+    const uint32_t tS = tmem + L::T_S, tO = tmem + L::T_O;
+    const uint64_t dQ = desc_kmajor_base(sb + L::Q);
+    const uint64_t dK0 = desc_kmajor_base(sb + L::K0);
+    const uint64_t dV0 = desc_mnmajor_base(sb + L::V0, kTile);
+    fwd_mma_schedule<NS, L::PSEP>(
+        w, bars, x.s0, x.s1, next,
+        [&](int st) {  // S = Q K^T
+          const uint64_t dK = desc_add(dK0, (uint32_t)st * L::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ss_elect(tS, dQ + kmajor_step(kk, kTile), dK + kmajor_step(kk, kTile), idS, kk > 0 ? 1u : 0u);
+        },
+        [&](int st, int it) {  // O += P~ V
+          const uint64_t dV = desc_add(dV0, (uint32_t)st * L::TILE);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_ts_elect(tO, tmem + L::T_P + (uint32_t)kk * 8u, dV + mnmajor_step(kk), idO,
+                            (it > 0 || kk > 0) ? 1u : 0u);
+        },
+        [&](int st, int kt, int it) {  // a tile that some row does not see all of: its values are looked over
+          if (kt * kTile + kTile <= seen_by_all) return true;
+          if (!warp_wait(w, bars.vf(st), (it / NS) & 1)) return false;
+          if (scrub_tile<D, F16>(sb + L::V0 + st * L::TILE, x.seq.m - kt * kTile) && lane == 0 && *scrubbed == kNone) {
+            *scrubbed = kt;
+            __threadfence_block();
+          }
+          __syncwarp();
+          return true;
+        });
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int r = threadIdx.x;
+    const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
+    const bool live = r < rows;
+    const int lim = a.causal ? min(x.seq.m, pos0 + i + 1) : x.seq.m;  // keys that the row sees
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tS = tmem + L::T_S + lane_off, tO = tmem + L::T_O + lane_off;
+    const float c2 = a.scale_log2;
+    float m_use = -INFINITY;  // running maximum in use, of the products
+    float l = 0.f;
+    bool ok = true;
+    int it = 0;
+    for (int kt = x.s0; kt < x.s1; ++kt, ++it) {
+      if (!(ok = warp_wait(w, bars.s(), it & 1))) break;
+      tc_fence_after();
+      float s[kTile];
+      float m8[8];
+      {
+        uint32_t u[64], v[64];
+        tmem_ld64(tS, u);
+        tmem_ld64_nowait(tS + 64, v);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(u[c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m8[j] = max16(s, j);
+        tmem_wait_ld64(v);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[64 + c] = __uint_as_float(v[c]);
+      }
+      if (L::PSEP) {  // S_j is in registers: the MMA warp may compute S_{j+1}
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.sfree());
+      }
+      if (kt * kTile + kTile > seen_by_all) {
+        const int low = lim - kt * kTile;
+#pragma unroll
+        for (int c = 0; c < kTile; ++c)
+          if (c >= low) s[c] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m8[j] = max16(s, j);
+      }
+#pragma unroll
+      for (int j = 4; j < 8; ++j) m8[j] = max16(s, j);
+      const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+      float alpha = 1.f;
+      if ((mx - m_use) * c2 > kRescaleThr) {
+        alpha = ex2((m_use - mx) * c2);  // 0 on the first tile that sees a key
+        m_use = mx;
+      }
+      float mneg = m_use == -INFINITY ? 0.f : -m_use * c2;
+      if (__any_sync(0xffffffffu, fabsf(mneg) > kLargeScore)) {
+        // the rounded maximum would be off by more than 2^-8: the difference first, which is
+        // exact near the maximum
+        const float top = m_use == -INFINITY ? 0.f : m_use;
+#pragma unroll
+        for (int c = 0; c < kTile; ++c) s[c] -= top;
+        mneg = 0.f;
+      }
+      const uint64_t c2p = f2pack(c2, c2), mp = f2pack(mneg, mneg);
+      uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+      // four chunks of 32 keys, each chunk's P~ stored as soon as it is formed; P~ is rounded to the
+      // inputs' type (half a step of each weight), l adds the fp32 weights
+      bool o_ready = !(L::PSEP && it > 0);
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int pr = 0; pr < 16; ++pr) {
+          const int c = 32 * ch + 2 * pr;
+          float x0, x1;
+          f2unpack(ffma2(f2pack(s[c], s[c + 1]), c2p, mp), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          acc[pr & 3] = fadd2(acc[pr & 3], f2pack(p0, p1));
+          pk[pr] = pack2<F16>(p0, p1);
+        }
+        if (!o_ready) {  // P~ V_{j-1} reads the P~ columns and writes O
+          if (!(ok = warp_wait(w, bars.o(), (it - 1) & 1))) break;
+          tc_fence_after();
+          o_ready = true;
+        }
+        tmem_st16(tmem + L::T_P + lane_off + 16 * ch, pk);
+      }
+      if (!ok) break;
+      l = l * alpha + sum_packed4(acc);
+      if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) scale_o_row<D>(tO, alpha);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.p());
+    }
+    // ------------------------------------------------------------ epilogue
+    bool have_o = false;
+    if (ok && it > 0) {
+      ok = warp_wait(w, bars.o(), (it - 1) & 1);
+      tc_fence_after();
+      have_o = ok;
+    }
+    if (ok) {
+      const bool whole = x.slot < 0;
+      const float inv_l = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+      const long long slot = (long long)x.slot * a.Hk + hk;
+      float* part = whole ? nullptr : a.slots + slot * (kTile * (D + 2));
+      if (whole) {
+        if (live) a.lse[(long long)token * a.Hq + head] = l == 0.f ? -INFINITY : fmaf(m_use, a.scale, __logf(l));
+      } else {
+        *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m_use, l);
+      }
+      // values that were zeroed: added to the rows that see them
+      const int from = *scrubbed;
+      const bool patch = from != kNone;
+      const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)x.seq.k0 * a.vs[0] + hk * a.vs[1];
+      const int end = min(lim, x.s1 * kTile);
+      uint16_t* dst = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1];
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        if (have_o) {
+          tmem_ld32(tO + c0, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (patch && live) {
+#pragma unroll 1
+          for (int j = from * kTile; j < end; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4*>(vrow + j * a.vs[0] + c0) + v);
+              const uint32_t h[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack2<F16>(h[k] & not_finite<F16>(h[k]));
+                o[8 * v + 2 * k] = __float_as_uint(__uint_as_float(o[8 * v + 2 * k]) + f.x);
+                o[8 * v + 2 * k + 1] = __float_as_uint(__uint_as_float(o[8 * v + 2 * k + 1]) + f.y);
+              }
+            }
+        }
+        if (whole && live) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint4 q;
+            q.x = pack2<F16>(__uint_as_float(o[v * 8 + 0]) * inv_l, __uint_as_float(o[v * 8 + 1]) * inv_l);
+            q.y = pack2<F16>(__uint_as_float(o[v * 8 + 2]) * inv_l, __uint_as_float(o[v * 8 + 3]) * inv_l);
+            q.z = pack2<F16>(__uint_as_float(o[v * 8 + 4]) * inv_l, __uint_as_float(o[v * 8 + 5]) * inv_l);
+            q.w = pack2<F16>(__uint_as_float(o[v * 8 + 6]) * inv_l, __uint_as_float(o[v * 8 + 7]) * inv_l);
+            *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q;
+          }
+        } else if (!whole) {
+          float* to = part + 2 * kTile + (size_t)r * D + c0;
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            *reinterpret_cast<uint4*>(to + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+// Joins the parts of the units that were cut: with M = max m_s, L = sum l_s 2^((m_s - M) c2),
+// O = sum O_s 2^((m_s - M) c2) / L.  D / 4 threads a row, four blocks for a unit and key head.
+constexpr int kJoinParts = 4;
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) packed_join_kernel(const PackedArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int cut = a.divHk.div((int)blockIdx.x), hk = (int)blockIdx.x - cut * a.Hk;
+  if (cut >= a.list.head[1]) return;
+  const PackedItem x = a.list.cuts[cut];
+  const int t0 = x.tile * a.tpt, rows = min(a.tpt, x.seq.n - t0) * a.G;
+  constexpr int TPR = D / 4, PER = 256 / TPR;
+  const int c = (int)threadIdx.x % TPR;
+  constexpr size_t words = kTile * (D + 2);
+  const size_t step = words * a.Hk;
+  const float* base = a.slots + ((size_t)x.s0 * a.Hk + hk) * words;
+  for (int r = blockIdx.y * PER + (int)threadIdx.x / TPR; r < rows; r += kJoinParts * PER) {
+    float top = -INFINITY;
+    for (int s = 0; s < x.s1; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(base + s * step + 2 * r);
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+    }
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < x.s1; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(base + s * step + 2 * r);
+      if (ml.y == 0.f) continue;  // saw no key
+      const float f = ml.x == top ? 1.f : ex2((ml.x - top) * a.scale_log2);
+      const float4 o = *reinterpret_cast<const float4*>(base + s * step + 2 * kTile + (size_t)r * D + 4 * c);
+      sum = fmaf(f, ml.y, sum);
+      acc[0] = fmaf(f, o.x, acc[0]);
+      acc[1] = fmaf(f, o.y, acc[1]);
+      acc[2] = fmaf(f, o.z, acc[2]);
+      acc[3] = fmaf(f, o.w, acc[3]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
+    if (!fa_bounds(a.rep.st, token < a.Tq && head < a.Hq)) continue;
+    uint16_t* to = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1] + 4 * c;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
+    if (c == 0) a.lse[(long long)token * a.Hq + head] = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __logf(sum));
+  }
+}
+
+template <int D, bool F16>
+cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, int cuts, cudaStream_t s) {
+  using L = Layout<D>;
+  const auto kern = packed_fwd_kernel<D, F16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3((unsigned)((long long)items * a.Hk));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = L::BYTES;
+  e = cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], a);
+  if (e != cudaSuccess || cuts == 0) return e;
+  cfg.gridDim = dim3((unsigned)((long long)cuts * a.Hk), kJoinParts);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, packed_join_kernel<D, F16>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, int cuts,
+                              cudaStream_t s) {
+  if (d == 64) return f16 ? launch_t<64, true>(a, tm, items, cuts, s) : launch_t<64, false>(a, tm, items, cuts, s);
+  return f16 ? launch_t<128, true>(a, tm, items, cuts, s) : launch_t<128, false>(a, tm, items, cuts, s);
+}
+
+}  // namespace fa

@@ -32,7 +32,7 @@ from typing import Optional
 import torch
 
 from . import FA_BF16, FA_F16, FA_F32, _check, load
-from ._abi import I64x2, I64x3, FaKv4AttnParams, FaKv4Cache, FaKv4Rows, FaPlanParams, FaQkParams
+from ._abi import I64x2, I64x3, FaKv4AttnParams, FaKv4Cache, FaKv4Rows, FaPackedParams, FaPlanParams, FaQkParams
 
 KV4_GROUP = 32    # channels that share a (scale, base) pair
 KV4_BLOCK = 16    # tokens of a cache block
@@ -48,8 +48,9 @@ _CODES = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}
 # with the extension (csrc/launch.cpp) that repeats the call: a call on sixteen tokens
 # takes the GPU a few microseconds, the checks would take several times that.
 
-_QK, _QK_BWD, _APPEND, _GATHER, _ATTENTION, _PLAN = range(6)
-_ENTRY = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attention", "fa_paged_plan")
+_QK, _QK_BWD, _APPEND, _GATHER, _ATTENTION, _PLAN, _PACKED, _PACKED_BWD = range(8)
+_ENTRY = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attention", "fa_paged_plan",
+          "fa_fwd_packed", "fa_bwd_packed")
 _STREAM = (3, 0)
 _launch = None  # the extension, from the first call on
 
@@ -429,3 +430,86 @@ def paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_siz
     got = _call(_PLAN, (seq_lens, new_lens, block_table, free_pages, free_count, *given), (int(page_size), int(T)),
                 stream, _plan_plan)
     return dict(zip(_PLAN_OUT, got))
+
+
+# ---------------------------------------------------------------- packed sequences
+
+def _packed_checked(q, k, v, cu_q, cu_k, lse, causal, scale, like_q, like_k, names):
+    """(C parameters, device); like_q, like_k: further tensors of q's and k's sizes, o, do and dq,
+    and dk and dv, None for one that is still to be made."""
+    dt = q.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q must be fp16 or bf16, not {dt}")
+    _need(q, "q", dt, (None, None, None))
+    Tq, Hq, d = q.shape
+    _need(k, "k", dt, (None, None, d))
+    Tk, Hk = k.shape[:2]
+    _need(v, "v", dt, (Tk, Hk, d))
+    _need(cu_q, "cu_q", torch.int32, (None,))
+    _contiguous(cu_q, "cu_q")
+    if cu_q.shape[0] < 2:
+        raise ValueError("cu_q needs at least two offsets")
+    if cu_k is not None:
+        _need(cu_k, "cu_k", torch.int32, cu_q.shape)
+        _contiguous(cu_k, "cu_k")
+    elif Tk != Tq:
+        raise ValueError(f"without cu_k, k must have as many rows as q ({Tq}), not {Tk}")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (Tq, Hq))
+        _contiguous(lse, "lse")
+    device = _one_device(q, k, v, cu_q, cu_k, lse, *like_q, *like_k)
+    strides = []
+    for x, name, T, H in [(x, n, Tq, Hq) for x, n in zip(like_q, names)] + [
+            (x, n, Tk, Hk) for x, n in zip(like_k, names[len(like_q):])]:
+        if x is None:  # a new tensor, contiguous
+            strides.append(I64x2(*_dense((T, H), (H * d, d))))
+        else:
+            _need(x, name, dt, (T, H, d))
+            strides.append(I64x2(*_strides(x, name, (0, 1))))
+    p = FaPackedParams(cu_q.shape[0] - 1, Tq, Tk, Hq, Hk, d, _CODES[dt], int(bool(causal)),
+                       1.0 / math.sqrt(d) if scale is None else float(scale), I64x2(*_strides(q, "q", (0, 1))),
+                       I64x2(*_strides(k, "k", (0, 1))), I64x2(*_strides(v, "v", (0, 1))), *strides)
+    return p, device
+
+
+def _plan_packed(q, k, v, cu_q, cu_k, out, lse, workspace, causal, scale):
+    p, device = _packed_checked(q, k, v, cu_q, cu_k, lse, causal, scale, (out,), (), ("out",))
+    new = _Outputs()
+    res = [new.given(5, out, q.shape, q.dtype), new.given(6, lse, q.shape[:2], torch.float32)]
+    ws, nbytes = _workspace(new, 7, workspace, load().fa_fwd_packed_workspace_size(ctypes.byref(p)), device)
+    return device, [_const(p), *map(_in, range(5)), *res, ws, _const(nbytes), _STREAM], new, res, p
+
+
+def _plan_packed_bwd(q, k, v, o, do, lse, cu_q, cu_k, dq, dk, dv, workspace, causal, scale):
+    if lse is None:
+        raise ValueError("lse must be the forward's")
+    for x, name in ((o, "o"), (do, "do")):
+        if x is None:
+            raise ValueError(f"{name} is missing")
+    p, device = _packed_checked(q, k, v, cu_q, cu_k, lse, causal, scale, (o, do, dq), (dk, dv), ("o", "do", "dq", "dk", "dv"))
+    new = _Outputs()
+    res = [new.given(8, dq, q.shape, q.dtype), new.given(9, dk, k.shape, q.dtype), new.given(10, dv, v.shape, q.dtype)]
+    ws, nbytes = _workspace(new, 11, workspace, load().fa_bwd_packed_workspace_size(ctypes.byref(p)), device)
+    return device, [_const(p), *map(_in, range(8)), *res, ws, _const(nbytes), _STREAM], new, res, p
+
+
+def attention_fwd_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: Optional[float] = None, out=None, lse=None,
+                         workspace=None, stream=None):
+    """(o, lse): attention of sequences of different lengths packed one behind the other.
+    Sequence r's queries are rows cu_q[r] : cu_q[r + 1] of q [Tq, Hq, d], its keys and values rows
+    cu_k[r] : cu_k[r + 1] (None: cu_q) of k and v [Tk, Hk, d]; Hq is a multiple of Hk.  With
+    ``causal`` the i-th of n queries over m keys sees the keys up to i + m - n, so that k and v may
+    begin with what is cached of the sequence.  o has q's shape, lse is fp32 [Tq, Hq]; a row that
+    sees no key: o = 0, lse = -inf; rows in no sequence are not written.  Lengths stay on the GPU:
+    the call does not synchronise."""
+    return _call(_PACKED, (q, k, v, cu_q, cu_k, out, lse, workspace), (bool(causal), None if scale is None else float(scale)),
+                 stream, _plan_packed)
+
+
+def attention_bwd_packed(q, k, v, o, do, lse, cu_q, cu_k=None, causal: bool = True, scale: Optional[float] = None, dq=None,
+                         dk=None, dv=None, workspace=None, stream=None):
+    """(dq, dk, dv): gradients of ``attention_fwd_packed`` for the gradient do at its o; o and lse
+    are its results.  dk and dv are summed over the query heads of a key head.  Views of a packed
+    gradient may be given for dq, dk, dv; their rows in no sequence are not written."""
+    return _call(_PACKED_BWD, (q, k, v, o, do, lse, cu_q, cu_k, dq, dk, dv, workspace),
+                 (bool(causal), None if scale is None else float(scale)), stream, _plan_packed_bwd)

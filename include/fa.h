@@ -510,6 +510,59 @@ fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int*
                         int* block_table, int* free_pages, const int* free_count, int* kv_lens,
                         int* cu_q, int* positions, int* slots, int* counts, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention of R sequences of different lengths packed one behind the other, with
+ * grouped heads, and its gradient.
+ *
+ * Sequence r's queries are rows cu_q[r] .. cu_q[r + 1] of q and its keys and values
+ * rows cu_k[r] .. cu_k[r + 1] of k and v; query head h reads key head h / (Hq / Hk).
+ * With n queries over m keys (any n and m, also 0) and `causal`, query i sees the
+ * keys j <= i + m - n: the last query stands at the last key, so that new rows over
+ * a longer cached prefix, or a whole prompt (m = n), are the same call.
+ *     O = softmax(scale * q K^T) V,  LSE = the log-sum-exp of the scaled scores;
+ * a row that sees no key gets O = 0 and LSE = -inf and has no part in the gradients.
+ *   R           sequences (1 to 2^24 - 1); cu_q, cu_k: device int32 [R + 1]; cu_k NULL: cu_q
+ *               (Tq = Tk).  Offsets outside the tensors or smaller than one before are
+ *               taken as the nearest that is neither, and recorded as FA_ERR_INDEX.
+ *   Tq, Tk      rows of q and of k and v, at most 2^30; Tq*Hq, Tk*Hk < 2^31.
+ *   Hq, Hk, d   query and key heads (Hq / Hk at most 128), head size (64 or 128).
+ *   dtype       FA_F16 or FA_BF16 of all tensors; lse: fp32 [Tq][Hq].
+ *   *_stride    element strides {token, head} of [T][H][d]; channels are contiguous.
+ *               Bases 16-byte aligned, strides multiples of 16 bytes, below 2^38, and not
+ *               0; written tensors must not overlap themselves.  q, k and v may be
+ *               views of one packed projection, in either order of tokens and heads.
+ * Results must not lie over inputs (dq may be q, o or do with the same strides).  Rows
+ * that are in no sequence are neither read into a result nor written.  What is not
+ * finite in k, v or q reaches, in the forward pass, the rows that see it; in the
+ * backward pass it may reach every gradient of its own sequence, and none of another.
+ * The workspace is 256-byte aligned and owned by the caller; its contents do not matter;
+ * calls that may run at the same time need workspaces of their own.
+ * The forward pass and dK, dV add in a fixed order; dQ is a sum of parts that arrive in
+ * any order (fp32), so that its last bits may differ from call to call, as fa_bwd's.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int R, Tq, Tk, Hq, Hk, d;
+  int dtype, causal;
+  float scale;
+  long long q_stride[2], k_stride[2], v_stride[2], o_stride[2];
+  long long do_stride[2], dq_stride[2], dk_stride[2], dv_stride[2]; /* backward */
+} fa_packed_params;
+
+/* Bytes of workspace (the work list, partial results of long tiles); 0 on invalid p. */
+size_t fa_fwd_packed_workspace_size(const fa_packed_params* p);
+fa_status fa_fwd_packed(const fa_packed_params* p, const void* q, const void* k, const void* v,
+                        const int* cu_q, const int* cu_k, void* o, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* dQ, dK, dV from the forward's inputs and results (the formulas are fa_bwd's); a key
+ * head's dK and dV are the sums over its query heads.  The workspace holds, besides, an
+ * fp32 accumulator of dQ. */
+size_t fa_bwd_packed_workspace_size(const fa_packed_params* p);
+fa_status fa_bwd_packed(const fa_packed_params* p, const void* q, const void* k, const void* v,
+                        const void* o, const void* dout, const float* lse, const int* cu_q,
+                        const int* cu_k, void* dq, void* dk, void* dv, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
