@@ -76,6 +76,11 @@ def signatures() -> dict:
         "fa_kv4_gather": (I, [CP, RP] + [P] * 5),
         "fa_kv4_attention_workspace_size": (S, [CP, AP]),
         "fa_kv4_attention": (I, [CP, AP] + [P] * 8 + [S, P]),
+        "fa_kv8_block_bytes": (I, [I]),
+        "fa_kv8_append": (I, [CP, RP] + [P] * 5),
+        "fa_kv8_gather": (I, [CP, RP] + [P] * 5),
+        "fa_kv8_attention_workspace_size": (S, [CP, AP]),
+        "fa_kv8_attention": (I, [CP, AP] + [P] * 8 + [S, P]),
         "fa_paged_plan": (I, [PP] + [P] * 11),
         "fa_fwd_packed_workspace_size": (S, [SP]),
         "fa_fwd_packed": (I, [SP] + [P] * 8 + [S, P]),

@@ -25,9 +25,10 @@ BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libfa_debug.so")
 SOURCES = ["fa_api.cu", "fwd_tc.cu", "fwd_f32.cu", "bwd_tc.cu", "bwd_aux.cu", "fa_noalloc.cu", "fwd_fp8.cu",
            "ops_api.cu", "qk_norm_rope.cu", "kv4.cu", "kv4_attn_d64.cu", "kv4_attn_d128.cu", "plan.cu",
+           "kv8.cu", "kv8_attn_d64.cu", "kv8_attn_d128.cu",
            "packed_api.cu", "packed_plan.cu", "packed_fwd.cu", "packed_bwd.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "bwd_sched.cuh", "fp8.h", "tiles.cuh", "fwd_common.cuh",
-           "ops.h", "kv4.cuh", "kv4_ring.cuh", "kv4_attn.cuh", "api_checks.h", "packed.h", "packed_sched.cuh"]
+           "ops.h", "kv4.cuh", "kv4_ring.cuh", "kv8.cuh", "kv_attn.cuh", "api_checks.h", "packed.h", "packed_sched.cuh"]
 # the short way from Python to the C entry points (a CPython extension; gcc, torch's headers)
 LAUNCH_SOURCE = os.path.join(CSRC, "launch.cpp")
 LAUNCH = os.path.join(HERE, "_launch.so")

@@ -14,8 +14,9 @@ constexpr int kKvBlock = 16;  // tokens
 constexpr int kKvGroup = 32;  // channels of a pair
 constexpr float kKvSaturate = 16384.f;
 
-template <int D>
+template <int D_>
 struct KvBlock {
+  static constexpr int D = D_, bits = 4;
   static constexpr int row = D / 2;                 // bytes of a token's codes
   static constexpr int groups = D / kKvGroup;       // pairs of a token
   static constexpr int codes = kKvBlock * row;

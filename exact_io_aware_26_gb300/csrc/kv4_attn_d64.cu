@@ -1,7 +1,7 @@
-// kv4_attn_d64.cu -- the cache attention's kernels for head size 64 (kv4_attn.cuh).
-#include "kv4_attn.cuh"
+// kv4_attn_d64.cu -- the 4-bit cache attention's kernels for head size 64 (kv_attn.cuh).
+#include "kv_attn.cuh"
 
 namespace fa {
-template cudaError_t launch_kv4_attention_d<64>(const Kv4AttnArgs&, bool, int, int, int, cudaStream_t);
-template int kv4_clusters_at_once<64>(int, int);
+template cudaError_t launch_kv_attention<KvBlock<64>>(const Kv4AttnArgs&, bool, int, int, int, cudaStream_t);
+template int kv_clusters_at_once<KvBlock<64>>(int, int);
 }

@@ -1,4 +1,4 @@
-// kv4_attn.cuh -- attention of each request's newest tokens over its 4-bit cache.
+// kv_attn.cuh -- attention of each request's newest tokens over its 4-bit or 8-bit cache.
 //
 // Bound: HBM.  A token of one head is 160 bytes (d = 128) for both its key and its
 // value, and 8 query rows need 4 * 8 * d FLOPs of it: 26 FLOPs a byte, far below
@@ -46,6 +46,7 @@
 #include <type_traits>
 
 #include "kv4.cuh"
+#include "kv8.cuh"
 #include "kv4_ring.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -58,20 +59,23 @@ constexpr float kLeast = 1e-37f;     // of a score's factor: a hidden token's -i
 constexpr int kUnit = 2 * kKvBlock;  // tokens a warp takes at a time
 constexpr int kReqCache = 128;       // requests whose lengths a CTA keeps at hand
 
-// CL: the CTAs are a cluster's.
-template <int D, int NT, bool CL>
+// CL: the CTAs are a cluster's.  A block of 8 bits has 1.6 times the bytes of one of 4, so that
+// as many bytes are on their way with fewer stages or CTAs.
+template <class Blk, int NT, bool CL>
 struct Cfg {
-  using Blk = KvBlock<D>;
+  static constexpr int D = Blk::D;
+  static constexpr bool wide = Blk::bits == 8;
   static constexpr int ROWS = 8 * NT;
   static constexpr int WARPS = CL ? 8 : 4, THREADS = 32 * WARPS;
-  static constexpr int CTAS_PER_SM = CL ? (NT == 1 ? 2 : 1) : NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int CTAS_PER_SM =
+      CL ? (NT == 1 && !(wide && D == 128) ? 2 : 1) : kv_share_ctas(Blk::bits, ROWS, 1);
   static constexpr int LDO = D + 4;  // row pitch of the joined O, in floats
   static constexpr int stage = 2 * Blk::bytes;
   // For the join each warp's O goes into its ring.  Eight rows of a share take the stage of the
   // tile's last unit, and the copies of the next tile go on in the others; otherwise it is
   // the whole ring, which then holds one tile at a time.
   static constexpr bool across = NT == 1 && !CL;
-  static constexpr int STAGES = D == 64 || NT == 4 ? 4 : 2;
+  static constexpr int STAGES = wide ? (D == 64 || NT == 4 ? 3 : 2) : D == 64 || NT == 4 ? 4 : 2;
   static constexpr int ring = WARPS * STAGES * stage;
   static_assert(ROWS * LDO * 4 <= (across ? stage : STAGES * stage), "a warp's O fits");
   static constexpr int qfrag = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;
@@ -116,6 +120,19 @@ __device__ __forceinline__ uint32_t code_pair(const Magic& k, uint32_t w) {
   uint32_t y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(k.mask), "r"(k.one));
   return y;
+}
+
+// Four int8 codes as two half2: 1024 + (code + 128) is the fp16 number 0x6400 | (code + 128), and
+// less 1152 it is the code.  One logic operation and a permute and a sum for each pair.
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = hadd2(__byte_perm(u, 0x64646464u, 0x4140), 0xE480E480u);
+  hi = hadd2(__byte_perm(u, 0x64646464u, 0x4342), 0xE480E480u);
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -237,10 +254,9 @@ struct Feed {
 
 // Fills src with the warp's next units of the share, at most 32, all of one tile; returns
 // how many (0: none left).
-template <int D, int ROWS, int kWarps>
+template <class Blk, int ROWS, int kWarps>
 __device__ __noinline__ int feed_refill(const Kv4AttnArgs& a, Feed<ROWS>& f, const Req* reqs, int reqs_r0, int warp,
                                         long long u1) {
-  using Blk = KvBlock<D>;
   const int lane = threadIdx.x & 31, page_log = a.c.page_log;
   __syncwarp();
   Walk<ROWS> w = f.w;
@@ -306,10 +322,11 @@ __device__ __noinline__ void drain_ring(W wc, uint32_t bar0, Ring<S> at, int n) 
   __syncwarp();
 }
 
-template <int D, int NT, bool F16, bool CL>
-__global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_PER_SM) kv4_attn_kernel(const Kv4AttnArgs a) {
-  using C = Cfg<D, NT, CL>;
-  using Blk = KvBlock<D>;
+template <class Blk, int NT, bool F16, bool CL>
+__global__ void __launch_bounds__(Cfg<Blk, NT, CL>::THREADS, Cfg<Blk, NT, CL>::CTAS_PER_SM) kv_attn_kernel(const Kv4AttnArgs a) {
+  using C = Cfg<Blk, NT, CL>;
+  constexpr int D = Blk::D;
+  constexpr bool wide = C::wide;
   constexpr int kWarps = C::WARPS, kThreads = C::THREADS;
   constexpr int ROWS = C::ROWS, S = C::STAGES, KS = D / 16, MT = D / 16, WPT = D / 32 /* words per lane of K */;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -442,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
   int turn = 0, ready = 0;  // of feed.src
   auto produce = [&](int stage) {  // the copies of this warp's next unit, if any is left
     if (turn == ready) {
-      ready = feed_refill<D, ROWS, kWarps>(a, feed, reqs, cache_r0, warp, u1);
+      ready = feed_refill<Blk, ROWS, kWarps>(a, feed, reqs, cache_r0, warp, u1);
       turn = 0;
       if (ready == 0) {
         if (C::across && lane == 0) feed.hidden[stage] = kStageIdle;
@@ -546,9 +563,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
           const int row = y.row0 + n, qi = a.G.div(row);
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(a.q) + (x.q0 + qi) * a.qs[0] +
-              ((long long)cw.h * a.G.d + (row - qi * (int)a.G.d)) * a.qs[1] + t4 * (D / 4));
+              ((long long)cw.h * a.G.d + (row - qi * (int)a.G.d)) * a.qs[1]);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) raw[jj][i] = __ldg(src + i);
+          for (int i = 0; i < D / 32; ++i)  // 8 bits: 16-channel chunks t4 and, of 128 channels, t4 + 4
+            raw[jj][i] = __ldg(src + (wide ? (t4 + 4 * (i >> 1)) * 2 + (i & 1) : t4 * (D / 32) + i));
         }
       }
     };
@@ -597,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint32_t v = pack2<true>(f[p], f[p + 4]);
+          const uint32_t v = wide ? pack2<true>(f[2 * p], f[2 * p + 1]) : pack2<true>(f[p], f[p + 4]);
           if constexpr (NT == 4) {
             reinterpret_cast<uint32_t*>(qfrag)[((j * KS + 2 * i + (p >> 1)) * 32 + lane) * 2 + (p & 1)] = v;
           } else {
@@ -637,86 +655,135 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
     }
-    const int kr = g ^ ((g >> 1) & 1);  // token of fragment row g of a block (and kr + 8 of row g + 8)
+    // token of fragment row g of a block, and how far that of row g + 8 is from it.  8 bits: rows 2 t,
+    // 2 t + 1, 2 t + 8 and 2 t + 9 are tokens 4 t to 4 t + 3, a word of values.
+    const int kr = wide ? 4 * (g >> 1) + (g & 1) : g ^ ((g >> 1) & 1);
+    constexpr int kr_next = wide ? 2 : 8;
+    // 8 bits: O stands for o * vref, the scale of the values of late (a power of two)
+    [[maybe_unused]] float vref = 1.f, inv_vref = 1.f;
+    auto product_k = [&](float (&s)[NT][4], int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint2 q0;
+        if constexpr (NT == 4) q0 = qfrag[(j * KS + i) * 32 + lane];
+        else q0 = make_uint2(qf[j][i][0], qf[j][i][1]);
+        mma16816(s[j], a0, a1, a2, a3, q0.x, q0.y);
+      }
+    };
     // S^T of a block: raw products
     auto scores = [&](uint32_t kb, float (&s)[NT][4]) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[j][c] = 0.f;
-      uint32_t wa[WPT], wb[WPT];
-      const uint32_t ra = kb + kr * Blk::row + t4 * (D / 8), rb = ra + 8 * Blk::row;
-      if constexpr (D == 128) {
-        const uint4 u = ld_shared_v4(ra), v = ld_shared_v4(rb);
-        wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
-        wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
-      } else {
-        const uint2 u = lds64(ra), v = lds64(rb);
-        wa[0] = u.x; wa[1] = u.y;
-        wb[0] = v.x; wb[1] = v.y;
-      }
-      const uint32_t pa = kb + Blk::codes + (kr * Blk::groups + (D == 128 ? t4 : t4 >> 1)) * 4;
-      const uint32_t xa = lds32(pa), xb = lds32(pa + 8 * Blk::groups * 4);
-      const uint32_t sa = __byte_perm(xa, xa, 0x1010), ca = __byte_perm(xa, xa, 0x3232);
-      const uint32_t sb = __byte_perm(xb, xb, 0x1010), cb = __byte_perm(xb, xb, 0x3232);
+      if constexpr (wide) {
+        const uint32_t ra = kb + kr * Blk::row + kv8_key_chunk<D>(kr, t4) * 16, rb = ra + kr_next * Blk::row;
 #pragma unroll
-      for (int i = 0; i < WPT; ++i) {
-        const uint32_t a0 = hfma2(code_pair<0>(magic, wa[i]), sa, ca), a1 = hfma2(code_pair<0>(magic, wb[i]), sb, cb);
-        const uint32_t a2 = hfma2(code_pair<1>(magic, wa[i]), sa, ca), a3 = hfma2(code_pair<1>(magic, wb[i]), sb, cb);
-        const uint32_t c0 = hfma2(code_pair<2>(magic, wa[i]), sa, ca), c1 = hfma2(code_pair<2>(magic, wb[i]), sb, cb);
-        const uint32_t c2 = hfma2(code_pair<3>(magic, wa[i]), sa, ca), c3 = hfma2(code_pair<3>(magic, wb[i]), sb, cb);
+        for (int h = 0; h < D / 64; ++h) {  // chunk t4 + 4 h: the other half of the row
+          const int off = h == 0 ? 0 : (g & 1) ? -64 : 64;
+          const uint4 u = ld_shared_v4(ra + off), v = ld_shared_v4(rb + off);
+          const uint32_t wu[4] = {u.x, u.y, u.z, u.w}, wv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint2 q0, q1;
-          if constexpr (NT == 4) {
-            q0 = qfrag[(j * KS + 2 * i) * 32 + lane];
-            q1 = qfrag[(j * KS + 2 * i + 1) * 32 + lane];
-          } else {
-            q0 = make_uint2(qf[j][2 * i][0], qf[j][2 * i][1]);
-            q1 = make_uint2(qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, a2, a3;
+            codes4(wu[i], a0, a2);
+            codes4(wv[i], a1, a3);
+            product_k(s, 4 * h + i, a0, a1, a2, a3);
           }
-          mma16816(s[j], a0, a1, a2, a3, q0.x, q0.y);
-          mma16816(s[j], c0, c1, c2, c3, q1.x, q1.y);
+        }
+        return;
+      } else {
+        uint32_t wa[WPT], wb[WPT];
+        const uint32_t ra = kb + kr * Blk::row + t4 * (D / 8), rb = ra + 8 * Blk::row;
+        if constexpr (D == 128) {
+          const uint4 u = ld_shared_v4(ra), v = ld_shared_v4(rb);
+          wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
+          wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
+        } else {
+          const uint2 u = lds64(ra), v = lds64(rb);
+          wa[0] = u.x; wa[1] = u.y;
+          wb[0] = v.x; wb[1] = v.y;
+        }
+        const uint32_t pa = kb + Blk::codes + (kr * Blk::groups + (D == 128 ? t4 : t4 >> 1)) * 4;
+        const uint32_t xa = lds32(pa), xb = lds32(pa + 8 * Blk::groups * 4);
+        const uint32_t sa = __byte_perm(xa, xa, 0x1010), ca = __byte_perm(xa, xa, 0x3232);
+        const uint32_t sb = __byte_perm(xb, xb, 0x1010), cb = __byte_perm(xb, xb, 0x3232);
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) {
+          const uint32_t a0 = hfma2(code_pair<0>(magic, wa[i]), sa, ca), a1 = hfma2(code_pair<0>(magic, wb[i]), sb, cb);
+          const uint32_t a2 = hfma2(code_pair<1>(magic, wa[i]), sa, ca), a3 = hfma2(code_pair<1>(magic, wb[i]), sb, cb);
+          const uint32_t c0 = hfma2(code_pair<2>(magic, wa[i]), sa, ca), c1 = hfma2(code_pair<2>(magic, wb[i]), sb, cb);
+          const uint32_t c2 = hfma2(code_pair<3>(magic, wa[i]), sa, ca), c3 = hfma2(code_pair<3>(magic, wb[i]), sb, cb);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint2 q0, q1;
+            if constexpr (NT == 4) {
+              q0 = qfrag[(j * KS + 2 * i) * 32 + lane];
+              q1 = qfrag[(j * KS + 2 * i + 1) * 32 + lane];
+            } else {
+              q0 = make_uint2(qf[j][2 * i][0], qf[j][2 * i][1]);
+              q1 = make_uint2(qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+            }
+            mma16816(s[j], a0, a1, a2, a3, q0.x, q0.y);
+            mma16816(s[j], c0, c1, c2, c3, q1.x, q1.y);
+          }
         }
       }
     };
     // O^T += V^T P^T of a block: this lane's tokens are those of fragment rows 2 t, 2 t + 1 and 8 more
     auto values = [&](uint32_t vb, const uint32_t (&p0)[NT], const uint32_t (&p1)[NT]) {
-      constexpr int WV = D / 64;  // words of codes of a token per lane (8 channels each)
-      const int e0 = 2 * t4, e1 = 2 * t4 + 1;
-      const int ke = e0 ^ ((e0 >> 1) & 1), kf = e1 ^ ((e1 >> 1) & 1);
-      uint32_t w[4][WV], pr[4];
+      if constexpr (wide) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int key = (q & 1 ? kf : ke) + (q >> 1) * 8;
-        const uint32_t at = vb + key * Blk::row + g * (D / 16);
-        if constexpr (D == 128) {
-          const uint2 u = lds64(at);
-          w[q][0] = u.x;
-          w[q][1] = u.y;
-        } else {
-          w[q][0] = lds32(at);
+        for (int n = 0; n < D / 32; ++n) {
+          const uint4 u = ld_shared_v4(vb + (8 * n + g) * 64 + t4 * 16);  // channels 4 (8 n + g) .., tokens 4 t4 ..
+          const uint32_t wu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t a0, a1, a2, a3;
+            codes4(wu[2 * e], a0, a2);
+            codes4(wu[2 * e + 1], a1, a3);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816(o[2 * n + e][j], a0, a1, a2, a3, p0[j], p1[j]);
+          }
         }
-        pr[q] = lds32(vb + Blk::codes + (key * Blk::groups + (D == 128 ? g >> 1 : g >> 2)) * 4);
-      }
-      const uint32_t sx = __byte_perm(pr[0], pr[1], 0x5410), cx = __byte_perm(pr[0], pr[1], 0x7632);
-      const uint32_t sy = __byte_perm(pr[2], pr[3], 0x5410), cy = __byte_perm(pr[2], pr[3], 0x7632);
+        return;
+      } else {
+        constexpr int WV = D / 64;  // words of codes of a token per lane (8 channels each)
+        const int e0 = 2 * t4, e1 = 2 * t4 + 1;
+        const int ke = e0 ^ ((e0 >> 1) & 1), kf = e1 ^ ((e1 >> 1) & 1);
+        uint32_t w[4][WV], pr[4];
 #pragma unroll
-      for (int i = 0; i < WV; ++i) {
-        const uint32_t xl = __byte_perm(w[0][i], w[1][i], 0x5410), xh = __byte_perm(w[0][i], w[1][i], 0x7632);
-        const uint32_t yl = __byte_perm(w[2][i], w[3][i], 0x5410), yh = __byte_perm(w[2][i], w[3][i], 0x7632);
-        auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-          a0 = hfma2(a0, sx, cx);
-          a1 = hfma2(a1, sx, cx);
-          a2 = hfma2(a2, sy, cy);
-          a3 = hfma2(a3, sy, cy);
+        for (int q = 0; q < 4; ++q) {
+          const int key = (q & 1 ? kf : ke) + (q >> 1) * 8;
+          const uint32_t at = vb + key * Blk::row + g * (D / 16);
+          if constexpr (D == 128) {
+            const uint2 u = lds64(at);
+            w[q][0] = u.x;
+            w[q][1] = u.y;
+          } else {
+            w[q][0] = lds32(at);
+          }
+          pr[q] = lds32(vb + Blk::codes + (key * Blk::groups + (D == 128 ? g >> 1 : g >> 2)) * 4);
+        }
+        const uint32_t sx = __byte_perm(pr[0], pr[1], 0x5410), cx = __byte_perm(pr[0], pr[1], 0x7632);
+        const uint32_t sy = __byte_perm(pr[2], pr[3], 0x5410), cy = __byte_perm(pr[2], pr[3], 0x7632);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma16816(o[mt][j], a0, a1, a2, a3, p0[j], p1[j]);
-        };
-        product(4 * i + 0, code_pair<0>(magic, xl), code_pair<0>(magic, xh), code_pair<0>(magic, yl), code_pair<0>(magic, yh));
-        product(4 * i + 1, code_pair<1>(magic, xl), code_pair<1>(magic, xh), code_pair<1>(magic, yl), code_pair<1>(magic, yh));
-        product(4 * i + 2, code_pair<2>(magic, xl), code_pair<2>(magic, xh), code_pair<2>(magic, yl), code_pair<2>(magic, yh));
-        product(4 * i + 3, code_pair<3>(magic, xl), code_pair<3>(magic, xh), code_pair<3>(magic, yl), code_pair<3>(magic, yh));
+        for (int i = 0; i < WV; ++i) {
+          const uint32_t xl = __byte_perm(w[0][i], w[1][i], 0x5410), xh = __byte_perm(w[0][i], w[1][i], 0x7632);
+          const uint32_t yl = __byte_perm(w[2][i], w[3][i], 0x5410), yh = __byte_perm(w[2][i], w[3][i], 0x7632);
+          auto product = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            a0 = hfma2(a0, sx, cx);
+            a1 = hfma2(a1, sx, cx);
+            a2 = hfma2(a2, sy, cy);
+            a3 = hfma2(a3, sy, cy);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816(o[mt][j], a0, a1, a2, a3, p0[j], p1[j]);
+          };
+          product(4 * i + 0, code_pair<0>(magic, xl), code_pair<0>(magic, xh), code_pair<0>(magic, yl), code_pair<0>(magic, yh));
+          product(4 * i + 1, code_pair<1>(magic, xl), code_pair<1>(magic, xh), code_pair<1>(magic, yl), code_pair<1>(magic, yh));
+          product(4 * i + 2, code_pair<2>(magic, xl), code_pair<2>(magic, xh), code_pair<2>(magic, yl), code_pair<2>(magic, yh));
+          product(4 * i + 3, code_pair<3>(magic, xl), code_pair<3>(magic, xh), code_pair<3>(magic, yl), code_pair<3>(magic, yh));
+        }
       }
     };
 
@@ -732,8 +799,38 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       const uint32_t kb = ring + stage * C::stage;
       const int key0 = y.u0 + u * kUnit;
       const uint32_t hidden = feed.hidden[stage];
-      const bool masked = hidden || key0 + kUnit > all_hi || key0 < all_lo;
-      if (masked) {
+      bool masked = hidden || key0 + kUnit > all_hi || key0 < all_lo;
+      // 8 bits: the blocks' scales, 0 for one that was not read (whose weights are 0), and marks
+      [[maybe_unused]] float ks[2], vs[2];
+      [[maybe_unused]] uint32_t k_nan = 0, v_nan = 0;
+      if constexpr (wide) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 tail = ld_shared_v4(kb + h * Blk::bytes + Blk::tail);
+          const bool read = !((hidden >> h) & 1u);
+          ks[h] = read ? __uint_as_float(tail.x) : 0.f;
+          vs[h] = read ? __uint_as_float(tail.y) : 0.f;
+          k_nan |= read ? (tail.z & 0xFFFFu) << (16 * h) : 0u;
+          v_nan |= read ? (tail.z >> 16) << (16 * h) : 0u;
+        }
+        masked |= (k_nan | v_nan) != 0u;
+        if (v_nan != 0u) {  // a NaN value makes the sums NaN of the rows that see its token
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int pos = x.kv - x.n + a.G.div(y.row0 + 8 * j + 2 * t4 + c);
+              const uint32_t behind = below(min(pos + 1, x.kv) - key0), before = below(first_seen(a, pos) - key0);
+              const float add = v_nan & behind & ~before ? NAN : 0.f;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[i][j][c] += add;
+                o[i][j][c + 2] += add;
+              }
+            }
+        }
+      }
+      if constexpr (!wide) if (masked) {
         // values that no row sees must not reach the product (0 x NaN), nor a NaN that only
         // some rows see: their pairs become 0, and a NaN one makes the sums NaN of the rows
         // that see its token, in its group's channels
@@ -772,6 +869,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
       float s[2][NT][4];
       scores(kb, s[0]);
       scores(kb + Blk::bytes, s[1]);
+      if constexpr (wide) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; c += 2)
+              f2unpack(fmul2(f2pack(s[h][j][c], s[h][j][c + 1]), f2pack(ks[h], ks[h])), s[h][j][c], s[h][j][c + 1]);
+      }
       if (masked) {  // hidden tokens
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -783,9 +889,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const int key = 16 * h + 8 * q + kr;
+                const int key = 16 * h + kr_next * q + kr;
                 const bool seen = !((hidden >> h) & 1u) && key < lim && key >= low;
                 float& v = s[h][j][2 * q + c];
+                if (wide && (k_nan >> key) & 1u) v = NAN;
                 v = seen ? v : -INFINITY;
               }
           }
@@ -824,6 +931,24 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p0[NT], p1[NT];
+        [[maybe_unused]] float ratio = 1.f;
+        if constexpr (wide) {
+          // the weights take the scale of the block's values relative to that of O: in [2^-8, 1], so
+          // that they stay in fp16's range; where it is not O takes the block's
+          ratio = vs[h] * inv_vref;
+          if (!(ratio <= 1.f && ratio >= 0x1p-8f) && vs[h] != 0.f) {
+            const float back = vref / vs[h];
+            vref = vs[h];
+            inv_vref = 1.f / vref;
+            ratio = 1.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[i][j][c] *= back;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -835,6 +960,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
           }
           l[j][0] += s[h][j][0] + s[h][j][2];
           l[j][1] += s[h][j][1] + s[h][j][3];
+          if constexpr (wide) {
+#pragma unroll
+            for (int c = 0; c < 4; c += 2)
+              f2unpack(fmul2(f2pack(s[h][j][c], s[h][j][c + 1]), f2pack(ratio, ratio)), s[h][j][c], s[h][j][c + 1]);
+          }
           p0[j] = transpose8x8(pack2<true>(s[h][j][0], s[h][j][1]));
           p1[j] = transpose8x8(pack2<true>(s[h][j][2], s[h][j][3]));
         }
@@ -874,6 +1004,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CL>::THREADS, Cfg<D, NT, CL>::CTAS_
           if (g == 0) {
             m_s[warp][row] = m[j][c] == -kNoMax ? kNoMax : -m[j][c] * factor[j][c];
             l_s[warp][row] = v;
+          }
+          if constexpr (wide) {  // channels 4 (8 n + g) .. of m-tiles 2 n and 2 n + 1
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+              *reinterpret_cast<float4*>(mine + row * C::LDO + 32 * n + 4 * g) =
+                  make_float4(o[2 * n][j][c] * vref, o[2 * n][j][c + 2] * vref, o[2 * n + 1][j][c] * vref, o[2 * n + 1][j][c + 2] * vref);
+            continue;
           }
           float* to = mine + row * C::LDO + g * (D / 8);
 #pragma unroll
@@ -1082,7 +1219,7 @@ __device__ __forceinline__ void add_shares(const float* part, int row, int c0, i
 }
 
 template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const Kv4AttnArgs a) {
   constexpr int ROWS = 8 * NT, CPL = D / 32, FEW = 16;
   __shared__ float top_s[kMergeWarps], sum_s[kMergeWarps];
   __shared__ __align__(16) float acc_s[kMergeWarps][D];
@@ -1143,10 +1280,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Kv4At
 }
 
 // ctas: of the launch; cluster: CTAs of a cluster, or 0 for shares.
-template <int D, int NT, bool F16>
+template <class Blk, int NT, bool F16>
 cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) {
-  using C = Cfg<D, NT, false>;
-  using CC = Cfg<D, NT, true>;
+  using C = Cfg<Blk, NT, false>;
+  using CC = Cfg<Blk, NT, true>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   cfg.attrs = at;
@@ -1154,7 +1291,7 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) 
   cfg.stream = s;
   cudaError_t e;
   if (cluster > 0) {
-    const auto k = kv4_attn_kernel<D, NT, F16, true>;
+    const auto k = kv_attn_kernel<Blk, NT, F16, true>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CC::smem)) != cudaSuccess) return e;
     if (cluster > 8 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
       return e;
@@ -1167,7 +1304,7 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) 
     cfg.dynamicSmemBytes = CC::smem;
     return cudaLaunchKernelEx(&cfg, k, a);
   }
-  const auto k = kv4_attn_kernel<D, NT, F16, false>;
+  const auto k = kv_attn_kernel<Blk, NT, F16, false>;
   if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem)) != cudaSuccess) return e;
   k<<<ctas, C::THREADS, C::smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1175,15 +1312,15 @@ cudaError_t launch(const Kv4AttnArgs& a, int ctas, int cluster, cudaStream_t s) 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.gridDim = dim3(ctas);
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, NT, F16>, a);
+  return cudaLaunchKernelEx(&cfg, kv_merge_kernel<Blk::D, NT, F16>, a);
 }
 
 }  // namespace
 
 // Clusters of a size that the GPU holds at once: what its groups of SMs have room for, fewer
 // than the CTAs alone would allow (of 16 CTAs, two to an SM: 14, not 19).
-template <int D>
-int kv4_clusters_at_once(int rows, int cluster) {
+template <class Blk>
+int kv_clusters_at_once(int rows, int cluster) {
   auto ask = [&](auto k, int threads, int smem) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -1205,20 +1342,20 @@ int kv4_clusters_at_once(int rows, int cluster) {
     }
     return n;
   };
-  return rows == 8    ? ask(kv4_attn_kernel<D, 1, false, true>, Cfg<D, 1, true>::THREADS, Cfg<D, 1, true>::smem)
-         : rows == 16 ? ask(kv4_attn_kernel<D, 2, false, true>, Cfg<D, 2, true>::THREADS, Cfg<D, 2, true>::smem)
-                      : ask(kv4_attn_kernel<D, 4, false, true>, Cfg<D, 4, true>::THREADS, Cfg<D, 4, true>::smem);
+  return rows == 8    ? ask(kv_attn_kernel<Blk, 1, false, true>, Cfg<Blk, 1, true>::THREADS, Cfg<Blk, 1, true>::smem)
+         : rows == 16 ? ask(kv_attn_kernel<Blk, 2, false, true>, Cfg<Blk, 2, true>::THREADS, Cfg<Blk, 2, true>::smem)
+                      : ask(kv_attn_kernel<Blk, 4, false, true>, Cfg<Blk, 4, true>::THREADS, Cfg<Blk, 4, true>::smem);
 }
 
-template <int D>
-cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s) {
+template <class Blk>
+cudaError_t launch_kv_attention(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s) {
   if (f16)
-    return rows == 8    ? launch<D, 1, true>(a, ctas, cluster, s)
-           : rows == 16 ? launch<D, 2, true>(a, ctas, cluster, s)
-                        : launch<D, 4, true>(a, ctas, cluster, s);
-  return rows == 8    ? launch<D, 1, false>(a, ctas, cluster, s)
-         : rows == 16 ? launch<D, 2, false>(a, ctas, cluster, s)
-                      : launch<D, 4, false>(a, ctas, cluster, s);
+    return rows == 8    ? launch<Blk, 1, true>(a, ctas, cluster, s)
+           : rows == 16 ? launch<Blk, 2, true>(a, ctas, cluster, s)
+                        : launch<Blk, 4, true>(a, ctas, cluster, s);
+  return rows == 8    ? launch<Blk, 1, false>(a, ctas, cluster, s)
+         : rows == 16 ? launch<Blk, 2, false>(a, ctas, cluster, s)
+                      : launch<Blk, 4, false>(a, ctas, cluster, s);
 }
 
 }  // namespace fa

@@ -66,6 +66,9 @@ struct Kv4RowArgs {
 };
 cudaError_t launch_kv4_append(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
+// The 8-bit cache (kv8.cuh).
+cudaError_t launch_kv8_append(const Kv4RowArgs& a, int d, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_kv8_gather(const Kv4RowArgs& a, int d, int dtype, cudaStream_t s);
 
 struct Kv4AttnArgs {
   Kv4Cache c;
@@ -92,12 +95,13 @@ inline int kv4_tile_rows(int G, int max_q_len) {
   const long long rows = (long long)G * max_q_len;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
-// The CTAs of a launch in shares: one wave.
-inline int kv4_share_ctas(int rows, int sms) { return sms * (rows == 8 ? 4 : rows == 16 ? 3 : 2); }
-template <int D>
-cudaError_t launch_kv4_attention_d(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s);
-template <int D>
-int kv4_clusters_at_once(int rows, int cluster);
+// The CTAs of a launch in shares over a cache of 4 or 8 bits: one wave.
+constexpr int kv_share_ctas(int bits, int rows, int sms) { return sms * (rows == 8 && bits == 4 ? 4 : rows <= 16 ? 3 : 2); }
+// Blk: KvBlock<d> or Kv8Block<d>.
+template <class Blk>
+cudaError_t launch_kv_attention(const Kv4AttnArgs& a, bool f16, int rows, int ctas, int cluster, cudaStream_t s);
+template <class Blk>
+int kv_clusters_at_once(int rows, int cluster);
 
 struct PlanArgs {
   int R, T, page, pages, width;

@@ -1,5 +1,5 @@
 // ops_api.cu -- the C ABI of the operators around the attention (include/fa.h): norm
-// and rotation of queries and keys, the 4-bit paged cache and its attention, block
+// and rotation of queries and keys, the 4-bit and 8-bit paged caches and their attention, block
 // tables and slot maps.  Host code: argument checks, before any CUDA call, and the
 // launches.
 #include <algorithm>
@@ -9,6 +9,7 @@
 
 #include "api_checks.h"
 #include "kv4.cuh"
+#include "kv8.cuh"
 #include "ops.h"
 
 using namespace fa;
@@ -124,9 +125,11 @@ fa_status qk_in_place(const void* x, const void* y, const long long* sx, const l
   return FA_OK;
 }
 
-// ------------------------------------------------------- 4-bit cache
+// ------------------------------------------------------- 4-bit and 8-bit cache
 
-fa_status cache_check(const fa_kv4_cache* c) {
+int block_bytes(int bits, int d) { return bits == 4 ? fa_kv4_block_bytes(d) : fa_kv8_block_bytes(d); }
+
+fa_status cache_check(const fa_kv4_cache* c, int bits) {
   if (!c) return fail(FA_ERR_INVALID, "cache description is NULL");
   if (c->d != 64 && c->d != 128) return fail(FA_ERR_UNSUPPORTED, "head size %d is not supported (64 or 128)", c->d);
   if (c->num_pages < 1 || c->Hk < 1) return fail(FA_ERR_INVALID, "num_pages and Hk must be >= 1");
@@ -134,7 +137,7 @@ fa_status cache_check(const fa_kv4_cache* c) {
     return fail(FA_ERR_UNSUPPORTED, "page_size %d must be a power of two from 16 to 4096", c->page_size);
   if ((long long)c->num_pages * c->page_size > 0x7FFFFFFFll)
     return fail(FA_ERR_UNSUPPORTED, "num_pages * page_size exceeds 2^31 - 1 slots");
-  const long long page = (long long)c->Hk * (c->page_size / 16) * fa_kv4_block_bytes(c->d);
+  const long long page = (long long)c->Hk * (c->page_size / 16) * block_bytes(bits, c->d);
   if (page > 0x7FFFFFFFll) return fail(FA_ERR_UNSUPPORTED, "a page of %lld bytes exceeds 2^31 - 1", page);
   if (c->page_stride < page || c->page_stride % 16 != 0)
     return fail(FA_ERR_INVALID, "page_stride %lld must be a multiple of 16, at least %lld", c->page_stride, page);
@@ -152,9 +155,9 @@ Kv4Cache cache_args(const fa_kv4_cache* c, const void* data) {
   return k;
 }
 
-fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* k, const void* v, const int* slots,
-                        const void* cache, bool gather, void* stream) {
-  FA_TRY(cache_check(c));
+fa_status rows_call(int bits, const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* k, const void* v,
+                    const int* slots, const void* cache, bool gather, void* stream) {
+  FA_TRY(cache_check(c, bits));
   if (!rows) return fail(FA_ERR_INVALID, "rows is NULL");
   if (rows->T < 0) return fail(FA_ERR_INVALID, "T is negative");
   if ((long long)rows->T * c->Hk >= (1ll << 30)) return fail(FA_ERR_UNSUPPORTED, "T*Hk exceeds 2^30 - 1");
@@ -173,7 +176,8 @@ fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
   }
   FA_TRY(need(cache, 16, "cache"));
   Report rep;
-  FA_TRY(api_device(&rep, nullptr));
+  int sms = 0;
+  FA_TRY(api_device(&rep, &sms));
   if (rows->T == 0) return FA_OK;
   Kv4RowArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -189,13 +193,15 @@ fa_status kv4_rows_call(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
   }
   a.st = rep.st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = gather ? launch_kv4_gather(a, c->d, rows->dtype, s) : launch_kv4_append(a, c->d, rows->dtype, s);
+  const cudaError_t e = bits == 4 ? (gather ? launch_kv4_gather(a, c->d, rows->dtype, s) : launch_kv4_append(a, c->d, rows->dtype, s))
+                        : gather  ? launch_kv8_gather(a, c->d, rows->dtype, s)
+                                  : launch_kv8_append(a, c->d, rows->dtype, sms, s);
   if (e != cudaSuccess) return api_cuda_fail(e, gather ? "cache gather launch" : "cache append launch");
   return FA_OK;
 }
 
-fa_status attn_check(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
-  FA_TRY(cache_check(c));
+fa_status attn_check(int bits, const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
+  FA_TRY(cache_check(c, bits));
   if (!p) return fail(FA_ERR_INVALID, "params is NULL");
   if (p->dtype != FA_F16 && p->dtype != FA_BF16)
     return fail(p->dtype == FA_F32 ? FA_ERR_UNSUPPORTED : FA_ERR_INVALID, "the cache's attention takes fp16 or bf16 queries");
@@ -225,14 +231,16 @@ long long kv4_tiles(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows
 }
 
 // How many clusters of 1 << log CTAs the current device `dev` holds at once, asked for once.
-long long kv4_clusters(int dev, int d, int rows, int log) {
+long long kv4_clusters(int dev, int bits, int d, int rows, int log) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][2][3][5];  // number + 1
+  static std::atomic<int> known[kDevices][2][2][3][5];  // number + 1
   if (dev < 0 || dev >= kDevices) return 0;
-  std::atomic<int>& k = known[dev][d == 128][rows == 8 ? 0 : rows == 16 ? 1 : 2][log];
+  std::atomic<int>& k = known[dev][bits == 8][d == 128][rows == 8 ? 0 : rows == 16 ? 1 : 2][log];
   int n = k.load(std::memory_order_relaxed);
   if (n == 0) {
-    n = 1 + (d == 64 ? kv4_clusters_at_once<64>(rows, 1 << log) : kv4_clusters_at_once<128>(rows, 1 << log));
+    const int size = 1 << log;
+    n = 1 + (bits == 4 ? (d == 64 ? kv_clusters_at_once<KvBlock<64>>(rows, size) : kv_clusters_at_once<KvBlock<128>>(rows, size))
+                       : (d == 64 ? kv_clusters_at_once<Kv8Block<64>>(rows, size) : kv_clusters_at_once<Kv8Block<128>>(rows, size)));
     k.store(n, std::memory_order_relaxed);
   }
   return n - 1;
@@ -246,14 +254,14 @@ long long kv4_clusters(int dev, int d, int rows, int log) {
 // 14.9 and 14.7 (6 and 4), of 49152 22.4 and 19.4 (12 and 8); d = 128, 8 tiles of 4096
 // tokens 10.5 and 11.1 us (1 and 1), of 8192 12.5 and 12.2 (2 and 1), of 16384 16.6 and 14.4
 // (4 and 2).
-int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int share_ctas) {
+int kv4_cluster(int bits, const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int share_ctas) {
   const long long tiles = kv4_tiles(c, p, rows);
   long long tokens = (long long)p->table_width * c->page_size;
   if (p->window > 0) tokens = std::min(tokens, (long long)p->window + p->max_q_len + 31);
   const long long units = (tokens + 31) / 32;
   int dev = 0, log = 4;
   if (tiles > 2 * kMaxSms || cudaGetDevice(&dev) != cudaSuccess) return 0;
-  while (tiles > kv4_clusters(dev, c->d, rows, log))
+  while (tiles > kv4_clusters(dev, bits, c->d, rows, log))
     if (--log < 0) return 0;
   const int cluster = 1 << log;
   const long long mine = (units + 8 * cluster - 1) / (8 * cluster);
@@ -262,6 +270,73 @@ int kv4_cluster(const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, in
 }
 
 size_t attn_part_bytes(int ctas, int rows, int d) { return align256((size_t)2 * ctas * rows * (d + 4) * 4); }
+
+size_t attn_workspace(int bits, const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
+  if (attn_check(bits, c, p) != FA_OK) return 0;
+  const int rows = kv4_tile_rows(p->Hq / c->Hk, p->max_q_len);
+  const int ctas = kv_share_ctas(bits, rows, kMaxSms);
+  return attn_part_bytes(ctas, rows, c->d) + align256((size_t)ctas * 32);
+}
+
+fa_status attn_call(int bits, const fa_kv4_cache* c, const fa_kv4_attn_params* p, const void* q, const void* cache,
+                    const int* block_table, const int* kv_lens, const int* cu_q, void* o, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  FA_TRY(attn_check(bits, c, p));
+  if (p->T > 0) {
+    FA_TRY(need(q, 16, "q"));
+    FA_TRY(need(o, 16, "o"));
+  }
+  FA_TRY(need(cache, 16, "cache"));
+  FA_TRY(need(block_table, 4, "block_table"));
+  FA_TRY(need(kv_lens, 4, "kv_lens"));
+  if (cu_q && !aligned(cu_q, 4)) return fail(FA_ERR_INVALID, "cu_q is not 4-byte aligned");
+  if (lse && !aligned(lse, 4)) return fail(FA_ERR_INVALID, "lse is not 4-byte aligned");
+  const size_t want = attn_workspace(bits, c, p);
+  if (!workspace || workspace_bytes < want || !aligned(workspace, 256))
+    return fail(FA_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", workspace,
+                workspace_bytes, want);
+  // shares read a request's queries when another has already written its rows
+  if (p->T > 0 && o == q) return fail(FA_ERR_INVALID, "o lies over q");
+  Report rep;
+  int sms = 0;
+  FA_TRY(api_device(&rep, &sms));
+  if (p->T == 0) return FA_OK;
+  Kv4AttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.c = cache_args(c, cache);
+  a.R = p->R;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.G = FastDiv::of((uint32_t)(p->Hq / c->Hk));
+  a.window = p->window;
+  a.table_width = p->table_width;
+  a.table_stride = p->table_stride;
+  a.table = block_table;
+  a.kv_lens = kv_lens;
+  a.cu_q = cu_q;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.q = q;
+  a.o = o;
+  std::memcpy(a.qs, p->q_stride, sizeof(a.qs));
+  std::memcpy(a.os, p->o_stride, sizeof(a.os));
+  a.lse = lse;
+  const int rows = kv4_tile_rows((int)a.G.d, p->max_q_len);
+  int ctas = kv_share_ctas(bits, rows, std::min(sms, kMaxSms));
+  a.part = static_cast<float*>(workspace);
+  a.meta = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attn_part_bytes(ctas, rows, c->d));
+  const int cluster = kv4_cluster(bits, c, p, rows, ctas);
+  if (cluster > 0) ctas = (int)std::min<long long>(kv4_tiles(c, p, rows), (1 << 20)) * cluster;
+  a.rep = rep;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f16 = p->dtype == FA_F16;
+  const cudaError_t e =
+      bits == 4 ? (c->d == 64 ? launch_kv_attention<KvBlock<64>>(a, f16, rows, ctas, cluster, st)
+                              : launch_kv_attention<KvBlock<128>>(a, f16, rows, ctas, cluster, st))
+                : (c->d == 64 ? launch_kv_attention<Kv8Block<64>>(a, f16, rows, ctas, cluster, st)
+                              : launch_kv_attention<Kv8Block<128>>(a, f16, rows, ctas, cluster, st));
+  if (e != cudaSuccess) return api_cuda_fail(e, "cache attention launch");
+  return FA_OK;
+}
 
 }  // namespace
 
@@ -343,78 +418,49 @@ int fa_kv4_block_bytes(int d) { return d == 128 ? KvBlock<128>::bytes : d == 64 
 fa_status fa_kv4_append(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* k, const void* v, const int* slots,
                         void* cache, void* stream) {
   NvtxRange nvtx_range("fa_kv4_append");
-  return kv4_rows_call(c, rows, k, v, slots, cache, false, stream);
+  return rows_call(4, c, rows, k, v, slots, cache, false, stream);
 }
 
 fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const void* cache, const int* slots, void* k,
                         void* v, void* stream) {
   NvtxRange nvtx_range("fa_kv4_gather");
-  return kv4_rows_call(c, rows, k, v, slots, cache, true, stream);
+  return rows_call(4, c, rows, k, v, slots, cache, true, stream);
 }
 
 size_t fa_kv4_attention_workspace_size(const fa_kv4_cache* c, const fa_kv4_attn_params* p) {
-  if (attn_check(c, p) != FA_OK) return 0;
-  const int rows = kv4_tile_rows(p->Hq / c->Hk, p->max_q_len);
-  const int ctas = kv4_share_ctas(rows, kMaxSms);
-  return attn_part_bytes(ctas, rows, c->d) + align256((size_t)ctas * 32);
+  return attn_workspace(4, c, p);
 }
 
 fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, const void* q, const void* cache,
                            const int* block_table, const int* kv_lens, const int* cu_q, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream) {
   NvtxRange nvtx_range("fa_kv4_attention");
-  FA_TRY(attn_check(c, p));
-  if (p->T > 0) {
-    FA_TRY(need(q, 16, "q"));
-    FA_TRY(need(o, 16, "o"));
-  }
-  FA_TRY(need(cache, 16, "cache"));
-  FA_TRY(need(block_table, 4, "block_table"));
-  FA_TRY(need(kv_lens, 4, "kv_lens"));
-  if (cu_q && !aligned(cu_q, 4)) return fail(FA_ERR_INVALID, "cu_q is not 4-byte aligned");
-  if (lse && !aligned(lse, 4)) return fail(FA_ERR_INVALID, "lse is not 4-byte aligned");
-  const size_t want = fa_kv4_attention_workspace_size(c, p);
-  if (!workspace || workspace_bytes < want || !aligned(workspace, 256))
-    return fail(FA_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", workspace,
-                workspace_bytes, want);
-  // shares read a request's queries when another has already written its rows
-  if (p->T > 0 && o == q) return fail(FA_ERR_INVALID, "o lies over q");
-  Report rep;
-  int sms = 0;
-  FA_TRY(api_device(&rep, &sms));
-  if (p->T == 0) return FA_OK;
-  Kv4AttnArgs a;
-  std::memset(&a, 0, sizeof(a));
-  a.c = cache_args(c, cache);
-  a.R = p->R;
-  a.T = p->T;
-  a.Hq = p->Hq;
-  a.G = FastDiv::of((uint32_t)(p->Hq / c->Hk));
-  a.window = p->window;
-  a.table_width = p->table_width;
-  a.table_stride = p->table_stride;
-  a.table = block_table;
-  a.kv_lens = kv_lens;
-  a.cu_q = cu_q;
-  a.scale_log2 = p->scale * 1.4426950408889634f;
-  a.q = q;
-  a.o = o;
-  std::memcpy(a.qs, p->q_stride, sizeof(a.qs));
-  std::memcpy(a.os, p->o_stride, sizeof(a.os));
-  a.lse = lse;
-  const int rows = kv4_tile_rows((int)a.G.d, p->max_q_len);
-  int ctas = kv4_share_ctas(rows, std::min(sms, kMaxSms));
-  a.part = static_cast<float*>(workspace);
-  a.meta = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attn_part_bytes(ctas, rows, c->d));
-  const int cluster = kv4_cluster(c, p, rows, ctas);
-  if (cluster > 0) ctas = (int)std::min<long long>(kv4_tiles(c, p, rows), (1 << 20)) * cluster;
-  a.rep = rep;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool f16 = p->dtype == FA_F16;
-  const cudaError_t e = c->d == 64 ? launch_kv4_attention_d<64>(a, f16, rows, ctas, cluster, st)
-                                   : launch_kv4_attention_d<128>(a, f16, rows, ctas, cluster, st);
-  if (e != cudaSuccess) return api_cuda_fail(e, "cache attention launch");
-  return FA_OK;
+  return attn_call(4, c, p, q, cache, block_table, kv_lens, cu_q, o, lse, workspace, workspace_bytes, stream);
+}
+
+int fa_kv8_block_bytes(int d) { return d == 128 ? Kv8Block<128>::bytes : d == 64 ? Kv8Block<64>::bytes : 0; }
+
+fa_status fa_kv8_append(const fa_kv8_cache* c, const fa_kv8_rows* rows, const void* k, const void* v, const int* slots,
+                        void* cache, void* stream) {
+  NvtxRange nvtx_range("fa_kv8_append");
+  return rows_call(8, c, rows, k, v, slots, cache, false, stream);
+}
+
+fa_status fa_kv8_gather(const fa_kv8_cache* c, const fa_kv8_rows* rows, const void* cache, const int* slots, void* k,
+                        void* v, void* stream) {
+  NvtxRange nvtx_range("fa_kv8_gather");
+  return rows_call(8, c, rows, k, v, slots, cache, true, stream);
+}
+
+size_t fa_kv8_attention_workspace_size(const fa_kv8_cache* c, const fa_kv8_attn_params* p) {
+  return attn_workspace(8, c, p);
+}
+
+fa_status fa_kv8_attention(const fa_kv8_cache* c, const fa_kv8_attn_params* p, const void* q, const void* cache,
+                           const int* block_table, const int* kv_lens, const int* cu_q, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("fa_kv8_attention");
+  return attn_call(8, c, p, q, cache, block_table, kv_lens, cu_q, o, lse, workspace, workspace_bytes, stream);
 }
 
 fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int* new_lens, int* block_table,

@@ -48,9 +48,9 @@ _CODES = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}
 # with the extension (csrc/launch.cpp) that repeats the call: a call on sixteen tokens
 # takes the GPU a few microseconds, the checks would take several times that.
 
-_QK, _QK_BWD, _APPEND, _GATHER, _ATTENTION, _PLAN, _PACKED, _PACKED_BWD = range(8)
+_QK, _QK_BWD, _APPEND, _GATHER, _ATTENTION, _PLAN, _PACKED, _PACKED_BWD, _APPEND8, _GATHER8, _ATTENTION8 = range(11)
 _ENTRY = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attention", "fa_paged_plan",
-          "fa_fwd_packed", "fa_bwd_packed")
+          "fa_fwd_packed", "fa_bwd_packed", "fa_kv8_append", "fa_kv8_gather", "fa_kv8_attention")
 _STREAM = (3, 0)
 _launch = None  # the extension, from the first call on
 
@@ -261,24 +261,41 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq, wk, freqs, positions=None, eps: float =
                  (float(eps), bool(interleaved), bool(heads_first)), stream, _plan_qk_bwd)
 
 
-# ---------------------------------------------------------------- the 4-bit cache
+# ---------------------------------------------------------------- the 4-bit and the 8-bit cache
 
 def kv4_block_bytes(d: int) -> int:
     """Bytes of a 16-token block of one head (``fa_kv4_block_bytes``)."""
     return int(load().fa_kv4_block_bytes(int(d)))
 
 
-def kv4_cache(num_pages: int, heads: int, d: int, page_size: int = 64, device="cuda"):
-    """A zeroed cache: uint8 [num_pages, heads, page_size / 16, kv4_block_bytes(d)]."""
+def kv8_block_bytes(d: int) -> int:
+    """Bytes of a 16-token block of one head of the 8-bit cache (``fa_kv8_block_bytes``)."""
+    return int(load().fa_kv8_block_bytes(int(d)))
+
+
+def _new_cache(block_bytes, num_pages, heads, d, page_size, device):
     if d not in (64, 128):
         raise ValueError("head size must be 64 or 128")
     if page_size < 16 or page_size > 4096 or page_size & (page_size - 1):
         raise ValueError("page_size must be a power of two from 16 to 4096")
-    return torch.zeros((num_pages, heads, page_size // KV4_BLOCK, kv4_block_bytes(d)), dtype=torch.uint8, device=device)
+    return torch.zeros((num_pages, heads, page_size // KV4_BLOCK, block_bytes(d)), dtype=torch.uint8, device=device)
 
 
-def _cache_params(cache, d: int) -> FaKv4Cache:
-    _need(cache, "cache", torch.uint8, (None, None, None, {64: 1280, 128: 2560}.get(d, -1)))
+def kv4_cache(num_pages: int, heads: int, d: int, page_size: int = 64, device="cuda"):
+    """A zeroed cache: uint8 [num_pages, heads, page_size / 16, kv4_block_bytes(d)]."""
+    return _new_cache(kv4_block_bytes, num_pages, heads, d, page_size, device)
+
+
+def kv8_cache(num_pages: int, heads: int, d: int, page_size: int = 64, device="cuda"):
+    """A zeroed cache of 8 bits a value: uint8 [num_pages, heads, page_size / 16, kv8_block_bytes(d)]."""
+    return _new_cache(kv8_block_bytes, num_pages, heads, d, page_size, device)
+
+
+_BLOCK_BYTES = {4: {64: 1280, 128: 2560}, 8: {64: 2064, 128: 4112}}
+
+
+def _cache_params(bits: int, cache, d: int) -> FaKv4Cache:
+    _need(cache, "cache", torch.uint8, (None, None, None, _BLOCK_BYTES[bits].get(d, -1)))
     P, H, n, b = cache.shape
     s = cache.stride()
     if s[3] != 1 or (n > 1 and s[2] != b) or (H > 1 and s[1] != n * b):
@@ -286,9 +303,9 @@ def _cache_params(cache, d: int) -> FaKv4Cache:
     return FaKv4Cache(P, KV4_BLOCK * n, H, d, s[0] if P > 1 else H * n * b)
 
 
-def _rows_checked(cache, slots, k, v, T, H, d, dtype, heads_first, names):
+def _rows_checked(bits, cache, slots, k, v, T, H, d, dtype, heads_first, names):
     """(cache parameters, row parameters, device)."""
-    c = _cache_params(cache, d)
+    c = _cache_params(bits, cache, d)
     if cache.shape[1] != H:
         raise ValueError(f"{names[0]} has {H} heads, the cache {cache.shape[1]}")
     _need(slots, "slots", torch.int32, (T,))
@@ -304,22 +321,22 @@ def _rows_checked(cache, slots, k, v, T, H, d, dtype, heads_first, names):
     return c, rows, _one_device(cache, slots, k, v)
 
 
-def _plan_append(k, v, slots, cache):
+def _plan_append(k, v, slots, cache, bits):
     if k.dtype not in _CODES:
         raise TypeError(f"unsupported dtype {k.dtype}")
     _need(k, "k", k.dtype, (None, None, None))
     T, H, d = k.shape
-    c, rows, device = _rows_checked(cache, slots, k, v, T, H, d, k.dtype, False, ("k", "v"))
+    c, rows, device = _rows_checked(bits, cache, slots, k, v, T, H, d, k.dtype, False, ("k", "v"))
     return device, [_const(c), _const(rows), *map(_in, range(4)), _STREAM], (), (), (c, rows)
 
 
-def _plan_gather(cache, slots, k, v, d, dtype, heads_first):
+def _plan_gather(cache, slots, k, v, d, dtype, heads_first, bits):
     if dtype not in _CODES:
         raise TypeError(f"unsupported dtype {dtype}")
     _need(cache, "cache", torch.uint8, (None, None, None, None))
     _need(slots, "slots", torch.int32, (None,))
     T, H = slots.shape[0], cache.shape[1]
-    c, rows, device = _rows_checked(cache, slots, k, v, T, H, d, dtype, heads_first, ("out[0]", "out[1]"))
+    c, rows, device = _rows_checked(bits, cache, slots, k, v, T, H, d, dtype, heads_first, ("out[0]", "out[1]"))
     new, shape = _Outputs(), (H, T, d) if heads_first else (T, H, d)
     res = [new.given(2, k, shape, dtype), new.given(3, v, shape, dtype)]
     return device, [_const(c), _const(rows), _in(0), _in(1), *res, _STREAM], new, res, (c, rows)
@@ -328,7 +345,14 @@ def _plan_gather(cache, slots, k, v, d, dtype, heads_first):
 def kv4_append(k, v, slots, cache, stream=None) -> None:
     """Quantise the keys and values [T, Hk, d] of T tokens into their slots (int32 [T];
     negative: left out; distinct otherwise) of the cache.  Values saturate at +-16384."""
-    _call(_APPEND, (k, v, slots, cache), (), stream, _plan_append)
+    _call(_APPEND, (k, v, slots, cache), (4,), stream, _plan_append)
+
+
+def kv8_append(k, v, slots, cache, stream=None) -> None:
+    """The same into a cache of 8 bits, whose blocks of 16 tokens of a head have one scale: new
+    tokens may raise it, and the codes that are there are rounded to it.  The tokens of one block
+    must be neighbours in the call; a block whose first token is among them begins anew."""
+    _call(_APPEND8, (k, v, slots, cache), (8,), stream, _plan_append)
 
 
 def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = False, out=None, stream=None):
@@ -336,15 +360,22 @@ def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = F
     ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d]; with a leading batch of one
     ``attention_fwd`` takes these for the T queries of the same tokens and Hq = Hk."""
     k, v = (None, None) if out is None else out
-    return _call(_GATHER, (cache, slots, k, v), (int(d), dtype, bool(heads_first)), stream, _plan_gather)
+    return _call(_GATHER, (cache, slots, k, v), (int(d), dtype, bool(heads_first), 4), stream, _plan_gather)
 
 
-def _plan_attention(q, cache, block_table, kv_lens, cu_q, out, lse, workspace, max_q_len, scale, window):
+def kv8_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = False, out=None, stream=None):
+    """(k, v): the values that T slots of an 8-bit cache hold, as ``kv4_gather``; as [T, Hk, d]
+    ``attention_fwd_packed`` takes them, for new rows over a cached prefix."""
+    k, v = (None, None) if out is None else out
+    return _call(_GATHER8, (cache, slots, k, v), (int(d), dtype, bool(heads_first), 8), stream, _plan_gather)
+
+
+def _plan_attention(q, cache, block_table, kv_lens, cu_q, out, lse, workspace, max_q_len, scale, window, bits):
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be fp16 or bf16, not {q.dtype}")
     _need(q, "q", q.dtype, (None, None, None))
     T, Hq, d = q.shape
-    c = _cache_params(cache, d)
+    c = _cache_params(bits, cache, d)
     _need(block_table, "block_table", torch.int32, (None, None))
     R, width = block_table.shape
     if width > 1 and block_table.stride(1) != 1:
@@ -369,7 +400,8 @@ def _plan_attention(q, cache, block_table, kv_lens, cu_q, out, lse, workspace, m
                         block_table.stride(0) if R > 1 else width, I64x2(*_strides(q, "q", (0, 1))), I64x2(*o_stride))
     new = _Outputs()
     res = [new.given(5, out, (T, Hq, d), q.dtype), new.given(6, lse, (T, Hq), torch.float32)]
-    ws, nbytes = _workspace(new, 7, workspace, load().fa_kv4_attention_workspace_size(ctypes.byref(c), ctypes.byref(p)), device)
+    size = load().fa_kv4_attention_workspace_size if bits == 4 else load().fa_kv8_attention_workspace_size
+    ws, nbytes = _workspace(new, 7, workspace, size(ctypes.byref(c), ctypes.byref(p)), device)
     return device, [_const(c), _const(p), *map(_in, range(5)), *res, ws, _const(nbytes), _STREAM], new, res, (c, p)
 
 
@@ -383,7 +415,14 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1,
     rows outside every request are not written.  ``max_q_len``: the most rows of a request,
     a hint.  Lengths stay on the GPU: the call does not synchronise."""
     return _call(_ATTENTION, (q, cache, block_table, kv_lens, cu_q, out, lse, workspace),
-                 (int(max_q_len), None if scale is None else float(scale), int(window)), stream, _plan_attention)
+                 (int(max_q_len), None if scale is None else float(scale), int(window), 4), stream, _plan_attention)
+
+
+def kv8_attention(q, cache, block_table, kv_lens, cu_q=None, max_q_len: int = 1, scale: Optional[float] = None,
+                  window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """(o, lse): ``kv4_attention`` over a cache of 8 bits."""
+    return _call(_ATTENTION8, (q, cache, block_table, kv_lens, cu_q, out, lse, workspace),
+                 (int(max_q_len), None if scale is None else float(scale), int(window), 8), stream, _plan_attention)
 
 
 # ---------------------------------------------------------------- block tables and slot maps

@@ -479,6 +479,44 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
                            const int* cu_q, void* o, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The same in 8 bits: codes of a signed byte with one scale for each block of 16 tokens
+ * of a head (one for its keys, one for its values).  Pages, slots, block tables, rows and
+ * requests are as above.  A block (fa_kv8_block_bytes(d) bytes: 32 d + 16) is
+ *     int8   keys    [16][d]              at d = 128 the 64-byte halves of odd tokens' rows
+ *                                         are in each other's place
+ *     int8   values  [d / 4][4][4][4]     channel c of token j at [c/4][j/4][c%4][j%4]
+ *     float  scale of the keys, scale of the values
+ *     uint16 marks of the keys, of the values: bit j set where token j's hold a NaN
+ *     4 bytes of 0
+ * and a value is its code times its scale, or NaN where its token is marked.
+ *
+ * fa_kv8_append: of each side, the scale of a block is the least power of two (at least
+ * 2^-64) with max|x| <= 127 * scale over its tokens' values x, saturated at +-16384, or 0
+ * where they are all 0; a code is rint(x / scale).  A block whose place 0 is among the
+ * call's slots begins anew: what it held counts no more.  Other blocks keep their tokens:
+ * where the new ones need a larger scale, the codes of the others become
+ * rint(code * old / new).  A token with a NaN is marked and its codes of that side are 0.
+ * The tokens of one block must be neighbours in the call (as fa_paged_plan puts them);
+ * slots >= 0 must be distinct.  Where they are not, those blocks' contents are void.
+ * fa_kv8_attention: a key's mark makes O and LSE of the rows that see it NaN, a value's
+ * mark their O.
+ * ------------------------------------------------------------------------ */
+typedef fa_kv4_cache fa_kv8_cache;
+typedef fa_kv4_rows fa_kv8_rows;
+typedef fa_kv4_attn_params fa_kv8_attn_params;
+
+int fa_kv8_block_bytes(int d);
+fa_status fa_kv8_append(const fa_kv8_cache* c, const fa_kv8_rows* rows, const void* k,
+                        const void* v, const int* slots, void* cache, void* stream);
+fa_status fa_kv8_gather(const fa_kv8_cache* c, const fa_kv8_rows* rows, const void* cache,
+                        const int* slots, void* k, void* v, void* stream);
+size_t fa_kv8_attention_workspace_size(const fa_kv8_cache* c, const fa_kv8_attn_params* p);
+fa_status fa_kv8_attention(const fa_kv8_cache* c, const fa_kv8_attn_params* p, const void* q,
+                           const void* cache, const int* block_table, const int* kv_lens,
+                           const int* cu_q, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /*
  * Block tables and slot maps of one step, from R request lengths, on the GPU.
  * Request r holds seq_lens[r] tokens in the first ceil(seq_lens[r] / page_size)
