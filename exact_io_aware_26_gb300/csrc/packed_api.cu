@@ -15,7 +15,7 @@ constexpr int kMostGroup = 128;  // query heads of a key head: a tile's rows
 // CTAs that the steps are shared among, for each SM, and the steps of a slice at least: below
 // that a part's fp32 result costs more than the steps it takes off the others.
 constexpr int kFwdCtas = 2, kBwdCtas = 1;
-constexpr long long kFwdLeast = 4, kBwdLeast = 2;
+constexpr int kFwdLeast = 4, kBwdLeast = 2;
 
 fa_status check(const fa_packed_params* p, bool bwd) {
   if (!p) return fail(FA_ERR_INVALID, "params is NULL");
@@ -54,8 +54,7 @@ fa_status check(const fa_packed_params* p, bool bwd) {
 
 // The sizes of a call's work list and where it lies in the workspace.
 struct Sizes {
-  int tpt, target, slots, items, cuts;
-  long long least;
+  int tpt, target, least, slots, items, cuts;
   size_t head, items_at, cuts_at, starts_at, slots_at, stat_at, acc_at, bytes;
   Sizes(const fa_packed_params* p, int sms, bool bwd) {
     const int G = p->Hq / p->Hk;
@@ -145,7 +144,8 @@ PackedPlanArgs plan_args(const PackedArgs& a, const Sizes& z, const int* cu_q, c
   q.causal = a.causal;
   q.bwd = bwd;
   q.target = z.target;
-  q.least = z.slots > 0 ? z.least : 1ll << 40;
+  q.cuttable = z.slots > 0;
+  q.least = z.least;
   q.cu_q = cu_q;
   q.cu_k = cu_k;
   q.list = a.list;

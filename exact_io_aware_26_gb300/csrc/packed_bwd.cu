@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       const int token = x.seq.k0 + kt * kTile + r;
       const bool store = r < keys && dbg_check(w, token < a.Tk);
       float* part = x.slot < 0 ? nullptr
-                               : a.slots + ((long long)x.slot * a.Hk + hk) * (2 * kTile * D) + (long long)r * D + g * L::DQG;
+                               : a.slots + ((long long)x.slot * a.Hk + hk) * (2 * kTile * D) + 4 * (g * L::DQG / 4 * kTile + r);
       constexpr int EC = L::DQG < 32 ? L::DQG : 32;
       for (int which = 0; which < 2; ++which) {
         const uint32_t col = (which == 0 ? L::T_DV : L::T_DK) + g * L::DQG;
@@ -581,10 +581,10 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
 #pragma unroll
             for (int k = 0; k < EC; ++k) u[k] = 0u;
           }
-          if (part) {
+          if (part) {  // four channels of all keys side by side: a warp's stores are whole lines
 #pragma unroll
             for (int v = 0; v < EC / 4; ++v)
-              *reinterpret_cast<uint4*>(part + (long long)which * (kTile * D) + c0 + 4 * v) =
+              *reinterpret_cast<uint4*>(part + which * (kTile * D) + 4 * kTile * (c0 / 4 + v)) =
                   make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
           } else if (store) {
 #pragma unroll
@@ -675,25 +675,28 @@ __global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, 
   const int cut = a.divHk.div(unit), hk = unit - cut * a.Hk;
   if (cut >= a.list.head[1]) return;
   const PackedItem x = a.list.cuts[cut];
-  constexpr int PER = 2 * kTile * D / 4, PART = PER / kSumParts;  // float4 of a slot, of a block
-  const float4* base = reinterpret_cast<const float4*>(a.slots) + ((size_t)x.s0 * a.Hk + hk) * PER;
+  // eight channels of a key a thread, keys side by side
+  constexpr int PER = 2 * kTile * D / 8, PART = PER / kSumParts;
+  constexpr size_t words = 2 * kTile * D;
+  const float* base = a.slots + ((size_t)x.s0 * a.Hk + hk) * words;
   const int keys = min(kTile, x.seq.m - x.tile * kTile);
   for (int e = part * PART + (int)threadIdx.x; e < (part + 1) * PART; e += blockDim.x) {
-    const int f = e * 4, which = f / (kTile * D), row = f / D % kTile, col = f % D;
+    const int row = e % kTile, pair = e / kTile, which = pair / (D / 8), col = pair % (D / 8) * 8;
     if (row >= keys) continue;
-    float4 acc = base[e];
-    for (int s = 1; s < x.s1; ++s) {
-      const float4 v = base[(size_t)s * a.Hk * PER + e];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+    float acc[8] = {};
+#pragma unroll 2
+    for (int s = 0; s < x.s1; ++s) {
+      const float4* from = reinterpret_cast<const float4*>(base + (size_t)s * a.Hk * words) + 2 * pair * kTile + row;
+      const float4 u = from[0], v = from[kTile];
+      acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;
+      acc[4] += v.x; acc[5] += v.y; acc[6] += v.z; acc[7] += v.w;
     }
     const float mul = which == 0 ? 1.f : a.scale;
     const long long* st = which == 0 ? a.dvs : a.dks;
     uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) +
                     (long long)(x.seq.k0 + x.tile * kTile + row) * st[0] + hk * st[1] + col;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(acc.x * mul, acc.y * mul), pack2<F16>(acc.z * mul, acc.w * mul));
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<F16>(acc[0] * mul, acc[1] * mul), pack2<F16>(acc[2] * mul, acc[3] * mul),
+                                                pack2<F16>(acc[4] * mul, acc[5] * mul), pack2<F16>(acc[6] * mul, acc[7] * mul));
   }
 }
 

@@ -357,10 +357,11 @@ __global__ void __launch_bounds__(192, 2)
             *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q;
           }
         } else if (!whole) {
-          float* to = part + 2 * kTile + (size_t)r * D + c0;
+          // four channels of all rows side by side: a warp's stores are whole lines
+          float* to = part + 2 * kTile + 4 * (c0 / 4 * kTile + r);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<uint4*>(to + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            *reinterpret_cast<uint4*>(to + 4 * kTile * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
         }
         __syncwarp();
       }
@@ -376,8 +377,9 @@ __global__ void __launch_bounds__(192, 2)
 }
 
 // Joins the parts of the units that were cut: with M = max m_s, L = sum l_s 2^((m_s - M) c2),
-// O = sum O_s 2^((m_s - M) c2) / L.  D / 4 threads a row, four blocks for a unit and key head.
-constexpr int kJoinParts = 4;
+// O = sum O_s 2^((m_s - M) c2) / L.  A block has 32 rows of a unit and key head, a thread an eighth of
+// a row; four parts are on their way together.
+constexpr int kJoinRows = 32;
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) packed_join_kernel(const PackedArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -385,36 +387,65 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const PackedArgs a) {
   if (cut >= a.list.head[1]) return;
   const PackedItem x = a.list.cuts[cut];
   const int t0 = x.tile * a.tpt, rows = min(a.tpt, x.seq.n - t0) * a.G;
-  constexpr int TPR = D / 4, PER = 256 / TPR;
-  const int c = (int)threadIdx.x % TPR;
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  if (r >= rows) return;
+  constexpr int NC = D / 32, AT_ONCE = 4;  // float4 of a thread
   constexpr size_t words = kTile * (D + 2);
   const size_t step = words * a.Hk;
   const float* base = a.slots + ((size_t)x.s0 * a.Hk + hk) * words;
-  for (int r = blockIdx.y * PER + (int)threadIdx.x / TPR; r < rows; r += kJoinParts * PER) {
-    float top = -INFINITY;
-    for (int s = 0; s < x.s1; ++s) {
-      const float2 ml = *reinterpret_cast<const float2*>(base + s * step + 2 * r);
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  float top = -INFINITY, sum = 0.f, acc[NC][4] = {};
+#pragma unroll 1
+  for (int s0 = 0; s0 < x.s1; s0 += AT_ONCE) {
+    float2 ml[AT_ONCE];
+    float4 o[AT_ONCE][NC];
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + k < x.s1) {
+        const float* from = base + (s0 + k) * step;
+        ml[k] = *reinterpret_cast<const float2*>(from + 2 * r);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          o[k][c] = *reinterpret_cast<const float4*>(from + 2 * kTile + 4 * ((part * NC + c) * kTile + r));
+      }
     }
-    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < x.s1; ++s) {
-      const float2 ml = *reinterpret_cast<const float2*>(base + s * step + 2 * r);
-      if (ml.y == 0.f) continue;  // saw no key
-      const float f = ml.x == top ? 1.f : ex2((ml.x - top) * a.scale_log2);
-      const float4 o = *reinterpret_cast<const float4*>(base + s * step + 2 * kTile + (size_t)r * D + 4 * c);
-      sum = fmaf(f, ml.y, sum);
-      acc[0] = fmaf(f, o.x, acc[0]);
-      acc[1] = fmaf(f, o.y, acc[1]);
-      acc[2] = fmaf(f, o.z, acc[2]);
-      acc[3] = fmaf(f, o.w, acc[3]);
+    float t = top;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k)
+      if (ml[k].y != 0.f) t = fmaxf(t, ml[k].x);  // a part that saw no key weighs nothing
+    const float back = top == t ? 1.f : ex2((top - t) * a.scale_log2);
+    top = t;
+    sum *= back;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[c][i] *= back;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      if (ml[k].y == 0.f) continue;
+      const float f = ml[k].x == top ? 1.f : ex2((ml[k].x - top) * a.scale_log2);
+      sum = fmaf(f, ml[k].y, sum);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        acc[c][0] = fmaf(f, o[k][c].x, acc[c][0]);
+        acc[c][1] = fmaf(f, o[k][c].y, acc[c][1]);
+        acc[c][2] = fmaf(f, o[k][c].z, acc[c][2]);
+        acc[c][3] = fmaf(f, o[k][c].w, acc[c][3]);
+      }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
-    if (!fa_bounds(a.rep.st, token < a.Tq && head < a.Hq)) continue;
-    uint16_t* to = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1] + 4 * c;
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
-    if (c == 0) a.lse[(long long)token * a.Hq + head] = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __logf(sum));
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
+  if (!fa_bounds(a.rep.st, token < a.Tq && head < a.Hq)) return;
+  uint16_t* to = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1] + 4 * NC * part;
+#pragma unroll
+  for (int c = 0; c < NC; c += 2)
+    *reinterpret_cast<uint4*>(to + 4 * c) =
+        make_uint4(pack2<F16>(acc[c][0] * inv, acc[c][1] * inv), pack2<F16>(acc[c][2] * inv, acc[c][3] * inv),
+                   pack2<F16>(acc[c + 1][0] * inv, acc[c + 1][1] * inv), pack2<F16>(acc[c + 1][2] * inv, acc[c + 1][3] * inv));
+  if (part == 0) a.lse[(long long)token * a.Hq + head] = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __logf(sum));
 }
 
 template <int D, bool F16>
@@ -435,7 +466,7 @@ cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, int 
   cfg.dynamicSmemBytes = L::BYTES;
   e = cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], a);
   if (e != cudaSuccess || cuts == 0) return e;
-  cfg.gridDim = dim3((unsigned)((long long)cuts * a.Hk), kJoinParts);
+  cfg.gridDim = dim3((unsigned)((long long)cuts * a.Hk), kTile / kJoinRows);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, packed_join_kernel<D, F16>, a);

@@ -5,47 +5,57 @@
 // slice is, and the slices in order of their steps, the longest first, by counting.  The main
 // kernel's CTAs take the list in order, so that what is left at the end is short.  Where in its
 // class of lengths an item stands, and which slots a cut unit has, is left to the order of
-// atomics: results do not depend on it.  Bound by latency: 3 us for a few sequences, of which the
-// main kernel's launch hides a part.
+// atomics: results do not depend on it.  Bound by latency, of which the main kernel's launch
+// hides a part.
 #include "packed.h"
 #include "ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32, kClasses = kThreads, kNear = 1024;
+constexpr int kThreads = 1024, kWarps = kThreads / 32, kClasses = kThreads, kNear = 1024, kWeighed = 4096;
+static_assert(kPackedCandidates == kWarps, "a warp weighs a candidate");
 
-// Inclusive scan of one value per thread over the CTA; `total` gets the last.
-template <class T, class Op>
-__device__ __forceinline__ T block_scan(T v, T* warp_s, T& total, Op op) {
+// Inclusive scans of N values per thread over the CTA; `total` gets the last.
+template <int N, class Op>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (*warp_s)[kWarps], int (&total)[N], Op op) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const T up = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v = op(up, v);
-  }
-  __syncthreads();  // warp_s read by a scan before
-  if (lane == 31) warp_s[warp] = v;
-  __syncthreads();
-  T w = warp_s[lane];
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const T up = __shfl_up_sync(0xffffffffu, w, off);
-    if (lane >= off) w = op(up, w);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, v[i], off);
+      if (lane >= off) v[i] = op(up, v[i]);
+    }
+    if (lane == 31) warp_s[i][warp] = v[i];
   }
-  total = __shfl_sync(0xffffffffu, w, 31);
-  const T before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-  return warp ? op(before, v) : v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int w = warp_s[i][lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w = op(up, w);
+    }
+    total[i] = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    if (warp) v[i] = op(before, v[i]);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // they wait for this grid's end
   __shared__ int near_s[3][kNear + 1];
-  __shared__ long long sum_s[kWarps];
-  __shared__ int scan_s[kWarps];
+  __shared__ int scan_s[4][kWarps];
+  __shared__ long long steps_s[kWarps];
+  __shared__ int longest_s[kWarps];
   __shared__ int class_s[kClasses];
+  __shared__ int work_s[kWeighed];
+  __shared__ float time_s[kWarps];
+  __shared__ int end_s[2][kThreads];
   __shared__ int slot_s, cut_s;
-  const int tid = threadIdx.x, R = a.R;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.R;
   int *first_q = a.list.starts, *first_k = first_q + R + 1, *first_u = first_k + R + 1;
   if (R <= kNear) {
     first_q = near_s[0];
@@ -59,17 +69,14 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   const int per = (R + kThreads) / kThreads, my0 = min(R + 1, tid * per), my1 = min(R + 1, my0 + per);
   auto offset = [&](const int* cu, int T, int r) { return min(max(__ldg(cu + r), 0), T); };
   auto larger = [](int x, int y) { return max(x, y); };
-  int most_q = 0, most_k = 0;
+  int most[2] = {0, 0}, last[2];
   for (int r = my0; r < my1; ++r) {
-    most_q = max(most_q, offset(a.cu_q, a.Tq, r));
-    most_k = max(most_k, offset(a.cu_k, a.Tk, r));
+    most[0] = max(most[0], offset(a.cu_q, a.Tq, r));
+    most[1] = max(most[1], offset(a.cu_k, a.Tk, r));
   }
-  int last;
-  const int up_q = block_scan(most_q, scan_s, last, larger), up_k = block_scan(most_k, scan_s, last, larger);
-  // of the threads before this one
-  __shared__ int end_s[2][kThreads];
-  end_s[0][tid] = up_q;
-  end_s[1][tid] = up_k;
+  block_scan(most, scan_s, last, larger);
+  end_s[0][tid] = most[0];
+  end_s[1][tid] = most[1];
   __syncthreads();
   int run_q = tid ? end_s[0][tid - 1] : 0, run_k = tid ? end_s[1][tid - 1] : 0;
   bool bad = false;
@@ -85,10 +92,12 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   auto sequence = [&](int r) {
     return PackedSeq{first_q[r], first_q[r + 1] - first_q[r], first_k[r], first_k[r + 1] - first_k[r]};
   };
-  int mine = 0;
-  for (int r = my0; r < min(my1, R); ++r) mine += packed_units(sequence(r), a.tpt, a.bwd);
-  int units;
-  int at = block_scan(mine, scan_s, units, [](int x, int y) { return x + y; }) - mine;
+  int mine[1] = {0}, all[1];
+  for (int r = my0; r < min(my1, R); ++r) mine[0] += packed_units(sequence(r), a.tpt, a.bwd);
+  int at = -mine[0];
+  block_scan(mine, scan_s + 2, all, [](int x, int y) { return x + y; });
+  const int units = all[0];
+  at += mine[0];
   for (int r = my0; r < my1; ++r) {
     first_u[r] = at;
     if (r < R) at += packed_units(sequence(r), a.tpt, a.bwd);
@@ -105,44 +114,93 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     x.seq = sequence(lo);
     x.tile = u - first_u[lo];
     packed_steps(x.seq, x.tile, a.tpt, a.causal, a.bwd, x.s0, x.s1);
-    x.slot = -1;
+  };
+  PackedItem own;  // this thread's first unit
+  own.s0 = own.s1 = 0;
+  if (tid < units) unit(tid, own);
+  auto with_units = [&](auto f) {  // f(unit) of every unit of this thread
+    if (tid < units) f(tid, own);
+    for (int u = tid + kThreads; u < units; u += kThreads) {
+      PackedItem x;
+      unit(u, x);
+      f(u, x);
+    }
   };
   long long steps = 0;
   int longest = 0;
-  for (int u = tid; u < units; u += kThreads) {
-    PackedItem x;
-    unit(u, x);
-    steps += x.s1 - x.s0;
-    longest = max(longest, x.s1 - x.s0);
+  with_units([&](int u, const PackedItem& x) {
+    const int w = x.s1 - x.s0;
+    steps += w;
+    longest = max(longest, w);
+    if (u < kWeighed) work_s[u] = w;
+  });
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, off);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    steps_s[warp] = steps;
+    longest_s[warp] = longest;
   }
-  long long all;
-  block_scan(steps, sum_s, all, [](long long x, long long y) { return x + y; });
-  int most;
-  block_scan(longest, scan_s, most, larger);
-  const long long slice = packed_slice(all, a.Hk, a.target, a.least);
-  most = (int)min((long long)most, slice);  // an upper bound of a slice's steps
-  auto class_of = [&](int w) { return (int)((long long)(most - w) * (kClasses - 1) / max(most, 1)); };
+  __syncthreads();
+  steps = steps_s[lane];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, off);
+  longest = __reduce_max_sync(0xffffffffu, longest_s[lane]);
 
-  // ---- the slices, counted and placed by their lengths
-  for (int u = tid; u < units; u += kThreads) {
-    PackedItem x;
-    unit(u, x);
-    const int w = x.s1 - x.s0, c = packed_cuts(w, slice);
-    for (int i = 0; i < c; ++i) {
-      int b, e;
-      packed_cut(w, c, i, b, e);
-      atomicAdd(&class_s[class_of(e - b)], 1);
+  // ---- how long a slice is: each warp weighs a candidate.  Not where no unit is longer than the
+  // shortest of them; and of more units than are kept only an even share is tried
+  const float even = packed_even(steps, a.Hk, a.target);
+  int slice = longest;
+  if (a.cuttable && longest > a.least && (float)longest > 0.75f * even) {
+    if (units <= kWeighed) {
+      const int mine_slice = packed_candidate(warp, even, a.least, longest);
+      int n = 0, cut = 0;
+      for (int u = lane; u < units; u += 32) {
+        const int c = packed_cuts(work_s[u], mine_slice);
+        n += c;
+        cut += c > 1 ? c : 0;
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+      cut = __reduce_add_sync(0xffffffffu, cut);
+      if (lane == 0) time_s[warp] = packed_time(mine_slice, n, cut, steps, a.Hk, a.target);
+      __syncthreads();
+      float best = time_s[lane];
+      int which = lane;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        const float t = __shfl_xor_sync(0xffffffffu, best, off);
+        const int k = __shfl_xor_sync(0xffffffffu, which, off);
+        if (t < best || (t == best && k < which)) {
+          best = t;
+          which = k;
+        }
+      }
+      slice = packed_candidate(which, even, a.least, longest);
+    } else {
+      slice = min(longest, max(a.least, (int)even + 1));
     }
   }
+  const float per_step = (float)(kClasses - 1) / (float)max(min(longest, slice), 1);
+  auto class_of = [&](int w) { return min(kClasses - 1, max(0, (int)((float)(slice - w) * per_step))); };
+
+  // ---- the slices, counted and placed by their lengths
+  with_units([&](int, const PackedItem& x) {
+    const int w = x.s1 - x.s0, c = packed_cuts(w, slice);
+    if (c == 1) {
+      atomicAdd(&class_s[class_of(w)], 1);
+    } else {  // the first w % c of one length, the others of one less
+      if (w % c) atomicAdd(&class_s[class_of(w / c + 1)], w % c);
+      atomicAdd(&class_s[class_of(w / c)], c - w % c);
+    }
+  });
   __syncthreads();
-  const int in_class = class_s[tid];
-  int items;
-  const int class_end = block_scan(in_class, scan_s, items, [](int x, int y) { return x + y; });
-  class_s[tid] = class_end - in_class;
+  int in_class[1] = {class_s[tid]}, items[1];
+  const int had = in_class[0];
+  block_scan(in_class, scan_s + 3, items, [](int x, int y) { return x + y; });
+  class_s[tid] = in_class[0] - had;
   __syncthreads();
-  for (int u = tid; u < units; u += kThreads) {
-    PackedItem x;
-    unit(u, x);
+  with_units([&](int, const PackedItem& unit_x) {
+    PackedItem x = unit_x;
     const int s0 = x.s0, w = x.s1 - x.s0, c = packed_cuts(w, slice);
     int slot = -1;
     if (c > 1) {
@@ -150,6 +208,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       PackedItem cut = x;
       cut.s0 = slot;
       cut.s1 = c;
+      cut.slot = 0;
       a.list.cuts[atomicAdd(&cut_s, 1)] = cut;
     }
     for (int i = 0; i < c; ++i) {
@@ -160,12 +219,12 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       x.slot = c > 1 ? slot + i : -1;
       a.list.items[atomicAdd(&class_s[class_of(e - b)], 1)] = x;
     }
-  }
+  });
   __syncthreads();
   if (tid == 0) {
-    a.list.head[0] = items;
+    a.list.head[0] = items[0];
     a.list.head[1] = cut_s;
-    a.list.head[2] = first_q[0];  // query and key rows that are a sequence's
+    a.list.head[2] = first_q[0];  // query rows that are a sequence's
     a.list.head[3] = first_q[R];
   }
 }

@@ -26,46 +26,64 @@ struct PackedSeq {
 // A CTA's work, for each key head: steps [s0, s1) of a unit; slot < 0 where these are all of the
 // unit's, else the place of its partial result.  In the list of cut units s0 is the first slot
 // and s1 the number of slots.
-struct PackedItem {
+struct alignas(16) PackedItem {
   PackedSeq seq;
   int tile, s0, s1, slot;
 };
 
+// n, m and tile * tpt are at most 2^30, so that all of this fits an int.
 __host__ __device__ inline int packed_units(const PackedSeq& s, int tpt, bool bwd) {
-  return bwd ? (int)(((long long)s.m + kPackedKeys - 1) / kPackedKeys) : (int)(((long long)s.n + tpt - 1) / tpt);
+  return bwd ? (s.m + kPackedKeys - 1) / kPackedKeys : (s.n + tpt - 1) / tpt;
 }
 
 // Steps [s0, s1) of unit `tile`; none (s0 = s1) where no query of it sees a key.
 __host__ __device__ inline void packed_steps(const PackedSeq& s, int tile, int tpt, bool causal, bool bwd, int& s0,
                                              int& s1) {
-  const long long ahead = (long long)s.m - s.n;  // keys before the first query's own
+  const int ahead = s.m - s.n;  // keys before the first query's own
+  s0 = 0;
   if (!bwd) {
-    long long end = s.m;  // keys that the tile's last row sees
-    if (causal) {
-      const long long last = (long long)(tile + 1) * tpt < s.n ? (long long)(tile + 1) * tpt : s.n;
-      end = ahead + last;
-    }
-    s0 = 0;
-    s1 = end <= 0 ? 0 : (int)((end + kPackedKeys - 1) / kPackedKeys);
+    int end = s.m;  // keys that the tile's last row sees
+    if (causal) end = ahead + ((tile + 1) * tpt < s.n ? (tile + 1) * tpt : s.n);
+    s1 = end <= 0 ? 0 : (int)(((unsigned)end + kPackedKeys - 1) / kPackedKeys);
     return;
   }
-  s1 = (int)(((long long)s.n + tpt - 1) / tpt);
-  s0 = 0;
+  s1 = (s.n + tpt - 1) / tpt;
   if (causal) {
-    const long long first = (long long)tile * kPackedKeys - ahead;  // first query that sees the tile's first key
-    if (first > 0) s0 = first >= s.n ? s1 : (int)(first / tpt);
+    const int first = tile * kPackedKeys - ahead;  // first query that sees the tile's first key
+    if (first > 0) s0 = first >= s.n ? s1 : first / tpt;
   }
 }
 
-// Steps of a slice, so that `target` CTAs have even shares of `steps` steps of each of `heads` key
-// heads, but at least `least`.  Units with more steps are cut: into c = ceil(w / P) < 2 w / P
-// slices, so that all of them take fewer than 2 target / heads slots.
-__host__ __device__ inline long long packed_slice(long long steps, int heads, int target, long long least) {
-  const long long even = (steps * heads + target - 1) / target;
-  return even > least ? even : least;
+// How long a slice is.  `even` is what each of `target` CTAs would have of all units' steps, times the
+// key heads.  A launch takes about as long as its longest slice and its start where all slices
+// run at once (a few more stand behind the shortest of them), and otherwise as an even share of
+// the steps and of the slices' starts, and half of the longest one behind it; parts of cut units
+// cost their fp32 sums, and the join a launch.  Candidates from 3/4 of `even` on are weighed (and the
+// longest unit's steps: nothing cut), the longer of equals first.  The constants, in steps, are from
+// sweeps: 8 requests of up to 512 rows over up to 8192 keys take 67 us cut at 33 steps, 73 at 18
+// to 30, 72 at 38 and 89 uncut; 4 causal sequences of up to 2048 32.8 uncut and 34.3 to 37.5 cut
+// at 13 to 8 of 14 steps, their backward pass 72.5 and 73.2 to 81.6 at 12 to 7.
+constexpr int kPackedCandidates = 32;
+constexpr float kPackedStart = 4.f, kPackedJoin = 2.f, kPackedPart = 1.5f;
+__host__ __device__ inline float packed_even(long long steps, int heads, int target) {
+  return (float)steps * (float)heads / (float)target;
 }
-__host__ __device__ inline int packed_slots(int heads, int target) { return 2 * target / heads + 1; }
-__host__ __device__ inline int packed_cuts(int w, long long slice) { return w <= slice ? 1 : (int)((w + slice - 1) / slice); }
+__host__ __device__ inline int packed_candidate(int k, float even, int least, int longest) {
+  if (k == 0) return longest;
+  const float p = even * (float)(kPackedCandidates - 1 - k + 12) * (1.f / 16.f);  // 2.6 to 3/4 of it
+  const int up = p < (float)longest ? (int)p + 1 : longest;
+  const int floor_ = least < longest ? least : longest;
+  return up < floor_ ? floor_ : up > longest ? longest : up;
+}
+__host__ __device__ inline int packed_cuts(int w, int slice) { return w <= slice ? 1 : (w + slice - 1) / slice; }
+__host__ __device__ inline float packed_time(int slice, int slices, int parts, long long steps, int heads, int target) {
+  const float join = parts > 0 ? kPackedJoin + packed_even(parts, heads, target) * kPackedPart : 0.f;
+  if ((float)slices * (float)heads <= 1.1f * (float)target) return (float)slice + kPackedStart + join;
+  return packed_even(steps, heads, target) + packed_even(slices, heads, target) * kPackedStart + 0.5f * (float)slice + join;
+}
+// A unit that is cut into c = ceil(w / P) slices has w > P, so that c < 2 w / P; with P at least 3/4 of
+// the even share all cut units take fewer than 8/3 target / heads slots.
+__host__ __device__ inline int packed_slots(int heads, int target) { return 8 * target / (3 * heads) + 1; }
 // Slice i of w steps cut into c: first step and end.
 __host__ __device__ inline void packed_cut(int w, int c, int i, int& a, int& b) {
   const int base = w / c, more = w % c;

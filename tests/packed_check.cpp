@@ -47,7 +47,7 @@ int main() {
     const int R = 1 + rng() % 20, heads = 1 + rng() % (round % 5 == 0 ? 700 : 16), target = 1 + rng() % 320;
     const int tpt = kTpt[rng() % 6];
     const bool bwd = rng() % 2, causal = rng() % 2;
-    const long long least = 1 + rng() % 6;
+    const int least = 1 + rng() % 6;
     std::vector<int> work;
     long long all = 0, rows = 0;
     for (int r = 0; r < R; ++r) {
@@ -60,23 +60,33 @@ int main() {
         all += b - a;
       }
     }
-    const long long slice = packed_slice(all, heads, target, least);
-    long long slots = 0, items = 0, cut = 0;
-    for (int w : work) {
-      const int c = packed_cuts(w, slice);
-      int at = 0;
-      for (int i = 0; i < c; ++i) {
-        int a, b;
-        packed_cut(w, c, i, a, b);
-        if (a != at || b - a > slice || (w > 0 && b <= a)) fail("slice", PackedSeq{}, w, c);
-        at = b;
+    int longest = 0;
+    for (int w : work) longest = w > longest ? w : longest;
+    const float even = packed_even(all, heads, target);
+    for (int k = 0; k < kPackedCandidates; ++k) {
+      // a call weighs the candidates only where some unit is longer than the shortest of them
+      if (k > 0 && !(longest > least && (float)longest > 0.75f * even)) break;
+      const int slice = packed_candidate(k, even, least, longest);
+      if (slice > longest || (slice < least && slice < longest)) fail("candidate", PackedSeq{}, slice, longest);
+      long long slots = 0, items = 0, cut = 0;
+      for (int w : work) {
+        const int c = packed_cuts(w, slice);
+        int at = 0;
+        for (int i = 0; i < c; ++i) {
+          int a, b;
+          packed_cut(w, c, i, a, b);
+          const int want = c == 1 ? w : i < w % c ? w / c + 1 : w / c;
+          if (a != at || b - a > slice || b - a != want || (w > 0 && b <= a)) fail("slice", PackedSeq{}, w, c);
+          at = b;
+        }
+        if (at != w) fail("slices", PackedSeq{}, w, c);
+        items += c;
+        if (c > 1) slots += c, ++cut;
       }
-      if (at != w) fail("slices", PackedSeq{}, w, c);
-      items += c;
-      if (c > 1) slots += c, ++cut;
+      const long long most = packed_slots(heads, target);
+      if (slots > most || cut > most / 2 || items > rows / (bwd ? 128 : tpt) + R + most) fail("capacity", PackedSeq{}, R, target);
+      if (!(packed_time(slice, (int)items, (int)slots, all, heads, target) > 0.f)) fail("time", PackedSeq{}, slice, longest);
     }
-    const long long most = packed_slots(heads, target);
-    if (slots > most || cut > most / 2 || items > rows / (bwd ? 128 : tpt) + R + most) fail("capacity", PackedSeq{}, R, target);
     ++checked;
   }
   std::printf("ok %lld\n", checked);
