@@ -74,7 +74,7 @@ struct Sizes {
     };
     items_at = place((size_t)items * sizeof(PackedItem));
     cuts_at = place((size_t)cuts * sizeof(PackedItem));
-    starts_at = place((size_t)3 * (p->R + 1) * sizeof(int));
+    starts_at = place((size_t)4 * (p->R + 1) * sizeof(int));
     slots_at = place((size_t)slots * p->Hk * packed_slot_words(p->d, bwd) * 4);
     const size_t rows = (size_t)p->Tq * p->Hq;
     stat_at = bwd ? place(2 * rows * 4) : at;

@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list, the rows' statistics, the zeroed accumulator
-  const int index = a.divHk.div((int)blockIdx.x), hk = (int)blockIdx.x - index * a.Hk;
-  if (index >= a.list.head[0]) return;
+  int index, hk;
+  if (!packed_place(a, index, hk)) return;
   const PackedItem x = a.list.items[index];
   const int kt = x.tile, q_end = x.s1, tpt = a.tpt, G = a.G;
   const int keys = min(kTile, x.seq.m - kt * kTile);  // of the tile that are the sequence's

@@ -104,18 +104,8 @@ __global__ void __launch_bounds__(192, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
-  const int count = a.list.head[0];
   int index, hk;
-  if (a.head_major) {
-    if (count == 0) return;
-    hk = (int)blockIdx.x / count;
-    index = (int)blockIdx.x - hk * count;
-    if (hk >= a.Hk) return;
-  } else {
-    index = a.divHk.div((int)blockIdx.x);
-    hk = (int)blockIdx.x - index * a.Hk;
-    if (index >= count) return;
-  }
+  if (!packed_place(a, index, hk)) return;
   const PackedItem x = a.list.items[index];
   const int t0 = x.tile * a.tpt;                       // the tile's first token in its sequence
   const int rows = min(a.tpt, x.seq.n - t0) * a.G;     // rows that are the sequence's

@@ -2,8 +2,9 @@
 //
 // One CTA: prefix maxima of the offsets (so that any offsets give sequences that lie in the
 // tensors, one behind the other), prefix sums of the units, the steps of every unit, how long a
-// slice is, and the slices in order of their steps, the longest first, by counting.  The main
-// kernel's CTAs take the list in order, so that what is left at the end is short.  Where in its
+// slice is, and the slices in order of their steps, the longest first, by counting (many units
+// sequence by sequence).  The main kernel's CTAs take the list in order, so that what is left at
+// the end is short.  Where in its
 // class of lengths an item stands, and which slots a cut unit has, is left to the order of
 // atomics: results do not depend on it.  Bound by latency, of which the main kernel's launch
 // hides a part.
@@ -14,6 +15,11 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32, kClasses = kThreads, kNear = 1024, kWeighed = 4096;
+// Units, times key heads, for each CTA that runs at a time, from which on the list goes sequence by
+// sequence, for the sake of L2.  In this order and by steps alone: 12 sequences up to 16384 tokens, 32
+// and 8 heads, d = 128, forward 7.33 and 7.70 ms, of up to 8192 backward 6.58 and 7.00; 20 up to
+// 4096, 12 and 4 heads, d = 64, backward (10 units for each CTA) 0.728 and 0.713.
+constexpr float kGrouped = 12.f;
 static_assert(kPackedCandidates == kWarps, "a warp weighs a candidate");
 
 // Inclusive scans of N values per thread over the CTA; `total` gets the last.
@@ -46,7 +52,7 @@ __device__ __forceinline__ void block_scan(int (&v)[N], int (*warp_s)[kWarps], i
 
 __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // they wait for this grid's end
-  __shared__ int near_s[3][kNear + 1];
+  __shared__ int near_s[4][kNear + 1];
   __shared__ int scan_s[4][kWarps];
   __shared__ long long steps_s[kWarps];
   __shared__ int longest_s[kWarps];
@@ -56,11 +62,12 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   __shared__ int end_s[2][kThreads];
   __shared__ int slot_s, cut_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.R;
-  int *first_q = a.list.starts, *first_k = first_q + R + 1, *first_u = first_k + R + 1;
+  int *first_q = a.list.starts, *first_k = first_q + R + 1, *first_u = first_k + R + 1, *place_u = first_u + R + 1;
   if (R <= kNear) {
     first_q = near_s[0];
     first_k = near_s[1];
     first_u = near_s[2];
+    place_u = near_s[3];
   }
   class_s[tid] = 0;
   if (tid == 0) slot_s = cut_s = 0;
@@ -113,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     }
     x.seq = sequence(lo);
     x.tile = u - first_u[lo];
+    x.slot = lo;  // until it is placed
     packed_steps(x.seq, x.tile, a.tpt, a.causal, a.bwd, x.s0, x.s1);
   };
   PackedItem own;  // this thread's first unit
@@ -183,7 +191,47 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   const float per_step = (float)(kClasses - 1) / (float)max(min(longest, slice), 1);
   auto class_of = [&](int w) { return min(kClasses - 1, max(0, (int)((float)(slice - w) * per_step))); };
 
-  // ---- the slices, counted and placed by their lengths
+  // ---- many whole units: the sequences by their longest units' steps, and the units of each behind one
+  // another, the longest first, so that the CTAs that run at a time read the same sequence
+  if (slice == longest && (float)units * (float)a.Hk >= kGrouped * (float)a.target) {
+    auto seq_class = [&](int r, const PackedSeq& q, int n) {
+      int s0, s1;
+      packed_steps(q, a.bwd ? 0 : n - 1, a.tpt, a.causal, a.bwd, s0, s1);
+      return class_of(s1 - s0);
+    };
+    for (int r = my0; r < min(my1, R); ++r) {
+      const PackedSeq q = sequence(r);
+      const int n = packed_units(q, a.tpt, a.bwd);
+      if (n > 0) atomicAdd(&class_s[seq_class(r, q, n)], n);
+    }
+    __syncthreads();
+    int of[1] = {class_s[tid]}, total[1];
+    const int had = of[0];
+    block_scan(of, scan_s + 3, total, [](int x, int y) { return x + y; });
+    class_s[tid] = of[0] - had;
+    __syncthreads();
+    for (int r = my0; r < min(my1, R); ++r) {
+      const PackedSeq q = sequence(r);
+      const int n = packed_units(q, a.tpt, a.bwd);
+      if (n > 0) place_u[r] = atomicAdd(&class_s[seq_class(r, q, n)], n);
+    }
+    __syncthreads();
+    with_units([&](int u, const PackedItem& unit_x) {
+      PackedItem x = unit_x;
+      const int r = x.slot, n = packed_units(x.seq, a.tpt, a.bwd);
+      x.slot = -1;
+      a.list.items[place_u[r] + (a.bwd ? x.tile : n - 1 - x.tile)] = x;
+    });
+    if (tid == 0) {
+      a.list.head[0] = units;
+      a.list.head[1] = 0;
+      a.list.head[2] = first_q[0];  // query rows that are a sequence's
+      a.list.head[3] = first_q[R];
+    }
+    return;
+  }
+
+  // ---- else the slices, counted and placed by their lengths
   with_units([&](int, const PackedItem& x) {
     const int w = x.s1 - x.s0, c = packed_cuts(w, slice);
     if (c == 1) {

@@ -302,6 +302,22 @@ def test_many_sequences(cuda_lib):
     check_bwd(grads, q, k, v, o, do, lse, new, new, True, 0.125, "f16")
 
 
+@pytest.mark.parametrize("R,most,Hq,Hk,d", [(40, 60, 96, 96, 64), (1500, 5, 4, 4, 64), (30, 200, 64, 64, 128)])
+def test_many_units(cuda_lib, R, most, Hq, Hk, d):
+    """So many tiles for each CTA that the list goes sequence by sequence; with sequences without
+    queries or keys among them."""
+    rng = torch.Generator().manual_seed(R)
+    new = torch.randint(0, most + 1, (R,), generator=rng).tolist()
+    keys = [n + int(torch.randint(0, 3, (1,), generator=rng)) if i % 7 else 0 for i, n in enumerate(new)]
+    q, k, v, do = make(new, keys, Hq, Hk, d, "bf16", 12)
+    dev = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.attention_fwd_packed(*dev[:3], offsets(new), offsets(keys))
+    check_fwd(o, lse, q, k, v, new, keys, True, d ** -0.5, "bf16")
+    grads = fa.attention_bwd_packed(*dev[:3], o, dev[3], lse, offsets(new), offsets(keys))
+    check_bwd(grads, q, k, v, o, do, lse, new, keys, True, d ** -0.5, "bf16")
+    assert fa.get_status() == fa.FA_OK
+
+
 def test_empty_tensors(cuda_lib):
     z = lambda T, H: torch.zeros(T, H, 64, dtype=torch.bfloat16, device="cuda")
     o, lse = fa.attention_fwd_packed(z(0, 4), z(0, 2), z(0, 2), offsets([0]))
