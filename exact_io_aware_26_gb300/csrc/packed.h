@@ -31,6 +31,8 @@ struct PackedArgs {
   int tpt, causal;
   float scale, scale_log2;
   PackedList list;
+  int direct;          // forward: no list; the CTAs find their units in the offsets
+  const int *cu_q, *cu_k;
   const void* v;       // for values that are not finite
   long long vs[2];     // element strides {token, head}
   void* o;             // forward: result; backward: its values
@@ -44,14 +46,57 @@ struct PackedArgs {
   Report rep;
 };
 
+constexpr int kPackedDirect = 32;  // sequences that need no list: a lane each
 #ifdef __CUDACC__
 // A CTA's item of the list and its key head, an item's key heads next to each other; false: none is
 // left for it.  (Key head after key head, 32 heads over 8 of 12 sequences up to 16384 tokens take 7.8 ms
 // instead of 7.3.)
-__device__ __forceinline__ bool packed_place(const PackedArgs& a, int& index, int& hk) {
-  index = a.divHk.div((int)blockIdx.x);
+__device__ __forceinline__ bool packed_place(const PackedArgs& a, PackedItem& x, int& hk) {
+  const int index = a.divHk.div((int)blockIdx.x);
   hk = (int)blockIdx.x - index * a.Hk;
-  return index < a.list.head[0];
+  if (index >= a.list.head[0]) return false;
+  x = a.list.items[index];
+  return true;
+}
+
+// Without a list: unit `index` of at most 32 sequences, from their offsets, which lane r of each warp
+// reads for sequence r; false: there is none.  Offsets that are wrong are taken as by the list's
+// kernel, and recorded by the first CTA.
+__device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, PackedItem& x) {
+  const int lane = threadIdx.x & 31, r = min(lane, a.R - 1);
+  const int q0 = __ldg(a.cu_q + r), q1 = __ldg(a.cu_q + r + 1), k0 = __ldg(a.cu_k + r), k1 = __ldg(a.cu_k + r + 1);
+  auto clamp = [](int v, int T) { return min(max(v, 0), T); };
+  PackedSeq s{clamp(q0, a.Tq), 0, clamp(k0, a.Tk), 0};
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int uq = __shfl_up_sync(0xffffffffu, s.q0, off), uk = __shfl_up_sync(0xffffffffu, s.k0, off);
+    if (lane >= off) {
+      s.q0 = max(s.q0, uq);
+      s.k0 = max(s.k0, uk);
+    }
+  }
+  s.n = max(clamp(q1, a.Tq), s.q0) - s.q0;
+  s.m = max(clamp(k1, a.Tk), s.k0) - s.k0;
+  if (blockIdx.x == 0 && lane < a.R && (s.q0 != q0 || s.q0 + s.n != q1 || s.k0 != k0 || s.k0 + s.m != k1))
+    atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
+  const int mine = lane < a.R ? packed_units(s, a.tpt, false) : 0;
+  int end = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, end, off);
+    if (lane >= off) end += up;
+  }
+  const uint32_t here = __ballot_sync(0xffffffffu, index < end && index >= end - mine);
+  if (here == 0u) return false;
+  const int from = __ffs((int)here) - 1;
+  x.seq.q0 = __shfl_sync(0xffffffffu, s.q0, from);
+  x.seq.n = __shfl_sync(0xffffffffu, s.n, from);
+  x.seq.k0 = __shfl_sync(0xffffffffu, s.k0, from);
+  x.seq.m = __shfl_sync(0xffffffffu, s.m, from);
+  x.tile = index - __shfl_sync(0xffffffffu, end - mine, from);
+  packed_steps(x.seq, x.tile, a.tpt, a.causal, false, x.s0, x.s1);
+  x.slot = -1;
+  return true;
 }
 #endif
 

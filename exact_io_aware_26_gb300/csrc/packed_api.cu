@@ -202,7 +202,12 @@ fa_status fa_fwd_packed(const fa_packed_params* p, const void* q, const void* k,
   FA_TRY(map_of(&tm[1], p, none ? q : k, none ? 1 : p->Tk, p->Hk, p->k_stride, 1, 128));
   FA_TRY(map_of(&tm[2], p, none ? q : v, none ? 1 : p->Tk, p->Hk, p->v_stride, 1, 128));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_packed_plan(plan_args(a, z, cu_q, cu_k, false), s);
+  // a few sequences that no cut can shorten need no list (three prompts of up to 32 tokens: 10.7 us with it)
+  a.direct = z.slots == 0 && p->R <= kPackedDirect;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  cudaError_t e = cudaSuccess;
+  if (!a.direct) e = launch_packed_plan(plan_args(a, z, cu_q, cu_k, false), s);
   if (e != cudaSuccess) return api_cuda_fail(e, "packed work list launch");
   e = launch_packed_fwd(a, p->d, p->dtype == FA_F16, tm, z.items, z.cuts, s);
   if (e != cudaSuccess) return api_cuda_fail(e, "packed forward launch");

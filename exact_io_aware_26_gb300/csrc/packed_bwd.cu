@@ -97,16 +97,19 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list, the rows' statistics, the zeroed accumulator
-  int index, hk;
-  if (!packed_place(a, index, hk)) return;
-  const PackedItem x = a.list.items[index];
+  PackedItem x;
+  int hk;
+  if (!packed_place(a, x, hk)) return;
   const int kt = x.tile, q_end = x.s1, tpt = a.tpt, G = a.G;
   const int keys = min(kTile, x.seq.m - kt * kTile);  // of the tile that are the sequence's
   const int ahead = x.seq.m - x.seq.n;
-  auto rows_of = [&](int qt) { return min(tpt, x.seq.n - qt * tpt) * G; };  // rows of a query tile
-  const int full = tpt * G;
-  // some row of query tile qt does not see some key of this tile
-  auto diagonal = [&](int qt) { return a.causal && kt * kTile + keys - 1 > qt * tpt + ahead; };
+  // rows of a query tile: all but the sequence's last one are full
+  const int full = tpt * G, q_last = (x.seq.n - 1) / tpt, last_rows = (x.seq.n - q_last * tpt) * G;
+  auto rows_of = [&](int qt) { return qt == q_last ? last_rows : full; };
+  // some row of the query tiles before this one does not see some key of this tile
+  const int whole_from = !a.causal ? 0 : max(0, (kt * kTile + keys - 1 - ahead + tpt - 1) / tpt);
+  auto diagonal = [&](int qt) { return qt < whole_from; };
+  const int q_row0 = x.seq.q0 * G;  // of the accumulator
 
   auto bar = [&](int i) { return sb + L::BAR + 8u * (uint32_t)i; };
   const uint32_t bar_kv = bar(0), bar_s_full = bar(1), bar_dp_full = bar(2), bar_dp_free = bar(3), bar_p_full = bar(4),
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_reduce_add_3d(&tmdQ, stg, c0, (x.seq.q0 + qt * tpt) * G + qd * 32, hk);
+            tma_reduce_add_3d(&tmdQ, stg, c0, q_row0 + qt * full + qd * 32, hk);
             bulk_commit_group();
           }
           pend = true;
@@ -401,9 +404,9 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     const uint64_t c2p = f2pack(a.scale_log2, a.scale_log2);
     const bool tail = keys < kTile;
     // the first of the warpgroup's columns whose query sees this key
+    const int sees = r >= keys ? 1 << 30 : a.causal ? kt * kTile + r - ahead : 0;  // the first query that sees it
     auto first_col = [&](int qt) {
-      if (r >= keys) return kTile;
-      const int i = a.causal ? kt * kTile + r - ahead - qt * tpt : 0;  // first such token of the tile
+      const int i = sees - qt * tpt;
       return (i <= 0 ? 0 : i >= tpt ? kTile : i * G) - CW * g;
     };
     const uint32_t stg = sb + L::STG + (uint32_t)warp * L::BOXB;
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_reduce_add_3d(&tmdQ, stg, g * L::DQG + c0, (x.seq.q0 + qt * tpt) * G + (warp & 3) * 32, hk);
+              tma_reduce_add_3d(&tmdQ, stg, g * L::DQG + c0, q_row0 + qt * full + (warp & 3) * 32, hk);
               bulk_commit_group();
             }
             pend = true;

@@ -39,7 +39,8 @@ struct Layout {
   static constexpr uint32_t TSLOT = BAR + FwdBars<NS>::kCount * 8;
   static constexpr uint32_t ABORT = TSLOT + 4;
   static constexpr uint32_t SCRUB = ABORT + 4;  // first key tile some of whose values were zeroed
-  static constexpr uint32_t BYTES = SCRUB + 4;
+  static constexpr uint32_t ITEM = (SCRUB + 4 + 15) & ~15u;  // for the epilogue, which keeps no registers for it
+  static constexpr uint32_t BYTES = ITEM + sizeof(PackedItem);
   // TMEM: S at [0, 128), O behind it; at d = 64 P~ has columns of its own, at d = 128 S's
   static constexpr uint32_t TMEM_COLS = 256;
   static constexpr bool PSEP = D == 64;
@@ -103,10 +104,16 @@ __global__ void __launch_bounds__(192, 2)
   const uint32_t sb = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
-  int index, hk;
-  if (!packed_place(a, index, hk)) return;
-  const PackedItem x = a.list.items[index];
+  PackedItem x;
+  int hk;
+  if (a.direct) {
+    const int index = a.divHk.div((int)blockIdx.x);
+    hk = (int)blockIdx.x - index * a.Hk;
+    if (!packed_direct(a, index, x)) return;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
+    if (!packed_place(a, x, hk)) return;
+  }
   const int t0 = x.tile * a.tpt;                       // the tile's first token in its sequence
   const int rows = min(a.tpt, x.seq.n - t0) * a.G;     // rows that are the sequence's
   const int pos0 = x.seq.m - x.seq.n + t0;             // its place among the keys
@@ -149,6 +156,7 @@ __global__ void __launch_bounds__(192, 2)
       tma_load_3d(sb + L::Q + c * (kTile * 128), &tmQ, bars.q(), c * 64, hk * a.G, x.seq.q0 + t0);
     kt_next = fwd_produce(w, bars, x.s0, x.s1, x.seq.m, NS, nk, nv, next, load_k, load_v);
   }
+  if (threadIdx.x == 0) *reinterpret_cast<PackedItem*>(smem + L::ITEM) = x;
   if (warp == 5) {
     tmem_alloc(sb + L::TSLOT, L::TMEM_COLS);
     tmem_relinquish();
@@ -200,9 +208,7 @@ __global__ void __launch_bounds__(192, 2)
   } else {
     // ------------------------------------------------------------ softmax
     const int r = threadIdx.x;
-    const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
-    const bool live = r < rows;
-    const int lim = a.causal ? min(x.seq.m, pos0 + i + 1) : x.seq.m;  // keys that the row sees
+    const int lim = a.causal ? min(x.seq.m, pos0 + a.divG.div(r) + 1) : x.seq.m;  // keys that the row sees
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + L::T_S + lane_off, tO = tmem + L::T_O + lane_off;
     const float c2 = a.scale_log2;
@@ -297,9 +303,14 @@ __global__ void __launch_bounds__(192, 2)
       have_o = ok;
     }
     if (ok) {
-      const bool whole = x.slot < 0;
+      // d = 128: the item again from shared memory, which spares the loop its registers
+      const PackedItem y = D == 128 ? *reinterpret_cast<const PackedItem*>(smem + L::ITEM) : x;
+      const int i = a.divG.div(r), first = y.tile * a.tpt, token = y.seq.q0 + first + i;
+      const int kv = D == 128 ? (int)blockIdx.x - a.divHk.div((int)blockIdx.x) * a.Hk : hk, head = kv * a.G + r - i * a.G;
+      const bool live = r < min(a.tpt, y.seq.n - first) * a.G;
+      const bool whole = y.slot < 0;
       const float inv_l = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
-      const long long slot = (long long)x.slot * a.Hk + hk;
+      const long long slot = (long long)y.slot * a.Hk + kv;
       float* part = whole ? nullptr : a.slots + slot * (kTile * (D + 2));
       if (whole) {
         if (live) a.lse[(long long)token * a.Hq + head] = l == 0.f ? -INFINITY : fmaf(m_use, a.scale, __logf(l));
@@ -309,8 +320,8 @@ __global__ void __launch_bounds__(192, 2)
       // values that were zeroed: added to the rows that see them
       const int from = *scrubbed;
       const bool patch = from != kNone;
-      const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)x.seq.k0 * a.vs[0] + hk * a.vs[1];
-      const int end = min(lim, x.s1 * kTile);
+      const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)y.seq.k0 * a.vs[0] + kv * a.vs[1];
+      const int end = min(lim, y.s1 * kTile);
       uint16_t* dst = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1];
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -449,7 +460,7 @@ cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, int 
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.direct ? 0 : 1;
   cfg.stream = s;
   cfg.gridDim = dim3((unsigned)((long long)items * a.Hk));
   cfg.blockDim = dim3(192);
