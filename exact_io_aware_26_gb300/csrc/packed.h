@@ -10,7 +10,8 @@ namespace fa {
 struct PackedList {
   int* head;           // [0] items, [1] cut units
   PackedItem* items;
-  PackedItem* cuts;
+  PackedItem* cuts;    // the cut units (s0, s1: the whole unit's steps)
+  int* left;           // of each cut unit and key head: the parts that are done (forward)
   int* starts;         // scratch: first query, key and unit of each sequence and behind the last; its place in the list
 };
 
@@ -104,9 +105,8 @@ __device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, Pa
 inline size_t packed_slot_words(int d, bool bwd) { return bwd ? (size_t)2 * 128 * d : (size_t)128 * (d + 2); }
 
 cudaError_t launch_packed_plan(const PackedPlanArgs& a, cudaStream_t s);
-// `items`: at most that many; `cuts`: at most that many cut units, 0 where none can be.
-cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, int cuts,
-                              cudaStream_t s);
+// `items`, `cuts`: at most that many items and cut units.
+cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s);
 cudaError_t launch_packed_bwd_preprocess(const PackedArgs& a, int d, bool f16, cudaStream_t s);
 cudaError_t launch_packed_bwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s);
 cudaError_t launch_packed_bwd_finalize(const PackedArgs& a, int d, bool f16, int cuts, cudaStream_t s);

@@ -55,7 +55,7 @@ fa_status check(const fa_packed_params* p, bool bwd) {
 // The sizes of a call's work list and where it lies in the workspace.
 struct Sizes {
   int tpt, target, least, slots, items, cuts;
-  size_t head, items_at, cuts_at, starts_at, slots_at, stat_at, acc_at, bytes;
+  size_t items_at, cuts_at, left_at, starts_at, slots_at, stat_at, acc_at, bytes;
   Sizes(const fa_packed_params* p, int sms, bool bwd) {
     const int G = p->Hq / p->Hk;
     tpt = 128 / G;
@@ -74,6 +74,7 @@ struct Sizes {
     };
     items_at = place((size_t)items * sizeof(PackedItem));
     cuts_at = place((size_t)cuts * sizeof(PackedItem));
+    left_at = place(bwd ? 0 : (size_t)cuts * p->Hk * sizeof(int));
     starts_at = place((size_t)4 * (p->R + 1) * sizeof(int));
     slots_at = place((size_t)slots * p->Hk * packed_slot_words(p->d, bwd) * 4);
     const size_t rows = (size_t)p->Tq * p->Hq;
@@ -119,6 +120,7 @@ PackedArgs common_args(const fa_packed_params* p, const Sizes& z, void* workspac
   a.list.head = reinterpret_cast<int*>(ws);
   a.list.items = reinterpret_cast<PackedItem*>(ws + z.items_at);
   a.list.cuts = reinterpret_cast<PackedItem*>(ws + z.cuts_at);
+  a.list.left = reinterpret_cast<int*>(ws + z.left_at);
   a.list.starts = reinterpret_cast<int*>(ws + z.starts_at);
   a.slots = reinterpret_cast<float*>(ws + z.slots_at);
   a.stat_lse = reinterpret_cast<float*>(ws + z.stat_at);
@@ -209,7 +211,7 @@ fa_status fa_fwd_packed(const fa_packed_params* p, const void* q, const void* k,
   cudaError_t e = cudaSuccess;
   if (!a.direct) e = launch_packed_plan(plan_args(a, z, cu_q, cu_k, false), s);
   if (e != cudaSuccess) return api_cuda_fail(e, "packed work list launch");
-  e = launch_packed_fwd(a, p->d, p->dtype == FA_F16, tm, z.items, z.cuts, s);
+  e = launch_packed_fwd(a, p->d, p->dtype == FA_F16, tm, z.items, s);
   if (e != cudaSuccess) return api_cuda_fail(e, "packed forward launch");
   return FA_OK;
 }

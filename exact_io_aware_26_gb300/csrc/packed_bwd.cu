@@ -681,14 +681,14 @@ __global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, 
   // eight channels of a key a thread, keys side by side
   constexpr int PER = 2 * kTile * D / 8, PART = PER / kSumParts;
   constexpr size_t words = 2 * kTile * D;
-  const float* base = a.slots + ((size_t)x.s0 * a.Hk + hk) * words;
+  const float* base = a.slots + ((size_t)x.first * a.Hk + hk) * words;
   const int keys = min(kTile, x.seq.m - x.tile * kTile);
   for (int e = part * PART + (int)threadIdx.x; e < (part + 1) * PART; e += blockDim.x) {
     const int row = e % kTile, pair = e / kTile, which = pair / (D / 8), col = pair % (D / 8) * 8;
     if (row >= keys) continue;
     float acc[8] = {};
 #pragma unroll 2
-    for (int s = 0; s < x.s1; ++s) {
+    for (int s = 0; s < x.parts; ++s) {
       const float4* from = reinterpret_cast<const float4*>(base + (size_t)s * a.Hk * words) + 2 * pair * kTile + row;
       const float4 u = from[0], v = from[kTile];
       acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;

@@ -7,7 +7,7 @@
 //     128 rows with its heads, and K and V are read once for all of them;
 //   - tiles taken from the list that packed_plan.cu makes of the offsets, longest first; units
 //     longer than an even share of the steps are cut along the keys, their parts (m, l, O in
-//     fp32) joined by a second kernel, so that few rows over many keys fill the GPU;
+//     fp32) joined by the CTA that is done last, so that few rows over many keys fill the GPU;
 //   - keys and values behind a sequence's end, which belong to the next sequence or to none, and
 //     those that only some rows of a tile see: scores are replaced by -inf, and values that are
 //     not finite, which a weight of 0 would make NaN, are zeroed in shared memory and added
@@ -92,6 +92,60 @@ __device__ __forceinline__ bool scrub_tile(uint32_t tile, int inside) {
   }
   fence_async_smem();
   return __any_sync(0xffffffffu, in);
+}
+
+// Joins the parts of a unit that was cut: with M = max m_s, L = sum l_s 2^((m_s - M) c2),
+// O = sum O_s 2^((m_s - M) c2) / L, in the order of the parts.  128 threads, one for each row, of the CTA
+// whose part was done last.
+template <int D, bool F16>
+__device__ __noinline__ void join_parts(const PackedArgs& a, const PackedItem& x, int hk, int r) {
+  const int t0 = x.tile * a.tpt;
+  if (r >= min(a.tpt, x.seq.n - t0) * a.G) return;
+  constexpr size_t words = kTile * (D + 2);
+  const size_t step = words * a.Hk;
+  const float* base = a.slots + ((size_t)x.first * a.Hk + hk) * words;
+  auto at = [&](int s) { return __ldcg(reinterpret_cast<const float2*>(base + s * step + 2 * r)); };
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < x.parts; ++s) {
+    const float2 ml = at(s);
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);  // a part that saw no key weighs nothing
+  }
+  auto weight = [&](const float2& ml) { return ml.y == 0.f ? 0.f : ml.x == top ? 1.f : ex2((ml.x - top) * a.scale_log2); };
+#pragma unroll 4
+  for (int s = 0; s < x.parts; ++s) {
+    const float2 ml = at(s);
+    if (ml.y != 0.f) sum = fmaf(weight(ml), ml.y, sum);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
+  if (!fa_bounds(a.rep.st, token < a.Tq && head < a.Hq)) return;
+  a.lse[(long long)token * a.Hq + head] = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __logf(sum));
+  uint16_t* to = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1];
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    float acc[32] = {};
+#pragma unroll 2
+    for (int s = 0; s < x.parts; ++s) {
+      const float2 ml = at(s);
+      if (ml.y == 0.f) continue;
+      const float f = weight(ml);
+      const float4* from = reinterpret_cast<const float4*>(base + s * step + 2 * kTile) + c0 / 4 * kTile + r;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 v = __ldcg(from + c * kTile);
+        acc[4 * c] = fmaf(f, v.x, acc[4 * c]);
+        acc[4 * c + 1] = fmaf(f, v.y, acc[4 * c + 1]);
+        acc[4 * c + 2] = fmaf(f, v.z, acc[4 * c + 2]);
+        acc[4 * c + 3] = fmaf(f, v.w, acc[4 * c + 3]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 32; c += 8)
+      *reinterpret_cast<uint4*>(to + c0 + c) =
+          make_uint4(pack2<F16>(acc[c] * inv, acc[c + 1] * inv), pack2<F16>(acc[c + 2] * inv, acc[c + 3] * inv),
+                     pack2<F16>(acc[c + 4] * inv, acc[c + 5] * inv), pack2<F16>(acc[c + 6] * inv, acc[c + 7] * inv));
+  }
 }
 
 template <int D, bool F16>
@@ -367,6 +421,19 @@ __global__ void __launch_bounds__(192, 2)
         __syncwarp();
       }
     }
+    if (x.slot >= 0) {  // the last of the unit's parts to be done joins them (every row's thread comes here)
+      volatile int* last = reinterpret_cast<volatile int*>(smem + L::SCRUB);
+      const PackedItem y = *reinterpret_cast<const PackedItem*>(smem + L::ITEM);
+      __threadfence();
+      named_barrier_sync(1, kTile);  // the rows' parts are out, and `scrubbed` read
+      if (r == 0) {
+        const bool done = *abort_cta == 0 && atomicAdd(a.list.left + y.cut * a.Hk + hk, 1) == y.parts - 1;
+        __threadfence();
+        *last = done;
+      }
+      named_barrier_sync(1, kTile);
+      if (*last) join_parts<D, F16>(a, y, hk, r);
+    }
   }
 
   tc_fence_before();
@@ -377,80 +444,8 @@ __global__ void __launch_bounds__(192, 2)
   }
 }
 
-// Joins the parts of the units that were cut: with M = max m_s, L = sum l_s 2^((m_s - M) c2),
-// O = sum O_s 2^((m_s - M) c2) / L.  A block has 32 rows of a unit and key head, a thread an eighth of
-// a row; four parts are on their way together.
-constexpr int kJoinRows = 32;
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) packed_join_kernel(const PackedArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int cut = a.divHk.div((int)blockIdx.x), hk = (int)blockIdx.x - cut * a.Hk;
-  if (cut >= a.list.head[1]) return;
-  const PackedItem x = a.list.cuts[cut];
-  const int t0 = x.tile * a.tpt, rows = min(a.tpt, x.seq.n - t0) * a.G;
-  const int r = blockIdx.y * kJoinRows + (threadIdx.x & 31), part = threadIdx.x >> 5;
-  if (r >= rows) return;
-  constexpr int NC = D / 32, AT_ONCE = 4;  // float4 of a thread
-  constexpr size_t words = kTile * (D + 2);
-  const size_t step = words * a.Hk;
-  const float* base = a.slots + ((size_t)x.s0 * a.Hk + hk) * words;
-  float top = -INFINITY, sum = 0.f, acc[NC][4] = {};
-#pragma unroll 1
-  for (int s0 = 0; s0 < x.s1; s0 += AT_ONCE) {
-    float2 ml[AT_ONCE];
-    float4 o[AT_ONCE][NC];
-#pragma unroll
-    for (int k = 0; k < AT_ONCE; ++k) {
-      ml[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) o[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + k < x.s1) {
-        const float* from = base + (s0 + k) * step;
-        ml[k] = *reinterpret_cast<const float2*>(from + 2 * r);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-          o[k][c] = *reinterpret_cast<const float4*>(from + 2 * kTile + 4 * ((part * NC + c) * kTile + r));
-      }
-    }
-    float t = top;
-#pragma unroll
-    for (int k = 0; k < AT_ONCE; ++k)
-      if (ml[k].y != 0.f) t = fmaxf(t, ml[k].x);  // a part that saw no key weighs nothing
-    const float back = top == t ? 1.f : ex2((top - t) * a.scale_log2);
-    top = t;
-    sum *= back;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[c][i] *= back;
-#pragma unroll
-    for (int k = 0; k < AT_ONCE; ++k) {
-      if (ml[k].y == 0.f) continue;
-      const float f = ml[k].x == top ? 1.f : ex2((ml[k].x - top) * a.scale_log2);
-      sum = fmaf(f, ml[k].y, sum);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        acc[c][0] = fmaf(f, o[k][c].x, acc[c][0]);
-        acc[c][1] = fmaf(f, o[k][c].y, acc[c][1]);
-        acc[c][2] = fmaf(f, o[k][c].z, acc[c][2]);
-        acc[c][3] = fmaf(f, o[k][c].w, acc[c][3]);
-      }
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
-  if (!fa_bounds(a.rep.st, token < a.Tq && head < a.Hq)) return;
-  uint16_t* to = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1] + 4 * NC * part;
-#pragma unroll
-  for (int c = 0; c < NC; c += 2)
-    *reinterpret_cast<uint4*>(to + 4 * c) =
-        make_uint4(pack2<F16>(acc[c][0] * inv, acc[c][1] * inv), pack2<F16>(acc[c][2] * inv, acc[c][3] * inv),
-                   pack2<F16>(acc[c + 1][0] * inv, acc[c + 1][1] * inv), pack2<F16>(acc[c + 1][2] * inv, acc[c + 1][3] * inv));
-  if (part == 0) a.lse[(long long)token * a.Hq + head] = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __logf(sum));
-}
-
-template <int D, bool F16>
-cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, int cuts, cudaStream_t s) {
+cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, cudaStream_t s) {
   using L = Layout<D>;
   const auto kern = packed_fwd_kernel<D, F16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
@@ -465,20 +460,14 @@ cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, int 
   cfg.gridDim = dim3((unsigned)((long long)items * a.Hk));
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = L::BYTES;
-  e = cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], a);
-  if (e != cudaSuccess || cuts == 0) return e;
-  cfg.gridDim = dim3((unsigned)((long long)cuts * a.Hk), kTile / kJoinRows);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, packed_join_kernel<D, F16>, a);
+  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], a);
 }
 
 }  // namespace
 
-cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, int cuts,
-                              cudaStream_t s) {
-  if (d == 64) return f16 ? launch_t<64, true>(a, tm, items, cuts, s) : launch_t<64, false>(a, tm, items, cuts, s);
-  return f16 ? launch_t<128, true>(a, tm, items, cuts, s) : launch_t<128, false>(a, tm, items, cuts, s);
+cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s) {
+  if (d == 64) return f16 ? launch_t<64, true>(a, tm, items, s) : launch_t<64, false>(a, tm, items, s);
+  return f16 ? launch_t<128, true>(a, tm, items, s) : launch_t<128, false>(a, tm, items, s);
 }
 
 }  // namespace fa

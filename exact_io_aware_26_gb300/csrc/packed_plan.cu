@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       PackedItem x = unit_x;
       const int r = x.slot, n = packed_units(x.seq, a.tpt, a.bwd);
       x.slot = -1;
+      x.first = x.parts = x.cut = x.unused = 0;
       a.list.items[place_u[r] + (a.bwd ? x.tile : n - 1 - x.tile)] = x;
     });
     if (tid == 0) {
@@ -250,21 +251,21 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   with_units([&](int, const PackedItem& unit_x) {
     PackedItem x = unit_x;
     const int s0 = x.s0, w = x.s1 - x.s0, c = packed_cuts(w, slice);
-    int slot = -1;
+    x.slot = -1;
+    x.first = x.parts = x.cut = x.unused = 0;
     if (c > 1) {
-      slot = atomicAdd(&slot_s, c);
-      PackedItem cut = x;
-      cut.s0 = slot;
-      cut.s1 = c;
-      cut.slot = 0;
-      a.list.cuts[atomicAdd(&cut_s, 1)] = cut;
+      x.first = atomicAdd(&slot_s, c);
+      x.parts = c;
+      x.cut = atomicAdd(&cut_s, 1);
+      a.list.cuts[x.cut] = x;
+      for (int h = 0; h < a.Hk && !a.bwd; ++h) a.list.left[x.cut * a.Hk + h] = 0;
     }
     for (int i = 0; i < c; ++i) {
       int b, e;
       packed_cut(w, c, i, b, e);
       x.s0 = s0 + b;
       x.s1 = s0 + e;
-      x.slot = c > 1 ? slot + i : -1;
+      x.slot = c > 1 ? x.first + i : -1;
       a.list.items[atomicAdd(&class_s[class_of(e - b)], 1)] = x;
     }
   });
