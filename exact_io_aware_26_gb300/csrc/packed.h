@@ -8,7 +8,7 @@ namespace fa {
 
 // The list of a call's work, made on the GPU (packed_plan.cu), in the workspace.
 struct PackedList {
-  int* head;           // [0] items, [1] cut units
+  int* head;           // [0] items, [1] cut units, [2], [3] first query row and end, [4] a counter
   PackedItem* items;
   PackedItem* cuts;    // the cut units (s0, s1: the whole unit's steps)
   int* left;           // of each cut unit and key head: the parts that are done (forward)

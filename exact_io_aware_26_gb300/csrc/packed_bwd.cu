@@ -21,12 +21,39 @@
 // Warp roles as in bwd_tc.cu: 4 NG compute warps in NG groups that split the 128 query
 // columns of a tile (TMEM lane = key row); a producer warp; a warp that owns TMEM and issues the
 // products; at d = 64 four warps that read dQ_i out of TMEM.
+#include <algorithm>
+
 #include "packed.h"
 #include "ptx.cuh"
 #include "tiles.cuh"
 
 namespace fa {
 namespace {
+
+// A CTA's item as its warps use it.
+struct alignas(16) Work {
+  int tile, s0, s1, slot;
+  int hk, key0, keys, first_key;  // the tile's first row of k; its keys; the query that is its first key's
+  int q_last, last_rows, whole_from, q_row0;  // the last query tile and its rows; tiles from which on all see all
+  Work() = default;
+  __device__ __forceinline__ Work(const PackedItem& x, int hk_, const PackedArgs& a) {
+    tile = x.tile;
+    s0 = x.s0;
+    s1 = x.s1;
+    slot = x.slot;
+    hk = hk_;
+    if (tile < 0) return;
+    const int at = tile * kTile, ahead = x.seq.m - x.seq.n;
+    key0 = x.seq.k0 + at;
+    keys = min(kTile, x.seq.m - at);
+    first_key = at - ahead;
+    q_last = (x.seq.n - 1) / a.tpt;
+    last_rows = (x.seq.n - q_last * a.tpt) * a.G;
+    // keys behind the sequence's end are seen by no query
+    whole_from = keys < kTile ? 0x7FFFFFFF : !a.causal ? 0 : max(0, (first_key + keys - 1 + a.tpt - 1) / a.tpt);
+    q_row0 = x.seq.q0 * a.G;
+  }
+};
 
 template <int D>
 struct Layout {
@@ -56,11 +83,13 @@ struct Layout {
   static_assert(STG_SEP || STG_BYTES == DSB, "staging size");
   static constexpr uint32_t BAR = STAT + NS * 256 * 4 + (STG_SEP ? STG_BYTES : 0);
   // 0 kv, 1 s_full, 2 dp_full, 3 dp_free, 4 p_full, 5 ds_full, 6 dq_full, 7 dq_free, 8 done,
-  // 9 pt_free, 10 tail (copies of tiles whose rows are to be zeroed), 11.. q_full, q_empty, ds_free
-  static constexpr uint32_t NBAR = 11 + 2 * NS + NDS;
+  // 9 pt_free, 10 tail (copies of tiles whose rows are to be zeroed), 11 acc_free (dV and dK read),
+  // 12.. item[2], item_free[2], q_full[NS], q_empty[NS], ds_free[NDS]
+  static constexpr uint32_t NBAR = 16 + 2 * NS + NDS;
   static constexpr uint32_t TSLOT = BAR + NBAR * 8;
   static constexpr uint32_t ABORT = TSLOT + 4;
-  static constexpr uint32_t BYTES = ABORT + 4;
+  static constexpr uint32_t ITEM = (ABORT + 4 + 15) & ~15u;  // two of Work
+  static constexpr uint32_t BYTES = ITEM + 2 * sizeof(Work);
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
@@ -97,27 +126,19 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list, the rows' statistics, the zeroed accumulator
-  PackedItem x;
-  int hk;
-  if (!packed_place(a, x, hk)) return;
-  const int kt = x.tile, q_end = x.s1, tpt = a.tpt, G = a.G;
-  const int keys = min(kTile, x.seq.m - kt * kTile);  // of the tile that are the sequence's
-  const int ahead = x.seq.m - x.seq.n;
-  // rows of a query tile: all but the sequence's last one are full
-  const int full = tpt * G, q_last = (x.seq.n - 1) / tpt, last_rows = (x.seq.n - q_last * tpt) * G;
-  auto rows_of = [&](int qt) { return qt == q_last ? last_rows : full; };
-  // some row of the query tiles before this one does not see some key of this tile
-  const int whole_from = !a.causal ? 0 : max(0, (kt * kTile + keys - 1 - ahead + tpt - 1) / tpt);
-  auto diagonal = [&](int qt) { return qt < whole_from; };
-  const int q_row0 = x.seq.q0 * G;  // of the accumulator
+  const int total = a.list.head[0] * a.Hk;
+  if ((int)blockIdx.x >= total) return;
+  const int tpt = a.tpt, G = a.G, full = tpt * G;
 
   auto bar = [&](int i) { return sb + L::BAR + 8u * (uint32_t)i; };
   const uint32_t bar_kv = bar(0), bar_s_full = bar(1), bar_dp_full = bar(2), bar_dp_free = bar(3), bar_p_full = bar(4),
                  bar_ds_full = bar(5), bar_dq_full = bar(6), bar_dq_free = bar(7), bar_done = bar(8),
-                 bar_pt_free = bar(9), bar_tail = bar(10);
-  auto bar_qf = [&](int s) { return bar(11 + s); };
-  auto bar_qe = [&](int s) { return bar(11 + NS + s); };
-  auto bar_ds_free = [&](int b) { return bar(11 + 2 * NS + b); };
+                 bar_pt_free = bar(9), bar_tail = bar(10), bar_acc_free = bar(11);
+  auto bar_item = [&](int k) { return bar(12 + (k & 1)); };
+  auto bar_item_free = [&](int k) { return bar(14 + (k & 1)); };
+  auto bar_qf = [&](int s) { return bar(16 + s); };
+  auto bar_qe = [&](int s) { return bar(16 + NS + s); };
+  auto bar_ds_free = [&](int b) { return bar(16 + 2 * NS + b); };
 
   volatile int* abort_cta = reinterpret_cast<volatile int*>(smem + L::ABORT);
   const WaitCtx w{abort_cta, a.rep.st, a.rep.epoch, a.rep.wait_ns};
@@ -125,24 +146,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     if (threadIdx.x == 0) raise_error(w, FA_ERR_CUDA);
     return;
   }
-  // debug build: the tile lies in its sequence, and that in the tensors
-  if (!dbg_check(w, keys > 0 && x.s0 >= 0 && x.s0 <= x.s1 && x.s1 <= packed_units(x.seq, tpt, false) && x.seq.q0 >= 0 &&
-                        x.seq.q0 + x.seq.n <= a.Tq && x.seq.k0 >= 0 && x.seq.k0 + x.seq.m <= a.Tk && hk < a.Hk))
-    return;
-  const uint32_t q_bytes = (uint32_t)full * D * 2u;
-  auto load_q = [&](int s, int qt, uint32_t at) {  // Q_i and dO_i into stage s
-    const uint32_t dst = sb + L::QS + (uint32_t)s * 2u * L::TILE;
-    const int token = x.seq.q0 + qt * tpt;
-    for (int c = 0; c < D / 64; ++c) {
-      tma_load_3d(dst + c * (kTile * 128), &tmQ, at, c * 64, hk * G, token);
-      tma_load_3d(dst + L::TILE + c * (kTile * 128), &tmdO, at, c * 64, hk * G, token);
-    }
-  };
-  // The producer lane sets up the barriers and issues the copies that need no wait: K_j, V_j and
-  // the first query tiles, up to one with rows to be zeroed.
-  const bool producer = warp == kProd && lane == 0;
-  int pre = 0;
-  if (producer) {
+  if (warp == kProd && lane == 0) {
     mbar_init(bar_kv, 2);
     mbar_init(bar_s_full, 1);
     mbar_init(bar_dp_full, 1);
@@ -155,23 +159,17 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     mbar_init(bar_done, 1);
     mbar_init(bar_pt_free, 1);
     mbar_init(bar_tail, 1);
+    mbar_init(bar_acc_free, L::NCW);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(bar_item(k), 1);
+      mbar_init(bar_item_free(k), L::NCW + 1 + L::NQW);
+    }
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar_qf(s), 1 + 32);  // the copies' arrival and every producer lane
       mbar_init(bar_qe(s), 1);
     }
     *abort_cta = 0;
     fence_barrier_init();
-    const uint32_t at_k = keys < kTile ? bar_tail : bar_kv;
-    mbar_arrive_expect_tx(bar_kv, (keys < kTile ? 1u : 2u) * L::TILE);
-    if (keys < kTile) mbar_arrive_expect_tx(bar_tail, L::TILE);
-    for (int c = 0; c < D / 64; ++c) {
-      tma_load_3d(sb + L::K + c * (kTile * 128), &tmK, at_k, c * 64, hk, x.seq.k0 + kt * kTile);
-      tma_load_3d(sb + L::V + c * (kTile * 128), &tmV, bar_kv, c * 64, hk, x.seq.k0 + kt * kTile);
-    }
-    for (int qt = x.s0; qt < q_end && pre < NS && rows_of(qt) == full; ++qt, ++pre) {
-      mbar_arrive_expect_tx(bar_qf(pre), 2 * q_bytes);
-      load_q(pre, qt, bar_qf(pre));
-    }
   }
   if (full < kTile) {  // rows that no copy writes
     for (int s = 0; s < 2 * NS; ++s) zero_rows<D>(sb + L::QS + (uint32_t)s * L::TILE, full, (int)threadIdx.x, L::NT);
@@ -185,64 +183,109 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::TSLOT);
+  // The CTA's k-th item, which the producer puts into shared memory; tile < 0: there is none left.
+  // Steps are counted through all items (`it`, for the phases of a step's barriers), and so are the
+  // items that have steps (those of kv, done and acc_free); an item without any, whose results
+  // are 0, passes no barrier but its own two.
+  auto place = [&](int k) { return reinterpret_cast<Work*>(smem + L::ITEM) + (k & 1); };
 
   if (warp == kProd) {
     // ------------------------------------------------------------ producer
-    pre = __shfl_sync(0xffffffffu, pre, 0);
-    int it = 0;
-    uint32_t tails = 0;  // copies issued on bar_tail
+    int it = 0, tails = 0, loads = 0;  // stages copied; copies on bar_tail; K_j, V_j copied
     bool go = true;
-    if (keys < kTile) {  // the keys behind the sequence's end
-      tails = 1;
-      go = warp_wait(w, bar_tail, 0);
-      if (go) {
-        zero_rows<D>(sb + L::K, keys, lane, 32);
-        fence_async_smem();
-        __syncwarp();
+    for (int k = 0; go; ++k) {
+      // the first item is the CTA's own, the others are taken in order as CTAs come to need them
+      int index = 0;
+      if (lane == 0) index = k == 0 ? (int)blockIdx.x : (int)gridDim.x + atomicAdd(a.list.head + 4, 1);
+      index = __shfl_sync(0xffffffffu, index, 0);
+      if (k >= 2 && !(go = warp_wait(w, bar_item_free(k), ((k >> 1) - 1) & 1))) break;
+      const int at = a.divHk.div(index), hk = index - at * a.Hk;
+      PackedItem x;
+      x.tile = -1;
+      if (index < total) x = a.list.items[at];
+      // debug build: the tile lies in its sequence, and that in the tensors
+      if (x.tile >= 0 && !__all_sync(0xffffffffu, dbg_check(w, x.tile * kTile < x.seq.m && x.s0 >= 0 && x.s0 <= x.s1 &&
+                                                                   x.s1 <= packed_units(x.seq, tpt, false) && x.seq.q0 >= 0 &&
+                                                                   x.seq.q0 + x.seq.n <= a.Tq && x.seq.k0 >= 0 &&
+                                                                   x.seq.k0 + x.seq.m <= a.Tk && hk < a.Hk)))
+        break;
+      if (lane == 0) {
+        *place(k) = Work(x, hk, a);
+        mbar_arrive(bar_item(k));
       }
-    }
-    if (go && lane == 0) mbar_arrive(bar_kv);
-    const float* lse = a.stat_lse + (long long)hk * a.Tq * G;
-    const float* dsum = a.stat_d + (long long)hk * a.Tq * G;
-    for (int qt = x.s0; go && qt < q_end; ++qt) {
-      const int s = it % NS, rows = rows_of(qt);
-      // statistics, negated as the compute warps use them, loaded before the wait for the stage
-      const long long row0 = (long long)(x.seq.q0 + qt * tpt) * G;
-      float l4[4], d4[4];
+      if (x.tile < 0) break;
+      if (x.s0 == x.s1) continue;  // no query sees the tile
+      const int kt = x.tile, keys = min(kTile, x.seq.m - kt * kTile);
+      const int q_last = (x.seq.n - 1) / tpt, last_rows = (x.seq.n - q_last * tpt) * G;
+      const float* lse = a.stat_lse + (long long)hk * a.Tq * G;
+      const float* dsum = a.stat_d + (long long)hk * a.Tq * G;
+      const uint32_t q_bytes = (uint32_t)full * D * 2u;
+      // Q and dO of the first query tiles go ahead of K_j and V_j, whose places are free when the last
+      // item's products are done; one stage is freed by those products only
+      const int ahead = min(x.s0 + NS - 1, x.s1);
+      for (int qt = x.s0; go && qt <= x.s1; ++qt) {
+        if (qt == ahead) {
+          if (loads > 0 && !(go = warp_wait(w, bar_done, (loads - 1) & 1))) break;
+          const bool tail = keys < kTile;  // rows behind the sequence's end
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar_kv, (tail ? 1u : 2u) * L::TILE);
+            if (tail) mbar_arrive_expect_tx(bar_tail, L::TILE);
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_3d(sb + L::K + c * (kTile * 128), &tmK, tail ? bar_tail : bar_kv, c * 64, hk, x.seq.k0 + kt * kTile);
+              tma_load_3d(sb + L::V + c * (kTile * 128), &tmV, bar_kv, c * 64, hk, x.seq.k0 + kt * kTile);
+            }
+          }
+          ++loads;
+          if (tail) {
+            if (!(go = warp_wait(w, bar_tail, tails++ & 1))) break;
+            zero_rows<D>(sb + L::K, keys, lane, 32);
+            fence_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(bar_kv);
+        }
+        if (qt == x.s1) break;
+        const int s = it % NS, rows = qt == q_last ? last_rows : full, token = x.seq.q0 + qt * tpt;
+        // statistics, negated as the compute warps use them, loaded before the wait for the stage
+        const long long row0 = (long long)token * G;
+        float l4[4], d4[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = 4 * lane + k;
-        l4[k] = r < rows ? -__ldg(lse + row0 + r) : -INFINITY;
-        d4[k] = r < rows ? -__ldg(dsum + row0 + r) : 0.f;
-      }
-      if (it >= NS && !warp_wait(w, bar_qe(s), ((it / NS) - 1) & 1)) break;
-      const bool tail = rows < full;  // the sequence's last query tile
-      if (lane == 0 && it >= pre) {
-        mbar_arrive_expect_tx(tail ? bar_tail : bar_qf(s), 2 * q_bytes);
-        load_q(s, qt, tail ? bar_tail : bar_qf(s));
-      }
-      float* st = reinterpret_cast<float*>(smem + L::STAT) + s * 256;
-      reinterpret_cast<float4*>(st)[lane] = make_float4(l4[0], l4[1], l4[2], l4[3]);
-      reinterpret_cast<float4*>(st + 128)[lane] = make_float4(d4[0], d4[1], d4[2], d4[3]);
-      if (tail) {
-        const uint32_t parity = tails++ & 1u;
-        if (!warp_wait(w, bar_tail, parity)) break;
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * lane + i;
+          l4[i] = r < rows ? -__ldg(lse + row0 + r) : -INFINITY;
+          d4[i] = r < rows ? -__ldg(dsum + row0 + r) : 0.f;
+        }
+        if (it >= NS && !(go = warp_wait(w, bar_qe(s), ((it / NS) - 1) & 1))) break;
+        const bool tail = rows < full;  // the sequence's last query tile
         const uint32_t dst = sb + L::QS + (uint32_t)s * 2u * L::TILE;
-        zero_rows<D>(dst, rows, lane, 32);
-        zero_rows<D>(dst + L::TILE, rows, lane, 32);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_qf(s));
+        if (lane == 0) {
+          const uint32_t on = tail ? bar_tail : bar_qf(s);
+          mbar_arrive_expect_tx(on, 2 * q_bytes);
+          for (int c = 0; c < D / 64; ++c) {
+            tma_load_3d(dst + c * (kTile * 128), &tmQ, on, c * 64, hk * G, token);
+            tma_load_3d(dst + L::TILE + c * (kTile * 128), &tmdO, on, c * 64, hk * G, token);
+          }
+        }
+        float* st = reinterpret_cast<float*>(smem + L::STAT) + s * 256;
+        reinterpret_cast<float4*>(st)[lane] = make_float4(l4[0], l4[1], l4[2], l4[3]);
+        reinterpret_cast<float4*>(st + 128)[lane] = make_float4(d4[0], d4[1], d4[2], d4[3]);
+        if (tail) {
+          if (!(go = warp_wait(w, bar_tail, tails++ & 1))) break;
+          zero_rows<D>(dst, rows, lane, 32);
+          zero_rows<D>(dst + L::TILE, rows, lane, 32);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_qf(s));
+        }
+        mbar_arrive(bar_qf(s));
+        ++it;
       }
-      mbar_arrive(bar_qf(s));
-      ++it;
     }
     if (lane == 0) {  // every copy has landed before the CTA ends
-      if (tails > 0) mbar_drain(w, bar_tail, (tails - 1) & 1u);
-      mbar_drain(w, bar_kv, 0);
-      const int issued = it > pre ? it : pre;
+      if (tails > 0) mbar_drain(w, bar_tail, (tails - 1) & 1);
+      if (loads > 0) mbar_drain(w, bar_kv, (loads - 1) & 1);
       for (int s = 0; s < NS; ++s) {
-        const int n = (issued - s + NS - 1) / NS;
+        const int n = (it - s + NS - 1) / NS;
         if (n > 0) mbar_drain(w, bar_qf(s), (n - 1) & 1);
       }
     }
@@ -251,6 +294,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     // Per query tile i, in the order of bwd_tc.cu:
     //   d = 64:  S^T_{i+1}, dV_i, dP^T_{i+1}, then dQ_i, dK_i
     //   d = 128: dV_i, S^T_{i+1} (over P^T), then dQ_i, dK_i, dP^T_{i+1} (over dQ_i)
+    // and at an item's first tile S^T and dP^T by themselves, beside the results' way out.
     constexpr uint32_t idS = idesc_f16(F16, kTile, kTile, false, false);
     constexpr uint32_t idKV = idesc_f16(F16, kTile, D, false, true);
     constexpr uint32_t idQ = idesc_f16(F16, kTile, D, true, true);
@@ -272,82 +316,100 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       tc_mma_ss_elect(tDP, dV_k + kmajor_step(kk, kTile),
                       desc_add(dQ_k0, stage_off(it) + L::TILE) + kmajor_step(kk, kTile), idS, kk > 0 ? 1u : 0u);
     };
-    auto mma_dv = [&](int it, int kk) {
+    auto mma_dv = [&](int it, int kk, bool first) {
       tc_mma_ts_elect(tDV, tmem + L::pt_col(kk), desc_add(dQ_mn0, stage_off(it) + L::TILE) + mnmajor_step(kk), idKV,
-                      (it > 0 || kk > 0) ? 1u : 0u);
+                      (!first || kk > 0) ? 1u : 0u);
     };
-    auto mma_dk = [&](int it, int kk) {
+    auto mma_dk = [&](int it, int kk, bool first) {
       tc_mma_ss_elect(tDK, desc_add(dS_k, ds_off(it)) + kmajor_step(kk, kTile),
-                      desc_add(dQ_mn0, stage_off(it)) + mnmajor_step(kk), idKV, (it > 0 || kk > 0) ? 1u : 0u);
+                      desc_add(dQ_mn0, stage_off(it)) + mnmajor_step(kk), idKV, (!first || kk > 0) ? 1u : 0u);
     };
     auto mma_dq = [&](int it, int kk) {
       tc_mma_ss_elect(tDQ, desc_add(dS_mn, ds_off(it)) + mnmajor_step(kk), dK_mn + mnmajor_step(kk), idQ,
                       kk > 0 ? 1u : 0u);
     };
-    bool ok = warp_wait(w, bar_kv, 0);
-    int qt = x.s0;
-    if (ok && qt < q_end && (ok = warp_wait(w, bar_qf(0), 0))) {
+    bool ok = true;
+    int it = 0, n = 0;  // steps, items with steps
+    for (int k = 0; ok; ++k) {
+      if (!(ok = warp_wait(w, bar_item(k), (k >> 1) & 1))) break;
+      const int tile = place(k)->tile, steps = place(k)->s1 - place(k)->s0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_item_free(k));
+      if (tile < 0) break;
+      if (steps == 0) continue;
+      if (!(ok = warp_wait(w, bar_kv, n & 1))) break;
+      if (!(ok = warp_wait(w, bar_qf(it % NS), (it / NS) & 1))) break;
+      // dP^T goes where the last item's was, and at d = 128 its dQ
+      if (it > 0 && !(ok = warp_wait(w, bar_dp_free, (it - 1) & 1))) break;
+      if (L::ALIAS && it > 0 && !(ok = warp_wait(w, bar_dq_free, (it - 1) & 1))) break;
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        mma_s(0, kk);
-        mma_dp(0, kk);
-      }
+      for (int kk = 0; kk < KS; ++kk) mma_s(it, kk);
       tc_commit_elect(bar_s_full);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) mma_dp(it, kk);
       tc_commit_elect(bar_dp_full);
-    }
-    for (int it = 0; ok && qt < q_end; ++it, ++qt) {
-      const bool next = qt + 1 < q_end;
-      if (!(ok = warp_wait(w, bar_p_full, it & 1))) break;
-      if (next && !(ok = warp_wait(w, bar_qf((it + 1) % NS), ((it + 1) / NS) & 1))) break;
-      tc_fence_after();
-      if (!L::ALIAS) {
-        if (next) {
+      // dV and dK go where the last item's were
+      if (n > 0 && !(ok = warp_wait(w, bar_acc_free, (n - 1) & 1))) break;
+      for (int j = 0; j < steps; ++j, ++it) {
+        const bool next = j + 1 < steps, first = j == 0;
+        if (!(ok = warp_wait(w, bar_p_full, it & 1))) break;
+        if (next && !(ok = warp_wait(w, bar_qf((it + 1) % NS), ((it + 1) / NS) & 1))) break;
+        tc_fence_after();
+        if (!L::ALIAS) {
+          if (next) {
 #pragma unroll
-          for (int kk = 0; kk < KS; ++kk) mma_s(it + 1, kk);
-          tc_commit_elect(bar_s_full);
+            for (int kk = 0; kk < KS; ++kk) mma_s(it + 1, kk);
+            tc_commit_elect(bar_s_full);
+          }
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) mma_dv(it, kk, first);
+          tc_commit_elect(bar_pt_free);
+          if (next) {
+            if (!(ok = warp_wait(w, bar_dp_free, it & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) mma_dp(it + 1, kk);
+            tc_commit_elect(bar_dp_full);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) mma_dv(it, kk, first);
+          if (next) {
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) mma_s(it + 1, kk);
+            tc_commit_elect(bar_s_full);
+          }
         }
+        if (!(ok = warp_wait(w, bar_ds_full, it & 1))) break;
+        if (!L::ALIAS && it > 0 && !(ok = warp_wait(w, bar_dq_free, (it - 1) & 1))) break;
+        tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) mma_dv(it, kk);
-        tc_commit_elect(bar_pt_free);
-        if (next) {
+        for (int kk = 0; kk < kTile / 16; ++kk) mma_dq(it, kk);
+        if (L::STG_SEP) tc_commit_elect(bar_dq_full);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) mma_dk(it, kk, first);
+        if (!L::STG_SEP) tc_commit_elect(bar_dq_full);  // the boxes lie over the dS^T that dK_i reads
+        tc_commit_elect(bar_ds_free(it % L::NDS));
+        tc_commit_elect(bar_qe(it % NS));
+        if (L::ALIAS && next) {  // dP^T_{i+1} goes over dQ_i
           if (!(ok = warp_wait(w, bar_dp_free, it & 1))) break;
+          if (!(ok = warp_wait(w, bar_dq_free, it & 1))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) mma_dp(it + 1, kk);
           tc_commit_elect(bar_dp_full);
         }
-      } else {
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) mma_dv(it, kk);
-        if (next) {
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) mma_s(it + 1, kk);
-          tc_commit_elect(bar_s_full);
-        }
       }
-      if (!(ok = warp_wait(w, bar_ds_full, it & 1))) break;
-      if (!L::ALIAS && it > 0 && !(ok = warp_wait(w, bar_dq_free, (it - 1) & 1))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk) mma_dq(it, kk);
-      if (L::STG_SEP) tc_commit_elect(bar_dq_full);
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk) mma_dk(it, kk);
-      if (!L::STG_SEP) tc_commit_elect(bar_dq_full);  // the boxes lie over the dS^T that dK_i reads
-      tc_commit_elect(bar_ds_free(it % L::NDS));
-      tc_commit_elect(bar_qe(it % NS));
-      if (L::ALIAS && next) {  // dP^T_{i+1} goes over dQ_i
-        if (!(ok = warp_wait(w, bar_dp_free, it & 1))) break;
-        if (!(ok = warp_wait(w, bar_dq_free, it & 1))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) mma_dp(it + 1, kk);
-        tc_commit_elect(bar_dp_full);
-      }
+      if (!ok) break;
+      tc_commit_elect(bar_done);
+      ++n;
     }
-    tc_commit_elect(bar_done);
-    if (lane == 0) mbar_drain(w, bar_done, 0);
+    if (!ok) {  // a wait gave up: what is under way completes this phase
+      tc_commit_elect(bar_done);
+      ++n;
+    }
+    if (n > 0 && lane == 0) mbar_drain(w, bar_done, (n - 1) & 1);  // before TMEM is released
     __syncwarp();
   } else if (warp > kMma) {
     if constexpr (L::QW) {
@@ -355,42 +417,49 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       const int qd = warp & 3;
       const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
       const uint32_t stg = sb + L::STG + (uint32_t)qd * L::BOXB;
-      bool pend = false;  // a reduce may still be reading the box
+      bool pend = false, ok = true;  // pend: a reduce may still be reading the box
       int it = 0;
-      for (int qt = x.s0; qt < q_end; ++qt, ++it) {
-        if (!warp_wait(w, bar_dq_full, it & 1)) break;
-        tc_fence_after();
-        const int rows = rows_of(qt);
-        const bool dead = 32 * qd + lane >= rows;  // a row of 0: of no query, or another sequence's
+      for (int k = 0; ok; ++k) {
+        if (!warp_wait(w, bar_item(k), (k >> 1) & 1)) break;
+        const Work x = *place(k);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_item_free(k));
+        if (x.tile < 0) break;
+        for (int qt = x.s0; qt < x.s1; ++qt, ++it) {
+          if (!(ok = warp_wait(w, bar_dq_full, it & 1))) break;
+          tc_fence_after();
+          const int rows = qt == x.q_last ? x.last_rows : full;
+          const bool dead = 32 * qd + lane >= rows;  // a row of 0: of no query, or another sequence's
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += L::DQC) {
-          uint32_t dq[L::DQC];
-          tmem_ld_n<L::DQC>(tmem + L::T_DQ + lane_off + (uint32_t)c0, dq);
-          if (c0 + L::DQC == D) {  // dQ_i is in registers: the next one may be computed
-            tc_fence_before();
+          for (int c0 = 0; c0 < D; c0 += L::DQC) {
+            uint32_t dq[L::DQC];
+            tmem_ld_n<L::DQC>(tmem + L::T_DQ + lane_off + (uint32_t)c0, dq);
+            if (c0 + L::DQC == D) {  // dQ_i is in registers: the next one may be computed
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_dq_free);
+            }
+            if (32 * qd >= rows) continue;
+            if (pend) {
+              if (lane == 0) bulk_wait_group_read0();
+              __syncwarp();
+            }
+            if (dead) {
+#pragma unroll
+              for (int i = 0; i < L::DQC; ++i) dq[i] = 0u;
+            }
+#pragma unroll
+            for (int v = 0; v < L::DQC / 4; ++v)
+              st_shared_v4(stg + (uint32_t)lane * 128u + (uint32_t)((v ^ (lane & 7)) * 16), dq[4 * v], dq[4 * v + 1],
+                           dq[4 * v + 2], dq[4 * v + 3]);
+            fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_dq_free);
+            if (lane == 0) {
+              tma_reduce_add_3d(&tmdQ, stg, c0, x.q_row0 + qt * full + qd * 32, x.hk);
+              bulk_commit_group();
+            }
+            pend = true;
           }
-          if (32 * qd >= rows) continue;
-          if (pend) {
-            if (lane == 0) bulk_wait_group_read0();
-            __syncwarp();
-          }
-          if (dead) {
-#pragma unroll
-            for (int k = 0; k < L::DQC; ++k) dq[k] = 0u;
-          }
-#pragma unroll
-          for (int v = 0; v < L::DQC / 4; ++v)
-            st_shared_v4(stg + (uint32_t)lane * 128u + (uint32_t)((v ^ (lane & 7)) * 16), dq[4 * v], dq[4 * v + 1],
-                         dq[4 * v + 2], dq[4 * v + 3]);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_reduce_add_3d(&tmdQ, stg, c0, q_row0 + qt * full + qd * 32, hk);
-            bulk_commit_group();
-          }
-          pend = true;
         }
       }
       if (lane == 0) bulk_wait_group0();
@@ -402,13 +471,6 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     const int r = (warp & 3) * 32 + lane;  // key row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint64_t c2p = f2pack(a.scale_log2, a.scale_log2);
-    const bool tail = keys < kTile;
-    // the first of the warpgroup's columns whose query sees this key
-    const int sees = r >= keys ? 1 << 30 : a.causal ? kt * kTile + r - ahead : 0;  // the first query that sees it
-    auto first_col = [&](int qt) {
-      const int i = sees - qt * tpt;
-      return (i <= 0 ? 0 : i >= tpt ? kTile : i * G) - CW * g;
-    };
     const uint32_t stg = sb + L::STG + (uint32_t)warp * L::BOXB;
     bool pend = false;
     auto stg_acquire = [&]() {
@@ -419,191 +481,206 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       }
     };
     auto stat = [&](int it) { return reinterpret_cast<const float*>(smem + L::STAT) + (it % NS) * 256; };
-    float p[CW];
-    // S^T -> P^T: fp32 in p[] for dS, 16-bit into TMEM for dV
-    auto p_phase = [&](int it, int qt) -> bool {
-      if (!warp_wait(w, bar_qf(it % NS), (it / NS) & 1)) return false;
-      if (!warp_wait(w, bar_s_full, it & 1)) return false;
-      tc_fence_after();
-      {
-        uint32_t u[CW];
-        tmem_ld_n<CW>(tmem + L::T_S + lane_off + CW * g, u);
-#pragma unroll
-        for (int c = 0; c < CW; ++c) p[c] = __uint_as_float(u[c]);
-      }
-      const float4* nl4 = reinterpret_cast<const float4*>(stat(it) + CW * g);  // -LSE log2 e
-      uint32_t pk[CW / 2];
-#pragma unroll
-      for (int c = 0; c < CW; c += 4) {
-        const float4 nl = nl4[c / 4];
-        float x0, x1, x2, x3;
-        f2unpack(ffma2(f2pack(p[c], p[c + 1]), c2p, f2pack(nl.x, nl.y)), x0, x1);
-        f2unpack(ffma2(f2pack(p[c + 2], p[c + 3]), c2p, f2pack(nl.z, nl.w)), x2, x3);
-        p[c] = ex2(x0);
-        p[c + 1] = ex2(x1);
-        p[c + 2] = ex2(x2);
-        p[c + 3] = ex2(x3);
-      }
-      if (tail || diagonal(qt)) {
-        const int first = first_col(qt);
-#pragma unroll
-        for (int c = 0; c < CW; ++c)
-          if (c < first) p[c] = 0.f;
-      }
-#pragma unroll
-      for (int c = 0; c < CW; c += 2) pk[c / 2] = pack2<F16>(p[c], p[c + 1]);
-      if constexpr (!L::ALIAS) {
-        if (it > 0) {  // dV of the tile before has read its P^T
-          if (!warp_wait(w, bar_pt_free, (it - 1) & 1)) return false;
-          tc_fence_after();
-        }
-      }
-      tmem_st_n<CW / 2>(tmem + L::pt_write_col(g) + lane_off, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p_full);
-      return true;
-    };
     bool ok = true;
-    int it = 0;
-    int qt = x.s0;
-    if (qt < q_end) ok = p_phase(0, qt);
-    for (; ok && qt < q_end; ++it, ++qt) {
-      // ---- dS_i = P_i (dP_i - D)
-      if (!(ok = warp_wait(w, bar_dp_full, it & 1))) break;
-      tc_fence_after();
-      uint32_t pk[CW / 2];
-      const float4* nd4 = reinterpret_cast<const float4*>(stat(it) + 128 + CW * g);  // -D
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        constexpr int HW = CW / 2;
-        uint32_t u[HW];
-        tmem_ld_n<HW>(tmem + L::T_DP + lane_off + CW * g + HW * hf, u);
-        if (hf == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_dp_free);
-        }
-#pragma unroll
-        for (int c = 0; c < HW; c += 4) {
-          const int cc = HW * hf + c;
-          const float4 nd = nd4[cc / 4];
-          float y0, y1, y2, y3;
-          f2unpack(fmul2(f2pack(p[cc], p[cc + 1]),
-                         fadd2(f2pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), f2pack(nd.x, nd.y))),
-                   y0, y1);
-          f2unpack(fmul2(f2pack(p[cc + 2], p[cc + 3]),
-                         fadd2(f2pack(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), f2pack(nd.z, nd.w))),
-                   y2, y3);
-          pk[cc / 2] = pack2<F16>(y0, y1);
-          pk[cc / 2 + 1] = pack2<F16>(y2, y3);
-        }
-      }
-      if (tail || diagonal(qt)) {  // 0, whatever dP is there
-        const int first = first_col(qt);
-#pragma unroll
-        for (int c = 0; c < CW; c += 2) {
-          if (c < first) pk[c / 2] &= 0xFFFF0000u;
-          if (c + 1 < first) pk[c / 2] &= 0x0000FFFFu;
-        }
-      }
-      if (it >= L::NDS && !(ok = warp_wait(w, bar_ds_free(it % L::NDS), ((it / L::NDS) - 1) & 1))) break;
-      if (!L::STG_SEP) stg_acquire();
-#pragma unroll
-      for (int ch = 0; ch < CW / 8; ++ch)
-        st_shared_v4(sb + L::DST + (uint32_t)(it % L::NDS) * L::DSB + sw128_chunk_offset(r, (CW / 8) * g + ch, kTile),
-                     pk[ch * 4 + 0], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_ds_full);
-
-      // ---- P of the next query tile, while dK_i, dQ_i, dP^T_{i+1} run
-      if (qt + 1 < q_end && !(ok = p_phase(it + 1, qt + 1))) break;
-
-      // ---- dQ_i -> the fp32 accumulator (d = 128; at d = 64 the dQ warps' job)
-      if constexpr (!L::QW) {
-        if (!(ok = warp_wait(w, bar_dq_full, it & 1))) break;
+    int it = 0, n = 0;  // steps, items with steps
+    for (int k = 0; ok; ++k) {
+      if (!(ok = warp_wait(w, bar_item(k), (k >> 1) & 1))) break;
+      const Work* x = place(k);
+      if (x->tile < 0) break;
+      const int s0 = x->s0, q_end = x->s1;
+      // query tiles some row of which does not see some key of the tile; the first query that sees this key
+      const int whole_from = x->whole_from, sees = r >= x->keys ? 1 << 30 : a.causal ? x->first_key + r : 0;
+      // the first of the warpgroup's columns whose query sees this key
+      auto first_col = [&](int qt) {
+        const int i = sees - qt * tpt;
+        return (i <= 0 ? 0 : i >= tpt ? kTile : i * G) - CW * g;
+      };
+      float p[CW];
+      // S^T -> P^T: fp32 in p[] for dS, 16-bit into TMEM for dV
+      auto p_phase = [&](int it, int qt) -> bool {
+        if (!warp_wait(w, bar_qf(it % NS), (it / NS) & 1)) return false;
+        if (!warp_wait(w, bar_s_full, it & 1)) return false;
         tc_fence_after();
-        const int rows = rows_of(qt);
-        uint32_t dq[L::DQG];
-        tmem_ld_n<L::DQG>(tmem + L::T_DQ + lane_off + g * L::DQG, dq);
+        {
+          uint32_t u[CW];
+          tmem_ld_n<CW>(tmem + L::T_S + lane_off + CW * g, u);
+#pragma unroll
+          for (int c = 0; c < CW; ++c) p[c] = __uint_as_float(u[c]);
+        }
+        const float4* nl4 = reinterpret_cast<const float4*>(stat(it) + CW * g);  // -LSE log2 e
+        uint32_t pk[CW / 2];
+#pragma unroll
+        for (int c = 0; c < CW; c += 4) {
+          const float4 nl = nl4[c / 4];
+          float x0, x1, x2, x3;
+          f2unpack(ffma2(f2pack(p[c], p[c + 1]), c2p, f2pack(nl.x, nl.y)), x0, x1);
+          f2unpack(ffma2(f2pack(p[c + 2], p[c + 3]), c2p, f2pack(nl.z, nl.w)), x2, x3);
+          p[c] = ex2(x0);
+          p[c + 1] = ex2(x1);
+          p[c + 2] = ex2(x2);
+          p[c + 3] = ex2(x3);
+        }
+        if (qt < whole_from) {
+          const int first = first_col(qt);
+#pragma unroll
+          for (int c = 0; c < CW; ++c)
+            if (c < first) p[c] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < CW; c += 2) pk[c / 2] = pack2<F16>(p[c], p[c + 1]);
+        if constexpr (!L::ALIAS) {
+          if (it > 0) {  // dV of the tile before has read its P^T
+            if (!warp_wait(w, bar_pt_free, (it - 1) & 1)) return false;
+            tc_fence_after();
+          }
+        }
+        tmem_st_n<CW / 2>(tmem + L::pt_write_col(g) + lane_off, pk);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_dq_free);
-        if (32 * (warp & 3) < rows) {
-          if (r >= rows) {  // a row of 0: of no query, or another sequence's
+        if (lane == 0) mbar_arrive(bar_p_full);
+        return true;
+      };
+      if (s0 < q_end) ok = p_phase(it, s0);
+      for (int qt = s0; ok && qt < q_end; ++it, ++qt) {
+        // ---- dS_i = P_i (dP_i - D)
+        if (!(ok = warp_wait(w, bar_dp_full, it & 1))) break;
+        tc_fence_after();
+        uint32_t pk[CW / 2];
+        const float4* nd4 = reinterpret_cast<const float4*>(stat(it) + 128 + CW * g);  // -D
 #pragma unroll
-            for (int k = 0; k < L::DQG; ++k) dq[k] = 0u;
+        for (int hf = 0; hf < 2; ++hf) {
+          constexpr int HW = CW / 2;
+          uint32_t u[HW];
+          tmem_ld_n<HW>(tmem + L::T_DP + lane_off + CW * g + HW * hf, u);
+          if (hf == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_dp_free);
           }
 #pragma unroll
-          for (int c0 = 0; c0 < L::DQG; c0 += L::DQC) {
-            stg_acquire();
+          for (int c = 0; c < HW; c += 4) {
+            const int cc = HW * hf + c;
+            const float4 nd = nd4[cc / 4];
+            float y0, y1, y2, y3;
+            f2unpack(fmul2(f2pack(p[cc], p[cc + 1]),
+                           fadd2(f2pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), f2pack(nd.x, nd.y))),
+                     y0, y1);
+            f2unpack(fmul2(f2pack(p[cc + 2], p[cc + 3]),
+                           fadd2(f2pack(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), f2pack(nd.z, nd.w))),
+                     y2, y3);
+            pk[cc / 2] = pack2<F16>(y0, y1);
+            pk[cc / 2 + 1] = pack2<F16>(y2, y3);
+          }
+        }
+        if (qt < whole_from) {  // 0, whatever dP is there
+          const int first = first_col(qt);
 #pragma unroll
-            for (int v = 0; v < L::DQC / 4; ++v)
-              st_shared_v4(stg + (uint32_t)lane * 128u + (uint32_t)((v ^ (lane & 7)) * 16), dq[c0 + 4 * v],
-                           dq[c0 + 4 * v + 1], dq[c0 + 4 * v + 2], dq[c0 + 4 * v + 3]);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_reduce_add_3d(&tmdQ, stg, g * L::DQG + c0, q_row0 + qt * full + (warp & 3) * 32, hk);
-              bulk_commit_group();
+          for (int c = 0; c < CW; c += 2) {
+            if (c < first) pk[c / 2] &= 0xFFFF0000u;
+            if (c + 1 < first) pk[c / 2] &= 0x0000FFFFu;
+          }
+        }
+        if (it >= L::NDS && !(ok = warp_wait(w, bar_ds_free(it % L::NDS), ((it / L::NDS) - 1) & 1))) break;
+        if (!L::STG_SEP) stg_acquire();
+#pragma unroll
+        for (int ch = 0; ch < CW / 8; ++ch)
+          st_shared_v4(sb + L::DST + (uint32_t)(it % L::NDS) * L::DSB + sw128_chunk_offset(r, (CW / 8) * g + ch, kTile),
+                       pk[ch * 4 + 0], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ds_full);
+
+        // ---- P of the next query tile, while dK_i, dQ_i, dP^T_{i+1} run
+        if (qt + 1 < q_end && !(ok = p_phase(it + 1, qt + 1))) break;
+
+        // ---- dQ_i -> the fp32 accumulator (d = 128; at d = 64 the dQ warps' job)
+        if constexpr (!L::QW) {
+          if (!(ok = warp_wait(w, bar_dq_full, it & 1))) break;
+          tc_fence_after();
+          const int rows = qt == x->q_last ? x->last_rows : full;
+          uint32_t dq[L::DQG];
+          tmem_ld_n<L::DQG>(tmem + L::T_DQ + lane_off + g * L::DQG, dq);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_dq_free);
+          if (32 * (warp & 3) < rows) {
+            if (r >= rows) {  // a row of 0: of no query, or another sequence's
+#pragma unroll
+              for (int i = 0; i < L::DQG; ++i) dq[i] = 0u;
             }
-            pend = true;
+#pragma unroll
+            for (int c0 = 0; c0 < L::DQG; c0 += L::DQC) {
+              stg_acquire();
+#pragma unroll
+              for (int v = 0; v < L::DQC / 4; ++v)
+                st_shared_v4(stg + (uint32_t)lane * 128u + (uint32_t)((v ^ (lane & 7)) * 16), dq[c0 + 4 * v],
+                             dq[c0 + 4 * v + 1], dq[c0 + 4 * v + 2], dq[c0 + 4 * v + 3]);
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_reduce_add_3d(&tmdQ, stg, g * L::DQG + c0, x->q_row0 + qt * full + (warp & 3) * 32, x->hk);
+                bulk_commit_group();
+              }
+              pend = true;
+            }
           }
         }
       }
+      // ------------------------------------------------------------ dK, dV of the item
+      if (!ok) break;
+      const bool have = q_end > s0;
+      if (have && !(ok = warp_wait(w, bar_done, n++ & 1))) break;
+      tc_fence_after();
+      {
+        const bool store = r < x->keys;
+        const int hk = x->hk, token = x->key0 + r;
+        float* part = x->slot < 0 ? nullptr
+                                  : a.slots + ((long long)x->slot * a.Hk + hk) * (2 * kTile * D) + 4 * (g * L::DQG / 4 * kTile + r);
+        constexpr int EC = L::DQG < 32 ? L::DQG : 32;
+        for (int which = 0; which < 2; ++which) {
+          const uint32_t col = (which == 0 ? L::T_DV : L::T_DK) + g * L::DQG;
+          const float mul = which == 0 ? 1.f : a.scale;
+          const long long* st = which == 0 ? a.dvs : a.dks;
+          uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) + (long long)token * st[0] + hk * st[1] + g * L::DQG;
+#pragma unroll
+          for (int c0 = 0; c0 < L::DQG; c0 += EC) {
+            uint32_t u[EC];
+            if (have) {
+              tmem_ld_n<EC>(tmem + col + lane_off + c0, u);
+            } else {
+#pragma unroll
+              for (int i = 0; i < EC; ++i) u[i] = 0u;
+            }
+            if (have && which == 1 && c0 + EC == L::DQG) {  // all is in registers: the next item's dV and dK may go there
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_acc_free);
+            }
+            if (part) {  // four channels of all keys side by side: a warp's stores are whole lines
+#pragma unroll
+              for (int v = 0; v < EC / 4; ++v)
+                *reinterpret_cast<uint4*>(part + which * (kTile * D) + 4 * kTile * (c0 / 4 + v)) =
+                    make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
+            } else if (store) {
+#pragma unroll
+              for (int v = 0; v < EC / 8; ++v) {
+                uint4 q;
+                q.x = pack2<F16>(__uint_as_float(u[v * 8 + 0]) * mul, __uint_as_float(u[v * 8 + 1]) * mul);
+                q.y = pack2<F16>(__uint_as_float(u[v * 8 + 2]) * mul, __uint_as_float(u[v * 8 + 3]) * mul);
+                q.z = pack2<F16>(__uint_as_float(u[v * 8 + 4]) * mul, __uint_as_float(u[v * 8 + 5]) * mul);
+                q.w = pack2<F16>(__uint_as_float(u[v * 8 + 6]) * mul, __uint_as_float(u[v * 8 + 7]) * mul);
+                *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q;
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (lane == 0) mbar_arrive(bar_item_free(k));
     }
     if (lane == 0) bulk_wait_group0();
-    __syncwarp();
-    // ------------------------------------------------------------ dK, dV
-    bool have = false;
-    if (ok) {
-      ok = warp_wait(w, bar_done, 0);
-      tc_fence_after();
-      have = ok && it > 0;
-    }
-    if (ok) {
-      const int token = x.seq.k0 + kt * kTile + r;
-      const bool store = r < keys && dbg_check(w, token < a.Tk);
-      float* part = x.slot < 0 ? nullptr
-                               : a.slots + ((long long)x.slot * a.Hk + hk) * (2 * kTile * D) + 4 * (g * L::DQG / 4 * kTile + r);
-      constexpr int EC = L::DQG < 32 ? L::DQG : 32;
-      for (int which = 0; which < 2; ++which) {
-        const uint32_t col = (which == 0 ? L::T_DV : L::T_DK) + g * L::DQG;
-        const float mul = which == 0 ? 1.f : a.scale;
-        const long long* st = which == 0 ? a.dvs : a.dks;
-        uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) + (long long)token * st[0] + hk * st[1] + g * L::DQG;
-#pragma unroll
-        for (int c0 = 0; c0 < L::DQG; c0 += EC) {
-          uint32_t u[EC];
-          if (have) {
-            tmem_ld_n<EC>(tmem + col + lane_off + c0, u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < EC; ++k) u[k] = 0u;
-          }
-          if (part) {  // four channels of all keys side by side: a warp's stores are whole lines
-#pragma unroll
-            for (int v = 0; v < EC / 4; ++v)
-              *reinterpret_cast<uint4*>(part + which * (kTile * D) + 4 * kTile * (c0 / 4 + v)) =
-                  make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
-          } else if (store) {
-#pragma unroll
-            for (int v = 0; v < EC / 8; ++v) {
-              uint4 q;
-              q.x = pack2<F16>(__uint_as_float(u[v * 8 + 0]) * mul, __uint_as_float(u[v * 8 + 1]) * mul);
-              q.y = pack2<F16>(__uint_as_float(u[v * 8 + 2]) * mul, __uint_as_float(u[v * 8 + 3]) * mul);
-              q.z = pack2<F16>(__uint_as_float(u[v * 8 + 4]) * mul, __uint_as_float(u[v * 8 + 5]) * mul);
-              q.w = pack2<F16>(__uint_as_float(u[v * 8 + 6]) * mul, __uint_as_float(u[v * 8 + 7]) * mul);
-              *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q;
-            }
-          }
-          __syncwarp();
-        }
-      }
-    }
   }
 
   tc_fence_before();
@@ -718,10 +795,13 @@ struct Launch {
   }
 };
 
+int sms() {
+  int dev = 0, n = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
 int stream_blocks(long long threads) {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const long long blocks = (threads + 255) / 256, most = (long long)sms * 8;
+  const long long blocks = (threads + 255) / 256, most = (long long)sms() * 8;
   return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
 
@@ -731,7 +811,7 @@ cudaError_t main_t(const PackedArgs& a, const CUtensorMap* tm, int items, cudaSt
   const auto kern = packed_bwd_kernel<D, F16>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
   if (e != cudaSuccess) return e;
-  Launch l((long long)items * a.Hk, L::NT, L::BYTES, s);
+  Launch l(std::min((long long)items * a.Hk, (long long)sms()), L::NT, L::BYTES, s);
   return cudaLaunchKernelEx(&l.cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], a);
 }
 template <int D, bool F16>

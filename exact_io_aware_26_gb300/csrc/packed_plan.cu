@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       a.list.head[1] = 0;
       a.list.head[2] = first_q[0];  // query rows that are a sequence's
       a.list.head[3] = first_q[R];
+      a.list.head[4] = 0;  // items taken by CTAs that were done with theirs (backward)
     }
     return;
   }
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     a.list.head[1] = cut_s;
     a.list.head[2] = first_q[0];  // query rows that are a sequence's
     a.list.head[3] = first_q[R];
+    a.list.head[4] = 0;  // items taken by CTAs that were done with theirs (backward)
   }
 }
 
