@@ -98,14 +98,9 @@ __device__ __forceinline__ void fwd_drain_copies(const WaitCtx& w, const FwdBars
 // has read P~.  issue_s(stage) issues the products of S = Q K_stage^T;
 // issue_pv(stage, j) those of O += P~ V_stage (O overwritten when j = 0).  At the
 // end every MMA issued must have completed before TMEM is released.
-// ready(stage, key tile, j), where given, runs before the wait for P~_j (it may wait for V_j, and
-// look it over while the softmax runs); false: a wait gave up.
-struct FwdAlwaysReady {
-  __device__ __forceinline__ bool operator()(int, int, int) const { return true; }
-};
-template <int NS, bool PSEP, class Next, class IssueS, class IssuePV, class Ready = FwdAlwaysReady>
+template <int NS, bool PSEP, class Next, class IssueS, class IssuePV>
 __device__ __forceinline__ void fwd_mma_schedule(const WaitCtx& w, const FwdBars<NS>& b, int kt, int kt_end,
-                                                 Next next, IssueS issue_s, IssuePV issue_pv, Ready ready = Ready()) {
+                                                 Next next, IssueS issue_s, IssuePV issue_pv) {
   auto s_tile = [&](int it) -> bool {
     const int st = it % NS;
     if (!warp_wait(w, b.kf(st), (it / NS) & 1)) return false;
@@ -124,7 +119,6 @@ __device__ __forceinline__ void fwd_mma_schedule(const WaitCtx& w, const FwdBars
       if (!(ok = warp_wait(w, b.sfree(), it & 1))) break;
       if (!(ok = s_tile(it + 1))) break;
     }
-    if (!(ok = ready(st, kt, it))) break;
     if (!(ok = warp_wait(w, b.p(), it & 1))) break;
     if (!(ok = warp_wait(w, b.vf(st), (it / NS) & 1))) break;
     tc_fence_after();

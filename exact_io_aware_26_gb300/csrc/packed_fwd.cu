@@ -18,6 +18,8 @@
 //
 // Warp roles (192 threads) as in fwd_tc.cu: warps 0-3 softmax (thread = row = TMEM lane), warp
 // 4 TMA producer, warp 5 TMEM owner and MMA issuer.
+#include <algorithm>
+
 #include "fwd_common.cuh"
 #include "packed.h"
 
@@ -28,6 +30,25 @@ constexpr float kRescaleThr = 8.f;  // the running maximum moves past 2^8 only
 constexpr float kLargeScore = 65536.f;  // log2 units, from which on the maximum is taken off first
 constexpr int kNone = 0x7FFFFFFF;
 
+// A CTA's item as its warps use it.
+struct alignas(16) Work {
+  PackedItem x;
+  int hk, rows, pos0, seen_by_all;  // key head; rows that are the sequence's; the first row's place among the keys
+  int scrub;                        // first key tile some of whose values were zeroed
+  int cuts, unused[2];              // parts of cut units that the CTA had before
+  Work() = default;
+  __device__ __forceinline__ Work(const PackedItem& item, int hk_, int cuts_, const PackedArgs& a) {
+    x = item;
+    hk = hk_;
+    cuts = cuts_;
+    const int t0 = x.tile * a.tpt;  // the tile's first token in its sequence
+    rows = min(a.tpt, x.seq.n - t0) * a.G;
+    pos0 = x.seq.m - x.seq.n + t0;
+    seen_by_all = a.causal ? min(x.seq.m, pos0 + 1) : x.seq.m;
+    scrub = kNone;
+  }
+};
+
 template <int D>
 struct Layout {
   static constexpr uint32_t TILE = kTile * D * 2;
@@ -36,11 +57,15 @@ struct Layout {
   static constexpr uint32_t K0 = Q + TILE;
   static constexpr uint32_t V0 = K0 + NS * TILE;
   static constexpr uint32_t BAR = V0 + NS * TILE;
-  static constexpr uint32_t TSLOT = BAR + FwdBars<NS>::kCount * 8;
+  // FwdBars, then item[2], item_free[2], o_free (O has been read), part (a cut unit's rows are out), last,
+  // q_free (an item's last S has been computed)
+  static constexpr uint32_t MORE = BAR + FwdBars<NS>::kCount * 8;
+  static constexpr uint32_t TSLOT = MORE + 8 * 8;
   static constexpr uint32_t ABORT = TSLOT + 4;
-  static constexpr uint32_t SCRUB = ABORT + 4;  // first key tile some of whose values were zeroed
-  static constexpr uint32_t ITEM = (SCRUB + 4 + 15) & ~15u;  // for the epilogue, which keeps no registers for it
-  static constexpr uint32_t BYTES = ITEM + sizeof(PackedItem);
+  static constexpr uint32_t LAST = ABORT + 4;  // whether this CTA joins the parts
+  static constexpr uint32_t ITEM = (LAST + 4 + 15) & ~15u;  // two of Work
+  static constexpr uint32_t BYTES = ITEM + 2 * sizeof(Work);
+  static_assert(2 * (BYTES + 1024) <= 233472, "two CTAs an SM");
   // TMEM: S at [0, 128), O behind it; at d = 64 P~ has columns of its own, at d = 128 S's
   static constexpr uint32_t TMEM_COLS = 256;
   static constexpr bool PSEP = D == 64;
@@ -104,18 +129,30 @@ __device__ __noinline__ void join_parts(const PackedArgs& a, const PackedItem& x
   constexpr size_t words = kTile * (D + 2);
   const size_t step = words * a.Hk;
   const float* base = a.slots + ((size_t)x.first * a.Hk + hk) * words;
-  auto at = [&](int s) { return __ldcg(reinterpret_cast<const float2*>(base + s * step + 2 * r)); };
+  // four (m, l) at a time, so that their loads are on their way together; a part that saw no key, or
+  // is none, weighs nothing
+  constexpr int ML = 4;
+  auto fetch = [&](int s0, float2 (&ml)[ML]) {
+#pragma unroll
+    for (int k = 0; k < ML; ++k)
+      ml[k] = s0 + k < x.parts ? __ldcg(reinterpret_cast<const float2*>(base + (s0 + k) * step + 2 * r)) : make_float2(-INFINITY, 0.f);
+  };
+  float2 ml[ML];
   float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < x.parts; ++s) {
-    const float2 ml = at(s);
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);  // a part that saw no key weighs nothing
+#pragma unroll 1
+  for (int s0 = 0; s0 < x.parts; s0 += ML) {
+    fetch(s0, ml);
+#pragma unroll
+    for (int k = 0; k < ML; ++k)
+      if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
   }
-  auto weight = [&](const float2& ml) { return ml.y == 0.f ? 0.f : ml.x == top ? 1.f : ex2((ml.x - top) * a.scale_log2); };
-#pragma unroll 4
-  for (int s = 0; s < x.parts; ++s) {
-    const float2 ml = at(s);
-    if (ml.y != 0.f) sum = fmaf(weight(ml), ml.y, sum);
+  auto weight = [&](const float2& p) { return p.y == 0.f ? 0.f : p.x == top ? 1.f : ex2((p.x - top) * a.scale_log2); };
+#pragma unroll 1
+  for (int s0 = 0; s0 < x.parts; s0 += ML) {
+    if (x.parts > ML) fetch(s0, ml);
+#pragma unroll
+    for (int k = 0; k < ML; ++k)
+      if (ml[k].y != 0.f) sum = fmaf(weight(ml[k]), ml[k].y, sum);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int i = a.divG.div(r), token = x.seq.q0 + t0 + i, head = hk * a.G + r - i * a.G;
@@ -125,19 +162,30 @@ __device__ __noinline__ void join_parts(const PackedArgs& a, const PackedItem& x
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += 32) {
     float acc[32] = {};
-#pragma unroll 2
-    for (int s = 0; s < x.parts; ++s) {
-      const float2 ml = at(s);
-      if (ml.y == 0.f) continue;
-      const float f = weight(ml);
-      const float4* from = reinterpret_cast<const float4*>(base + s * step + 2 * kTile) + c0 / 4 * kTile + r;
+#pragma unroll 1
+    for (int s0 = 0; s0 < x.parts; s0 += ML) {
+      if (x.parts > ML) fetch(s0, ml);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float4 v = __ldcg(from + c * kTile);
-        acc[4 * c] = fmaf(f, v.x, acc[4 * c]);
-        acc[4 * c + 1] = fmaf(f, v.y, acc[4 * c + 1]);
-        acc[4 * c + 2] = fmaf(f, v.z, acc[4 * c + 2]);
-        acc[4 * c + 3] = fmaf(f, v.w, acc[4 * c + 3]);
+      for (int k = 0; k < ML; k += 2) {  // two parts at a time
+        float4 v[2][8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool there = ml[k + e].y != 0.f;
+          const float4* from = reinterpret_cast<const float4*>(base + (s0 + k + e) * step + 2 * kTile) + c0 / 4 * kTile + r;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[e][c] = there ? __ldcg(from + c * kTile) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = weight(ml[k + e]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            acc[4 * c] = fmaf(f, v[e][c].x, acc[4 * c]);
+            acc[4 * c + 1] = fmaf(f, v[e][c].y, acc[4 * c + 1]);
+            acc[4 * c + 2] = fmaf(f, v[e][c].z, acc[4 * c + 2]);
+            acc[4 * c + 3] = fmaf(f, v[e][c].w, acc[4 * c + 3]);
+          }
+        }
       }
     }
 #pragma unroll
@@ -158,59 +206,87 @@ __global__ void __launch_bounds__(192, 2)
   const uint32_t sb = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  PackedItem x;
-  int hk;
-  if (a.direct) {
-    const int index = a.divHk.div((int)blockIdx.x);
-    hk = (int)blockIdx.x - index * a.Hk;
-    if (!packed_direct(a, index, x)) return;
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
-    if (!packed_place(a, x, hk)) return;
-  }
-  const int t0 = x.tile * a.tpt;                       // the tile's first token in its sequence
-  const int rows = min(a.tpt, x.seq.n - t0) * a.G;     // rows that are the sequence's
-  const int pos0 = x.seq.m - x.seq.n + t0;             // its place among the keys
-  const int seen_by_all = a.causal ? min(x.seq.m, pos0 + 1) : x.seq.m;
-
+  if (!a.direct) asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
+  const int total = a.direct ? 0x7FFFFFFF : a.list.head[0] * a.Hk;
+  if ((int)blockIdx.x >= total) return;
   const FwdBars<NS> bars{sb + L::BAR};
+  auto more = [&](int i) { return sb + L::MORE + 8u * (uint32_t)i; };
+  auto bar_item = [&](int k) { return more(k & 1); };
+  auto bar_item_free = [&](int k) { return more(2 + (k & 1)); };
+  const uint32_t bar_o_free = more(4), bar_part = more(5), bar_last = more(6), bar_q_free = more(7);
   volatile int* abort_cta = reinterpret_cast<volatile int*>(smem + L::ABORT);
-  volatile int* scrubbed = reinterpret_cast<volatile int*>(smem + L::SCRUB);
   const WaitCtx w{abort_cta, a.rep.st, a.rep.epoch, a.rep.wait_ns};
   if ((sb & 1023u) != 0) {  // the swizzled layouts need a 1024-byte aligned base
     if (threadIdx.x == 0) raise_error(w, FA_ERR_CUDA);
     return;
   }
-  // debug build: the tile lies in its sequence, and that in the tensors
-  if (!dbg_check(w, rows > 0 && x.s0 >= 0 && x.s0 <= x.s1 && x.s1 <= packed_units(x.seq, a.tpt, true) && x.seq.q0 >= 0 &&
-                        x.seq.q0 + x.seq.n <= a.Tq && x.seq.k0 >= 0 && x.seq.k0 + x.seq.m <= a.Tk && hk < a.Hk))
-    return;
-
-  const bool producer = warp == 4 && lane == 0;
-  int nk = 0, nv = 0;  // producer lane: K and V copies issued
-  int kt_next = x.s1;
-  auto load_k = [&](int st, int kt) {
-    mbar_arrive_expect_tx(bars.kf(st), L::TILE);
-    for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(sb + L::K0 + st * L::TILE + c * (kTile * 128), &tmK, bars.kf(st), c * 64, hk, x.seq.k0 + kt * kTile);
+  // The CTA's k-th item, which the producer puts into shared memory; tile < 0: there is none left.
+  // Key tiles are counted through all items (`it`, for the phases of a tile's barriers), and so are
+  // the items that have any (n: those of q, q_free and o_free).
+  auto place = [&](int k) { return reinterpret_cast<Work*>(smem + L::ITEM) + (k & 1); };
+  // producer: its item; K and V copies, items with copies, parts of cut units so far
+  PackedItem x;
+  int hk = 0, it = 0, nv = 0, n = 0, cuts = 0;
+  auto publish = [&](int k, int index) -> bool {  // false: a check of the debug build failed
+    const int at = a.divHk.div(index);
+    hk = index - at * a.Hk;
+    x.tile = -1;
+    if (a.direct) {
+      if (k == 0 && !packed_direct(a, at, x)) x.tile = -1;
+    } else if (index < total) {
+      x = a.list.items[at];
+    }
+    // debug build: the tile lies in its sequence, and that in the tensors
+    if (x.tile >= 0 && !__all_sync(0xffffffffu, dbg_check(w, x.tile * a.tpt < x.seq.n && x.s0 >= 0 && x.s0 <= x.s1 &&
+                                                                 x.s1 <= packed_units(x.seq, a.tpt, true) && x.seq.q0 >= 0 &&
+                                                                 x.seq.q0 + x.seq.n <= a.Tq && x.seq.k0 >= 0 &&
+                                                                 x.seq.k0 + x.seq.m <= a.Tk && hk < a.Hk)))
+      return false;
+    if (lane == 0) {
+      *place(k) = Work(x, hk, cuts, a);
+      mbar_arrive(bar_item(k));
+    }
+    if (x.tile >= 0 && x.slot >= 0) ++cuts;
+    return true;
   };
-  auto load_v = [&](int st, int kt) {
-    mbar_arrive_expect_tx(bars.vf(st), L::TILE);
-    for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(sb + L::V0 + st * L::TILE + c * (kTile * 128), &tmV, bars.vf(st), c * 64, hk, x.seq.k0 + kt * kTile);
-  };
-  auto next = [](int kt) { return kt; };
-  if (producer) {
-    bars.init();
-    *abort_cta = 0;
-    *scrubbed = kNone;
-    fence_barrier_init();
+  auto load_q = [&] {
     mbar_arrive_expect_tx(bars.q(), (uint32_t)(a.tpt * a.G) * D * 2u);
     for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(sb + L::Q + c * (kTile * 128), &tmQ, bars.q(), c * 64, hk * a.G, x.seq.q0 + t0);
-    kt_next = fwd_produce(w, bars, x.s0, x.s1, x.seq.m, NS, nk, nv, next, load_k, load_v);
+      tma_load_3d(sb + L::Q + c * (kTile * 128), &tmQ, bars.q(), c * 64, hk * a.G, x.seq.q0 + x.tile * a.tpt);
+  };
+  auto load_tile = [&](const CUtensorMap* tm, uint32_t to, uint32_t on, int kt) {
+    mbar_arrive_expect_tx(on, L::TILE);
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(to + c * (kTile * 128), tm, on, c * 64, hk, x.seq.k0 + kt * kTile);
+  };
+  bool go = true;
+  if (warp == 4) {
+    if (lane == 0) {
+      bars.init();
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(bar_item(k), 1);
+        mbar_init(bar_item_free(k), 5);
+      }
+      mbar_init(bar_o_free, 4);
+      mbar_init(bar_part, 4);
+      mbar_init(bar_last, 1);
+      mbar_init(bar_q_free, 1);
+      *abort_cta = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+    // the first item is the CTA's own; its copies that need no wait go beside the set-up
+    go = publish(0, (int)blockIdx.x);
+    if (go && x.tile >= 0 && x.s0 < x.s1) {
+      n = 1;
+      if (lane == 0) load_q();
+      for (; it < NS && x.s0 + it < x.s1; ++it, ++nv)
+        if (lane == 0) {
+          load_tile(&tmK, sb + L::K0 + it * L::TILE, bars.kf(it), x.s0 + it);
+          load_tile(&tmV, sb + L::V0 + it * L::TILE, bars.vf(it), x.s0 + it);
+        }
+    }
   }
-  if (threadIdx.x == 0) *reinterpret_cast<PackedItem*>(smem + L::ITEM) = x;
   if (warp == 5) {
     tmem_alloc(sb + L::TSLOT, L::TMEM_COLS);
     tmem_relinquish();
@@ -222,160 +298,234 @@ __global__ void __launch_bounds__(192, 2)
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      if (kt_next >= 0) fwd_produce(w, bars, kt_next, x.s1, x.seq.m, 1 << 30, nk, nv, next, load_k, load_v);
-      fwd_drain_copies(w, bars, nk, nv);
+    for (int k = 0; go && x.tile >= 0; ) {
+      if (x.s0 < x.s1) {  // some row sees a key
+        if (k > 0) {
+          if (n > 0 && !(go = warp_wait(w, bar_q_free, (n - 1) & 1))) break;
+          if (lane == 0) load_q();
+          ++n;
+        }
+        for (int kt = x.s0 + (k == 0 ? it : 0); kt < x.s1; ++kt) {
+          const int st = it % NS;
+          const uint32_t ph = ((it / NS) - 1) & 1;
+          if (it >= NS && !(go = warp_wait(w, bars.ke(st), ph))) break;
+          if (lane == 0) load_tile(&tmK, sb + L::K0 + st * L::TILE, bars.kf(st), kt);
+          ++it;
+          if (nv >= NS && !(go = warp_wait(w, bars.ve(st), ph))) break;
+          if (lane == 0) load_tile(&tmV, sb + L::V0 + st * L::TILE, bars.vf(st), kt);
+          ++nv;
+        }
+        if (!go) break;
+      }
+      // the next one: taken in order as CTAs come to need them
+      ++k;
+      int index = 0x7FFFFFFF;
+      if (!a.direct) {
+        if (lane == 0) index = (int)gridDim.x + atomicAdd(a.list.head + 4, 1);
+        index = __shfl_sync(0xffffffffu, index, 0);
+      }
+      if (k >= 2 && !(go = warp_wait(w, bar_item_free(k), ((k >> 1) - 1) & 1))) break;
+      if (!(go = publish(k, index))) break;
+    }
+    if (lane == 0) {  // every copy has landed before the CTA ends
+      if (n > 0) mbar_drain(w, bars.q(), (n - 1) & 1);
+      for (int st = 0; st < NS; ++st) {
+        const int ck = (it - st + NS - 1) / NS, cv = (nv - st + NS - 1) / NS;  // copies into stage st
+        if (ck > 0) mbar_drain(w, bars.kf(st), (ck - 1) & 1);
+        if (cv > 0) mbar_drain(w, bars.vf(st), (cv - 1) & 1);
+      }
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
+    // The schedule of fwd_common.cuh for each item: at d = 64 S_{j+1} as soon as S_j has been copied out,
+    // at d = 128 after P~ V_j.  An item's first S goes beside the last one's way out.
     constexpr uint32_t idS = idesc_f16(F16, kTile, kTile, false, false);
     constexpr uint32_t idO = idesc_f16(F16, kTile, D, false, true);
     const uint32_t tS = tmem + L::T_S, tO = tmem + L::T_O;
     const uint64_t dQ = desc_kmajor_base(sb + L::Q);
     const uint64_t dK0 = desc_kmajor_base(sb + L::K0);
     const uint64_t dV0 = desc_mnmajor_base(sb + L::V0, kTile);
-    fwd_mma_schedule<NS, L::PSEP>(
-        w, bars, x.s0, x.s1, next,
-        [&](int st) {  // S = Q K^T
-          const uint64_t dK = desc_add(dK0, (uint32_t)st * L::TILE);
+    auto s_tile = [&](int it, bool last) -> bool {  // S = Q K^T; last: of the item
+      const int st = it % NS;
+      if (!warp_wait(w, bars.kf(st), (it / NS) & 1)) return false;
+      tc_fence_after();
+      const uint64_t dK = desc_add(dK0, (uint32_t)st * L::TILE);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ss_elect(tS, dQ + kmajor_step(kk, kTile), dK + kmajor_step(kk, kTile), idS, kk > 0 ? 1u : 0u);
-        },
-        [&](int st, int it) {  // O += P~ V
+      for (int kk = 0; kk < D / 16; ++kk)
+        tc_mma_ss_elect(tS, dQ + kmajor_step(kk, kTile), dK + kmajor_step(kk, kTile), idS, kk > 0 ? 1u : 0u);
+      tc_commit_elect(bars.s());
+      tc_commit_elect(bars.ke(st));
+      if (last) tc_commit_elect(bar_q_free);
+      return true;
+    };
+    bool ok = true;
+    int it = 0, n = 0;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = warp_wait(w, bar_item(k), (k >> 1) & 1))) break;
+      Work* x = place(k);
+      const int tile = x->x.tile, s0 = x->x.s0, s1 = x->x.s1, m = x->x.seq.m, seen_by_all = x->seen_by_all;
+      if (tile >= 0 && s0 < s1) {
+        if (!(ok = warp_wait(w, bars.q(), n & 1))) break;
+        if (L::PSEP && it > 0 && !(ok = warp_wait(w, bars.sfree(), (it - 1) & 1))) break;
+        if (!(ok = s_tile(it, s0 + 1 == s1))) break;
+        for (int kt = s0; kt < s1; ++kt, ++it) {
+          const int st = it % NS;
+          const bool next = kt + 1 < s1;
+          if (L::PSEP && next) {
+            if (!(ok = warp_wait(w, bars.sfree(), it & 1))) break;
+            if (!(ok = s_tile(it + 1, kt + 2 == s1))) break;
+          }
+          if (kt * kTile + kTile > seen_by_all) {  // some row does not see all of it: its values are looked over
+            if (!(ok = warp_wait(w, bars.vf(st), (it / NS) & 1))) break;
+            if (scrub_tile<D, F16>(sb + L::V0 + st * L::TILE, m - kt * kTile) && lane == 0 && x->scrub == kNone) {
+              x->scrub = kt;
+              __threadfence_block();
+            }
+            __syncwarp();
+          }
+          if (!(ok = warp_wait(w, bars.p(), it & 1))) break;
+          if (!(ok = warp_wait(w, bars.vf(st), (it / NS) & 1))) break;
+          if (kt == s0 && n > 0 && !(ok = warp_wait(w, bar_o_free, (n - 1) & 1))) break;
+          tc_fence_after();
           const uint64_t dV = desc_add(dV0, (uint32_t)st * L::TILE);
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
+          for (int kk = 0; kk < kTile / 16; ++kk)  // O += P~ V
             tc_mma_ts_elect(tO, tmem + L::T_P + (uint32_t)kk * 8u, dV + mnmajor_step(kk), idO,
-                            (it > 0 || kk > 0) ? 1u : 0u);
-        },
-        [&](int st, int kt, int it) {  // a tile that some row does not see all of: its values are looked over
-          if (kt * kTile + kTile <= seen_by_all) return true;
-          if (!warp_wait(w, bars.vf(st), (it / NS) & 1)) return false;
-          if (scrub_tile<D, F16>(sb + L::V0 + st * L::TILE, x.seq.m - kt * kTile) && lane == 0 && *scrubbed == kNone) {
-            *scrubbed = kt;
-            __threadfence_block();
-          }
-          __syncwarp();
-          return true;
-        });
+                            (kt > s0 || kk > 0) ? 1u : 0u);
+          tc_commit_elect(bars.o());
+          tc_commit_elect(bars.ve(st));
+          if (!L::PSEP && next && !(ok = s_tile(it + 1, kt + 2 == s1))) break;
+        }
+        if (!ok) break;
+        ++n;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_item_free(k));
+      if (tile < 0) break;
+    }
+    tc_commit_elect(bars.fin());
+    if (lane == 0) mbar_drain(w, bars.fin(), 0);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     const int r = threadIdx.x;
-    const int lim = a.causal ? min(x.seq.m, pos0 + a.divG.div(r) + 1) : x.seq.m;  // keys that the row sees
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + L::T_S + lane_off, tO = tmem + L::T_O + lane_off;
     const float c2 = a.scale_log2;
-    float m_use = -INFINITY;  // running maximum in use, of the products
-    float l = 0.f;
     bool ok = true;
     int it = 0;
-    for (int kt = x.s0; kt < x.s1; ++kt, ++it) {
-      if (!(ok = warp_wait(w, bars.s(), it & 1))) break;
-      tc_fence_after();
-      float s[kTile];
-      float m8[8];
-      {
-        uint32_t u[64], v[64];
-        tmem_ld64(tS, u);
-        tmem_ld64_nowait(tS + 64, v);
+    for (int k = 0; ok; ++k) {
+      if (!(ok = warp_wait(w, bar_item(k), (k >> 1) & 1))) break;
+      // keys that the row sees (formed where it is wanted: the loop has no registers to spare)
+      auto limit = [&](const Work* x) { return a.causal ? min(x->x.seq.m, x->pos0 + a.divG.div(r) + 1) : x->x.seq.m; };
+      if (place(k)->x.tile < 0) break;
+      const int first = it, end = it + place(k)->x.s1 - place(k)->x.s0;
+      const int masked = it + (place(k)->seen_by_all >> 7) - place(k)->x.s0;  // tiles from here on hide a key from some row
+      static_assert(kTile == 128, "of the shift");
+      float m_use = -INFINITY;  // running maximum in use, of the products
+      float l = 0.f;
+      for (; it < end; ++it) {
+        if (!(ok = warp_wait(w, bars.s(), it & 1))) break;
+        tc_fence_after();
+        float s[kTile];
+        float m8[8];
+        {
+          uint32_t u[64], v[64];
+          tmem_ld64(tS, u);
+          tmem_ld64_nowait(tS + 64, v);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(u[c]);
+          for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(u[c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m8[j] = max16(s, j);
-        tmem_wait_ld64(v);
+          for (int j = 0; j < 4; ++j) m8[j] = max16(s, j);
+          tmem_wait_ld64(v);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[64 + c] = __uint_as_float(v[c]);
-      }
-      if (L::PSEP) {  // S_j is in registers: the MMA warp may compute S_{j+1}
+          for (int c = 0; c < 64; ++c) s[64 + c] = __uint_as_float(v[c]);
+        }
+        if (L::PSEP) {  // S_j is in registers: the MMA warp may compute S_{j+1}
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.sfree());
+        }
+        if (it >= masked) {
+          const Work* x = place(k);
+          const int low = limit(x) - (x->x.s1 - (end - it)) * kTile;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c >= low) s[c] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) m8[j] = max16(s, j);
+        }
+#pragma unroll
+        for (int j = 4; j < 8; ++j) m8[j] = max16(s, j);
+        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        float alpha = 1.f;
+        if ((mx - m_use) * c2 > kRescaleThr) {
+          alpha = ex2((m_use - mx) * c2);  // 0 on the first tile that sees a key
+          m_use = mx;
+        }
+        float mneg = m_use == -INFINITY ? 0.f : -m_use * c2;
+        if (__any_sync(0xffffffffu, fabsf(mneg) > kLargeScore)) {
+          // the rounded maximum would be off by more than 2^-8: the difference first, which is
+          // exact near the maximum
+          const float top = m_use == -INFINITY ? 0.f : m_use;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) s[c] -= top;
+          mneg = 0.f;
+        }
+        const uint64_t c2p = f2pack(c2, c2), mp = f2pack(mneg, mneg);
+        uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+        // four chunks of 32 keys, each chunk's P~ stored as soon as it is formed; P~ is rounded to the
+        // inputs' type (half a step of each weight), l adds the fp32 weights
+        bool o_ready = !(L::PSEP && it > first);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int pr = 0; pr < 16; ++pr) {
+            const int c = 32 * ch + 2 * pr;
+            float x0, x1;
+            f2unpack(ffma2(f2pack(s[c], s[c + 1]), c2p, mp), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            acc[pr & 3] = fadd2(acc[pr & 3], f2pack(p0, p1));
+            pk[pr] = pack2<F16>(p0, p1);
+          }
+          if (!o_ready) {  // P~ V_{j-1} reads the P~ columns and writes O
+            if (!(ok = warp_wait(w, bars.o(), (it - 1) & 1))) break;
+            tc_fence_after();
+            o_ready = true;
+          }
+          tmem_st16(tmem + L::T_P + lane_off + 16 * ch, pk);
+        }
+        if (!ok) break;
+        // (before a row's first key its O is 0, or of the item before)
+        if (__any_sync(0xffffffffu, alpha != 1.f && l != 0.f)) scale_o_row<D>(tO, alpha);
+        l = l * alpha + sum_packed4(acc);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.sfree());
+        if (lane == 0) mbar_arrive(bars.p());
       }
-      if (kt * kTile + kTile > seen_by_all) {
-        const int low = lim - kt * kTile;
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c >= low) s[c] = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m8[j] = max16(s, j);
-      }
-#pragma unroll
-      for (int j = 4; j < 8; ++j) m8[j] = max16(s, j);
-      const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-      float alpha = 1.f;
-      if ((mx - m_use) * c2 > kRescaleThr) {
-        alpha = ex2((m_use - mx) * c2);  // 0 on the first tile that sees a key
-        m_use = mx;
-      }
-      float mneg = m_use == -INFINITY ? 0.f : -m_use * c2;
-      if (__any_sync(0xffffffffu, fabsf(mneg) > kLargeScore)) {
-        // the rounded maximum would be off by more than 2^-8: the difference first, which is
-        // exact near the maximum
-        const float top = m_use == -INFINITY ? 0.f : m_use;
-#pragma unroll
-        for (int c = 0; c < kTile; ++c) s[c] -= top;
-        mneg = 0.f;
-      }
-      const uint64_t c2p = f2pack(c2, c2), mp = f2pack(mneg, mneg);
-      uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-      // four chunks of 32 keys, each chunk's P~ stored as soon as it is formed; P~ is rounded to the
-      // inputs' type (half a step of each weight), l adds the fp32 weights
-      bool o_ready = !(L::PSEP && it > 0);
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int pr = 0; pr < 16; ++pr) {
-          const int c = 32 * ch + 2 * pr;
-          float x0, x1;
-          f2unpack(ffma2(f2pack(s[c], s[c + 1]), c2p, mp), x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          acc[pr & 3] = fadd2(acc[pr & 3], f2pack(p0, p1));
-          pk[pr] = pack2<F16>(p0, p1);
-        }
-        if (!o_ready) {  // P~ V_{j-1} reads the P~ columns and writes O
-          if (!(ok = warp_wait(w, bars.o(), (it - 1) & 1))) break;
-          tc_fence_after();
-          o_ready = true;
-        }
-        tmem_st16(tmem + L::T_P + lane_off + 16 * ch, pk);
-      }
-      if (!ok) break;
-      l = l * alpha + sum_packed4(acc);
-      if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) scale_o_row<D>(tO, alpha);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars.p());
-    }
-    // ------------------------------------------------------------ epilogue
-    bool have_o = false;
-    if (ok && it > 0) {
-      ok = warp_wait(w, bars.o(), (it - 1) & 1);
+      // ------------------------------------------------------------ the item's results
+      const Work* x = place(k);
+      const bool have_o = x->x.s0 < x->x.s1;
+      if (!ok || (have_o && !(ok = warp_wait(w, bars.o(), (it - 1) & 1)))) break;
       tc_fence_after();
-      have_o = ok;
-    }
-    if (ok) {
-      // d = 128: the item again from shared memory, which spares the loop its registers
-      const PackedItem y = D == 128 ? *reinterpret_cast<const PackedItem*>(smem + L::ITEM) : x;
-      const int i = a.divG.div(r), first = y.tile * a.tpt, token = y.seq.q0 + first + i;
-      const int kv = D == 128 ? (int)blockIdx.x - a.divHk.div((int)blockIdx.x) * a.Hk : hk, head = kv * a.G + r - i * a.G;
-      const bool live = r < min(a.tpt, y.seq.n - first) * a.G;
-      const bool whole = y.slot < 0;
+      const int i = a.divG.div(r), token = x->x.seq.q0 + x->x.tile * a.tpt + i, hk = x->hk, head = hk * a.G + r - i * a.G;
+      const bool live = r < x->rows;
+      const int slot = x->x.slot;
+      const bool whole = slot < 0;
       const float inv_l = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
-      const long long slot = (long long)y.slot * a.Hk + kv;
-      float* part = whole ? nullptr : a.slots + slot * (kTile * (D + 2));
+      float* part = whole ? nullptr : a.slots + ((long long)slot * a.Hk + hk) * (kTile * (D + 2));
       if (whole) {
         if (live) a.lse[(long long)token * a.Hq + head] = l == 0.f ? -INFINITY : fmaf(m_use, a.scale, __logf(l));
       } else {
         *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m_use, l);
       }
       // values that were zeroed: added to the rows that see them
-      const int from = *scrubbed;
+      const int from = *reinterpret_cast<const volatile int*>(&x->scrub);
       const bool patch = from != kNone;
-      const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)y.seq.k0 * a.vs[0] + kv * a.vs[1];
-      const int end = min(lim, y.s1 * kTile);
+      const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)x->x.seq.k0 * a.vs[0] + hk * a.vs[1];
+      const int last_key = min(limit(x), x->x.s1 * kTile);
       uint16_t* dst = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1];
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -384,20 +534,25 @@ __global__ void __launch_bounds__(192, 2)
           tmem_ld32(tO + c0, o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
+          for (int c = 0; c < 32; ++c) o[c] = 0u;
+        }
+        if (have_o && c0 + 32 == D) {  // all is in registers: the next item's O may go there
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_o_free);
         }
         if (patch && live) {
 #pragma unroll 1
-          for (int j = from * kTile; j < end; ++j)
+          for (int j = from * kTile; j < last_key; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               const uint4 u = __ldg(reinterpret_cast<const uint4*>(vrow + j * a.vs[0] + c0) + v);
               const uint32_t h[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = unpack2<F16>(h[k] & not_finite<F16>(h[k]));
-                o[8 * v + 2 * k] = __float_as_uint(__uint_as_float(o[8 * v + 2 * k]) + f.x);
-                o[8 * v + 2 * k + 1] = __float_as_uint(__uint_as_float(o[8 * v + 2 * k + 1]) + f.y);
+              for (int c = 0; c < 4; ++c) {
+                const float2 f = unpack2<F16>(h[c] & not_finite<F16>(h[c]));
+                o[8 * v + 2 * c] = __float_as_uint(__uint_as_float(o[8 * v + 2 * c]) + f.x);
+                o[8 * v + 2 * c + 1] = __float_as_uint(__uint_as_float(o[8 * v + 2 * c + 1]) + f.y);
               }
             }
         }
@@ -420,19 +575,27 @@ __global__ void __launch_bounds__(192, 2)
         }
         __syncwarp();
       }
-    }
-    if (x.slot >= 0) {  // the last of the unit's parts to be done joins them (every row's thread comes here)
-      volatile int* last = reinterpret_cast<volatile int*>(smem + L::SCRUB);
-      const PackedItem y = *reinterpret_cast<const PackedItem*>(smem + L::ITEM);
-      __threadfence();
-      named_barrier_sync(1, kTile);  // the rows' parts are out, and `scrubbed` read
-      if (r == 0) {
-        const bool done = *abort_cta == 0 && atomicAdd(a.list.left + y.cut * a.Hk + hk, 1) == y.parts - 1;
-        __threadfence();
-        *last = done;
+      if (!whole) {  // the last of the unit's parts to be done joins them
+        // (the rows' stores are ordered before the count by the barrier within the CTA, which is one
+        // lane's to see, and by that lane's fence)
+        volatile int* last = reinterpret_cast<volatile int*>(smem + L::LAST);
+        if (lane == 0) mbar_arrive(bar_part);
+        if (warp == 0) {
+          if (!(ok = warp_wait(w, bar_part, x->cuts & 1))) break;
+          if (lane == 0) {
+            __threadfence();
+            const bool done = atomicAdd(a.list.left + x->x.cut * a.Hk + hk, 1) == x->x.parts - 1;
+            __threadfence();
+            *last = done;
+            mbar_arrive(bar_last);
+          }
+          __syncwarp();
+        }
+        if (!(ok = warp_wait(w, bar_last, x->cuts & 1))) break;
+        if (*last) join_parts<D, F16>(a, x->x, hk, r);
+        __syncwarp();
       }
-      named_barrier_sync(1, kTile);
-      if (*last) join_parts<D, F16>(a, y, hk, r);
+      if (lane == 0) mbar_arrive(bar_item_free(k));
     }
   }
 
@@ -457,7 +620,11 @@ cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, cuda
   cfg.attrs = at;
   cfg.numAttrs = a.direct ? 0 : 1;
   cfg.stream = s;
-  cfg.gridDim = dim3((unsigned)((long long)items * a.Hk));
+  // CTAs that stay and take one item after the other; without a list an item each
+  const long long all = (long long)items * a.Hk;
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cfg.gridDim = dim3((unsigned)(a.direct ? all : std::min(all, 2ll * sms)));
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = L::BYTES;
   return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], a);
