@@ -19,7 +19,7 @@ struct PackedPlanArgs {
   int R, Tq, Tk, Hk;
   int tpt, causal, bwd;
   int target;          // CTAs to share the steps among
-  int cuttable, least; // whether units may be cut; steps that a slice has at least
+  int slots, least;    // places for parts of cut units (0: none is cut); steps that a slice has at least
   const int* cu_q;
   const int* cu_k;
   PackedList list;

@@ -146,7 +146,7 @@ PackedPlanArgs plan_args(const PackedArgs& a, const Sizes& z, const int* cu_q, c
   q.causal = a.causal;
   q.bwd = bwd;
   q.target = z.target;
-  q.cuttable = z.slots > 0;
+  q.slots = z.slots;
   q.least = z.least;
   q.cu_q = cu_q;
   q.cu_k = cu_k;

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   // shortest of them; and of more units than are kept only an even share is tried
   const float even = packed_even(steps, a.Hk, a.target);
   int slice = longest;
-  if (a.cuttable && longest > a.least && (float)longest > 0.75f * even) {
+  if (a.slots > 0 && longest > a.least && (float)longest > 0.75f * even) {
     if (units <= kWeighed) {
       const int mine_slice = packed_candidate(warp, even, a.least, longest);
       int n = 0, cut = 0;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       slice = min(longest, max(a.least, (int)even + 1));
     }
   }
-  const float per_step = (float)(kClasses - 1) / (float)max(min(longest, slice), 1);
+  float per_step = (float)(kClasses - 1) / (float)max(slice, 1);
   auto class_of = [&](int w) { return min(kClasses - 1, max(0, (int)((float)(slice - w) * per_step))); };
 
   // ---- many whole units: the sequences by their longest units' steps, and the units of each behind one
@@ -234,16 +234,29 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   }
 
   // ---- else the slices, counted and placed by their lengths
-  with_units([&](int, const PackedItem& x) {
-    const int w = x.s1 - x.s0, c = packed_cuts(w, slice);
-    if (c == 1) {
-      atomicAdd(&class_s[class_of(w)], 1);
-    } else {  // the first w % c of one length, the others of one less
-      if (w % c) atomicAdd(&class_s[class_of(w / c + 1)], w % c);
-      atomicAdd(&class_s[class_of(w / c)], c - w % c);
-    }
-  });
+  for (;;) {
+    with_units([&](int, const PackedItem& x) {
+      const int w = x.s1 - x.s0, c = packed_cuts(w, slice);
+      if (c == 1) {
+        atomicAdd(&class_s[class_of(w)], 1);
+      } else {  // the first w % c of one length, the others of one less
+        if (w % c) atomicAdd(&class_s[class_of(w / c + 1)], w % c);
+        atomicAdd(&class_s[class_of(w / c)], c - w % c);
+        atomicAdd(&slot_s, c);
+      }
+    });
+    __syncthreads();
+    if (slot_s <= a.slots) break;
+    // more parts than there is room for (packed_slots rules it out): nothing is cut
+    __syncthreads();
+    slice = longest;
+    per_step = (float)(kClasses - 1) / (float)max(slice, 1);
+    class_s[tid] = 0;
+    if (tid == 0) slot_s = 0;
+    __syncthreads();
+  }
   __syncthreads();
+  if (tid == 0) slot_s = 0;
   int in_class[1] = {class_s[tid]}, items[1];
   const int had = in_class[0];
   block_scan(in_class, scan_s + 3, items, [](int x, int y) { return x + y; });
