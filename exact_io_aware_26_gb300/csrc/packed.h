@@ -8,7 +8,8 @@ namespace fa {
 
 // The list of a call's work, made on the GPU (packed_plan.cu), in the workspace.
 struct PackedList {
-  int* head;           // [0] items, [1] cut units, [2], [3] first query row and end, [4] a counter
+  int* head;           // [0] items, [1] cut units, [2], [3] first query row and end, [4] items that CTAs took
+                       // after their first
   PackedItem* items;
   PackedItem* cuts;    // the cut units (s0, s1: the whole unit's steps)
   int* left;           // of each cut unit and key head: the parts that are done (forward)
@@ -32,7 +33,7 @@ struct PackedArgs {
   int tpt, causal;
   float scale, scale_log2;
   PackedList list;
-  int direct;          // forward: no list; the CTAs find their units in the offsets
+  int direct;          // forward: no list; each CTA finds its unit in the offsets
   const int *cu_q, *cu_k;
   const void* v;       // for values that are not finite
   long long vs[2];     // element strides {token, head}
@@ -49,17 +50,6 @@ struct PackedArgs {
 
 constexpr int kPackedDirect = 32;  // sequences that need no list: a lane each
 #ifdef __CUDACC__
-// A CTA's item of the list and its key head, an item's key heads next to each other; false: none is
-// left for it.  (Key head after key head, 32 heads over 8 of 12 sequences up to 16384 tokens take 7.8 ms
-// instead of 7.3.)
-__device__ __forceinline__ bool packed_place(const PackedArgs& a, PackedItem& x, int& hk) {
-  const int index = a.divHk.div((int)blockIdx.x);
-  hk = (int)blockIdx.x - index * a.Hk;
-  if (index >= a.list.head[0]) return false;
-  x = a.list.items[index];
-  return true;
-}
-
 // Without a list: unit `index` of at most 32 sequences, from their offsets, which lane r of each warp
 // reads for sequence r; false: there is none.  Offsets that are wrong are taken as by the list's
 // kernel, and recorded by the first CTA.
@@ -105,7 +95,9 @@ __device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, Pa
 inline size_t packed_slot_words(int d, bool bwd) { return bwd ? (size_t)2 * 128 * d : (size_t)128 * (d + 2); }
 
 cudaError_t launch_packed_plan(const PackedPlanArgs& a, cudaStream_t s);
-// `items`, `cuts`: at most that many items and cut units.
+// `items`, `cuts`: at most that many items and cut units of the list.  The CTAs stay and take item
+// after item, an item's key heads next to each other.  (Key head after key head, 32 heads over 8 of 12
+// sequences up to 16384 tokens take 7.8 ms instead of 7.3.)
 cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s);
 cudaError_t launch_packed_bwd_preprocess(const PackedArgs& a, int d, bool f16, cudaStream_t s);
 cudaError_t launch_packed_bwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s);

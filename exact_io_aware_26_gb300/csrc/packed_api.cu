@@ -181,7 +181,7 @@ fa_status fa_fwd_packed(const fa_packed_params* p, const void* q, const void* k,
     FA_TRY(need(q, 16, "q"));
     FA_TRY(need(o, 16, "o"));
     FA_TRY(need(lse, 4, "lse"));
-    if (o == q) return fail(FA_ERR_INVALID, "o lies over q");
+    if (o == q || o == k || o == v) return fail(FA_ERR_INVALID, "o lies over an input");
   }
   if (p->Tk > 0) {
     FA_TRY(need(k, 16, "k"));
@@ -243,6 +243,7 @@ fa_status fa_bwd_packed(const fa_packed_params* p, const void* q, const void* k,
   for (const void* result : {(const void*)dk, (const void*)dv})
     for (const void* input : {q, k, v, dout})
       if (result && result == input) return fail(FA_ERR_INVALID, "dk or dv lies over an input");
+  if ((dk && dk == dv) || (dq && (dq == dk || dq == dv))) return fail(FA_ERR_INVALID, "two gradients lie over each other");
   FA_TRY(workspace_check(workspace, workspace_bytes, fa_bwd_packed_workspace_size(p)));
   Report rep;
   int sms = 0;

@@ -4,10 +4,10 @@
 // tensors, one behind the other), prefix sums of the units, the steps of every unit, how long a
 // slice is, and the slices in order of their steps, the longest first, by counting (many units
 // sequence by sequence).  The main kernel's CTAs take the list in order, so that what is left at
-// the end is short.  Where in its
-// class of lengths an item stands, and which slots a cut unit has, is left to the order of
-// atomics: results do not depend on it.  Bound by latency, of which the main kernel's launch
-// hides a part.
+// the end is short.  Where in its class of lengths an item stands, and which slots a cut unit has,
+// is left to the order of atomics: results do not depend on it.  Bound by latency (three
+// prompts of up to 32 tokens take 10.7 us with the list, 6.1 without), of which the main kernel's
+// launch hides a part.
 #include "packed.h"
 #include "ptx.cuh"
 
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       a.list.head[1] = 0;
       a.list.head[2] = first_q[0];  // query rows that are a sequence's
       a.list.head[3] = first_q[R];
-      a.list.head[4] = 0;  // items taken by CTAs that were done with theirs (backward)
+      a.list.head[4] = 0;
     }
     return;
   }
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     a.list.head[1] = cut_s;
     a.list.head[2] = first_q[0];  // query rows that are a sequence's
     a.list.head[3] = first_q[R];
-    a.list.head[4] = 0;  // items taken by CTAs that were done with theirs (backward)
+    a.list.head[4] = 0;
   }
 }
 

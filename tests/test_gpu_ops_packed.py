@@ -222,6 +222,70 @@ def test_offsets_that_are_wrong_stay_in_the_tensors(cuda_lib):
         check_bwd([g[:100] for g in grads], q[:100], k[:100], v[:100], o[:100], do[:100], lse[:100], [100], [100], True, 0.125, "bf16")
 
 
+@pytest.mark.parametrize("R", [31, 32, 33])
+@pytest.mark.parametrize("most", [512, 513])
+def test_where_the_work_list_begins(cuda_lib, R, most):
+    """Up to 32 sequences over up to 512 rows of keys go without a work list."""
+    rng = torch.Generator().manual_seed(R)
+    new = torch.randint(0, 4, (R,), generator=rng).tolist()
+    keys = torch.randint(0, 9, (R,), generator=rng).tolist()
+    new[-1], keys[-1] = 200, 0
+    keys[-1] = most - sum(keys)
+    q, k, v, do = make(new, keys, 6, 2, 64, "bf16", 14)
+    for causal in (True, False):
+        o, lse = fa.attention_fwd_packed(q.cuda(), k.cuda(), v.cuda(), offsets(new), offsets(keys), causal=causal)
+        check_fwd(o, lse, q, k, v, new, keys, causal, 0.125, "bf16")
+    # offsets that are wrong: behind the tensors, back again
+    cu_q, cu_k = offsets(new), offsets(keys)
+    cu_q[-1], cu_k[-1] = 2 ** 30, -3
+    o, lse = fa.attention_fwd_packed(q.cuda(), k.cuda(), v.cuda(), cu_q, cu_k)
+    assert fa.get_status() == fa.FA_ERR_INDEX
+    a, b = sum(new[:-1]), sum(keys[:-1])
+    check_fwd(o[:a], lse[:a], q[:a], k[:b], v[:b], new[:-1], keys[:-1], True, 0.125, "bf16")
+    assert bool((o[a:] == 0).all()) and bool((lse[a:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("d,Hq,Hk,dtype", [(64, 3, 1, "bf16"), (128, 2, 2, "f16")])
+def test_a_long_sequence(cuda_lib, d, Hq, Hk, dtype):
+    """140,001 tokens: the rows and keys at its end, rows from all over it, and its first rows."""
+    N, last = 140001, 40
+    g = torch.Generator().manual_seed(15)
+    q, do = (torch.randn(N, Hq, d, generator=g).to(DTYPES[dtype]) for _ in range(2))
+    k, v = (torch.randn(N, Hk, d, generator=g).to(DTYPES[dtype]) for _ in range(2))
+    scale, cu = d ** -0.5, offsets([N])
+    o, lse = fa.attention_fwd_packed(q.cuda(), k.cuda(), v.cuda(), cu)
+    grads = fa.attention_bwd_packed(q.cuda(), k.cuda(), v.cuda(), o, do.cuda(), lse, cu)
+    assert fa.get_status() == fa.FA_OK
+    o, lse, grads = o.cpu(), lse.cpu(), [x.cpu() for x in grads]
+    for a, b in [(0, 50), (N - last, N)] + [(int(x), int(x) + 1) for x in torch.randint(0, N, (4,), generator=g)]:
+        rows = [x[a:b] for x in (q, o, lse, do)]
+        check_fwd(*rows[1:3], rows[0], k[:b], v[:b], [b - a], [b], True, scale, dtype)
+        want, bounds = ref.backward(rows[0], k[:b], v[:b], rows[1], rows[3], rows[2], [b - a], [b], True, scale,
+                                    half_step(dtype), tiny(dtype))
+        assert bool(((grads[0][a:b].double() - want[0]).abs() <= bounds[0]).all())
+        if b == N:  # only these rows see the last keys
+            for i in (1, 2):
+                assert bool(((grads[i][a:].double() - want[i][a:]).abs() <= bounds[i][a:]).all())
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """Rows 2^26 elements apart: the results of the same rows next to each other."""
+    new, step = [30, 13], 1 << 26
+    T = sum(new)
+    q, k, v, do = (x.cuda() for x in make(new, new, 4, 2, 128, "bf16", 16))
+    cu = offsets(new)
+    o, lse = fa.attention_fwd_packed(q, k, v, cu)
+    want = fa.attention_bwd_packed(q, k, v, o, do, lse, cu)
+    room = torch.empty((T - 1) * step + (1 << 16), dtype=torch.bfloat16, device="cuda")
+    at = lambda i, H: room.as_strided((T, H, 128), (step, 128, 1), i << 10)
+    far = [at(i, x.shape[1]).copy_(x) for i, x in enumerate((q, k, v, do))]
+    fo, fl = fa.attention_fwd_packed(*far[:3], cu, out=at(4, 4))
+    assert torch.equal(fo, o) and torch.equal(fl, lse)
+    got = fa.attention_bwd_packed(*far[:3], fo, far[3], fl, cu, dq=at(5, 4), dk=at(6, 2), dv=at(7, 2))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))  # one key tile a row: dq, too, repeats
+    assert fa.get_status() == fa.FA_OK
+
+
 def test_layouts(cuda_lib):
     """Views of packed projections, heads before tokens, results inside wider rows."""
     new = [33, 90]
@@ -335,6 +399,7 @@ def test_refusals_of_the_binding(cuda_lib):
     q, k, v, do = (x.cuda() for x in make([8], [8], 4, 2, 64, "bf16"))
     cu = offsets([8])
     o, lse = fa.attention_fwd_packed(q, k, v, cu)
+    other = torch.empty_like(k)
     for call, error in [
         (lambda: fa.attention_fwd_packed(q.float(), k, v, cu), TypeError),
         (lambda: fa.attention_fwd_packed(q, k.half(), v, cu), TypeError),
@@ -347,12 +412,14 @@ def test_refusals_of_the_binding(cuda_lib):
         (lambda: fa.attention_fwd_packed(q, k, v, cu, lse=lse[:, :2]), ValueError),
         (lambda: fa.attention_fwd_packed(q[:, :3], k, v, cu), fa.FaError),
         (lambda: fa.attention_fwd_packed(q, k, v, cu, out=q), fa.FaError),
+        (lambda: fa.attention_fwd_packed(k, k, v, cu, out=v), fa.FaError),
         (lambda: fa.attention_fwd_packed(q, k[:, :1].expand(8, 2, 64), v, cu), fa.FaError),
         (lambda: fa.attention_fwd_packed(q, k, v, cu, scale=-1.0), fa.FaError),
         (lambda: fa.attention_fwd_packed(q, k, v, cu, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")), fa.FaError),
         (lambda: fa.attention_bwd_packed(q, k, v, o, do, None, cu), ValueError),
         (lambda: fa.attention_bwd_packed(q, k, v, o, do[:4], lse, cu), ValueError),
         (lambda: fa.attention_bwd_packed(q, k, v, o, do, lse, cu, dk=k), fa.FaError),
+        (lambda: fa.attention_bwd_packed(q, k, v, o, do, lse, cu, dk=other, dv=other), fa.FaError),
         (lambda: fa.attention_bwd_packed(q, k, v, o, do, lse, cu, dq=do.float()), TypeError),
     ]:
         with pytest.raises(error):

@@ -83,15 +83,16 @@ def test_pointers(lib):
         for ws, nbytes in ((None, size), (OK, size - 1), (OK + 16, size)):
             assert entry(p, *good[:-1], ws, nbytes, None) == fa.FA_ERR_WORKSPACE
         assert entry(None, *good, size, None) == fa.FA_ERR_INVALID
-    a = [OK + (i << 20) for i in range(8)]
-    a[5] = a[0]  # o over q
-    assert lib.fa_fwd_packed(p, *a, 1 << 40, None) == fa.FA_ERR_INVALID
+    for j in (0, 1, 2):  # o over q, k, v
+        a = [OK + (i << 20) for i in range(8)]
+        a[5] = a[j]
+        assert lib.fa_fwd_packed(p, *a, 1 << 40, None) == fa.FA_ERR_INVALID
     b = [OK + (i << 20) for i in range(12)]
-    for i in (9, 10):  # dk, dv over q, k, v, do
-        for j in (0, 1, 2, 4):
-            c = list(b)
-            c[i] = c[j]
-            assert lib.fa_bwd_packed(p, *c, 1 << 40, None) == fa.FA_ERR_INVALID
+    # dk, dv over q, k, v, do; gradients over each other
+    for i, j in [(i, j) for i in (9, 10) for j in (0, 1, 2, 4)] + [(9, 8), (10, 8), (10, 9)]:
+        c = list(b)
+        c[i] = c[j]
+        assert lib.fa_bwd_packed(p, *c, 1 << 40, None) == fa.FA_ERR_INVALID
     without = [OK + (i << 20) for i in range(8)]
     without[4] = None
     assert lib.fa_fwd_packed(ctypes.byref(params(Tk=9)), *without, 1 << 40, None) == fa.FA_ERR_INVALID
