@@ -59,11 +59,11 @@ __host__ __device__ inline void packed_steps(const PackedSeq& s, int tile, int t
 // key heads.  A launch takes about as long as its longest slice and its start where all slices
 // run at once (a few more stand behind the shortest of them), and otherwise as an even share of
 // the steps and of the slices' starts, and half of the longest one behind it; parts of cut units
-// cost their fp32 sums, and the join a launch.  Candidates from 3/4 of `even` on are weighed (and the
+// cost their fp32 sums, and their join.  Candidates from 3/4 of `even` on are weighed (and the
 // longest unit's steps: nothing cut), the longer of equals first.  The constants, in steps, are from
-// sweeps: 8 requests of up to 512 rows over up to 8192 keys take 67 us cut at 33 steps, 73 at 18
-// to 30, 72 at 38 and 89 uncut; 4 causal sequences of up to 2048 32.8 uncut and 34.3 to 37.5 cut
-// at 13 to 8 of 14 steps, their backward pass 72.5 and 73.2 to 81.6 at 12 to 7.
+// sweeps: 8 requests of up to 512 rows over up to 8192 keys take 65 us cut at 30 or 33 steps, 73 at 27,
+// 84 at 18 and 22, 70 at 38 and 89 uncut; 4 causal sequences of up to 2048 30 uncut and 34, 35 and 39
+// cut at 13, 12 and 10 of 14 steps.
 constexpr int kPackedCandidates = 32;
 constexpr float kPackedStart = 4.f, kPackedJoin = 2.f, kPackedPart = 1.5f;
 __host__ __device__ inline float packed_even(long long steps, int heads, int target) {
@@ -77,10 +77,11 @@ __host__ __device__ inline int packed_candidate(int k, float even, int least, in
   return up < floor_ ? floor_ : up > longest ? longest : up;
 }
 __host__ __device__ inline int packed_cuts(int w, int slice) { return w <= slice ? 1 : (w + slice - 1) / slice; }
-__host__ __device__ inline float packed_time(int slice, int slices, int parts, long long steps, int heads, int target) {
-  const float join = parts > 0 ? kPackedJoin + packed_even(parts, heads, target) * kPackedPart : 0.f;
-  if ((float)slices * (float)heads <= 1.1f * (float)target) return (float)slice + kPackedStart + join;
-  return packed_even(steps, heads, target) + packed_even(slices, heads, target) * kPackedStart + 0.5f * (float)slice + join;
+// share: key heads for each of the target's CTAs, so that slices * share is the slices that each has.
+__host__ __device__ inline float packed_time(int slice, int slices, int parts, float even, float share) {
+  const float join = parts > 0 ? kPackedJoin + (float)parts * share * kPackedPart : 0.f;
+  if ((float)slices * share <= 1.1f) return (float)slice + kPackedStart + join;
+  return even + (float)slices * share * kPackedStart + 0.5f * (float)slice + join;
 }
 // A unit that is cut into c = ceil(w / P) slices has w > P, so that c < 2 w / P; with P at least 3/4 of
 // the even share all cut units take fewer than 8/3 target / heads slots.
