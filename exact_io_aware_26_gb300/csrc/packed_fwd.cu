@@ -464,7 +464,10 @@ __global__ void __launch_bounds__(192, 2)
           m_use = mx;
         }
         float mneg = m_use == -INFINITY ? 0.f : -m_use * c2;
-        if (__any_sync(0xffffffffu, fabsf(mneg) > kLargeScore)) {
+        // (rows that are not the sequence's, of other sequences or of nobody, have no say in it: results
+        // do not depend on what is there)
+        if (__any_sync(0xffffffffu, fabsf(mneg) > kLargeScore) &&
+            __any_sync(0xffffffffu, fabsf(mneg) > kLargeScore && r < place(k)->rows)) {
           // the rounded maximum would be off by more than 2^-8: the difference first, which is
           // exact near the maximum
           const float top = m_use == -INFINITY ? 0.f : m_use;

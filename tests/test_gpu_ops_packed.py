@@ -353,6 +353,34 @@ def test_same_results_again_and_from_graphs(cuda_lib):
     assert fa.get_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("d,Hq,Hk,new,keys", [(128, 6, 2, [200, 1, 31], [200, 900, 3]), (64, 5, 1, [33, 20, 90], [33, 700, 90])])
+def test_what_other_rows_hold_changes_no_bit(cuda_lib, d, Hq, Hk, new, keys):
+    """Neighbours of any size, and what earlier calls left in the places of rows that are nobody's (with
+    3 and 5 heads to a key head a tile has 126 and 125)."""
+    q, k, v, do = (x.cuda() for x in make(new, keys, Hq, Hk, d, "bf16", 17))
+    cu_q, cu_k = offsets(new), offsets(keys)
+
+    def run():
+        o, lse = fa.attention_fwd_packed(q, k, v, cu_q, cu_k)
+        return (o, lse) + fa.attention_bwd_packed(q, k, v, o, do, lse, cu_q, cu_k)
+
+    want = [x.clone() for x in run()]
+    full = torch.rand(60000, 2, d, device="cuda").bfloat16()
+    for size in (1e6, -1e12, 1e24, float("inf"), float("nan")):
+        fa.attention_fwd_packed(full * size, full, full, offsets([200] * 300))  # all 128 rows of every CTA's tiles
+        got = run()
+        assert all(torch.equal(got[i], want[i]) for i in (0, 1, 3, 4))
+    middle_q, middle_k = slice(new[0], new[0] + new[1]), slice(keys[0], keys[0] + keys[1])
+    for x, at in ((q, middle_q), (do, middle_q), (k, middle_k), (v, middle_k)):
+        x[at] *= 1e4
+    got = run()
+    rest_q = [i for i in range(sum(new)) if not middle_q.start <= i < middle_q.stop]
+    rest_k = [i for i in range(sum(keys)) if not middle_k.start <= i < middle_k.stop]
+    for i, rest in ((0, rest_q), (1, rest_q), (3, rest_k), (4, rest_k)):
+        assert torch.equal(got[i][rest], want[i][rest])
+    assert fa.get_status() == fa.FA_OK
+
+
 def test_many_sequences(cuda_lib):
     """More sequences than the work list's kernel has threads, most of them short or empty."""
     rng = torch.Generator().manual_seed(9)
