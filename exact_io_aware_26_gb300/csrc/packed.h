@@ -21,6 +21,7 @@ struct PackedPlanArgs {
   int tpt, causal, bwd;
   int target;          // CTAs to share the steps among
   int slots, least;    // places for parts of cut units (0: none is cut); steps that a slice has at least
+  int units;           // at most that many
   const int* cu_q;
   const int* cu_k;
   PackedList list;
@@ -48,12 +49,13 @@ struct PackedArgs {
   Report rep;
 };
 
-constexpr int kPackedDirect = 32;  // sequences that need no list: a lane each
+constexpr int kPackedFew = 32;  // sequences that a warp's lanes hold, one each
 #ifdef __CUDACC__
-// Without a list: unit `index` of at most 32 sequences, from their offsets, which lane r of each warp
-// reads for sequence r; false: there is none.  Offsets that are wrong are taken as by the list's
-// kernel, and recorded by the first CTA.
-__device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, PackedItem& x) {
+// At most 32 sequences from their offsets, lane r of a warp sequence r (and the last one in the lanes
+// behind it): each begins where the furthest offset up to its own lies.  wrong: some offset of
+// the lane's is outside the tensors or smaller than one before.
+template <class Args>
+__device__ __forceinline__ PackedSeq packed_lane_sequence(const Args& a, bool& wrong) {
   const int lane = threadIdx.x & 31, r = min(lane, a.R - 1);
   const int q0 = __ldg(a.cu_q + r), q1 = __ldg(a.cu_q + r + 1), k0 = __ldg(a.cu_k + r), k1 = __ldg(a.cu_k + r + 1);
   auto clamp = [](int v, int T) { return min(max(v, 0), T); };
@@ -68,15 +70,29 @@ __device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, Pa
   }
   s.n = max(clamp(q1, a.Tq), s.q0) - s.q0;
   s.m = max(clamp(k1, a.Tk), s.k0) - s.k0;
-  if (blockIdx.x == 0 && lane < a.R && (s.q0 != q0 || s.q0 + s.n != q1 || s.k0 != k0 || s.k0 + s.m != k1))
-    atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
-  const int mine = lane < a.R ? packed_units(s, a.tpt, false) : 0;
+  wrong = s.q0 != q0 || s.q0 + s.n != q1 || s.k0 != k0 || s.k0 + s.m != k1;
+  return s;
+}
+// The units up to and including those of the lane's sequence, of which it has `mine`.
+__device__ __forceinline__ int packed_lane_end(int mine) {
+  const int lane = threadIdx.x & 31;
   int end = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int up = __shfl_up_sync(0xffffffffu, end, off);
     if (lane >= off) end += up;
   }
+  return end;
+}
+
+// Without a list: unit `index` of at most 32 sequences; false: there is none.  Offsets that are wrong
+// are recorded by the first CTA.
+__device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, PackedItem& x) {
+  const int lane = threadIdx.x & 31;
+  bool wrong;
+  const PackedSeq s = packed_lane_sequence(a, wrong);
+  if (blockIdx.x == 0 && wrong) atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
+  const int mine = lane < a.R ? packed_units(s, a.tpt, false) : 0, end = packed_lane_end(mine);
   const uint32_t here = __ballot_sync(0xffffffffu, index < end && index >= end - mine);
   if (here == 0u) return false;
   const int from = __ffs((int)here) - 1;

@@ -54,7 +54,7 @@ fa_status check(const fa_packed_params* p, bool bwd) {
 
 // The sizes of a call's work list and where it lies in the workspace.
 struct Sizes {
-  int tpt, target, least, slots, items, cuts;
+  int tpt, target, least, slots, units, items, cuts;
   size_t items_at, cuts_at, left_at, starts_at, slots_at, stat_at, acc_at, bytes;
   Sizes(const fa_packed_params* p, int sms, bool bwd) {
     const int G = p->Hq / p->Hk;
@@ -65,7 +65,8 @@ struct Sizes {
     const long long most = bwd ? ((long long)p->Tq + tpt - 1) / tpt : ((long long)p->Tk + 127) / 128;
     slots = most > least ? packed_slots(p->Hk, target) : 0;
     cuts = slots / 2;
-    items = (int)((bwd ? p->Tk / 128 : p->Tq / tpt) + (long long)p->R + slots);
+    units = (int)((bwd ? p->Tk / 128 : p->Tq / tpt) + (long long)p->R);
+    items = units + slots;
     size_t at = 256;
     auto place = [&](size_t n) {
       const size_t here = at;
@@ -148,6 +149,7 @@ PackedPlanArgs plan_args(const PackedArgs& a, const Sizes& z, const int* cu_q, c
   q.target = z.target;
   q.slots = z.slots;
   q.least = z.least;
+  q.units = z.units;
   q.cu_q = cu_q;
   q.cu_k = cu_k;
   q.list = a.list;
@@ -205,7 +207,7 @@ fa_status fa_fwd_packed(const fa_packed_params* p, const void* q, const void* k,
   FA_TRY(map_of(&tm[2], p, none ? q : v, none ? 1 : p->Tk, p->Hk, p->v_stride, 1, 128));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // a few sequences that no cut can shorten need no list (three prompts of up to 32 tokens: 10.7 us with it)
-  a.direct = z.slots == 0 && p->R <= kPackedDirect;
+  a.direct = z.slots == 0 && p->R <= kPackedFew;
   a.cu_q = cu_q;
   a.cu_k = cu_k;
   cudaError_t e = cudaSuccess;

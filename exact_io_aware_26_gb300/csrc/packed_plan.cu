@@ -52,6 +52,11 @@ __device__ __forceinline__ void block_scan(int (&v)[N], int (*warp_s)[kWarps], i
   }
 }
 
+// FEW: at most 32 sequences, which each warp has in its lanes, of at most kThreads units, one a thread's, and
+// fewer than kGrouped asks for: half of the barriers and of the instructions (4 sequences of up to 2048
+// tokens 28.4 us and 29.8 without it, their backward pass 68.4 and 70.2, 8 pieces over a cached prefix
+// 63.2 and 65.3).
+template <bool FEW>
 __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // they wait for this grid's end
   __shared__ int near_s[4][kNear + 1];
@@ -76,46 +81,71 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
 
   // ---- the sequences: each begins where the furthest offset up to its own lies
   const int per = (R + kThreads) / kThreads, my0 = min(R + 1, tid * per), my1 = min(R + 1, my0 + per);
-  auto offset = [&](const int* cu, int T, int r) { return min(max(__ldg(cu + r), 0), T); };
-  auto larger = [](int x, int y) { return max(x, y); };
-  int most[2] = {0, 0}, last[2];
-#pragma unroll 1
-  for (int r = my0; r < my1; ++r) {
-    most[0] = max(most[0], offset(a.cu_q, a.Tq, r));
-    most[1] = max(most[1], offset(a.cu_k, a.Tk, r));
-  }
-  block_scan(most, scan_s, last, larger);
-  end_s[0][tid] = most[0];
-  end_s[1][tid] = most[1];
-  __syncthreads();
-  int run_q = tid ? end_s[0][tid - 1] : 0, run_k = tid ? end_s[1][tid - 1] : 0;
-  bool bad = false;
-#pragma unroll 1
-  for (int r = my0; r < my1; ++r) {
-    run_q = max(run_q, offset(a.cu_q, a.Tq, r));
-    run_k = max(run_k, offset(a.cu_k, a.Tk, r));
-    bad |= run_q != __ldg(a.cu_q + r) || run_k != __ldg(a.cu_k + r);
-    first_q[r] = run_q;
-    first_k[r] = run_k;
-  }
-  if (bad) atomicCAS(&a.st->code, 0, (int)FA_ERR_INDEX);
-  __syncthreads();
   auto sequence = [&](int r) {
     return PackedSeq{first_q[r], first_q[r + 1] - first_q[r], first_k[r], first_k[r + 1] - first_k[r]};
   };
-  int mine[1] = {0}, all[1];
+  PackedItem own;  // this thread's first unit
+  own.s0 = own.s1 = 0;
+  int units, rows0, rows1;  // units; query rows that are a sequence's
+  if constexpr (FEW) {
+    bool wrong;
+    const PackedSeq s = packed_lane_sequence(a, wrong);
+    if (warp == 0 && wrong) atomicCAS(&a.st->code, 0, (int)FA_ERR_INDEX);
+    const int mine = lane < R ? packed_units(s, a.tpt, a.bwd) : 0, end = packed_lane_end(mine);
+    units = __shfl_sync(0xffffffffu, end, 31);
+    rows0 = __shfl_sync(0xffffffffu, s.q0, 0);
+    rows1 = __shfl_sync(0xffffffffu, s.q0 + s.n, 31);
+    int of = 0;  // the sequence of unit tid: those before it end at it at most
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      if (__shfl_sync(0xffffffffu, end, of + off - 1) <= tid) of += off;
+    own.seq.q0 = __shfl_sync(0xffffffffu, s.q0, of);
+    own.seq.n = __shfl_sync(0xffffffffu, s.n, of);
+    own.seq.k0 = __shfl_sync(0xffffffffu, s.k0, of);
+    own.seq.m = __shfl_sync(0xffffffffu, s.m, of);
+    own.tile = tid - __shfl_sync(0xffffffffu, end - mine, of);
+    if (tid < units) packed_steps(own.seq, own.tile, a.tpt, a.causal, a.bwd, own.s0, own.s1);
+  } else {
+    auto offset = [&](const int* cu, int T, int r) { return min(max(__ldg(cu + r), 0), T); };
+    auto larger = [](int x, int y) { return max(x, y); };
+    int most[2] = {0, 0}, last[2];
 #pragma unroll 1
-  for (int r = my0; r < min(my1, R); ++r) mine[0] += packed_units(sequence(r), a.tpt, a.bwd);
-  int at = -mine[0];
-  block_scan(mine, scan_s + 2, all, [](int x, int y) { return x + y; });
-  const int units = all[0];
-  at += mine[0];
+    for (int r = my0; r < my1; ++r) {
+      most[0] = max(most[0], offset(a.cu_q, a.Tq, r));
+      most[1] = max(most[1], offset(a.cu_k, a.Tk, r));
+    }
+    block_scan(most, scan_s, last, larger);
+    end_s[0][tid] = most[0];
+    end_s[1][tid] = most[1];
+    __syncthreads();
+    int run_q = tid ? end_s[0][tid - 1] : 0, run_k = tid ? end_s[1][tid - 1] : 0;
+    bool bad = false;
 #pragma unroll 1
-  for (int r = my0; r < my1; ++r) {
-    first_u[r] = at;
-    if (r < R) at += packed_units(sequence(r), a.tpt, a.bwd);
+    for (int r = my0; r < my1; ++r) {
+      run_q = max(run_q, offset(a.cu_q, a.Tq, r));
+      run_k = max(run_k, offset(a.cu_k, a.Tk, r));
+      bad |= run_q != __ldg(a.cu_q + r) || run_k != __ldg(a.cu_k + r);
+      first_q[r] = run_q;
+      first_k[r] = run_k;
+    }
+    if (bad) atomicCAS(&a.st->code, 0, (int)FA_ERR_INDEX);
+    __syncthreads();
+    int mine[1] = {0}, all[1];
+#pragma unroll 1
+    for (int r = my0; r < min(my1, R); ++r) mine[0] += packed_units(sequence(r), a.tpt, a.bwd);
+    int at = -mine[0];
+    block_scan(mine, scan_s + 2, all, [](int x, int y) { return x + y; });
+    units = all[0];
+    at += mine[0];
+#pragma unroll 1
+    for (int r = my0; r < my1; ++r) {
+      first_u[r] = at;
+      if (r < R) at += packed_units(sequence(r), a.tpt, a.bwd);
+    }
+    __syncthreads();
+    rows0 = first_q[0];
+    rows1 = first_q[R];
   }
-  __syncthreads();
 
   // ---- a unit's sequence, tile and steps
   auto unit = [&](int u, PackedItem& x) {
@@ -129,10 +159,12 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     x.slot = lo;  // until it is placed
     packed_steps(x.seq, x.tile, a.tpt, a.causal, a.bwd, x.s0, x.s1);
   };
-  PackedItem own;  // this thread's first unit
-  own.s0 = own.s1 = 0;
-  if (tid < units) unit(tid, own);
+  if (!FEW && tid < units) unit(tid, own);
   auto with_units = [&](auto f) {  // f(unit) of every unit of this thread
+    if constexpr (FEW) {
+      if (tid < units) f(tid, own);
+      return;
+    }
     PackedItem x = own;
 #pragma unroll 1
     for (int u = tid; u < units; u += kThreads) {
@@ -146,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     const int w = x.s1 - x.s0;
     steps += w;
     longest = max(longest, w);
-    if (u < kWeighed) work_s[u] = w;
+    if (FEW || u < kWeighed) work_s[u] = w;
   });
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, off);
@@ -166,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   const float even = packed_even(steps, a.Hk, a.target);
   int slice = longest;
   if (a.slots > 0 && longest > a.least && (float)longest > 0.75f * even) {
-    if (units <= kWeighed) {
+    if (FEW || units <= kWeighed) {
       const int mine_slice = packed_candidate(warp, even, a.least, longest);
       int n = 0, cut = 0;
       for (int u = lane; u < units; u += 32) {
@@ -199,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
 
   // ---- many whole units: the sequences by their longest units' steps, and the units of each behind one
   // another, the longest first, so that the CTAs that run at a time read the same sequence
-  if (slice == longest && (float)units * (float)a.Hk >= kGrouped * (float)a.target) {
+  if (!FEW && slice == longest && (float)units * (float)a.Hk >= kGrouped * (float)a.target) {
     auto seq_class = [&](int r, const PackedSeq& q, int n) {
       int s0, s1;
       packed_steps(q, a.bwd ? 0 : n - 1, a.tpt, a.causal, a.bwd, s0, s1);
@@ -234,8 +266,8 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     if (tid == 0) {
       a.list.head[0] = units;
       a.list.head[1] = 0;
-      a.list.head[2] = first_q[0];  // query rows that are a sequence's
-      a.list.head[3] = first_q[R];
+      a.list.head[2] = rows0;
+      a.list.head[3] = rows1;
       a.list.head[4] = 0;
     }
     return;
@@ -295,8 +327,8 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   if (tid == 0) {
     a.list.head[0] = items[0];
     a.list.head[1] = cut_s;
-    a.list.head[2] = first_q[0];  // query rows that are a sequence's
-    a.list.head[3] = first_q[R];
+    a.list.head[2] = rows0;
+    a.list.head[3] = rows1;
     a.list.head[4] = 0;
   }
 }
@@ -304,7 +336,11 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
 }  // namespace
 
 cudaError_t launch_packed_plan(const PackedPlanArgs& a, cudaStream_t s) {
-  packed_plan_kernel<<<1, kThreads, 0, s>>>(a);
+  const bool few = a.R <= kPackedFew && a.units <= kThreads && (float)a.units * (float)a.Hk < kGrouped * (float)a.target;
+  if (few)
+    packed_plan_kernel<true><<<1, kThreads, 0, s>>>(a);
+  else
+    packed_plan_kernel<false><<<1, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
