@@ -1,7 +1,7 @@
 // kv_attn.cuh -- attention of each request's newest tokens over its 4-bit or 8-bit cache.
 //
-// Bound: HBM.  A token of one head is 160 bytes (d = 128) for both its key and its
-// value, and 8 query rows need 4 * 8 * d FLOPs of it: 26 FLOPs a byte, far below
+// Bound: HBM.  A token of one head is 160 bytes (d = 128; in 8 bits 257) for both its key and
+// its value, and 8 query rows need 4 * 8 * d FLOPs of it: 26 (16) FLOPs a byte, far below
 // what the tensor cores give.  What limits the kernel besides is turning codes into
 // fp16 operands, so that is done once per token for all query heads of its key head,
 // in registers, straight into tensor-core fragments.
@@ -42,6 +42,7 @@
 // 145 us for 748 MB, 5.2 TB/s; the unit loop alone goes at 5.9 TB/s, with the integer pipe at
 // 54% (codes to fp16) and four warps a scheduler, and about 13 us are start-up, uneven ends
 // and the second kernel.  (Clusters): one request of 23,400 tokens, 12 heads, d = 64: 14.5 us.
+// In 8 bits, 1202 MB of the same requests: 190 us, 6.3 TB/s; the day's one request 15.7 us.
 #pragma once
 #include <type_traits>
 

@@ -90,7 +90,7 @@ struct Kv4AttnArgs {
   int4* meta;       // two per CTA: the tile that starts in its share and goes on
   Report rep;
 };
-// Rows of a query tile: 8, 16 or 32 (kv4_attn.cuh).
+// Rows of a query tile: 8, 16 or 32 (kv_attn.cuh).
 inline int kv4_tile_rows(int G, int max_q_len) {
   const long long rows = (long long)G * max_q_len;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;

@@ -253,7 +253,9 @@ long long kv4_clusters(int dev, int bits, int d, int rows, int log) {
 // shares: d = 64, 12 tiles of 16384 tokens 12.7 and 15.0 us (4 units a warp and 3), of 24576
 // 14.9 and 14.7 (6 and 4), of 49152 22.4 and 19.4 (12 and 8); d = 128, 8 tiles of 4096
 // tokens 10.5 and 11.1 us (1 and 1), of 8192 12.5 and 12.2 (2 and 1), of 16384 16.6 and 14.4
-// (4 and 2).
+// (4 and 2).  In 8 bits: d = 64, 48 tiles of 2048 tokens 9.2 and 10.9 us, 12 of 16384
+// 12.4 and 12.8; d = 128, 8 tiles of 4096 tokens 9.4 and 10.6, 64 of 2048 12.4 and 16.6, 32 tiles of
+// 32 rows over 8192 tokens 28.8 and 36.2.
 int kv4_cluster(int bits, const fa_kv4_cache* c, const fa_kv4_attn_params* p, int rows, int share_ctas) {
   const long long tiles = kv4_tiles(c, p, rows);
   long long tokens = (long long)p->table_width * c->page_size;

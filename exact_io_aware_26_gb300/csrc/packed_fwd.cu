@@ -201,7 +201,8 @@ __device__ __noinline__ void join_parts(const PackedArgs& a, const PackedItem& x
   }
 }
 
-template <int D, bool F16>
+// DIRECT: no list; each CTA has one item, which it finds in the offsets, and nothing is cut.
+template <int D, bool F16, bool DIRECT>
 __global__ void __launch_bounds__(192, 2)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PackedArgs a) {
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(192, 2)
   const uint32_t sb = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (!a.direct) asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
+  if (!DIRECT) asm volatile("griddepcontrol.wait;" ::: "memory");  // the list
   const FwdBars<NS> bars{sb + L::BAR};
   auto more = [&](int i) { return sb + L::MORE + 8u * (uint32_t)i; };
   auto bar_item = [&](int k) { return more(k & 1); };
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(192, 2)
     const int at = a.divHk.div(index);
     hk = index - at * a.Hk;
     x.tile = -1;
-    if (a.direct) {
-      if (k == 0 && !packed_direct(a, at, x)) x.tile = -1;
+    if (DIRECT) {
+      if (!packed_direct(a, at, x)) x.tile = -1;
     } else if (k == 0) {  // there is room for it in the list: on its way beside the list's length
       total = a.list.head[0] * a.Hk;
       x = a.list.items[at];
@@ -324,13 +325,12 @@ __global__ void __launch_bounds__(192, 2)
         }
         if (!go) break;
       }
+      if (DIRECT) break;
       // the next one: taken in order as CTAs come to need them
       ++k;
-      int index = 0x7FFFFFFF;
-      if (!a.direct) {
-        if (lane == 0) index = (int)gridDim.x + atomicAdd(a.list.head + 4, 1);
-        index = __shfl_sync(0xffffffffu, index, 0);
-      }
+      int index = 0;
+      if (lane == 0) index = (int)gridDim.x + atomicAdd(a.list.head + 4, 1);
+      index = __shfl_sync(0xffffffffu, index, 0);
       if (k >= 2 && !(go = warp_wait(w, bar_item_free(k), ((k >> 1) - 1) & 1))) break;
       if (!(go = publish(k, index))) break;
     }
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(192, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_item_free(k));
-      if (tile < 0) break;
+      if (DIRECT || tile < 0) break;
     }
     tc_commit_elect(bars.fin());
     if (lane == 0) mbar_drain(w, bars.fin(), 0);
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(192, 2)
       const int i = a.divG.div(r), token = x->x.seq.q0 + x->x.tile * a.tpt + i, hk = x->hk, head = hk * a.G + r - i * a.G;
       const bool live = r < x->rows;
       const int slot = x->x.slot;
-      const bool whole = slot < 0;
+      const bool whole = DIRECT || slot < 0;
       const float inv_l = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
       float* part = whole ? nullptr : a.slots + ((long long)slot * a.Hk + hk) * (kTile * (D + 2));
       if (whole) {
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(192, 2)
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0u;
         }
-        if (have_o && c0 + 32 == D) {  // all is in registers: the next item's O may go there
+        if (!DIRECT && have_o && c0 + 32 == D) {  // all is in registers: the next item's O may go there
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_o_free);
@@ -605,6 +605,7 @@ __global__ void __launch_bounds__(192, 2)
         if (*last) join_parts<D, F16>(a, x->x, hk, r);
         __syncwarp();
       }
+      if (DIRECT) break;
       if (lane == 0) mbar_arrive(bar_item_free(k));
     }
   }
@@ -617,10 +618,10 @@ __global__ void __launch_bounds__(192, 2)
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool DIRECT>
 cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, cudaStream_t s) {
   using L = Layout<D>;
-  const auto kern = packed_fwd_kernel<D, F16>;
+  const auto kern = packed_fwd_kernel<D, F16, DIRECT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -628,23 +629,28 @@ cudaError_t launch_t(const PackedArgs& a, const CUtensorMap* tm, int items, cuda
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = a.direct ? 0 : 1;
+  cfg.numAttrs = DIRECT ? 0 : 1;
   cfg.stream = s;
   // CTAs that stay and take one item after the other; without a list an item each
   const long long all = (long long)items * a.Hk;
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  cfg.gridDim = dim3((unsigned)(a.direct ? all : std::min(all, 2ll * sms)));
+  cfg.gridDim = dim3((unsigned)(DIRECT ? all : std::min(all, 2ll * sms)));
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = L::BYTES;
   return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], a);
 }
 
+template <int D, bool F16>
+cudaError_t launch_any(const PackedArgs& a, const CUtensorMap* tm, int items, cudaStream_t s) {
+  return a.direct ? launch_t<D, F16, true>(a, tm, items, s) : launch_t<D, F16, false>(a, tm, items, s);
+}
+
 }  // namespace
 
 cudaError_t launch_packed_fwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s) {
-  if (d == 64) return f16 ? launch_t<64, true>(a, tm, items, s) : launch_t<64, false>(a, tm, items, s);
-  return f16 ? launch_t<128, true>(a, tm, items, s) : launch_t<128, false>(a, tm, items, s);
+  if (d == 64) return f16 ? launch_any<64, true>(a, tm, items, s) : launch_any<64, false>(a, tm, items, s);
+  return f16 ? launch_any<128, true>(a, tm, items, s) : launch_any<128, false>(a, tm, items, s);
 }
 
 }  // namespace fa

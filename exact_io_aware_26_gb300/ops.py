@@ -1,6 +1,6 @@
-"""The operators around the attention: norms and rotation of queries and keys, the
-4-bit paged cache with the attention that reads it, and block tables from request
-lengths.  Binding only, like the package's front: arguments are checked and turned
+"""The operators around the attention: norms and rotation of queries and keys, attention of
+packed sequences with grouped heads, the 4-bit and 8-bit paged caches with the attention that
+reads them, and block tables from request lengths.  Binding only, like the package's front: arguments are checked and turned
 into the C ABI of ``include/fa.h``; the kernels do the rest.
 
 Training, from a packed projection [B, N, Hq + 2 Hk, d] to the attention's layout:
@@ -11,12 +11,22 @@ Training, from a packed projection [B, N, Hq + 2 Hk, d] to the attention's layou
     dq, dk, dv = fa.attention_bwd(q, k, v, o, do, lse, causal=True)
     dxq, dxk, dwq, dwk = fa.qk_norm_rope_bwd(qkv[:, :, :H], qkv[:, :, H:2*H], dq, dk, wq, wk, freqs)
 
+Training on sequences of different lengths, packed one behind the other (cu: their offsets):
+
+    o, lse = fa.attention_fwd_packed(q, k, v, cu)              # q [T, Hq, d], k and v [T, Hk, d]
+    dq, dk, dv = fa.attention_bwd_packed(q, k, v, o, do, lse, cu)
+
 Serving, one step of R requests:
 
     plan = fa.paged_plan(seq_lens, new_lens, block_table, free_pages, free_count, page_size, T)
     q, k = fa.qk_norm_rope(xq[None], xk[None], wq, wk, freqs, positions=plan["positions"][None], heads_first=False)
     fa.kv4_append(k[0], v, plan["slots"], cache)
     o, lse = fa.kv4_attention(q[0], cache, block_table, plan["kv_lens"], cu_q=plan["cu_q"])
+
+(``kv8_...`` the same over a cache of 8 bits.)  Prompts, or pieces of them over what is cached:
+
+    k16, v16 = fa.kv8_gather(cache, slots, d)                  # all the requests' tokens
+    o, lse = fa.attention_fwd_packed(q[0], k16, v16, plan["cu_q"], cu_k)
 
 Every tensor lies on the current device.  Results and workspaces are allocated on
 ``stream`` (default: the current one); inputs that another stream may free are marked
@@ -358,7 +368,8 @@ def kv8_append(k, v, slots, cache, stream=None) -> None:
 def kv4_gather(cache, slots, d: int, dtype=torch.bfloat16, heads_first: bool = False, out=None, stream=None):
     """(k, v): the cached keys and values of T slots (zeros for a negative one), rounded to
     ``dtype``: [T, Hk, d], or, ``heads_first``, [Hk, T, d]; with a leading batch of one
-    ``attention_fwd`` takes these for the T queries of the same tokens and Hq = Hk."""
+    ``attention_fwd`` takes these for the T queries of the same tokens and Hq = Hk, and, as
+    [T, Hk, d], ``attention_fwd_packed`` for new rows over them and grouped heads."""
     k, v = (None, None) if out is None else out
     return _call(_GATHER, (cache, slots, k, v), (int(d), dtype, bool(heads_first), 4), stream, _plan_gather)
 
