@@ -54,10 +54,17 @@ constexpr int kPackedFew = 32;  // sequences that a warp's lanes hold, one each
 // At most 32 sequences from their offsets, lane r of a warp sequence r (and the last one in the lanes
 // behind it): each begins where the furthest offset up to its own lies.  wrong: some offset of
 // the lane's is outside the tensors or smaller than one before.
+struct PackedOffsets {
+  int q0, q1, k0, k1;
+};
 template <class Args>
-__device__ __forceinline__ PackedSeq packed_lane_sequence(const Args& a, bool& wrong) {
-  const int lane = threadIdx.x & 31, r = min(lane, a.R - 1);
-  const int q0 = __ldg(a.cu_q + r), q1 = __ldg(a.cu_q + r + 1), k0 = __ldg(a.cu_k + r), k1 = __ldg(a.cu_k + r + 1);
+__device__ __forceinline__ PackedOffsets packed_lane_offsets(const Args& a) {
+  const int r = min((int)(threadIdx.x & 31), a.R - 1);
+  return PackedOffsets{__ldg(a.cu_q + r), __ldg(a.cu_q + r + 1), __ldg(a.cu_k + r), __ldg(a.cu_k + r + 1)};
+}
+template <class Args>
+__device__ __forceinline__ PackedSeq packed_lane_sequence(const Args& a, const PackedOffsets& cu, bool& wrong) {
+  const int lane = threadIdx.x & 31, q0 = cu.q0, q1 = cu.q1, k0 = cu.k0, k1 = cu.k1;
   auto clamp = [](int v, int T) { return min(max(v, 0), T); };
   PackedSeq s{clamp(q0, a.Tq), 0, clamp(k0, a.Tk), 0};
 #pragma unroll
@@ -87,10 +94,10 @@ __device__ __forceinline__ int packed_lane_end(int mine) {
 
 // Without a list: unit `index` of at most 32 sequences; false: there is none.  Offsets that are wrong
 // are recorded by the first CTA.
-__device__ __forceinline__ bool packed_direct(const PackedArgs& a, int index, PackedItem& x) {
+__device__ __forceinline__ bool packed_direct(const PackedArgs& a, const PackedOffsets& cu, int index, PackedItem& x) {
   const int lane = threadIdx.x & 31;
   bool wrong;
-  const PackedSeq s = packed_lane_sequence(a, wrong);
+  const PackedSeq s = packed_lane_sequence(a, cu, wrong);
   if (blockIdx.x == 0 && wrong) atomicCAS(&a.rep.st->code, 0, (int)FA_ERR_INDEX);
   const int mine = lane < a.R ? packed_units(s, a.tpt, false) : 0, end = packed_lane_end(mine);
   const uint32_t here = __ballot_sync(0xffffffffu, index < end && index >= end - mine);

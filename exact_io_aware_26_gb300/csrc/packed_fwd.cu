@@ -229,21 +229,9 @@ __global__ void __launch_bounds__(192, 2)
   // the items that have any (n: those of q, q_free and o_free).
   auto place = [&](int k) { return reinterpret_cast<Work*>(smem + L::ITEM) + (k & 1); };
   // producer: its item; K and V copies, items with copies, parts of cut units so far
-  PackedItem x;
+  PackedItem x{};
   int hk = 0, it = 0, nv = 0, n = 0, cuts = 0, total = 0;
-  auto publish = [&](int k, int index) -> bool {  // false: a check of the debug build failed
-    const int at = a.divHk.div(index);
-    hk = index - at * a.Hk;
-    x.tile = -1;
-    if (DIRECT) {
-      if (!packed_direct(a, at, x)) x.tile = -1;
-    } else if (k == 0) {  // there is room for it in the list: on its way beside the list's length
-      total = a.list.head[0] * a.Hk;
-      x = a.list.items[at];
-      if (index >= total) x.tile = -1;
-    } else if (index < total) {
-      x = a.list.items[at];
-    }
+  auto publish = [&](int k) -> bool {  // false: a check of the debug build failed
     // debug build: the tile lies in its sequence, and that in the tensors
     if (x.tile >= 0 && !__all_sync(0xffffffffu, dbg_check(w, x.tile * a.tpt < x.seq.n && x.s0 >= 0 && x.s0 <= x.s1 &&
                                                                  x.s1 <= packed_units(x.seq, a.tpt, true) && x.seq.q0 >= 0 &&
@@ -269,6 +257,8 @@ __global__ void __launch_bounds__(192, 2)
   };
   bool go = true;
   if (warp == 4) {
+    PackedOffsets cu{};
+    if (DIRECT) cu = packed_lane_offsets(a);  // on their way beside the barriers' set-up
     if (lane == 0) {
       bars.init();
       for (int k = 0; k < 2; ++k) {
@@ -283,8 +273,18 @@ __global__ void __launch_bounds__(192, 2)
       fence_barrier_init();
     }
     __syncwarp();
-    // the first item is the CTA's own; its copies that need no wait go beside the set-up
-    go = publish(0, (int)blockIdx.x);
+    // the first item is the CTA's own
+    const int index = (int)blockIdx.x, at = a.divHk.div(index);
+    hk = index - at * a.Hk;
+    if (DIRECT) {
+      if (!packed_direct(a, cu, at, x)) x.tile = -1;
+    } else {  // there is room for it in the list: on its way beside the list's length
+      total = a.list.head[0] * a.Hk;
+      x = a.list.items[at];
+      if (index >= total) x.tile = -1;
+    }
+    go = publish(0);
+    // its copies that need no wait go beside the rest of the set-up
     if (go && x.tile >= 0 && x.s0 < x.s1) {
       n = 1;
       if (lane == 0) load_q();
@@ -332,7 +332,11 @@ __global__ void __launch_bounds__(192, 2)
       if (lane == 0) index = (int)gridDim.x + atomicAdd(a.list.head + 4, 1);
       index = __shfl_sync(0xffffffffu, index, 0);
       if (k >= 2 && !(go = warp_wait(w, bar_item_free(k), ((k >> 1) - 1) & 1))) break;
-      if (!(go = publish(k, index))) break;
+      const int at = a.divHk.div(index);
+      hk = index - at * a.Hk;
+      x.tile = -1;
+      if (index < total) x = a.list.items[at];
+      if (!(go = publish(k))) break;
     }
     if (lane == 0) {  // every copy has landed before the CTA ends
       if (n > 0) mbar_drain(w, bars.q(), (n - 1) & 1);

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   int units, rows0, rows1;  // units; query rows that are a sequence's
   if constexpr (FEW) {
     bool wrong;
-    const PackedSeq s = packed_lane_sequence(a, wrong);
+    const PackedSeq s = packed_lane_sequence(a, packed_lane_offsets(a), wrong);
     if (warp == 0 && wrong) atomicCAS(&a.st->code, 0, (int)FA_ERR_INDEX);
     const int mine = lane < R ? packed_units(s, a.tpt, a.bwd) : 0, end = packed_lane_end(mine);
     units = __shfl_sync(0xffffffffu, end, 31);
