@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       const float* dsum = a.stat_d + (long long)hk * a.Tq * G;
       const uint32_t q_bytes = (uint32_t)full * D * 2u;
       // Q and dO of the first query tiles go ahead of K_j and V_j, whose places are free when the last
-      // item's products are done; one stage is freed by those products only
-      const int ahead = min(x.s0 + NS - 1, x.s1);
+      // item's products are done; one stage is freed by those products only.  (A CTA's first K_j and V_j at
+      // once: at d = 64 4 sequences of up to 2048 tokens 66.8 and 67.7 us; at d = 128 it gains nothing.)
+      const int ahead = D == 64 && loads == 0 ? x.s0 : min(x.s0 + NS - 1, x.s1);
       for (int qt = x.s0; go && qt <= x.s1; ++qt) {
         if (qt == ahead) {
           if (loads > 0 && !(go = warp_wait(w, bar_done, (loads - 1) & 1))) break;
@@ -638,15 +639,18 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       tc_fence_after();
       {
         const bool store = r < x->keys;
-        const int hk = x->hk, token = x->key0 + r;
+        const int hk = x->hk;
         float* part = x->slot < 0 ? nullptr
                                   : a.slots + ((long long)x->slot * a.Hk + hk) * (2 * kTile * D) + 4 * (g * L::DQG / 4 * kTile + r);
         constexpr int EC = L::DQG < 32 ? L::DQG : 32;
+#pragma unroll 1
         for (int which = 0; which < 2; ++which) {
           const uint32_t col = (which == 0 ? L::T_DV : L::T_DK) + g * L::DQG;
           const float mul = which == 0 ? 1.f : a.scale;
           const long long* st = which == 0 ? a.dvs : a.dks;
-          uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) + (long long)token * st[0] + hk * st[1] + g * L::DQG;
+          constexpr int N = D == 64 ? 2 : 1;  // lanes that store a key's row
+          uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) + (long long)(x->key0 + (r & -N)) * st[0] + hk * st[1] +
+                          g * L::DQG + 8 * (r % N);
 #pragma unroll
           for (int c0 = 0; c0 < L::DQG; c0 += EC) {
             uint32_t u[EC];
@@ -666,15 +670,33 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
               for (int v = 0; v < EC / 4; ++v)
                 *reinterpret_cast<uint4*>(part + which * (kTile * D) + 4 * kTile * (c0 / 4 + v)) =
                     make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
-            } else if (store) {
+            } else {
+              uint4 q[EC / 8];
 #pragma unroll
               for (int v = 0; v < EC / 8; ++v) {
-                uint4 q;
-                q.x = pack2<F16>(__uint_as_float(u[v * 8 + 0]) * mul, __uint_as_float(u[v * 8 + 1]) * mul);
-                q.y = pack2<F16>(__uint_as_float(u[v * 8 + 2]) * mul, __uint_as_float(u[v * 8 + 3]) * mul);
-                q.z = pack2<F16>(__uint_as_float(u[v * 8 + 4]) * mul, __uint_as_float(u[v * 8 + 5]) * mul);
-                q.w = pack2<F16>(__uint_as_float(u[v * 8 + 6]) * mul, __uint_as_float(u[v * 8 + 7]) * mul);
-                *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q;
+                q[v].x = pack2<F16>(__uint_as_float(u[v * 8 + 0]) * mul, __uint_as_float(u[v * 8 + 1]) * mul);
+                q[v].y = pack2<F16>(__uint_as_float(u[v * 8 + 2]) * mul, __uint_as_float(u[v * 8 + 3]) * mul);
+                q[v].z = pack2<F16>(__uint_as_float(u[v * 8 + 4]) * mul, __uint_as_float(u[v * 8 + 5]) * mul);
+                q[v].w = pack2<F16>(__uint_as_float(u[v * 8 + 6]) * mul, __uint_as_float(u[v * 8 + 7]) * mul);
+              }
+              if constexpr (D == 64) {
+                // two lanes with 32 bytes of a key each exchange 16, so that they store side by side (4
+                // sequences of up to 2048 tokens 64.2 us and not 66.8; four lanes with 64 bytes at d = 128
+                // and in the forward pass were slower so)
+                static_assert(EC == 16);
+                const bool odd = lane & 1;
+                uint4 t = odd ? q[0] : q[1];
+                t.x = __shfl_xor_sync(0xffffffffu, t.x, 1);
+                t.y = __shfl_xor_sync(0xffffffffu, t.y, 1);
+                t.z = __shfl_xor_sync(0xffffffffu, t.z, 1);
+                t.w = __shfl_xor_sync(0xffffffffu, t.w, 1);
+                if (odd) q[0] = t; else q[1] = t;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if ((r & ~1) + j < x->keys) *reinterpret_cast<uint4*>(dst + j * st[0]) = q[j];
+              } else if (store) {
+#pragma unroll
+                for (int v = 0; v < EC / 8; ++v) *reinterpret_cast<uint4*>(dst + c0 + v * 8) = q[v];
               }
             }
             __syncwarp();

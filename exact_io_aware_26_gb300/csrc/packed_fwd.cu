@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(192, 2)
       const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)x->x.seq.k0 * a.vs[0] + hk * a.vs[1];
       const int last_key = min(limit(x), x->x.s1 * kTile);
       uint16_t* dst = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1];
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t o[32];
         if (have_o) {
