@@ -7,7 +7,7 @@
 //     128 rows with its heads, and K and V are read once for all of them;
 //   - tiles taken from the list that packed_plan.cu makes of the offsets, longest first, by CTAs that
 //     stay: the next tile's copies and first scores run beside the last one's results' way out
-//     (1520 sequences of 512 tokens, d = 128: 267 us with a CTA for each tile, 229 so);
+//     (1520 sequences of 512 tokens, one head, d = 128: 267 us with a CTA for each tile, 229 so);
 //   - units longer than an even share of the steps cut along the keys, their parts (m, l, O in
 //     fp32) joined by the CTA that is done last, so that few rows over many keys fill the GPU (8
 //     requests of up to 512 rows over up to 8192 keys: 89 us uncut, 65 cut);
@@ -541,6 +541,8 @@ __global__ void __launch_bounds__(192, 2)
       const uint16_t* vrow = static_cast<const uint16_t*>(a.v) + (long long)x->x.seq.k0 * a.vs[0] + hk * a.vs[1];
       const int last_key = min(limit(x), x->x.s1 * kTile);
       uint16_t* dst = static_cast<uint16_t*>(a.o) + (long long)token * a.os[0] + head * a.os[1];
+      // (rolled: an item's end is bound by the fetching of its instructions; unrolled, 12 sequences of up to
+      // 16384 tokens take 7.6 ms and not 7.3, 4 of up to 2048 28.0 us and not 27.7)
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t o[32];
