@@ -19,7 +19,7 @@
 //
 // Bound: the tensor core (five products, 10 d FLOPs a seen pair and query head) beside the
 // exponentials and the elementwise steps; one CTA an SM.  Measured, causal, with the kernels before
-// and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 914 TFLOP/s (6.5 ms).
+// and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 951 TFLOP/s (6.23 ms).
 //
 // Warp roles as in bwd_tc.cu: 4 NG compute warps in NG groups that split the 128 query
 // columns of a tile (TMEM lane = key row); a producer warp; a warp that owns TMEM and issues the
