@@ -30,7 +30,7 @@ def forward(q, k, v, new, keys, causal, scale, half_step, tiny):
     Bounds, with e = half_step (the inputs' type) and w the weights relative to their sum:
     a score is off by d roundings of 2^-23 of its terms (fp32 accumulation), s, and the exponential
     by 2^-21 and 2^-23 of its argument; a weight for the product by e (or `tiny` / 2 where subnormal);
-    the sums over m keys by m 2^-23; the result by e."""
+    the sums over m keys by m 2^-23; the result by e, or `tiny` / 2 below the normal numbers."""
     Hq, d = q.shape[1:]
     G = Hq // k.shape[1]
     o, ob = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
@@ -48,7 +48,7 @@ def forward(q, k, v, new, keys, causal, scale, half_step, tiny):
         off = s + 2.0 ** -21 + torch.where(mask, (x - x.amax(-1, keepdim=True)).abs().nan_to_num(0, 0, 0) * 2.0 ** -23, 0.0)
         most = (p * off).sum(-1, keepdim=True)  # of the sum of the weights
         b = (p * (off + half_step + m * 2.0 ** -23 + most)) @ V.abs() + tiny / 2 * m * V.abs().amax(1, keepdim=True)
-        o[rows], ob[rows] = y.transpose(0, 1), (b + half_step * (y.abs() + b)).transpose(0, 1)
+        o[rows], ob[rows] = y.transpose(0, 1), (b + half_step * (y.abs() + b) + tiny / 2).transpose(0, 1)
         lse[rows] = l[..., 0].T
         lb[rows] = (most + m * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * l.abs().nan_to_num(0, 0, 0))[..., 0].T
     return o, lse, ob, lb
@@ -59,7 +59,8 @@ def backward(q, k, v, o, do, lse, new, keys, causal, scale, half_step, tiny):
 
     A weight is off by what its score, the saved LSE (2^-24 of it) and the exponential are; it is
     rounded by e for dV; dP and D by d roundings of 2^-23 of their terms; dS by e for dK, dQ
-    (or `tiny` / 2 where subnormal); sums by their length times 2^-23; results by e."""
+    (or `tiny` / 2 where subnormal); sums by their length times 2^-23; results by e, or, below the
+    normal numbers, where they are multiples of `tiny`, by half of that."""
     Hq, d = q.shape[1:]
     Hk = k.shape[1]
     G = Hq // Hk
@@ -88,5 +89,5 @@ def backward(q, k, v, o, do, lse, new, keys, causal, scale, half_step, tiny):
             y, b = found[i].transpose(0, 1), slack[i].transpose(0, 1)
             if i:
                 y, b = y.unflatten(1, (Hk, G)).sum(2), b.unflatten(1, (Hk, G)).sum(2)
-            grads[i][at], bounds[i][at] = y, b + e * (y.abs() + b)
+            grads[i][at], bounds[i][at] = y, b + e * (y.abs() + b) + tiny / 2
     return grads, bounds

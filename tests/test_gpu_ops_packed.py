@@ -65,6 +65,7 @@ CASES = [
     ([64, 130], [900, 2000], 10, 2, 64, "f16", False),
     ([200, 50], [100, 0], 3, 3, 128, "bf16", True),        # rows that see no key, a sequence without keys
     ([0, 0], [130, 5], 2, 1, 64, "f16", True),             # keys without a query
+    ([4, 1, 0, 2, 3], [1, 2, 0, 11, 5], 3, 3, 128, "f16", True),  # gradients below fp16's normal numbers
     ([1, 1, 4], [4000, 257, 1000], 8, 8, 64, "bf16", True),
     ([16], [6000], 8, 1, 128, "f16", True),                # cut along the keys
     ([700], None, 4, 1, 64, "bf16", True),                 # backward cut along the queries
