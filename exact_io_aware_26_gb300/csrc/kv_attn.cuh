@@ -660,8 +660,10 @@ __global__ void __launch_bounds__(Cfg<Blk, NT, CL>::THREADS, Cfg<Blk, NT, CL>::C
     // 2 t + 1, 2 t + 8 and 2 t + 9 are tokens 4 t to 4 t + 3, a word of values.
     const int kr = wide ? 4 * (g >> 1) + (g & 1) : g ^ ((g >> 1) & 1);
     constexpr int kr_next = wide ? 2 : 8;
-    // 8 bits: O stands for o * vref, the scale of the values of late (a power of two)
-    [[maybe_unused]] float vref = 1.f, inv_vref = 1.f;
+    // 8 bits: O stands for o * vref, the scale of the values of late (a power of two; before the first
+    // block far above any, so that the first one's is taken, while o is 0)
+    constexpr float kNoScale = 0x1p40f;
+    [[maybe_unused]] float vref = kNoScale, inv_vref = 1.f / kNoScale;
     auto product_k = [&](float (&s)[NT][4], int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -938,16 +940,18 @@ __global__ void __launch_bounds__(Cfg<Blk, NT, CL>::THREADS, Cfg<Blk, NT, CL>::C
           // that they stay in fp16's range; where it is not O takes the block's
           ratio = vs[h] * inv_vref;
           if (!(ratio <= 1.f && ratio >= 0x1p-8f) && vs[h] != 0.f) {
-            const float back = vref / vs[h];
+            if (vref != kNoScale) {
+              const float back = vref / vs[h];
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) o[i][j][c] *= back;
+            }
             vref = vs[h];
             inv_vref = 1.f / vref;
             ratio = 1.f;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[i][j][c] *= back;
           }
         }
 #pragma unroll

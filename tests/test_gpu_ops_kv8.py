@@ -306,6 +306,25 @@ def test_a_small_value_with_all_of_the_weight(cuda_lib):
         assert abs(float(lse) - 200.0) < 1e-3 + 200 * 2.0 ** -9
 
 
+@pytest.mark.parametrize("n", [2, 30, 200])
+def test_small_weights_of_small_values(cuda_lib, n):
+    """One token has nearly all of the weight and a value of 0, the others have e^-12 of it each and values
+    below 1/2: they are the result, of which no bits are lost to their block's small scale."""
+    d, pages = 64, -(-n // 16)
+    k, v = np.zeros((n, 1, d), np.float32), np.full((n, 1, d), 0.4375, np.float32)
+    k[0, 0, 0], v[0] = 12.0, 0.0
+    cache = fa.kv8_cache(pages, 1, d, page_size=16)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    fa.kv8_append(dev(k), dev(v), slots, cache)
+    held = [to_np64(x) for x in fa.kv8_gather(cache, slots, d, dtype=torch.float32)]
+    q = torch.zeros(1, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    want = ref.attention(to_np64(q), [held[0]], [held[1]], [n], [0, 1], 1.0, 0)
+    for t in (table, torch.cat([table, torch.full((1, 6250 - pages), -1, dtype=torch.int32, device="cuda")], 1)):
+        check(*fa.kv8_attention(q, cache, t, torch.tensor([n], dtype=torch.int32, device="cuda"), scale=1.0), want, "bf16")
+
+
 def test_queries_outside_fp16s_range(cuda_lib):
     q, cache, table, lens, cu, k, v = build([200], [1], 4, 1, 64, "bf16", 16, 6)
     for size in (2.0 ** 100, 2.0 ** -100):
