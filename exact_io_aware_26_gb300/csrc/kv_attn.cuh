@@ -660,8 +660,8 @@ __global__ void __launch_bounds__(Cfg<Blk, NT, CL>::THREADS, Cfg<Blk, NT, CL>::C
     // 2 t + 1, 2 t + 8 and 2 t + 9 are tokens 4 t to 4 t + 3, a word of values.
     const int kr = wide ? 4 * (g >> 1) + (g & 1) : g ^ ((g >> 1) & 1);
     constexpr int kr_next = wide ? 2 : 8;
-    // 8 bits: O stands for o * vref, the scale of the values of late (a power of two; before the first
-    // block far above any, so that the first one's is taken, while o is 0)
+    // 8 bits: O stands for o * vref, 2^-7 times the scale of the values of late (before the first block far
+    // above any, so that the first one's is taken, while o is 0)
     constexpr float kNoScale = 0x1p40f;
     [[maybe_unused]] float vref = kNoScale, inv_vref = 1.f / kNoScale;
     auto product_k = [&](float (&s)[NT][4], int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -936,12 +936,15 @@ __global__ void __launch_bounds__(Cfg<Blk, NT, CL>::THREADS, Cfg<Blk, NT, CL>::C
         uint32_t p0[NT], p1[NT];
         [[maybe_unused]] float ratio = 1.f;
         if constexpr (wide) {
-          // the weights take the scale of the block's values relative to that of O: in [2^-8, 1], so
-          // that they stay in fp16's range; where it is not O takes the block's
+          // the weights, at most 2^8, take the scale of the block's values relative to vref: in [1, 2^7], so
+          // that they stay below fp16's largest number and none is rounded to less than without it,
+          // whatever the blocks before; where it is not O takes the block's.  (In [2^-8, 1] a weight of e^-12
+          // behind a block of values 2^8 times as large would be 0.)
           ratio = vs[h] * inv_vref;
-          if (!(ratio <= 1.f && ratio >= 0x1p-8f) && vs[h] != 0.f) {
+          if (!(ratio <= 0x1p7f && ratio >= 1.f) && vs[h] != 0.f) {
+            const float to = vs[h] * 0x1p-7f;
             if (vref != kNoScale) {
-              const float back = vref / vs[h];
+              const float back = vref / to;
 #pragma unroll
               for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -949,9 +952,9 @@ __global__ void __launch_bounds__(Cfg<Blk, NT, CL>::THREADS, Cfg<Blk, NT, CL>::C
 #pragma unroll
                   for (int c = 0; c < 4; ++c) o[i][j][c] *= back;
             }
-            vref = vs[h];
-            inv_vref = 1.f / vref;
-            ratio = 1.f;
+            vref = to;
+            inv_vref = 1.f / to;
+            ratio = 0x1p7f;
           }
         }
 #pragma unroll
