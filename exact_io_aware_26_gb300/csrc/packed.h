@@ -14,6 +14,7 @@ struct PackedList {
   PackedItem* cuts;    // the cut units (s0, s1: the whole unit's steps)
   int* left;           // of each cut unit and key head: the parts that are done (forward)
   int* starts;         // scratch: first query, key and unit of each sequence and behind the last; its place in the list
+                       // (backward in fp16: the first two for the other kernels)
 };
 
 struct PackedPlanArgs {
@@ -25,6 +26,7 @@ struct PackedPlanArgs {
   const int* cu_q;
   const int* cu_k;
   PackedList list;
+  float4* most;        // backward in fp16: to be zeroed, else nullptr
   DevStatus* st;
 };
 
@@ -46,6 +48,8 @@ struct PackedArgs {
   float* slots;        // partial results of cut units
   float *stat_lse, *stat_d;  // backward: [Hk][Tq * G] LSE log2 e (+inf: no key seen) and rowsum(dO O)
   float* dq_acc;       // backward: [Hk][Tq * G][d]
+  int* seq_of;         // backward in fp16: [Tq] the sequence of a row, any for one of none
+  float4* most;        // backward in fp16: [R][Hk] largest |dO|^2, |V|^2 and |D| of a sequence and key head
   Report rep;
 };
 

@@ -55,7 +55,7 @@ fa_status check(const fa_packed_params* p, bool bwd) {
 // The sizes of a call's work list and where it lies in the workspace.
 struct Sizes {
   int tpt, target, least, slots, units, items, cuts;
-  size_t items_at, cuts_at, left_at, starts_at, slots_at, stat_at, acc_at, bytes;
+  size_t items_at, cuts_at, left_at, starts_at, slots_at, stat_at, acc_at, most_at, seq_at, bytes;
   Sizes(const fa_packed_params* p, int sms, bool bwd) {
     const int G = p->Hq / p->Hk;
     tpt = 128 / G;
@@ -81,6 +81,9 @@ struct Sizes {
     const size_t rows = (size_t)p->Tq * p->Hq;
     stat_at = bwd ? place(2 * rows * 4) : at;
     acc_at = bwd ? place(rows * p->d * 4) : at;
+    const bool scaled = bwd && p->dtype == FA_F16;
+    most_at = scaled ? place((size_t)p->R * p->Hk * sizeof(float4)) : 0;
+    seq_at = scaled ? place((size_t)p->Tq * 4) : 0;
     bytes = at;
   }
 };
@@ -127,6 +130,8 @@ PackedArgs common_args(const fa_packed_params* p, const Sizes& z, void* workspac
   a.stat_lse = reinterpret_cast<float*>(ws + z.stat_at);
   a.stat_d = a.stat_lse + (size_t)p->Tq * p->Hq;
   a.dq_acc = reinterpret_cast<float*>(ws + z.acc_at);
+  a.seq_of = reinterpret_cast<int*>(ws + z.seq_at);
+  a.most = z.most_at ? reinterpret_cast<float4*>(ws + z.most_at) : nullptr;
   std::memcpy(a.vs, p->v_stride, sizeof(a.vs));
   std::memcpy(a.os, p->o_stride, sizeof(a.os));
   std::memcpy(a.dos, p->do_stride, sizeof(a.dos));
@@ -153,6 +158,7 @@ PackedPlanArgs plan_args(const PackedArgs& a, const Sizes& z, const int* cu_q, c
   q.cu_q = cu_q;
   q.cu_k = cu_k;
   q.list = a.list;
+  q.most = a.most;
   q.st = a.rep.st;
   return q;
 }

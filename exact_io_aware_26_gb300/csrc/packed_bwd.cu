@@ -17,6 +17,13 @@
 // Q, dO and K there are zeroed in shared memory before the products read them, dS of hidden pairs
 // is 0, and rows of dQ there are added as 0.
 //
+// In fp16 P^T and dS^T are kept where the type has all its bits, and below its largest number: P times
+// 2^13, and dS, for a sequence and key head, times the power of two that its largest |dO|, |V| and |D|
+// allow (|dP - D| <= |dO| |V| + |D|).  The gradients take both back, exactly, in fp32.  (Without them a
+// weight over 2^16 keys has eight bits, and dS over 4096 keys of a dO of 2^-13 is 0.)  bf16 needs neither.
+// It costs a pass over V, the maxima and their way to the tiles: 4 sequences up to 2048 tokens, 12 heads,
+// d = 64, 72 us and 64 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.32 ms and 6.23.
+//
 // Bound: the tensor core (five products, 10 d FLOPs a seen pair and query head) beside the
 // exponentials and the elementwise steps; one CTA an SM.  Measured, causal, with the kernels before
 // and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 951 TFLOP/s (6.23 ms).
@@ -32,6 +39,27 @@
 
 namespace fa {
 namespace {
+
+// fp16: log2 of the factor of P^T (P is at most 1, but for roundings of the scores), and its reciprocal.
+constexpr float kPScale = 13.f, kPDown = 0x1p-13f;
+// fp16: the factor of dS of a sequence and key head, from its largest |dO|^2 < 2^(x + 1), |V|^2 < 2^(y + 1)
+// and |D| < 2^(z + 1): |dP - D| < 2^((x + y + 2) / 2) + 2^(z + 1) <= 2^e, and 2^(1 - e) brings that to 2, so
+// that 2^13 P |dP - D| stays below 2^14 and what is 2^-26 of that has all its bits.  (At most 2^60: the bound
+// of numbers that are not 0 is 2^-48 at least, and no dP of fp16 numbers times that is infinite, also not in rows
+// that have no say in it, whose P is 0.)
+__device__ __forceinline__ float dS_up(const float4& most) {
+  auto exponent = [](float f) { return (int)(__float_as_uint(f) >> 23) - 127; };  // -127 of 0
+  const int e = max((exponent(most.x) + exponent(most.y) + 3) >> 1, exponent(most.z) + 1) + 1;
+  return __uint_as_float((uint32_t)min(max(128 - e, 1), 187) << 23);
+}
+// Here and not where it is used, so that it is on its way beside other loads.
+__device__ __forceinline__ float4 ld_early(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+// Of a power of two.
+__device__ __forceinline__ float reciprocal(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 
 // A CTA's item as its warps use it.
 struct alignas(16) Work {
@@ -92,7 +120,8 @@ struct Layout {
   static constexpr uint32_t TSLOT = BAR + NBAR * 8;
   static constexpr uint32_t ABORT = TSLOT + 4;
   static constexpr uint32_t ITEM = (ABORT + 4 + 15) & ~15u;  // two of Work
-  static constexpr uint32_t BYTES = ITEM + 2 * sizeof(Work);
+  static constexpr uint32_t UP = ITEM + 2 * sizeof(Work);  // fp16: their factors of dS, twice, there before the first tile's bar_qf
+  static constexpr uint32_t BYTES = UP + 2 * 8;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
@@ -189,6 +218,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
   // items that have steps (those of kv, done and acc_free); an item without any, whose results
   // are 0, passes no barrier but its own two.
   auto place = [&](int k) { return reinterpret_cast<Work*>(smem + L::ITEM) + (k & 1); };
+  auto place_up = [&](int k) { return reinterpret_cast<float2*>(smem + L::UP) + (k & 1); };
 
   if (warp == kProd) {
     // ------------------------------------------------------------ producer
@@ -223,6 +253,9 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
       const float* lse = a.stat_lse + (long long)hk * a.Tq * G;
       const float* dsum = a.stat_d + (long long)hk * a.Tq * G;
       const uint32_t q_bytes = (uint32_t)full * D * 2u;
+      float up = 1.f;
+      float4 most{};
+      if (F16) most = ld_early(a.most + (long long)x.r * a.Hk + hk);
       // Q and dO of the first query tiles go ahead of K_j and V_j, whose places are free when the last
       // item's products are done; one stage is freed by those products only.  (A CTA's first K_j and V_j at
       // once: at d = 64 4 sequences of up to 2048 tokens 66.8 and 67.7 us; at d = 128 it gains nothing.)
@@ -256,10 +289,18 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * lane + i;
-          l4[i] = r < rows ? -__ldg(lse + row0 + r) : -INFINITY;
+          l4[i] = r < rows ? (F16 ? kPScale - __ldg(lse + row0 + r) : -__ldg(lse + row0 + r)) : -INFINITY;
           d4[i] = r < rows ? -__ldg(dsum + row0 + r) : 0.f;
         }
         if (it >= NS && !(go = warp_wait(w, bar_qe(s), ((it / NS) - 1) & 1))) break;
+        if (F16) {
+          if (qt == x.s0) {
+            up = dS_up(most);
+            if (lane == 0) *place_up(k) = make_float2(up, up);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d4[i] *= up;
+        }
         const bool tail = rows < full;  // the sequence's last query tile
         const uint32_t dst = sb + L::QS + (uint32_t)s * 2u * L::TILE;
         if (lane == 0) {
@@ -546,12 +587,20 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
         return true;
       };
       if (s0 < q_end) ok = p_phase(it, s0);
+      auto item_up = [&] { return *reinterpret_cast<const volatile uint64_t*>(place_up(k)); };
+      uint64_t up2 = 0ull;
+      if (F16 && D == 128 && s0 < q_end) up2 = item_up();
       for (int qt = s0; ok && qt < q_end; ++it, ++qt) {
         // ---- dS_i = P_i (dP_i - D)
         if (!(ok = warp_wait(w, bar_dp_full, it & 1))) break;
         tc_fence_after();
         uint32_t pk[CW / 2];
-        const float4* nd4 = reinterpret_cast<const float4*>(stat(it) + 128 + CW * g);  // -D
+        const float4* nd4 = reinterpret_cast<const float4*>(stat(it) + 128 + CW * g);  // -D, in fp16 times the factor
+        if (F16 && D == 64) up2 = item_up();  // (a register that it would spill: 16 bytes)
+        auto ds = [&](uint32_t a0, uint32_t a1, float n0, float n1) {  // dP - D, the same
+          const uint64_t dp = f2pack(__uint_as_float(a0), __uint_as_float(a1)), nd = f2pack(n0, n1);
+          return F16 ? ffma2(dp, up2, nd) : fadd2(dp, nd);
+        };
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           constexpr int HW = CW / 2;
@@ -567,12 +616,8 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
             const int cc = HW * hf + c;
             const float4 nd = nd4[cc / 4];
             float y0, y1, y2, y3;
-            f2unpack(fmul2(f2pack(p[cc], p[cc + 1]),
-                           fadd2(f2pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), f2pack(nd.x, nd.y))),
-                     y0, y1);
-            f2unpack(fmul2(f2pack(p[cc + 2], p[cc + 3]),
-                           fadd2(f2pack(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), f2pack(nd.z, nd.w))),
-                     y2, y3);
+            f2unpack(fmul2(f2pack(p[cc], p[cc + 1]), ds(u[c], u[c + 1], nd.x, nd.y)), y0, y1);
+            f2unpack(fmul2(f2pack(p[cc + 2], p[cc + 3]), ds(u[c + 2], u[c + 3], nd.z, nd.w)), y2, y3);
             pk[cc / 2] = pack2<F16>(y0, y1);
             pk[cc / 2 + 1] = pack2<F16>(y2, y3);
           }
@@ -646,7 +691,8 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
           const uint32_t col = (which == 0 ? L::T_DV : L::T_DK) + g * L::DQG;
-          const float mul = which == 0 ? 1.f : a.scale;
+          float mul = which == 0 ? 1.f : a.scale;
+          if (F16) mul *= which == 0 ? kPDown : have ? kPDown * reciprocal(place_up(k)->x) : 1.f;
           const long long* st = which == 0 ? a.dvs : a.dks;
           constexpr int N = D == 64 ? 2 : 1;  // lanes that store a key's row
           uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) + (long long)(x->key0 + (r & -N)) * st[0] + hk * st[1] +
@@ -718,7 +764,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
 
 // Before the main kernel: the rows' statistics in the order of the query tiles' rows, and the
 // accumulator of dQ zeroed.  Streams O, dO and the accumulator; runs beside the list's making.
-template <int D, bool F16>
+template <int D>
 __global__ void __launch_bounds__(256) packed_rows_kernel(const PackedArgs a) {
   constexpr int TPR = D / 8;
   const long long total = (long long)a.Tq * a.Hq * TPR, n = (long long)gridDim.x * blockDim.x;
@@ -735,7 +781,7 @@ __global__ void __launch_bounds__(256) packed_rows_kernel(const PackedArgs a) {
       const uint32_t ov[4] = {o.x, o.y, o.z, o.w}, gv[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 u = unpack2<F16>(ov[i]), v = unpack2<F16>(gv[i]);
+        const float2 u = unpack2<false>(ov[i]), v = unpack2<false>(gv[i]);
         acc = fmaf(u.x, v.x, acc);
         acc = fmaf(u.y, v.y, acc);
       }
@@ -753,8 +799,179 @@ __global__ void __launch_bounds__(256) packed_rows_kernel(const PackedArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // so that what waits for this grid finds the list too
 }
 
+// The last sequence that does not begin behind the token: r, and its first and end.  Of fewer than
+// 32, each lane holds a first (`mine`), so that a search is no chain of loads; whole warps call it.
+struct Place {
+  int r = 0, begin = 0, end = 0;
+};
+__device__ __forceinline__ int lane_first(const int* first, int R) { return first[min((int)(threadIdx.x & 31), R)]; }
+__device__ __forceinline__ Place place_of(const int* first, int mine, int R, int token) {
+  Place p;
+  if (R < 32) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const int at = __shfl_sync(0xffffffffu, mine, p.r + off);
+      if (p.r + off < R && at <= token) p.r += off;
+    }
+    p.begin = __shfl_sync(0xffffffffu, mine, p.r);
+    p.end = __shfl_sync(0xffffffffu, mine, p.r + 1);
+    return p;
+  }
+  int hi = R;
+  while (hi - p.r > 1) {
+    const int mid = (p.r + hi) >> 1;
+    if (first[mid] <= token) p.r = mid; else hi = mid;
+  }
+  p.begin = first[p.r];
+  p.end = first[p.r + 1];
+  return p;
+}
+
+// The same in fp16, and what dS's factors are formed from: the largest |dO|^2, |D| and |V|^2 of each
+// sequence and key head.  Rows that have no part in the gradients, or are not finite, have no say in them.
+// A block has a run of rows, and one of V's beside it, and its warps keep their own maxima until they are
+// another sequence's or head's; those of warps that end alike are one atomic (an atomic a warp, all to
+// the same few words, took 5 us of 4 sequences up to 2048 tokens).
+constexpr int kRowsCtas = 5;  // an SM: 48 registers (6 spill: 13 us of 4 sequences up to 2048 tokens, and not 11.4)
+template <int D>
+__global__ void __launch_bounds__(256, kRowsCtas) packed_rows_f16_kernel(const PackedArgs a) {
+  constexpr int TPR = D / 8, PER = 32 / TPR;  // lanes of a row, rows of a warp's turn
+  const int lane = threadIdx.x & 31, c = lane % TPR, sub = lane / TPR;
+  struct Run {  // a block's warps take its rows in turn
+    int at, left, turns;  // the warp's first row, the rows from there on, its turns
+    __device__ __forceinline__ explicit Run(int all) {
+      constexpr int TURN = 8 * PER;  // of a block
+      const int per = (int)(((long long)all + TURN * gridDim.x - 1) / (TURN * gridDim.x));
+      const long long first = (long long)blockIdx.x * per * TURN + (threadIdx.x >> 5) * PER;
+      at = first < all ? (int)first : 0;
+      left = first < all ? all - at : 0;
+      turns = min(per, (int)(((long long)left + TURN - 1) / TURN));
+    }
+  };
+  const Run rows(a.Tq * a.Hq), keys(a.Tk * a.Hk);
+  const int span = a.Tq * a.G;
+  const int *first_q = a.list.starts, *first_k = first_q + a.R + 1;
+  auto add_up = [](float x) {  // over a row's lanes
+#pragma unroll
+    for (int off = TPR / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+  };
+  // Maxima of a sequence and key head; unit: which, -1 at first and of rows that are no sequence's.
+  struct Most {
+    long long unit = -1;
+    float x = 0.f, y = 0.f;
+    Place of;  // the last row's sequence
+  } of_q, of_k;
+  auto warp_most = [](float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); };  // x >= 0
+  auto raise = [&](long long unit, int which, float x) {
+    if (x > 0.f) atomicMax(reinterpret_cast<int*>(a.most + unit) + which, __float_as_int(x));
+  };
+  auto flush = [&](const Most& m, int x_at, int y_at) {
+    const float x = warp_most(m.x), y = warp_most(m.y);
+    if (lane == 0 && m.unit >= 0) {
+      raise(m.unit, x_at, x);
+      if (y_at >= 0) raise(m.unit, y_at, y);
+    }
+  };
+  int mine_q = 0, mine_k = 0;
+  auto take = [&](Most& m, const int* first, int mine, bool in, int token, int hk, float x, float y, int x_at, int y_at) {
+    if (__any_sync(0xffffffffu, in && (token < m.of.begin || token >= m.of.end))) m.of = place_of(first, mine, a.R, token);
+    const long long unit = in && token >= m.of.begin && token < m.of.end ? (long long)m.of.r * a.Hk + hk : -1;
+    if (!__all_sync(0xffffffffu, unit == m.unit)) {
+      flush(m, x_at, y_at);
+      m.x = m.y = 0.f;
+      m.unit = __shfl_sync(0xffffffffu, unit, 31);
+      if (unit != m.unit) {
+        if (unit >= 0 && c == 0) {
+          raise(unit, x_at, x);
+          if (y_at >= 0) raise(unit, y_at, y);
+        }
+        return;
+      }
+    }
+    m.x = fmaxf(m.x, x);
+    m.y = fmaxf(m.y, y);
+  };
+  for (int j = 0; j < max(rows.turns, keys.turns); ++j) {
+    const int ahead = j * 8 * PER + sub, at = rows.at + ahead, key = keys.at + ahead;
+    const bool in = j < rows.turns && ahead < rows.left, key_in = j < keys.turns && ahead < keys.left;
+    uint4 o = make_uint4(0u, 0u, 0u, 0u), g = o, v = o;
+    int token = 0, hk = 0, key_token = 0, key_hk = 0;
+    float lse = 0.f;
+    if (in) {
+      hk = at / span;
+      const int rest = at - hk * span;
+      token = a.divG.div(rest);
+      const int head = hk * a.G + rest - token * a.G;
+      o = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + token * a.os[0] + head * a.os[1] + 8 * c);
+      g = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + token * a.dos[0] + head * a.dos[1] + 8 * c);
+      lse = a.lse[(long long)token * a.Hq + head];
+    }
+    if (key_in) {
+      key_hk = key / a.Tk;
+      key_token = key - key_hk * a.Tk;
+      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + key_token * a.vs[0] + key_hk * a.vs[1] + 8 * c);
+    }
+    float dot = 0.f, square = 0.f, v_square = 0.f;
+    const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<true>(ow[i]), y = unpack2<true>(gw[i]), z = unpack2<true>(vw[i]);
+      dot = fmaf(x.y, y.y, fmaf(x.x, y.x, dot));
+      square = fmaf(y.y, y.y, fmaf(y.x, y.x, square));
+      v_square = fmaf(z.y, z.y, fmaf(z.x, z.x, v_square));
+    }
+    dot = add_up(dot);
+    square = add_up(square);
+    v_square = add_up(v_square);
+    if (in) {
+      float4* z = reinterpret_cast<float4*>(a.dq_acc + (long long)at * D + 8 * c);
+      z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c == 0) {
+        a.stat_d[at] = dot;
+        a.stat_lse[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+      }
+    }
+    if (j == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the sequences, and the maxima zeroed
+      mine_q = lane_first(first_q, a.R);
+      mine_k = lane_first(first_k, a.R);
+    }
+    const bool counts = in && lse != -INFINITY && square < INFINITY;
+    if (j < rows.turns) take(of_q, first_q, mine_q, in, token, hk, counts ? square : 0.f, counts && fabsf(dot) < INFINITY ? fabsf(dot) : 0.f, 0, 2);
+    if (in && c == 0 && at == token * a.G) a.seq_of[token] = of_q.of.r;  // once for each token
+    if (j < keys.turns) take(of_k, first_k, mine_k, key_in, key_token, key_hk, v_square < INFINITY ? v_square : 0.f, 0.f, 1, -1);
+  }
+  // what is left: by the block
+  __shared__ long long unit_s[2][8];
+  __shared__ float most_s[3][8];
+  const float x = warp_most(of_q.x), y = warp_most(of_k.x), z = warp_most(of_q.y);
+  if (lane == 0) {
+    const int i = threadIdx.x >> 5;
+    most_s[0][i] = x;
+    most_s[1][i] = y;
+    most_s[2][i] = z;
+    unit_s[0][i] = of_q.unit;
+    unit_s[1][i] = of_k.unit;
+  }
+  __syncthreads();
+  if (threadIdx.x < 24) {  // warp i's k-th maximum: joined with the others of the same unit by the first of them
+    const int k = threadIdx.x / 8, i = threadIdx.x % 8, of = k & 1;
+    const long long unit = unit_s[of][i];
+    float x = most_s[k][i];
+    bool first = unit >= 0;
+    for (int j = 0; j < 8; ++j)
+      if (unit_s[of][j] == unit) {
+        x = fmaxf(x, most_s[k][j]);
+        first &= j >= i;
+      }
+    if (first) raise(unit, k, x);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // so that what waits for this grid finds the list too
+}
+
 // After it: dQ = scale * accumulator, for rows that are a sequence's; and dK, dV of the cut key
-// tiles from their parts, in order.
+// tiles from their parts, in order.  (fp16: less the factors of P and dS.)
 constexpr int kSumParts = 8;
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, int dq_blocks) {
@@ -770,9 +987,13 @@ __global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, 
       const long long at = ((long long)hk * a.Tq + token) * a.G + (head - hk * a.G);
       const float4* src = reinterpret_cast<const float4*>(a.dq_acc + at * D + 8 * c);
       const float4 x = src[0], y = src[1];
+      float mul = a.scale;
+      if constexpr (F16) {
+        mul *= kPDown * reciprocal(dS_up(a.most[(long long)a.seq_of[token] * a.Hk + hk]));
+      }
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dq) + token * a.dqs[0] + head * a.dqs[1] + 8 * c) =
-          make_uint4(pack2<F16>(x.x * a.scale, x.y * a.scale), pack2<F16>(x.z * a.scale, x.w * a.scale),
-                     pack2<F16>(y.x * a.scale, y.y * a.scale), pack2<F16>(y.z * a.scale, y.w * a.scale));
+          make_uint4(pack2<F16>(x.x * mul, x.y * mul), pack2<F16>(x.z * mul, x.w * mul),
+                     pack2<F16>(y.x * mul, y.y * mul), pack2<F16>(y.z * mul, y.w * mul));
     }
     return;
   }
@@ -785,6 +1006,7 @@ __global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, 
   constexpr size_t words = 2 * kTile * D;
   const float* base = a.slots + ((size_t)x.first * a.Hk + hk) * words;
   const int keys = min(kTile, x.seq.m - x.tile * kTile);
+  const float up = F16 ? dS_up(a.most[(long long)x.r * a.Hk + hk]) : 1.f;
   for (int e = part * PART + (int)threadIdx.x; e < (part + 1) * PART; e += blockDim.x) {
     const int row = e % kTile, pair = e / kTile, which = pair / (D / 8), col = pair % (D / 8) * 8;
     if (row >= keys) continue;
@@ -796,7 +1018,8 @@ __global__ void __launch_bounds__(256) packed_finish_kernel(const PackedArgs a, 
       acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;
       acc[4] += v.x; acc[5] += v.y; acc[6] += v.z; acc[7] += v.w;
     }
-    const float mul = which == 0 ? 1.f : a.scale;
+    float mul = which == 0 ? 1.f : a.scale;
+    if (F16) mul *= which == 0 ? kPDown : kPDown * reciprocal(up);
     const long long* st = which == 0 ? a.dvs : a.dks;
     uint16_t* dst = static_cast<uint16_t*>(which == 0 ? a.dv : a.dk) +
                     (long long)(x.seq.k0 + x.tile * kTile + row) * st[0] + hk * st[1] + col;
@@ -841,8 +1064,10 @@ cudaError_t main_t(const PackedArgs& a, const CUtensorMap* tm, int items, cudaSt
 }
 template <int D, bool F16>
 cudaError_t rows_t(const PackedArgs& a, cudaStream_t s) {
-  Launch l(stream_blocks((long long)a.Tq * a.Hq * (D / 8)), 256, 0, s);
-  return cudaLaunchKernelEx(&l.cfg, packed_rows_kernel<D, F16>, a);
+  const long long rows = std::max((long long)a.Tq * a.Hq, F16 ? (long long)a.Tk * a.Hk : 0ll);
+  const int blocks = stream_blocks(rows * (D / 8));
+  Launch l(F16 ? std::min(blocks, kRowsCtas * sms()) : blocks, 256, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, F16 ? packed_rows_f16_kernel<D> : packed_rows_kernel<D>, a);
 }
 template <int D, bool F16>
 cudaError_t finish_t(const PackedArgs& a, int cuts, cudaStream_t s) {

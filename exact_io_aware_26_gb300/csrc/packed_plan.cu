@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
   }
   class_s[tid] = 0;
   if (tid == 0) slot_s = cut_s = 0;
+  if (a.most)
+    for (long long i = tid; i < (long long)R * a.Hk; i += kThreads) a.most[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 
   // ---- the sequences: each begins where the furthest offset up to its own lies
   const int per = (R + kThreads) / kThreads, my0 = min(R + 1, tid * per), my1 = min(R + 1, my0 + per);
@@ -91,6 +93,15 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     bool wrong;
     const PackedSeq s = packed_lane_sequence(a, packed_lane_offsets(a), wrong);
     if (warp == 0 && wrong) atomicCAS(&a.st->code, 0, (int)FA_ERR_INDEX);
+    if (a.most && warp == 0 && lane < R) {
+      int *const q = a.list.starts + lane, *const k = q + R + 1;
+      *q = s.q0;
+      *k = s.k0;
+      if (lane == R - 1) {
+        q[1] = s.q0 + s.n;
+        k[1] = s.k0 + s.m;
+      }
+    }
     const int mine = lane < R ? packed_units(s, a.tpt, a.bwd) : 0, end = packed_lane_end(mine);
     units = __shfl_sync(0xffffffffu, end, 31);
     rows0 = __shfl_sync(0xffffffffu, s.q0, 0);
@@ -104,6 +115,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     own.seq.k0 = __shfl_sync(0xffffffffu, s.k0, of);
     own.seq.m = __shfl_sync(0xffffffffu, s.m, of);
     own.tile = tid - __shfl_sync(0xffffffffu, end - mine, of);
+    own.r = of;
     if (tid < units) packed_steps(own.seq, own.tile, a.tpt, a.causal, a.bwd, own.s0, own.s1);
   } else {
     auto offset = [&](const int* cu, int T, int r) { return min(max(__ldg(cu + r), 0), T); };
@@ -127,6 +139,10 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
       bad |= run_q != __ldg(a.cu_q + r) || run_k != __ldg(a.cu_k + r);
       first_q[r] = run_q;
       first_k[r] = run_k;
+      if (a.most) {
+        a.list.starts[r] = run_q;
+        a.list.starts[R + 1 + r] = run_k;
+      }
     }
     if (bad) atomicCAS(&a.st->code, 0, (int)FA_ERR_INDEX);
     __syncthreads();
@@ -156,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     }
     x.seq = sequence(lo);
     x.tile = u - first_u[lo];
-    x.slot = lo;  // until it is placed
+    x.r = lo;
     packed_steps(x.seq, x.tile, a.tpt, a.causal, a.bwd, x.s0, x.s1);
   };
   if (!FEW && tid < units) unit(tid, own);
@@ -258,10 +274,10 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     __syncthreads();
     with_units([&](int u, const PackedItem& unit_x) {
       PackedItem x = unit_x;
-      const int r = x.slot, n = packed_units(x.seq, a.tpt, a.bwd);
+      const int n = packed_units(x.seq, a.tpt, a.bwd);
       x.slot = -1;
-      x.first = x.parts = x.cut = x.unused = 0;
-      a.list.items[place_u[r] + (a.bwd ? x.tile : n - 1 - x.tile)] = x;
+      x.first = x.parts = x.cut = 0;
+      a.list.items[place_u[x.r] + (a.bwd ? x.tile : n - 1 - x.tile)] = x;
     });
     if (tid == 0) {
       a.list.head[0] = units;
@@ -306,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) packed_plan_kernel(const PackedPlanA
     PackedItem x = unit_x;
     const int s0 = x.s0, w = x.s1 - x.s0, c = packed_cuts(w, slice);
     x.slot = -1;
-    x.first = x.parts = x.cut = x.unused = 0;
+    x.first = x.parts = x.cut = 0;
     if (c > 1) {
       x.first = atomicAdd(&slot_s, c);
       x.parts = c;

@@ -25,11 +25,11 @@ struct PackedSeq {
 
 // A CTA's work, for each key head: steps [s0, s1) of a unit; slot < 0 where these are all of the
 // unit's, else the place of its partial result, one of `parts` from slot `first` on of the unit that was
-// cut as the `cut`-th.
+// cut as the `cut`-th.  r: which sequence.
 struct alignas(16) PackedItem {
   PackedSeq seq;
   int tile, s0, s1, slot;
-  int first, parts, cut, unused;
+  int first, parts, cut, r;
 };
 
 // n, m and tile * tpt are at most 2^30, so that all of this fits an int.

@@ -575,6 +575,10 @@ fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int*
  * backward pass it may reach every gradient of its own sequence, and none of another.
  * The workspace is 256-byte aligned and owned by the caller; its contents do not matter;
  * calls that may run at the same time need workspaces of their own.
+ * In fp16 the backward pass holds the weights and dS times powers of two (of dS one for each
+ * sequence and key head, from its largest |dO|, |V| and |D|), so that small and large incoming
+ * gradients, and weights over many keys, keep the type's bits.  lse has to be the forward's: a
+ * weight that it makes larger than 4 may be infinite there.
  * The forward pass and dK, dV add in a fixed order; dQ is a sum of parts that arrive in
  * any order (fp32), so that its last bits may differ from call to call, as fa_bwd's.
  * ------------------------------------------------------------------------ */
