@@ -46,7 +46,7 @@ struct PackedArgs {
   void *dq, *dk, *dv;
   long long os[2], dos[2], dqs[2], dks[2], dvs[2];
   float* slots;        // partial results of cut units
-  float *stat_lse, *stat_d;  // backward: [Hk][Tq * G] LSE log2 e (+inf: no key seen) and rowsum(dO O)
+  float *stat_lse, *stat_d;  // backward: [Hk][Tq * G] LSE (+inf: no key seen) and rowsum(dO O)
   float* dq_acc;       // backward: [Hk][Tq * G][d]
   int* seq_of;         // backward in fp16: [Tq] the sequence of a row, any for one of none
   float4* most;        // backward in fp16: [R][Hk] largest |dO|^2, |V|^2 and |D| of a sequence and key head

@@ -22,11 +22,16 @@
 // allow (|dP - D| <= |dO| |V| + |D|).  The gradients take both back, exactly, in fp32.  (Without them a
 // weight over 2^16 keys has eight bits, and dS over 4096 keys of a dO of 2^-13 is 0.)  bf16 needs neither.
 // It costs a pass over V, the maxima and their way to the tiles: 4 sequences up to 2048 tokens, 12 heads,
-// d = 64, 72 us and 64 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.32 ms and 6.23.
+// d = 64, 74 us and 65.4 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.28 ms and 6.24.
+//
+// P is exp((scale S) - LSE), the product rounded as the forward rounds it into LSE, so that a key with all
+// of the weight has exactly 1 however large the scores are (as 2^(scale log2 e S - log2 e LSE), one fma,
+// 0.98 at a score of 10^6 and 0.80 at 2^24).  The three instructions cost 4 sequences up to 2048 tokens
+// 1.7 us of 64, 12 up to 8192 23 of 6218; looking for large scores and a way of their own cost 2.5 to 4.
 //
 // Bound: the tensor core (five products, 10 d FLOPs a seen pair and query head) beside the
 // exponentials and the elementwise steps; one CTA an SM.  Measured, causal, with the kernels before
-// and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 951 TFLOP/s (6.23 ms).
+// and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 950 TFLOP/s (6.24 ms).
 //
 // Warp roles as in bwd_tc.cu: 4 NG compute warps in NG groups that split the 128 query
 // columns of a tile (TMEM lane = key row); a producer warp; a warp that owns TMEM and issues the
@@ -42,6 +47,7 @@ namespace {
 
 // fp16: log2 of the factor of P^T (P is at most 1, but for roundings of the scores), and its reciprocal.
 constexpr float kPScale = 13.f, kPDown = 0x1p-13f;
+constexpr float kLog2e = 1.4426950408889634f;
 // fp16: the factor of dS of a sequence and key head, from its largest |dO|^2 < 2^(x + 1), |V|^2 < 2^(y + 1)
 // and |D| < 2^(z + 1): |dP - D| < 2^((x + y + 2) / 2) + 2^(z + 1) <= 2^e, and 2^(1 - e) brings that to 2, so
 // that 2^13 P |dP - D| stays below 2^14 and what is 2^-26 of that has all its bits.  (At most 2^60: the bound
@@ -107,7 +113,7 @@ struct Layout {
   static constexpr int NDS = D == 64 ? 2 : 1;
   static constexpr uint32_t DSB = kTile * kTile * 2;
   static constexpr uint32_t DST = QS + NS * 2 * TILE;
-  static constexpr uint32_t STAT = DST + NDS * DSB;  // per stage -LSE log2 e [128], -D [128]
+  static constexpr uint32_t STAT = DST + NDS * DSB;  // per stage -LSE [128], -D [128]
   static constexpr bool STG_SEP = D == 64;           // dQ boxes: of their own, or over dS^T
   static constexpr uint32_t STG_BYTES = (QW ? NQW : NCW) * BOXB;
   static constexpr uint32_t STG = STG_SEP ? STAT + NS * 256 * 4 : DST;
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * lane + i;
-          l4[i] = r < rows ? (F16 ? kPScale - __ldg(lse + row0 + r) : -__ldg(lse + row0 + r)) : -INFINITY;
+          l4[i] = r < rows ? -__ldg(lse + row0 + r) : -INFINITY;
           d4[i] = r < rows ? -__ldg(dsum + row0 + r) : 0.f;
         }
         if (it >= NS && !(go = warp_wait(w, bar_qe(s), ((it / NS) - 1) & 1))) break;
@@ -515,7 +521,10 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     const int g = warp >> 2;               // query columns [CW g, CW g + CW)
     const int r = (warp & 3) * 32 + lane;  // key row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint64_t c2p = f2pack(a.scale_log2, a.scale_log2);
+    const uint64_t scale2 = f2pack(a.scale, a.scale);
+    // as an fma with 0, because a product and a sum of pairs become one instruction, whatever their rounding says
+    auto scaled = [&](float x, float y) { return ffma2(f2pack(x, y), scale2, 0ull); };
+    auto weight = [](float x) { return ex2(F16 ? fmaf(x, kLog2e, kPScale) : x * kLog2e); };
     const uint32_t stg = sb + L::STG + (uint32_t)warp * L::BOXB;
     bool pend = false;
     auto stg_acquire = [&]() {
@@ -552,18 +561,18 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
 #pragma unroll
           for (int c = 0; c < CW; ++c) p[c] = __uint_as_float(u[c]);
         }
-        const float4* nl4 = reinterpret_cast<const float4*>(stat(it) + CW * g);  // -LSE log2 e
+        const float4* nl4 = reinterpret_cast<const float4*>(stat(it) + CW * g);  // -LSE
         uint32_t pk[CW / 2];
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
           const float4 nl = nl4[c / 4];
           float x0, x1, x2, x3;
-          f2unpack(ffma2(f2pack(p[c], p[c + 1]), c2p, f2pack(nl.x, nl.y)), x0, x1);
-          f2unpack(ffma2(f2pack(p[c + 2], p[c + 3]), c2p, f2pack(nl.z, nl.w)), x2, x3);
-          p[c] = ex2(x0);
-          p[c + 1] = ex2(x1);
-          p[c + 2] = ex2(x2);
-          p[c + 3] = ex2(x3);
+          f2unpack(fadd2(scaled(p[c], p[c + 1]), f2pack(nl.x, nl.y)), x0, x1);
+          f2unpack(fadd2(scaled(p[c + 2], p[c + 3]), f2pack(nl.z, nl.w)), x2, x3);
+          p[c] = weight(x0);
+          p[c + 1] = weight(x1);
+          p[c + 2] = weight(x2);
+          p[c + 3] = weight(x3);
         }
         if (qt < whole_from) {
           const int first = first_col(qt);
@@ -793,7 +802,7 @@ __global__ void __launch_bounds__(256) packed_rows_kernel(const PackedArgs a) {
     if (in && c == 0) {
       const float lse = a.lse[row];
       a.stat_d[at] = acc;
-      a.stat_lse[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+      a.stat_lse[at] = lse == -INFINITY ? INFINITY : lse;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // so that what waits for this grid finds the list too
@@ -929,7 +938,7 @@ __global__ void __launch_bounds__(256, kRowsCtas) packed_rows_f16_kernel(const P
       z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c == 0) {
         a.stat_d[at] = dot;
-        a.stat_lse[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+        a.stat_lse[at] = lse == -INFINITY ? INFINITY : lse;
       }
     }
     if (j == 0) {

@@ -1,4 +1,4 @@
-"""The range of packed attention's gradient: incoming gradients and weights of any size.
+"""The range of packed attention's gradient: incoming gradients, weights and scores of any size.
 
 Inputs are chosen so that the gradients have a closed form and every term of a sum has the same sign:
 what one of them loses the sum loses too.  q and k are orthogonal, so that all m keys of a row weigh
@@ -13,6 +13,7 @@ import math
 import pytest
 import torch
 
+import _packed_ref as ref
 import exact_io_aware_26_gb300 as fa
 from _parity import DTYPES
 
@@ -135,3 +136,38 @@ def test_rows_that_see_no_key_have_no_say(cuda_lib):
     for g in grads[1:]:
         assert bool((g[0][:30] == 0).all()) and all(torch.equal(a[30:] if i == 0 else a, b[30:] if i == 0 else b)
                                                     for i, (a, b) in enumerate(zip(g, grads[0])))
+
+
+@pytest.mark.parametrize("dtype,a,b,scale", [("bf16", 160.0, 640.0, 1.0), ("f16", 1001.0, 999.0, 1.0), ("f16", 1001.0, 999.0, 0.3337),
+                                             ("bf16", 2.0 ** 12, 2.0 ** 12 * 1.25, 0.7), ("bf16", 2.0 ** 20, 2.0 ** 20, 1.1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_any_size(cuda_lib, d, dtype, a, b, scale):
+    """One key far above the others has all of a head's weight, however large the scores: its dV is the
+    sum of the rows' do.  The other head of the key head has ordinary scores in the same tiles."""
+    T, at = 300, 50
+    g = torch.Generator().manual_seed(3)
+    q, do = (torch.randn(T, 2, d, generator=g) for _ in (0, 1))
+    k, v = (torch.randn(T, 1, d, generator=g) for _ in (0, 1))
+    q[:, 0], q[:, 1, 0] = 0.0, 0.0
+    q[:, 0, 0], k[:, 0, 0], k[at, 0, 0] = a, 0.0, b
+    q[:, 1] *= (d ** -0.5 / scale)
+    do[:at, 0] = 0.0
+    q, k, v, do = (x.to(DTYPES[dtype]) for x in (q, k, v, do))
+    o, lse = fa.attention_fwd_packed(q.cuda(), k.cuda(), v.cuda(), offsets([T]), scale=scale)
+    dq, dk, dv = (x.double().cpu() for x in fa.attention_bwd_packed(q.cuda(), k.cuda(), v.cuda(), o, do.cuda(), lse, offsets([T]), scale=scale))
+    assert fa.get_status() == fa.FA_OK
+    o, lse = o.cpu(), lse.cpu()
+    e, tiny = torch.finfo(DTYPES[dtype]).eps / 2, 2.0 ** -24 if dtype == "f16" else 0.0
+    want, bounds = ref.backward(q[:, 1:], k, v, o[:, 1:], do[:, 1:], lse[:, 1:], [T], [T], True, scale, e, tiny)
+    # the first head's part: P = 1 at one key, in fp32 sums of T terms
+    more = do[at:, 0].double().sum(0)
+    slack = do[at:, 0].double().abs().sum(0) * (T * 2.0 ** -23 + 2.0 ** -20)
+    got, total = dv[at, 0], want[2][at, 0] + more
+    bound = bounds[2][at, 0] + slack + e * more.abs()
+    assert bool(((got - total).abs() <= bound).all()), f"dv: {((got - total).abs() / bound).max():.1f} of the bound"
+    rest = [j for j in range(T) if j != at]
+    assert bool(((dv[rest] - want[2][rest]).abs() <= bounds[2][rest]).all())
+    assert bool(((dq[:, 1:] - want[0]).abs() <= bounds[0]).all())
+    # the first head's dS is 0 but for fp32 roundings, and its queries are 0 in these channels
+    assert bool(((dk[:, :, 1:] - want[1][:, :, 1:]).abs() <= bounds[1][:, :, 1:]).all())
+    assert bool(dq.isfinite().all()) and bool(dk.isfinite().all())
