@@ -62,5 +62,47 @@ inline fa_status check_strides(const long long* stride, const long long* size, i
   return FA_OK;
 }
 
+// The memory of a tensor [size[0]][size[1]][inner], in bytes.
+struct Extent {
+  uintptr_t base;
+  long long stride[2], size[2], inner;
+  Extent(const void* p, const long long* element_stride, const long long* n, long long channels, long long e)
+      : base(reinterpret_cast<uintptr_t>(p)), stride{element_stride[0] * e, element_stride[1] * e}, size{n[0], n[1]},
+        inner(channels * e) {}
+  // Bytes from the base on, of the dimensions whose stride is below `period`; negative where another one's is
+  // no multiple of it, or they do not fit into it.
+  long long within(long long period) const {
+    long long n = inner;
+    for (int i = 0; i < 2; ++i) {
+      if (size[i] <= 1) continue;
+      if (stride[i] < period)
+        n += stride[i] * (size[i] - 1);
+      else if (stride[i] % period != 0)
+        return -1;
+    }
+    return n <= period ? n : -1;
+  }
+};
+// Whether two tensors share no byte: one ends before the other begins, or they are rows (or heads) that take
+// turns at the distance of a stride of either, such as the views of one packed projection.  Other
+// layouts that take turns count as one over the other.
+inline bool apart(const Extent& a, const Extent& b) {
+  for (const Extent* x : {&a, &b})
+    if (!x->base || x->size[0] == 0 || x->size[1] == 0) return true;
+  constexpr long long kAll = 0x7FFFFFFFFFFFFFFFll;
+  if (b.base >= a.base ? b.base - a.base >= (uintptr_t)a.within(kAll) : a.base - b.base >= (uintptr_t)b.within(kAll)) return true;
+  for (const Extent* x : {&a, &b})
+    for (int i = 0; i < 2; ++i) {
+      const long long period = x->stride[i];
+      if (x->size[i] <= 1 || period <= 0) continue;
+      const long long na = a.within(period), nb = b.within(period);
+      if (na < 0 || nb < 0) continue;
+      const long long at = b.base >= a.base ? (long long)((b.base - a.base) % (uintptr_t)period)
+                                            : (period - (long long)((a.base - b.base) % (uintptr_t)period)) % period;
+      if (at >= na && at + nb <= period) return true;
+    }
+  return false;
+}
+
 }  // namespace
 }  // namespace fa

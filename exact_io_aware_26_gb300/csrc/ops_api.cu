@@ -298,7 +298,10 @@ fa_status attn_call(int bits, const fa_kv4_cache* c, const fa_kv4_attn_params* p
     return fail(FA_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", workspace,
                 workspace_bytes, want);
   // shares read a request's queries when another has already written its rows
-  if (p->T > 0 && o == q) return fail(FA_ERR_INVALID, "o lies over q");
+  const long long size[2] = {p->T, p->Hq}, dense[2] = {p->Hq, 1};
+  const Extent eq(q, p->q_stride, size, c->d, 2), eo(o, p->o_stride, size, c->d, 2), el(lse, dense, size, 1, 4);
+  if (!apart(eo, eq)) return fail(FA_ERR_INVALID, "o lies over q");
+  if (!apart(el, eq) || !apart(el, eo)) return fail(FA_ERR_INVALID, "lse lies over q or o");
   Report rep;
   int sms = 0;
   FA_TRY(api_device(&rep, &sms));

@@ -163,6 +163,31 @@ PackedPlanArgs plan_args(const PackedArgs& a, const Sizes& z, const int* cu_q, c
   return q;
 }
 
+// Results are written while other CTAs still read the inputs (dq when all have been read).
+fa_status forward_overlaps(const fa_packed_params* p, const void* q, const void* k, const void* v, const void* o,
+                           const void* lse) {
+  const long long sq[2] = {p->Tq, p->Hq}, sk[2] = {p->Tk, p->Hk}, dense[2] = {p->Hq, 1};
+  const Extent in[3] = {{q, p->q_stride, sq, p->d, 2}, {k, p->k_stride, sk, p->d, 2}, {v, p->v_stride, sk, p->d, 2}};
+  const Extent eo(o, p->o_stride, sq, p->d, 2), el(lse, dense, sq, 1, 4);
+  for (const Extent& x : in) {
+    if (!apart(eo, x)) return fail(FA_ERR_INVALID, "o lies over an input");
+    if (!apart(el, x)) return fail(FA_ERR_INVALID, "lse lies over an input");
+  }
+  return apart(el, eo) ? FA_OK : fail(FA_ERR_INVALID, "o and lse lie over each other");
+}
+
+fa_status backward_overlaps(const fa_packed_params* p, const void* q, const void* k, const void* v, const void* dout,
+                            const void* dq, const void* dk, const void* dv) {
+  const long long sq[2] = {p->Tq, p->Hq}, sk[2] = {p->Tk, p->Hk};
+  const Extent in[4] = {{q, p->q_stride, sq, p->d, 2}, {k, p->k_stride, sk, p->d, 2}, {v, p->v_stride, sk, p->d, 2},
+                        {dout, p->do_stride, sq, p->d, 2}};
+  const Extent eq(dq, p->dq_stride, sq, p->d, 2), ek(dk, p->dk_stride, sk, p->d, 2), ev(dv, p->dv_stride, sk, p->d, 2);
+  for (const Extent& x : in)
+    if (!apart(ek, x) || !apart(ev, x)) return fail(FA_ERR_INVALID, "dk or dv lies over an input");
+  if (!apart(ek, ev) || !apart(eq, ek) || !apart(eq, ev)) return fail(FA_ERR_INVALID, "two gradients lie over each other");
+  return FA_OK;
+}
+
 fa_status offsets_check(const fa_packed_params* p, const int* cu_q, const int*& cu_k) {
   FA_TRY(need(cu_q, 4, "cu_q"));
   if (!cu_k) {
@@ -189,12 +214,12 @@ fa_status fa_fwd_packed(const fa_packed_params* p, const void* q, const void* k,
     FA_TRY(need(q, 16, "q"));
     FA_TRY(need(o, 16, "o"));
     FA_TRY(need(lse, 4, "lse"));
-    if (o == q || o == k || o == v) return fail(FA_ERR_INVALID, "o lies over an input");
   }
   if (p->Tk > 0) {
     FA_TRY(need(k, 16, "k"));
     FA_TRY(need(v, 16, "v"));
   }
+  FA_TRY(forward_overlaps(p, q, k, v, o, lse));
   FA_TRY(workspace_check(workspace, workspace_bytes, fa_fwd_packed_workspace_size(p)));
   Report rep;
   int sms = 0;
@@ -247,11 +272,7 @@ fa_status fa_bwd_packed(const fa_packed_params* p, const void* q, const void* k,
     FA_TRY(need(dk, 16, "dk"));
     FA_TRY(need(dv, 16, "dv"));
   }
-  // key tiles' results are written while others still read q, k, v and do
-  for (const void* result : {(const void*)dk, (const void*)dv})
-    for (const void* input : {q, k, v, dout})
-      if (result && result == input) return fail(FA_ERR_INVALID, "dk or dv lies over an input");
-  if ((dk && dk == dv) || (dq && (dq == dk || dq == dv))) return fail(FA_ERR_INVALID, "two gradients lie over each other");
+  FA_TRY(backward_overlaps(p, q, k, v, dout, dq, dk, dv));
   FA_TRY(workspace_check(workspace, workspace_bytes, fa_bwd_packed_workspace_size(p)));
   Report rep;
   int sms = 0;

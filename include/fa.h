@@ -458,8 +458,8 @@ fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
  * Lengths are device memory: the tokens of all requests are cut into equal shares
  * on the GPU.  A page outside the cache contributes nothing and is recorded as
  * FA_ERR_INDEX, as is a length beyond table_width * page_size, which is cut to that.
- * o must not lie over q.  Calls that may run at the same time need workspaces of their
- * own.  Limits: T*Hq < 2^31, table_width * page_size <= 2^30, num_pages * page_size < 2^31,
+ * o and lse must not lie over q or each other, in part neither.  Calls that may run at
+ * the same time need workspaces of their own.  Limits: T*Hq < 2^31, table_width * page_size <= 2^30, num_pages * page_size < 2^31,
  * a page below 2^31 bytes.
  */
 typedef struct {
@@ -569,8 +569,10 @@ fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int*
  *               Bases 16-byte aligned, strides multiples of 16 bytes, below 2^38, and not
  *               0; written tensors must not overlap themselves.  q, k and v may be
  *               views of one packed projection, in either order of tokens and heads.
- * Results must not lie over inputs (dq may be q, o or do with the same strides).  Rows
- * that are in no sequence are neither read into a result nor written.  What is not
+ * Results must not lie over inputs or each other, not in part either, and are refused then
+ * (dq may be q, o or do with the same strides).  Views of one buffer whose rows or heads
+ * take turns, at the distance of a stride of one of them, lie beside each other.
+ * Rows that are in no sequence are neither read into a result nor written.  What is not
  * finite in k, v or q reaches, in the forward pass, the rows that see it; in the
  * backward pass it may reach every gradient of its own sequence, and none of another.
  * The workspace is 256-byte aligned and owned by the caller; its contents do not matter;
