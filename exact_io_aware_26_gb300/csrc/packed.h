@@ -33,6 +33,7 @@ struct PackedPlanArgs {
 struct PackedArgs {
   int R, Tq, Tk, Hq, Hk, G;
   FastDiv divG, divHk;
+  FastDiv divRows, divTk;  // backward: by Tq * G and Tk
   int tpt, causal;
   float scale, scale_log2;
   PackedList list;

@@ -116,6 +116,8 @@ PackedArgs common_args(const fa_packed_params* p, const Sizes& z, void* workspac
   a.G = p->Hq / p->Hk;
   a.divG = FastDiv::of((uint32_t)a.G);
   a.divHk = FastDiv::of((uint32_t)a.Hk);
+  a.divRows = FastDiv::of((uint32_t)std::max(p->Tq * a.G, 1));
+  a.divTk = FastDiv::of((uint32_t)std::max(p->Tk, 1));
   a.tpt = z.tpt;
   a.causal = p->causal != 0;
   a.scale = p->scale;

@@ -22,16 +22,16 @@
 // allow (|dP - D| <= |dO| |V| + |D|).  The gradients take both back, exactly, in fp32.  (Without them a
 // weight over 2^16 keys has eight bits, and dS over 4096 keys of a dO of 2^-13 is 0.)  bf16 needs neither.
 // It costs a pass over V, the maxima and their way to the tiles: 4 sequences up to 2048 tokens, 12 heads,
-// d = 64, 74 us and 65.4 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.28 ms and 6.24.
+// d = 64, 72.5 us and 65.4 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.26 ms and 6.23.
 //
 // P is exp((scale S) - LSE), the product rounded as the forward rounds it into LSE, so that a key with all
 // of the weight has exactly 1 however large the scores are (as 2^(scale log2 e S - log2 e LSE), one fma,
 // 0.98 at a score of 10^6 and 0.80 at 2^24).  The three instructions cost 4 sequences up to 2048 tokens
-// 1.7 us of 64, 12 up to 8192 23 of 6218; looking for large scores and a way of their own cost 2.5 to 4.
+// 1.7 us of 64, 12 up to 8192 5 to 20 of 6220; looking for large scores and a way of their own cost 2.5 to 4.
 //
 // Bound: the tensor core (five products, 10 d FLOPs a seen pair and query head) beside the
 // exponentials and the elementwise steps; one CTA an SM.  Measured, causal, with the kernels before
-// and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 950 TFLOP/s (6.24 ms).
+// and behind it: 12 sequences of up to 8192 tokens, 32 and 8 heads, d = 128, 951 TFLOP/s (6.23 ms).
 //
 // Warp roles as in bwd_tc.cu: 4 NG compute warps in NG groups that split the 128 query
 // columns of a tile (TMEM lane = key row); a producer warp; a warp that owns TMEM and issues the
@@ -299,14 +299,6 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
           d4[i] = r < rows ? -__ldg(dsum + row0 + r) : 0.f;
         }
         if (it >= NS && !(go = warp_wait(w, bar_qe(s), ((it / NS) - 1) & 1))) break;
-        if (F16) {
-          if (qt == x.s0) {
-            up = dS_up(most);
-            if (lane == 0) *place_up(k) = make_float2(up, up);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d4[i] *= up;
-        }
         const bool tail = rows < full;  // the sequence's last query tile
         const uint32_t dst = sb + L::QS + (uint32_t)s * 2u * L::TILE;
         if (lane == 0) {
@@ -316,6 +308,14 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
             tma_load_3d(dst + c * (kTile * 128), &tmQ, on, c * 64, hk * G, token);
             tma_load_3d(dst + L::TILE + c * (kTile * 128), &tmdO, on, c * 64, hk * G, token);
           }
+        }
+        if (F16) {  // behind the copies, which need not wait for it
+          if (qt == x.s0) {
+            up = dS_up(most);
+            if (lane == 0) *place_up(k) = make_float2(up, up);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d4[i] *= up;
         }
         float* st = reinterpret_cast<float*>(smem + L::STAT) + s * 256;
         reinterpret_cast<float4*>(st)[lane] = make_float4(l4[0], l4[1], l4[2], l4[3]);
@@ -841,7 +841,7 @@ __device__ __forceinline__ Place place_of(const int* first, int mine, int R, int
 // A block has a run of rows, and one of V's beside it, and its warps keep their own maxima until they are
 // another sequence's or head's; those of warps that end alike are one atomic (an atomic a warp, all to
 // the same few words, took 5 us of 4 sequences up to 2048 tokens).
-constexpr int kRowsCtas = 5;  // an SM: 48 registers (6 spill: 13 us of 4 sequences up to 2048 tokens, and not 11.4)
+constexpr int kRowsCtas = 5;  // an SM: 48 registers (6 spill: 13 us of 4 sequences up to 2048 tokens, and not 11.4; by now 10.4)
 template <int D>
 __global__ void __launch_bounds__(256, kRowsCtas) packed_rows_f16_kernel(const PackedArgs a) {
   constexpr int TPR = D / 8, PER = 32 / TPR;  // lanes of a row, rows of a warp's turn
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(256, kRowsCtas) packed_rows_f16_kernel(const P
     int token = 0, hk = 0, key_token = 0, key_hk = 0;
     float lse = 0.f;
     if (in) {
-      hk = at / span;
+      hk = a.divRows.div(at);
       const int rest = at - hk * span;
       token = a.divG.div(rest);
       const int head = hk * a.G + rest - token * a.G;
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(256, kRowsCtas) packed_rows_f16_kernel(const P
       lse = a.lse[(long long)token * a.Hq + head];
     }
     if (key_in) {
-      key_hk = key / a.Tk;
+      key_hk = a.divTk.div(key);
       key_token = key - key_hk * a.Tk;
       v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + key_token * a.vs[0] + key_hk * a.vs[1] + 8 * c);
     }
