@@ -393,5 +393,7 @@ def __getattr__(name):
 
 
 _OPS = ("rope_freqs", "qk_norm_rope", "qk_norm_rope_bwd", "kv4_block_bytes", "kv4_cache", "kv4_append", "kv4_gather",
-        "kv4_attention", "paged_plan", "attention_fwd_packed", "attention_bwd_packed", "kv8_block_bytes", "kv8_cache", "kv8_append", "kv8_gather", "kv8_attention", "FaPackedParams", "FaQkParams", "FaKv4Cache", "FaKv4Rows", "FaKv4AttnParams", "FaPlanParams",
+        "kv4_attention", "paged_plan", "attention_fwd_packed", "attention_bwd_packed", "kv8_block_bytes", "kv8_cache",
+        "kv8_append", "kv8_gather", "kv8_attention", "FaPackedParams", "FaQkParams", "FaKv4Cache", "FaKv4Rows",
+        "FaKv4AttnParams", "FaPlanParams",
         "KV4_GROUP", "KV4_BLOCK", "KV4_SATURATE", "PLAN_MAX_REQUESTS")

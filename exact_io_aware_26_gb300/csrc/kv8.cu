@@ -290,7 +290,8 @@ __device__ __forceinline__ void append_some(const char* x0, long long row_bytes,
 template <int D, int DT>
 constexpr bool kBoth = D == 64 && DT != FA_F32;
 template <int D, int DT>
-__global__ void __launch_bounds__(kAppend, D == 128 && DT == FA_F32 ? 4 : 8) kv8_append_kernel(const Kv4RowArgs a, int tokens, int span, int sides) {
+__global__ void __launch_bounds__(kAppend, D == 128 && DT == FA_F32 ? 4 : 8)
+    kv8_append_kernel(const Kv4RowArgs a, int tokens, int span, int sides) {
   using Blk = Kv8Block<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = blockIdx.x * kWarps + warp, side0 = sides == 2 ? 0 : w & 1, row = sides == 2 ? w : w >> 1;
@@ -391,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 6) kv8_gather_kernel(const Kv4RowArg
 #pragma unroll
     for (int i = 0; i < kGather; ++i) {
       store4<DT>(a.x[0], to_k + (long long)i * a.xs[0][0], values_of(kw[i], tail.z >> (o + i) & 1u ? NAN : __uint_as_float(tail.x)));
-      store4<DT>(a.x[1], to_v + (long long)i * a.xs[1][0], values_of(vw[i], tail.z >> (16 + o + i) & 1u ? NAN : __uint_as_float(tail.y)));
+      store4<DT>(a.x[1], to_v + (long long)i * a.xs[1][0],
+                 values_of(vw[i], tail.z >> (16 + o + i) & 1u ? NAN : __uint_as_float(tail.y)));
     }
     return;
   }

@@ -25,8 +25,8 @@ Serving, one step of R requests:
 
 (``kv8_...`` the same over a cache of 8 bits.)  Prompts, or pieces of them over what is cached:
 
-    k16, v16 = fa.kv8_gather(cache, slots, d)                  # all the requests' tokens
-    o, lse = fa.attention_fwd_packed(q[0], k16, v16, plan["cu_q"], cu_k)
+    k16, v16 = fa.kv8_gather(cache, slots, d)                  # of all the requests' tokens; slots and cu_k
+    o, lse = fa.attention_fwd_packed(q[0], k16, v16, plan["cu_q"], cu_k)  # are the caller's to make
 
 Every tensor lies on the current device.  Results and workspaces are allocated on
 ``stream`` (default: the current one); inputs that another stream may free are marked
@@ -361,7 +361,8 @@ def kv4_append(k, v, slots, cache, stream=None) -> None:
 def kv8_append(k, v, slots, cache, stream=None) -> None:
     """The same into a cache of 8 bits, whose blocks of 16 tokens of a head have one scale: new
     tokens may raise it, and the codes that are there are rounded to it.  The tokens of one block
-    must be neighbours in the call; a block whose first token is among them begins anew."""
+    must be neighbours in the call, else the block is void (``paged_plan`` puts them so); a block whose
+    first token is among them begins anew."""
     _call(_APPEND8, (k, v, slots, cache), (8,), stream, _plan_append)
 
 

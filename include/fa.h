@@ -459,8 +459,8 @@ fa_status fa_kv4_gather(const fa_kv4_cache* c, const fa_kv4_rows* rows, const vo
  * on the GPU.  A page outside the cache contributes nothing and is recorded as
  * FA_ERR_INDEX, as is a length beyond table_width * page_size, which is cut to that.
  * o and lse must not lie over q or each other, in part neither.  Calls that may run at
- * the same time need workspaces of their own.  Limits: T*Hq < 2^31, table_width * page_size <= 2^30, num_pages * page_size < 2^31,
- * a page below 2^31 bytes.
+ * the same time need workspaces of their own.  Limits: T*Hq < 2^31, table_width * page_size
+ * <= 2^30, num_pages * page_size < 2^31, a page below 2^31 bytes.
  */
 typedef struct {
   int R, T, Hq, dtype;
@@ -492,13 +492,15 @@ fa_status fa_kv4_attention(const fa_kv4_cache* c, const fa_kv4_attn_params* p, c
  * and a value is its code times its scale, or NaN where its token is marked.
  *
  * fa_kv8_append: of each side, the scale of a block is the least power of two (at least
- * 2^-64) with max|x| <= 127 * scale over its tokens' values x, saturated at +-16384, or 0
- * where they are all 0; a code is rint(x / scale).  A block whose place 0 is among the
- * call's slots begins anew: what it held counts no more.  Other blocks keep their tokens:
- * where the new ones need a larger scale, the codes of the others become
- * rint(code * old / new).  A token with a NaN is marked and its codes of that side are 0.
- * The tokens of one block must be neighbours in the call (as fa_paged_plan puts them);
- * slots >= 0 must be distinct.  Where they are not, those blocks' contents are void.
+ * 2^-64) with max|x| <= 127 * scale over the values x that were put into it since it
+ * began, saturated at +-16384, or 0 where they are all 0; a code is rint(x / scale).  A
+ * block whose place 0 is among the call's slots begins anew: what it held counts no more.
+ * Other blocks keep their tokens: where the new ones need a larger scale, the codes of the
+ * others become rint(code * old / new); a token that is written over (a draft that was
+ * taken back) leaves the scale it raised, and what was rounded to it.  A token with a NaN is marked and its codes of that side are 0.
+ * The tokens of one block must be neighbours in the call (as fa_paged_plan puts them; the
+ * 4-bit cache takes any order); slots >= 0 must be distinct.  Where they are not, those
+ * blocks' contents are void, and nothing is recorded.
  * fa_kv8_attention: a key's mark makes O and LSE of the rows that see it NaN, a value's
  * mark their O.
  * ------------------------------------------------------------------------ */
@@ -573,7 +575,8 @@ fa_status fa_paged_plan(const fa_plan_params* p, const int* seq_lens, const int*
  * (dq may be q, o or do with the same strides).  Views of one buffer whose rows or heads
  * take turns, at the distance of a stride of one of them, lie beside each other.
  * Rows that are in no sequence are neither read into a result nor written.  What is not
- * finite in k, v or q reaches, in the forward pass, the rows that see it; in the
+ * finite in k, v or q reaches, in the forward pass, the rows that see it (an infinite value
+ * makes its channel there infinite or, where its weight is 0 in the type, NaN); in the
  * backward pass it may reach every gradient of its own sequence, and none of another.
  * The workspace is 256-byte aligned and owned by the caller; its contents do not matter;
  * calls that may run at the same time need workspaces of their own.
