@@ -171,3 +171,93 @@ def test_scores_of_any_size(cuda_lib, d, dtype, a, b, scale):
     # the first head's dS is 0 but for fp32 roundings, and its queries are 0 in these channels
     assert bool(((dk[:, :, 1:] - want[1][:, :, 1:]).abs() <= bounds[1][:, :, 1:]).all())
     assert bool(dq.isfinite().all()) and bool(dk.isfinite().all())
+
+
+def random_batch(new, keys, Hq, Hk, d, seed):
+    g = torch.Generator().manual_seed(seed)
+    q, do = (torch.randn(sum(new), Hq, d, generator=g).half().cuda() for _ in (0, 1))
+    k, v = (torch.randn(sum(keys), Hk, d, generator=g).half().cuda() for _ in (0, 1))
+    return q, k, v, do
+
+
+@pytest.mark.parametrize("R,d,Hq,Hk", [(4, 64, 6, 2), (40, 128, 2, 2), (1100, 64, 2, 1)])
+def test_neighbours_change_no_bit_in_fp16(cuda_lib, R, d, Hq, Hk):
+    """A sequence's dk and dv are the same bits whatever the others hold, with and without a lane for each
+    sequence, and with their offsets in shared memory or not."""
+    rng = torch.Generator().manual_seed(R)
+    new = torch.randint(0, 200 if R < 10 else 60 if R < 100 else 4, (R,), generator=rng).tolist()
+    new[1], new[2] = 70, 33
+    keys = [n + (5 if i % 3 else 0) for i, n in enumerate(new)]
+    q, k, v, do = random_batch(new, keys, Hq, Hk, d, R)
+    cu_q, cu_k = offsets(new), offsets(keys)
+
+    def call():
+        o, lse = fa.attention_fwd_packed(q, k, v, cu_q, cu_k)
+        return fa.attention_bwd_packed(q, k, v, o, do, lse, cu_q, cu_k)
+
+    want = [x.clone() for x in call()]
+    at_q, at_k = slice(new[0], new[0] + 70), slice(keys[0], keys[0] + keys[1])
+    v[at_k] *= 100
+    do[at_q] *= 1000
+    got = call()
+    rest = [i for i in range(sum(keys)) if not at_k.start <= i < at_k.stop]
+    assert torch.equal(got[1][rest], want[1][rest]) and torch.equal(got[2][rest], want[2][rest])
+    rows = [i for i in range(sum(new)) if not at_q.start <= i < at_q.stop]
+    # dq: a sum of at most 3 parts in any order, and a step of fp16 (as in test_graphs_in_fp16)
+    w = want[0][rows].float().abs()
+    close = (got[0][rows].float() - want[0][rows].float()).abs() <= 2.0 ** -10 * w + 2.0 ** -24 + 2.0 ** -14 * float(w.max())
+    assert bool(close.all())
+    assert fa.get_status() == fa.FA_OK
+
+
+def test_graphs_in_fp16(cuda_lib):
+    """A captured call takes the lengths and sizes that are there when it is replayed, and its workspace's
+    contents do not matter."""
+    new, other, keys = [64, 500, 3], [100, 400, 67], [2000, 500, 9]
+    q, k, v, do = random_batch(new, keys, 8, 2, 64, 6)
+    live, cu_k = offsets(new), offsets(keys)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    want = []
+    for i, (c, size) in enumerate(((new, 1.0), (other, 1e-3), (new, 300.0))):
+        w = fa.attention_fwd_packed(q, k, v, offsets(c), cu_k)
+        want.append((c, size, w, fa.attention_bwd_packed(q, k, v, w[0], do * size, w[1], offsets(c), cu_k)))
+    o, lse, grad = torch.empty_like(want[0][2][0]), torch.empty_like(want[0][2][1]), do.clone()
+    o.copy_(want[0][2][0])
+    lse.copy_(want[0][2][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.attention_bwd_packed(q, k, v, o, grad, lse, live, cu_k, workspace=ws)
+    for c, size, w, g in want + want[:1]:
+        live.copy_(offsets(c))
+        o.copy_(w[0])
+        lse.copy_(w[1])
+        grad.copy_(do * size)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[1], g[1]) and torch.equal(got[2], g[2])
+        # dq is a fp32 sum of up to 16 parts (2000 keys) in any order: off by 16 * 2^-24 of the parts' sum, with each part
+        # at most 4 times the largest result 2^-14 of that; and rounded to fp16, a step of which is at most
+        # 2^-10 of it, or 2^-24 below the normal numbers
+        w = g[0].float().abs()
+        close = (got[0].float() - g[0].float()).abs() <= 2.0 ** -10 * w + 2.0 ** -24 + 2.0 ** -14 * float(w.max())
+        assert bool(close.all())
+    assert fa.get_status() == fa.FA_OK
+
+
+def test_wrong_offsets_and_empty_tensors_in_fp16(cuda_lib):
+    q, k, v, do = random_batch([300], [300], 4, 2, 64, 8)
+    good = offsets([100, 200])
+    o, lse = fa.attention_fwd_packed(q, k, v, good)
+    want = fa.attention_bwd_packed(q, k, v, o, do, lse, good)
+    for bad in ([0, 100, 5000], [0, 100, 50], [0, 100, -7], [0, 100, 2 ** 31 - 1], [-2 ** 31, 100, 90]):
+        grads = fa.attention_bwd_packed(q, k, v, o, do, lse, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert fa.get_status() == fa.FA_ERR_INDEX
+        assert torch.equal(grads[1][:100], want[1][:100]) and torch.equal(grads[2][:100], want[2][:100])
+    z = lambda T, H: torch.zeros(T, H, 64, dtype=torch.half, device="cuda")
+    none = torch.full((5, 4), -math.inf, device="cuda")
+    dq, dk, dv = fa.attention_bwd_packed(q[:5], z(0, 2), z(0, 2), z(5, 4), do[:5], none, offsets([5]), offsets([0]))
+    assert bool((dq == 0).all()) and dk.shape == (0, 2, 64)
+    dq, dk, dv = fa.attention_bwd_packed(z(0, 4), k[:5], v[:5], z(0, 4), z(0, 4), none[:0], offsets([0]), offsets([5]))
+    assert bool((dk == 0).all()) and bool((dv == 0).all()) and dq.shape == (0, 4, 64)
+    assert fa.get_status() == fa.FA_OK
