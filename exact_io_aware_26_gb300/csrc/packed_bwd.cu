@@ -10,7 +10,7 @@
 // need no pass of their own, and their order is fixed.  The CTAs stay and take the list that
 // packed_plan.cu makes, key tiles by the query tiles they visit, the longest first: the next tile's
 // copies and first products run beside the last one's results' way out (1520 sequences of 512
-// tokens, one head, d = 64: 417 us with a CTA for each tile, 345 so, and 357 with the weights as below).  A tile longer than an even share is cut; its
+// tokens, one head, d = 64: 417 us with a CTA for each tile, 345 so, and 350 with the weights as below).  A tile longer than an even share is cut; its
 // parts are fp32 sums that the last kernel adds.
 //
 // What lies behind a sequence's end in its last tiles is another sequence's or nobody's: rows of
@@ -22,12 +22,13 @@
 // allow (|dP - D| <= |dO| |V| + |D|).  The gradients take both back, exactly, in fp32.  (Without them a
 // weight over 2^16 keys has eight bits, and dS over 4096 keys of a dO of 2^-13 is 0.)  bf16 needs neither.
 // It costs a pass over V, the maxima and their way to the tiles: 4 sequences up to 2048 tokens, 12 heads,
-// d = 64, 72.5 us and 65.4 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.26 ms and 6.23.
+// d = 64, 72.4 us and 65.0 in bf16; 12 up to 8192, 32 and 8 heads, d = 128, 6.26 ms and 6.23.
 //
 // P is exp((scale S) - LSE), the product rounded as the forward rounds it into LSE, so that a key with all
 // of the weight has exactly 1 however large the scores are (as 2^(scale log2 e S - log2 e LSE), one fma,
-// 0.98 at a score of 10^6 and 0.80 at 2^24).  The three instructions cost 4 sequences up to 2048 tokens
-// 1.7 us of 64, 12 up to 8192 5 to 20 of 6220; looking for large scores and a way of their own cost 2.5 to 4.
+// 0.98 at a score of 10^6 and 0.80 at 2^24).  Three instructions for one cost 4 sequences up to 2048 tokens, d =
+// 64, 1.8 us of 64, and two where scale is a power of two, whose products need no rounding, 0.8; at d = 128
+// 12 up to 8192 5 to 20 us of 6220; looking for large scores and a way of their own cost 2.5 to 4 of the 64.
 //
 // Bound: the tensor core (five products, 10 d FLOPs a seen pair and query head) beside the
 // exponentials and the elementwise steps; one CTA an SM.  Measured, causal, with the kernels before
@@ -37,6 +38,7 @@
 // columns of a tile (TMEM lane = key row); a producer warp; a warp that owns TMEM and issues the
 // products; at d = 64 four warps that read dQ_i out of TMEM.
 #include <algorithm>
+#include <cmath>
 
 #include "packed.h"
 #include "ptx.cuh"
@@ -151,7 +153,8 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int t, int n)
     for (int i = t; i < chunks; i += n) st_shared_v4(tile + (uint32_t)(c * kTile * 128 + from * 128 + 16 * i), 0u, 0u, 0u, 0u);
 }
 
-template <int D, bool F16>
+// EXACT: scale is a power of two (1 / 8 at d = 64), so that no product with it is rounded.
+template <int D, bool F16, bool EXACT>
 __global__ void __launch_bounds__(Layout<D>::NT, 1)
     packed_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -522,8 +525,11 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
     const int r = (warp & 3) * 32 + lane;  // key row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint64_t scale2 = f2pack(a.scale, a.scale);
-    // as an fma with 0, because a product and a sum of pairs become one instruction, whatever their rounding says
-    auto scaled = [&](float x, float y) { return ffma2(f2pack(x, y), scale2, 0ull); };
+    // scale S - LSE, the product rounded: as an fma with 0, because a product and a sum of pairs become one
+    // instruction, whatever their rounding says
+    auto less_lse = [&](float x, float y, uint64_t nl) {
+      return EXACT ? ffma2(f2pack(x, y), scale2, nl) : fadd2(ffma2(f2pack(x, y), scale2, 0ull), nl);
+    };
     auto weight = [](float x) { return ex2(F16 ? fmaf(x, kLog2e, kPScale) : x * kLog2e); };
     const uint32_t stg = sb + L::STG + (uint32_t)warp * L::BOXB;
     bool pend = false;
@@ -567,8 +573,8 @@ __global__ void __launch_bounds__(Layout<D>::NT, 1)
         for (int c = 0; c < CW; c += 4) {
           const float4 nl = nl4[c / 4];
           float x0, x1, x2, x3;
-          f2unpack(fadd2(scaled(p[c], p[c + 1]), f2pack(nl.x, nl.y)), x0, x1);
-          f2unpack(fadd2(scaled(p[c + 2], p[c + 3]), f2pack(nl.z, nl.w)), x2, x3);
+          f2unpack(less_lse(p[c], p[c + 1], f2pack(nl.x, nl.y)), x0, x1);
+          f2unpack(less_lse(p[c + 2], p[c + 3], f2pack(nl.z, nl.w)), x2, x3);
           p[c] = weight(x0);
           p[c + 1] = weight(x1);
           p[c + 2] = weight(x2);
@@ -1062,10 +1068,10 @@ int stream_blocks(long long threads) {
   return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool EXACT>
 cudaError_t main_t(const PackedArgs& a, const CUtensorMap* tm, int items, cudaStream_t s) {
   using L = Layout<D>;
-  const auto kern = packed_bwd_kernel<D, F16>;
+  const auto kern = packed_bwd_kernel<D, F16, EXACT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
   if (e != cudaSuccess) return e;
   Launch l(std::min((long long)items * a.Hk, (long long)sms()), L::NT, L::BYTES, s);
@@ -1092,8 +1098,11 @@ cudaError_t launch_packed_bwd_preprocess(const PackedArgs& a, int d, bool f16, c
   return f16 ? rows_t<128, true>(a, s) : rows_t<128, false>(a, s);
 }
 cudaError_t launch_packed_bwd(const PackedArgs& a, int d, bool f16, const CUtensorMap* tm, int items, cudaStream_t s) {
-  if (d == 64) return f16 ? main_t<64, true>(a, tm, items, s) : main_t<64, false>(a, tm, items, s);
-  return f16 ? main_t<128, true>(a, tm, items, s) : main_t<128, false>(a, tm, items, s);
+  int e;
+  if (d == 64 && std::frexp(a.scale, &e) == 0.5f)
+    return f16 ? main_t<64, true, true>(a, tm, items, s) : main_t<64, false, true>(a, tm, items, s);
+  if (d == 64) return f16 ? main_t<64, true, false>(a, tm, items, s) : main_t<64, false, false>(a, tm, items, s);
+  return f16 ? main_t<128, true, false>(a, tm, items, s) : main_t<128, false, false>(a, tm, items, s);
 }
 cudaError_t launch_packed_bwd_finalize(const PackedArgs& a, int d, bool f16, int cuts, cudaStream_t s) {
   if (d == 64) return f16 ? finish_t<64, true>(a, cuts, s) : finish_t<64, false>(a, cuts, s);
