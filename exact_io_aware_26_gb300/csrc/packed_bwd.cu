@@ -10,7 +10,7 @@
 // need no pass of their own, and their order is fixed.  The CTAs stay and take the list that
 // packed_plan.cu makes, key tiles by the query tiles they visit, the longest first: the next tile's
 // copies and first products run beside the last one's results' way out (1520 sequences of 512
-// tokens, one head, d = 64: 417 us with a CTA for each tile, 345 so, and 350 with the weights as below).  A tile longer than an even share is cut; its
+// tokens, one head, d = 64: 417 us with a CTA for each tile, 345 so, and 347 with the weights as below).  A tile longer than an even share is cut; its
 // parts are fp32 sums that the last kernel adds.
 //
 // What lies behind a sequence's end in its last tiles is another sequence's or nobody's: rows of
